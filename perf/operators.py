@@ -21,6 +21,7 @@ own = False
 
 E4M3_MAX = 448.0
 INT8_MAX = 127.0
+SCALE_MIN = 2.0 ** -100  # the least scale of a block: its reciprocal is finite
 # A mean cache or document length below stands for lengths drawn evenly, so
 # work() counts the expected number of visible pairs.
 ATTN = dict(op="fwd", B=1, h=8, group=1, n=64, d=64, mask="causal", left=0, docs=0, cap=0.0,
@@ -251,7 +252,7 @@ def _gradients(s):
 
 
 def _encode(x, fmt):
-    """8-bit codes of x (already divided by its scale), nearest, ties to even."""
+    """8-bit codes of x (already over its scale), nearest, ties to even."""
     if fmt == "int8":
         return x.round().clamp(-INT8_MAX, INT8_MAX).to(torch.int8)
     return x.clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
@@ -281,13 +282,13 @@ def _append(s, new, cache, scale):
     i = (b[:, None, None], torch.arange(h, device=dev)[None, :, None], blk[:, None, :])
     was = scale[i]                                                     # [B, h, nb]
     kept = torch.where(held.any(3)[..., 0], was, 0.0)
-    now = torch.maximum(kept, x.abs().amax((-1, -2)) / top)
-    part = torch.where(now > 0, now, 1.0)[..., None, None]
+    now = torch.maximum(kept, x.abs().amax((-1, -2)) / top).clamp(min=SCALE_MIN)
+    inv = torch.reciprocal(now)[..., None, None]
     codes = blocks[i]
-    old = codes.float() * (kept[..., None, None] / part)
+    old = codes.float() * (kept[..., None, None] * inv)
     raw = codes.view(torch.int8)
     out = torch.where(held, _encode(old, fmt).view(torch.int8), raw)
-    out = torch.where(fresh, _encode(x / part, fmt).view(torch.int8), out)
+    out = torch.where(fresh, _encode(x * inv, fmt).view(torch.int8), out)
     blocks.view(torch.int8)[i] = out
     scale[i] = torch.where(fresh.any(3)[..., 0], now, was)
 
@@ -483,7 +484,7 @@ def _exact_cache(s, name):
         for blk in range(lens[b] // T, (end - 1) // T + 1):
             a, z = max(lens[b], blk * T), min(end, (blk + 1) * T)
             x = new[b, :, a - lens[b]:z - lens[b]].double()
-            to = x.abs().amax((-1, -2)) / top
+            to = (x.abs().amax((-1, -2)) / top).clamp(min=SCALE_MIN)
             if a > blk * T:
                 to = torch.maximum(to, scale[b, :, blk])
                 cache[b, :, blk * T:a] *= (scale[b, :, blk] / to)[:, None, None]
