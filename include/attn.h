@@ -254,6 +254,89 @@ int attn_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
                         float* lse, int B, int h, int n_q, int L_max, int d_k, float scale,
                         const int* cache_lens, struct CUstream_st* stream);
 
+/* What the rows of a key/value cache hold. */
+typedef enum {
+  ATTN_CACHE_BF16 = 0,
+  ATTN_CACHE_E4M3 = 1, /* 8-bit codes, value = scale * e4m3 number */
+  ATTN_CACHE_INT8 = 2  /* 8-bit codes, value = scale * int8 number in [-127, 127] */
+} attn_cache_format;
+
+/*
+ * attn_cache_append -- writes new keys and values into a cache held in 8 bits,
+ * with one float32 scale for each block of block_tokens tokens and head: the
+ * cache that attn_decode_scored reads.  Sequence b holds cache_lens[b] tokens
+ * before the call; its new token i goes to row cache_lens[b] + i.  For each
+ * block (of one sequence, one head, keys or values) that new tokens x fall into:
+ *   scale = max(held, max |x| / c_max, 2^-100),  code = round(x * (1 / scale)),
+ * held = the scale of the tokens that the block holds already (0 if none),
+ * c_max = 448 (e4m3) or 127 (int8), round = to the nearest code, ties to even;
+ * where the scale grew, the codes held become round(code * (held * (1/scale))).
+ * All of it in float32.  Rows behind the new tokens and blocks without new
+ * tokens are left as they were, scales included.
+ *   k_new, v_new : bf16 [B, h, n_new, d_k], finite.
+ *   k_cache, v_cache : 8-bit codes [B, h, L_max, d_k], 16-byte aligned.
+ *   k_scale, v_scale : float [B, h, ceil(L_max / block_tokens)], contiguous.
+ *   strides  : host array of 12 element counts, three (b, h, row) per tensor in
+ *              the order k_new, v_new, k_cache, v_cache, each > 0 and a
+ *              multiple of 16 bytes; NULL for contiguous tensors.
+ *   cache_format : ATTN_CACHE_E4M3 or ATTN_CACHE_INT8.
+ *   block_tokens : 16, 32, 64 or 128.
+ *   cache_lens : device int32[B] (clamped to [0, L_max]), or NULL when the
+ *              caches are empty.  Not changed: the caller adds the new lengths.
+ *   new_lens : device int32[B] (clamped to [0, n_new]): only the first
+ *              new_lens[b] of the n_new tokens are written (a padded batch of
+ *              prompts); NULL: all.  Tokens that would land past L_max are
+ *              dropped.
+ *   d_k      : 16, 32, 64 or 128 (else ATTN_ERR_UNSUPPORTED).
+ * One kernel on `stream`; nothing is allocated.  The caches must not overlap
+ * the new tokens, and two calls on one cache must be ordered on one stream.
+ */
+int attn_cache_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, int B, int h, int n_new, int L_max, int d_k,
+                      const int64_t* strides, int cache_format, int block_tokens,
+                      const int* cache_lens, const int* new_lens, struct CUstream_st* stream);
+
+/*
+ * attn_decode_scored -- a decoding step with changed scores, key heads shared
+ * by groups of query heads, and a cache in bf16 or in 8 bits.  The n_q new
+ * queries of sequence b are its newest tokens (already in the cache): query i
+ * stands at position p = cache_lens[b] - n_q + i and sees the keys j <= p, or
+ * with a window the keys p - window <= j <= p:
+ *   s_j = scale * q.k_j;   capped: softcap * tanh(s_j / softcap);
+ *   biased: minus slopes[head] * (p - j);   O = softmax(s) V,  LSE = ln sum e^s.
+ * (attn_decode lets all n_q queries see the whole cache; for n_q = 1 the two
+ * agree.)  A query that sees no key (p < 0) gets O = 0 and LSE = -inf.
+ *   q, o     : bf16 [B, h, n_q, d_k], 1 <= n_q <= 8; lse float [B, h, n_q] or NULL.
+ *   k_cache, v_cache : [B, h_kv, L_max, d_k] in cache_format; h is a multiple of
+ *              h_kv, and query head i reads key head i / (h / h_kv).  Rows past
+ *              cache_lens[b] or before every query's window are never used,
+ *              whatever they hold.
+ *   k_scale, v_scale, block_tokens : as for attn_cache_append (finite, >= 0);
+ *              ignored for ATTN_CACHE_BF16.
+ *   strides  : host array of 12 element counts (q, k_cache, v_cache, o; three
+ *              each, > 0 and a multiple of 16 bytes), or NULL: contiguous.
+ *   softcap  : > 0, or 0 for none.   slopes : device float[h], or NULL for none.
+ *   cache_lens : device int32[B] (clamped to [0, L_max]), or NULL: all L_max.
+ *   window   : >= 0, or -1 for none.
+ *   workspace, workspace_bytes : at least attn_decode_scored_workspace_bytes(...)
+ *              bytes, 16-byte aligned; may be NULL when that is 0.
+ *   d_k      : 16, 32, 64 or 128, B*h*n_q <= 2^24, L_max <= 2^30 (else
+ *              ATTN_ERR_UNSUPPORTED).
+ * 8-bit codes enter the products exactly; probabilities are rounded to f16
+ * (8-bit caches) or bf16 before the second product.
+ */
+int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
+                       const float* k_scale, const float* v_scale, void* o, float* lse, int B,
+                       int h, int h_kv, int n_q, int L_max, int d_k, const int64_t* strides,
+                       int cache_format, int block_tokens, float scale, float softcap,
+                       const float* slopes, const int* cache_lens, int window, void* workspace,
+                       size_t workspace_bytes, struct CUstream_st* stream);
+
+/* Scratch bytes attn_decode_scored needs on the current device (0 when no
+ * split is needed, or for unsupported sizes). */
+size_t attn_decode_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int L_max, int d_k,
+                                          int cache_format, int window);
+
 /*
  * attn_bwd -- gradients of attn_fwd: given dout = dLoss/dO, writes
  *   dq = dLoss/dQ, dk = dLoss/dK, dv = dLoss/dV

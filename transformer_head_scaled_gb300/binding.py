@@ -26,6 +26,9 @@ ATTN_ERR_CUDA = -3
 ATTN_ERR_TIMEOUT = -4
 ATTN_ERR_SCRATCH_TOO_SMALL = -5
 MASK_WINDOW = 3  # attn_fwd_strided: the window of attn_fwd_window
+CACHE_BF16, CACHE_E4M3, CACHE_INT8 = 0, 1, 2  # attn_cache_format
+_CACHE_FORMATS = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3,
+                  torch.int8: CACHE_INT8}
 DECODE_NOALLOC_SCRATCH_BYTES = 1 << 20
 
 # Every entry point declared in include/attn.h.
@@ -33,7 +36,8 @@ EXPORTS = ("attn_fwd", "attn_fwd_f32", "attn_fwd_window", "attn_fwd_strided", "a
            "attn_fwd_host_buffer_bytes", "attn_decode", "attn_decode_strided",
            "attn_decode_workspace_bytes", "attn_decode_window",
            "attn_decode_window_workspace_bytes", "attn_decode_noalloc", "attn_bwd", "attn_bwd_window", "attn_bwd_strided",
-           "attn_bwd_workspace_bytes",
+           "attn_bwd_workspace_bytes", "attn_cache_append", "attn_decode_scored",
+           "attn_decode_scored_workspace_bytes",
            "attn_check", "attn_status_string",
            "attn_last_cuda_error", "attn_set_wait_limit_ns", "attn_launch_count",
            "attn_diag_tile", "attn_diag_wait_timeout")
@@ -104,6 +108,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                                 vp]
         lib.attn_bwd_workspace_bytes.restype = ctypes.c_size_t
         lib.attn_bwd_workspace_bytes.argtypes = [i32, i32, i32, i32]
+        lib.attn_cache_append.restype = i32
+        lib.attn_cache_append.argtypes = [vp] * 6 + [i32] * 5 + [vp, i32, i32, vp, vp, vp]
+        lib.attn_decode_scored.restype = i32
+        lib.attn_decode_scored.argtypes = ([vp] * 7 + [i32] * 6 + [vp, i32, i32, f32, f32, vp, vp,
+                                                                   i32, vp, ctypes.c_size_t, vp])
+        lib.attn_decode_scored_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_decode_scored_workspace_bytes.argtypes = [i32] * 8
         lib.attn_check.restype = i32
         lib.attn_check.argtypes = [vp]
         lib.attn_status_string.restype = ctypes.c_char_p
@@ -593,6 +604,209 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_bwd_window" if window is not None else "attn_bwd")
     return dq, dk, dv
+
+
+def _stream_of(device: torch.device, stream) -> torch.cuda.Stream:
+    """The stream a call runs on: `stream` (a torch stream or a raw pointer), or
+    the current stream of the tensors' device."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+class _launch_on:
+    """Makes the tensors' device current for a call, and the call's stream too,
+    so that a workspace allocated for it belongs to that stream."""
+
+    def __init__(self, device: torch.device, stream):
+        self._device = torch.cuda.device(device)
+        self._at = device, stream
+
+    def __enter__(self) -> int:
+        self._device.__enter__()
+        stream = _stream_of(*self._at)
+        self._stream = torch.cuda.stream(stream)
+        self._stream.__enter__()
+        return int(stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        self._stream.__exit__(*exc)
+        self._device.__exit__(*exc)
+
+
+def _views(what: str, dtype, *tensors) -> None:
+    """[B, h, n, d] CUDA views of one dtype on one device with unit last stride."""
+    for t in tensors:
+        if (not t.is_cuda or t.dtype != dtype or t.dim() != 4 or t.stride(-1) != 1
+                or t.device != tensors[0].device):
+            raise ValueError(f"{what} must be {dtype} CUDA [B, h, n, d] views on one device with "
+                             "unit last stride")
+
+
+def _vector(name: str, t, dtype, count: int, device) -> None:
+    if t is not None and (t.dtype != dtype or t.device != device or t.numel() != count
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {count} entries on "
+                         f"{device}")
+
+
+def _strides(*tensors):
+    """The (b, h, row) element strides of [B, h, n, d] views.  The stride of a
+    dimension of one entry is never stepped over, whatever the view says."""
+    flat = []
+    for t in tensors:
+        room = max(t.shape[2] * t.shape[3], 1) if t.numel() else 1
+        for dim in range(3):
+            step = t.stride(dim)
+            flat.append(step if t.shape[dim] > 1 else -(-max(step, room) // 16) * 16)
+    return flat
+
+
+def _strides_ptr(strides):
+    return ctypes.cast((ctypes.c_int64 * len(strides))(*[int(x) for x in strides]),
+                       ctypes.c_void_p)
+
+
+def _workspace(need: int, given, device):
+    """The caller's scratch when it is large enough, else a new one."""
+    if need == 0:
+        return None
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {device}")
+        if given.numel() * given.element_size() >= need:
+            return given
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def attn_cache_append_raw(k_new_ptr, v_new_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, B, h, n_new, L_max, d,
+                          strides, cache_format, block_tokens, lens_ptr, new_lens_ptr,
+                          stream_ptr) -> int:
+    """The C call itself, on raw device pointers; ``strides`` = 12 element counts or None."""
+    return load().attn_cache_append(
+        k_new_ptr, v_new_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, B, h, n_new, L_max, d,
+        None if strides is None else _strides_ptr(strides), int(cache_format), int(block_tokens),
+        lens_ptr, new_lens_ptr, stream_ptr)
+
+
+def attn_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                      cache_lens: torch.Tensor | None, block_tokens: int = 64,
+                      new_lens: torch.Tensor | None = None, stream=None) -> None:
+    """Writes bf16 k_new, v_new [B, h, n_new, d] behind the first cache_lens[b]
+    tokens (None: empty) of 8-bit caches [B, h, L_max, d] (torch.float8_e4m3fn
+    or torch.int8 codes), one float32 scale per block of block_tokens tokens and
+    head in k_scale, v_scale [B, h, ceil(L_max / block_tokens)].  With new_lens
+    only the first new_lens[b] new tokens.  cache_lens is not changed."""
+    _views("k_new and v_new", torch.bfloat16, k_new, v_new)
+    fmt = _CACHE_FORMATS.get(k_cache.dtype, CACHE_BF16)
+    if fmt == CACHE_BF16:
+        raise ValueError("the caches must hold torch.float8_e4m3fn or torch.int8 codes")
+    _views("k_cache and v_cache", k_cache.dtype, k_cache, v_cache)
+    B, h, n_new, d = k_new.shape
+    L_max = k_cache.shape[2]
+    if (v_new.shape != k_new.shape or tuple(k_cache.shape) != (B, h, L_max, d)
+            or v_cache.shape != k_cache.shape or k_cache.device != k_new.device):
+        raise ValueError("k_new, v_new must be [B, h, n_new, d] and the caches [B, h, L_max, d]")
+    if block_tokens not in (16, 32, 64, 128):
+        raise ValueError("block_tokens must be 16, 32, 64 or 128")
+    dev = k_new.device
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _vector(name, t, torch.float32, B * h * -(-L_max // block_tokens), dev)
+    _vector("cache_lens", cache_lens, torch.int32, B, dev)
+    _vector("new_lens", new_lens, torch.int32, B, dev)
+    with _launch_on(dev, stream) as ptr:
+        rc = attn_cache_append_raw(_ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                   _ptr(k_scale), _ptr(v_scale), B, h, n_new, L_max, d,
+                                   _strides(k_new, v_new, k_cache, v_cache), fmt, block_tokens,
+                                   _ptr(cache_lens), _ptr(new_lens), ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_append")
+
+
+def decode_scored_workspace_bytes(B: int, h: int, h_kv: int, n_q: int, L_max: int, d: int,
+                                  cache_format: int = CACHE_BF16,
+                                  window: int | None = None) -> int:
+    """Scratch bytes attn_decode_scored needs on the current device (0: none)."""
+    return int(load().attn_decode_scored_workspace_bytes(
+        B, h, h_kv, n_q, L_max, d, cache_format, -1 if window is None else int(window)))
+
+
+def attn_decode_scored_raw(q_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, o_ptr, lse_ptr, B, h, h_kv, n_q,
+                           L_max, d, strides, cache_format, block_tokens, scale, softcap,
+                           slopes_ptr, lens_ptr, window, ws_ptr, ws_bytes, stream_ptr) -> int:
+    """The C call itself, on raw device pointers; ``strides`` = 12 element counts or None."""
+    return load().attn_decode_scored(
+        q_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, o_ptr, lse_ptr, B, h, h_kv, n_q, L_max, d,
+        None if strides is None else _strides_ptr(strides), int(cache_format), int(block_tokens),
+        float(scale), float(softcap), slopes_ptr, lens_ptr, int(window), ws_ptr, int(ws_bytes),
+        stream_ptr)
+
+
+def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       cache_lens: torch.Tensor | None = None,
+                       k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                       block_tokens: int = 64, scale: float | None = None, softcap: float = 0.0,
+                       slopes: torch.Tensor | None = None, window: int | None = None,
+                       out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """n_q <= 8 newest queries q [B, h, n_q, d] (bf16) against a cache [B, h_kv,
+    L_max, d] of bf16 rows or of 8-bit codes with scales (see attn_cache_append);
+    query i stands at position cache_lens[b] - n_q + i and sees the keys up to
+    there (with `window`: that key and the `window` before it).  softcap > 0
+    caps the scores by a tanh, slopes [h] (float32) bias them by distance.
+    Returns (o, lse)."""
+    _views("q", torch.bfloat16, q)
+    fmt = _CACHE_FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise ValueError("the caches must be bf16, torch.float8_e4m3fn or torch.int8")
+    _views("k_cache and v_cache", k_cache.dtype, k_cache, v_cache)
+    B, h, n_q, d = q.shape
+    h_kv, L_max = k_cache.shape[1:3]
+    if (tuple(k_cache.shape) != (B, h_kv, L_max, d) or v_cache.shape != k_cache.shape
+            or h_kv < 1 or h % h_kv != 0 or k_cache.device != q.device):
+        raise ValueError("caches must be [B, h_kv, L_max, d] with q's B and d, h a multiple of h_kv")
+    dev = q.device
+    if fmt == CACHE_BF16:
+        k_scale = v_scale = None
+    else:
+        if block_tokens not in (16, 32, 64, 128):
+            raise ValueError("block_tokens must be 16, 32, 64 or 128")
+        if k_scale is None or v_scale is None:
+            raise ValueError("an 8-bit cache needs k_scale and v_scale")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _vector(name, t, torch.float32, B * h_kv * -(-L_max // block_tokens), dev)
+    _vector("cache_lens", cache_lens, torch.int32, B, dev)
+    _vector("slopes", slopes, torch.float32, h, dev)
+    if window is not None and window < 0:
+        raise ValueError("window must be >= 0 (None for none)")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _launch_on(dev, stream) as ptr:
+        if out is None:
+            out = torch.empty((B, h, n_q, d), dtype=q.dtype, device=dev)
+        _views("q and out", torch.bfloat16, q, out)
+        if out.shape != q.shape:
+            raise ValueError("out must be shaped like q")
+        if lse is None:
+            lse = torch.empty((B, h, n_q), dtype=torch.float32, device=dev)
+        _vector("lse", lse, torch.float32, B * h * n_q, dev)
+        workspace = _workspace(
+            decode_scored_workspace_bytes(B, h, h_kv, n_q, L_max, d, fmt, window), workspace, dev)
+        rc = attn_decode_scored_raw(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(out),
+            _ptr(lse), B, h, h_kv, n_q, L_max, d, _strides(q, k_cache, v_cache, out), fmt,
+            block_tokens, scale, softcap, _ptr(slopes), _ptr(cache_lens),
+            -1 if window is None else window, _ptr(workspace), _nbytes(workspace), ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_scored")
+    return out, lse
 
 
 def check(stream=None) -> None:

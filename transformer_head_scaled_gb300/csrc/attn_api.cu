@@ -795,3 +795,172 @@ int attn_diag_wait_timeout(uint64_t limit_ns, struct CUstream_st* stream) {
 }
 
 }  // extern "C"
+
+namespace attn {
+namespace {
+// A row stride in elements of `elem` bytes that keeps rows 16-byte aligned.
+bool stride16_ok(long long elems, int elem) {
+  return elems > 0 && elems < (1LL << 40) / elem && (elems * elem) % 16 == 0;
+}
+
+bool block_tokens_ok(int t) { return t == 16 || t == 32 || t == 64 || t == 128; }
+
+// Strides of `count` [B, h, n, d] tensors from a host array of 3 * count
+// element counts, or contiguous ones when the array is null.
+bool read_strides(Strides* st, const int64_t* in, int count, const int* heads, const int* rows,
+                  int d, const int* elem) {
+  for (int i = 0; i < count; ++i) {
+    st[i] = in ? Strides{in[3 * i], in[3 * i + 1], in[3 * i + 2]} : bhsd(heads[i], rows[i], d);
+    if (!stride16_ok(st[i].b, elem[i]) || !stride16_ok(st[i].h, elem[i]) ||
+        !stride16_ok(st[i].n, elem[i]))
+      return false;
+  }
+  return true;
+}
+
+bool int_ptr_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+int elem_bytes(int cache_format) { return cache_format == ATTN_CACHE_BF16 ? 2 : 1; }
+
+// The most keys n_q queries with this window see.
+int scored_seen(int n_q, int L_max, int window) {
+  return window >= 0 && window < L_max - n_q ? window + n_q : L_max;
+}
+
+// Sizes of attn_decode_scored, shared with its workspace query.
+int scored_decode_sizes(int B, int h, int h_kv, int n_q, int L_max, int d_k, int cache_format,
+                        int window) {
+  if (B < 1 || h < 1 || h_kv < 1 || n_q < 1 || L_max < 1 || d_k < 1 || h % h_kv != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (cache_format < ATTN_CACHE_BF16 || cache_format > ATTN_CACHE_INT8 || window < -1)
+    return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * h > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if (!tc_head_size(d_k) || n_q > kDecodeMaxQueries) return ATTN_ERR_UNSUPPORTED;
+  // one CTA per key head, row tile and chunk: a grid of at most 2^31 - 1
+  if (static_cast<long long>(B) * h * n_q > (1LL << 24) || L_max > (1 << 30))
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+int attn_cache_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, int B, int h, int n_new, int L_max, int d_k,
+                      const int64_t* strides, int cache_format, int block_tokens,
+                      const int* cache_lens, const int* new_lens, struct CUstream_st* stream) {
+  if (!k_new || !v_new || !k_cache || !v_cache || !k_scale || !v_scale) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !int_ptr_ok(k_scale) || !int_ptr_ok(v_scale) || !int_ptr_ok(cache_lens) ||
+      !int_ptr_ok(new_lens))
+    return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || h < 1 || n_new < 1 || L_max < 1 || d_k < 1) return ATTN_ERR_INVALID_ARG;
+  if (cache_format != ATTN_CACHE_E4M3 && cache_format != ATTN_CACHE_INT8)
+    return ATTN_ERR_INVALID_ARG;
+  if (!block_tokens_ok(block_tokens)) return ATTN_ERR_INVALID_ARG;
+  const int heads[4] = {h, h, h, h}, rows[4] = {n_new, n_new, L_max, L_max}, elem[4] = {2, 2, 1, 1};
+  Strides st[4];
+  if (tc_head_size(d_k) && !read_strides(st, strides, 4, heads, rows, d_k, elem))
+    return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * h > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  if (!tc_head_size(d_k)) return ATTN_ERR_UNSUPPORTED;
+  // one block of threads at most per cache block that can be touched
+  if (static_cast<double>(B) * h * cache_blocks_touched(n_new, L_max, block_tokens) * 2.0 >
+      2147483647.0)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceInfo* di = nullptr;
+  int rc;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  CacheAppendProblem pb{k_new, v_new, k_cache, v_cache, k_scale, v_scale, B, h, n_new, L_max, d_k,
+                        cache_format == ATTN_CACHE_E4M3, block_tokens, cache_lens, new_lens,
+                        st[0], st[1], st[2], st[3]};
+  cudaError_t e = launch_cache_append(pb, make_ctx(*di, stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1);
+  return ATTN_OK;
+}
+
+size_t attn_decode_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int L_max, int d_k,
+                                          int cache_format, int window) {
+  if (scored_decode_sizes(B, h, h_kv, n_q, L_max, d_k, cache_format, window) != ATTN_OK) return 0;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di) != ATTN_OK) return 0;
+  return scored_decode_plan(B, h, h_kv, n_q, scored_seen(n_q, L_max, window), d_k,
+                            elem_bytes(cache_format), di->num_sms)
+      .workspace_bytes;
+}
+
+int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
+                       const float* k_scale, const float* v_scale, void* o, float* lse, int B,
+                       int h, int h_kv, int n_q, int L_max, int d_k, const int64_t* strides,
+                       int cache_format, int block_tokens, float scale, float softcap,
+                       const float* slopes, const int* cache_lens, int window, void* workspace,
+                       size_t workspace_bytes, struct CUstream_st* stream) {
+  if (!q || !k_cache || !v_cache || !o) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
+      !int_ptr_ok(k_scale) || !int_ptr_ok(v_scale) || !int_ptr_ok(lse) || !int_ptr_ok(slopes) ||
+      !int_ptr_ok(cache_lens))
+    return ATTN_ERR_INVALID_ARG;
+  int rc = scored_decode_sizes(B, h, h_kv, n_q, L_max, d_k, cache_format, window);
+  if (rc == ATTN_ERR_INVALID_ARG) return rc;
+  if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (!(std::isfinite(softcap) && softcap >= 0.f)) return ATTN_ERR_INVALID_ARG;
+  const bool q8 = cache_format != ATTN_CACHE_BF16;
+  if (q8 && (!k_scale || !v_scale || !block_tokens_ok(block_tokens))) return ATTN_ERR_INVALID_ARG;
+  const int e1 = elem_bytes(cache_format);
+  const int heads[4] = {h, h_kv, h_kv, h}, rows[4] = {n_q, L_max, L_max, n_q},
+            elem[4] = {2, e1, e1, 2};
+  Strides st[4];
+  if (rc == ATTN_OK && !read_strides(st, strides, 4, heads, rows, d_k, elem))
+    return ATTN_ERR_INVALID_ARG;
+  if (rc != ATTN_OK) return rc;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  const ScoredDecodePlan plan = scored_decode_plan(
+      B, h, h_kv, n_q, scored_seen(n_q, L_max, window), d_k, e1, di->num_sms);
+  if (plan.workspace_bytes > 0 &&
+      (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
+    return ATTN_ERR_INVALID_ARG;
+  ScoredDecodeProblem pb{q, k_cache, v_cache, k_scale, v_scale, o, lse, B, h, h_kv, n_q, L_max,
+                         d_k, q8 ? block_tokens : 128, scale, softcap, slopes, cache_lens,
+                         window < L_max ? window : -1, st[0], st[1], st[2], st[3]};
+  const LaunchCtx ctx = make_ctx(*di, stream);
+  float* ws = static_cast<float*>(workspace);
+  const cudaError_t e = cache_format == ATTN_CACHE_BF16   ? launch_decode_scored_bf16(pb, plan, ws, ctx)
+                        : cache_format == ATTN_CACHE_E4M3 ? launch_decode_scored_e4m3(pb, plan, ws, ctx)
+                                                          : launch_decode_scored_int8(pb, plan, ws, ctx);
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(plan.splits > 1 ? 2 : 1);
+  return ATTN_OK;
+}
+
+}  // extern "C"
+
+namespace attn {
+
+ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int d, int elem_bytes,
+                                    int num_sms) {
+  ScoredDecodePlan plan;
+  const int rows = H / HK * n_q;
+  plan.row_tile = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
+  plan.row_tiles = (rows + plan.row_tile - 1) / plan.row_tile;
+  // keys per warp and tile: about 4 KB of keys, as in the kernel
+  const int row_bytes = d * elem_bytes;
+  const int kt = row_bytes >= 256 ? 16 : (row_bytes >= 128 ? 32 : 64);
+  const long long units = static_cast<long long>(B) * HK * plan.row_tiles;
+  const int max_tiles = (seen + kt - 1) / kt;
+  // about four rounds of three resident CTAs per SM, so that unequal cache
+  // lengths even out, and at least two tiles for each of a CTA's four warps
+  const long long want = 4LL * 3 * num_sms;
+  long long splits = (want + units - 1) / units;
+  if (splits > max_tiles / 8) splits = max_tiles / 8;
+  if (splits < 1) splits = 1;
+  plan.splits = static_cast<int>(splits);
+  plan.workspace_bytes = splits > 1 ? static_cast<size_t>(units) * splits * plan.row_tile *
+                                          (d + 2) * sizeof(float)
+                                    : 0;
+  return plan;
+}
+
+}  // namespace attn

@@ -1,0 +1,226 @@
+// attn_cache.cu -- writing new keys and values into a cache held in 8 bits,
+// with one float32 scale for each block of T tokens and head.
+//
+// A cache row holds codes c with  value = scale[b, h, token / T] * c,  c an
+// e4m3 number (|c| <= 448) or an int8 one (|c| <= 127).  For the block that a
+// call's new tokens x of one (b, h) fall into, with `held` = the scale of the
+// tokens the block holds already (0 when it holds none):
+//
+//   scale = max(held, max |x| / c_max, 2^-100),   c = round(x * (1 / scale)),
+//   held codes  c <- round(c * (held * (1 / scale)))   when the scale grew,
+//
+// round = to the nearest code, ties to even.  The least scale keeps the
+// reciprocal finite.  A scale that never shrinks while its block fills means
+// a held code is rounded again only when a larger token arrives.  The codes
+// are products with the correctly rounded reciprocal instead of quotients:
+// one multiplication each, and the quotient differs from them by less than
+// 2^-23 relative, which matters only next to a border between two codes.
+//
+// Bound by memory: each new element is read once (2 bytes) and written once
+// (1 byte).  A block's maximum is needed before its first code, so a block's
+// new tokens wait in registers between the two.  Two layouts of the same
+// work, chosen by the new elements a block can get (template Layout below):
+// one CTA per block, or one warp per block when a step brings few tokens and
+// the launch, not the bytes, is what costs.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "attn_internal.cuh"
+
+namespace attn {
+namespace {
+
+struct CacheParams {
+  const __nv_bfloat16* src[2];  // new keys, new values
+  uint8_t* dst[2];              // their caches
+  float* scale[2];
+  const int* lens;      // tokens held per sequence, or null (none)
+  const int* new_lens;  // new tokens per sequence, or null (n_new each)
+  RowStrides ss[2], sd[2];
+  int H, n_new, L_max, T, num_blocks, touched;
+};
+
+constexpr float kScaleMin = 0x1p-100f;
+
+template <bool E4M3>
+__device__ __forceinline__ float code_max() {
+  return E4M3 ? 448.f : 127.f;
+}
+
+// Four values (already over their scale) to four codes, nearest, ties to even.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  if (E4M3) {
+    // the conversion rounds to nearest even and saturates at 448
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  }
+  auto one = [](float x) {
+    return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x)))) & 0xffu;
+  };
+  return one(a) | (one(b) << 8) | (one(c) << 16) | (one(d) << 24);
+}
+
+template <bool E4M3>
+__device__ __forceinline__ float decode1(uint32_t byte) {
+  if (E4M3) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
+    return __half2float(__half(h));
+  }
+  return static_cast<float>(static_cast<int8_t>(byte));
+}
+
+// THREADS threads work on one block of one (b, head) and of keys or values;
+// CHUNKS chunks of 8 elements each wait in a thread's registers.  WARP: one
+// warp per block, eight blocks to a CTA; else one CTA per block.
+template <bool E4M3, bool WARP, int THREADS, int CHUNKS>
+__global__ void __launch_bounds__(WARP ? 256 : THREADS)
+    attn_cache_append_kernel(const CacheParams p, long long units, int chunks_per_row) {
+  __shared__ float red[WARP ? 1 : THREADS / 32];
+  const long long unit =
+      WARP ? static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && unit >= units) return;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  // unit = ((b * H + head) * touched + block) * 2 + (keys or values)
+  const int kv = static_cast<int>(unit & 1);
+  const long long rest = unit >> 1;
+  const long long bh = rest / p.touched;
+  const int b = static_cast<int>(bh / p.H), hh = static_cast<int>(bh - b * static_cast<long long>(p.H));
+  const int len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
+  const int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
+  const int end = min(len + more, p.L_max);  // tokens that do not fit are dropped
+  const int blk = len / p.T + static_cast<int>(rest - bh * p.touched);
+  const int row0 = blk * p.T;
+  const int first = max(len, row0), last = min(end, row0 + p.T);  // new rows of this block
+  if (first >= last) return;  // the same for every thread of the unit
+
+  const __nv_bfloat16* src = p.src[kv] + b * p.ss[kv].b + hh * p.ss[kv].h +
+                             static_cast<long long>(first - len) * p.ss[kv].n;
+  uint8_t* dst = p.dst[kv] + b * p.sd[kv].b + hh * p.sd[kv].h;
+  const int chunks = (last - first) * chunks_per_row;
+
+  uint4 w[CHUNKS];
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < CHUNKS; ++i) {
+    const int c = tid + i * THREADS;
+    if (c < chunks) {
+      const int r = c / chunks_per_row;
+      w[i] = __ldg(reinterpret_cast<const uint4*>(src + r * p.ss[kv].n) + (c - r * chunks_per_row));
+    } else {
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  float* scale_at = p.scale[kv] + bh * p.num_blocks + blk;
+  const float held = first > row0 ? *scale_at : 0.f;
+#pragma unroll
+  for (int i = 0; i < CHUNKS; ++i) {
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __bfloat1622float2(x[e]);
+      top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+  if (!WARP) {
+    if ((tid & 31) == 0) red[tid >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) top = fmaxf(top, red[i]);
+  } else {
+    __syncwarp();  // every lane has read the held scale before it is replaced
+  }
+  const float scale = fmaxf(fmaxf(held, __fdiv_rn(top, code_max<E4M3>())), kScaleMin);
+  const float inv = __frcp_rn(scale);
+#pragma unroll
+  for (int i = 0; i < CHUNKS; ++i) {
+    const int c = tid + i * THREADS;
+    if (c >= chunks) break;
+    const int r = c / chunks_per_row;
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+    const float2 f0 = __bfloat1622float2(x[0]), f1 = __bfloat1622float2(x[1]),
+                 f2 = __bfloat1622float2(x[2]), f3 = __bfloat1622float2(x[3]);
+    uint2 out;
+    out.x = encode4<E4M3>(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv);
+    out.y = encode4<E4M3>(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv);
+    *(reinterpret_cast<uint2*>(dst + static_cast<long long>(first + r) * p.sd[kv].n) +
+      (c - r * chunks_per_row)) = out;
+  }
+  if (scale != held) {
+    if (tid == 0) *scale_at = scale;
+    // the rows the block held are rescaled; rows behind the new ones stay
+    const float ratio = held * inv;
+    const int old = (first - row0) * chunks_per_row;
+    for (int c = tid; c < old; c += THREADS) {
+      const int r = c / chunks_per_row;
+      uint2* at = reinterpret_cast<uint2*>(dst + static_cast<long long>(row0 + r) * p.sd[kv].n) +
+                  (c - r * chunks_per_row);
+      uint2 v = *at;
+      uint32_t* words = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        words[e] = encode4<E4M3>(decode1<E4M3>(words[e] & 0xffu) * ratio,
+                                 decode1<E4M3>((words[e] >> 8) & 0xffu) * ratio,
+                                 decode1<E4M3>((words[e] >> 16) & 0xffu) * ratio,
+                                 decode1<E4M3>(words[e] >> 24) * ratio);
+      *at = v;
+    }
+  }
+}
+
+template <bool E4M3>
+cudaError_t launch_append(const CacheParams& p, long long units, int chunks_per_row,
+                          cudaStream_t stream) {
+  // most 8-element chunks of new tokens that one block can get
+  const int most = (p.n_new < p.T ? p.n_new : p.T) * chunks_per_row;
+  if (most <= 4 * 32) {
+    const unsigned grid = static_cast<unsigned>((units + 7) / 8);
+    attn_cache_append_kernel<E4M3, true, 32, 4><<<grid, 256, 0, stream>>>(p, units, chunks_per_row);
+  } else if (most <= 4 * 128) {
+    attn_cache_append_kernel<E4M3, false, 128, 4>
+        <<<static_cast<unsigned>(units), 128, 0, stream>>>(p, units, chunks_per_row);
+  } else {
+    attn_cache_append_kernel<E4M3, false, 256, 8>
+        <<<static_cast<unsigned>(units), 256, 0, stream>>>(p, units, chunks_per_row);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheAppendProblem& pb, const LaunchCtx& ctx) {
+  CacheParams p;
+  p.src[0] = static_cast<const __nv_bfloat16*>(pb.k_new);
+  p.src[1] = static_cast<const __nv_bfloat16*>(pb.v_new);
+  p.dst[0] = static_cast<uint8_t*>(pb.k_cache);
+  p.dst[1] = static_cast<uint8_t*>(pb.v_cache);
+  p.scale[0] = pb.k_scale;
+  p.scale[1] = pb.v_scale;
+  p.lens = pb.cache_lens;
+  p.new_lens = pb.new_lens;
+  p.ss[0] = pb.skn;
+  p.ss[1] = pb.svn;
+  p.sd[0] = pb.skc;
+  p.sd[1] = pb.svc;
+  p.H = pb.H;
+  p.n_new = pb.n_new;
+  p.L_max = pb.L_max;
+  p.T = pb.block_tokens;
+  p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
+  p.touched = cache_blocks_touched(pb.n_new, pb.L_max, pb.block_tokens);
+  const long long units = 2LL * pb.B * pb.H * p.touched;
+  return pb.e4m3 ? launch_append<true>(p, units, pb.d / 8, ctx.stream)
+                 : launch_append<false>(p, units, pb.d / 8, ctx.stream);
+}
+
+int cache_blocks_touched(int n_new, int L_max, int block_tokens) {
+  // n_new tokens that start on a block's last row reach this many blocks
+  const long long n = (static_cast<long long>(n_new) + block_tokens - 2) / block_tokens + 1;
+  const long long all = (static_cast<long long>(L_max) + block_tokens - 1) / block_tokens;
+  return static_cast<int>(n < all ? n : all);
+}
+
+}  // namespace attn

@@ -1,0 +1,12 @@
+// attn_decode_scored_int8.cu -- the decoding step with changed scores
+// (attn_decode_scored.cuh) for a cache of int8 rows.
+#include "attn_decode_scored.cuh"
+
+namespace attn {
+
+cudaError_t launch_decode_scored_int8(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
+                                    float* workspace, const LaunchCtx& ctx) {
+  return launch_scored_decode_fmt<kCacheInt8>(pb, plan, workspace, ctx);
+}
+
+}  // namespace attn

@@ -154,6 +154,56 @@ bool bwd_head_size_ok(int d);
 cudaError_t launch_bwd(const BwdProblem& pb, const CUtensorMap* maps, void* workspace,
                        const LaunchCtx& ctx);
 
+// New keys and values into an 8-bit cache with a scale per block of tokens.
+struct CacheAppendProblem {
+  const void* k_new;  // bf16 [B, H, n_new, d]
+  const void* v_new;
+  void* k_cache;  // 8-bit codes [B, H, L_max, d]
+  void* v_cache;
+  float* k_scale;  // [B, H, ceil(L_max / block_tokens)]
+  float* v_scale;
+  int B, H, n_new, L_max, d;
+  bool e4m3;  // else int8
+  int block_tokens;
+  const int* cache_lens;  // device int32[B] or null (empty caches)
+  const int* new_lens;    // device int32[B] or null (n_new each)
+  RowStrides skn, svn, skc, svc;
+};
+cudaError_t launch_cache_append(const CacheAppendProblem& pb, const LaunchCtx& ctx);
+// Blocks that the new tokens of one sequence can fall into.
+int cache_blocks_touched(int n_new, int L_max, int block_tokens);
+
+// Decoding with changed scores against a bf16, e4m3 or int8 cache.
+struct ScoredDecodeProblem {
+  const void* q;  // bf16 [B, H, n_q, d]
+  const void* k_cache;  // [B, HK, L_max, d]
+  const void* v_cache;
+  const float* k_scale;  // [B, HK, ceil(L_max / block_tokens)]; unused for bf16
+  const float* v_scale;
+  void* o;
+  float* lse;  // or null
+  int B, H, HK, n_q, L_max, d, block_tokens;
+  float scale, softcap;  // softcap <= 0: none
+  const float* slopes;   // device float[H] or null
+  const int* cache_lens;  // device int32[B] or null
+  int window;  // -1: every key up to the query
+  RowStrides sq, sk, sv, so;
+};
+struct ScoredDecodePlan {
+  int row_tile, row_tiles;  // query rows of one key head per CTA, and how many such tiles
+  int splits;
+  size_t workspace_bytes;
+};
+// seen: the most keys one call can read per sequence.
+ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int d, int elem_bytes,
+                                    int num_sms);
+cudaError_t launch_decode_scored_bf16(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
+                                      float* workspace, const LaunchCtx& ctx);
+cudaError_t launch_decode_scored_e4m3(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
+                                      float* workspace, const LaunchCtx& ctx);
+cudaError_t launch_decode_scored_int8(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
+                                      float* workspace, const LaunchCtx& ctx);
+
 // Diagnostics.  The tensor maps are 2-D (64, 128) bf16, one box each.
 cudaError_t launch_diag_tile(const CUtensorMap& tmq, const CUtensorMap& tmk,
                              const CUtensorMap& tmv, const void* p, float* s, float* o,

@@ -360,6 +360,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 1 / x on the special-function unit (PTX rcp.approx.ftz.f32, at most 1 ulp off).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // max(a, b, c) in one instruction (three-input max.f32, sm_100 and later).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
