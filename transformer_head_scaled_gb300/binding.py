@@ -8,6 +8,7 @@ missing, :func:`load` raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -606,41 +607,45 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     return dq, dk, dv
 
 
-def _stream_of(device: torch.device, stream) -> torch.cuda.Stream:
-    """The stream a call runs on: `stream` (a torch stream or a raw pointer), or
-    the current stream of the tensors' device."""
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if hasattr(stream, "cuda_stream"):
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
-
-
-class _launch_on:
+class _call_on:
     """Makes the tensors' device current for a call, and the call's stream too,
-    so that a workspace allocated for it belongs to that stream."""
+    so that what is allocated for it belongs to that stream; gives the stream's
+    pointer.  Nothing has to be switched for a call on the current stream of the
+    current device."""
+
+    __slots__ = ("_device", "_stream")
 
     def __init__(self, device: torch.device, stream):
-        self._device = torch.cuda.device(device)
-        self._at = device, stream
+        self._device = None
+        if stream is not None or device.index != torch.cuda.current_device():
+            self._device = torch.cuda.device(device)
+        self._stream = stream if self._device is not None else device.index
 
     def __enter__(self) -> int:
+        if self._device is None:
+            return torch._C._cuda_getCurrentRawStream(self._stream)
         self._device.__enter__()
-        stream = _stream_of(*self._at)
+        stream = self._stream
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
         self._stream = torch.cuda.stream(stream)
         self._stream.__enter__()
         return int(stream.cuda_stream)
 
     def __exit__(self, *exc):
-        self._stream.__exit__(*exc)
-        self._device.__exit__(*exc)
+        if self._device is not None:
+            self._stream.__exit__(*exc)
+            self._device.__exit__(*exc)
 
 
 def _views(what: str, dtype, *tensors) -> None:
     """[B, h, n, d] CUDA views of one dtype on one device with unit last stride."""
+    device = tensors[0].device
     for t in tensors:
-        if (not t.is_cuda or t.dtype != dtype or t.dim() != 4 or t.stride(-1) != 1
-                or t.device != tensors[0].device):
+        if (t.dtype != dtype or t.dim() != 4 or t.device != device or not t.is_cuda
+                or t.stride(3) != 1):
             raise ValueError(f"{what} must be {dtype} CUDA [B, h, n, d] views on one device with "
                              "unit last stride")
 
@@ -657,16 +662,20 @@ def _strides(*tensors):
     dimension of one entry is never stepped over, whatever the view says."""
     flat = []
     for t in tensors:
-        room = max(t.shape[2] * t.shape[3], 1) if t.numel() else 1
-        for dim in range(3):
-            step = t.stride(dim)
-            flat.append(step if t.shape[dim] > 1 else -(-max(step, room) // 16) * 16)
+        step, shape = t.stride(), t.shape
+        if 1 in shape[:3]:
+            room = -(-max(*step, shape[2] * shape[3]) // 16) * 16
+            flat += [step[i] if shape[i] > 1 else room for i in range(3)]
+        else:
+            flat += step[:3]
     return flat
 
 
-def _strides_ptr(strides):
-    return ctypes.cast((ctypes.c_int64 * len(strides))(*[int(x) for x in strides]),
-                       ctypes.c_void_p)
+_INT64S = {n: ctypes.c_int64 * n for n in (12, 24)}
+
+
+def _strides_array(strides):
+    return None if strides is None else _INT64S[len(strides)](*strides)
 
 
 def _workspace(need: int, given, device):
@@ -676,7 +685,7 @@ def _workspace(need: int, given, device):
     if given is not None:
         if given.device != device or not given.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {device}")
-        if given.numel() * given.element_size() >= need:
+        if _nbytes(given) >= need:
             return given
     return torch.empty(need, dtype=torch.uint8, device=device)
 
@@ -691,8 +700,7 @@ def attn_cache_append_raw(k_new_ptr, v_new_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, B,
     """The C call itself, on raw device pointers; ``strides`` = 12 element counts or None."""
     return load().attn_cache_append(
         k_new_ptr, v_new_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, B, h, n_new, L_max, d,
-        None if strides is None else _strides_ptr(strides), int(cache_format), int(block_tokens),
-        lens_ptr, new_lens_ptr, stream_ptr)
+        _strides_array(strides), cache_format, block_tokens, lens_ptr, new_lens_ptr, stream_ptr)
 
 
 def attn_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.Tensor,
@@ -721,13 +729,19 @@ def attn_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.T
         _vector(name, t, torch.float32, B * h * -(-L_max // block_tokens), dev)
     _vector("cache_lens", cache_lens, torch.int32, B, dev)
     _vector("new_lens", new_lens, torch.int32, B, dev)
-    with _launch_on(dev, stream) as ptr:
+    with _call_on(dev, stream) as ptr:
         rc = attn_cache_append_raw(_ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
                                    _ptr(k_scale), _ptr(v_scale), B, h, n_new, L_max, d,
                                    _strides(k_new, v_new, k_cache, v_cache), fmt, block_tokens,
                                    _ptr(cache_lens), _ptr(new_lens), ptr)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_append")
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_scored_bytes(device: int, *sizes) -> int:
+    """The workspace size follows from the sizes and the device alone."""
+    return int(load().attn_decode_scored_workspace_bytes(*sizes))
 
 
 def decode_scored_workspace_bytes(B: int, h: int, h_kv: int, n_q: int, L_max: int, d: int,
@@ -744,9 +758,8 @@ def attn_decode_scored_raw(q_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, o_ptr, lse_ptr, 
     """The C call itself, on raw device pointers; ``strides`` = 12 element counts or None."""
     return load().attn_decode_scored(
         q_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, o_ptr, lse_ptr, B, h, h_kv, n_q, L_max, d,
-        None if strides is None else _strides_ptr(strides), int(cache_format), int(block_tokens),
-        float(scale), float(softcap), slopes_ptr, lens_ptr, int(window), ws_ptr, int(ws_bytes),
-        stream_ptr)
+        _strides_array(strides), cache_format, block_tokens, scale, softcap, slopes_ptr, lens_ptr,
+        window, ws_ptr, ws_bytes, stream_ptr)
 
 
 def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -788,22 +801,25 @@ def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         raise ValueError("window must be >= 0 (None for none)")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    with _launch_on(dev, stream) as ptr:
+    with _call_on(dev, stream) as ptr:
         if out is None:
             out = torch.empty((B, h, n_q, d), dtype=q.dtype, device=dev)
-        _views("q and out", torch.bfloat16, q, out)
-        if out.shape != q.shape:
-            raise ValueError("out must be shaped like q")
+        else:
+            _views("q and out", torch.bfloat16, q, out)
+            if out.shape != q.shape:
+                raise ValueError("out must be shaped like q")
         if lse is None:
             lse = torch.empty((B, h, n_q), dtype=torch.float32, device=dev)
-        _vector("lse", lse, torch.float32, B * h * n_q, dev)
+        else:
+            _vector("lse", lse, torch.float32, B * h * n_q, dev)
+        window = -1 if window is None else window
         workspace = _workspace(
-            decode_scored_workspace_bytes(B, h, h_kv, n_q, L_max, d, fmt, window), workspace, dev)
+            _decode_scored_bytes(dev.index, B, h, h_kv, n_q, L_max, d, fmt, window), workspace, dev)
         rc = attn_decode_scored_raw(
             _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(out),
             _ptr(lse), B, h, h_kv, n_q, L_max, d, _strides(q, k_cache, v_cache, out), fmt,
             block_tokens, scale, softcap, _ptr(slopes), _ptr(cache_lens),
-            -1 if window is None else window, _ptr(workspace), _nbytes(workspace), ptr)
+            window, _ptr(workspace), _nbytes(workspace), ptr)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_scored")
     return out, lse

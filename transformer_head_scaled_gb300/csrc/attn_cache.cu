@@ -76,17 +76,16 @@ __device__ __forceinline__ float decode1(uint32_t byte) {
 // warp per block, eight blocks to a CTA; else one CTA per block.
 template <bool E4M3, bool WARP, int THREADS, int CHUNKS>
 __global__ void __launch_bounds__(WARP ? 256 : THREADS)
-    attn_cache_append_kernel(const CacheParams p, long long units, int chunks_per_row) {
+    attn_cache_append_kernel(const CacheParams p, unsigned units, int cpr_log2) {
   __shared__ float red[WARP ? 1 : THREADS / 32];
-  const long long unit =
-      WARP ? static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+  const unsigned unit = WARP ? blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && unit >= units) return;
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
   // unit = ((b * H + head) * touched + block) * 2 + (keys or values)
-  const int kv = static_cast<int>(unit & 1);
-  const long long rest = unit >> 1;
-  const long long bh = rest / p.touched;
-  const int b = static_cast<int>(bh / p.H), hh = static_cast<int>(bh - b * static_cast<long long>(p.H));
+  const int kv = unit & 1u;
+  const unsigned rest = unit >> 1;
+  const unsigned bh = rest / static_cast<unsigned>(p.touched);
+  const int b = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(b) * p.H;
   const int len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
   const int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
   const int end = min(len + more, p.L_max);  // tokens that do not fit are dropped
@@ -98,7 +97,7 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   const __nv_bfloat16* src = p.src[kv] + b * p.ss[kv].b + hh * p.ss[kv].h +
                              static_cast<long long>(first - len) * p.ss[kv].n;
   uint8_t* dst = p.dst[kv] + b * p.sd[kv].b + hh * p.sd[kv].h;
-  const int chunks = (last - first) * chunks_per_row;
+  const int chunks = (last - first) << cpr_log2;  // 8-element chunks, a row's side by side
 
   uint4 w[CHUNKS];
   float top = 0.f;
@@ -106,13 +105,13 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   for (int i = 0; i < CHUNKS; ++i) {
     const int c = tid + i * THREADS;
     if (c < chunks) {
-      const int r = c / chunks_per_row;
-      w[i] = __ldg(reinterpret_cast<const uint4*>(src + r * p.ss[kv].n) + (c - r * chunks_per_row));
+      const int r = c >> cpr_log2;
+      w[i] = __ldg(reinterpret_cast<const uint4*>(src + r * p.ss[kv].n) + (c - (r << cpr_log2)));
     } else {
       w[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  float* scale_at = p.scale[kv] + bh * p.num_blocks + blk;
+  float* scale_at = p.scale[kv] + static_cast<long long>(bh) * p.num_blocks + blk;
   const float held = first > row0 ? *scale_at : 0.f;
 #pragma unroll
   for (int i = 0; i < CHUNKS; ++i) {
@@ -139,7 +138,7 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   for (int i = 0; i < CHUNKS; ++i) {
     const int c = tid + i * THREADS;
     if (c >= chunks) break;
-    const int r = c / chunks_per_row;
+    const int r = c >> cpr_log2;
     const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
     const float2 f0 = __bfloat1622float2(x[0]), f1 = __bfloat1622float2(x[1]),
                  f2 = __bfloat1622float2(x[2]), f3 = __bfloat1622float2(x[3]);
@@ -147,17 +146,17 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
     out.x = encode4<E4M3>(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv);
     out.y = encode4<E4M3>(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv);
     *(reinterpret_cast<uint2*>(dst + static_cast<long long>(first + r) * p.sd[kv].n) +
-      (c - r * chunks_per_row)) = out;
+      (c - (r << cpr_log2))) = out;
   }
   if (scale != held) {
     if (tid == 0) *scale_at = scale;
     // the rows the block held are rescaled; rows behind the new ones stay
     const float ratio = held * inv;
-    const int old = (first - row0) * chunks_per_row;
+    const int old = (first - row0) << cpr_log2;
     for (int c = tid; c < old; c += THREADS) {
-      const int r = c / chunks_per_row;
+      const int r = c >> cpr_log2;
       uint2* at = reinterpret_cast<uint2*>(dst + static_cast<long long>(row0 + r) * p.sd[kv].n) +
-                  (c - r * chunks_per_row);
+                  (c - (r << cpr_log2));
       uint2 v = *at;
       uint32_t* words = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
@@ -172,19 +171,18 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
 }
 
 template <bool E4M3>
-cudaError_t launch_append(const CacheParams& p, long long units, int chunks_per_row,
-                          cudaStream_t stream) {
+cudaError_t launch_append(const CacheParams& p, unsigned units, int cpr_log2, cudaStream_t stream) {
   // most 8-element chunks of new tokens that one block can get
-  const int most = (p.n_new < p.T ? p.n_new : p.T) * chunks_per_row;
+  const int most = (p.n_new < p.T ? p.n_new : p.T) << cpr_log2;
   if (most <= 4 * 32) {
-    const unsigned grid = static_cast<unsigned>((units + 7) / 8);
-    attn_cache_append_kernel<E4M3, true, 32, 4><<<grid, 256, 0, stream>>>(p, units, chunks_per_row);
+    attn_cache_append_kernel<E4M3, true, 32, 4>
+        <<<(units + 7) / 8, 256, 0, stream>>>(p, units, cpr_log2);
   } else if (most <= 4 * 128) {
-    attn_cache_append_kernel<E4M3, false, 128, 4>
-        <<<static_cast<unsigned>(units), 128, 0, stream>>>(p, units, chunks_per_row);
+    attn_cache_append_kernel<E4M3, false, 128, 4><<<units, 128, 0, stream>>>(p, units, cpr_log2);
+  } else if (most <= 4 * 256) {
+    attn_cache_append_kernel<E4M3, false, 256, 4><<<units, 256, 0, stream>>>(p, units, cpr_log2);
   } else {
-    attn_cache_append_kernel<E4M3, false, 256, 8>
-        <<<static_cast<unsigned>(units), 256, 0, stream>>>(p, units, chunks_per_row);
+    attn_cache_append_kernel<E4M3, false, 512, 4><<<units, 512, 0, stream>>>(p, units, cpr_log2);
   }
   return cudaGetLastError();
 }
@@ -211,9 +209,11 @@ cudaError_t launch_cache_append(const CacheAppendProblem& pb, const LaunchCtx& c
   p.T = pb.block_tokens;
   p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
   p.touched = cache_blocks_touched(pb.n_new, pb.L_max, pb.block_tokens);
-  const long long units = 2LL * pb.B * pb.H * p.touched;
-  return pb.e4m3 ? launch_append<true>(p, units, pb.d / 8, ctx.stream)
-                 : launch_append<false>(p, units, pb.d / 8, ctx.stream);
+  const unsigned units = 2u * pb.B * pb.H * p.touched;  // the caller keeps it below 2^31
+  int cpr_log2 = 1;  // 8-element chunks of a row
+  while ((8 << cpr_log2) < pb.d) ++cpr_log2;
+  return pb.e4m3 ? launch_append<true>(p, units, cpr_log2, ctx.stream)
+                 : launch_append<false>(p, units, cpr_log2, ctx.stream);
 }
 
 int cache_blocks_touched(int n_new, int L_max, int block_tokens) {
