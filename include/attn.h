@@ -319,8 +319,10 @@ int attn_cache_append(const void* k_new, const void* v_new, void* k_cache, void*
  *   cache_lens : device int32[B] (clamped to [0, L_max]), or NULL: all L_max.
  *   window   : >= 0, or -1 for none.
  *   workspace, workspace_bytes : at least attn_decode_scored_workspace_bytes(...)
- *              bytes, 16-byte aligned; may be NULL when that is 0.
- *   d_k      : 16, 32, 64 or 128, B*h*n_q <= 2^24, L_max <= 2^30 (else
+ *              bytes, 16-byte aligned; may be NULL when that is 0.  Its contents
+ *              on entry do not matter; calls that may overlap need one each.
+ *   d_k      : 16, 32, 64 or 128, B*h*n_q <= 2^24, L_max <= 2^30 and fewer than
+ *              2^31 groups of 16 keys over all sequences and key heads (else
  *              ATTN_ERR_UNSUPPORTED).
  * 8-bit codes enter the products exactly; probabilities are rounded to f16
  * (8-bit caches) or bf16 before the second product.
@@ -332,8 +334,8 @@ int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
                        const float* slopes, const int* cache_lens, int window, void* workspace,
                        size_t workspace_bytes, struct CUstream_st* stream);
 
-/* Scratch bytes attn_decode_scored needs on the current device (0 when no
- * split is needed, or for unsupported sizes). */
+/* Scratch bytes attn_decode_scored needs on the current device (0 when
+ * none is needed, or for unsupported sizes). */
 size_t attn_decode_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int L_max, int d_k,
                                           int cache_format, int window);
 

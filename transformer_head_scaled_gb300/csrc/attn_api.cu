@@ -820,6 +820,30 @@ bool read_strides(Strides* st, const int64_t* in, int count, const int* heads, c
 
 bool int_ptr_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// A cache as 4-D (row bytes, L_max, h, B) bytes with a (min(row bytes, 128),
+// tile keys, 1, 1) box in the widest swizzle a box row fits; strides in
+// elements of `elem` bytes.
+int encode_4d_bytes(CUtensorMap* map, const void* base, int row_bytes, int n, int h, int B,
+                    Strides st, int elem) {
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(n),
+                        static_cast<cuuint64_t>(h), static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.n) * elem,
+                           static_cast<cuuint64_t>(st.h) * elem,
+                           static_cast<cuuint64_t>(st.b) * elem};
+  const int inner = row_bytes < 128 ? row_bytes : 128;
+  const CUtensorMapSwizzle swz = inner == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                 : inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                 : inner == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
+                                               : CU_TENSOR_MAP_SWIZZLE_NONE;
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(inner),
+                       static_cast<cuuint32_t>(scored_decode_tile_keys(row_bytes)), 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
 int elem_bytes(int cache_format) { return cache_format == ATTN_CACHE_BF16 ? 2 : 1; }
 
 // The most keys n_q queries with this window see.
@@ -836,8 +860,11 @@ int scored_decode_sizes(int B, int h, int h_kv, int n_q, int L_max, int d_k, int
     return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * h > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   if (!tc_head_size(d_k) || n_q > kDecodeMaxQueries) return ATTN_ERR_UNSUPPORTED;
-  // one CTA per key head, row tile and chunk: a grid of at most 2^31 - 1
-  if (static_cast<long long>(B) * h * n_q > (1LL << 24) || L_max > (1 << 30))
+  // the kernel counts the visible cache's tiles of 16 keys or more, over all
+  // sequences and key heads (and tiles of query rows), in 31 bits
+  if (static_cast<long long>(B) * h * n_q > (1LL << 24) || L_max > (1 << 30) ||
+      static_cast<long long>(B) * h_kv * ((h / h_kv * n_q + 31) / 32) * (L_max / 16 + 2LL) >
+          0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
@@ -922,16 +949,21 @@ int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
   if (plan.workspace_bytes > 0 &&
       (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
     return ATTN_ERR_INVALID_ARG;
-  ScoredDecodeProblem pb{q, k_cache, v_cache, k_scale, v_scale, o, lse, B, h, h_kv, n_q, L_max,
+  CUtensorMap maps[2];
+  if ((rc = encode_4d_bytes(&maps[0], k_cache, d_k * e1, L_max, h_kv, B, st[1], e1)) != ATTN_OK)
+    return rc;
+  if ((rc = encode_4d_bytes(&maps[1], v_cache, d_k * e1, L_max, h_kv, B, st[2], e1)) != ATTN_OK)
+    return rc;
+  ScoredDecodeProblem pb{q, k_scale, v_scale, o, lse, B, h, h_kv, n_q, L_max,
                          d_k, q8 ? block_tokens : 128, scale, softcap, slopes, cache_lens,
-                         window < L_max ? window : -1, st[0], st[1], st[2], st[3]};
+                         window < L_max ? window : -1, st[0], st[3]};
   const LaunchCtx ctx = make_ctx(*di, stream);
   float* ws = static_cast<float*>(workspace);
-  const cudaError_t e = cache_format == ATTN_CACHE_BF16   ? launch_decode_scored_bf16(pb, plan, ws, ctx)
-                        : cache_format == ATTN_CACHE_E4M3 ? launch_decode_scored_e4m3(pb, plan, ws, ctx)
-                                                          : launch_decode_scored_int8(pb, plan, ws, ctx);
+  const cudaError_t e = cache_format == ATTN_CACHE_BF16   ? launch_decode_scored_bf16(pb, maps, plan, ws, ctx)
+                        : cache_format == ATTN_CACHE_E4M3 ? launch_decode_scored_e4m3(pb, maps, plan, ws, ctx)
+                                                          : launch_decode_scored_int8(pb, maps, plan, ws, ctx);
   if (e != cudaSuccess) return cuda_fail(e);
-  g_launches.fetch_add(plan.splits > 1 ? 2 : 1);
+  g_launches.fetch_add(plan.whole ? 1 : 2);
   return ATTN_OK;
 }
 
@@ -945,21 +977,23 @@ ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int
   const int rows = H / HK * n_q;
   plan.row_tile = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
   plan.row_tiles = (rows + plan.row_tile - 1) / plan.row_tile;
-  // keys per warp and tile: about 4 KB of keys, as in the kernel
-  const int row_bytes = d * elem_bytes;
-  const int kt = row_bytes >= 256 ? 16 : (row_bytes >= 128 ? 32 : 64);
+  const int kt = scored_decode_tile_keys(d * elem_bytes);
   const long long units = static_cast<long long>(B) * HK * plan.row_tiles;
-  const int max_tiles = (seen + kt - 1) / kt;
-  // about four rounds of three resident CTAs per SM, so that unequal cache
-  // lengths even out, and at least two tiles for each of a CTA's four warps
-  const long long want = 4LL * 3 * num_sms;
-  long long splits = (want + units - 1) / units;
-  if (splits > max_tiles / 8) splits = max_tiles / 8;
-  if (splits < 1) splits = 1;
-  plan.splits = static_cast<int>(splits);
-  plan.workspace_bytes = splits > 1 ? static_cast<size_t>(units) * splits * plan.row_tile *
-                                          (d + 2) * sizeof(float)
-                                    : 0;
+  const long long most = (seen + 15 + kt - 1) / kt;  // tiles of a unit; a window may start inside a group
+  const long long resident = static_cast<long long>(num_sms) * scored_decode_warps(plan.row_tile);
+  plan.whole = units * 2 >= resident && most <= 32;
+  if (plan.whole) {
+    plan.warps = static_cast<int>(units < resident ? units : resident);
+    plan.part_off = plan.workspace_bytes = 0;
+    return plan;
+  }
+  // every resident warp takes a share of the tiles, if there are that many
+  const long long useful = (units * most + scored_decode_min_tiles() - 1) / scored_decode_min_tiles();
+  plan.warps = static_cast<int>(useful < resident ? useful : resident);
+  // the sequences' first tiles, then two partial results per warp
+  plan.part_off = (static_cast<size_t>(B) + 1 + 3) / 4 * 4;
+  plan.workspace_bytes = (plan.part_off + static_cast<size_t>(plan.warps) * 2 * plan.row_tile *
+                                              (d + 2)) * sizeof(float);
   return plan;
 }
 

@@ -33,11 +33,20 @@
 // multiplies in bf16, P rounded to bf16 as in the forward.  Softmax
 // statistics, scores and accumulators are fp32.
 //
-// One CTA of four warps works on one chunk of one key head's cache; warp w
-// takes every fourth tile of KT keys with its own running softmax, the warps
-// are merged in shared memory, and chunks through the workspace by a second
-// kernel.  A warp asks for a tile's values before its scores and for the next
-// tile's keys before its softmax, so about KT rows are in flight per warp.
+// Work split, two ways (scored_decode_plan chooses):
+//  * whole: every warp takes whole units (a unit is one sequence, key head and
+//    tile of query rows), the w-th, the (w + W)-th and so on, and writes them
+//    out.  For caches short enough that the longest one is a short job for one
+//    warp, and enough of them to occupy the SMs.
+//  * split: the visible cache is one list of tiles of KT keys, unit by unit, and
+//    every resident warp takes an equal run of it, whatever the lengths are; a
+//    run may end one unit and begin another.  Units that several warps share go
+//    through the workspace to a second kernel.
+// Either way a warp keeps its own running softmax and its own ring of STAGES
+// tiles in shared memory, filled by TMA across unit boundaries: it waits for
+// its own copies only, never for another warp, and memory stays busy while it
+// computes.
+//
 #pragma once
 
 #include <cuda_bf16.h>
@@ -62,23 +71,26 @@ constexpr float kRescale = 8.0f;
 
 struct ScoredDecParams {
   const __nv_bfloat16* q;
-  const uint8_t* k;
-  const uint8_t* v;
   const float* k_scale;
   const float* v_scale;
   __nv_bfloat16* o;
   float* lse;
-  float* part;  // [unit][split][rows of the unit][D + 2]
+  float* part;        // [warp][2][query rows][D + 2]: O, running maximum, row sum
+  unsigned* first;  // split: [B + 1], the list index of each sequence's first tile, and the total
   const int* cache_lens;
   const float* slopes;
-  RowStrides sq, sk, sv, so;
-  int HK, G, n_q, L_max, T_log2, num_blocks, window, splits, row_tiles;
+  RowStrides sq, so;
+  uint64_t limit_ns;
+  int* status;
+  int B, HK, G, n_q, L_max, T_log2, num_blocks, window, row_tiles;
+  int warps, units;
+  bool whole;
   float scale, softcap;
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -86,7 +98,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
 }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -116,57 +128,80 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   }
 }
 
-// BYTES (2, 4, 8 or 16) from global memory into the first words of w.
+// BYTES (2, 4, 8 or 16) from shared memory into the first words of w.
 template <int BYTES>
-__device__ __forceinline__ void load_bytes(const uint8_t* src, bool in, uint32_t* w) {
+__device__ __forceinline__ void load_bytes(const uint8_t* at, uint32_t* w) {
   if (BYTES == 16) {
-    const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
     w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
   } else if (BYTES == 8) {
-    const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
+    const uint2 x = *reinterpret_cast<const uint2*>(at);
     w[0] = x.x, w[1] = x.y;
   } else if (BYTES == 4) {
-    w[0] = in ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
   } else {
-    w[0] = in ? __ldg(reinterpret_cast<const uint16_t*>(src)) : 0u;
+    w[0] = *reinterpret_cast<const uint16_t*>(at);
   }
 }
+
+// Keys per warp and tile for rows of `row_bytes`: 2 KB of keys, 16 to 64 of them.
+constexpr int scored_tile_keys(int row_bytes) {
+  return row_bytes >= 128 ? 16 : (row_bytes >= 64 ? 32 : 64);
+}
+
+// Resident CTAs per SM that the registers allow, by row tiles.
+constexpr int scored_ctas(int row_tiles) { return row_tiles > 1 ? 2 : 4; }
+// A warp's run is at least this many tiles: below it the start of a run and the
+// join of its result cost more than the tiles.
+constexpr int kMinTiles = 2;
 
 // Shapes per cache format, head size D and row tiles (8 queries each).
 template <int FMT_, int D_, int NR_>
 struct DCfg {
   static constexpr int FMT = FMT_, D = D_, NR = NR_;
   static constexpr int ES = FMT_ == kCacheBf16 ? 2 : 1;
-  static constexpr int RB = D_ * ES;  // bytes of a cache row
-  // keys per warp and tile: about 4 KB of keys, or 2 KB where the accumulators
-  // of more query rows need the registers
-  static constexpr int KT1 = RB >= 256 ? 16 : (RB >= 128 ? 32 : 64);
-  static constexpr int KT = NR_ > 1 && KT1 > 16 ? KT1 / 2 : KT1;
+  static constexpr int RB = D_ * ES;               // bytes of a cache row
+  static constexpr int BB = RB < 128 ? RB : 128;   // bytes of a row in one TMA box
+  static constexpr int NB = RB / BB;               // boxes per tile
+  static constexpr int KT = scored_tile_keys(RB);
+  static constexpr uint32_t TILE = KT * RB;        // a tile of keys (or of values)
+  static constexpr uint32_t BOX = KT * BB;
+  static constexpr int STAGES = 3;
   static constexpr int NT = KT / 8;   // 8-key column tiles of S
   static constexpr int NG = KT / 16;  // 16-key groups (one k step of O^T)
-  // K: a lane's share of a row, in loads of KV bytes
+  // K: a lane's quarter of a row, in loads of KV bytes
   static constexpr int KV = RB / 4 < 16 ? RB / 4 : 16;
-  static constexpr int KL = RB / 4 / KV;
   static constexpr int KW = KV / 4;          // words per load
   static constexpr int KE = KV / ES;         // elements per load
+  static constexpr int KB = BB / 4 / KV;     // loads per box
+  static constexpr int KL = NB * KB;         // loads per row
   static constexpr int KS = D_ / 16;         // k steps of S
-  // V: a lane's share of a row, in loads of VV bytes
-  static constexpr int VV = RB / 8 < 16 ? RB / 8 : 16;
-  static constexpr int VL = RB / 8 / VV;
+  // V: a lane's eighth of a row, in loads of VV bytes, one per box
+  static constexpr int VV = BB / 8;
   static constexpr int VW = VV < 4 ? 1 : VV / 4;
   static constexpr int VE = VV / ES;
-  static constexpr int MT = D_ / 16;         // 16-row tiles of O^T
+  static constexpr int MT = D_ / 16;                // 16-row tiles of O^T
   static constexpr int MQ = NR_ > 1 ? NR_ / 2 : 1;  // 16-query tiles of S
-  // CTAs per SM that the registers allow
-  static constexpr int CTAS = NR_ > 1 ? 2 : 3;
+  static constexpr uint32_t RING = STAGES * 2 * TILE;  // shared memory of a warp
+  static constexpr int CTAS = scored_ctas(NR_);
+  // Which key of an 8-key tile is column c: an order in which neither the rows
+  // that a key load touches nor those of a value load share banks.
+  static constexpr uint32_t ORDER = RB == 64 ? 0x65742130u : (RB == 32 ? 0x57463120u : 0x76543210u);
+  __device__ static constexpr int key_of(int c) { return (ORDER >> (4 * c)) & 7; }
+  // the 16-byte chunk position XOR of row r inside its swizzle atom
+  __device__ static constexpr uint32_t swz(uint32_t r) {
+    return BB >= 32 ? ((r * BB) >> 7) & (BB / 16 - 1) : 0u;
+  }
+  static_assert(RB >= 128 || NB == 1, "one box");
 };
 
-// One element pair per lane and m16n8k16 step s: which elements of a row
-// lane t holds is  load i, elements 4 s' .. 4 s' + 3  with s = i * KE/4 + s'.
+// The d index of the first element that lane t holds for k step s of S: the
+// lane's words in load order, four elements per step.
 template <class C>
 __device__ __forceinline__ int key_elem(int step, int t) {
-  constexpr int per = C::KE / 4;
-  return (step / per) * 4 * C::KE + t * C::KE + 4 * (step % per);
+  constexpr int per = C::KE / 4;  // steps per load
+  const int load = step / per, box = load / C::KB, i = load % C::KB;
+  return box * (C::BB / C::ES) + (t * C::KB + i) * C::KE + 4 * (step % per);
 }
 // The d index of a lane's e-th value element (group g).
 template <class C>
@@ -174,89 +209,211 @@ __device__ __forceinline__ int val_elem(int e, int g) {
   return (e / C::VE) * 8 * C::VE + g * C::VE + e % C::VE;
 }
 
+// The visible keys of a sequence, in tiles.
+struct SeqTiles {
+  int L;      // tokens in the cache
+  int key0;   // first key that any of the queries sees
+  int base0;  // where its tiles begin: a 16-key boundary, so that no 16-key group
+              // crosses a scale block
+  int tiles;
+};
+template <int KT>
+__device__ __forceinline__ SeqTiles seq_tiles(const ScoredDecParams& p, int b) {
+  SeqTiles s;
+  s.L = p.L_max;
+  if (p.cache_lens != nullptr) s.L = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
+  s.key0 = p.window >= 0 ? max(s.L - p.n_q - p.window, 0) : 0;
+  s.base0 = s.key0 & ~15;
+  s.tiles = (s.L - s.base0 + KT - 1) / KT;
+  return s;
+}
+
+// A place in a warp's work: a tile of a unit = b * subs + sub, sub = key head *
+// row_tiles + row tile.
+template <int KT>
+struct Cursor {
+  SeqTiles s;
+  int unit, b, sub, tile;
+  __device__ __forceinline__ void at_unit(const ScoredDecParams& p, int subs, int u) {
+    unit = u;
+    tile = 0;
+    const int nb = u / static_cast<unsigned>(subs);
+    sub = u - nb * subs;
+    if (nb != b) {
+      b = nb;
+      s = seq_tiles<KT>(p, b);
+    }
+  }
+  // the next unit of this warp; with skip, the next one that has tiles
+  __device__ __forceinline__ bool next(const ScoredDecParams& p, int subs, bool skip) {
+    const int step = p.whole ? p.warps : 1;
+    int u = unit;
+    do {
+      if (p.units - u <= step) return false;
+      u += step;
+      at_unit(p, subs, u);
+    } while (skip && s.tiles == 0);
+    return true;
+  }
+};
+
+// Tiles per warp: an equal share, kMinTiles at least.
+__device__ __forceinline__ unsigned share_of(unsigned total, int warps) {
+  const unsigned each = total / static_cast<unsigned>(warps) + 1;
+  return each < kMinTiles ? kMinTiles : each;
+}
+
 template <int FMT, int D, int NR>
 __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
-    attn_decode_scored_kernel(const ScoredDecParams p) {
+    attn_decode_scored_kernel(const __grid_constant__ CUtensorMap tmk,
+                              const __grid_constant__ CUtensorMap tmv, const ScoredDecParams p) {
   using C = DCfg<FMT, D, NR>;
   constexpr int KT = C::KT, NT = C::NT, NG = C::NG, MQ = C::MQ;
   constexpr bool Q8 = FMT != kCacheBf16;
   constexpr int ROWS = NR * 8;
-  extern __shared__ float sm[];  // per warp [ROWS][D + 2]: O, m, l
+  constexpr int RS = NR > 1 ? 2 : 1;  // used 8-row halves of a 16-query tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[DW][C::STAGES];
   grid_launch_dependents();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  // unit = ((b * HK + key head) * row_tiles + row tile) * splits + split
-  const int split = static_cast<int>(blockIdx.x % p.splits);
-  const long long unit = blockIdx.x / p.splits;
-  const int rt = static_cast<int>(unit % p.row_tiles);
-  const long long bk = unit / p.row_tiles;
-  const int b = static_cast<int>(bk / p.HK), hk = static_cast<int>(bk % p.HK);
+  const int subs = p.HK * p.row_tiles;
+  const int w = blockIdx.x * DW + warp;
+
+  // ---- where this warp's work begins, and how many tiles it is
+  Cursor<KT> cur;
+  cur.b = -1;
+  int count = 0;
+  if (p.whole) {
+    if (w >= p.warps) return;
+    cur.at_unit(p, subs, w);
+    Cursor<KT> c = cur;
+    do count += c.s.tiles;
+    while (c.next(p, subs, false));
+  } else {
+    __shared__ unsigned upto[DW * 32];  // tiles of the list up to each thread's sequences
+    __shared__ unsigned warp_sum[DW];
+    // thread i sums the sequences [i, i + 1) * per
+    const int per = (p.B + DW * 32 - 1) / (DW * 32);
+    const int seq0 = min(static_cast<int>(threadIdx.x) * per, p.B), seq1 = min(seq0 + per, p.B);
+    unsigned sum = 0;
+    for (int b = seq0; b < seq1; ++b) sum += seq_tiles<KT>(p, b).tiles;
+    sum *= subs;
+    unsigned run = sum;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, run, m);
+      if (lane >= m) run += x;
+    }
+    if (lane == 31) warp_sum[warp] = run;
+    __syncthreads();
+    unsigned total = 0;
+#pragma unroll
+    for (int i = 0; i < DW; ++i) {
+      if (i < warp) run += warp_sum[i];
+      total += warp_sum[i];
+    }
+    upto[threadIdx.x] = run;
+    if (blockIdx.x == 0) {  // for the second kernel
+      unsigned at = run - sum;
+      for (int b = seq0; b < seq1; ++b) {
+        p.first[b] = at;
+        at += seq_tiles<KT>(p, b).tiles * subs;
+      }
+      if (threadIdx.x == 0) p.first[p.B] = total;
+    }
+    __syncthreads();
+    const unsigned share = share_of(total, p.warps);
+    // (share * warps stays below 2^32: total < 2^31, and warps * kMinTiles is small)
+    const unsigned begin = share * w;
+    if (w >= p.warps || begin >= total) return;  // a whole warp; no barrier of the CTA follows
+    count = min(share, total - begin);
+    int chunk = 0;
+#pragma unroll
+    for (int i = 0; i < DW; ++i)
+      chunk += __popc(__ballot_sync(0xffffffffu, upto[i * 32 + lane] <= begin));
+    unsigned at = chunk > 0 ? upto[chunk - 1] : 0u;
+    int b = chunk * per;
+    for (;; ++b) {
+      cur.s = seq_tiles<KT>(p, b);
+      const unsigned here = static_cast<unsigned>(cur.s.tiles) * subs;
+      if (begin - at < here || b + 1 >= p.B) break;
+      at += here;
+    }
+    cur.b = b;
+    cur.sub = (begin - at) / static_cast<unsigned>(cur.s.tiles);
+    cur.tile = (begin - at) - static_cast<unsigned>(cur.sub) * cur.s.tiles;
+    cur.unit = b * subs + cur.sub;
+  }
+
+  // ---- this warp's ring
+  uint8_t* const ring_at = sm + warp * C::RING;
+  const uint32_t ring = smem_u32(ring_at);
+  const uint32_t bars = smem_u32(&full[warp][0]);
+  const int never = 0;
+  Cursor<KT> ahead = cur;  // where the next copy is from (lane 0)
+  if (ahead.s.tiles == 0) ahead.next(p, subs, true);
+  auto fill = [&](int n) {  // the run's tile n into its slot (one lane)
+    const uint32_t slot = n % C::STAGES, bar = bars + 8 * slot;
+    const int row = ahead.s.base0 + ahead.tile * KT;
+    const int hk = p.row_tiles == 1 ? ahead.sub : ahead.sub / p.row_tiles;
+    mbar_arrive_expect_tx(bar, 2 * C::TILE);
+#pragma unroll
+    for (int x = 0; x < C::NB; ++x) {
+      tma_load_4d(ring + slot * 2 * C::TILE + x * C::BOX, &tmk, bar, x * C::BB, row, hk, ahead.b);
+      tma_load_4d(ring + slot * 2 * C::TILE + C::TILE + x * C::BOX, &tmv, bar, x * C::BB, row, hk,
+                  ahead.b);
+    }
+    if (++ahead.tile == ahead.s.tiles) ahead.next(p, subs, true);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(bars + 8 * i, 1);
+    fence_mbar_init();
+    for (int n = 0; n < min(count, C::STAGES); ++n) fill(n);
+  }
+  __syncwarp();
+
+  // this lane's rows of an 8-key tile: one as a key, two (a column pair) as values
+  const int krow = C::key_of(g), vrow0 = C::key_of(2 * t), vrow1 = C::key_of(2 * t + 1);
+  const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
+  const float cap2 = p.softcap * kLog2e;
+  // a product times this is the score in log2 units, or the cap's exponent
+  const float unit_scale = p.scale * kLog2e * (capped ? 2.f / p.softcap : 1.f);
+
+  bool ok = true;
+  int it = 0;
+  do {
+  // ---- one unit of the work: `seg` of its tiles
+  const int seg = min(cur.s.tiles - cur.tile, count - it);
+  const int seg_it = it;
+  const bool leads = it == 0;
+  const int b = cur.b, hk = p.row_tiles == 1 ? cur.sub : cur.sub / p.row_tiles, rt = cur.sub - hk * p.row_tiles;
   const int rows = min(p.G * p.n_q - rt * ROWS, ROWS);  // query rows of this unit
-
-  int L = p.L_max;
-  if (p.cache_lens != nullptr) L = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
-  // keys any row of the unit can see, from a 16-key boundary on (so that a
-  // 16-key group never crosses a scale block)
-  const int key0 = p.window >= 0 ? max(L - p.n_q - p.window, 0) : 0;
-  const int base0 = key0 & ~15;
-  // an equal share of this sequence's tiles per split
-  const int tiles = (L - base0 + KT - 1) / KT;
-  const int per = (tiles + p.splits - 1) / p.splits;
-  const int tile_end = min(tiles, (split + 1) * per);
-  const int tile0 = split * per + warp;
-
-  const long long krow0 = (b * p.sk.b + hk * p.sk.h) * C::ES;
-  const long long vrow0 = (b * p.sv.b + hk * p.sv.h) * C::ES;
-  const uint8_t* kp = p.k + krow0 + t * C::KV;
-  const uint8_t* vp = p.v + vrow0 + g * C::VV;
-  const long long ksn = p.sk.n * C::ES, vsn = p.sv.n * C::ES;
-
-  uint32_t kr[NT][C::KL * C::KW];  // K: lane g's row of each 8-key tile
-  uint32_t vr[NG][4][C::VL * C::VW];  // V: keys 2t, 2t+1, 2t+8, 2t+9 of each group
-  float ks[NG], vs[NG];
+  const int L = cur.s.L, key0 = cur.s.key0, base0 = cur.s.base0 + cur.tile * KT;
+  const long long bk = static_cast<long long>(b) * p.HK + hk;
   const float* ksp = Q8 ? p.k_scale + bk * p.num_blocks : nullptr;
   const float* vsp = Q8 ? p.v_scale + bk * p.num_blocks : nullptr;
-
-  auto load_k = [&](int tile) {
-    const int base = base0 + tile * KT;
+  // one scale per 16-key group; a tile that lies in one block reads it once
+  const bool one_block = (1 << p.T_log2) >= KT && (base0 & (KT - 1)) == 0;
+  auto load_scales = [&](const float* from, int base, float (&to)[NG]) {
+    if (one_block) {
+      const float x = __ldg(from + (base >> p.T_log2));
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int j = base + 8 * n + g;
-      const bool in = j < L && j >= key0;
-      const uint8_t* src = kp + j * ksn;
+      for (int n = 0; n < NG; ++n) to[n] = x;
+    } else {
 #pragma unroll
-      for (int i = 0; i < C::KL; ++i)
-        load_bytes<C::KV>(src + 4 * C::KV * i, in, &kr[n][i * C::KW]);
-    }
-    if (Q8) {
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const int j = base + 16 * n;
-        ks[n] = j < L ? __ldg(ksp + (j >> p.T_log2)) : 0.f;
-      }
+      for (int n = 0; n < NG; ++n)
+        to[n] = base + 16 * n < L ? __ldg(from + ((base + 16 * n) >> p.T_log2)) : 0.f;
     }
   };
-  auto load_v = [&](int tile) {
-    const int base = base0 + tile * KT;
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = base + 16 * n + 2 * t + (e & 1) + (e >> 1) * 8;
-        const bool in = j < L && j >= key0;
-        const uint8_t* src = vp + j * vsn;
-#pragma unroll
-        for (int i = 0; i < C::VL; ++i)
-          load_bytes<C::VV>(src + 8 * C::VV * i, in, &vr[n][e][i * C::VW]);
-      }
-      if (Q8) {
-        const int j = base + 16 * n;
-        vs[n] = j < L ? __ldg(vsp + (j >> p.T_log2)) : 0.f;
-      }
-    }
-  };
-  if (tile0 < tile_end) load_k(tile0);
+  float ks[NG], vs[NG];
+  if (Q8 && seg > 0) {
+    load_scales(ksp, base0, ks);
+    load_scales(vsp, base0, vs);
+  }
 
   // Queries in operand form: rows g and g + 8 of each 16-query tile.
   uint32_t qa[MQ][C::KS][4];
@@ -284,13 +441,13 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
           top = fmaxf(fmaxf(fmaxf(top, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(y.x))), fabsf(y.y));
         }
       }
-      qscale[m][r] = p.scale;
+      qscale[m][r] = unit_scale;
       if (Q8) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max(min(static_cast<int>((__float_as_uint(top) >> 23) & 255u) - 127, 126), -126);
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        qscale[m][r] = p.scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        qscale[m][r] = unit_scale * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 #pragma unroll
         for (int s = 0; s < C::KS; ++s) {
 #pragma unroll
@@ -306,11 +463,6 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
       nslope[m][r] = p.slopes != nullptr && in ? -__ldg(p.slopes + head) * kLog2e : 0.f;
     }
   }
-  const bool capped = p.softcap > 0.f;
-  const float inv_cap = capped ? 1.f / p.softcap : 0.f;
-  const float cap2 = p.softcap * kLog2e;
-  const bool biased = p.slopes != nullptr;
-
   float m_run[MQ][2], l_run[MQ][2];
   float acc[C::MT][NR][4];
 #pragma unroll
@@ -325,9 +477,14 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
       for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
   float vref = 0.f, inv_vref = 0.f;  // the value scale that P is held relative to
 
-  for (int tile = tile0; tile < tile_end; tile += DW) {
-    const int base = base0 + tile * KT;
-    load_v(tile);
+  for (int k = 0; k < seg; ++k, ++it) {
+    const int base = base0 + k * KT;
+    const uint32_t slot = it % C::STAGES;
+    ok = __all_sync(0xffffffffu,
+                    mbar_wait(bars + 8 * slot, (it / C::STAGES) & 1, p.limit_ns, &never));
+    if (!ok) break;
+    const uint8_t* kt = ring_at + slot * 2 * C::TILE;
+    const uint8_t* vt = kt + C::TILE;
     // ---- S = Q K^T
     float s[MQ][NT][4];
 #pragma unroll
@@ -336,14 +493,24 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
       for (int m = 0; m < MQ; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[m][n][e] = 0.f;
+      const uint32_t r = 8 * n + krow;
+      uint32_t kr[C::KL * C::KW];
+#pragma unroll
+      for (int i = 0; i < C::KL; ++i) {
+        // byte t * KV * KB + i * KV of the row's box
+        const uint32_t byte = (t * C::KB + i % C::KB) * C::KV;
+        load_bytes<C::KV>(kt + (i / C::KB) * C::BOX + r * C::BB +
+                              ((byte & ~15u) ^ (C::swz(r) << 4)) + (byte & 15u),
+                          &kr[i * C::KW]);
+      }
 #pragma unroll
       for (int st = 0; st < C::KS; ++st) {
         uint32_t b0, b1;
         if (Q8) {
-          widen4<FMT>(kr[n][st], b0, b1);  // word st: elements 4 st .. 4 st + 3 of the lane
+          widen4<FMT>(kr[st], b0, b1);  // word st: elements 4 st .. 4 st + 3 of the lane
         } else {
-          b0 = kr[n][2 * st];
-          b1 = kr[n][2 * st + 1];
+          b0 = kr[2 * st];
+          b1 = kr[2 * st + 1];
         }
 #pragma unroll
         for (int m = 0; m < MQ; ++m) {
@@ -354,57 +521,71 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
         }
       }
     }
-    float kf[NG];
-#pragma unroll
-    for (int n = 0; n < NG; ++n) kf[n] = Q8 ? ks[n] : 1.f;
-    if (tile + DW < tile_end) load_k(tile + DW);
 
-    // ---- scores in log2 units, masked; their maximum per row
-    float mx[MQ][2];
+    // ---- scores in log2 units are s * f (f = 1 once the cap or the bias is
+    // in), masked; mx: this lane's largest of a row
+    float mx[MQ][2], f[MQ][2][NG];
 #pragma unroll
     for (int m = 0; m < MQ; ++m) {
 #pragma unroll
-      for (int r = 0; r < (NR > 1 ? 2 : 1); ++r) {
-        mx[m][r] = -INFINITY;
-        const float far = static_cast<float>(pos[m][r] - base);  // distance to the tile's first key
-        const bool whole =
-            base + KT - 1 <= pos[m][r] && base >= key0 &&
-            (p.window < 0 || base >= pos[m][r] - p.window);
+      for (int r = 0; r < RS; ++r) {
+        // (never 0, so that a masked score stays -inf)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float f = qscale[m][r] * kf[n / 2];
+        for (int n = 0; n < NG; ++n)
+          f[m][r][n] = Q8 ? fmaxf(qscale[m][r] * ks[n], 1e-37f) : qscale[m][r];
+        if (capped || biased) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = s[m][n][2 * r + c] * f;
-            if (capped) {
-              // tanh(y) = 1 - 2 / (1 + e^2y)
-              const float e2 = ex2(x * inv_cap * (2.f * kLog2e));
-              x = fmaf(-2.f * cap2, rcp(1.f + e2), cap2);
-            } else {
-              x *= kLog2e;
+          for (int n = 0; n < NT; ++n) {
+            s[m][n][2 * r] *= f[m][r][n / 2];
+            s[m][n][2 * r + 1] *= f[m][r][n / 2];
+          }
+#pragma unroll
+          for (int n = 0; n < NG; ++n) f[m][r][n] = 1.f;
+          if (capped) {
+            // tanh(y) = 1 - 2 / (1 + 2^(2 y log2(e))); the exponent is in place
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+                s[m][n][2 * r + c] = fmaf(-2.f * cap2, rcp(1.f + ex2(s[m][n][2 * r + c])), cap2);
+          }
+          if (biased) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              // distance to this lane's key of the first 8-key tile
+              const float far = static_cast<float>(pos[m][r] - base - (c ? vrow1 : vrow0));
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                s[m][n][2 * r + c] = fmaf(nslope[m][r], far - static_cast<float>(8 * n),
+                                          s[m][n][2 * r + c]);
             }
-            const int col = 8 * n + 2 * t + c;
-            if (biased) x = fmaf(nslope[m][r], far - static_cast<float>(col), x);
-            if (!whole) {
-              const int j = base + col;
-              if (j > pos[m][r] || j < key0 || (p.window >= 0 && j < pos[m][r] - p.window))
-                x = -INFINITY;
-            }
-            s[m][n][2 * r + c] = x;
-            mx[m][r] = fmaxf(mx[m][r], x);
           }
         }
+        // keys [lo, hi) of the tile are visible
+        const int hi = pos[m][r] + 1 - base;
+        const int lo = p.window >= 0 ? max(pos[m][r] - p.window, key0) - base : -base;
+        if (hi < KT || lo > 0) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int col = 8 * n + (c ? vrow1 : vrow0);
+              if (col >= hi || col < lo) s[m][n][2 * r + c] = -INFINITY;
+            }
+        }
+        mx[m][r] = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+          mx[m][r] = fmaxf(mx[m][r], f[m][r][n] * fmaxf(fmaxf(s[m][2 * n][2 * r], s[m][2 * n][2 * r + 1]),
+                                                        fmaxf(s[m][2 * n + 1][2 * r],
+                                                              s[m][2 * n + 1][2 * r + 1])));
       }
     }
     bool grow = false;
 #pragma unroll
     for (int m = 0; m < MQ; ++m)
 #pragma unroll
-      for (int r = 0; r < (NR > 1 ? 2 : 1); ++r) {
-        mx[m][r] = fmaxf(mx[m][r], __shfl_xor_sync(0xffffffffu, mx[m][r], 1));
-        mx[m][r] = fmaxf(mx[m][r], __shfl_xor_sync(0xffffffffu, mx[m][r], 2));
-        grow |= mx[m][r] > m_run[m][r] + kRescale;
-      }
+      for (int r = 0; r < RS; ++r) grow |= mx[m][r] > m_run[m][r] + kRescale;
     float vtop = 0.f;
     if (Q8) {
 #pragma unroll
@@ -420,11 +601,13 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
 #pragma unroll
       for (int m = 0; m < MQ; ++m) {
 #pragma unroll
-        for (int r = 0; r < (NR > 1 ? 2 : 1); ++r) {
-          float alpha = 1.f;
-          if (mx[m][r] > m_run[m][r] + kRescale) {
-            alpha = ex2(m_run[m][r] - mx[m][r]);  // 0 when nothing was seen before
-            m_run[m][r] = mx[m][r];
+        for (int r = 0; r < RS; ++r) {
+          float top = mx[m][r], alpha = 1.f;
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          if (top > m_run[m][r] + kRescale) {
+            alpha = ex2(m_run[m][r] - top);  // 0 when nothing was seen before
+            m_run[m][r] = top;
             l_run[m][r] *= alpha;
           }
           alpha *= vfac;
@@ -441,32 +624,72 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
         }
       }
     }
-    // ---- P, its row sums, and P^T as the operand of O^T
+    // ---- P, its row sums, and P^T as the operand of O^T.  A group's value
+    // scale rides in the exponent (down to 2^-100 of the reference, so that the
+    // group's share of the row sum can be had back).
+    float lv[NG], unlv[NG];
+    if (Q8) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        lv[n] = fmaxf(__log2f(vs[n] * inv_vref), -100.f);
+        unlv[n] = ex2(-lv[n]);
+      }
+    }
     uint32_t pb[NG][NR][2];
 #pragma unroll
     for (int m = 0; m < MQ; ++m) {
 #pragma unroll
-      for (int r = 0; r < (NR > 1 ? 2 : 1); ++r) {
-        const float base_m = m_run[m][r] == -INFINITY ? 0.f : m_run[m][r];
-        float sum = 0.f;
+      for (int r = 0; r < RS; ++r) {
+        const float neg_m = m_run[m][r] == -INFINITY ? 0.f : -m_run[m][r];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float p0 = ex2(s[m][n][2 * r] - base_m), p1 = ex2(s[m][n][2 * r + 1] - base_m);
-          sum += p0 + p1;
+        for (int n = 0; n < NG; ++n) {
+          const float off = Q8 ? neg_m + lv[n] : neg_m, fn = f[m][r][n];
+          const float p0 = ex2(fmaf(s[m][2 * n][2 * r], fn, off)),
+                      p1 = ex2(fmaf(s[m][2 * n][2 * r + 1], fn, off)),
+                      p2 = ex2(fmaf(s[m][2 * n + 1][2 * r], fn, off)),
+                      p3 = ex2(fmaf(s[m][2 * n + 1][2 * r + 1], fn, off));
+          const float sum = (p0 + p1) + (p2 + p3);
           if (Q8) {
-            const float f = vs[n / 2] * inv_vref;
-            const __half2 y = __floats2half2_rn(p0 * f, p1 * f);
-            pb[n / 2][2 * m + r][n & 1] = *reinterpret_cast<const uint32_t*>(&y);
+            l_run[m][r] = fmaf(sum, unlv[n], l_run[m][r]);
+            const __half2 y = __floats2half2_rn(p0, p1), z = __floats2half2_rn(p2, p3);
+            pb[n][2 * m + r][0] = *reinterpret_cast<const uint32_t*>(&y);
+            pb[n][2 * m + r][1] = *reinterpret_cast<const uint32_t*>(&z);
           } else {
-            pb[n / 2][2 * m + r][n & 1] = pack_bf16x2(p0, p1);
+            l_run[m][r] += sum;
+            pb[n][2 * m + r][0] = pack_bf16x2(p0, p1);
+            pb[n][2 * m + r][1] = pack_bf16x2(p2, p3);
           }
         }
-        l_run[m][r] += sum;
       }
     }
+    if (Q8 && k + 1 < seg) {  // the next tile's scales
+      load_scales(ksp, base + KT, ks);
+      load_scales(vsp, base + KT, vs);
+    }
     // ---- O^T += V^T P^T
+    const bool whole = base >= key0 && base + KT <= L;
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
+      // rows of keys 2t, 2t + 1, 2t + 8 and 2t + 9 (columns of S) of the group
+      uint32_t vr[4][C::NB * C::VW];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t r = 16 * n + ((e & 1) ? vrow1 : vrow0) + (e >> 1) * 8;
+        const uint32_t byte = g * C::VV;
+#pragma unroll
+        for (int i = 0; i < C::NB; ++i)
+          load_bytes<C::VV>(vt + i * C::BOX + r * C::BB +
+                                ((byte & ~15u) ^ (C::swz(r) << 4)) + (byte & 15u),
+                            &vr[e][i * C::VW]);
+        if (!whole) {
+          // rows that are no keys of this sequence may hold anything (NaN)
+          const int j = base + static_cast<int>(r);
+          if (j >= L || j < key0) {
+#pragma unroll
+            for (int i = 0; i < C::NB * C::VW; ++i) vr[e][i] = 0u;
+          }
+        }
+      }
       // pairs (key 2t, 2t+1) and (2t+8, 2t+9) of one d each
       auto product = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
@@ -478,127 +701,156 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
         }
       };
       if (Q8) {
-        constexpr int WORDS = C::VL * C::VW;
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
+        for (int w = 0; w < C::NB * C::VW; ++w) {
           // elements 4w .. 4w+3 of the lane: two 16-row tiles (one when D = 16)
           uint32_t a[2][2], c[2][2];
-          widen4<FMT>(__byte_perm(vr[n][0][w], vr[n][1][w], 0x5140), a[0][0], a[0][1]);
-          widen4<FMT>(__byte_perm(vr[n][2][w], vr[n][3][w], 0x5140), c[0][0], c[0][1]);
+          widen4<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x5140), a[0][0], a[0][1]);
+          widen4<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x5140), c[0][0], c[0][1]);
           product(2 * w, a[0][0], a[0][1], c[0][0], c[0][1]);
           if (C::MT > 1) {
-            widen4<FMT>(__byte_perm(vr[n][0][w], vr[n][1][w], 0x7362), a[1][0], a[1][1]);
-            widen4<FMT>(__byte_perm(vr[n][2][w], vr[n][3][w], 0x7362), c[1][0], c[1][1]);
+            widen4<FMT>(__byte_perm(vr[0][w], vr[1][w], 0x7362), a[1][0], a[1][1]);
+            widen4<FMT>(__byte_perm(vr[2][w], vr[3][w], 0x7362), c[1][0], c[1][1]);
             product((2 * w + 1) % C::MT, a[1][0], a[1][1], c[1][0], c[1][1]);
           }
         }
       } else {
 #pragma unroll
         for (int w = 0; w < C::MT; ++w) {
-          product(w, __byte_perm(vr[n][0][w], vr[n][1][w], 0x5410),
-                  __byte_perm(vr[n][0][w], vr[n][1][w], 0x7632),
-                  __byte_perm(vr[n][2][w], vr[n][3][w], 0x5410),
-                  __byte_perm(vr[n][2][w], vr[n][3][w], 0x7632));
+          product(w, __byte_perm(vr[0][w], vr[1][w], 0x5410),
+                  __byte_perm(vr[0][w], vr[1][w], 0x7632),
+                  __byte_perm(vr[2][w], vr[3][w], 0x5410),
+                  __byte_perm(vr[2][w], vr[3][w], 0x7632));
         }
       }
     }
+    // every lane has read the slot: its next tile may land in it
+    __syncwarp();
+    if (lane == 0 && it + C::STAGES < count) fill(it + C::STAGES);
   }
+  if (!ok) break;
 
-  // ---- the warps' partial results into shared memory
-  float* mine = sm + static_cast<size_t>(warp) * ROWS * (D + 2);
+  // ---- this warp's result of the unit: whole, or a part of it
 #pragma unroll
   for (int m = 0; m < MQ; ++m)
 #pragma unroll
-    for (int r = 0; r < (NR > 1 ? 2 : 1); ++r) {
-      float l = l_run[m][r];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (t == 0) {
-        float* row = mine + (m * 16 + r * 8 + g) * (D + 2);
-        row[D] = m_run[m][r];
-        row[D + 1] = l;
+    for (int r = 0; r < RS; ++r) {
+      l_run[m][r] += __shfl_xor_sync(0xffffffffu, l_run[m][r], 1);
+      l_run[m][r] += __shfl_xor_sync(0xffffffffu, l_run[m][r], 2);
+    }
+  const bool whole_unit = it - seg_it == cur.s.tiles;
+  float* part = p.part + (static_cast<long long>(w) * 2 + (leads ? 0 : 1)) * ROWS * (D + 2);
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      // this lane's accumulators hold query rows 2t + c of the 8-row tile x
+      const float mm = __shfl_sync(0xffffffffu, m_run[x / 2][x & 1], 8 * t + 4 * c);
+      const float ll = __shfl_sync(0xffffffffu, l_run[x / 2][x & 1], 8 * t + 4 * c);
+      const int row = x * 8 + 2 * t + c;
+      if (row >= rows) continue;
+      if (whole_unit) {
+        const int gr = rt * ROWS + row, head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
+        const float inv = (ll > 0.f ? 1.f / ll : 0.f) * (Q8 ? vref : 1.f);
+        __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
+        uint32_t word[C::MT];
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+          word[i] = pack_bf16x2(acc[i][x][c] * inv, acc[i][x][2 + c] * inv);
+        constexpr int V = C::VE / 2 < 4 ? C::VE / 2 : 4;  // words side by side
+#pragma unroll
+        for (int i = 0; i < C::MT; i += V) {
+          __nv_bfloat16* at = out + val_elem<C>(2 * i, g);
+          if (V == 4)
+            *reinterpret_cast<uint4*>(at) = make_uint4(word[i], word[i + 1], word[i + 2], word[i + 3]);
+          else if (V == 2)
+            *reinterpret_cast<uint2*>(at) = make_uint2(word[i], word[i + 1]);
+          else
+            *reinterpret_cast<uint32_t*>(at) = word[i];
+        }
+        if (g == 0 && p.lse != nullptr)
+          p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
+              ll > 0.f ? (mm + __log2f(ll)) * kLn2 : -INFINITY;
+      } else {
+        float* at = part + row * (D + 2);
+        const float f = Q8 ? vref : 1.f;
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i)
+          *reinterpret_cast<float2*>(at + val_elem<C>(2 * i, g)) =
+              make_float2(acc[i][x][c] * f, acc[i][x][2 + c] * f);
+        if (g == 0) *reinterpret_cast<float2*>(at + D) = make_float2(mm, ll);
       }
     }
-#pragma unroll
-  for (int x = 0; x < NR; ++x)
-#pragma unroll
-    for (int i = 0; i < C::MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = x * 8 + 2 * t + (e & 1);
-        const int d = val_elem<C>(2 * i + (e >> 1), g);
-        mine[row * (D + 2) + d] = acc[i][x][e] * (Q8 ? vref : 1.f);
-      }
-  __syncthreads();
-  for (int row = warp; row < rows; row += DW) {
-    float mm = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < DW; ++w) mm = fmaxf(mm, sm[(w * ROWS + row) * (D + 2) + D]);
-    const float mb = mm == -INFINITY ? 0.f : mm;
-    float f[DW], ll = 0.f;
-#pragma unroll
-    for (int w = 0; w < DW; ++w) {
-      f[w] = ex2(sm[(w * ROWS + row) * (D + 2) + D] - mb);
-      ll += f[w] * sm[(w * ROWS + row) * (D + 2) + D + 1];
-    }
-    const int gr = rt * ROWS + row;
-    const int head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
-    float* part = p.part == nullptr
-                      ? nullptr
-                      : p.part + ((unit * p.splits + split) * ROWS + row) * (D + 2);
-    __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
-    for (int d = lane; d < D; d += 32) {
-      float a = 0.f;
-#pragma unroll
-      for (int w = 0; w < DW; ++w) a += f[w] * sm[(w * ROWS + row) * (D + 2) + d];
-      if (part != nullptr)
-        part[d] = a;
-      else
-        out[d] = __float2bfloat16_rn(a * inv);
-    }
-    if (lane == 0) {
-      if (part != nullptr) {
-        part[D] = mm;
-        part[D + 1] = ll;
-      } else if (p.lse != nullptr) {
-        p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
-            ll > 0.f ? (mm + __log2f(ll)) * kLn2 : -INFINITY;
-      }
-    }
+  }
+  } while ((p.whole || it < count) && cur.next(p, subs, !p.whole));
+  if (!ok && lane == 0) {
+    atomicCAS(p.status, kDevOk, kDevTimeout);
+    // copies still in flight land before the shared memory goes away
+    for (int n = it; n < min(count, it + C::STAGES); ++n)
+      mbar_wait(bars + 8 * (n % C::STAGES), (n / C::STAGES) & 1, p.limit_ns, &never);
   }
 }
 
-// Joins the chunks of one query row: one warp per row.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) attn_decode_scored_merge_kernel(const ScoredDecParams p,
-                                                                       long long total) {
-  grid_dependency_wait();  // the chunks' results are complete
-  const long long w = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= total) return;
-  const int lane = threadIdx.x & 31;
-  const int R = p.G * p.n_q;
-  const long long bk = w / R;
-  const int gr = static_cast<int>(w - bk * R);
-  const long long unit = bk * p.row_tiles + gr / ROWS;
-  const float* part = p.part + (unit * p.splits * ROWS + gr % ROWS) * (D + 2);
-  const long long step = static_cast<long long>(ROWS) * (D + 2);
-  float mm = -INFINITY;
-  for (int s = lane; s < p.splits; s += 32) mm = fmaxf(mm, part[s * step + D]);
+// Joins the parts of a query row.  ONE_WARP: a warp per row, eight rows to a
+// CTA, for the few parts that a unit has when there are many units; else a CTA
+// of eight warps per row, each warp every eighth part.  Units that one warp of
+// the first kernel covered are complete; units without keys get O = 0 and LSE
+// = -inf here.
+template <int D, int ROWS, bool ONE_WARP>
+__global__ void __launch_bounds__(256)
+    attn_decode_scored_merge_kernel(const ScoredDecParams p, unsigned total_rows) {
+  constexpr int E = (D + 31) / 32;
+  __shared__ float joined[ONE_WARP ? 1 : 8][D + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned id = ONE_WARP ? blockIdx.x * 8 + warp : blockIdx.x;
+  const unsigned R = p.G * p.n_q;  // rows of one key head
+  const unsigned bk = id / R;
+  const int gr = id - bk * R, b = bk / static_cast<unsigned>(p.HK), hk = bk - b * p.HK;
+  const int rt = gr / ROWS, row = gr - rt * ROWS;
+  const unsigned subs = p.HK * p.row_tiles, sub = hk * p.row_tiles + rt;
+  grid_dependency_wait();  // the parts are complete
+  if (id >= total_rows) return;
+  const unsigned here = p.first[b], next = p.first[b + 1], share = share_of(p.first[p.B], p.warps);
+  const unsigned tiles = (next - here) / subs, u0 = here + tiles * sub;
+  const unsigned w0 = u0 / share;
+  const int n = tiles > 0 ? static_cast<int>((u0 + tiles - 1) / share - w0) + 1 : 0;
+  if (n == 1) return;
+  // part i: the first warp's run may have begun before the unit
+  const float* part = p.part + (static_cast<long long>(w0) * 2 * ROWS + row) * (D + 2);
+  constexpr int NEXT = 2 * ROWS * (D + 2);
+  const int late = share * w0 < u0 ? ROWS * (D + 2) : 0;
+  auto part_at = [&](int i) { return part + static_cast<long long>(i) * NEXT + (i == 0 ? late : 0); };
+  const int first = ONE_WARP ? 0 : warp;
+  constexpr int STEP = ONE_WARP ? 1 : 8;
+  float mm = -INFINITY, ll = 0.f, a[E] = {};
+  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, part_at(i)[D]);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
   const float mb = mm == -INFINITY ? 0.f : mm;
-  constexpr int E = (D + 31) / 32;
-  float a[E] = {}, ll = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
-    const float f = ex2(part[s * step + D] - mb);
-    ll += f * part[s * step + D + 1];
+#pragma unroll 8
+  for (int i = first; i < n; i += STEP) {
+    const float* at = part_at(i);
+    const float f = ex2(at[D] - mb);
+    ll += f * at[D + 1];
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (lane + 32 * e < D) a[e] += f * part[s * step + lane + 32 * e];
+      if (lane + 32 * e < D) a[e] += f * at[lane + 32 * e];
   }
-  const int b = static_cast<int>(bk / p.HK), hk = static_cast<int>(bk % p.HK);
+  if (!ONE_WARP) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (lane + 32 * e < D) joined[warp][lane + 32 * e] = a[e];
+    if (lane == 0) joined[warp][D] = ll;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int o = 1; o < 8; ++o) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (lane + 32 * e < D) a[e] += joined[o][lane + 32 * e];
+      ll += joined[o][D];
+    }
+  }
   const int head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
   __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
   const float inv = ll > 0.f ? 1.f / ll : 0.f;
@@ -611,49 +863,50 @@ __global__ void __launch_bounds__(128) attn_decode_scored_merge_kernel(const Sco
 }
 
 template <int FMT, int D, int NR>
-cudaError_t launch_scored_decode_rows(const ScoredDecParams& p, long long bk,
+cudaError_t launch_scored_decode_rows(const ScoredDecParams& p, const CUtensorMap* maps,
                                       const LaunchCtx& ctx) {
-  const size_t smem = static_cast<size_t>(DW) * NR * 8 * (D + 2) * sizeof(float);
+  const size_t smem = DW * DCfg<FMT, D, NR>::RING + 1024;
   auto* kernel = attn_decode_scored_kernel<FMT, D, NR>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const long long units = bk * p.row_tiles * p.splits;
-  kernel<<<static_cast<unsigned>(units), DW * 32, smem, ctx.stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
-  const long long total = bk * p.G * p.n_q;
-  return launch_dependent(attn_decode_scored_merge_kernel<D, NR * 8>,
-                          dim3(static_cast<unsigned>((total + 3) / 4)), dim3(128), 0, ctx.stream, p,
-                          total);
+  kernel<<<(p.warps + DW - 1) / DW, DW * 32, smem, ctx.stream>>>(maps[0], maps[1], p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.whole) return cudaSuccess;
+  const unsigned rows = static_cast<unsigned>(p.B) * p.HK * p.G * p.n_q;
+  // parts of a unit, on average
+  if (p.warps / p.units < 8)
+    return launch_dependent(attn_decode_scored_merge_kernel<D, NR * 8, true>, dim3((rows + 7) / 8),
+                            dim3(256), 0, ctx.stream, p, rows);
+  return launch_dependent(attn_decode_scored_merge_kernel<D, NR * 8, false>, dim3(rows), dim3(256),
+                          0, ctx.stream, p, rows);
 }
 
 template <int FMT, int D>
-cudaError_t launch_scored_decode_d(const ScoredDecParams& p, long long bk, int row_tile,
+cudaError_t launch_scored_decode_d(const ScoredDecParams& p, const CUtensorMap* maps, int row_tile,
                                    const LaunchCtx& ctx) {
   switch (row_tile) {
-    case 8: return launch_scored_decode_rows<FMT, D, 1>(p, bk, ctx);
-    case 16: return launch_scored_decode_rows<FMT, D, 2>(p, bk, ctx);
-    default: return launch_scored_decode_rows<FMT, D, 4>(p, bk, ctx);
+    case 8: return launch_scored_decode_rows<FMT, D, 1>(p, maps, ctx);
+    case 16: return launch_scored_decode_rows<FMT, D, 2>(p, maps, ctx);
+    default: return launch_scored_decode_rows<FMT, D, 4>(p, maps, ctx);
   }
 }
 
 template <int FMT>
-cudaError_t launch_scored_decode_fmt(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
-                                     float* workspace, const LaunchCtx& ctx) {
+cudaError_t launch_scored_decode_fmt(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                     const ScoredDecodePlan& plan, float* workspace,
+                                     const LaunchCtx& ctx) {
   ScoredDecParams p;
   p.q = static_cast<const __nv_bfloat16*>(pb.q);
-  p.k = static_cast<const uint8_t*>(pb.k_cache);
-  p.v = static_cast<const uint8_t*>(pb.v_cache);
   p.k_scale = pb.k_scale;
   p.v_scale = pb.v_scale;
   p.o = static_cast<__nv_bfloat16*>(pb.o);
   p.lse = pb.lse;
-  p.part = plan.splits > 1 ? workspace : nullptr;
+  p.first = reinterpret_cast<unsigned*>(workspace);
+  p.part = workspace + plan.part_off;
   p.cache_lens = pb.cache_lens;
   p.slopes = pb.slopes;
   p.sq = pb.sq;
-  p.sk = pb.sk;
-  p.sv = pb.sv;
   p.so = pb.so;
   p.HK = pb.HK;
   p.G = pb.H / pb.HK;
@@ -663,16 +916,20 @@ cudaError_t launch_scored_decode_fmt(const ScoredDecodeProblem& pb, const Scored
   while ((1 << p.T_log2) < pb.block_tokens) ++p.T_log2;
   p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
   p.window = pb.window;
-  p.splits = plan.splits;
   p.row_tiles = plan.row_tiles;
+  p.warps = plan.warps;
+  p.B = pb.B;
   p.scale = pb.scale;
   p.softcap = pb.softcap;
-  const long long bk = static_cast<long long>(pb.B) * pb.HK;
+  p.limit_ns = ctx.limit_ns;
+  p.status = ctx.status;
+  p.units = pb.B * pb.HK * plan.row_tiles;
+  p.whole = plan.whole;
   switch (pb.d) {
-    case 16: return launch_scored_decode_d<FMT, 16>(p, bk, plan.row_tile, ctx);
-    case 32: return launch_scored_decode_d<FMT, 32>(p, bk, plan.row_tile, ctx);
-    case 64: return launch_scored_decode_d<FMT, 64>(p, bk, plan.row_tile, ctx);
-    case 128: return launch_scored_decode_d<FMT, 128>(p, bk, plan.row_tile, ctx);
+    case 16: return launch_scored_decode_d<FMT, 16>(p, maps, plan.row_tile, ctx);
+    case 32: return launch_scored_decode_d<FMT, 32>(p, maps, plan.row_tile, ctx);
+    case 64: return launch_scored_decode_d<FMT, 64>(p, maps, plan.row_tile, ctx);
+    case 128: return launch_scored_decode_d<FMT, 128>(p, maps, plan.row_tile, ctx);
     default: return cudaErrorInvalidValue;
   }
 }

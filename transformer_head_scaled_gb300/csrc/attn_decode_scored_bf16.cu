@@ -4,9 +4,14 @@
 
 namespace attn {
 
-cudaError_t launch_decode_scored_bf16(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
-                                    float* workspace, const LaunchCtx& ctx) {
-  return launch_scored_decode_fmt<kCacheBf16>(pb, plan, workspace, ctx);
+cudaError_t launch_decode_scored_bf16(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                    const ScoredDecodePlan& plan, float* workspace,
+                                    const LaunchCtx& ctx) {
+  return launch_scored_decode_fmt<kCacheBf16>(pb, maps, plan, workspace, ctx);
 }
+
+int scored_decode_tile_keys(int row_bytes) { return scored_tile_keys(row_bytes); }
+int scored_decode_warps(int row_tile) { return DW * scored_ctas(row_tile / 8); }
+int scored_decode_min_tiles() { return kMinTiles; }
 
 }  // namespace attn

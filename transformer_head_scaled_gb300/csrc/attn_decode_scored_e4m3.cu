@@ -4,9 +4,10 @@
 
 namespace attn {
 
-cudaError_t launch_decode_scored_e4m3(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
-                                    float* workspace, const LaunchCtx& ctx) {
-  return launch_scored_decode_fmt<kCacheE4M3>(pb, plan, workspace, ctx);
+cudaError_t launch_decode_scored_e4m3(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                    const ScoredDecodePlan& plan, float* workspace,
+                                    const LaunchCtx& ctx) {
+  return launch_scored_decode_fmt<kCacheE4M3>(pb, maps, plan, workspace, ctx);
 }
 
 }  // namespace attn

@@ -4,9 +4,10 @@
 
 namespace attn {
 
-cudaError_t launch_decode_scored_int8(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
-                                    float* workspace, const LaunchCtx& ctx) {
-  return launch_scored_decode_fmt<kCacheInt8>(pb, plan, workspace, ctx);
+cudaError_t launch_decode_scored_int8(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                    const ScoredDecodePlan& plan, float* workspace,
+                                    const LaunchCtx& ctx) {
+  return launch_scored_decode_fmt<kCacheInt8>(pb, maps, plan, workspace, ctx);
 }
 
 }  // namespace attn

@@ -176,8 +176,6 @@ int cache_blocks_touched(int n_new, int L_max, int block_tokens);
 // Decoding with changed scores against a bf16, e4m3 or int8 cache.
 struct ScoredDecodeProblem {
   const void* q;  // bf16 [B, H, n_q, d]
-  const void* k_cache;  // [B, HK, L_max, d]
-  const void* v_cache;
   const float* k_scale;  // [B, HK, ceil(L_max / block_tokens)]; unused for bf16
   const float* v_scale;
   void* o;
@@ -187,22 +185,35 @@ struct ScoredDecodeProblem {
   const float* slopes;   // device float[H] or null
   const int* cache_lens;  // device int32[B] or null
   int window;  // -1: every key up to the query
-  RowStrides sq, sk, sv, so;
+  RowStrides sq, so;  // of q and o; the caches' are in their tensor maps
 };
 struct ScoredDecodePlan {
   int row_tile, row_tiles;  // query rows of one key head per CTA, and how many such tiles
-  int splits;
+  bool whole;  // a warp takes whole units (sequence, key head, row tile)
+  int warps;   // that share the units, or the list of their tiles
+  size_t part_off;  // floats before the partial results in the workspace
   size_t workspace_bytes;
 };
+// The kernel's shapes: keys of one tile, for cache rows of `row_bytes`; resident
+// warps per SM and least tiles per warp, for `row_tile` query rows.
+int scored_decode_tile_keys(int row_bytes);
+int scored_decode_warps(int row_tile);
+int scored_decode_min_tiles();
+// maps[0..1]: the key and the value cache as 4-D (row bytes, L_max, HK, B) byte
+// tensors with a (min(row bytes, 128), tile keys, 1, 1) box in the widest
+// swizzle that a box row fits.
 // seen: the most keys one call can read per sequence.
 ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int d, int elem_bytes,
                                     int num_sms);
-cudaError_t launch_decode_scored_bf16(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
-                                      float* workspace, const LaunchCtx& ctx);
-cudaError_t launch_decode_scored_e4m3(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
-                                      float* workspace, const LaunchCtx& ctx);
-cudaError_t launch_decode_scored_int8(const ScoredDecodeProblem& pb, const ScoredDecodePlan& plan,
-                                      float* workspace, const LaunchCtx& ctx);
+cudaError_t launch_decode_scored_bf16(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                      const ScoredDecodePlan& plan, float* workspace,
+                                      const LaunchCtx& ctx);
+cudaError_t launch_decode_scored_e4m3(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                      const ScoredDecodePlan& plan, float* workspace,
+                                      const LaunchCtx& ctx);
+cudaError_t launch_decode_scored_int8(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                      const ScoredDecodePlan& plan, float* workspace,
+                                      const LaunchCtx& ctx);
 
 // Diagnostics.  The tensor maps are 2-D (64, 128) bf16, one box each.
 cudaError_t launch_diag_tile(const CUtensorMap& tmq, const CUtensorMap& tmk,
