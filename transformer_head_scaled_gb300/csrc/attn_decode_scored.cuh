@@ -273,8 +273,9 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
   constexpr int ROWS = NR * 8;
   constexpr int RS = NR > 1 ? 2 : 1;  // used 8-row halves of a 16-query tile
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
+  // the rings at a 1024-byte boundary (an offset, so that the compiler still
+  // knows the address space)
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   __shared__ uint64_t full[DW][C::STAGES];
   grid_launch_dependents();
 
@@ -356,8 +357,8 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
   const int never = 0;
   Cursor<KT> ahead = cur;  // where the next copy is from (lane 0)
   if (ahead.s.tiles == 0) ahead.next(p, subs, true);
-  auto fill = [&](int n) {  // the run's tile n into its slot (one lane)
-    const uint32_t slot = n % C::STAGES, bar = bars + 8 * slot;
+  auto fill = [&](uint32_t slot) {  // the next tile into a slot (one lane)
+    const uint32_t bar = bars + 8 * slot;
     const int row = ahead.s.base0 + ahead.tile * KT;
     const int hk = p.row_tiles == 1 ? ahead.sub : ahead.sub / p.row_tiles;
     mbar_arrive_expect_tx(bar, 2 * C::TILE);
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
 
   bool ok = true;
   int it = 0;
+  uint32_t slot = 0, phase = 0;  // of tile `it`
   do {
   // ---- one unit of the work: `seg` of its tiles
   const int seg = min(cur.s.tiles - cur.tile, count - it);
@@ -393,6 +395,8 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
   const int b = cur.b, hk = p.row_tiles == 1 ? cur.sub : cur.sub / p.row_tiles, rt = cur.sub - hk * p.row_tiles;
   const int rows = min(p.G * p.n_q - rt * ROWS, ROWS);  // query rows of this unit
   const int L = cur.s.L, key0 = cur.s.key0, base0 = cur.s.base0 + cur.tile * KT;
+  // first key that the last query sees
+  const int last_lo = p.window >= 0 ? max(L - 1 - p.window, 0) : 0;
   const long long bk = static_cast<long long>(b) * p.HK + hk;
   const float* ksp = Q8 ? p.k_scale + bk * p.num_blocks : nullptr;
   const float* vsp = Q8 ? p.v_scale + bk * p.num_blocks : nullptr;
@@ -426,7 +430,8 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
       const int row = m * 16 + r * 8 + g;
       const bool in = row < rows && (NR > 1 || r == 0);
       const int gr = rt * ROWS + (in ? row : 0);
-      const int head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
+      const int in_group = p.n_q == 1 ? gr : gr / p.n_q, qi = gr - in_group * p.n_q;
+      const int head = hk * p.G + in_group;
       const __nv_bfloat16* src = p.q + b * p.sq.b + head * p.sq.h + qi * p.sq.n;
       float top = 0.f;
 #pragma unroll
@@ -479,9 +484,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
 
   for (int k = 0; k < seg; ++k, ++it) {
     const int base = base0 + k * KT;
-    const uint32_t slot = it % C::STAGES;
-    ok = __all_sync(0xffffffffu,
-                    mbar_wait(bars + 8 * slot, (it / C::STAGES) & 1, p.limit_ns, &never));
+    ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * slot, phase, p.limit_ns, &never));
     if (!ok) break;
     const uint8_t* kt = ring_at + slot * 2 * C::TILE;
     const uint8_t* vt = kt + C::TILE;
@@ -522,6 +525,10 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
       }
     }
 
+    // every row sees every key of the tile, unless it is an edge of the cache
+    // or of the window
+    const bool edge = base + KT > L - p.n_q + 1 || base < last_lo;
+
     // ---- scores in log2 units are s * f (f = 1 once the cap or the bias is
     // in), masked; mx: this lane's largest of a row
     float mx[MQ][2], f[MQ][2][NG];
@@ -561,10 +568,10 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
             }
           }
         }
-        // keys [lo, hi) of the tile are visible
-        const int hi = pos[m][r] + 1 - base;
-        const int lo = p.window >= 0 ? max(pos[m][r] - p.window, key0) - base : -base;
-        if (hi < KT || lo > 0) {
+        if (edge) {
+          // keys [lo, hi) of the tile are visible
+          const int hi = pos[m][r] + 1 - base;
+          const int lo = p.window >= 0 ? max(pos[m][r] - p.window, key0) - base : -base;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -667,7 +674,19 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
       load_scales(vsp, base + KT, vs);
     }
     // ---- O^T += V^T P^T
-    const bool whole = base >= key0 && base + KT <= L;
+    if (base < key0 || base + KT > L) {
+      // rows that are no keys of this sequence may hold anything (NaN): zero
+      // them in the ring
+#pragma unroll 1
+      for (int i = lane; i < KT * C::RB / 16; i += 32) {
+        const int r = i % KT, j = base + r;  // chunk i / KT of the row's boxes
+        if (j < key0 || j >= L)
+          *reinterpret_cast<uint4*>(ring_at + slot * 2 * C::TILE + C::TILE +
+                                    (i / KT) / (C::BB / 16) * C::BOX + r * C::BB +
+                                    (i / KT) % (C::BB / 16) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+    }
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
       // rows of keys 2t, 2t + 1, 2t + 8 and 2t + 9 (columns of S) of the group
@@ -681,14 +700,6 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
           load_bytes<C::VV>(vt + i * C::BOX + r * C::BB +
                                 ((byte & ~15u) ^ (C::swz(r) << 4)) + (byte & 15u),
                             &vr[e][i * C::VW]);
-        if (!whole) {
-          // rows that are no keys of this sequence may hold anything (NaN)
-          const int j = base + static_cast<int>(r);
-          if (j >= L || j < key0) {
-#pragma unroll
-            for (int i = 0; i < C::NB * C::VW; ++i) vr[e][i] = 0u;
-          }
-        }
       }
       // pairs (key 2t, 2t+1) and (2t+8, 2t+9) of one d each
       auto product = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
@@ -724,9 +735,12 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
         }
       }
     }
-    // every lane has read the slot: its next tile may land in it
+    // every lane has read (and perhaps written) the slot: its next tile may
+    // land in it
+    if (base < key0 || base + KT > L) fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && it + C::STAGES < count) fill(it + C::STAGES);
+    if (lane == 0 && it + C::STAGES < count) fill(slot);
+    if (++slot == C::STAGES) slot = 0, phase ^= 1;
   }
   if (!ok) break;
 
@@ -750,7 +764,9 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
       const int row = x * 8 + 2 * t + c;
       if (row >= rows) continue;
       if (whole_unit) {
-        const int gr = rt * ROWS + row, head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
+        const int gr = rt * ROWS + row;
+        const int in_group = p.n_q == 1 ? gr : gr / p.n_q, qi = gr - in_group * p.n_q;
+        const int head = hk * p.G + in_group;
         const float inv = (ll > 0.f ? 1.f / ll : 0.f) * (Q8 ? vref : 1.f);
         __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
         uint32_t word[C::MT];
