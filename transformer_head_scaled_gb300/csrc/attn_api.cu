@@ -821,8 +821,8 @@ bool read_strides(Strides* st, const int64_t* in, int count, const int* heads, c
 bool int_ptr_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A cache as 4-D (row bytes, L_max, h, B) bytes with a (min(row bytes, 128),
-// tile keys, 1, 1) box in the widest swizzle a box row fits; strides in
-// elements of `elem` bytes.
+// tile keys, 1, 1) box, with the 128-byte swizzle where box rows are 128 bytes;
+// strides in elements of `elem` bytes.
 int encode_4d_bytes(CUtensorMap* map, const void* base, int row_bytes, int n, int h, int B,
                     Strides st, int elem) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(n),
@@ -831,10 +831,8 @@ int encode_4d_bytes(CUtensorMap* map, const void* base, int row_bytes, int n, in
                            static_cast<cuuint64_t>(st.h) * elem,
                            static_cast<cuuint64_t>(st.b) * elem};
   const int inner = row_bytes < 128 ? row_bytes : 128;
-  const CUtensorMapSwizzle swz = inner == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-                                 : inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                 : inner == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
-                                               : CU_TENSOR_MAP_SWIZZLE_NONE;
+  const CUtensorMapSwizzle swz =
+      inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
   cuuint32_t box[4] = {static_cast<cuuint32_t>(inner),
                        static_cast<cuuint32_t>(scored_decode_tile_keys(row_bytes)), 1u, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
@@ -954,9 +952,9 @@ int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
     return rc;
   if ((rc = encode_4d_bytes(&maps[1], v_cache, d_k * e1, L_max, h_kv, B, st[2], e1)) != ATTN_OK)
     return rc;
-  ScoredDecodeProblem pb{q, k_scale, v_scale, o, lse, B, h, h_kv, n_q, L_max,
+  ScoredDecodeProblem pb{q, k_cache, v_cache, k_scale, v_scale, o, lse, B, h, h_kv, n_q, L_max,
                          d_k, q8 ? block_tokens : 128, scale, softcap, slopes, cache_lens,
-                         window < L_max ? window : -1, st[0], st[3]};
+                         window < L_max ? window : -1, st[0], st[1], st[2], st[3]};
   const LaunchCtx ctx = make_ctx(*di, stream);
   float* ws = static_cast<float*>(workspace);
   const cudaError_t e = cache_format == ATTN_CACHE_BF16   ? launch_decode_scored_bf16(pb, maps, plan, ws, ctx)

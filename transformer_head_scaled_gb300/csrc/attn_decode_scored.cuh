@@ -80,6 +80,10 @@ struct ScoredDecParams {
   const int* cache_lens;
   const float* slopes;
   RowStrides sq, so;
+  const uint8_t* k;  // the caches and their byte strides, for copies of runs of rows
+  const uint8_t* v;
+  RowStrides sk, sv;
+  bool run_k, run_v;  // the rows of a head lie side by side
   uint64_t limit_ns;
   int* status;
   int B, HK, G, n_q, L_max, T_log2, num_blocks, window, row_tiles;
@@ -184,14 +188,17 @@ struct DCfg {
   static constexpr int MQ = NR_ > 1 ? NR_ / 2 : 1;  // 16-query tiles of S
   static constexpr uint32_t RING = STAGES * 2 * TILE;  // shared memory of a warp
   static constexpr int CTAS = scored_ctas(NR_);
-  // Which key of an 8-key tile is column c: an order in which neither the rows
-  // that a key load touches nor those of a value load share banks.
-  static constexpr uint32_t ORDER = RB == 64 ? 0x65742130u : (RB == 32 ? 0x57463120u : 0x76543210u);
+  // Rows shorter than 128 bytes whose cache rows lie side by side are copied as
+  // one run of bytes: a tiled copy takes about four cycles of the SM's copy
+  // engine per box row, which for 64-byte rows is the time of 16 bytes a cycle,
+  // less than an SM's share of the memory rate.
+  static constexpr bool RUNS = RB < 128;
+  // Which key of an 8-key tile is column c: for 32-byte rows an order in which
+  // the rows that a value load touches do not share banks.
+  static constexpr uint32_t ORDER = RB == 32 ? 0x57463120u : 0x76543210u;
   __device__ static constexpr int key_of(int c) { return (ORDER >> (4 * c)) & 7; }
-  // the 16-byte chunk position XOR of row r inside its swizzle atom
-  __device__ static constexpr uint32_t swz(uint32_t r) {
-    return BB >= 32 ? ((r * BB) >> 7) & (BB / 16 - 1) : 0u;
-  }
+  // the 16-byte chunk position XOR of row r: 128-byte rows are swizzled
+  __device__ static constexpr uint32_t swz(uint32_t r) { return BB == 128 ? r & 7 : 0u; }
   static_assert(RB >= 128 || NB == 1, "one box");
 };
 
@@ -361,12 +368,29 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
     const uint32_t bar = bars + 8 * slot;
     const int row = ahead.s.base0 + ahead.tile * KT;
     const int hk = p.row_tiles == 1 ? ahead.sub : ahead.sub / p.row_tiles;
-    mbar_arrive_expect_tx(bar, 2 * C::TILE);
+    const uint32_t dst = ring + slot * 2 * C::TILE;
+    if (C::RUNS) {
+      // (rows past L_max are not copied: what the slot held there is masked)
+      const uint32_t bytes = min(KT, p.L_max - row) * C::RB;
+      mbar_arrive_expect_tx(bar, (p.run_k ? bytes : C::TILE) + (p.run_v ? bytes : C::TILE));
+      if (p.run_k)
+        bulk_copy_in(dst, p.k + ahead.b * p.sk.b + hk * p.sk.h + static_cast<long long>(row) * C::RB,
+                     bytes, bar);
+      else
+        tma_load_4d(dst, &tmk, bar, 0, row, hk, ahead.b);
+      if (p.run_v)
+        bulk_copy_in(dst + C::TILE,
+                     p.v + ahead.b * p.sv.b + hk * p.sv.h + static_cast<long long>(row) * C::RB,
+                     bytes, bar);
+      else
+        tma_load_4d(dst + C::TILE, &tmv, bar, 0, row, hk, ahead.b);
+    } else {
+      mbar_arrive_expect_tx(bar, 2 * C::TILE);
 #pragma unroll
-    for (int x = 0; x < C::NB; ++x) {
-      tma_load_4d(ring + slot * 2 * C::TILE + x * C::BOX, &tmk, bar, x * C::BB, row, hk, ahead.b);
-      tma_load_4d(ring + slot * 2 * C::TILE + C::TILE + x * C::BOX, &tmv, bar, x * C::BB, row, hk,
-                  ahead.b);
+      for (int x = 0; x < C::NB; ++x) {
+        tma_load_4d(dst + x * C::BOX, &tmk, bar, x * C::BB, row, hk, ahead.b);
+        tma_load_4d(dst + C::TILE + x * C::BOX, &tmv, bar, x * C::BB, row, hk, ahead.b);
+      }
     }
     if (++ahead.tile == ahead.s.tiles) ahead.next(p, subs, true);
   };
@@ -923,6 +947,13 @@ cudaError_t launch_scored_decode_fmt(const ScoredDecodeProblem& pb, const CUtens
   p.cache_lens = pb.cache_lens;
   p.slopes = pb.slopes;
   p.sq = pb.sq;
+  constexpr int es = FMT == kCacheBf16 ? 2 : 1;
+  p.k = static_cast<const uint8_t*>(pb.k_cache);
+  p.v = static_cast<const uint8_t*>(pb.v_cache);
+  p.sk = RowStrides{pb.sk.b * es, pb.sk.h * es, pb.sk.n * es};
+  p.sv = RowStrides{pb.sv.b * es, pb.sv.h * es, pb.sv.n * es};
+  p.run_k = pb.sk.n == pb.d;
+  p.run_v = pb.sv.n == pb.d;
   p.so = pb.so;
   p.HK = pb.HK;
   p.G = pb.H / pb.HK;

@@ -176,6 +176,8 @@ int cache_blocks_touched(int n_new, int L_max, int block_tokens);
 // Decoding with changed scores against a bf16, e4m3 or int8 cache.
 struct ScoredDecodeProblem {
   const void* q;  // bf16 [B, H, n_q, d]
+  const void* k_cache;  // [B, HK, L_max, d]
+  const void* v_cache;
   const float* k_scale;  // [B, HK, ceil(L_max / block_tokens)]; unused for bf16
   const float* v_scale;
   void* o;
@@ -185,7 +187,7 @@ struct ScoredDecodeProblem {
   const float* slopes;   // device float[H] or null
   const int* cache_lens;  // device int32[B] or null
   int window;  // -1: every key up to the query
-  RowStrides sq, so;  // of q and o; the caches' are in their tensor maps
+  RowStrides sq, sk, sv, so;
 };
 struct ScoredDecodePlan {
   int row_tile, row_tiles;  // query rows of one key head per CTA, and how many such tiles
@@ -200,8 +202,8 @@ int scored_decode_tile_keys(int row_bytes);
 int scored_decode_warps(int row_tile);
 int scored_decode_min_tiles();
 // maps[0..1]: the key and the value cache as 4-D (row bytes, L_max, HK, B) byte
-// tensors with a (min(row bytes, 128), tile keys, 1, 1) box in the widest
-// swizzle that a box row fits.
+// tensors with a (min(row bytes, 128), tile keys, 1, 1) box, with the 128-byte
+// swizzle where box rows are 128 bytes.
 // seen: the most keys one call can read per sequence.
 ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int d, int elem_bytes,
                                     int num_sms);
