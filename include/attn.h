@@ -56,7 +56,8 @@ typedef enum {
   ATTN_ERR_UNSUPPORTED = -2, /* head size or device the library does not cover */
   ATTN_ERR_CUDA = -3,        /* a CUDA runtime/driver call failed, see attn_last_cuda_error */
   ATTN_ERR_TIMEOUT = -4,     /* a kernel gave up on a bounded wait (see attn_check) */
-  ATTN_ERR_SCRATCH_TOO_SMALL = -5 /* attn_decode_noalloc: sizes need more than its fixed scratch */
+  ATTN_ERR_SCRATCH_TOO_SMALL = -5, /* attn_decode_noalloc: sizes need more than its fixed scratch */
+  ATTN_ERR_WRONG_PLAN = -6    /* a call got a mask plan made for other sizes (see attn_check) */
 } attn_status;
 
 /*
@@ -254,6 +255,88 @@ int attn_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
                         float* lse, int B, int h, int n_q, int L_max, int d_k, float scale,
                         const int* cache_lens, struct CUstream_st* stream);
 
+/*
+ * attn_mask_plan -- the plan of a mask under which every query sees one run of
+ * keys, for attn_fwd_scored and attn_bwd_scored: one plan serves every layer
+ * (and both directions) of a batch.  Query i of batch entry b sees key j iff
+ *   (i - window_left <= j <= i + window_right, a side of -1 bounding nothing,
+ *    or j < prefix_lens[b])
+ *   and j < key_lens[b]
+ *   and i and j lie in the same document: the same run of equal ids in
+ *   doc_ids[b], and that id is not negative.
+ * window_right = 0 is the causal mask, with window_left = w a causal window;
+ * with prefix_lens the first tokens are seen by all (a prefix language model);
+ * with doc_ids several documents share one row without seeing each other, and
+ * tokens of a negative id (padding) see nothing and are not seen.
+ *   key_lens, prefix_lens : device int32[B] (clamped to [0, n_k]), or NULL.
+ *   doc_ids  : device int32 [B, n_q], or NULL; needs n_q == n_k.
+ *   prefix_lens needs window_left == -1 (else a query would see two runs).
+ *   plan, plan_bytes : caller-owned device memory of at least
+ *              attn_mask_plan_bytes(B, n_q, n_k) bytes, 16-byte aligned.
+ *   B, n_q, n_k >= 1, at most 2^30 tokens (else ATTN_ERR_UNSUPPORTED).
+ * One kernel on `stream`, two with doc_ids.
+ */
+int attn_mask_plan(int B, int n_q, int n_k, int window_left, int window_right,
+                   const int* key_lens, const int* doc_ids, const int* prefix_lens, void* plan,
+                   size_t plan_bytes, struct CUstream_st* stream);
+
+/* Bytes of a plan for these sizes (0 for unsupported sizes). */
+size_t attn_mask_plan_bytes(int B, int n_q, int n_k);
+
+/*
+ * attn_fwd_scored -- attn_fwd with changed scores, under a mask plan, with key
+ * heads shared by groups of query heads.  For query i and key j of head hh:
+ *   s = scale * q_i.k_j;   capped: softcap * tanh(s / softcap);
+ *   biased: minus slopes[hh] * |i - j|;   O = softmax(s) V,  LSE = ln sum e^s.
+ *   q, o     : bf16 [B, h, n_q, d_k];  k, v : bf16 [B, h_kv, n_k, d_k], h a
+ *              multiple of h_kv: query head i reads key head i / (h / h_kv).
+ *   lse      : float [B, h, n_q] contiguous, or NULL (then not written).
+ *   strides  : host array of 12 element counts, three (b, h, row) per tensor in
+ *              the order q, k, v, o, each > 0 and a multiple of 8; NULL:
+ *              contiguous.
+ *   softcap  : > 0, or 0 for none.  slopes : device float[h], or NULL for none.
+ *   plan, plan_bytes : what attn_mask_plan wrote for (B, n_q, n_k), on this
+ *              stream or ordered before it; NULL: every query sees every key.
+ *              A plan of other sizes is found on the device: nothing is
+ *              computed and attn_check reports ATTN_ERR_WRONG_PLAN.
+ * d_k in {16, 32, 64, 128}.  A query that sees no key gets O = 0, LSE = -inf.
+ * Values that a mask hides must be finite, as for attn_fwd.  Scores, cap, bias
+ * and softmax are computed in fp32; P is rounded to bf16 before the second
+ * product.  Other arguments and status codes as attn_fwd.
+ */
+int attn_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B, int h,
+                    int h_kv, int n_q, int n_k, int d_k, const int64_t* strides, float scale,
+                    float softcap, const float* slopes, const void* plan, size_t plan_bytes,
+                    struct CUstream_st* stream);
+
+/*
+ * attn_bwd_scored -- gradients of attn_fwd_scored, given dout = dLoss/dO and
+ * the o and lse of the forward with the same scale, softcap, slopes and plan:
+ *   dV = P^T dO,  dP = dO V^T,  D_i = sum_c dO[i,c] O[i,c],
+ *   dS = P * (dP - D_i) * (1 - tanh^2(s / softcap)),
+ *   dQ = scale dS K,  dK = scale dS^T Q,
+ * dK and dV summed over the query heads that share a key head (inside one
+ * accumulator, in head order).  The slopes are constants: they get no gradient.
+ *   strides  : host array of 24 element counts, three (b, h, row) per tensor in
+ *              the order q, k, v, o, dout, dq, dk, dv (k, v, dk, dv have h_kv
+ *              heads), each > 0 and a multiple of 8; NULL: contiguous.
+ *   workspace, workspace_bytes : at least attn_bwd_scored_workspace_bytes(B, h,
+ *              n_q, d_k) bytes, 16-byte aligned; contents on entry do not matter.
+ * d_k in {16, 32, 64} (else ATTN_ERR_UNSUPPORTED).  Queries that see no key get
+ * dq = 0, keys that no query sees dk = dv = 0.  dq, dk, dv must not overlap the
+ * inputs; dout must be finite, in rows that see no key too.  dQ is summed over
+ * key tiles in fp32 in the order in which they finish.  Other arguments,
+ * roundings and status codes as attn_bwd and attn_fwd_scored.  Three kernels.
+ */
+int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                    const float* lse, void* dq, void* dk, void* dv, int B, int h, int h_kv,
+                    int n_q, int n_k, int d_k, const int64_t* strides, float scale, float softcap,
+                    const float* slopes, const void* plan, size_t plan_bytes, void* workspace,
+                    size_t workspace_bytes, struct CUstream_st* stream);
+
+/* Scratch bytes attn_bwd_scored needs (0 for unsupported sizes). */
+size_t attn_bwd_scored_workspace_bytes(int B, int h, int n_q, int d_k);
+
 /* What the rows of a key/value cache hold. */
 typedef enum {
   ATTN_CACHE_BF16 = 0,
@@ -408,7 +491,8 @@ size_t attn_bwd_workspace_bytes(int B, int h, int n_q, int d_k);
  * attn_check -- synchronise `stream`, then report (and clear) any error a
  * kernel of this library recorded on the current device since the last check:
  * ATTN_ERR_TIMEOUT when a bounded wait inside a kernel ran out (the kernel
- * returned early and its outputs are incomplete), ATTN_ERR_CUDA when the
+ * returned early and its outputs are incomplete), ATTN_ERR_WRONG_PLAN when a
+ * call was handed a mask plan of other sizes (nothing was computed), ATTN_ERR_CUDA when the
  * synchronisation itself failed, else ATTN_OK.
  */
 int attn_check(struct CUstream_st* stream);

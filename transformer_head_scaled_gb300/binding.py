@@ -26,6 +26,7 @@ ATTN_ERR_UNSUPPORTED = -2
 ATTN_ERR_CUDA = -3
 ATTN_ERR_TIMEOUT = -4
 ATTN_ERR_SCRATCH_TOO_SMALL = -5
+ATTN_ERR_WRONG_PLAN = -6
 MASK_WINDOW = 3  # attn_fwd_strided: the window of attn_fwd_window
 CACHE_BF16, CACHE_E4M3, CACHE_INT8 = 0, 1, 2  # attn_cache_format
 _CACHE_FORMATS = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3,
@@ -38,7 +39,8 @@ EXPORTS = ("attn_fwd", "attn_fwd_f32", "attn_fwd_window", "attn_fwd_strided", "a
            "attn_decode_workspace_bytes", "attn_decode_window",
            "attn_decode_window_workspace_bytes", "attn_decode_noalloc", "attn_bwd", "attn_bwd_window", "attn_bwd_strided",
            "attn_bwd_workspace_bytes", "attn_cache_append", "attn_decode_scored",
-           "attn_decode_scored_workspace_bytes",
+           "attn_decode_scored_workspace_bytes", "attn_mask_plan", "attn_mask_plan_bytes",
+           "attn_fwd_scored", "attn_bwd_scored", "attn_bwd_scored_workspace_bytes",
            "attn_check", "attn_status_string",
            "attn_last_cuda_error", "attn_set_wait_limit_ns", "attn_launch_count",
            "attn_diag_tile", "attn_diag_wait_timeout")
@@ -116,6 +118,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                                    i32, vp, ctypes.c_size_t, vp])
         lib.attn_decode_scored_workspace_bytes.restype = ctypes.c_size_t
         lib.attn_decode_scored_workspace_bytes.argtypes = [i32] * 8
+        lib.attn_mask_plan.restype = i32
+        lib.attn_mask_plan.argtypes = [i32] * 5 + [vp] * 4 + [ctypes.c_size_t, vp]
+        lib.attn_mask_plan_bytes.restype = ctypes.c_size_t
+        lib.attn_mask_plan_bytes.argtypes = [i32] * 3
+        lib.attn_fwd_scored.restype = i32
+        lib.attn_fwd_scored.argtypes = [vp] * 5 + [i32] * 6 + [vp, f32, f32, vp, vp,
+                                                               ctypes.c_size_t, vp]
+        lib.attn_bwd_scored.restype = i32
+        lib.attn_bwd_scored.argtypes = [vp] * 9 + [i32] * 6 + [vp, f32, f32, vp, vp,
+                                                               ctypes.c_size_t, vp,
+                                                               ctypes.c_size_t, vp]
+        lib.attn_bwd_scored_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_bwd_scored_workspace_bytes.argtypes = [i32] * 4
         lib.attn_check.restype = i32
         lib.attn_check.argtypes = [vp]
         lib.attn_status_string.restype = ctypes.c_char_p
@@ -823,6 +838,172 @@ def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_scored")
     return out, lse
+
+
+@functools.lru_cache(maxsize=256)
+def mask_plan_bytes(B: int, n_q: int, n_k: int) -> int:
+    """Bytes of a mask plan for these sizes (0 for unsupported sizes)."""
+    return int(load().attn_mask_plan_bytes(B, n_q, n_k))
+
+
+def attn_mask_plan_raw(B, n_q, n_k, left, right, lens_ptr, docs_ptr, prefix_ptr, plan_ptr,
+                       plan_bytes, stream_ptr) -> int:
+    """The C call itself, on raw device pointers; returns the status code."""
+    return load().attn_mask_plan(B, n_q, n_k, left, right, lens_ptr, docs_ptr, prefix_ptr,
+                                 plan_ptr, plan_bytes, stream_ptr)
+
+
+def attn_mask_plan(B: int, n_q: int, n_k: int, left: int | None = None, right: int | None = None,
+                   key_lens: torch.Tensor | None = None, doc_ids: torch.Tensor | None = None,
+                   prefix_lens: torch.Tensor | None = None, plan: torch.Tensor | None = None,
+                   device=None, stream=None) -> torch.Tensor:
+    """The plan of a mask for attn_fwd_scored and attn_bwd_scored, a uint8 tensor
+    (``plan`` when one is given): query i sees the keys i - left .. i + right
+    (None: unbounded; right=0 is causal) and, with prefix_lens [B], the first
+    prefix_lens[b] keys; of them those below key_lens[b] and, with doc_ids
+    [B, n], those of its own run of equal ids (negative: no document)."""
+    if device is None:
+        given = [t for t in (key_lens, doc_ids, prefix_lens, plan) if t is not None]
+        device = given[0].device if given else "cuda"
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("a mask plan lives on a CUDA device")
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    if (left is not None and left < 0) or (right is not None and right < 0):
+        raise ValueError("left and right must be >= 0 (None: unbounded)")
+    _vector("key_lens", key_lens, torch.int32, B, dev)
+    _vector("prefix_lens", prefix_lens, torch.int32, B, dev)
+    _vector("doc_ids", doc_ids, torch.int32, B * n_q, dev)
+    if doc_ids is not None and n_q != n_k:
+        raise ValueError("documents need n_q == n_k")
+    if prefix_lens is not None and left is not None:
+        raise ValueError("a prefix and a left bound leave a query two runs of keys")
+    need = mask_plan_bytes(B, n_q, n_k)
+    if plan is not None and (plan.device != dev or not plan.is_contiguous()
+                             or _nbytes(plan) < need):
+        raise ValueError(f"plan must be contiguous, on {dev} and of at least {need} bytes")
+    with _call_on(dev, stream) as ptr:
+        if plan is None:
+            plan = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        rc = attn_mask_plan_raw(B, n_q, n_k, -1 if left is None else left,
+                                -1 if right is None else right, _ptr(key_lens), _ptr(doc_ids),
+                                _ptr(prefix_lens), _ptr(plan), _nbytes(plan), ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_mask_plan")
+    return plan
+
+
+def _scored_shapes(q, k, v, slopes, plan):
+    """Sizes of a call with changed scores, checked: B, h, h_kv, n_q, n_k, d."""
+    _views("q, k, v", torch.bfloat16, q, k, v)
+    B, h, n_q, d = q.shape
+    h_kv, n_k = k.shape[1:3]
+    if (tuple(k.shape) != (B, h_kv, n_k, d) or v.shape != k.shape or h_kv < 1 or h % h_kv != 0):
+        raise ValueError("k and v must be [B, h_kv, n_k, d] with q's B and d, h a multiple of h_kv")
+    _vector("slopes", slopes, torch.float32, h, q.device)
+    if plan is not None and (plan.device != q.device or not plan.is_contiguous()
+                             or _nbytes(plan) < mask_plan_bytes(B, n_q, n_k)):
+        raise ValueError("plan must be attn_mask_plan's for these sizes and this device")
+    return B, h, h_kv, n_q, n_k, d
+
+
+def attn_fwd_scored_raw(q_ptr, k_ptr, v_ptr, o_ptr, lse_ptr, B, h, h_kv, n_q, n_k, d, strides,
+                        scale, softcap, slopes_ptr, plan_ptr, plan_bytes, stream_ptr) -> int:
+    """The C call itself, on raw device pointers; ``strides`` = 12 element counts or None."""
+    return load().attn_fwd_scored(q_ptr, k_ptr, v_ptr, o_ptr, lse_ptr, B, h, h_kv, n_q, n_k, d,
+                                  _strides_array(strides), scale, softcap, slopes_ptr, plan_ptr,
+                                  plan_bytes, stream_ptr)
+
+
+def attn_fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    plan: torch.Tensor | None = None, scale: float | None = None,
+                    softcap: float = 0.0, slopes: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    stream=None):
+    """Attention with changed scores on bf16 views q [B, h, n_q, d] and k, v
+    [B, h_kv, n_k, d] (h a multiple of h_kv): softcap > 0 caps them by a tanh,
+    slopes [h] (float32) take slopes * |i - j| off.  ``plan``: the mask
+    (attn_mask_plan; None: every query sees every key).  Returns (o, lse)."""
+    B, h, h_kv, n_q, n_k, d = _scored_shapes(q, k, v, slopes, plan)
+    dev = q.device
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _call_on(dev, stream) as ptr:
+        if out is None:
+            out = torch.empty((B, h, n_q, d), dtype=q.dtype, device=dev)
+        else:
+            _views("q and out", torch.bfloat16, q, out)
+            if out.shape != q.shape:
+                raise ValueError("out must be shaped like q")
+        if lse is None:
+            lse = torch.empty((B, h, n_q), dtype=torch.float32, device=dev)
+        else:
+            _vector("lse", lse, torch.float32, B * h * n_q, dev)
+        rc = attn_fwd_scored_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, h, h_kv, n_q,
+                                 n_k, d, _strides(q, k, v, out), scale, softcap, _ptr(slopes),
+                                 _ptr(plan), _nbytes(plan), ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_scored")
+    return out, lse
+
+
+@functools.lru_cache(maxsize=256)
+def bwd_scored_workspace_bytes(B: int, h: int, n_q: int, d: int = 64) -> int:
+    """Scratch bytes attn_bwd_scored needs (0 for unsupported sizes)."""
+    return int(load().attn_bwd_scored_workspace_bytes(B, h, n_q, d))
+
+
+def attn_bwd_scored_raw(q_ptr, k_ptr, v_ptr, o_ptr, dout_ptr, lse_ptr, dq_ptr, dk_ptr, dv_ptr, B, h,
+                        h_kv, n_q, n_k, d, strides, scale, softcap, slopes_ptr, plan_ptr,
+                        plan_bytes, ws_ptr, ws_bytes, stream_ptr) -> int:
+    """The C call itself, on raw device pointers; ``strides`` = 24 element counts or None."""
+    return load().attn_bwd_scored(q_ptr, k_ptr, v_ptr, o_ptr, dout_ptr, lse_ptr, dq_ptr, dk_ptr,
+                                  dv_ptr, B, h, h_kv, n_q, n_k, d, _strides_array(strides), scale,
+                                  softcap, slopes_ptr, plan_ptr, plan_bytes, ws_ptr, ws_bytes,
+                                  stream_ptr)
+
+
+def attn_bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                    lse: torch.Tensor, dout: torch.Tensor, plan: torch.Tensor | None = None,
+                    scale: float | None = None, softcap: float = 0.0,
+                    slopes: torch.Tensor | None = None, dq: torch.Tensor | None = None,
+                    dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Gradients (dq, dk, dv) of attn_fwd_scored for dout = dLoss/dO, given its o
+    and lse and the same plan, scale, softcap and slopes; d in {16, 32, 64}.
+    All tensors but lse may be views of any strides with unit last stride."""
+    B, h, h_kv, n_q, n_k, d = _scored_shapes(q, k, v, slopes, plan)
+    dev = q.device
+    _views("q, o, dout", torch.bfloat16, q, o, dout)
+    if o.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("o and dout must be shaped like q")
+    if lse is None:
+        raise ValueError("lse must be the forward's")
+    _vector("lse", lse, torch.float32, B * h * n_q, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is not None:
+            _views(f"q and {name}", torch.bfloat16, q, t)
+            if t.shape != like.shape:
+                raise ValueError(f"{name} must be shaped like {name[1]}")
+    with _call_on(dev, stream) as ptr:
+        if dq is None:
+            dq = torch.empty((B, h, n_q, d), dtype=q.dtype, device=dev)
+        if dk is None:
+            dk = torch.empty((B, h_kv, n_k, d), dtype=q.dtype, device=dev)
+        if dv is None:
+            dv = torch.empty((B, h_kv, n_k, d), dtype=q.dtype, device=dev)
+        workspace = _workspace(max(bwd_scored_workspace_bytes(B, h, n_q, d), 16), workspace, dev)
+        rc = attn_bwd_scored_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
+                                 _ptr(dq), _ptr(dk), _ptr(dv), B, h, h_kv, n_q, n_k, d,
+                                 _strides(q, k, v, o, dout, dq, dk, dv), scale, softcap,
+                                 _ptr(slopes), _ptr(plan), _nbytes(plan), _ptr(workspace),
+                                 _nbytes(workspace), ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_bwd_scored")
+    return dq, dk, dv
 
 
 def check(stream=None) -> None:

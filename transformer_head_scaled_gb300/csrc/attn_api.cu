@@ -738,7 +738,7 @@ int attn_check(struct CUstream_st* stream) {
   if (status != kDevOk) {
     const int zero = 0;
     if ((e = cudaMemcpyToSymbol(g_status, &zero, sizeof(int))) != cudaSuccess) return cuda_fail(e);
-    return ATTN_ERR_TIMEOUT;
+    return status == kDevWrongPlan ? ATTN_ERR_WRONG_PLAN : ATTN_ERR_TIMEOUT;
   }
   return ATTN_OK;
 }
@@ -752,6 +752,7 @@ const char* attn_status_string(int status) {
     case ATTN_ERR_TIMEOUT: return "a bounded wait inside a kernel timed out";
     case ATTN_ERR_SCRATCH_TOO_SMALL:
       return "these sizes need more scratch than the library's fixed scratch array holds";
+    case ATTN_ERR_WRONG_PLAN: return "a mask plan was made for other sizes";
     default: return "unknown status";
   }
 }
@@ -996,3 +997,156 @@ ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int
 }
 
 }  // namespace attn
+
+namespace attn {
+namespace {
+
+constexpr int kMostTokens = 1 << 30;  // tokens of a sequence, so that sums of two stay in int
+
+int check_mask_sizes(int B, int n_q, int n_k) {
+  if (B < 1 || n_q < 1 || n_k < 1) return ATTN_ERR_INVALID_ARG;
+  const long long n = n_q > n_k ? n_q : n_k;
+  if (n > kMostTokens || B * ((n + kMaskTile - 1) / kMaskTile) > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// What attn_fwd_scored and attn_bwd_scored check alike.
+int check_scored(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                 int B, int h, int h_kv, int n_q, int n_k, int d_k, float scale, float softcap,
+                 const float* slopes, const void* plan, size_t plan_bytes) {
+  int rc = check_common(q, k, v, o, lse, B, h, n_q, n_k, d_k, scale, ATTN_MASK_NONE, nullptr, 2);
+  if (rc != ATTN_OK) return rc;
+  if (h_kv < 1 || h % h_kv != 0) return ATTN_ERR_INVALID_ARG;
+  if (!(std::isfinite(softcap) && softcap >= 0.f) || !int_ptr_ok(slopes))
+    return ATTN_ERR_INVALID_ARG;
+  if ((rc = check_mask_sizes(B, n_q, n_k)) != ATTN_OK) return rc;
+  // one work item per 256 queries, or per 128 keys, of a head
+  const long long n = n_q > n_k ? n_q : n_k;
+  if (static_cast<long long>(B) * h * ((n + 127) / 128) > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  if (plan != nullptr && (!aligned16(plan) || plan_bytes < mask_layout(B, n_q, n_k).bytes))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+ScoreMod score_mod(float softcap, const float* slopes, int h, int h_kv, const void* plan, int B,
+                   int n_q, int n_k) {
+  ScoreMod mod{softcap, slopes, h / h_kv, {}, plan != nullptr};
+  if (plan != nullptr) mod.plan = mask_plan_at(plan, B, n_q, n_k);
+  return mod;
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+size_t attn_mask_plan_bytes(int B, int n_q, int n_k) {
+  return check_mask_sizes(B, n_q, n_k) == ATTN_OK ? mask_layout(B, n_q, n_k).bytes : 0;
+}
+
+int attn_mask_plan(int B, int n_q, int n_k, int window_left, int window_right,
+                   const int* key_lens, const int* doc_ids, const int* prefix_lens, void* plan,
+                   size_t plan_bytes, struct CUstream_st* stream) {
+  int rc = check_mask_sizes(B, n_q, n_k);
+  if (rc == ATTN_ERR_INVALID_ARG) return rc;
+  if (window_left < -1 || window_right < -1) return ATTN_ERR_INVALID_ARG;
+  if (!int_ptr_ok(key_lens) || !int_ptr_ok(doc_ids) || !int_ptr_ok(prefix_lens))
+    return ATTN_ERR_INVALID_ARG;
+  if (doc_ids != nullptr && n_q != n_k) return ATTN_ERR_INVALID_ARG;
+  if (prefix_lens != nullptr && window_left >= 0) return ATTN_ERR_INVALID_ARG;
+  if (plan == nullptr || !aligned16(plan)) return ATTN_ERR_INVALID_ARG;
+  if (rc != ATTN_OK) return rc;
+  if (plan_bytes < mask_layout(B, n_q, n_k).bytes) return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  const int reach = n_q + n_k;  // a side longer than both sequences bounds nothing
+  const MaskProblem pb{B,
+                       n_q,
+                       n_k,
+                       window_left < reach ? window_left : -1,
+                       window_right < reach ? window_right : -1,
+                       key_lens,
+                       doc_ids,
+                       prefix_lens};
+  const cudaError_t e = launch_mask_plan(pb, plan, make_ctx(*di, stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(doc_ids != nullptr ? 2 : 1);
+  return ATTN_OK;
+}
+
+int attn_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B, int h,
+                    int h_kv, int n_q, int n_k, int d_k, const int64_t* strides, float scale,
+                    float softcap, const float* slopes, const void* plan, size_t plan_bytes,
+                    struct CUstream_st* stream) {
+  int rc = check_scored(q, k, v, o, lse, B, h, h_kv, n_q, n_k, d_k, scale, softcap, slopes, plan,
+                        plan_bytes);
+  if (rc != ATTN_OK) return rc;
+  if (!tc_head_size(d_k)) return ATTN_ERR_UNSUPPORTED;
+  const int heads[4] = {h, h_kv, h_kv, h}, rows[4] = {n_q, n_k, n_k, n_q}, elem[4] = {2, 2, 2, 2};
+  Strides st[4];
+  if (!read_strides(st, strides, 4, heads, rows, d_k, elem)) return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  CUtensorMap tmq, tmk, tmv, tmo;
+  const int kv_rows = fwd_tc_kv_rows(d_k);
+  if ((rc = encode_4d(&tmq, q, d_k, n_q, h, B, st[0], 128)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&tmk, k, d_k, n_k, h_kv, B, st[1], kv_rows)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&tmv, v, d_k, n_k, h_kv, B, st[2], kv_rows)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&tmo, o, d_k, n_q, h, B, st[3], 128)) != ATTN_OK) return rc;
+  const Problem pb{q, k, v, o, lse, B, h, n_q, n_k, d_k, scale, kMaskNone, nullptr, 0, 0};
+  const ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k);
+  const cudaError_t e = launch_fwd_tc(pb, tmq, tmk, tmv, tmo, make_ctx(*di, stream), &mod);
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1);
+  return ATTN_OK;
+}
+
+size_t attn_bwd_scored_workspace_bytes(int B, int h, int n_q, int d_k) {
+  if (B < 1 || h < 1 || n_q < 1 || !bwd_head_size_ok(d_k)) return 0;
+  if (static_cast<long long>(B) * h > 0x7fffffffLL) return 0;
+  return bwd_layout(B, h, n_q, d_k).scored_bytes;
+}
+
+int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                    const float* lse, void* dq, void* dk, void* dv, int B, int h, int h_kv,
+                    int n_q, int n_k, int d_k, const int64_t* strides, float scale, float softcap,
+                    const float* slopes, const void* plan, size_t plan_bytes, void* workspace,
+                    size_t workspace_bytes, struct CUstream_st* stream) {
+  int rc = check_scored(q, k, v, o, lse, B, h, h_kv, n_q, n_k, d_k, scale, softcap, slopes, plan,
+                        plan_bytes);
+  if (rc != ATTN_OK) return rc;
+  if (!dout || !lse || !dq || !dk || !dv || !workspace) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+      !aligned16(workspace))
+    return ATTN_ERR_INVALID_ARG;
+  if (!bwd_head_size_ok(d_k)) return ATTN_ERR_UNSUPPORTED;
+  // order: q, k, v, o, dout, dq, dk, dv
+  const int heads[8] = {h, h_kv, h_kv, h, h, h, h_kv, h_kv},
+            rows[8] = {n_q, n_k, n_k, n_q, n_q, n_q, n_k, n_k}, elem[8] = {2, 2, 2, 2, 2, 2, 2, 2};
+  Strides st[8];
+  if (!read_strides(st, strides, 8, heads, rows, d_k, elem)) return ATTN_ERR_INVALID_ARG;
+  const BwdLayout lay = bwd_layout(B, h, n_q, d_k);
+  if (workspace_bytes < lay.scored_bytes) return ATTN_ERR_INVALID_ARG;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  CUtensorMap maps[7];
+  if ((rc = encode_4d(&maps[0], q, d_k, n_q, h, B, st[0], 128)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&maps[1], k, d_k, n_k, h_kv, B, st[1], 128)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&maps[2], v, d_k, n_k, h_kv, B, st[2], 128)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&maps[3], dout, d_k, n_q, h, B, st[4], 128)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&maps[4], dk, d_k, n_k, h_kv, B, st[6], 64)) != ATTN_OK) return rc;
+  if ((rc = encode_4d(&maps[5], dv, d_k, n_k, h_kv, B, st[7], 64)) != ATTN_OK) return rc;
+  if ((rc = encode_3d_f32(&maps[6], static_cast<uint8_t*>(workspace) + lay.dq_acc_off, d_k, n_q,
+                          static_cast<long long>(B) * h)) != ATTN_OK)
+    return rc;
+  const BwdProblem pb{q, k, v, o, dout, lse, dq, dk, dv, B, h, n_q, n_k, d_k, scale,
+                      kMaskNone, nullptr, 0, 0, st[3], st[4], st[5]};
+  const ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k);
+  const cudaError_t e = launch_bwd(pb, maps, workspace, make_ctx(*di, stream), &mod);
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(3);
+  return ATTN_OK;
+}
+
+}  // extern "C"

@@ -112,7 +112,12 @@ struct BCfg {
   static_assert(COL_PT + 64 <= 512, "tensor memory");
 };
 
-template <int D_>
+// Instantiations: the masks given by lengths (none, causal, key padding), the
+// restricted window, and changed scores under a mask plan; each keeps its code
+// out of the others'.
+enum Mode : int { kPlain = 0, kBand = 1, kScored = 2 };
+
+template <int D_, int MODE>
 struct __align__(1024) Smem {
   using C = BCfg<D_>;
   uint8_t k[2][C::TILE];
@@ -127,6 +132,8 @@ struct __align__(1024) Smem {
   // dQ, or dV / dK in bf16, swizzled as the tensor map it is copied with
   uint8_t stage[2][STAGE_BYTES];
   uint8_t cst[QSTAGES][CONST_TILE_BYTES];  // the constant tile of each Q stage
+  // with a cap: LSE * log2(e) of each Q stage's queries (see pre_kernel)
+  float lse[MODE == kScored ? QSTAGES : 1][MODE == kScored ? BM : 4];
   // Two 8 x 8 bf16 core matrices that select columns of the constant tile:
   // [0] rows (1,1,1,0,0,0,0,0) picks b, [1] rows (0,0,0,1,1,1,0,0) picks -D.
   uint8_t sel[2][512];
@@ -150,17 +157,54 @@ struct Params {
   int num_qt, num_kt, num_items;
   float scale_log2;  // scale * log2(e)
   float scale;
+  // changed scores (kScored): BH counts key heads then
+  int group;              // query heads per key head
+  float cap_log2;         // softcap * log2(e); 0: no cap
+  float cap_in;           // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
+  const float* slopes;    // distance bias per query head, or null
+  const float* lse_log2;  // with a cap: [B * H][num_qt * 128]
+  bool masked;
+  MaskPlan plan;
   uint64_t limit_ns;
   int* status;
 };
 
 // A work item: key tile kt of head bh and the query tiles qt0 .. qt0+n-1
 // that see at least one of its keys.
+// (kScored: bh is a key head's, and the n tiles are nq query tiles of each of
+// its query heads in turn.)
 struct Item {
   int bh, kt, qt0, n, key_limit;
+  int nq;
+  bool desc;  // kScored: heaviest key tiles first
 };
 
-__device__ __forceinline__ Item bwd_item(const Params& p, int t) {
+__device__ __forceinline__ Item bwd_item_planned(const Params& p, int t, bool desc) {
+  Item it;
+  if (desc) {
+    it.kt = t / p.BH;
+    it.bh = t % p.BH;
+  } else {
+    it.bh = t / p.num_kt;
+    it.kt = t % p.num_kt;
+  }
+  it.key_limit = p.n_k;
+  it.qt0 = 0;
+  it.nq = p.num_qt;
+  if (p.masked) {
+    const int4 r = __ldg(p.plan.tile_rows +
+                         static_cast<size_t>(it.bh / (p.H / p.group)) * p.num_kt + it.kt);
+    it.qt0 = r.x / BM;
+    it.nq = r.y > 0 ? (r.y + BM - 1) / BM - it.qt0 : 0;
+  }
+  it.n = it.nq * p.group;
+  it.desc = desc;
+  return it;
+}
+
+template <int MODE>
+__device__ __forceinline__ Item bwd_item(const Params& p, int t, bool desc) {
+  if constexpr (MODE == kScored) return bwd_item_planned(p, t, desc);
   Item it;
   if (p.mask == kMaskCausal) {
     // key tiles with the most query tiles first (longest-processing-time order)
@@ -196,13 +240,16 @@ __device__ __forceinline__ Item bwd_item(const Params& p, int t) {
       it.n = p.num_qt;
     }
   }
+  it.nq = it.n;
   return it;
 }
 
 // Index of the next item of this CTA at or after `from` with work, or -1.
-__device__ __forceinline__ int next_item(const Params& p, int from, Item& out) {
-  for (int x = from; x < p.num_items; x += gridDim.x) {
-    out = bwd_item(p, x);
+template <int MODE>
+__device__ __forceinline__ int next_item(const Params& p, int num_items, bool desc, int from,
+                                         Item& out) {
+  for (int x = from; x < num_items; x += gridDim.x) {
+    out = bwd_item<MODE>(p, x, desc);
     if (out.n > 0) return x;
   }
   return -1;
@@ -276,9 +323,57 @@ __device__ __forceinline__ uint64_t sdesc_swz(uint32_t smem_addr, uint32_t lbo_b
   return d;
 }
 
-// BAND = restricted self-attention (its own instantiation, so that the
-// window's two extra compares per score stay out of the other masks' code).
-template <bool BAND, int D_>
+// P of one thread's key and 64 queries with changed scores: w gets it in bf16
+// pairs for dV, pf what multiplies dP - D: P times the cap's derivative.
+// Columns outside [lim, hi) are forbidden.  dist: the key's index less the
+// first query's.  Without a cap the scores hold -LSE/scale already; with one
+// the constant is taken off here, because it must not pass through the tanh.
+__device__ __forceinline__ void scored_probabilities(const Params& p, const uint32_t (&s0)[32],
+                                                     const uint32_t (&s1)[32], float (&pf)[64],
+                                                     uint32_t (&w)[32], int lim, int hi, int dist,
+                                                     int head, bool capped, const float* lse) {
+  const float nslope = p.slopes != nullptr ? -LOG2E * __ldg(p.slopes + head) : 0.f;
+  const float far = static_cast<float>(dist);
+#pragma unroll
+  for (int i2 = 0; i2 < 32; i2 += 2) {
+    const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
+    const int c0 = 2 * i2;
+    float x[4], d[4];
+    if (capped) {
+      // tanh(y) = 1 - 2 / (1 + 2^(2 y log2(e)))
+      float t[4];
+      fma2(x[0], x[1], __uint_as_float(src[0]), __uint_as_float(src[1]), p.cap_in, p.cap_in, 0.f,
+           0.f);
+      fma2(x[2], x[3], __uint_as_float(src[2]), __uint_as_float(src[3]), p.cap_in, p.cap_in, 0.f,
+           0.f);
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        add2(t[e], t[e + 1], ex2(x[e]), ex2(x[e + 1]), 1.f, 1.f);
+        fma2(t[e], t[e + 1], rcp(t[e]), rcp(t[e + 1]), -2.f, -2.f, 1.f, 1.f);
+      }
+      const float4 l = *reinterpret_cast<const float4*>(lse + c0);
+      fma2(x[0], x[1], t[0], t[1], p.cap_log2, p.cap_log2, -l.x, -l.y);
+      fma2(x[2], x[3], t[2], t[3], p.cap_log2, p.cap_log2, -l.z, -l.w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = fmaf(-t[e], t[e], 1.f);
+    } else {
+      fma2(x[0], x[1], __uint_as_float(src[0]), __uint_as_float(src[1]), p.scale_log2,
+           p.scale_log2, 0.f, 0.f);
+      fma2(x[2], x[3], __uint_as_float(src[2]), __uint_as_float(src[3]), p.scale_log2,
+           p.scale_log2, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (p.slopes != nullptr) x[e] = fmaf(nslope, fabsf(far - static_cast<float>(c0 + e)), x[e]);
+      x[e] = c0 + e < lim || c0 + e >= hi ? 0.f : ex2(x[e]);
+      pf[c0 + e] = capped ? x[e] * d[e] : x[e];
+    }
+    w[i2] = pack_bf16x2(x[0], x[1]);
+    w[i2 + 1] = pack_bf16x2(x[2], x[3]);
+  }
+}
+
+template <int MODE, int D_>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                        const __grid_constant__ CUtensorMap tmk,
@@ -288,10 +383,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                        const __grid_constant__ CUtensorMap tmdv,
                        const __grid_constant__ CUtensorMap tmdq, const Params p) {
   using C = BCfg<D_>;
+  using S = Smem<D_, MODE>;
   constexpr int D = D_;
+  constexpr bool BAND = MODE == kBand, SCORED = MODE == kScored;
   extern __shared__ uint8_t smem_raw[];
-  Smem<D_>& sm = *reinterpret_cast<Smem<D_>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+  S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const volatile int* abort = &sm.abort;
@@ -360,39 +457,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // its tail, nothing below runs before it has completed.
   grid_dependency_wait();
 
+  int num_items = p.num_items;
+  bool desc = false;
+  if constexpr (SCORED) {
+    if (p.masked) {
+      const int4 h = __ldg(p.plan.header);
+      desc = h.w != 0;
+      if (h.x != p.n_q || h.y != p.n_k || h.z * (p.H / p.group) != p.BH) {
+        // a plan of other sizes: report it and do nothing
+        num_items = 0;
+        if (threadIdx.x == 0) atomicCAS(p.status, kDevOk, kDevWrongPlan);
+      }
+    }
+  }
+  const bool capped = SCORED && p.cap_log2 > 0.f;
+  // heads of K, V, dK and dV, and the query head of a key head's g-th group member
+  const int kv_heads = SCORED ? p.H / p.group : p.H;
+  auto q_head = [&](int bh, int g) { return SCORED ? bh % kv_heads * p.group + g : bh % p.H; };
+  // the item's next tile pair: the next query tile, then the next query head
+  auto step = [](const Item& item, int& qt, int& g) {
+    if (++qt == item.qt0 + item.nq) {
+      qt = item.qt0;
+      ++g;
+    }
+  };
+
   if (warp == LOAD_WARP) {
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       uint32_t it = 0, nv = 0, nq = 0, no = 0;  // K, V, Q and dO loads issued
       bool ok = true;
       Item item;
-      for (int x = next_item(p, blockIdx.x, item); x >= 0 && ok;
-           x = next_item(p, x + gridDim.x, item)) {
+      for (int x = next_item<MODE>(p, num_items, desc, blockIdx.x, item); x >= 0 && ok;
+           x = next_item<MODE>(p, num_items, desc, x + gridDim.x, item)) {
         const uint32_t slot = it & 1;
         ok = mbar_wait(smem_u32(&sm.k_empty[slot]), ((it >> 1) & 1) ^ 1, p.limit_ns, abort);
         if (!ok) break;
         mbar_arrive_expect_tx(smem_u32(&sm.k_full[slot]), C::TILE);
-        tma_load_4d(smem_u32(sm.k[slot]), &tmk, smem_u32(&sm.k_full[slot]), 0, item.kt * BN,
-                    item.bh % p.H, item.bh / p.H);
+        const int b = item.bh / kv_heads, hk = item.bh % kv_heads;
+        tma_load_4d(smem_u32(sm.k[slot]), &tmk, smem_u32(&sm.k_full[slot]), 0, item.kt * BN, hk, b);
         ++it;
-        for (int i = 0; i < item.n && ok; ++i) {
-          const int qt = item.qt0 + i;
+        int qt = item.qt0, g = 0;
+        for (int i = 0; i < item.n && ok; ++i, step(item, qt, g)) {
+          const int hq = q_head(item.bh, g);
           const uint32_t st = nq % QSTAGES;
           ok = mbar_wait(smem_u32(&sm.q_empty[st]), ((nq / QSTAGES) & 1) ^ 1, p.limit_ns, abort);
           if (!ok) break;
           const uint32_t qb = smem_u32(&sm.q_full[st]);
-          mbar_arrive_expect_tx(qb, C::TILE + CONST_TILE_BYTES);
-          tma_load_4d(smem_u32(sm.q[st]), &tmq, qb, 0, qt * BM, item.bh % p.H, item.bh / p.H);
-          const size_t tile = static_cast<size_t>(item.bh) * p.num_qt + qt;
+          mbar_arrive_expect_tx(qb, C::TILE + CONST_TILE_BYTES + (capped ? BM * 4 : 0));
+          tma_load_4d(smem_u32(sm.q[st]), &tmq, qb, 0, qt * BM, hq, b);
+          const size_t tile = (static_cast<size_t>(b) * p.H + hq) * p.num_qt + qt;
           bulk_load(smem_u32(sm.cst[st]), p.cst + tile * CONST_TILE_BYTES, CONST_TILE_BYTES, qb);
+          if constexpr (SCORED) {
+            if (capped) bulk_load(smem_u32(sm.lse[st]), p.lse_log2 + tile * BM, BM * 4, qb);
+          }
           ++nq;
           if (i == 0) {
             // V of this item, once the previous item's last dP has read the slot
             ok = mbar_wait(smem_u32(&sm.v_empty), (nv & 1) ^ 1, p.limit_ns, abort);
             if (!ok) break;
             mbar_arrive_expect_tx(smem_u32(&sm.v_full), C::TILE);
-            tma_load_4d(smem_u32(sm.v), &tmv, smem_u32(&sm.v_full), 0, item.kt * BN,
-                        item.bh % p.H, item.bh / p.H);
+            tma_load_4d(smem_u32(sm.v), &tmv, smem_u32(&sm.v_full), 0, item.kt * BN, hk, b);
             ++nv;
           }
           const uint32_t os = no % OSTAGES;
@@ -400,8 +525,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           const uint32_t ob = smem_u32(&sm.o_full[os]);
           mbar_arrive_expect_tx(ob, C::TILE);
-          tma_load_4d(smem_u32(sm.dout[os]), &tmdo, ob, 0, qt * BM, item.bh % p.H,
-                      item.bh / p.H);
+          tma_load_4d(smem_u32(sm.dout[os]), &tmdo, ob, 0, qt * BM, hq, b);
           ++no;
         }
       }
@@ -490,7 +614,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     uint32_t it = 0, t = 0;
     Item cur;
-    int cx = next_item(p, blockIdx.x, cur);
+    int cx = next_item<MODE>(p, num_items, desc, blockIdx.x, cur);
     int ci = 0;  // index of tile t inside its item
     if (cx >= 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0) && wait(&sm.v_full, 0) &&
         wait(&sm.o_full[0], 0)) {
@@ -504,7 +628,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int nxx = cx, ni = ci + 1;
         uint32_t nit = it;
         if (ni >= cur.n) {
-          nxx = next_item(p, cx + gridDim.x, nx);
+          nxx = next_item<MODE>(p, num_items, desc, cx + gridDim.x, nx);
           ni = 0;
           nit = it + 1;
         }
@@ -608,9 +732,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       named_bar_sync(bar_id, 64);
     };
     uint32_t it = 0, t = 0;
-    for (int x = blockIdx.x; x < p.num_items && ok; x += gridDim.x) {
-      const Item item = bwd_item(p, x);
+    for (int x = blockIdx.x; x < num_items && ok; x += gridDim.x) {
+      const Item item = bwd_item<MODE>(p, x, desc);
       const int key_row0 = item.kt * BN + 64 * g;
+      const int b = item.bh / kv_heads, hk = item.bh % kv_heads;
       if (item.n == 0) {
         // no query sees these keys: dK = dV = 0
         uint32_t w[32];
@@ -620,38 +745,40 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         st_row_swz<C::RB>(stage, rg, w);
         stage_release();
         if (leader && key_row0 < p.n_k) {
-          tma_store_4d(&tmdk, stage, 0, key_row0, item.bh % p.H, item.bh / p.H);
-          tma_store_4d(&tmdv, stage, 0, key_row0, item.bh % p.H, item.bh / p.H);
+          tma_store_4d(&tmdk, stage, 0, key_row0, hk, b);
+          tma_store_4d(&tmdv, stage, 0, key_row0, hk, b);
           bulk_commit_group();
         }
         continue;
       }
-      for (int i = 0; i < item.n; ++i, ++t) {
+      int qt = item.qt0, member = 0;
+      for (int i = 0; i < item.n; ++i, ++t, step(item, qt, member)) {
         if (!wait(&sm.dq_full, t & 1)) break;
         tc_fence_after();
-        uint32_t a[32], b[32];
+        uint32_t a[32], a2[32];
         tmem_ld32(tmem + lane_off + C::COL_DQ, a);
-        if constexpr (D > 32) tmem_ld32(tmem + lane_off + C::COL_DQ + 32, b);
+        if constexpr (D > 32) tmem_ld32(tmem + lane_off + C::COL_DQ + 32, a2);
         tmem_ld_wait(a);
-        if constexpr (D > 32) reg_fence(b);
+        if constexpr (D > 32) reg_fence(a2);
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.dq_free));
         // fp32 boxes of min(d, 32) columns x 64 rows per group, each added
         // into the accumulator by one TMA reduce; rows past n_q are not touched
-        const int q_row0 = (item.qt0 + i) * BM + 64 * g;
+        const int q_row0 = qt * BM + 64 * g;
+        const int qbh = SCORED ? b * p.H + q_head(item.bh, member) : item.bh;
         stage_acquire();
         st_row_swz<C::QRB>(stage, rg, a);
         stage_release();
         if (leader && q_row0 < p.n_q) {
-          tma_reduce_add_3d(&tmdq, stage, 0, q_row0, item.bh);
+          tma_reduce_add_3d(&tmdq, stage, 0, q_row0, qbh);
           bulk_commit_group();
         }
         if constexpr (D > 32) {
           stage_acquire();
-          st_row_swz<C::QRB>(stage, rg, b);
+          st_row_swz<C::QRB>(stage, rg, a2);
           stage_release();
           if (leader && q_row0 < p.n_q) {
-            tma_reduce_add_3d(&tmdq, stage, 32, q_row0, item.bh);
+            tma_reduce_add_3d(&tmdq, stage, 32, q_row0, qbh);
             bulk_commit_group();
           }
         }
@@ -662,13 +789,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // both are in registers
 #pragma unroll 1
       for (int which = 0; which < 2; ++which) {
-        uint32_t a[32], b[32], w[32];
+        uint32_t a[32], a2[32], w[32];
         const uint32_t col = which == 0 ? C::COL_DV : C::COL_DK;
         const float sc = which == 0 ? 1.f : p.scale;
         tmem_ld32(tmem + lane_off + col, a);
-        if constexpr (D > 32) tmem_ld32(tmem + lane_off + col + 32, b);
+        if constexpr (D > 32) tmem_ld32(tmem + lane_off + col + 32, a2);
         tmem_ld_wait(a);
-        if constexpr (D > 32) reg_fence(b);
+        if constexpr (D > 32) reg_fence(a2);
         if (which == 1) {
           tc_fence_before();
           mbar_arrive(smem_u32(&sm.dkv_free));
@@ -679,14 +806,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             w[i] = pack_bf16x2(__uint_as_float(a[2 * i]) * sc, __uint_as_float(a[2 * i + 1]) * sc);
           if constexpr (D > 32)
             w[16 + i] =
-                pack_bf16x2(__uint_as_float(b[2 * i]) * sc, __uint_as_float(b[2 * i + 1]) * sc);
+                pack_bf16x2(__uint_as_float(a2[2 * i]) * sc, __uint_as_float(a2[2 * i + 1]) * sc);
         }
         stage_acquire();
         st_row_swz<C::RB>(stage, rg, w);
         stage_release();
         if (leader && key_row0 < p.n_k) {
-          tma_store_4d(which == 0 ? &tmdv : &tmdk, stage, 0, key_row0, item.bh % p.H,
-                       item.bh / p.H);
+          tma_store_4d(which == 0 ? &tmdv : &tmdk, stage, 0, key_row0, hk, b);
           bulk_commit_group();
         }
       }
@@ -711,12 +837,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     };
     uint32_t t = 0;
     Item item;
-    for (int x = next_item(p, blockIdx.x, item); x >= 0 && ok;
-         x = next_item(p, x + gridDim.x, item)) {
+    for (int x = next_item<MODE>(p, num_items, desc, blockIdx.x, item); x >= 0 && ok;
+         x = next_item<MODE>(p, num_items, desc, x + gridDim.x, item)) {
       const int j = item.kt * BN + r;  // this thread's key
       const bool row_valid = j < item.key_limit;
-      for (int i = 0; i < item.n; ++i, ++t) {
-        const int qt = item.qt0 + i;
+      // the queries of this key, and those of every key of the tile
+      int2 rows = make_int2(0, p.n_q), all = make_int2(0, p.n_q);
+      if constexpr (SCORED) {
+        if (p.masked) {
+          const size_t b = item.bh / kv_heads;
+          rows = row_valid ? __ldg(p.plan.key_rows + b * p.n_k + j) : make_int2(0, 0);
+          const int4 v = __ldg(p.plan.tile_rows + b * p.num_kt + item.kt);
+          all = make_int2(v.z, v.w);
+        }
+      }
+      int qt = item.qt0, member = 0;
+      for (int i = 0; i < item.n; ++i, ++t, step(item, qt, member)) {
         // leading columns whose query precedes this key (causal diagonal
         // tile), or all of them for a key past the sequence; with the window,
         // the columns outside [lim, hi) (queries i with j < i - left or
@@ -724,6 +860,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         int lim = 0, hi = 64;
         if (!row_valid) {
           lim = 64;
+        } else if (SCORED) {
+          const int qbase = qt * BM + 64 * half;
+          if (qt * BM < all.x || qt * BM + BM > all.y) {
+            lim = min(max(rows.x - qbase, 0), 64);
+            hi = min(max(rows.y - qbase, 0), 64);
+          }
         } else if (p.mask == kMaskCausal && qt == item.kt) {
           lim = min(max(r - 64 * half, 0), 64);
         } else if (BAND) {
@@ -732,6 +874,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           hi = min(max(j + p.win_left - qbase + 1, 0), 64);
         }
         if (!wait(&sm.s_full, t & 1)) break;
+        // (the stage's lse was copied with its Q; the stage is held until dK of
+        // this tile pair, which waits for dS)
+        if (SCORED && capped && !wait(&sm.q_full[t % QSTAGES], (t / QSTAGES) & 1)) break;
         tc_fence_after();
         uint32_t s0[32], s1[32];
         tmem_ld32(tS, s0);
@@ -744,6 +889,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // P = 2^(scale * log2(e) * S') (S' already holds -LSE/scale), zero
         // where forbidden
         float pf[64];
+        uint32_t w[32];
+        if constexpr (SCORED) {
+          scored_probabilities(p, s0, s1, pf, w, lim, hi, j - qt * BM - 64 * half,
+                                   q_head(item.bh, member), capped,
+                                   capped ? sm.lse[t % QSTAGES] + 64 * half : nullptr);
+        } else {
 #pragma unroll
         for (int i2 = 0; i2 < 32; i2 += 2) {
           const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
@@ -756,9 +907,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           pf[c0 + 2] = (c0 + 2 < lim || (BAND && c0 + 2 >= hi)) ? 0.f : ex2(x2);
           pf[c0 + 3] = (c0 + 3 < lim || (BAND && c0 + 3 >= hi)) ? 0.f : ex2(x3);
         }
-        uint32_t w[32];
 #pragma unroll
         for (int i2 = 0; i2 < 32; ++i2) w[i2] = pack_bf16x2(pf[2 * i2], pf[2 * i2 + 1]);
+        }
         // P^T of the previous tile pair has been read by its dV product
         if (!wait(&sm.p_free, (t & 1) ^ 1)) break;
         tc_fence_after();
@@ -837,7 +988,8 @@ __global__ void __launch_bounds__(256)
     attn_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                         const float* __restrict__ lse, uint8_t* __restrict__ cst,
                         float* __restrict__ dq_acc, int H, int n_q, int num_qt, float inv_scale,
-                        long long rows, RowStrides so, RowStrides sdo) {
+                        long long rows, RowStrides so, RowStrides sdo,
+                        float* __restrict__ lse_log2) {
   // the main kernel may start launching now: it waits for this grid to
   // complete before it reads the constants or adds into dq_acc
   grid_launch_dependents();
@@ -880,7 +1032,8 @@ __global__ void __launch_bounds__(256)
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     if (sub == 0 && valid) {
       const float l = lse[static_cast<size_t>(bh) * n_q + i];
-      const float b = isfinite(l) ? -l * inv_scale : 0.f;  // -inf only for a row that sees no key
+      // -inf only for a row that sees no key; a cap takes LSE off after the tanh
+      const float b = isfinite(l) && lse_log2 == nullptr ? -l * inv_scale : 0.f;
       const uint2 pb = split3_bf16(b);
       const uint2 pd = split3_bf16(-acc);
       w.x = pb.x;                         // b_hi, b_mid
@@ -888,6 +1041,10 @@ __global__ void __launch_bounds__(256)
       w.z = (pd.x >> 16) | (pd.y << 16);  // -D_mid, -D_lo
     }
     *reinterpret_cast<uint4*>(tile + (n & 7) * 16 + (n >> 3) * 256 + sub * 128) = w;
+    if (lse_log2 != nullptr && sub == 0) {
+      const float l = valid ? lse[static_cast<size_t>(bh) * n_q + i] : 0.f;
+      lse_log2[(static_cast<size_t>(bh) * num_qt + qt) * BM + n] = isfinite(l) ? l * LOG2E : 0.f;
+    }
   }
 }
 
@@ -921,20 +1078,38 @@ BwdLayout bwd_layout(int B, int H, int n_q, int d) {
   l.num_qt = (n_q + BM - 1) / BM;
   l.cst_off = 0;
   l.dq_acc_off = bh * l.num_qt * CONST_TILE_BYTES;
-  l.bytes = l.dq_acc_off + bh * static_cast<size_t>(n_q) * d * 4;
+  l.lse_off = l.dq_acc_off + bh * static_cast<size_t>(n_q) * d * 4;
+  l.bytes = l.lse_off;
+  l.scored_bytes = l.lse_off + bh * l.num_qt * BM * 4;
   return l;
 }
 
 namespace {
 
+template <int MODE, int D>
+cudaError_t launch_bwd_main(const Params& p, const CUtensorMap* maps, const LaunchCtx& ctx) {
+  static_assert(sizeof(Smem<D, MODE>) + 1024 <= 232448, "shared memory");
+  const size_t smem = sizeof(Smem<D, MODE>) + 1024;
+  cudaError_t err = cudaFuncSetAttribute(attn_bwd_tc_kernel<MODE, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  const int grid = p.num_items < ctx.num_sms ? p.num_items : ctx.num_sms;
+  return launch_dependent(attn_bwd_tc_kernel<MODE, D>, dim3(grid), dim3(NUM_THREADS), smem,
+                          ctx.stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
+                          maps[6], p);
+}
+
 template <int D>
 cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* workspace,
-                         const LaunchCtx& ctx) {
-  static_assert(sizeof(Smem<D>) + 1024 <= 232448, "shared memory");
+                         const LaunchCtx& ctx, const ScoreMod* mod) {
   const BwdLayout lay = bwd_layout(pb.B, pb.H, pb.n_q, D);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint8_t* cst = ws + lay.cst_off;
   float* dq_acc = reinterpret_cast<float*>(ws + lay.dq_acc_off);
+  float* lse_log2 = mod != nullptr && mod->softcap > 0.f
+                        ? reinterpret_cast<float*>(ws + lay.lse_off)
+                        : nullptr;
   const long long bh = static_cast<long long>(pb.B) * pb.H;
 
   const long long rows = bh * static_cast<long long>(lay.num_qt) * BM;
@@ -943,11 +1118,11 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   attn_bwd_pre_kernel<D><<<static_cast<unsigned>(pre_blocks), 256, 0, ctx.stream>>>(
       static_cast<const __nv_bfloat16*>(pb.o), static_cast<const __nv_bfloat16*>(pb.dout), pb.lse,
       cst, dq_acc, pb.H, pb.n_q, static_cast<int>(lay.num_qt), 1.f / pb.scale, rows, pb.so,
-      pb.sdo);
+      pb.sdo, lse_log2);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
 
-  Params p;
+  Params p{};
   p.cst = cst;
   p.key_lens = pb.key_lens;
   p.H = pb.H;
@@ -964,21 +1139,25 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   p.scale = pb.scale;
   p.limit_ns = ctx.limit_ns;
   p.status = ctx.status;
-  const size_t smem = sizeof(Smem<D>) + 1024;
-  const bool band = pb.mask == kMaskBand;
-  err = cudaFuncSetAttribute(band ? reinterpret_cast<const void*>(attn_bwd_tc_kernel<true, D>)
-                                  : reinterpret_cast<const void*>(attn_bwd_tc_kernel<false, D>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (err != cudaSuccess) return err;
-  const int grid = p.num_items < ctx.num_sms ? p.num_items : ctx.num_sms;
   // the main and the dQ kernels start while their predecessor drains
   // (programmatic dependent launch; each waits for it before reading its output)
-  err = band ? launch_dependent(attn_bwd_tc_kernel<true, D>, dim3(grid), dim3(NUM_THREADS), smem,
-                                ctx.stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
-                                maps[6], p)
-             : launch_dependent(attn_bwd_tc_kernel<false, D>, dim3(grid), dim3(NUM_THREADS), smem,
-                                ctx.stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
-                                maps[6], p);
+  if (mod != nullptr) {
+    p.mask = kMaskNone;
+    p.group = mod->group;
+    p.BH = p.BH / mod->group;
+    p.num_items = p.BH * p.num_kt;
+    p.cap_log2 = mod->softcap * LOG2E;
+    p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
+    p.slopes = mod->slopes;
+    p.lse_log2 = lse_log2;
+    p.masked = mod->masked;
+    p.plan = mod->plan;
+    err = launch_bwd_main<kScored, D>(p, maps, ctx);
+  } else if (pb.mask == kMaskBand) {
+    err = launch_bwd_main<kBand, D>(p, maps, ctx);
+  } else {
+    err = launch_bwd_main<kPlain, D>(p, maps, ctx);
+  }
   if (err != cudaSuccess) return err;
 
   const long long n8 = bh * pb.n_q * (D / 8);
@@ -993,11 +1172,11 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
 bool bwd_head_size_ok(int d) { return d == 16 || d == 32 || d == 64; }
 
 cudaError_t launch_bwd(const BwdProblem& pb, const CUtensorMap* maps, void* workspace,
-                       const LaunchCtx& ctx) {
+                       const LaunchCtx& ctx, const ScoreMod* mod) {
   switch (pb.d) {
-    case 16: return launch_bwd_d<16>(pb, maps, workspace, ctx);
-    case 32: return launch_bwd_d<32>(pb, maps, workspace, ctx);
-    case 64: return launch_bwd_d<64>(pb, maps, workspace, ctx);
+    case 16: return launch_bwd_d<16>(pb, maps, workspace, ctx, mod);
+    case 32: return launch_bwd_d<32>(pb, maps, workspace, ctx, mod);
+    case 64: return launch_bwd_d<64>(pb, maps, workspace, ctx, mod);
     default: return cudaErrorInvalidValue;
   }
 }

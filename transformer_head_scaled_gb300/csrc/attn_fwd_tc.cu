@@ -110,6 +110,11 @@ struct __align__(1024) Smem {
   int abort;
 };
 
+// Instantiations: the masks given by lengths (none, causal, key padding), the
+// restricted window, and changed scores under a mask plan; each keeps its code
+// out of the others'.
+enum Mode : int { kPlain = 0, kBand = 1, kScored = 2 };
+
 struct Params {
   __nv_bfloat16* o;
   float* lse;
@@ -120,6 +125,13 @@ struct Params {
   int num_qblocks;
   int num_items;
   float scale_log2;  // scale * log2(e): exp(scale*s) = 2^(s*scale_log2)
+  // changed scores (kScored)
+  int group;            // query heads per key head
+  float cap_log2;       // softcap * log2(e); 0: no cap
+  float cap_in;         // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
+  const float* slopes;  // distance bias per head, or null
+  bool masked;
+  MaskPlan plan;
   uint64_t limit_ns;
   int* status;
 };
@@ -134,8 +146,45 @@ struct Item {
   int n[QT];
 };
 
-template <bool BAND, int BN>
-__device__ __forceinline__ Item decode_item(const Params& p, int t) {
+// An item under a mask plan.  desc: later queries see more keys, so that the
+// heaviest row blocks come first as under the causal mask.
+template <int BN>
+__device__ __forceinline__ Item decode_item_planned(const Params& p, int t, bool desc) {
+  Item it;
+  if (desc) {
+    it.qb = p.num_qblocks - 1 - t / p.BH;
+    it.bh = t % p.BH;
+  } else {
+    it.qb = t % p.num_qblocks;
+    it.bh = t / p.num_qblocks;
+  }
+  it.key_limit = p.n_k;
+  it.j0 = 0;
+  int first[QT], end[QT];
+#pragma unroll
+  for (int s = 0; s < QT; ++s) {
+    const int tile = it.qb * QT + s;
+    first[s] = end[s] = 0;
+    if (tile * BM >= p.n_q) continue;
+    end[s] = p.n_k;
+    if (p.masked) {
+      const int4 r = __ldg(p.plan.block_keys +
+                           static_cast<size_t>(it.bh / p.H) * ((p.n_q + BM - 1) / BM) + tile);
+      first[s] = r.x;
+      end[s] = r.y;
+    }
+  }
+  // both Q tiles walk the same stream of K/V tiles, from the first that either needs
+  it.j0 = min(end[0] > 0 ? first[0] : 0x7fffffff, end[1] > 0 ? first[1] : 0x7fffffff) / BN;
+#pragma unroll
+  for (int s = 0; s < QT; ++s) it.n[s] = end[s] > 0 ? (end[s] + BN - 1) / BN - it.j0 : 0;
+  return it;
+}
+
+template <int MODE, int BN>
+__device__ __forceinline__ Item decode_item(const Params& p, int t, bool desc) {
+  if constexpr (MODE == kScored) return decode_item_planned<BN>(p, t, desc);
+  constexpr bool BAND = MODE == kBand;
   Item it;
   if (p.mask == kMaskCausal) {
     // heaviest row blocks first (longest-processing-time order)
@@ -198,9 +247,7 @@ __device__ __forceinline__ void record_timeout(const Params& p, SmemT& sm) {
   *reinterpret_cast<volatile int*>(&sm.abort) = 1;
 }
 
-// BAND = restricted self-attention (its own instantiation, so that the
-// other masks' code is not touched by the window logic).
-template <bool BAND, int D_>
+template <int MODE, int D_>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                        const __grid_constant__ CUtensorMap tmk,
@@ -209,6 +256,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   using C = Cfg<D_>;
   constexpr int D = C::D, BN = C::BN, QBUF = C::QBUF, KSTAGES = C::KSTAGES,
                 VSTAGES = C::VSTAGES;
+  constexpr bool SCORED = MODE == kScored;
+  constexpr bool BAND = MODE == kBand;
+  constexpr bool OFFSET = MODE != kPlain;  // an item's stream may begin past key 0
   extern __shared__ uint8_t smem_raw[];
   Smem<D_>& sm = *reinterpret_cast<Smem<D_>*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -255,6 +305,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
+  int num_items = p.num_items;
+  bool desc = false;
+  if constexpr (SCORED) {
+    if (p.masked) {
+      const int4 h = __ldg(p.plan.header);
+      desc = h.w != 0;
+      if (h.x != p.n_q || h.y != p.n_k || h.z * p.H != p.BH) {
+        // a plan of other sizes: report it and write nothing
+        num_items = 0;
+        if (threadIdx.x == 0) atomicCAS(p.status, kDevOk, kDevWrongPlan);
+      }
+    }
+  }
+  // K and V have one head for every `group` query heads
+  auto kv_head = [&](int bh) { return SCORED ? bh % p.H / p.group : bh % p.H; };
+
   if (warp >= LOAD_WARP) {
     setmaxnreg_dec<PRODUCER_REGS>();
    if (warp == LOAD_WARP || warp == VLOAD_WARP) {
@@ -272,8 +338,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t cnt = 0;
       uint32_t items = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < p.num_items && ok; t += gridDim.x, ++items) {
-        const Item it = decode_item<BAND, BN>(p, t);
+      for (int t = blockIdx.x; t < num_items && ok; t += gridDim.x, ++items) {
+        const Item it = decode_item<MODE, BN>(p, t, desc);
         const int nmax = max(it.n[0], it.n[1]);
         // Q tiles of this item into buffer items % 2 (free once the S
         // products of item - 2 are done), then its K tiles.
@@ -300,8 +366,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int cb = 0; cb < C::NB; ++cb)
             tma_load_4d(smem_u32(ring + slot * C::KV_TILE) + cb * C::KV_BLOCK, map,
-                        smem_u32(&full[slot]), 64 * cb, ((BAND ? it.j0 : 0) + j) * BN,
-                        it.bh % p.H, it.bh / p.H);
+                        smem_u32(&full[slot]), 64 * cb, ((OFFSET ? it.j0 : 0) + j) * BN,
+                        kv_head(it.bh), it.bh / p.H);
           ++cnt;
         }
       }
@@ -396,8 +462,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       };
 
       uint32_t g0 = 0, items = 0;
-      for (int t = blockIdx.x; t < p.num_items && ok; t += gridDim.x, ++items) {
-        const Item it = decode_item<BAND, BN>(p, t);
+      for (int t = blockIdx.x; t < num_items && ok; t += gridDim.x, ++items) {
+        const Item it = decode_item<MODE, BN>(p, t, desc);
         const int n = it.n[s];
         const int nmax = max(it.n[0], it.n[1]);
         // The previous item's last PV product goes first unless this item's
@@ -464,7 +530,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int OC = C::OW / 32;     // 32-column chunks of O
     const bool causal = p.mask == kMaskCausal;
     constexpr bool band = BAND;
-    const float c = p.scale_log2;
+    const bool capped = SCORED && p.cap_log2 > 0.f;
+    const bool biased = SCORED && p.slopes != nullptr;
+    // what is left to multiply a score by (the cap and the bias leave log2 units)
+    const float c = capped || biased ? 1.f : p.scale_log2;
     uint32_t u = 0;  // tiles this stage has processed (all items)
     // Ping-pong: on the tiles both Q tiles visit, the two softmax warpgroups
     // take turns for the exp phase (the MUFU-bound part), so that one
@@ -473,12 +542,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t turns = 0;
     if (s == 1) mbar_arrive(smem_u32(&sm.turn[0]));  // Q tile 0 goes first
     bool ok = true;
-    for (int t = blockIdx.x; t < p.num_items && ok; t += gridDim.x) {
-      const Item it = decode_item<BAND, BN>(p, t);
+    for (int t = blockIdx.x; t < num_items && ok; t += gridDim.x) {
+      const Item it = decode_item<MODE, BN>(p, t, desc);
       const int row0 = it.qb * ROWS + s * BM;
       const int row = row0 + quarter * 32 + lane;
       float m = -INFINITY;  // running max of scale*log2(e)*score (possibly stale)
       float l = 0.f;        // running sum of 2^(x - m)
+      // this row's keys, and those that every row of the Q tile sees
+      int row_lo = 0, row_hi = p.n_k, all_lo = 0, all_hi = p.n_k;
+      float nslope = 0.f;  // -slope in log2 units
+      if constexpr (SCORED) {
+        if (p.masked && it.n[s] > 0) {
+          const size_t b = it.bh / p.H;
+          const int4 r = __ldg(p.plan.block_keys + b * ((p.n_q + BM - 1) / BM) + row0 / BM);
+          all_lo = r.z;
+          all_hi = r.w;
+          const int2 v = row < p.n_q ? __ldg(p.plan.row_keys + b * p.n_q + row) : make_int2(0, 0);
+          row_lo = v.x;
+          row_hi = v.y;
+        }
+        if (biased) nslope = -1.4426950408889634f * __ldg(p.slopes + it.bh % p.H);
+      }
       for (int j = 0; j < it.n[s]; ++j, ++u) {
         ok = mbar_wait(smem_u32(&sm.s_full[s]), u & 1, p.limit_ns, abort);
         ok = __all_sync(0xffffffffu, ok);
@@ -494,8 +578,61 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.s_free[s]));
 
-        const int kbase = ((BAND ? it.j0 : 0) + j) * BN;
-        if (kbase + BN > it.key_limit || (causal && kbase + BN - 1 > row0) ||
+        const int kbase = ((OFFSET ? it.j0 : 0) + j) * BN;
+        if constexpr (SCORED) {
+          if (capped) {
+            // cap * tanh(y) = cap - 2 cap / (1 + 2^(2 y log2(e))), in log2 units
+#pragma unroll
+            for (int q4 = 0; q4 < SC; ++q4)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float x0, x1;
+                fma2(x0, x1, __uint_as_float(r[q4][i]), __uint_as_float(r[q4][i + 1]), p.cap_in,
+                     p.cap_in, 0.f, 0.f);
+                add2(x0, x1, ex2(x0), ex2(x1), 1.f, 1.f);
+                fma2(x0, x1, rcp(x0), rcp(x1), -2.f * p.cap_log2, -2.f * p.cap_log2, p.cap_log2,
+                     p.cap_log2);
+                r[q4][i] = __float_as_uint(x0);
+                r[q4][i + 1] = __float_as_uint(x1);
+              }
+          }
+          if (biased) {
+            const float f = capped ? 1.f : p.scale_log2;
+            const float far = static_cast<float>(row - kbase);  // distance to the first column
+            if (kbase + BN - 1 <= row0) {
+              // every key lies before every query: the bias is linear in the column
+              const float b0 = nslope * far;
+#pragma unroll
+              for (int q4 = 0; q4 < SC; ++q4)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float b1, b2, x0, x1;
+                  const float col = static_cast<float>(q4 * 32 + i);
+                  fma2(b1, b2, col, col + 1.f, -nslope, -nslope, b0, b0);
+                  fma2(x0, x1, __uint_as_float(r[q4][i]), __uint_as_float(r[q4][i + 1]), f, f, b1,
+                       b2);
+                  r[q4][i] = __float_as_uint(x0);
+                  r[q4][i + 1] = __float_as_uint(x1);
+                }
+            } else {
+#pragma unroll
+              for (int q4 = 0; q4 < SC; ++q4)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  r[q4][i] = __float_as_uint(
+                      fmaf(__uint_as_float(r[q4][i]), f,
+                           nslope * fabsf(far - static_cast<float>(q4 * 32 + i))));
+            }
+          }
+          if (kbase < all_lo || kbase + BN > all_hi) {
+            const int lim = row_hi - kbase, lo = row_lo - kbase;  // columns [lo, lim) are visible
+#pragma unroll
+            for (int q4 = 0; q4 < SC; ++q4)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (q4 * 32 + i >= lim || q4 * 32 + i < lo) r[q4][i] = __float_as_uint(-INFINITY);
+          }
+        } else if (kbase + BN > it.key_limit || (causal && kbase + BN - 1 > row0) ||
             (band && (kbase < row0 + BM - 1 - p.win_left || kbase + BN - 1 > row0 + p.win_right))) {
           int lim = it.key_limit - kbase;  // columns >= lim are forbidden
           int lo = 0;                      // and columns < lo
@@ -656,7 +793,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-template <bool BAND, int D_>
+template <int MODE, int D_>
 cudaError_t launch_instance(const Params& p, const CUtensorMap& tmq, const CUtensorMap& tmk,
                             const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx) {
   static_assert(sizeof(Smem<D_>) + 1024 <= 232448, "dynamic shared memory per CTA");
@@ -664,22 +801,23 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& tmq, const CUten
   // The register hand-over inside the kernel assumes the launch holds
   // LAUNCH_REGS per thread; refuse to launch a build that does not.
   cudaFuncAttributes attr;
-  cudaError_t err = cudaFuncGetAttributes(&attr, attn_fwd_tc_kernel<BAND, D_>);
+  cudaError_t err = cudaFuncGetAttributes(&attr, attn_fwd_tc_kernel<MODE, D_>);
   if (err != cudaSuccess) return err;
   if (attr.numRegs != LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-  err = cudaFuncSetAttribute(attn_fwd_tc_kernel<BAND, D_>,
+  err = cudaFuncSetAttribute(attn_fwd_tc_kernel<MODE, D_>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (err != cudaSuccess) return err;
   const int grid = p.num_items < ctx.num_sms ? p.num_items : ctx.num_sms;
-  attn_fwd_tc_kernel<BAND, D_><<<grid, NUM_THREADS, smem, ctx.stream>>>(tmq, tmk, tmv, tmo, p);
+  attn_fwd_tc_kernel<MODE, D_><<<grid, NUM_THREADS, smem, ctx.stream>>>(tmq, tmk, tmv, tmo, p);
   return cudaGetLastError();
 }
 
 template <int D_>
-cudaError_t launch_d(const Params& p, bool band, const CUtensorMap& tmq, const CUtensorMap& tmk,
+cudaError_t launch_d(const Params& p, int mode, const CUtensorMap& tmq, const CUtensorMap& tmk,
                      const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx) {
-  return band ? launch_instance<true, D_>(p, tmq, tmk, tmv, tmo, ctx)
-              : launch_instance<false, D_>(p, tmq, tmk, tmv, tmo, ctx);
+  return mode == kScored ? launch_instance<kScored, D_>(p, tmq, tmk, tmv, tmo, ctx)
+         : mode == kBand ? launch_instance<kBand, D_>(p, tmq, tmk, tmv, tmo, ctx)
+                         : launch_instance<kPlain, D_>(p, tmq, tmk, tmv, tmo, ctx);
 }
 
 }  // namespace
@@ -687,8 +825,9 @@ cudaError_t launch_d(const Params& p, bool band, const CUtensorMap& tmq, const C
 int fwd_tc_kv_rows(int d) { return d == 128 ? Cfg<128>::BN : Cfg<64>::BN; }
 
 cudaError_t launch_fwd_tc(const Problem& pb, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                          const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx) {
-  Params p;
+                          const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx,
+                          const ScoreMod* mod) {
+  Params p{};
   p.o = static_cast<__nv_bfloat16*>(pb.o);
   p.lse = pb.lse;
   p.key_lens = pb.key_lens;
@@ -704,12 +843,21 @@ cudaError_t launch_fwd_tc(const Problem& pb, const CUtensorMap& tmq, const CUten
   p.scale_log2 = pb.scale * 1.4426950408889634f;
   p.limit_ns = ctx.limit_ns;
   p.status = ctx.status;
-  const bool band = pb.mask == kMaskBand;
+  if (mod != nullptr) {
+    p.mask = kMaskNone;
+    p.group = mod->group;
+    p.cap_log2 = mod->softcap * 1.4426950408889634f;
+    p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
+    p.slopes = mod->slopes;
+    p.masked = mod->masked;
+    p.plan = mod->plan;
+  }
+  const int mode = mod != nullptr ? kScored : (pb.mask == kMaskBand ? kBand : kPlain);
   switch (pb.d) {
-    case 16: return launch_d<16>(p, band, tmq, tmk, tmv, tmo, ctx);
-    case 32: return launch_d<32>(p, band, tmq, tmk, tmv, tmo, ctx);
-    case 64: return launch_d<64>(p, band, tmq, tmk, tmv, tmo, ctx);
-    case 128: return launch_d<128>(p, band, tmq, tmk, tmv, tmo, ctx);
+    case 16: return launch_d<16>(p, mode, tmq, tmk, tmv, tmo, ctx);
+    case 32: return launch_d<32>(p, mode, tmq, tmk, tmv, tmo, ctx);
+    case 64: return launch_d<64>(p, mode, tmq, tmk, tmv, tmo, ctx);
+    case 128: return launch_d<128>(p, mode, tmq, tmk, tmv, tmo, ctx);
     default: return cudaErrorInvalidValue;
   }
 }

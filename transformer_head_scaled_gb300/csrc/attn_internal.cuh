@@ -11,7 +11,42 @@ namespace attn {
 enum MaskKind : int { kMaskNone = 0, kMaskCausal = 1, kMaskKeyPadding = 2, kMaskBand = 3 };
 
 // Written (first error wins) into the library's device status word.
-enum DeviceStatus : int { kDevOk = 0, kDevTimeout = 1 };
+enum DeviceStatus : int { kDevOk = 0, kDevTimeout = 1, kDevWrongPlan = 2 };
+
+// The plan of a mask under which every query sees one run of keys: device
+// arrays inside the caller's plan buffer (attn_mask_plan).  Intervals are
+// [x, y); per 128 queries (or keys): {x, y} = the union's bounds, {z, w} = the
+// intersection, z >= w when it is empty.
+constexpr int kMaskTile = 128;
+struct MaskPlan {
+  const int4* header;      // n_q, n_k, B, 1 when later queries see more keys
+  const int2* row_keys;    // [B][n_q] keys of a query
+  const int2* key_rows;    // [B][n_k] queries of a key
+  const int4* block_keys;  // [B][ceil(n_q / 128)]
+  const int4* tile_rows;   // [B][ceil(n_k / 128)]
+};
+struct MaskLayout {
+  size_t row_keys, key_rows, block_keys, tile_rows, runs, bytes;
+};
+MaskLayout mask_layout(int B, int n_q, int n_k);
+MaskPlan mask_plan_at(const void* plan, int B, int n_q, int n_k);
+
+struct MaskProblem {
+  int B, n_q, n_k;
+  int left, right;  // -1: no bound on that side
+  const int* key_lens;
+  const int* doc_ids;  // [B][n_q], n_q == n_k
+  const int* prefix_lens;
+};
+
+// Changed scores (attn_fwd_scored, attn_bwd_scored).
+struct ScoreMod {
+  float softcap;        // 0: none
+  const float* slopes;  // device [H] or null
+  int group;            // query heads per key head
+  MaskPlan plan;
+  bool masked;          // whether there is a plan
+};
 
 // One forward problem, device pointers, [B, H, n, d] contiguous.
 struct Problem {
@@ -26,6 +61,9 @@ struct Problem {
   const int* key_lens;
   int win_left, win_right;  // kMaskBand: query i sees keys i - win_left .. i + win_right
 };
+
+struct LaunchCtx;
+cudaError_t launch_mask_plan(const MaskProblem& pb, void* plan, const LaunchCtx& ctx);
 
 // Launch context shared by every launcher.
 struct LaunchCtx {
@@ -75,8 +113,11 @@ inline cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 bl
 // V and O as 3-D (d, n, B*H) bf16 tensors with a (min(d, 64), rows, 1) box
 // in the widest swizzle a box row fits (128, 64 or 32 bytes); rows = 128 for
 // Q and O, fwd_tc_kv_rows(d) for K and V.
+// With `mod`: changed scores, under its plan instead of pb's mask; K and V then
+// have H / mod->group heads.
 cudaError_t launch_fwd_tc(const Problem& pb, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                          const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx);
+                          const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx,
+                          const ScoreMod* mod = nullptr);
 int fwd_tc_kv_rows(int d);
 
 // fp32 SIMT path (d in {16, 32, 64, 128}).
@@ -144,6 +185,8 @@ struct BwdProblem {
 // accumulator [B, H, n_q, d].
 struct BwdLayout {
   size_t num_qt, cst_off, dq_acc_off, bytes;
+  // with changed scores: LSE * log2(e), padded to whole query tiles, behind them
+  size_t lse_off, scored_bytes;
 };
 BwdLayout bwd_layout(int B, int H, int n_q, int d);
 bool bwd_head_size_ok(int d);
@@ -151,8 +194,10 @@ bool bwd_head_size_ok(int d);
 // dV the same with a (d, 64, 1, 1) box (any strides); the dQ accumulator as 3-D (d, n_q, B*H)
 // fp32 with a (min(d, 32), 64, 1) box; each in the swizzle of its box's row
 // bytes.  Three launches (preprocess, main, dQ convert).
+// With `mod`: changed scores, under its plan instead of pb's mask; the K, V, dK
+// and dV maps then have H / mod->group heads.
 cudaError_t launch_bwd(const BwdProblem& pb, const CUtensorMap* maps, void* workspace,
-                       const LaunchCtx& ctx);
+                       const LaunchCtx& ctx, const ScoreMod* mod = nullptr);
 
 // New keys and values into an 8-bit cache with a scale per block of tokens.
 struct CacheAppendProblem {
