@@ -1030,8 +1030,8 @@ int check_scored(const void* q, const void* k, const void* v, const void* o, con
 }
 
 ScoreMod score_mod(float softcap, const float* slopes, int h, int h_kv, const void* plan, int B,
-                   int n_q, int n_k) {
-  ScoreMod mod{softcap, slopes, h / h_kv, {}, plan != nullptr};
+                   int n_q, int n_k, const Strides* st) {
+  ScoreMod mod{softcap, slopes, h / h_kv, {}, plan != nullptr, st[0], st[1], st[2]};
   if (plan != nullptr) mod.plan = mask_plan_at(plan, B, n_q, n_k);
   return mod;
 }
@@ -1095,7 +1095,7 @@ int attn_fwd_scored(const void* q, const void* k, const void* v, void* o, float*
   if ((rc = encode_4d(&tmv, v, d_k, n_k, h_kv, B, st[2], kv_rows)) != ATTN_OK) return rc;
   if ((rc = encode_4d(&tmo, o, d_k, n_q, h, B, st[3], 128)) != ATTN_OK) return rc;
   const Problem pb{q, k, v, o, lse, B, h, n_q, n_k, d_k, scale, kMaskNone, nullptr, 0, 0};
-  const ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k);
+  const ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k, st);
   const cudaError_t e = launch_fwd_tc(pb, tmq, tmk, tmv, tmo, make_ctx(*di, stream), &mod);
   if (e != cudaSuccess) return cuda_fail(e);
   g_launches.fetch_add(1);
@@ -1142,7 +1142,7 @@ int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, 
     return rc;
   const BwdProblem pb{q, k, v, o, dout, lse, dq, dk, dv, B, h, n_q, n_k, d_k, scale,
                       kMaskNone, nullptr, 0, 0, st[3], st[4], st[5]};
-  const ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k);
+  const ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k, st);
   const cudaError_t e = launch_bwd(pb, maps, workspace, make_ctx(*di, stream), &mod);
   if (e != cudaSuccess) return cuda_fail(e);
   g_launches.fetch_add(3);

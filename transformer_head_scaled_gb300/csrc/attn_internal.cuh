@@ -39,6 +39,12 @@ struct MaskProblem {
   const int* prefix_lens;
 };
 
+// Element strides of a [B, H, n, d] view across batch entries, heads and rows
+// (d contiguous).
+struct RowStrides {
+  long long b, h, n;
+};
+
 // Changed scores (attn_fwd_scored, attn_bwd_scored).
 struct ScoreMod {
   float softcap;        // 0: none
@@ -46,6 +52,7 @@ struct ScoreMod {
   int group;            // query heads per key head
   MaskPlan plan;
   bool masked;          // whether there is a plan
+  RowStrides sq, sk, sv;  // of q, k, v (the backward reads a few rows with plain loads)
 };
 
 // One forward problem, device pointers, [B, H, n, d] contiguous.
@@ -123,11 +130,6 @@ int fwd_tc_kv_rows(int d);
 // fp32 SIMT path (d in {16, 32, 64, 128}).
 cudaError_t launch_fwd_f32(const Problem& pb, const LaunchCtx& ctx);
 
-// Element strides of a [B, H, n, d] view across batch entries, heads and rows
-// (d contiguous).
-struct RowStrides {
-  long long b, h, n;
-};
 
 // Decode path (n_q <= kDecodeMaxQueries new queries against a cache).
 constexpr int kDecodeMaxQueries = 8;
