@@ -82,6 +82,71 @@ def test_decode_scored_arguments_rejected_on_host(lib):
     assert lib.attn_decode_scored_workspace_bytes(1, 3, 2, 1, 64, 64, 1, -1) == 0
 
 
+def test_mask_plan_arguments_rejected_on_host(lib):
+    def call(B=1, n_q=64, n_k=64, left=-1, right=0, lens=None, docs=None, prefix=None, plan=A,
+             size=1 << 20):
+        return binding.attn_mask_plan_raw(B, n_q, n_k, left, right, lens, docs, prefix, plan, size,
+                                          None)
+    for name in ("B", "n_q", "n_k"):
+        assert call(**{name: 0}) == INV and call(**{name: -1}) == INV, name
+    assert call(left=-2) == INV and call(right=-2) == INV
+    for name in ("lens", "docs", "prefix"):
+        assert call(**{name: A + 2}) == INV, name
+    assert call(plan=None) == INV and call(plan=A + 8) == INV
+    assert call(size=lib.attn_mask_plan_bytes(1, 64, 64) - 1) == INV
+    assert call(docs=A, n_k=65) == INV            # documents need n_q == n_k
+    assert call(prefix=A, left=3) == INV          # two runs of keys
+    assert call(n_q=(1 << 30) + 1) == UNS
+    assert call(B=1 << 20, n_q=1 << 20, n_k=1 << 20) == UNS
+    assert lib.attn_mask_plan_bytes(0, 1, 1) == 0
+    assert lib.attn_mask_plan_bytes(1, (1 << 30) + 1, 1) == 0
+
+
+def _scored_refusals(call, tensors, strides):
+    for name in tensors:
+        assert call(**{name: None}) == INV, name
+        assert call(**{name: A + 8}) == INV, name
+    for name in ("B", "h", "hk", "n_q", "n_k", "d"):
+        assert call(**{name: 0}) == INV and call(**{name: -1}) == INV, name
+    assert call(h=3, hk=2) == INV
+    assert call(slopes=A + 2) == INV and call(lse=A + 2) == INV
+    for bad in (0.0, -1.0, math.nan, math.inf):
+        assert call(scale=bad) == INV
+    for bad in (-1.0, math.nan, math.inf):
+        assert call(cap=bad) == INV
+    assert call(plan=A + 8) == INV
+    assert call(plan=A, plan_bytes=100) == INV    # too small for these sizes
+    for at in range(strides):
+        for bad in (0, -8, 4):
+            s = [64] * strides
+            s[at] = bad
+            assert call(strides=s) == INV, (at, bad)
+    assert call(d=48) == UNS and call(d=256) == UNS
+    assert call(n_q=(1 << 30) + 1, d=16) == UNS
+
+
+def test_fwd_scored_arguments_rejected_on_host(lib):
+    def call(q=A, k=A, v=A, o=A, lse=None, B=1, h=2, hk=1, n_q=8, n_k=8, d=64, strides=None,
+             scale=0.125, cap=0.0, slopes=None, plan=None, plan_bytes=0):
+        return binding.attn_fwd_scored_raw(q, k, v, o, lse, B, h, hk, n_q, n_k, d, strides, scale,
+                                           cap, slopes, plan, plan_bytes, None)
+    _scored_refusals(call, ("q", "k", "v", "o"), 12)
+
+
+def test_bwd_scored_arguments_rejected_on_host(lib):
+    def call(q=A, k=A, v=A, o=A, dout=A, lse=A, dq=A, dk=A, dv=A, B=1, h=2, hk=1, n_q=8, n_k=8,
+             d=64, strides=None, scale=0.125, cap=0.0, slopes=None, plan=None, plan_bytes=0, ws=A,
+             ws_bytes=1 << 40):
+        return binding.attn_bwd_scored_raw(q, k, v, o, dout, lse, dq, dk, dv, B, h, hk, n_q, n_k, d,
+                                           strides, scale, cap, slopes, plan, plan_bytes, ws,
+                                           ws_bytes, None)
+    _scored_refusals(call, ("q", "k", "v", "o", "dout", "dq", "dk", "dv", "ws"), 24)
+    assert call(lse=None) == INV
+    assert call(ws_bytes=lib.attn_bwd_scored_workspace_bytes(1, 2, 8, 64) - 1) == INV
+    assert call(d=128) == UNS
+    assert lib.attn_bwd_scored_workspace_bytes(1, 2, 8, 128) == 0
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_types():
     x = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16)
     c = torch.zeros(1, 1, 64, 64, dtype=torch.int8)
@@ -90,3 +155,9 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         binding.attn_cache_append(x, x, c, c, s, s, None)
     with pytest.raises(ValueError):
         binding.attn_decode_scored(x, c, c, k_scale=s, v_scale=s)
+    with pytest.raises(ValueError):
+        binding.attn_mask_plan(1, 4, 4, device="cpu")
+    with pytest.raises(ValueError):
+        binding.attn_fwd_scored(x, x, x)
+    with pytest.raises(ValueError):
+        binding.attn_bwd_scored(x, x, x, x, s, x)
