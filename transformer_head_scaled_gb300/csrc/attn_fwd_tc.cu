@@ -93,7 +93,12 @@ struct Cfg {
   static_assert(col_p(QT) <= 512, "tensor memory");
 };
 
-template <int D_>
+// Instantiations: the masks given by lengths (none, causal, key padding), the
+// restricted window, and changed scores under a mask plan; each keeps its code
+// out of the others'.
+enum Mode : int { kPlain = 0, kBand = 1, kScored = 2 };
+
+template <int D_, int MODE>
 struct __align__(1024) Smem {
   using C = Cfg<D_>;
   uint8_t q[C::QBUF][QT][C::Q_TILE];
@@ -108,12 +113,14 @@ struct __align__(1024) Smem {
   uint64_t turn[QT];  // softmax ping-pong: Q tile s may run its exp phase
   uint32_t tmem_base;
   int abort;
+  // Distance bias (kScored), as operands of one more K = 16 step of S: row j of
+  // idx holds j eight times, the rows of slope[s] are all (hi, mid, lo, 0, ...),
+  // half the slope over the scale in three bf16 parts.  8 x 16-byte core
+  // matrices; both K halves and all row groups of slope[s] are the same one, so
+  // that the step adds slope * j / scale to column j of S.
+  alignas(128) uint8_t idx[MODE == kScored ? C::BN * 16 : 16];
+  alignas(128) uint8_t slope[QT][MODE == kScored ? 128 : 16];
 };
-
-// Instantiations: the masks given by lengths (none, causal, key padding), the
-// restricted window, and changed scores under a mask plan; each keeps its code
-// out of the others'.
-enum Mode : int { kPlain = 0, kBand = 1, kScored = 2 };
 
 struct Params {
   __nv_bfloat16* o;
@@ -129,7 +136,10 @@ struct Params {
   int group;            // query heads per key head
   float cap_log2;       // softcap * log2(e); 0: no cap
   float cap_in;         // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
+  float cap_small;      // largest |q.k| of the polynomial (below)
+  float cap_poly[4];    // its coefficients, in powers of (q.k)^2, in log2 units
   const float* slopes;  // distance bias per head, or null
+  float inv_scale, inv_scale_log2;
   bool masked;
   MaskPlan plan;
   uint64_t limit_ns;
@@ -247,6 +257,15 @@ __device__ __forceinline__ void record_timeout(const Params& p, SmemT& sm) {
   *reinterpret_cast<volatile int*>(&sm.abort) = 1;
 }
 
+__device__ __forceinline__ float bf16_round(float x) {
+  return __bfloat162float(__float2bfloat16_rn(x));
+}
+
+// tanh(y) = y (T0 + T1 y^2 + T2 y^4 + T3 y^6) for |y| <= TANH_SMALL, within 1.3e-7
+// of it (a least-maximum fit made for this file over that interval).
+constexpr float TANH_SMALL = 0.5f;
+constexpr float T0 = 0.999997676f, T1 = -0.333206552f, T2 = 0.131451457f, T3 = -0.0433724845f;
+
 template <int MODE, int D_>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmq,
@@ -260,7 +279,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr bool BAND = MODE == kBand;
   constexpr bool OFFSET = MODE != kPlain;  // an item's stream may begin past key 0
   extern __shared__ uint8_t smem_raw[];
-  Smem<D_>& sm = *reinterpret_cast<Smem<D_>*>(
+  using S = Smem<D_, MODE>;
+  S& sm = *reinterpret_cast<S*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -299,6 +319,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == MMA_WARP) {
     tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
     tmem_relinquish();
+  }
+  if constexpr (SCORED) {
+    // column index j (exact in bf16 up to 256) as bf16 pairs
+    for (int w = threadIdx.x; w < BN * 4; w += NUM_THREADS) {
+      const float j = static_cast<float>(w >> 2);
+      reinterpret_cast<uint32_t*>(sm.idx)[w] = pack_bf16x2(j, j);
+    }
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -426,6 +454,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t t_s = tmem + C::col_s(s), t_o = tmem + C::col_o(s),
                      t_p = tmem + C::col_p(s);
 
+      // the bias step: rows of 16 bytes in 8-row core matrices, the two K
+      // halves (LBO 0) and, for the slope, all row groups (SBO 0) the same
+      const bool bias_mma = SCORED && p.slopes != nullptr && !(p.cap_log2 > 0.f);
+      const uint64_t d_idx = sdesc(smem_u32(sm.idx), 0, 128, 0);
+      const uint64_t d_slope = sdesc(smem_u32(sm.slope[s]), 0, 0, 0);
+
       const bool leader = elect_one();
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -479,11 +513,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!k_wait(g)) break;
           if (u > 0 && !wait(&sm.s_free[s], (u - 1) & 1)) break;
           tc_fence_after();
+          if constexpr (SCORED) {
+            if (bias_mma && j == 0) {
+              // this item's head; every earlier S product has completed
+              const float slope = 0.5f * p.inv_scale * __ldg(p.slopes + it.bh % p.H);
+              const float hi = bf16_round(slope), mid = bf16_round(slope - hi);
+              const uint32_t word = lane & 3;
+              reinterpret_cast<uint32_t*>(sm.slope[s])[lane] =
+                  word == 0 ? pack_bf16x2(hi, mid)
+                            : (word == 1 ? pack_bf16x2(slope - hi - mid, 0.f) : 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
           const uint64_t b = dk + (g % KSTAGES) * KV16;
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ss(t_s, dq + qstep(kk), b + kstep(kk), IDESC_S, kk > 0 ? 1u : 0u);
+            if (SCORED && bias_mma) mma_ss(t_s, d_slope, d_idx, IDESC_S, 1u);
             tc_commit(smem_u32(&sm.s_full[s]));
             tc_commit(smem_u32(&sm.k_empty[g % KSTAGES]));
             if (j == n - 1) tc_commit(smem_u32(&sm.q_empty[qb][s]));  // Q tile s no longer read
@@ -532,8 +580,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr bool band = BAND;
     const bool capped = SCORED && p.cap_log2 > 0.f;
     const bool biased = SCORED && p.slopes != nullptr;
-    // what is left to multiply a score by (the cap and the bias leave log2 units)
-    const float c = capped || biased ? 1.f : p.scale_log2;
+    // what is left to multiply a score by (the cap leaves log2 units)
+    const float c = capped ? 1.f : p.scale_log2;
     uint32_t u = 0;  // tiles this stage has processed (all items)
     // Ping-pong: on the tiles both Q tiles visit, the two softmax warpgroups
     // take turns for the exp phase (the MUFU-bound part), so that one
@@ -550,7 +598,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float l = 0.f;        // running sum of 2^(x - m)
       // this row's keys, and those that every row of the Q tile sees
       int row_lo = 0, row_hi = p.n_k, all_lo = 0, all_hi = p.n_k;
-      float nslope = 0.f;  // -slope in log2 units
+      float slope2 = 0.f;  // slope in log2 units
       if constexpr (SCORED) {
         if (p.masked && it.n[s] > 0) {
           const size_t b = it.bh / p.H;
@@ -561,7 +609,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           row_lo = v.x;
           row_hi = v.y;
         }
-        if (biased) nslope = -1.4426950408889634f * __ldg(p.slopes + it.bh % p.H);
+        if (biased) slope2 = 1.4426950408889634f * __ldg(p.slopes + it.bh % p.H);
       }
       for (int j = 0; j < it.n[s]; ++j, ++u) {
         ok = mbar_wait(smem_u32(&sm.s_full[s]), u & 1, p.limit_ns, abort);
@@ -579,52 +627,91 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_arrive(smem_u32(&sm.s_free[s]));
 
         const int kbase = ((OFFSET ? it.j0 : 0) + j) * BN;
+        float offset = 0.f;  // what every score of the row still gets (log2 units)
+        float top_raw = 0.f;  // largest raw score, where the cap's own maximum follows from it
+        const bool edge = SCORED && (kbase < all_lo || kbase + BN > all_hi);
         if constexpr (SCORED) {
           if (capped) {
-            // cap * tanh(y) = cap - 2 cap / (1 + 2^(2 y log2(e))), in log2 units
+            float hi4[4], lo4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hi4[i] = -INFINITY, lo4[i] = INFINITY;
 #pragma unroll
             for (int q4 = 0; q4 < SC; ++q4)
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float x0, x1;
-                fma2(x0, x1, __uint_as_float(r[q4][i]), __uint_as_float(r[q4][i + 1]), p.cap_in,
-                     p.cap_in, 0.f, 0.f);
-                add2(x0, x1, ex2(x0), ex2(x1), 1.f, 1.f);
-                fma2(x0, x1, rcp(x0), rcp(x1), -2.f * p.cap_log2, -2.f * p.cap_log2, p.cap_log2,
-                     p.cap_log2);
-                r[q4][i] = __float_as_uint(x0);
-                r[q4][i + 1] = __float_as_uint(x1);
-              }
-          }
-          if (biased) {
-            const float f = capped ? 1.f : p.scale_log2;
-            const float far = static_cast<float>(row - kbase);  // distance to the first column
-            if (kbase + BN - 1 <= row0) {
-              // every key lies before every query: the bias is linear in the column
-              const float b0 = nslope * far;
+              for (int i = 0; i < 32; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float x = __uint_as_float(r[q4][i + 2 * e]),
+                              y = __uint_as_float(r[q4][i + 2 * e + 1]);
+                  hi4[e] = max3(hi4[e], x, y);
+                  lo4[e] = min3(lo4[e], x, y);
+                }
+            top_raw = fmaxf(max3(hi4[0], hi4[1], hi4[2]), hi4[3]);
+            const float low = fminf(min3(lo4[0], lo4[1], lo4[2]), lo4[3]);
+            if (__all_sync(0xffffffffu, fmaxf(top_raw, -low) <= p.cap_small)) {
+              // small arguments: a polynomial in the raw score on the FMA pipe
 #pragma unroll
               for (int q4 = 0; q4 < SC; ++q4)
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                  float b1, b2, x0, x1;
-                  const float col = static_cast<float>(q4 * 32 + i);
-                  fma2(b1, b2, col, col + 1.f, -nslope, -nslope, b0, b0);
-                  fma2(x0, x1, __uint_as_float(r[q4][i]), __uint_as_float(r[q4][i + 1]), f, f, b1,
-                       b2);
+                  const float x0 = __uint_as_float(r[q4][i]), x1 = __uint_as_float(r[q4][i + 1]);
+                  float z0, z1, y0, y1;
+                  fma2(z0, z1, x0, x1, x0, x1, 0.f, 0.f);
+                  fma2(y0, y1, z0, z1, p.cap_poly[3], p.cap_poly[3], p.cap_poly[2], p.cap_poly[2]);
+                  fma2(y0, y1, z0, z1, y0, y1, p.cap_poly[1], p.cap_poly[1]);
+                  fma2(y0, y1, z0, z1, y0, y1, p.cap_poly[0], p.cap_poly[0]);
+                  fma2(y0, y1, x0, x1, y0, y1, 0.f, 0.f);
+                  r[q4][i] = __float_as_uint(y0);
+                  r[q4][i + 1] = __float_as_uint(y1);
+                }
+            } else {
+              // cap * tanh(y) = cap - 2 cap / (1 + 2^(2 y log2(e))), in log2 units
+#pragma unroll
+              for (int q4 = 0; q4 < SC; ++q4)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float x0, x1;
+                  fma2(x0, x1, __uint_as_float(r[q4][i]), __uint_as_float(r[q4][i + 1]), p.cap_in,
+                       p.cap_in, 0.f, 0.f);
+                  add2(x0, x1, ex2(x0), ex2(x1), 1.f, 1.f);
+                  fma2(x0, x1, rcp(x0), rcp(x1), -2.f * p.cap_log2, -2.f * p.cap_log2, p.cap_log2,
+                       p.cap_log2);
                   r[q4][i] = __float_as_uint(x0);
                   r[q4][i + 1] = __float_as_uint(x1);
                 }
-            } else {
+            }
+          }
+          if (biased) {
+            // -slope |i - j| = slope (kbase - i) + slope (j - kbase), less 2 slope
+            // (j - i) for the keys after the query; without a cap the second
+            // term is in S already
+            const float to_row = static_cast<float>(row - kbase);  // column of the query itself
+            offset = -slope2 * to_row;
+            if (capped) {
+#pragma unroll
+              for (int q4 = 0; q4 < SC; ++q4)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const float col = static_cast<float>(q4 * 32 + i);
+                  float x0, x1;
+                  fma2(x0, x1, col, col + 1.f, slope2, slope2, __uint_as_float(r[q4][i]),
+                       __uint_as_float(r[q4][i + 1]));
+                  r[q4][i] = __float_as_uint(x0);
+                  r[q4][i + 1] = __float_as_uint(x1);
+                }
+            }
+            if (__any_sync(0xffffffffu, row_hi > row + 1 && kbase + BN > row + 1)) {
+              const float f = capped ? -2.f * slope2 : -2.f * slope2 * p.inv_scale_log2;
 #pragma unroll
               for (int q4 = 0; q4 < SC; ++q4)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   r[q4][i] = __float_as_uint(
-                      fmaf(__uint_as_float(r[q4][i]), f,
-                           nslope * fabsf(far - static_cast<float>(q4 * 32 + i))));
+                      fmaf(f, fmaxf(static_cast<float>(q4 * 32 + i) - to_row, 0.f),
+                           __uint_as_float(r[q4][i])));
             }
           }
-          if (kbase < all_lo || kbase + BN > all_hi) {
+          if (edge) {
             const int lim = row_hi - kbase, lo = row_lo - kbase;  // columns [lo, lim) are visible
 #pragma unroll
             for (int q4 = 0; q4 < SC; ++q4)
@@ -648,6 +735,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (q4 * 32 + i >= lim || q4 * 32 + i < lo) r[q4][i] = __float_as_uint(-INFINITY);
         }
 
+        float mt;  // the row's largest score of this tile, in log2 units
+        if (SCORED && capped && !biased && !edge) {
+          // the cap is monotone: its maximum is that of the largest raw score
+          mt = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(top_raw * p.cap_in)), p.cap_log2);
+        } else {
         float mx[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) mx[i] = -INFINITY;
@@ -660,7 +752,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mx[2] = max3(mx[2], __uint_as_float(r[q4][i + 4]), __uint_as_float(r[q4][i + 5]));
             mx[3] = max3(mx[3], __uint_as_float(r[q4][i + 6]), __uint_as_float(r[q4][i + 7]));
           }
-        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+        mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+        if (SCORED) mt += offset;
+        }
 
         bool rescale_o = false;
         float alpha = 1.f;
@@ -677,7 +771,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                           mbar_wait(smem_u32(&sm.turn[s]), turns & 1, p.limit_ns, abort));
           if (!ok) break;
         }
-        const float neg_m = (m == -INFINITY) ? 0.f : -m;
+        const float neg_m = ((m == -INFINITY) ? 0.f : -m) + (SCORED ? offset : 0.f);
         float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
         uint32_t pk[SC / 2][32];
 #pragma unroll
@@ -796,8 +890,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int MODE, int D_>
 cudaError_t launch_instance(const Params& p, const CUtensorMap& tmq, const CUtensorMap& tmk,
                             const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx) {
-  static_assert(sizeof(Smem<D_>) + 1024 <= 232448, "dynamic shared memory per CTA");
-  const size_t smem = sizeof(Smem<D_>) + 1024;
+  static_assert(sizeof(Smem<D_, MODE>) + 1024 <= 232448, "dynamic shared memory per CTA");
+  const size_t smem = sizeof(Smem<D_, MODE>) + 1024;
   // The register hand-over inside the kernel assumes the launch holds
   // LAUNCH_REGS per thread; refuse to launch a build that does not.
   cudaFuncAttributes attr;
@@ -848,7 +942,16 @@ cudaError_t launch_fwd_tc(const Problem& pb, const CUtensorMap& tmq, const CUten
     p.group = mod->group;
     p.cap_log2 = mod->softcap * 1.4426950408889634f;
     p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
+    if (mod->softcap > 0.f) {
+      const double k = static_cast<double>(pb.scale) / mod->softcap;  // tanh's argument per q.k
+      const double t[4] = {T0, T1, T2, T3};
+      p.cap_small = static_cast<float>(TANH_SMALL / k);
+      double f = p.cap_log2 * k;
+      for (int i = 0; i < 4; ++i, f *= k * k) p.cap_poly[i] = static_cast<float>(t[i] * f);
+    }
     p.slopes = mod->slopes;
+    p.inv_scale = 1.f / pb.scale;
+    p.inv_scale_log2 = 1.f / p.scale_log2;
     p.masked = mod->masked;
     p.plan = mod->plan;
   }

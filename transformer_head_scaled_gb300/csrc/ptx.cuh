@@ -385,6 +385,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// min(a, b, c) in one instruction.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // (a0, a1) * (b0, b1) + (c0, c1) as one packed fma.rn.f32x2.
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
                                      float c0, float c1) {
