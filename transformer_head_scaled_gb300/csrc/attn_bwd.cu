@@ -112,11 +112,6 @@ struct BCfg {
   static_assert(COL_PT + 64 <= 512, "tensor memory");
 };
 
-// Instantiations: the masks given by lengths (none, causal, key padding), the
-// restricted window, and changed scores under a mask plan; each keeps its code
-// out of the others'.
-enum Mode : int { kPlain = 0, kBand = 1, kScored = 2 };
-
 template <int D_, int MODE>
 struct __align__(1024) Smem {
   using C = BCfg<D_>;
@@ -132,8 +127,9 @@ struct __align__(1024) Smem {
   // dQ, or dV / dK in bf16, swizzled as the tensor map it is copied with
   uint8_t stage[2][STAGE_BYTES];
   uint8_t cst[QSTAGES][CONST_TILE_BYTES];  // the constant tile of each Q stage
-  // with a cap: LSE * log2(e) of each Q stage's queries (see pre_kernel)
-  float lse[MODE == kScored ? QSTAGES : 1][MODE == kScored ? BM : 4];
+  // with a cap: the constants of each Q stage's queries in log2 units (LSE and,
+  // with a distance bias, the query's share of it)
+  float lse[MODE & kCap ? QSTAGES : 1][MODE & kCap ? BM : 4];
   // Two 8 x 8 bf16 core matrices that select columns of the constant tile:
   // [0] rows (1,1,1,0,0,0,0,0) picks b, [1] rows (0,0,0,1,1,1,0,0) picks -D.
   uint8_t sel[2][512];
@@ -162,6 +158,7 @@ struct Params {
   float cap_log2;         // softcap * log2(e); 0: no cap
   float cap_in;           // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
   const float* slopes;    // distance bias per query head, or null
+  float inv_scale_log2;
   const float* lse_log2;  // with a cap: [B * H][num_qt * 128]
   bool masked;
   MaskPlan plan;
@@ -204,7 +201,7 @@ __device__ __forceinline__ Item bwd_item_planned(const Params& p, int t, bool de
 
 template <int MODE>
 __device__ __forceinline__ Item bwd_item(const Params& p, int t, bool desc) {
-  if constexpr (MODE == kScored) return bwd_item_planned(p, t, desc);
+  if constexpr ((MODE & kScored) != 0) return bwd_item_planned(p, t, desc);
   Item it;
   if (p.mask == kMaskCausal) {
     // key tiles with the most query tiles first (longest-processing-time order)
@@ -325,51 +322,100 @@ __device__ __forceinline__ uint64_t sdesc_swz(uint32_t smem_addr, uint32_t lbo_b
 
 // P of one thread's key and 64 queries with changed scores: w gets it in bf16
 // pairs for dV, pf what multiplies dP - D: P times the cap's derivative.
-// Columns outside [lim, hi) are forbidden.  dist: the key's index less the
-// first query's.  Without a cap the scores hold -LSE/scale already; with one
-// the constant is taken off here, because it must not pass through the tanh.
-__device__ __forceinline__ void scored_probabilities(const Params& p, const uint32_t (&s0)[32],
-                                                     const uint32_t (&s1)[32], float (&pf)[64],
-                                                     uint32_t (&w)[32], int lim, int hi, int dist,
-                                                     int head, bool capped, const float* lse) {
-  const float nslope = p.slopes != nullptr ? -LOG2E * __ldg(p.slopes + head) : 0.f;
-  const float far = static_cast<float>(dist);
+//
+// The distance bias -slope |i - j| is slope (j - i0) - slope (i - i0), i0 the
+// query tile's first query: the second term is in the per-query constants
+// already (attn_bwd_pre_kernel), the first, `bias` in log2 units, is this
+// thread's.  Keys after their query get 2 slope (j - i) less; `after`: some
+// visible key is, `ahead` = j - the first of the 64 queries, f = -2 slope in
+// log2 units.  `edge`: some query of the warp's tile does not see some key;
+// columns outside [lim, hi) are forbidden for this one.
+template <int MODE>
+__device__ __forceinline__ void scored_probabilities(const Params& p, uint32_t (&s0)[32],
+                                                     uint32_t (&s1)[32], float (&pf)[64],
+                                                     uint32_t (&w)[32], bool edge, int lim, int hi,
+                                                     float bias, bool after, float ahead, float f,
+                                                     const float* lse) {
+  constexpr bool CAP = (MODE & kCap) != 0, BIAS = (MODE & kBias) != 0;
+  const float c = p.scale_log2;
+  if constexpr (!CAP) {
+    // without a cap the bias after the query and the mask can go onto the raw
+    // scores; what is left is one fma and one exponential per score
+    if (BIAS && after) {
+      const float g = f * p.inv_scale_log2;
 #pragma unroll
-  for (int i2 = 0; i2 < 32; i2 += 2) {
-    const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
-    const int c0 = 2 * i2;
-    float x[4], d[4];
-    if (capped) {
-      // tanh(y) = 1 - 2 / (1 + 2^(2 y log2(e)))
-      float t[4];
+      for (int i = 0; i < 32; ++i) {
+        s0[i] = __float_as_uint(fmaf(g, fmaxf(ahead - static_cast<float>(i), 0.f),
+                                     __uint_as_float(s0[i])));
+        s1[i] = __float_as_uint(fmaf(g, fmaxf(ahead - static_cast<float>(32 + i), 0.f),
+                                     __uint_as_float(s1[i])));
+      }
+    }
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (i < lim || i >= hi) s0[i] = __float_as_uint(-INFINITY);
+        if (32 + i < lim || 32 + i >= hi) s1[i] = __float_as_uint(-INFINITY);
+      }
+    }
+#pragma unroll
+    for (int i2 = 0; i2 < 32; i2 += 2) {
+      const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
+      float x0, x1, x2, x3;
+      fma2(x0, x1, __uint_as_float(src[0]), __uint_as_float(src[1]), c, c, bias, bias);
+      fma2(x2, x3, __uint_as_float(src[2]), __uint_as_float(src[3]), c, c, bias, bias);
+      const int c0 = 2 * i2;
+      pf[c0 + 0] = ex2(x0);
+      pf[c0 + 1] = ex2(x1);
+      pf[c0 + 2] = ex2(x2);
+      pf[c0 + 3] = ex2(x3);
+    }
+#pragma unroll
+    for (int i2 = 0; i2 < 32; ++i2) w[i2] = pack_bf16x2(pf[2 * i2], pf[2 * i2 + 1]);
+  } else {
+    // the score times the cap's derivative, from r = 1 / (1 + 2^(2 y log2(e))):
+    // tanh(y) = 1 - 2 r, 1 - tanh^2(y) = 4 r (1 - r).  LSE comes off after the
+    // tanh, from shared memory (it is a constant of the column, not of the thread).
+    const float top = p.cap_log2 + bias, m2 = -2.f * p.cap_log2;
+#pragma unroll
+    for (int i2 = 0; i2 < 32; i2 += 2) {
+      const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
+      const int c0 = 2 * i2;
+      const float4 l = *reinterpret_cast<const float4*>(lse + c0);
+      float r[4], x[4], d[4];
       fma2(x[0], x[1], __uint_as_float(src[0]), __uint_as_float(src[1]), p.cap_in, p.cap_in, 0.f,
            0.f);
       fma2(x[2], x[3], __uint_as_float(src[2]), __uint_as_float(src[3]), p.cap_in, p.cap_in, 0.f,
            0.f);
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        add2(t[e], t[e + 1], ex2(x[e]), ex2(x[e + 1]), 1.f, 1.f);
-        fma2(t[e], t[e + 1], rcp(t[e]), rcp(t[e + 1]), -2.f, -2.f, 1.f, 1.f);
+        add2(r[e], r[e + 1], ex2(x[e]), ex2(x[e + 1]), 1.f, 1.f);
+        r[e] = rcp(r[e]);
+        r[e + 1] = rcp(r[e + 1]);
+        fma2(d[e], d[e + 1], r[e], r[e + 1], -r[e], -r[e + 1], r[e], r[e + 1]);  // r (1 - r)
       }
-      const float4 l = *reinterpret_cast<const float4*>(lse + c0);
-      fma2(x[0], x[1], t[0], t[1], p.cap_log2, p.cap_log2, -l.x, -l.y);
-      fma2(x[2], x[3], t[2], t[3], p.cap_log2, p.cap_log2, -l.z, -l.w);
+      add2(x[0], x[1], top, top, -l.x, -l.y);
+      add2(x[2], x[3], top, top, -l.z, -l.w);
+      fma2(x[0], x[1], r[0], r[1], m2, m2, x[0], x[1]);
+      fma2(x[2], x[3], r[2], r[3], m2, m2, x[2], x[3]);
+      if (BIAS && after) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = fmaf(-t[e], t[e], 1.f);
-    } else {
-      fma2(x[0], x[1], __uint_as_float(src[0]), __uint_as_float(src[1]), p.scale_log2,
-           p.scale_log2, 0.f, 0.f);
-      fma2(x[2], x[3], __uint_as_float(src[2]), __uint_as_float(src[3]), p.scale_log2,
-           p.scale_log2, 0.f, 0.f);
-    }
+        for (int e = 0; e < 4; ++e)
+          x[e] = fmaf(f, fmaxf(ahead - static_cast<float>(c0 + e), 0.f), x[e]);
+      }
+      if (edge) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (p.slopes != nullptr) x[e] = fmaf(nslope, fabsf(far - static_cast<float>(c0 + e)), x[e]);
-      x[e] = c0 + e < lim || c0 + e >= hi ? 0.f : ex2(x[e]);
-      pf[c0 + e] = capped ? x[e] * d[e] : x[e];
+        for (int e = 0; e < 4; ++e)
+          if (c0 + e < lim || c0 + e >= hi) x[e] = -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = ex2(x[e]);
+        pf[c0 + e] = x[e] * (4.f * d[e]);
+      }
+      w[i2] = pack_bf16x2(x[0], x[1]);
+      w[i2 + 1] = pack_bf16x2(x[2], x[3]);
     }
-    w[i2] = pack_bf16x2(x[0], x[1]);
-    w[i2 + 1] = pack_bf16x2(x[2], x[3]);
   }
 }
 
@@ -385,7 +431,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   using C = BCfg<D_>;
   using S = Smem<D_, MODE>;
   constexpr int D = D_;
-  constexpr bool BAND = MODE == kBand, SCORED = MODE == kScored;
+  constexpr bool BAND = MODE == kBand, SCORED = (MODE & kScored) != 0, CAP = (MODE & kCap) != 0;
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                 ~static_cast<uintptr_t>(1023));
@@ -470,7 +516,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   }
-  const bool capped = SCORED && p.cap_log2 > 0.f;
   // heads of K, V, dK and dV, and the query head of a key head's g-th group member
   const int kv_heads = SCORED ? p.H / p.group : p.H;
   auto q_head = [&](int bh, int g) { return SCORED ? bh % kv_heads * p.group + g : bh % p.H; };
@@ -504,13 +549,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           ok = mbar_wait(smem_u32(&sm.q_empty[st]), ((nq / QSTAGES) & 1) ^ 1, p.limit_ns, abort);
           if (!ok) break;
           const uint32_t qb = smem_u32(&sm.q_full[st]);
-          mbar_arrive_expect_tx(qb, C::TILE + CONST_TILE_BYTES + (capped ? BM * 4 : 0));
+          mbar_arrive_expect_tx(qb, C::TILE + CONST_TILE_BYTES + (CAP ? BM * 4 : 0));
           tma_load_4d(smem_u32(sm.q[st]), &tmq, qb, 0, qt * BM, hq, b);
           const size_t tile = (static_cast<size_t>(b) * p.H + hq) * p.num_qt + qt;
           bulk_load(smem_u32(sm.cst[st]), p.cst + tile * CONST_TILE_BYTES, CONST_TILE_BYTES, qb);
-          if constexpr (SCORED) {
-            if (capped) bulk_load(smem_u32(sm.lse[st]), p.lse_log2 + tile * BM, BM * 4, qb);
-          }
+          if constexpr (CAP)
+            bulk_load(smem_u32(sm.lse[st]), p.lse_log2 + tile * BM, BM * 4, qb);
           ++nq;
           if (i == 0) {
             // V of this item, once the previous item's last dP has read the slot
@@ -841,15 +885,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
          x = next_item<MODE>(p, num_items, desc, x + gridDim.x, item)) {
       const int j = item.kt * BN + r;  // this thread's key
       const bool row_valid = j < item.key_limit;
-      // the queries of this key, and those of every key of the tile
-      int2 rows = make_int2(0, p.n_q), all = make_int2(0, p.n_q);
+      int2 rows = make_int2(0, row_valid ? p.n_q : 0);  // kScored: this key's queries
       if constexpr (SCORED) {
-        if (p.masked) {
-          const size_t b = item.bh / kv_heads;
-          rows = row_valid ? __ldg(p.plan.key_rows + b * p.n_k + j) : make_int2(0, 0);
-          const int4 v = __ldg(p.plan.tile_rows + b * p.num_kt + item.kt);
-          all = make_int2(v.z, v.w);
-        }
+        if (p.masked && row_valid)
+          rows = __ldg(p.plan.key_rows + static_cast<size_t>(item.bh / kv_heads) * p.n_k + j);
       }
       int qt = item.qt0, member = 0;
       for (int i = 0; i < item.n; ++i, ++t, step(item, qt, member)) {
@@ -862,10 +901,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           lim = 64;
         } else if (SCORED) {
           const int qbase = qt * BM + 64 * half;
-          if (qt * BM < all.x || qt * BM + BM > all.y) {
-            lim = min(max(rows.x - qbase, 0), 64);
-            hi = min(max(rows.y - qbase, 0), 64);
-          }
+          lim = min(max(rows.x - qbase, 0), 64);
+          hi = min(max(rows.y - qbase, 0), 64);
         } else if (p.mask == kMaskCausal && qt == item.kt) {
           lim = min(max(r - 64 * half, 0), 64);
         } else if (BAND) {
@@ -876,7 +913,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!wait(&sm.s_full, t & 1)) break;
         // (the stage's lse was copied with its Q; the stage is held until dK of
         // this tile pair, which waits for dS)
-        if (SCORED && capped && !wait(&sm.q_full[t % QSTAGES], (t / QSTAGES) & 1)) break;
+        if (CAP && !wait(&sm.q_full[t % QSTAGES], (t / QSTAGES) & 1)) break;
         tc_fence_after();
         uint32_t s0[32], s1[32];
         tmem_ld32(tS, s0);
@@ -891,9 +928,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float pf[64];
         uint32_t w[32];
         if constexpr (SCORED) {
-          scored_probabilities(p, s0, s1, pf, w, lim, hi, j - qt * BM - 64 * half,
-                                   q_head(item.bh, member), capped,
-                                   capped ? sm.lse[t % QSTAGES] + 64 * half : nullptr);
+          float bias = 0.f, f = 0.f;
+          const int ahead = j - qt * BM - 64 * half;
+          bool after = false;
+          if constexpr ((MODE & kBias) != 0) {
+            const float slope2 = LOG2E * __ldg(p.slopes + q_head(item.bh, member));
+            bias = slope2 * static_cast<float>(j - qt * BM);
+            f = -2.f * slope2;
+            // a query of this half that sees this key and comes before it
+            after = __any_sync(0xffffffffu, lim < hi && lim < ahead);
+          }
+          const bool edge = __any_sync(0xffffffffu, lim > 0 || hi < 64);
+          scored_probabilities<MODE>(p, s0, s1, pf, w, edge, lim, hi, bias, after,
+                                     static_cast<float>(ahead), f,
+                                     sm.lse[CAP ? t % QSTAGES : 0] + (CAP ? 64 * half : 0));
         } else {
 #pragma unroll
         for (int i2 = 0; i2 < 32; i2 += 2) {
@@ -1102,7 +1150,10 @@ __global__ void __launch_bounds__(256)
     if (sub == 0 && valid) {
       const float l = lse[static_cast<size_t>(bh) * n_q + i];
       // -inf only for a row that sees no key; a cap takes LSE off after the tanh
-      const float b = isfinite(l) && !(SCORED && mod.lse_log2 != nullptr) ? -l * inv_scale : 0.f;
+      float b = isfinite(l) && !(SCORED && mod.lse_log2 != nullptr) ? -l * inv_scale : 0.f;
+      // the distance bias's share of the query, counted from its tile's first
+      if (SCORED && mod.slopes != nullptr && mod.lse_log2 == nullptr)
+        b = fmaf(-__ldg(mod.slopes + hh) * inv_scale, static_cast<float>(n), b);
       const uint2 pb = split3_bf16(b);
       const uint2 pd = split3_bf16(-acc);
       w.x = pb.x;                         // b_hi, b_mid
@@ -1112,7 +1163,9 @@ __global__ void __launch_bounds__(256)
     *reinterpret_cast<uint4*>(tile + (n & 7) * 16 + (n >> 3) * 256 + sub * 128) = w;
     if (SCORED && mod.lse_log2 != nullptr && sub == 0) {
       const float l = valid ? lse[static_cast<size_t>(bh) * n_q + i] : 0.f;
-      mod.lse_log2[(static_cast<size_t>(bh) * num_qt + qt) * BM + n] = isfinite(l) ? l * LOG2E : 0.f;
+      const float far = mod.slopes != nullptr ? __ldg(mod.slopes + hh) * static_cast<float>(n) : 0.f;
+      mod.lse_log2[(static_cast<size_t>(bh) * num_qt + qt) * BM + n] =
+          ((isfinite(l) ? l : 0.f) + far) * LOG2E;
     }
   }
 }
@@ -1237,10 +1290,15 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
     p.cap_log2 = mod->softcap * LOG2E;
     p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
     p.slopes = mod->slopes;
+    p.inv_scale_log2 = 1.f / p.scale_log2;
     p.lse_log2 = lse_log2;
     p.masked = mod->masked;
     p.plan = mod->plan;
-    err = launch_bwd_main<kScored, D>(p, maps, ctx);
+    const bool cap = mod->softcap > 0.f, bias = mod->slopes != nullptr;
+    err = cap && bias ? launch_bwd_main<kScored | kCap | kBias, D>(p, maps, ctx)
+          : cap       ? launch_bwd_main<kScored | kCap, D>(p, maps, ctx)
+          : bias      ? launch_bwd_main<kScored | kBias, D>(p, maps, ctx)
+                      : launch_bwd_main<kScored, D>(p, maps, ctx);
   } else if (pb.mask == kMaskBand) {
     err = launch_bwd_main<kBand, D>(p, maps, ctx);
   } else {

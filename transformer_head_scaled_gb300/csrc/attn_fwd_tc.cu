@@ -93,11 +93,6 @@ struct Cfg {
   static_assert(col_p(QT) <= 512, "tensor memory");
 };
 
-// Instantiations: the masks given by lengths (none, causal, key padding), the
-// restricted window, and changed scores under a mask plan; each keeps its code
-// out of the others'.
-enum Mode : int { kPlain = 0, kBand = 1, kScored = 2 };
-
 template <int D_, int MODE>
 struct __align__(1024) Smem {
   using C = Cfg<D_>;
@@ -113,13 +108,13 @@ struct __align__(1024) Smem {
   uint64_t turn[QT];  // softmax ping-pong: Q tile s may run its exp phase
   uint32_t tmem_base;
   int abort;
-  // Distance bias (kScored), as operands of one more K = 16 step of S: row j of
+  // Distance bias (kBias without kCap), as operands of one more K = 16 step of S: row j of
   // idx holds j eight times, the rows of slope[s] are all (hi, mid, lo, 0, ...),
   // half the slope over the scale in three bf16 parts.  8 x 16-byte core
   // matrices; both K halves and all row groups of slope[s] are the same one, so
   // that the step adds slope * j / scale to column j of S.
-  alignas(128) uint8_t idx[MODE == kScored ? C::BN * 16 : 16];
-  alignas(128) uint8_t slope[QT][MODE == kScored ? 128 : 16];
+  alignas(128) uint8_t idx[MODE & kBias ? C::BN * 16 : 16];
+  alignas(128) uint8_t slope[QT][MODE & kBias ? 128 : 16];
 };
 
 struct Params {
@@ -193,7 +188,7 @@ __device__ __forceinline__ Item decode_item_planned(const Params& p, int t, bool
 
 template <int MODE, int BN>
 __device__ __forceinline__ Item decode_item(const Params& p, int t, bool desc) {
-  if constexpr (MODE == kScored) return decode_item_planned<BN>(p, t, desc);
+  if constexpr ((MODE & kScored) != 0) return decode_item_planned<BN>(p, t, desc);
   constexpr bool BAND = MODE == kBand;
   Item it;
   if (p.mask == kMaskCausal) {
@@ -275,7 +270,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   using C = Cfg<D_>;
   constexpr int D = C::D, BN = C::BN, QBUF = C::QBUF, KSTAGES = C::KSTAGES,
                 VSTAGES = C::VSTAGES;
-  constexpr bool SCORED = MODE == kScored;
+  constexpr bool SCORED = (MODE & kScored) != 0, CAP = (MODE & kCap) != 0,
+                 BIAS = (MODE & kBias) != 0;
+  constexpr bool BIAS_MMA = BIAS && !CAP;  // the bias rides on the score product
   constexpr bool BAND = MODE == kBand;
   constexpr bool OFFSET = MODE != kPlain;  // an item's stream may begin past key 0
   extern __shared__ uint8_t smem_raw[];
@@ -320,7 +317,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
     tmem_relinquish();
   }
-  if constexpr (SCORED) {
+  if constexpr (BIAS_MMA) {
     // column index j (exact in bf16 up to 256) as bf16 pairs
     for (int w = threadIdx.x; w < BN * 4; w += NUM_THREADS) {
       const float j = static_cast<float>(w >> 2);
@@ -456,7 +453,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
       // the bias step: rows of 16 bytes in 8-row core matrices, the two K
       // halves (LBO 0) and, for the slope, all row groups (SBO 0) the same
-      const bool bias_mma = SCORED && p.slopes != nullptr && !(p.cap_log2 > 0.f);
       const uint64_t d_idx = sdesc(smem_u32(sm.idx), 0, 128, 0);
       const uint64_t d_slope = sdesc(smem_u32(sm.slope[s]), 0, 0, 0);
 
@@ -513,8 +509,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!k_wait(g)) break;
           if (u > 0 && !wait(&sm.s_free[s], (u - 1) & 1)) break;
           tc_fence_after();
-          if constexpr (SCORED) {
-            if (bias_mma && j == 0) {
+          if constexpr (BIAS_MMA) {
+            if (j == 0) {
               // this item's head; every earlier S product has completed
               const float slope = 0.5f * p.inv_scale * __ldg(p.slopes + it.bh % p.H);
               const float hi = bf16_round(slope), mid = bf16_round(slope - hi);
@@ -531,7 +527,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ss(t_s, dq + qstep(kk), b + kstep(kk), IDESC_S, kk > 0 ? 1u : 0u);
-            if (SCORED && bias_mma) mma_ss(t_s, d_slope, d_idx, IDESC_S, 1u);
+            if constexpr (BIAS_MMA) mma_ss(t_s, d_slope, d_idx, IDESC_S, 1u);
             tc_commit(smem_u32(&sm.s_full[s]));
             tc_commit(smem_u32(&sm.k_empty[g % KSTAGES]));
             if (j == n - 1) tc_commit(smem_u32(&sm.q_empty[qb][s]));  // Q tile s no longer read
@@ -578,10 +574,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     constexpr int OC = C::OW / 32;     // 32-column chunks of O
     const bool causal = p.mask == kMaskCausal;
     constexpr bool band = BAND;
-    const bool capped = SCORED && p.cap_log2 > 0.f;
-    const bool biased = SCORED && p.slopes != nullptr;
     // what is left to multiply a score by (the cap leaves log2 units)
-    const float c = capped ? 1.f : p.scale_log2;
+    const float c = CAP ? 1.f : p.scale_log2;
     uint32_t u = 0;  // tiles this stage has processed (all items)
     // Ping-pong: on the tiles both Q tiles visit, the two softmax warpgroups
     // take turns for the exp phase (the MUFU-bound part), so that one
@@ -596,20 +590,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int row = row0 + quarter * 32 + lane;
       float m = -INFINITY;  // running max of scale*log2(e)*score (possibly stale)
       float l = 0.f;        // running sum of 2^(x - m)
-      // this row's keys, and those that every row of the Q tile sees
-      int row_lo = 0, row_hi = p.n_k, all_lo = 0, all_hi = p.n_k;
-      float slope2 = 0.f;  // slope in log2 units
+      int row_lo = 0, row_hi = p.n_k;  // kScored: this row's keys
+      float slope2 = 0.f;              // kBias: slope in log2 units
       if constexpr (SCORED) {
-        if (p.masked && it.n[s] > 0) {
-          const size_t b = it.bh / p.H;
-          const int4 r = __ldg(p.plan.block_keys + b * ((p.n_q + BM - 1) / BM) + row0 / BM);
-          all_lo = r.z;
-          all_hi = r.w;
-          const int2 v = row < p.n_q ? __ldg(p.plan.row_keys + b * p.n_q + row) : make_int2(0, 0);
+        // (rows past n_q are computed with every key, and not stored)
+        if (p.masked && it.n[s] > 0 && row < p.n_q) {
+          const int2 v = __ldg(p.plan.row_keys + static_cast<size_t>(it.bh / p.H) * p.n_q + row);
           row_lo = v.x;
           row_hi = v.y;
         }
-        if (biased) slope2 = 1.4426950408889634f * __ldg(p.slopes + it.bh % p.H);
+        if constexpr (BIAS) slope2 = 1.4426950408889634f * __ldg(p.slopes + it.bh % p.H);
       }
       for (int j = 0; j < it.n[s]; ++j, ++u) {
         ok = mbar_wait(smem_u32(&sm.s_full[s]), u & 1, p.limit_ns, abort);
@@ -629,9 +619,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int kbase = ((OFFSET ? it.j0 : 0) + j) * BN;
         float offset = 0.f;  // what every score of the row still gets (log2 units)
         float top_raw = 0.f;  // largest raw score, where the cap's own maximum follows from it
-        const bool edge = SCORED && (kbase < all_lo || kbase + BN > all_hi);
+        // whether a row of this warp does not see the whole tile
+        const bool edge =
+            SCORED && __any_sync(0xffffffffu, kbase < row_lo || kbase + BN > row_hi);
         if constexpr (SCORED) {
-          if (capped) {
+          if constexpr (CAP) {
             float hi4[4], lo4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) hi4[i] = -INFINITY, lo4[i] = INFINITY;
@@ -681,13 +673,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
           }
-          if (biased) {
+          if constexpr (BIAS) {
             // -slope |i - j| = slope (kbase - i) + slope (j - kbase), less 2 slope
             // (j - i) for the keys after the query; without a cap the second
             // term is in S already
             const float to_row = static_cast<float>(row - kbase);  // column of the query itself
             offset = -slope2 * to_row;
-            if (capped) {
+            if constexpr (CAP) {
 #pragma unroll
               for (int q4 = 0; q4 < SC; ++q4)
 #pragma unroll
@@ -701,7 +693,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (__any_sync(0xffffffffu, row_hi > row + 1 && kbase + BN > row + 1)) {
-              const float f = capped ? -2.f * slope2 : -2.f * slope2 * p.inv_scale_log2;
+              const float f = CAP ? -2.f * slope2 : -2.f * slope2 * p.inv_scale_log2;
 #pragma unroll
               for (int q4 = 0; q4 < SC; ++q4)
 #pragma unroll
@@ -736,7 +728,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
 
         float mt;  // the row's largest score of this tile, in log2 units
-        if (SCORED && capped && !biased && !edge) {
+        if (CAP && !BIAS && !edge) {
           // the cap is monotone: its maximum is that of the largest raw score
           mt = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(top_raw * p.cap_in)), p.cap_log2);
         } else {
@@ -753,7 +745,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mx[3] = max3(mx[3], __uint_as_float(r[q4][i + 6]), __uint_as_float(r[q4][i + 7]));
           }
         mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-        if (SCORED) mt += offset;
+        if (BIAS) mt += offset;
         }
 
         bool rescale_o = false;
@@ -771,7 +763,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                           mbar_wait(smem_u32(&sm.turn[s]), turns & 1, p.limit_ns, abort));
           if (!ok) break;
         }
-        const float neg_m = ((m == -INFINITY) ? 0.f : -m) + (SCORED ? offset : 0.f);
+        const float neg_m = ((m == -INFINITY) ? 0.f : -m) + (BIAS ? offset : 0.f);
         float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
         uint32_t pk[SC / 2][32];
 #pragma unroll
@@ -909,9 +901,15 @@ cudaError_t launch_instance(const Params& p, const CUtensorMap& tmq, const CUten
 template <int D_>
 cudaError_t launch_d(const Params& p, int mode, const CUtensorMap& tmq, const CUtensorMap& tmk,
                      const CUtensorMap& tmv, const CUtensorMap& tmo, const LaunchCtx& ctx) {
-  return mode == kScored ? launch_instance<kScored, D_>(p, tmq, tmk, tmv, tmo, ctx)
-         : mode == kBand ? launch_instance<kBand, D_>(p, tmq, tmk, tmv, tmo, ctx)
-                         : launch_instance<kPlain, D_>(p, tmq, tmk, tmv, tmo, ctx);
+  switch (mode) {
+    case kPlain: return launch_instance<kPlain, D_>(p, tmq, tmk, tmv, tmo, ctx);
+    case kBand: return launch_instance<kBand, D_>(p, tmq, tmk, tmv, tmo, ctx);
+    case kScored: return launch_instance<kScored, D_>(p, tmq, tmk, tmv, tmo, ctx);
+    case kScored | kCap: return launch_instance<kScored | kCap, D_>(p, tmq, tmk, tmv, tmo, ctx);
+    case kScored | kBias: return launch_instance<kScored | kBias, D_>(p, tmq, tmk, tmv, tmo, ctx);
+    default:
+      return launch_instance<kScored | kCap | kBias, D_>(p, tmq, tmk, tmv, tmo, ctx);
+  }
 }
 
 }  // namespace
@@ -955,7 +953,9 @@ cudaError_t launch_fwd_tc(const Problem& pb, const CUtensorMap& tmq, const CUten
     p.masked = mod->masked;
     p.plan = mod->plan;
   }
-  const int mode = mod != nullptr ? kScored : (pb.mask == kMaskBand ? kBand : kPlain);
+  const int mode = mod == nullptr
+                       ? (pb.mask == kMaskBand ? kBand : kPlain)
+                       : kScored | (mod->softcap > 0.f ? kCap : 0) | (mod->slopes ? kBias : 0);
   switch (pb.d) {
     case 16: return launch_d<16>(p, mode, tmq, tmk, tmv, tmo, ctx);
     case 32: return launch_d<32>(p, mode, tmq, tmk, tmv, tmo, ctx);

@@ -55,6 +55,12 @@ struct ScoreMod {
   RowStrides sq, sk, sv;  // of q, k, v (the backward reads a few rows with plain loads)
 };
 
+// Instantiations of the tensor-core kernels: the masks given by lengths (none,
+// causal, key padding), the restricted window, and changed scores under a mask
+// plan, with a cap and a distance bias or without; each keeps its code out of
+// the others'.
+enum Mode : int { kPlain = 0, kBand = 1, kScored = 2, kCap = 4, kBias = 8 };
+
 // One forward problem, device pointers, [B, H, n, d] contiguous.
 struct Problem {
   const void* q;
