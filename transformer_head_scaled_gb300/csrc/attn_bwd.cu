@@ -158,7 +158,6 @@ struct Params {
   float cap_log2;         // softcap * log2(e); 0: no cap
   float cap_in;           // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
   const float* slopes;    // distance bias per query head, or null
-  float inv_scale_log2;
   const float* lse_log2;  // with a cap: [B * H][num_qt * 128]
   bool masked;
   MaskPlan plan;
@@ -320,101 +319,81 @@ __device__ __forceinline__ uint64_t sdesc_swz(uint32_t smem_addr, uint32_t lbo_b
   return d;
 }
 
-// P of one thread's key and 64 queries with changed scores: w gets it in bf16
-// pairs for dV, pf what multiplies dP - D: P times the cap's derivative.
+// P of one thread's key and 64 queries with changed scores: emit(i, a, b, c, d)
+// gets it in bf16 pairs of columns 2i .. 2i + 7 for dV, pf what multiplies dP -
+// D: P times the cap's derivative.
 //
 // The distance bias -slope |i - j| is slope (j - i0) - slope (i - i0), i0 the
 // query tile's first query: the second term is in the per-query constants
 // already (attn_bwd_pre_kernel), the first, `bias` in log2 units, is this
-// thread's.  Keys after their query get 2 slope (j - i) less; `after`: some
-// visible key is, `ahead` = j - the first of the 64 queries, f = -2 slope in
-// log2 units.  `edge`: some query of the warp's tile does not see some key;
-// columns outside [lim, hi) are forbidden for this one.
-template <int MODE>
-__device__ __forceinline__ void scored_probabilities(const Params& p, uint32_t (&s0)[32],
-                                                     uint32_t (&s1)[32], float (&pf)[64],
-                                                     uint32_t (&w)[32], bool edge, int lim, int hi,
-                                                     float bias, bool after, float ahead, float f,
-                                                     const float* lse) {
+// thread's.  Keys after their query get 2 slope (j - i) less; SLOW: some visible
+// key is, or some query of the warp's tile does not see some key (two loops
+// instead of branches in one, which would keep its instructions from being
+// interleaved).  `ahead` = j - the first of the 64 queries, f = -2 slope in log2
+// units; columns outside [lim, hi) are forbidden for this key.
+//
+// With a cap, from r = 1 / (1 + 2^(2 y log2(e))): tanh(y) = 1 - 2 r, 1 -
+// tanh^2(y) = 4 r (1 - r).  LSE comes off after the tanh, from shared memory (it
+// is a constant of the column, not of the thread).  (Polynomials for small
+// arguments, as in the forward, were slower here: registers bound this loop, not
+// the special-function unit.)
+template <int MODE, bool SLOW, class Emit>
+__device__ __forceinline__ void scored_probabilities(const Params& p, const uint32_t (&s0)[32],
+                                                     const uint32_t (&s1)[32], float (&pf)[64],
+                                                     int lim, int hi, float bias, float ahead,
+                                                     float f, const float* lse, Emit emit) {
   constexpr bool CAP = (MODE & kCap) != 0, BIAS = (MODE & kBias) != 0;
   const float c = p.scale_log2;
-  if constexpr (!CAP) {
-    // without a cap the bias after the query and the mask can go onto the raw
-    // scores; what is left is one fma and one exponential per score
-    if (BIAS && after) {
-      const float g = f * p.inv_scale_log2;
+  const float top = p.cap_log2 + bias, m2 = -2.f * p.cap_log2;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        s0[i] = __float_as_uint(fmaf(g, fmaxf(ahead - static_cast<float>(i), 0.f),
-                                     __uint_as_float(s0[i])));
-        s1[i] = __float_as_uint(fmaf(g, fmaxf(ahead - static_cast<float>(32 + i), 0.f),
-                                     __uint_as_float(s1[i])));
-      }
-    }
-    if (edge) {
+  for (int c0 = 0; c0 < 64; c0 += 8) {
+    const uint32_t* src = c0 < 32 ? s0 + c0 : s1 + (c0 - 32);
+    float x[8];
+    if constexpr (CAP) {
+      float r[8];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (i < lim || i >= hi) s0[i] = __float_as_uint(-INFINITY);
-        if (32 + i < lim || 32 + i >= hi) s1[i] = __float_as_uint(-INFINITY);
-      }
-    }
-#pragma unroll
-    for (int i2 = 0; i2 < 32; i2 += 2) {
-      const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
-      float x0, x1, x2, x3;
-      fma2(x0, x1, __uint_as_float(src[0]), __uint_as_float(src[1]), c, c, bias, bias);
-      fma2(x2, x3, __uint_as_float(src[2]), __uint_as_float(src[3]), c, c, bias, bias);
-      const int c0 = 2 * i2;
-      pf[c0 + 0] = ex2(x0);
-      pf[c0 + 1] = ex2(x1);
-      pf[c0 + 2] = ex2(x2);
-      pf[c0 + 3] = ex2(x3);
-    }
-#pragma unroll
-    for (int i2 = 0; i2 < 32; ++i2) w[i2] = pack_bf16x2(pf[2 * i2], pf[2 * i2 + 1]);
-  } else {
-    // the score times the cap's derivative, from r = 1 / (1 + 2^(2 y log2(e))):
-    // tanh(y) = 1 - 2 r, 1 - tanh^2(y) = 4 r (1 - r).  LSE comes off after the
-    // tanh, from shared memory (it is a constant of the column, not of the thread).
-    const float top = p.cap_log2 + bias, m2 = -2.f * p.cap_log2;
-#pragma unroll
-    for (int i2 = 0; i2 < 32; i2 += 2) {
-      const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
-      const int c0 = 2 * i2;
-      const float4 l = *reinterpret_cast<const float4*>(lse + c0);
-      float r[4], x[4], d[4];
-      fma2(x[0], x[1], __uint_as_float(src[0]), __uint_as_float(src[1]), p.cap_in, p.cap_in, 0.f,
-           0.f);
-      fma2(x[2], x[3], __uint_as_float(src[2]), __uint_as_float(src[3]), p.cap_in, p.cap_in, 0.f,
-           0.f);
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        add2(r[e], r[e + 1], ex2(x[e]), ex2(x[e + 1]), 1.f, 1.f);
+      for (int e = 0; e < 8; e += 2) {
+        fma2(r[e], r[e + 1], __uint_as_float(src[e]), __uint_as_float(src[e + 1]), p.cap_in,
+             p.cap_in, 0.f, 0.f);
+        add2(r[e], r[e + 1], ex2(r[e]), ex2(r[e + 1]), 1.f, 1.f);
         r[e] = rcp(r[e]);
         r[e + 1] = rcp(r[e + 1]);
-        fma2(d[e], d[e + 1], r[e], r[e + 1], -r[e], -r[e + 1], r[e], r[e + 1]);  // r (1 - r)
       }
-      add2(x[0], x[1], top, top, -l.x, -l.y);
-      add2(x[2], x[3], top, top, -l.z, -l.w);
-      fma2(x[0], x[1], r[0], r[1], m2, m2, x[0], x[1]);
-      fma2(x[2], x[3], r[2], r[3], m2, m2, x[2], x[3]);
-      if (BIAS && after) {
+      const float4 l0 = *reinterpret_cast<const float4*>(lse + c0),
+                   l1 = *reinterpret_cast<const float4*>(lse + c0 + 4);
+      fma2(x[0], x[1], r[0], r[1], m2, m2, top - l0.x, top - l0.y);
+      fma2(x[2], x[3], r[2], r[3], m2, m2, top - l0.z, top - l0.w);
+      fma2(x[4], x[5], r[4], r[5], m2, m2, top - l1.x, top - l1.y);
+      fma2(x[6], x[7], r[6], r[7], m2, m2, top - l1.z, top - l1.w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = fmaf(f, fmaxf(ahead - static_cast<float>(c0 + e), 0.f), x[e]);
+      for (int e = 0; e < 8; e += 2) {
+        float q0, q1;
+        fma2(q0, q1, r[e], r[e + 1], -4.f, -4.f, 4.f, 4.f);
+        fma2(pf[c0 + e], pf[c0 + e + 1], r[e], r[e + 1], q0, q1, 0.f, 0.f);
       }
-      if (edge) {
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (c0 + e < lim || c0 + e >= hi) x[e] = -INFINITY;
-      }
+      for (int e = 0; e < 8; e += 2)
+        fma2(x[e], x[e + 1], __uint_as_float(src[e]), __uint_as_float(src[e + 1]), c, c, bias,
+             bias);
+    }
+    if constexpr (SLOW) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[e] = ex2(x[e]);
-        pf[c0 + e] = x[e] * (4.f * d[e]);
+      for (int e = 0; e < 8; ++e) {
+        if (BIAS) x[e] = fmaf(f, fmaxf(ahead - static_cast<float>(c0 + e), 0.f), x[e]);
+        if (c0 + e < lim || c0 + e >= hi) x[e] = -INFINITY;
       }
-      w[i2] = pack_bf16x2(x[0], x[1]);
-      w[i2 + 1] = pack_bf16x2(x[2], x[3]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = ex2(x[e]);
+    emit(c0 / 2, pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+         pack_bf16x2(x[6], x[7]));
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      if constexpr (CAP)
+        fma2(pf[c0 + e], pf[c0 + e + 1], pf[c0 + e], pf[c0 + e + 1], x[e], x[e + 1], 0.f, 0.f);
+      else
+        pf[c0 + e] = x[e], pf[c0 + e + 1] = x[e + 1];
     }
   }
 }
@@ -926,42 +905,55 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // P = 2^(scale * log2(e) * S') (S' already holds -LSE/scale), zero
         // where forbidden
         float pf[64];
-        uint32_t w[32];
         if constexpr (SCORED) {
           float bias = 0.f, f = 0.f;
           const int ahead = j - qt * BM - 64 * half;
-          bool after = false;
+          bool slow = __any_sync(0xffffffffu, lim > 0 || hi < 64);
           if constexpr ((MODE & kBias) != 0) {
             const float slope2 = LOG2E * __ldg(p.slopes + q_head(item.bh, member));
             bias = slope2 * static_cast<float>(j - qt * BM);
             f = -2.f * slope2;
             // a query of this half that sees this key and comes before it
-            after = __any_sync(0xffffffffu, lim < hi && lim < ahead);
+            slow = slow || __any_sync(0xffffffffu, lim < hi && lim < ahead);
           }
-          const bool edge = __any_sync(0xffffffffu, lim > 0 || hi < 64);
-          scored_probabilities<MODE>(p, s0, s1, pf, w, edge, lim, hi, bias, after,
-                                     static_cast<float>(ahead), f,
-                                     sm.lse[CAP ? t % QSTAGES : 0] + (CAP ? 64 * half : 0));
+          const float* lse = sm.lse[CAP ? t % QSTAGES : 0] + (CAP ? 64 * half : 0);
+          // P^T goes to tensor memory eight columns at a time, so that it takes
+          // no registers, once its previous tile has been read by dV
+          auto emit = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+            if (i == 0) {
+              wait(&sm.p_free, (t & 1) ^ 1);
+              tc_fence_after();
+            }
+            tmem_st4(tPT + i, a0, a1, a2, a3);
+          };
+          if (slow)
+            scored_probabilities<MODE, true>(p, s0, s1, pf, lim, hi, bias,
+                                             static_cast<float>(ahead), f, lse, emit);
+          else
+            scored_probabilities<MODE, false>(p, s0, s1, pf, lim, hi, bias,
+                                              static_cast<float>(ahead), f, lse, emit);
+          if (!ok) break;
         } else {
 #pragma unroll
-        for (int i2 = 0; i2 < 32; i2 += 2) {
-          const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
-          float x0, x1, x2, x3;
-          fma2(x0, x1, __uint_as_float(src[0]), __uint_as_float(src[1]), c, c, 0.f, 0.f);
-          fma2(x2, x3, __uint_as_float(src[2]), __uint_as_float(src[3]), c, c, 0.f, 0.f);
-          const int c0 = 2 * i2;
-          pf[c0 + 0] = (c0 + 0 < lim || (BAND && c0 + 0 >= hi)) ? 0.f : ex2(x0);
-          pf[c0 + 1] = (c0 + 1 < lim || (BAND && c0 + 1 >= hi)) ? 0.f : ex2(x1);
-          pf[c0 + 2] = (c0 + 2 < lim || (BAND && c0 + 2 >= hi)) ? 0.f : ex2(x2);
-          pf[c0 + 3] = (c0 + 3 < lim || (BAND && c0 + 3 >= hi)) ? 0.f : ex2(x3);
-        }
+          for (int i2 = 0; i2 < 32; i2 += 2) {
+            const uint32_t* src = i2 < 16 ? s0 + 2 * i2 : s1 + 2 * (i2 - 16);
+            float x0, x1, x2, x3;
+            fma2(x0, x1, __uint_as_float(src[0]), __uint_as_float(src[1]), c, c, 0.f, 0.f);
+            fma2(x2, x3, __uint_as_float(src[2]), __uint_as_float(src[3]), c, c, 0.f, 0.f);
+            const int c0 = 2 * i2;
+            pf[c0 + 0] = (c0 + 0 < lim || (BAND && c0 + 0 >= hi)) ? 0.f : ex2(x0);
+            pf[c0 + 1] = (c0 + 1 < lim || (BAND && c0 + 1 >= hi)) ? 0.f : ex2(x1);
+            pf[c0 + 2] = (c0 + 2 < lim || (BAND && c0 + 2 >= hi)) ? 0.f : ex2(x2);
+            pf[c0 + 3] = (c0 + 3 < lim || (BAND && c0 + 3 >= hi)) ? 0.f : ex2(x3);
+          }
+          uint32_t w[32];
 #pragma unroll
-        for (int i2 = 0; i2 < 32; ++i2) w[i2] = pack_bf16x2(pf[2 * i2], pf[2 * i2 + 1]);
+          for (int i2 = 0; i2 < 32; ++i2) w[i2] = pack_bf16x2(pf[2 * i2], pf[2 * i2 + 1]);
+          // P^T of the previous tile pair has been read by its dV product
+          if (!wait(&sm.p_free, (t & 1) ^ 1)) break;
+          tc_fence_after();
+          tmem_st32(tPT, w);
         }
-        // P^T of the previous tile pair has been read by its dV product
-        if (!wait(&sm.p_free, (t & 1) ^ 1)) break;
-        tc_fence_after();
-        tmem_st32(tPT, w);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(smem_u32(&sm.p_full));
@@ -1290,7 +1282,6 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
     p.cap_log2 = mod->softcap * LOG2E;
     p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
     p.slopes = mod->slopes;
-    p.inv_scale_log2 = 1.f / p.scale_log2;
     p.lse_log2 = lse_log2;
     p.masked = mod->masked;
     p.plan = mod->plan;

@@ -117,6 +117,28 @@ struct __align__(1024) Smem {
   alignas(128) uint8_t slope[QT][MODE & kBias ? 128 : 16];
 };
 
+// tanh for small arguments: y (kTanh[0] + kTanh[1] y^2 + kTanh[2] y^4), within
+// 1.8e-7 of it for |y| <= kTanhSmall (a least-maximum fit over that interval,
+// made for this file).  Scores seldom reach 0.3 of a cap, and then a tile needs
+// no second exponential and no reciprocal per score.
+constexpr double kTanhSmall = 0.3;
+constexpr double kTanh[3] = {0.99999601, -0.3329748, 0.12522591};
+
+// The cap in units of q.k (x) and log2: softcap * log2(e) * tanh(scale * x /
+// softcap) = x (poly[0] + poly[1] x^2 + poly[2] x^4) for |x| <= small.
+struct CapPoly {
+  float small, poly[3];
+};
+CapPoly cap_poly(float scale, float softcap) {
+  CapPoly c{};
+  if (!(softcap > 0.f)) return c;
+  const double k = static_cast<double>(scale) / softcap;
+  c.small = static_cast<float>(kTanhSmall / k);
+  double f = scale * 1.4426950408889634;
+  for (int i = 0; i < 3; ++i, f *= k * k) c.poly[i] = static_cast<float>(kTanh[i] * f);
+  return c;
+}
+
 struct Params {
   __nv_bfloat16* o;
   float* lse;
@@ -131,8 +153,7 @@ struct Params {
   int group;            // query heads per key head
   float cap_log2;       // softcap * log2(e); 0: no cap
   float cap_in;         // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
-  float cap_small;      // largest |q.k| of the polynomial (below)
-  float cap_poly[4];    // its coefficients, in powers of (q.k)^2, in log2 units
+  CapPoly cap;
   const float* slopes;  // distance bias per head, or null
   float inv_scale, inv_scale_log2;
   bool masked;
@@ -163,6 +184,7 @@ __device__ __forceinline__ Item decode_item_planned(const Params& p, int t, bool
     it.qb = t % p.num_qblocks;
     it.bh = t / p.num_qblocks;
   }
+  const size_t qtiles = (p.n_q + BM - 1) / BM;
   it.key_limit = p.n_k;
   it.j0 = 0;
   int first[QT], end[QT];
@@ -173,8 +195,7 @@ __device__ __forceinline__ Item decode_item_planned(const Params& p, int t, bool
     if (tile * BM >= p.n_q) continue;
     end[s] = p.n_k;
     if (p.masked) {
-      const int4 r = __ldg(p.plan.block_keys +
-                           static_cast<size_t>(it.bh / p.H) * ((p.n_q + BM - 1) / BM) + tile);
+      const int4 r = __ldg(p.plan.block_keys + it.bh / p.H * qtiles + tile);
       first[s] = r.x;
       end[s] = r.y;
     }
@@ -255,11 +276,6 @@ __device__ __forceinline__ void record_timeout(const Params& p, SmemT& sm) {
 __device__ __forceinline__ float bf16_round(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
-
-// tanh(y) = y (T0 + T1 y^2 + T2 y^4 + T3 y^6) for |y| <= TANH_SMALL, within 1.3e-7
-// of it (a least-maximum fit made for this file over that interval).
-constexpr float TANH_SMALL = 0.5f;
-constexpr float T0 = 0.999997676f, T1 = -0.333206552f, T2 = 0.131451457f, T3 = -0.0433724845f;
 
 template <int MODE, int D_>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -619,6 +635,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int kbase = ((OFFSET ? it.j0 : 0) + j) * BN;
         float offset = 0.f;  // what every score of the row still gets (log2 units)
         float top_raw = 0.f;  // largest raw score, where the cap's own maximum follows from it
+        bool merged = false;  // the cap's polynomial is left to the exponential's argument
         // whether a row of this warp does not see the whole tile
         const bool edge =
             SCORED && __any_sync(0xffffffffu, kbase < row_lo || kbase + BN > row_hi);
@@ -640,8 +657,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             top_raw = fmaxf(max3(hi4[0], hi4[1], hi4[2]), hi4[3]);
             const float low = fminf(min3(lo4[0], lo4[1], lo4[2]), lo4[3]);
-            if (__all_sync(0xffffffffu, fmaxf(top_raw, -low) <= p.cap_small)) {
-              // small arguments: a polynomial in the raw score on the FMA pipe
+            const bool small = __all_sync(0xffffffffu, fmaxf(top_raw, -low) <= p.cap.small);
+            merged = small && !BIAS && !edge;
+            if (merged) {
+              // (the polynomial is taken in the exponential's argument below)
+            } else if (small) {
 #pragma unroll
               for (int q4 = 0; q4 < SC; ++q4)
 #pragma unroll
@@ -649,9 +669,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   const float x0 = __uint_as_float(r[q4][i]), x1 = __uint_as_float(r[q4][i + 1]);
                   float z0, z1, y0, y1;
                   fma2(z0, z1, x0, x1, x0, x1, 0.f, 0.f);
-                  fma2(y0, y1, z0, z1, p.cap_poly[3], p.cap_poly[3], p.cap_poly[2], p.cap_poly[2]);
-                  fma2(y0, y1, z0, z1, y0, y1, p.cap_poly[1], p.cap_poly[1]);
-                  fma2(y0, y1, z0, z1, y0, y1, p.cap_poly[0], p.cap_poly[0]);
+                  fma2(y0, y1, z0, z1, p.cap.poly[2], p.cap.poly[2], p.cap.poly[1], p.cap.poly[1]);
+                  fma2(y0, y1, z0, z1, y0, y1, p.cap.poly[0], p.cap.poly[0]);
                   fma2(y0, y1, x0, x1, y0, y1, 0.f, 0.f);
                   r[q4][i] = __float_as_uint(y0);
                   r[q4][i + 1] = __float_as_uint(y1);
@@ -766,6 +785,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const float neg_m = ((m == -INFINITY) ? 0.f : -m) + (BIAS ? offset : 0.f);
         float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
         uint32_t pk[SC / 2][32];
+        if (CAP && merged) {
+          // the cap's polynomial in the argument: x (c0 + c1 x^2 + c2 x^4) - m
+#pragma unroll
+          for (int q4 = 0; q4 < SC; ++q4) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float r0 = __uint_as_float(r[q4][i]), r1 = __uint_as_float(r[q4][i + 1]);
+              float z0, z1, x0, x1;
+              fma2(z0, z1, r0, r1, r0, r1, 0.f, 0.f);
+              fma2(x0, x1, z0, z1, p.cap.poly[2], p.cap.poly[2], p.cap.poly[1], p.cap.poly[1]);
+              fma2(x0, x1, z0, z1, x0, x1, p.cap.poly[0], p.cap.poly[0]);
+              fma2(x0, x1, r0, r1, x0, x1, neg_m, neg_m);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              add2(ls0, ls1, ls0, ls1, p0, p1);
+              pk[q4 >> 1][(q4 & 1) * 16 + (i >> 1)] = pack_bf16x2(p0, p1);
+            }
+          }
+        } else {
 #pragma unroll
         for (int q4 = 0; q4 < SC; ++q4) {
 #pragma unroll
@@ -781,6 +818,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             pk[q4 >> 1][(q4 & 1) * 16 + (i >> 1)] = pack_bf16x2(p0, p1);
             pk[q4 >> 1][(q4 & 1) * 16 + (i >> 1) + 1] = pack_bf16x2(p2, p3);
           }
+        }
         }
         l += (ls0 + ls1) + (ls2 + ls3);
         if (pingpong) {
@@ -940,13 +978,7 @@ cudaError_t launch_fwd_tc(const Problem& pb, const CUtensorMap& tmq, const CUten
     p.group = mod->group;
     p.cap_log2 = mod->softcap * 1.4426950408889634f;
     p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
-    if (mod->softcap > 0.f) {
-      const double k = static_cast<double>(pb.scale) / mod->softcap;  // tanh's argument per q.k
-      const double t[4] = {T0, T1, T2, T3};
-      p.cap_small = static_cast<float>(TANH_SMALL / k);
-      double f = p.cap_log2 * k;
-      for (int i = 0; i < 4; ++i, f *= k * k) p.cap_poly[i] = static_cast<float>(t[i] * f);
-    }
+    p.cap = cap_poly(pb.scale, mod->softcap);
     p.slopes = mod->slopes;
     p.inv_scale = 1.f / pb.scale;
     p.inv_scale_log2 = 1.f / p.scale_log2;
