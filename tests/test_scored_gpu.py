@@ -108,12 +108,12 @@ def test_plan_is_the_mask(name, n_q, n_k):
     plan, see = _mask(name, B, n_q, n_k)
     raw = plan.cpu().numpy()
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
-    qt, kt = -(-n_q // 128), -(-n_k // 128)
+    qb, kt = -(-n_q // 256), -(-n_k // 128)
     at, parts = 256, []
-    for count, width in ((B * n_q, 2), (B * n_k, 2), (B * qt, 4), (B * kt, 4)):
+    for count, width in ((B * n_q, 2), (B * n_k, 2), (B * qb, 8), (B * kt, 4)):
         parts.append(raw[at:at + count * width * 4].view(np.int32).reshape(count, width))
         at += up(count * width * 4)
-    rows, keys, blocks, tiles = parts
+    rows, keys, q_items, k_items = parts
     assert list(raw[:12].view(np.int32)) == [n_q, n_k, B]
     for b in range(B):
         for got, want in ((rows[b * n_q:(b + 1) * n_q], see[b]),
@@ -121,15 +121,25 @@ def test_plan_is_the_mask(name, n_q, n_k):
             n = want.shape[1]
             made = (np.arange(n) >= got[:, :1]) & (np.arange(n) < got[:, 1:])
             assert np.array_equal(made, want)
-        for got, want in ((blocks[b * qt:(b + 1) * qt], see[b]), (tiles[b * kt:(b + 1) * kt], see[b].T)):
-            for t in range(len(got)):
-                part = want[128 * t:128 * t + 128]
-                any_, all_ = np.flatnonzero(part.any(0)), np.flatnonzero(part.all(0))
-                assert (got[t, 0], got[t, 1]) == ((any_[0], any_[-1] + 1) if any_.size else (0, 0))
-                if all_.size:
-                    assert (got[t, 2], got[t, 3]) == (all_[0], all_[-1] + 1)
-                else:
-                    assert got[t, 2] >= got[t, 3]
+
+    def span(part):
+        seen = np.flatnonzero(part.any(0))
+        return (seen[0], seen[-1] + 1) if seen.size else (0, 0)
+    assert sorted(map(tuple, q_items[:, :2])) == [(b, x) for b in range(B) for x in range(qb)]
+    for b, block, first, end0, end1, work, *_ in q_items:
+        halves = [span(see[b][256 * block + 128 * i:256 * block + 128 * i + 128]) for i in (0, 1)]
+        assert (end0, end1) == (halves[0][1], halves[1][1])
+        assert first == min((lo for lo, hi in halves if hi), default=0)
+        assert work == sum(-(-hi // 128) - first // 128 for _, hi in halves if hi)
+    assert sorted(map(tuple, k_items[:, :2])) == [(b, x) for b in range(B) for x in range(kt)]
+    for b, tile, first, count in k_items:
+        lo, hi = span(see[b].T[128 * tile:128 * tile + 128])
+        assert (first, count) == ((lo // 128, -(-hi // 128) - lo // 128) if hi else (0, 0))
+    if MASKS[name].get("docs"):   # by falling work, ties in index order
+        for work, index in ((q_items[:, 5], q_items[:, 0] * qb + q_items[:, 1]),
+                            (k_items[:, 3], k_items[:, 0] * kt + k_items[:, 1])):
+            place = list(zip(-work, index))
+            assert place == sorted(place)
 
 
 def _check_fwd(got, q, k, v, see, scale, cap, slopes):

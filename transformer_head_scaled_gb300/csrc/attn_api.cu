@@ -1071,7 +1071,7 @@ int attn_mask_plan(int B, int n_q, int n_k, int window_left, int window_right,
                        prefix_lens};
   const cudaError_t e = launch_mask_plan(pb, plan, make_ctx(*di, stream));
   if (e != cudaSuccess) return cuda_fail(e);
-  g_launches.fetch_add(doc_ids != nullptr ? 2 : 1);
+  g_launches.fetch_add(doc_ids == nullptr ? 1 : (mask_plan_ordered(pb) ? 3 : 2));
   return ATTN_OK;
 }
 

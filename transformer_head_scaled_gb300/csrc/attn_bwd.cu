@@ -172,35 +172,32 @@ struct Params {
 struct Item {
   int bh, kt, qt0, n, key_limit;
   int nq;
-  bool desc;  // kScored: heaviest key tiles first
 };
 
-__device__ __forceinline__ Item bwd_item_planned(const Params& p, int t, bool desc) {
+// An item of changed scores: the plan's, for every key head in turn.
+__device__ __forceinline__ Item bwd_item_planned(const Params& p, int t) {
   Item it;
-  if (desc) {
-    it.kt = t / p.BH;
-    it.bh = t % p.BH;
-  } else {
-    it.bh = t / p.num_kt;
-    it.kt = t % p.num_kt;
-  }
+  const int heads = p.H / p.group, e = t / heads, hk = t - e * heads;
   it.key_limit = p.n_k;
-  it.qt0 = 0;
-  it.nq = p.num_qt;
   if (p.masked) {
-    const int4 r = __ldg(p.plan.tile_rows +
-                         static_cast<size_t>(it.bh / (p.H / p.group)) * p.num_kt + it.kt);
-    it.qt0 = r.x / BM;
-    it.nq = r.y > 0 ? (r.y + BM - 1) / BM - it.qt0 : 0;
+    const int4 k = __ldg(reinterpret_cast<const int4*>(p.plan.key_items + e));
+    it.bh = k.x * heads + hk;
+    it.kt = k.y;
+    it.qt0 = k.z;
+    it.nq = k.w;
+  } else {
+    it.kt = e % p.num_kt;
+    it.bh = e / p.num_kt * heads + hk;
+    it.qt0 = 0;
+    it.nq = p.num_qt;
   }
   it.n = it.nq * p.group;
-  it.desc = desc;
   return it;
 }
 
 template <int MODE>
-__device__ __forceinline__ Item bwd_item(const Params& p, int t, bool desc) {
-  if constexpr ((MODE & kScored) != 0) return bwd_item_planned(p, t, desc);
+__device__ __forceinline__ Item bwd_item(const Params& p, int t) {
+  if constexpr ((MODE & kScored) != 0) return bwd_item_planned(p, t);
   Item it;
   if (p.mask == kMaskCausal) {
     // key tiles with the most query tiles first (longest-processing-time order)
@@ -240,15 +237,28 @@ __device__ __forceinline__ Item bwd_item(const Params& p, int t, bool desc) {
   return it;
 }
 
-// Index of the next item of this CTA at or after `from` with work, or -1.
+// The items of this CTA, one after the other: every gridDim.x-th, or, of planned
+// ones, back and forth.
 template <int MODE>
-__device__ __forceinline__ int next_item(const Params& p, int num_items, bool desc, int from,
-                                         Item& out) {
-  for (int x = from; x < num_items; x += gridDim.x) {
-    out = bwd_item<MODE>(p, x, desc);
-    if (out.n > 0) return x;
+struct Walk {
+  int x, step;
+  __device__ __forceinline__ Walk()
+      : x(blockIdx.x), step((MODE & kScored) ? first_step() : static_cast<int>(gridDim.x)) {}
+  __device__ __forceinline__ void next() {
+    x += step;
+    if (MODE & kScored) step = 2 * gridDim.x - step;
   }
-  return -1;
+};
+
+// Moves on to the next item with work, this one included; false: there is none.
+template <int MODE>
+__device__ __forceinline__ bool find_item(const Params& p, int num_items, Walk<MODE>& at,
+                                          Item& out) {
+  for (; at.x < num_items; at.next()) {
+    out = bwd_item<MODE>(p, at.x);
+    if (out.n > 0) return true;
+  }
+  return false;
 }
 
 template <class SmemT>
@@ -483,11 +493,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   grid_dependency_wait();
 
   int num_items = p.num_items;
-  bool desc = false;
   if constexpr (SCORED) {
     if (p.masked) {
       const int4 h = __ldg(p.plan.header);
-      desc = h.w != 0;
       if (h.x != p.n_q || h.y != p.n_k || h.z * (p.H / p.group) != p.BH) {
         // a plan of other sizes: report it and do nothing
         num_items = 0;
@@ -512,8 +520,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t it = 0, nv = 0, nq = 0, no = 0;  // K, V, Q and dO loads issued
       bool ok = true;
       Item item;
-      for (int x = next_item<MODE>(p, num_items, desc, blockIdx.x, item); x >= 0 && ok;
-           x = next_item<MODE>(p, num_items, desc, x + gridDim.x, item)) {
+      for (Walk<MODE> at; ok && find_item(p, num_items, at, item); at.next()) {
         const uint32_t slot = it & 1;
         ok = mbar_wait(smem_u32(&sm.k_empty[slot]), ((it >> 1) & 1) ^ 1, p.limit_ns, abort);
         if (!ok) break;
@@ -637,9 +644,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     uint32_t it = 0, t = 0;
     Item cur;
-    int cx = next_item<MODE>(p, num_items, desc, blockIdx.x, cur);
+    Walk<MODE> at;
+    const bool any = find_item(p, num_items, at, cur);
     int ci = 0;  // index of tile t inside its item
-    if (cx >= 0 && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0) && wait(&sm.v_full, 0) &&
+    if (any && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0) && wait(&sm.v_full, 0) &&
         wait(&sm.o_full[0], 0)) {
       tc_fence_after();
       issue_s(0, 0);
@@ -648,14 +656,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t slot = it & 1, st = t % QSTAGES, os = t % OSTAGES;
         // the next tile pair (possibly of the next item)
         Item nx = cur;
-        int nxx = cx, ni = ci + 1;
+        int ni = ci + 1;
         uint32_t nit = it;
+        bool has_next = true;
         if (ni >= cur.n) {
-          nxx = next_item<MODE>(p, num_items, desc, cx + gridDim.x, nx);
+          at.next();
+          has_next = find_item(p, num_items, at, nx);
           ni = 0;
           nit = it + 1;
         }
-        const bool has_next = nxx >= 0;
         const uint32_t nslot = nit & 1, nst = (t + 1) % QSTAGES, nos = (t + 1) % OSTAGES;
         // its score product goes first, as soon as S'^T of this one is in the
         // elementwise warps' registers
@@ -716,7 +725,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (!has_next) break;
         cur = nx;
-        cx = nxx;
         ci = ni;
         it = nit;
         ++t;
@@ -755,8 +763,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       named_bar_sync(bar_id, 64);
     };
     uint32_t it = 0, t = 0;
-    for (int x = blockIdx.x; x < num_items && ok; x += gridDim.x) {
-      const Item item = bwd_item<MODE>(p, x, desc);
+    for (Walk<MODE> at; at.x < num_items && ok; at.next()) {
+      const Item item = bwd_item<MODE>(p, at.x);
       const int key_row0 = item.kt * BN + 64 * g;
       const int b = item.bh / kv_heads, hk = item.bh % kv_heads;
       if (item.n == 0) {
@@ -860,8 +868,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     };
     uint32_t t = 0;
     Item item;
-    for (int x = next_item<MODE>(p, num_items, desc, blockIdx.x, item); x >= 0 && ok;
-         x = next_item<MODE>(p, num_items, desc, x + gridDim.x, item)) {
+    for (Walk<MODE> at; ok && find_item(p, num_items, at, item); at.next()) {
       const int j = item.kt * BN + r;  // this thread's key
       const bool row_valid = j < item.key_limit;
       int2 rows = make_int2(0, row_valid ? p.n_q : 0);  // kScored: this key's queries

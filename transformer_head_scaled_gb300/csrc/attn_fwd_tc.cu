@@ -172,44 +172,34 @@ struct Item {
   int n[QT];
 };
 
-// An item under a mask plan.  desc: later queries see more keys, so that the
-// heaviest row blocks come first as under the causal mask.
+// An item of changed scores: the plan's, for every head in turn.
 template <int BN>
-__device__ __forceinline__ Item decode_item_planned(const Params& p, int t, bool desc) {
+__device__ __forceinline__ Item decode_item_planned(const Params& p, int t) {
   Item it;
-  if (desc) {
-    it.qb = p.num_qblocks - 1 - t / p.BH;
-    it.bh = t % p.BH;
-  } else {
-    it.qb = t % p.num_qblocks;
-    it.bh = t / p.num_qblocks;
-  }
-  const size_t qtiles = (p.n_q + BM - 1) / BM;
+  const int e = t / p.H, hh = t - e * p.H;
   it.key_limit = p.n_k;
-  it.j0 = 0;
-  int first[QT], end[QT];
-#pragma unroll
-  for (int s = 0; s < QT; ++s) {
-    const int tile = it.qb * QT + s;
-    first[s] = end[s] = 0;
-    if (tile * BM >= p.n_q) continue;
-    end[s] = p.n_k;
-    if (p.masked) {
-      const int4 r = __ldg(p.plan.block_keys + it.bh / p.H * qtiles + tile);
-      first[s] = r.x;
-      end[s] = r.y;
-    }
+  if (p.masked) {
+    const int4* q = reinterpret_cast<const int4*>(p.plan.query_items + e);
+    const int4 a = __ldg(q), b = __ldg(q + 1);
+    it.bh = a.x * p.H + hh;
+    it.qb = a.y;
+    it.j0 = a.z / BN;
+    it.n[0] = a.w > 0 ? (a.w + BN - 1) / BN - it.j0 : 0;
+    it.n[1] = b.x > 0 ? (b.x + BN - 1) / BN - it.j0 : 0;
+  } else {
+    it.qb = e % p.num_qblocks;
+    it.bh = e / p.num_qblocks * p.H + hh;
+    it.j0 = 0;
+    const int tiles = (p.n_k + BN - 1) / BN;
+    it.n[0] = tiles;
+    it.n[1] = it.qb * ROWS + BM < p.n_q ? tiles : 0;
   }
-  // both Q tiles walk the same stream of K/V tiles, from the first that either needs
-  it.j0 = min(end[0] > 0 ? first[0] : 0x7fffffff, end[1] > 0 ? first[1] : 0x7fffffff) / BN;
-#pragma unroll
-  for (int s = 0; s < QT; ++s) it.n[s] = end[s] > 0 ? (end[s] + BN - 1) / BN - it.j0 : 0;
   return it;
 }
 
 template <int MODE, int BN>
-__device__ __forceinline__ Item decode_item(const Params& p, int t, bool desc) {
-  if constexpr ((MODE & kScored) != 0) return decode_item_planned<BN>(p, t, desc);
+__device__ __forceinline__ Item decode_item(const Params& p, int t) {
+  if constexpr ((MODE & kScored) != 0) return decode_item_planned<BN>(p, t);
   constexpr bool BAND = MODE == kBand;
   Item it;
   if (p.mask == kMaskCausal) {
@@ -347,11 +337,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = sm.tmem_base;
 
   int num_items = p.num_items;
-  bool desc = false;
   if constexpr (SCORED) {
     if (p.masked) {
       const int4 h = __ldg(p.plan.header);
-      desc = h.w != 0;
       if (h.x != p.n_q || h.y != p.n_k || h.z * p.H != p.BH) {
         // a plan of other sizes: report it and write nothing
         num_items = 0;
@@ -359,6 +347,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   }
+  // the step from a CTA's item to its next one, and what turns it into the one
+  // after (planned items are dealt out back and forth)
+  const int step0 = SCORED ? first_step() : static_cast<int>(gridDim.x);
+  auto turn = [](int step) { return SCORED ? 2 * static_cast<int>(gridDim.x) - step : step; };
   // K and V have one head for every `group` query heads
   auto kv_head = [&](int bh) { return SCORED ? bh % p.H / p.group : bh % p.H; };
 
@@ -379,8 +371,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t cnt = 0;
       uint32_t items = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < num_items && ok; t += gridDim.x, ++items) {
-        const Item it = decode_item<MODE, BN>(p, t, desc);
+      for (int t = blockIdx.x, step = step0; t < num_items && ok;
+           t += step, step = turn(step), ++items) {
+        const Item it = decode_item<MODE, BN>(p, t);
         const int nmax = max(it.n[0], it.n[1]);
         // Q tiles of this item into buffer items % 2 (free once the S
         // products of item - 2 are done), then its K tiles.
@@ -508,8 +501,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       };
 
       uint32_t g0 = 0, items = 0;
-      for (int t = blockIdx.x; t < num_items && ok; t += gridDim.x, ++items) {
-        const Item it = decode_item<MODE, BN>(p, t, desc);
+      for (int t = blockIdx.x, step = step0; t < num_items && ok;
+           t += step, step = turn(step), ++items) {
+        const Item it = decode_item<MODE, BN>(p, t);
         const int n = it.n[s];
         const int nmax = max(it.n[0], it.n[1]);
         // The previous item's last PV product goes first unless this item's
@@ -600,8 +594,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t turns = 0;
     if (s == 1) mbar_arrive(smem_u32(&sm.turn[0]));  // Q tile 0 goes first
     bool ok = true;
-    for (int t = blockIdx.x; t < num_items && ok; t += gridDim.x) {
-      const Item it = decode_item<MODE, BN>(p, t, desc);
+    for (int t = blockIdx.x, step = step0; t < num_items && ok; t += step, step = turn(step)) {
+      const Item it = decode_item<MODE, BN>(p, t);
       const int row0 = it.qb * ROWS + s * BM;
       const int row = row0 + quarter * 32 + lane;
       float m = -INFINITY;  // running max of scale*log2(e)*score (possibly stale)

@@ -14,19 +14,37 @@ enum MaskKind : int { kMaskNone = 0, kMaskCausal = 1, kMaskKeyPadding = 2, kMask
 enum DeviceStatus : int { kDevOk = 0, kDevTimeout = 1, kDevWrongPlan = 2 };
 
 // The plan of a mask under which every query sees one run of keys: device
-// arrays inside the caller's plan buffer (attn_mask_plan).  Intervals are
-// [x, y); per 128 queries (or keys): {x, y} = the union's bounds, {z, w} = the
-// intersection, z >= w when it is empty.
+// arrays inside the caller's plan buffer (attn_mask_plan).  Intervals are [x, y).
 constexpr int kMaskTile = 128;
-struct MaskPlan {
-  const int4* header;      // n_q, n_k, B, 1 when later queries see more keys
-  const int2* row_keys;    // [B][n_q] keys of a query
-  const int2* key_rows;    // [B][n_k] queries of a key
-  const int4* block_keys;  // [B][ceil(n_q / 128)]
-  const int4* tile_rows;   // [B][ceil(n_k / 128)]
+// A work item of the forward: 256 queries of a batch entry, the first key that
+// any of them sees and the end of those that each half sees (0: none).
+struct __align__(16) QueryItem {
+  int b, block, first, end[2];
+  int work;  // 128-key tiles
+  int pad[2];
 };
+// A work item of the backward: 128 keys, the first 128-query tile that sees any
+// of them, and how many tiles do.
+struct __align__(16) KeyItem {
+  int b, tile, first, count;
+};
+struct MaskPlan {
+  const int4* header;    // n_q, n_k, B
+  const int2* row_keys;  // [B][n_q] keys of a query
+  const int2* key_rows;  // [B][n_k] queries of a key
+  // in the order in which they are dealt out, for every head alike
+  const QueryItem* query_items;  // [B * ceil(n_q / 256)]
+  const KeyItem* key_items;      // [B * ceil(n_k / 128)]
+};
+constexpr int kMostOrdered = 2048;  // items that a plan orders by their work
+
+// A persistent kernel deals planned items out back and forth: in every second
+// round the CTAs take them in reverse, so that who got the heaviest of one round
+// gets the lightest of the next.  The step from a CTA's item of an even round to
+// its next one; from an odd round it is 2 * gridDim.x less this.
+__device__ __forceinline__ int first_step() { return 2 * (gridDim.x - 1 - blockIdx.x) + 1; }
 struct MaskLayout {
-  size_t row_keys, key_rows, block_keys, tile_rows, runs, bytes;
+  size_t row_keys, key_rows, query_items, key_items, query_items_in, key_items_in, runs, bytes;
 };
 MaskLayout mask_layout(int B, int n_q, int n_k);
 MaskPlan mask_plan_at(const void* plan, int B, int n_q, int n_k);
@@ -75,6 +93,7 @@ struct Problem {
   int win_left, win_right;  // kMaskBand: query i sees keys i - win_left .. i + win_right
 };
 
+bool mask_plan_ordered(const MaskProblem& pb);
 struct LaunchCtx;
 cudaError_t launch_mask_plan(const MaskProblem& pb, void* plan, const LaunchCtx& ctx);
 

@@ -7,55 +7,63 @@
 //   * i and j lie in the same document: the same maximal run of equal ids, not
 //     negative.
 // Each of these leaves query i an interval of keys and key j an interval of
-// queries, so the attention kernels need nothing but intervals: per query and
-// per key for the elements of a tile, and per 128 queries and per 128 keys (the
-// union, which tiles to visit, and the intersection, which tiles need no
-// test).  The plan is these four arrays; one plan serves the forward and the
-// backward of every layer that shares the mask.
+// queries, so the attention kernels need nothing but intervals, and, per work
+// item, the tiles that it has to visit: the forward's items are 256 queries with
+// the keys that each half sees, the backward's 128 keys with the queries that see
+// them.  The items stand in the order in which they are to be dealt out, the
+// heaviest first where that is known: under a causal mask the last queries (the
+// first keys); with documents, whose work has no simple order, by counting.  One
+// plan serves the forward and the backward of every layer that shares the mask.
 //
-// Two kernels, both bound by launch and latency (16 bytes written per token):
-//   1. with documents: per 128 tokens, the first and the last token that
-//      begins a run;
-//   2. per 128 queries and 128 keys: the runs around them from those, the
-//      intervals and their unions and intersections.
+// Kernels, all bound by launch and latency (16 bytes written per token):
+//   1. with documents: per 256 tokens, the first and the last token that begins
+//      a run;
+//   2. per 256 queries and 256 keys: the runs around them from those, the
+//      intervals, and the items;
+//   3. with documents: the items by falling work, each one's rank the number of
+//      items with more (kMostOrdered of them at most; more even out anyway).
 #include "attn_internal.cuh"
 
 namespace attn {
 namespace {
 
-constexpr int TILE = kMaskTile;
+constexpr int BLOCK = 256;  // tokens per CTA: an item of the forward, two of the backward
+constexpr int WARPS = BLOCK / 32;
 
 struct MaskParams {
   int4* header;
   int2* row_keys;
   int2* key_rows;
-  int4* block_keys;
-  int4* tile_rows;
-  int2* runs;  // scratch: per tile {first, last} token that begins a run, or {n, -1}
+  QueryItem* query_items;
+  KeyItem* key_items;
+  // with ordering: the items before it
+  QueryItem* query_items_in;
+  KeyItem* key_items_in;
+  int2* runs;  // per block {first, last} token that begins a run, or {n, -1}
   const int* key_lens;
   const int* doc_ids;
   const int* prefix_lens;
-  int B, n_q, n_k, left, right, qt, kt;
+  int B, n_q, n_k, left, right, qb, kb, ordered;
 };
 
 __device__ __forceinline__ bool begins_run(const int* ids, int i) {
   return i == 0 || __ldg(ids + i) != __ldg(ids + i - 1);
 }
 
-__global__ void __launch_bounds__(TILE) attn_mask_runs_kernel(const MaskParams p) {
+__global__ void __launch_bounds__(BLOCK) attn_mask_runs_kernel(const MaskParams p) {
   grid_launch_dependents();
-  __shared__ unsigned bits[TILE / 32];
-  const int b = blockIdx.x / p.qt, tile = blockIdx.x - b * p.qt;
-  const int i = tile * TILE + threadIdx.x;
+  __shared__ unsigned bits[WARPS];
+  const int b = blockIdx.x / p.qb, block = blockIdx.x - b * p.qb;
+  const int i = block * BLOCK + threadIdx.x;
   const int* ids = p.doc_ids + static_cast<size_t>(b) * p.n_q;
   const unsigned vote = __ballot_sync(0xffffffffu, i < p.n_q && begins_run(ids, i));
   if ((threadIdx.x & 31) == 0) bits[threadIdx.x >> 5] = vote;
   __syncthreads();
   if (threadIdx.x == 0) {
     int first = p.n_q, last = -1;
-    for (int w = 0; w < TILE / 32; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       if (bits[w] == 0) continue;
-      const int at = tile * TILE + 32 * w;
+      const int at = block * BLOCK + 32 * w;
       if (last < 0) first = at + __ffs(bits[w]) - 1;
       last = at + 31 - __clz(bits[w]);
     }
@@ -63,83 +71,71 @@ __global__ void __launch_bounds__(TILE) attn_mask_runs_kernel(const MaskParams p
   }
 }
 
-// Smallest of lo and largest of hi over the CTA, for two pairs at once; every
-// thread gets the result.
-__device__ __forceinline__ int4 reduce_bounds(int min_a, int max_b, int max_c, int min_d,
-                                              int4* scratch) {
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) {
-    min_a = min(min_a, __shfl_xor_sync(0xffffffffu, min_a, m));
-    max_b = max(max_b, __shfl_xor_sync(0xffffffffu, max_b, m));
-    max_c = max(max_c, __shfl_xor_sync(0xffffffffu, max_c, m));
-    min_d = min(min_d, __shfl_xor_sync(0xffffffffu, min_d, m));
-  }
+// Smallest lo and largest hi of each half of the CTA (threads 0-127, 128-255);
+// every thread gets both: {lo, hi, lo, hi}.
+__device__ __forceinline__ int4 reduce_halves(int lo, int hi, int2* scratch) {
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
   __syncthreads();  // the scratch may still be read for the previous reduction
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = make_int4(min_a, max_b, max_c, min_d);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = make_int2(lo, hi);
   __syncthreads();
-  int4 r = scratch[0];
+  int4 r = make_int4(0x7fffffff, 0, 0x7fffffff, 0);
 #pragma unroll
-  for (int w = 1; w < TILE / 32; ++w) {
-    const int4 x = scratch[w];
-    r = make_int4(min(r.x, x.x), max(r.y, x.y), max(r.z, x.z), min(r.w, x.w));
+  for (int w = 0; w < WARPS / 2; ++w) {
+    const int2 x = scratch[w], y = scratch[w + WARPS / 2];
+    r = make_int4(min(r.x, x.x), max(r.y, x.y), min(r.z, y.x), max(r.w, y.y));
   }
   return r;
 }
 
-// {first, end} of the union of the CTA's intervals and of their intersection;
-// an empty interval adds nothing to the union and empties the intersection.
-// `in`: this thread has an interval at all.
-__device__ __forceinline__ int4 summary(int2 v, bool in, int4* scratch) {
-  const bool some = in && v.x < v.y;
-  const int4 r = reduce_bounds(some ? v.x : 0x7fffffff, some ? v.y : 0,
-                               in ? (some ? v.x : 0x7fffffff) : 0,
-                               in ? (some ? v.y : 0) : 0x7fffffff, scratch);
-  return r.y > 0 ? make_int4(r.x, r.y, r.z, r.w) : make_int4(0, 0, 0, 0);
+__device__ __forceinline__ int tiles_of(int first, int end) {
+  return end > 0 ? (end + kMaskTile - 1) / kMaskTile - first / kMaskTile : 0;
 }
 
-__global__ void __launch_bounds__(TILE) attn_mask_plan_kernel(const MaskParams p) {
-  __shared__ int4 scratch[TILE / 32];
-  __shared__ unsigned bits[TILE / 32];
-  const int tiles = max(p.qt, p.kt);
-  const int b = blockIdx.x / tiles, tile = blockIdx.x - b * tiles;
-  const int i = tile * TILE + threadIdx.x;  // as a query and as a key
-  if (blockIdx.x == 0 && threadIdx.x == 0)
-    *p.header = make_int4(p.n_q, p.n_k, p.B, p.right >= 0 ? 1 : 0);
+__global__ void __launch_bounds__(BLOCK) attn_mask_plan_kernel(const MaskParams p) {
+  grid_launch_dependents();
+  __shared__ int2 scratch[WARPS];
+  __shared__ unsigned bits[WARPS];
+  const int blocks = max(p.qb, p.kb);
+  const int b = blockIdx.x / blocks, block = blockIdx.x - b * blocks;
+  const int i = block * BLOCK + threadIdx.x;  // as a query and as a key
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.header = make_int4(p.n_q, p.n_k, p.B, 0);
   int run0 = 0, run1 = 0x7fffffff;  // this token's document
   if (p.doc_ids != nullptr) {
     const int* ids = p.doc_ids + static_cast<size_t>(b) * p.n_q;
     const unsigned vote = __ballot_sync(0xffffffffu, i < p.n_q && begins_run(ids, i));
     if ((threadIdx.x & 31) == 0) bits[threadIdx.x >> 5] = vote;
-    grid_dependency_wait();  // the tiles' runs
-    // the last run that begins before this tile, and the first one after it
+    grid_dependency_wait();  // the blocks' runs
+    // the last run that begins before this block, and the first one after it
     int before = 0, after = p.n_q;
-    const int2* runs = p.runs + static_cast<size_t>(b) * p.qt;
-    for (int t = threadIdx.x; t < p.qt; t += TILE) {
+    const int2* runs = p.runs + static_cast<size_t>(b) * p.qb;
+    for (int t = threadIdx.x; t < p.qb; t += BLOCK) {
       const int2 r = runs[t];
-      if (t < tile) before = max(before, r.y);
-      if (t > tile) after = min(after, r.x);
+      if (t < block) before = max(before, r.y);
+      if (t > block) after = min(after, r.x);
     }
-    const int4 near = reduce_bounds(after, before, 0, 0, scratch);
-    run0 = near.y;
-    run1 = near.x;
-    // the nearest beginnings inside the tile
+    const int4 near = reduce_halves(after, before, scratch);
+    run0 = max(near.y, near.w);
+    run1 = min(near.x, near.z);
+    // the nearest beginnings inside the block
     const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
 #pragma unroll
-    for (int x = 0; x < TILE / 32; ++x) {
+    for (int x = 0; x < WARPS; ++x) {
       const unsigned low = x < w ? bits[x] : (x == w ? bits[x] & (0xffffffffu >> (31 - l)) : 0u);
-      if (low != 0) run0 = max(run0, tile * TILE + 32 * x + 31 - __clz(low));
+      if (low != 0) run0 = max(run0, block * BLOCK + 32 * x + 31 - __clz(low));
     }
 #pragma unroll
-    for (int x = TILE / 32 - 1; x >= 0; --x) {
+    for (int x = WARPS - 1; x >= 0; --x) {
       const unsigned high = x > w ? bits[x] : (x == w && l < 31 ? bits[x] & (0xfffffffeu << l) : 0u);
-      if (high != 0) run1 = min(run1, tile * TILE + 32 * x + __ffs(high) - 1);
+      if (high != 0) run1 = min(run1, block * BLOCK + 32 * x + __ffs(high) - 1);
     }
     if (i < p.n_q && __ldg(ids + i) < 0) run0 = run1 = 0;  // no document
   }
   const int limit = p.key_lens != nullptr ? min(max(__ldg(p.key_lens + b), 0), p.n_k) : p.n_k;
   const int prefix = p.prefix_lens != nullptr ? min(max(__ldg(p.prefix_lens + b), 0), p.n_k) : 0;
+  const bool later_heavier = p.right >= 0;
   // (left and right are at most n_q + n_k, so nothing here leaves int)
-  if (tile < p.qt) {
+  if (block < p.qb) {
     int2 v = make_int2(0, 0);
     if (i < p.n_q) {
       const int lo = max(run0, p.left >= 0 ? i - p.left : 0);
@@ -148,10 +144,23 @@ __global__ void __launch_bounds__(TILE) attn_mask_plan_kernel(const MaskParams p
       if (lo < hi) v = make_int2(lo, hi);
       p.row_keys[static_cast<size_t>(b) * p.n_q + i] = v;
     }
-    const int4 s = summary(v, i < p.n_q, scratch);
-    if (threadIdx.x == 0) p.block_keys[static_cast<size_t>(b) * p.qt + tile] = s;
+    const int4 r = reduce_halves(v.x < v.y ? v.x : 0x7fffffff, v.y, scratch);
+    if (threadIdx.x == 0) {
+      QueryItem item;
+      item.b = b;
+      item.block = block;
+      item.first = max(r.y, r.w) > 0 ? min(r.x, r.z) : 0;
+      item.end[0] = r.y;
+      item.end[1] = r.w;
+      item.work = tiles_of(item.first, r.y) + tiles_of(item.first, r.w);
+      item.pad[0] = item.pad[1] = 0;
+      if (p.ordered)
+        p.query_items_in[blockIdx.x / blocks * p.qb + block] = item;
+      else
+        p.query_items[later_heavier ? (p.qb - 1 - block) * p.B + b : b * p.qb + block] = item;
+    }
   }
-  if (tile < p.kt) {
+  if (block < p.kb) {
     int2 v = make_int2(0, 0);
     if (i < p.n_k) {
       const int lo = max(run0, i < prefix || p.right < 0 ? 0 : max(i - p.right, 0));
@@ -159,9 +168,43 @@ __global__ void __launch_bounds__(TILE) attn_mask_plan_kernel(const MaskParams p
       if (lo < hi && i < limit) v = make_int2(lo, hi);
       p.key_rows[static_cast<size_t>(b) * p.n_k + i] = v;
     }
-    const int4 s = summary(v, i < p.n_k, scratch);
-    if (threadIdx.x == 0) p.tile_rows[static_cast<size_t>(b) * p.kt + tile] = s;
+    const int4 r = reduce_halves(v.x < v.y ? v.x : 0x7fffffff, v.y, scratch);
+    const int kt = (p.n_k + kMaskTile - 1) / kMaskTile, tile = 2 * block + threadIdx.x;
+    if (threadIdx.x < 2 && tile < kt) {
+      const int first = threadIdx.x == 0 ? r.x : r.z, end = threadIdx.x == 0 ? r.y : r.w;
+      KeyItem item;
+      item.b = b;
+      item.tile = tile;
+      item.first = end > 0 ? first / kMaskTile : 0;
+      item.count = tiles_of(first, end);
+      if (p.ordered)
+        p.key_items_in[b * kt + tile] = item;
+      else
+        p.key_items[later_heavier ? tile * p.B + b : b * kt + tile] = item;
+    }
   }
+}
+
+// The items by falling work, ties in index order.  grid.y: 0 the forward's, 1 the
+// backward's.
+__global__ void __launch_bounds__(BLOCK) attn_mask_order_kernel(const MaskParams p) {
+  __shared__ int work[kMostOrdered];
+  const bool keys = blockIdx.y == 1;
+  const int n = p.B * (keys ? (p.n_k + kMaskTile - 1) / kMaskTile : p.qb);
+  if (static_cast<int>(blockIdx.x) * BLOCK >= n) return;
+  grid_dependency_wait();  // the items
+  for (int e = threadIdx.x; e < n; e += BLOCK)
+    work[e] = keys ? p.key_items_in[e].count : p.query_items_in[e].work;
+  __syncthreads();
+  const int e = blockIdx.x * BLOCK + threadIdx.x;
+  if (e >= n) return;
+  const int mine = work[e];
+  int rank = 0;
+  for (int x = 0; x < n; ++x) rank += work[x] > mine || (work[x] == mine && x < e);
+  if (keys)
+    p.key_items[rank] = p.key_items_in[e];
+  else
+    p.query_items[rank] = p.query_items_in[e];
 }
 
 }  // namespace
@@ -169,19 +212,26 @@ __global__ void __launch_bounds__(TILE) attn_mask_plan_kernel(const MaskParams p
 MaskLayout mask_layout(int B, int n_q, int n_k) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   MaskLayout l;
-  const size_t qt = (static_cast<size_t>(n_q) + TILE - 1) / TILE,
-               kt = (static_cast<size_t>(n_k) + TILE - 1) / TILE;
+  const size_t qb = (static_cast<size_t>(n_q) + BLOCK - 1) / BLOCK,
+               kt = (static_cast<size_t>(n_k) + kMaskTile - 1) / kMaskTile;
+  const size_t queries = up(B * qb * sizeof(QueryItem)), keys = up(B * kt * sizeof(KeyItem));
+  // (the copy before ordering; larger plans are not ordered)
+  const bool room = B * qb <= kMostOrdered && B * kt <= kMostOrdered;
   size_t off = 256;  // the header
   l.row_keys = off;
   off += up(static_cast<size_t>(B) * n_q * sizeof(int2));
   l.key_rows = off;
   off += up(static_cast<size_t>(B) * n_k * sizeof(int2));
-  l.block_keys = off;
-  off += up(B * qt * sizeof(int4));
-  l.tile_rows = off;
-  off += up(B * kt * sizeof(int4));
+  l.query_items = off;
+  off += queries;
+  l.key_items = off;
+  off += keys;
+  l.query_items_in = off;
+  off += room ? queries : 0;
+  l.key_items_in = off;
+  off += room ? keys : 0;
   l.runs = off;
-  off += up(B * qt * sizeof(int2));
+  off += up(B * qb * sizeof(int2));
   l.bytes = off;
   return l;
 }
@@ -193,9 +243,16 @@ MaskPlan mask_plan_at(const void* plan, int B, int n_q, int n_k) {
   m.header = reinterpret_cast<const int4*>(base);
   m.row_keys = reinterpret_cast<const int2*>(base + l.row_keys);
   m.key_rows = reinterpret_cast<const int2*>(base + l.key_rows);
-  m.block_keys = reinterpret_cast<const int4*>(base + l.block_keys);
-  m.tile_rows = reinterpret_cast<const int4*>(base + l.tile_rows);
+  m.query_items = reinterpret_cast<const QueryItem*>(base + l.query_items);
+  m.key_items = reinterpret_cast<const KeyItem*>(base + l.key_items);
   return m;
+}
+
+bool mask_plan_ordered(const MaskProblem& pb) {
+  const long long qb = (static_cast<long long>(pb.n_q) + BLOCK - 1) / BLOCK,
+                  kt = (static_cast<long long>(pb.n_k) + kMaskTile - 1) / kMaskTile;
+  return pb.doc_ids != nullptr && pb.B * kt > 1 && pb.B * qb <= kMostOrdered &&
+         pb.B * kt <= kMostOrdered;
 }
 
 cudaError_t launch_mask_plan(const MaskProblem& pb, void* plan, const LaunchCtx& ctx) {
@@ -205,8 +262,10 @@ cudaError_t launch_mask_plan(const MaskProblem& pb, void* plan, const LaunchCtx&
   p.header = reinterpret_cast<int4*>(base);
   p.row_keys = reinterpret_cast<int2*>(base + l.row_keys);
   p.key_rows = reinterpret_cast<int2*>(base + l.key_rows);
-  p.block_keys = reinterpret_cast<int4*>(base + l.block_keys);
-  p.tile_rows = reinterpret_cast<int4*>(base + l.tile_rows);
+  p.query_items = reinterpret_cast<QueryItem*>(base + l.query_items);
+  p.key_items = reinterpret_cast<KeyItem*>(base + l.key_items);
+  p.query_items_in = reinterpret_cast<QueryItem*>(base + l.query_items_in);
+  p.key_items_in = reinterpret_cast<KeyItem*>(base + l.key_items_in);
   p.runs = reinterpret_cast<int2*>(base + l.runs);
   p.key_lens = pb.key_lens;
   p.doc_ids = pb.doc_ids;
@@ -216,17 +275,22 @@ cudaError_t launch_mask_plan(const MaskProblem& pb, void* plan, const LaunchCtx&
   p.n_k = pb.n_k;
   p.left = pb.left;
   p.right = pb.right;
-  p.qt = (pb.n_q + TILE - 1) / TILE;
-  p.kt = (pb.n_k + TILE - 1) / TILE;
-  const unsigned grid = static_cast<unsigned>(pb.B) * (p.qt > p.kt ? p.qt : p.kt);
+  p.qb = (pb.n_q + BLOCK - 1) / BLOCK;
+  p.kb = (pb.n_k + BLOCK - 1) / BLOCK;
+  p.ordered = mask_plan_ordered(pb) ? 1 : 0;
+  const unsigned grid = static_cast<unsigned>(pb.B) * (p.qb > p.kb ? p.qb : p.kb);
   if (pb.doc_ids == nullptr) {
-    attn_mask_plan_kernel<<<grid, TILE, 0, ctx.stream>>>(p);
+    attn_mask_plan_kernel<<<grid, BLOCK, 0, ctx.stream>>>(p);
     return cudaGetLastError();
   }
-  attn_mask_runs_kernel<<<static_cast<unsigned>(pb.B) * p.qt, TILE, 0, ctx.stream>>>(p);
+  attn_mask_runs_kernel<<<static_cast<unsigned>(pb.B) * p.qb, BLOCK, 0, ctx.stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(attn_mask_plan_kernel, dim3(grid), dim3(TILE), 0, ctx.stream, p);
+  e = launch_dependent(attn_mask_plan_kernel, dim3(grid), dim3(BLOCK), 0, ctx.stream, p);
+  if (e != cudaSuccess || !p.ordered) return e;
+  const int kt = (pb.n_k + kMaskTile - 1) / kMaskTile;
+  return launch_dependent(attn_mask_order_kernel, dim3((pb.B * kt + BLOCK - 1) / BLOCK, 2),
+                          dim3(BLOCK), 0, ctx.stream, p);
 }
 
 }  // namespace attn
