@@ -672,25 +672,32 @@ def _vector(name: str, t, dtype, count: int, device) -> None:
                          f"{device}")
 
 
-def _strides(*tensors):
-    """The (b, h, row) element strides of [B, h, n, d] views.  The stride of a
-    dimension of one entry is never stepped over, whatever the view says."""
+_INT64S = {n: ctypes.c_int64 * n for n in (12, 24)}
+
+
+def _strides_array(strides):
+    """A host array of element strides (None: contiguous tensors)."""
+    if strides is None or isinstance(strides, ctypes.Array):
+        return strides
+    return _INT64S[len(strides)](*strides)
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides_of(layouts):
     flat = []
-    for t in tensors:
-        step, shape = t.stride(), t.shape
+    for step, shape in layouts:
         if 1 in shape[:3]:
             room = -(-max(*step, shape[2] * shape[3]) // 16) * 16
             flat += [step[i] if shape[i] > 1 else room for i in range(3)]
         else:
             flat += step[:3]
-    return flat
+    return _strides_array(flat)
 
 
-_INT64S = {n: ctypes.c_int64 * n for n in (12, 24)}
-
-
-def _strides_array(strides):
-    return None if strides is None else _INT64S[len(strides)](*strides)
+def _strides(*tensors):
+    """The (b, h, row) element strides of [B, h, n, d] views.  The stride of a
+    dimension of one entry is never stepped over, whatever the view says."""
+    return _strides_of(tuple([(t.stride(), t.shape) for t in tensors]))
 
 
 def _workspace(need: int, given, device):
@@ -840,6 +847,12 @@ def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     return out, lse
 
 
+def _not_negative(name: str, x: int) -> int:
+    if x < 0:
+        raise ValueError(f"{name} must be >= 0 (None: unbounded)")
+    return x
+
+
 @functools.lru_cache(maxsize=256)
 def mask_plan_bytes(B: int, n_q: int, n_k: int) -> int:
     """Bytes of a mask plan for these sizes (0 for unsupported sizes)."""
@@ -862,23 +875,28 @@ def attn_mask_plan(B: int, n_q: int, n_k: int, left: int | None = None, right: i
     (None: unbounded; right=0 is causal) and, with prefix_lens [B], the first
     prefix_lens[b] keys; of them those below key_lens[b] and, with doc_ids
     [B, n], those of its own run of equal ids (negative: no document)."""
-    if device is None:
+    dev = device
+    if dev is None:
         given = [t for t in (key_lens, doc_ids, prefix_lens, plan) if t is not None]
-        device = given[0].device if given else "cuda"
-    dev = torch.device(device)
+        dev = given[0].device if given else torch.device("cuda")
+    elif not isinstance(dev, torch.device):
+        dev = torch.device(dev)
     if dev.type != "cuda":
         raise ValueError("a mask plan lives on a CUDA device")
     if dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    if (left is not None and left < 0) or (right is not None and right < 0):
-        raise ValueError("left and right must be >= 0 (None: unbounded)")
-    _vector("key_lens", key_lens, torch.int32, B, dev)
-    _vector("prefix_lens", prefix_lens, torch.int32, B, dev)
-    _vector("doc_ids", doc_ids, torch.int32, B * n_q, dev)
-    if doc_ids is not None and n_q != n_k:
-        raise ValueError("documents need n_q == n_k")
-    if prefix_lens is not None and left is not None:
-        raise ValueError("a prefix and a left bound leave a query two runs of keys")
+    left = -1 if left is None else _not_negative("left", left)
+    right = -1 if right is None else _not_negative("right", right)
+    if key_lens is not None:
+        _vector("key_lens", key_lens, torch.int32, B, dev)
+    if prefix_lens is not None:
+        _vector("prefix_lens", prefix_lens, torch.int32, B, dev)
+        if left >= 0:
+            raise ValueError("a prefix and a left bound leave a query two runs of keys")
+    if doc_ids is not None:
+        _vector("doc_ids", doc_ids, torch.int32, B * n_q, dev)
+        if n_q != n_k:
+            raise ValueError("documents need n_q == n_k")
     need = mask_plan_bytes(B, n_q, n_k)
     if plan is not None and (plan.device != dev or not plan.is_contiguous()
                              or _nbytes(plan) < need):
@@ -886,9 +904,8 @@ def attn_mask_plan(B: int, n_q: int, n_k: int, left: int | None = None, right: i
     with _call_on(dev, stream) as ptr:
         if plan is None:
             plan = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        rc = attn_mask_plan_raw(B, n_q, n_k, -1 if left is None else left,
-                                -1 if right is None else right, _ptr(key_lens), _ptr(doc_ids),
-                                _ptr(prefix_lens), _ptr(plan), _nbytes(plan), ptr)
+        rc = attn_mask_plan_raw(B, n_q, n_k, left, right, _ptr(key_lens), _ptr(doc_ids),
+                                _ptr(prefix_lens), plan.data_ptr(), _nbytes(plan), ptr)
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_mask_plan")
     return plan
