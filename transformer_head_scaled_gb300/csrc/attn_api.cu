@@ -825,7 +825,7 @@ bool int_ptr_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) ==
 // tile keys, 1, 1) box, with the 128-byte swizzle where box rows are 128 bytes;
 // strides in elements of `elem` bytes.
 int encode_4d_bytes(CUtensorMap* map, const void* base, int row_bytes, int n, int h, int B,
-                    Strides st, int elem) {
+                    Strides st, int elem, int box_rows) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(n),
                         static_cast<cuuint64_t>(h), static_cast<cuuint64_t>(B)};
   cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.n) * elem,
@@ -834,8 +834,7 @@ int encode_4d_bytes(CUtensorMap* map, const void* base, int row_bytes, int n, in
   const int inner = row_bytes < 128 ? row_bytes : 128;
   const CUtensorMapSwizzle swz =
       inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(inner),
-                       static_cast<cuuint32_t>(scored_decode_tile_keys(row_bytes)), 1u, 1u};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(inner), static_cast<cuuint32_t>(box_rows), 1u, 1u};
   cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
   CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
@@ -949,9 +948,11 @@ int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
       (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
     return ATTN_ERR_INVALID_ARG;
   CUtensorMap maps[2];
-  if ((rc = encode_4d_bytes(&maps[0], k_cache, d_k * e1, L_max, h_kv, B, st[1], e1)) != ATTN_OK)
+  if ((rc = encode_4d_bytes(&maps[0], k_cache, d_k * e1, L_max, h_kv, B, st[1], e1,
+                            plan.tile_keys)) != ATTN_OK)
     return rc;
-  if ((rc = encode_4d_bytes(&maps[1], v_cache, d_k * e1, L_max, h_kv, B, st[2], e1)) != ATTN_OK)
+  if ((rc = encode_4d_bytes(&maps[1], v_cache, d_k * e1, L_max, h_kv, B, st[2], e1,
+                            plan.tile_keys)) != ATTN_OK)
     return rc;
   ScoredDecodeProblem pb{q, k_cache, v_cache, k_scale, v_scale, o, lse, B, h, h_kv, n_q, L_max,
                          d_k, q8 ? block_tokens : 128, scale, softcap, slopes, cache_lens,
@@ -976,18 +977,26 @@ ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int
   const int rows = H / HK * n_q;
   plan.row_tile = rows <= 8 ? 8 : (rows <= 16 ? 16 : 32);
   plan.row_tiles = (rows + plan.row_tile - 1) / plan.row_tile;
-  const int kt = scored_decode_tile_keys(d * elem_bytes);
+  const int row_bytes = d * elem_bytes;
   const long long units = static_cast<long long>(B) * HK * plan.row_tiles;
-  const long long most = (seen + 15 + kt - 1) / kt;  // tiles of a unit; a window may start inside a group
-  const long long resident = static_cast<long long>(num_sms) * scored_decode_warps(plan.row_tile);
-  plan.whole = units * 2 >= resident && most <= 32;
+  auto tiles_of = [&](int kt) { return (seen + 2LL * kt - 2) / kt; };  // a window may start inside one
+  // whole units per warp when there are enough of them to occupy the SMs and the
+  // longest is at most 32 small tiles (about 20 us of one warp)
+  int kt = scored_decode_tile_keys(row_bytes, false);
+  const long long small = static_cast<long long>(num_sms) * scored_decode_warps(plan.row_tile, false);
+  plan.whole = units * 2 >= small && tiles_of(kt) <= 32;
+  plan.tile_keys = kt;
   if (plan.whole) {
-    plan.warps = static_cast<int>(units < resident ? units : resident);
+    plan.warps = static_cast<int>(units < small ? units : small);
     plan.part_off = plan.workspace_bytes = 0;
     return plan;
   }
   // every resident warp takes a share of the tiles, if there are that many
-  const long long useful = (units * most + scored_decode_min_tiles() - 1) / scored_decode_min_tiles();
+  const bool big = scored_decode_big(row_bytes, plan.row_tile, false);
+  plan.tile_keys = kt = scored_decode_tile_keys(row_bytes, big);
+  const long long resident = static_cast<long long>(num_sms) * scored_decode_warps(plan.row_tile, big);
+  const long long useful =
+      (units * tiles_of(kt) + scored_decode_min_tiles() - 1) / scored_decode_min_tiles();
   plan.warps = static_cast<int>(useful < resident ? useful : resident);
   // the sequences' first tiles, then two partial results per warp
   plan.part_off = (static_cast<size_t>(B) + 1 + 3) / 4 * 4;

@@ -148,29 +148,34 @@ __device__ __forceinline__ void load_bytes(const uint8_t* at, uint32_t* w) {
   }
 }
 
-// Keys per warp and tile for rows of `row_bytes`: 2 KB of keys, 16 to 64 of them.
-constexpr int scored_tile_keys(int row_bytes) {
-  return row_bytes >= 128 ? 16 : (row_bytes >= 64 ? 32 : 64);
+// Keys per warp and tile for rows of `row_bytes`: 2 KB of keys, 16 to 64 of
+// them; 4 KB where the work is split and one tile of query rows leaves the
+// registers for it (131072-token contexts 139 -> 132 us; whole short caches are
+// faster in small tiles, 27 against 31 us).
+constexpr bool scored_big_tiles(int row_bytes, int row_tiles, bool whole) {
+  return !whole && row_tiles == 1 && (row_bytes == 64 || row_bytes == 128);
 }
-
+constexpr int scored_tile_keys(int row_bytes, bool big) {
+  return (row_bytes >= 128 ? 16 : (row_bytes >= 64 ? 32 : 64)) * (big ? 2 : 1);
+}
 // Resident CTAs per SM that the registers allow, by row tiles.
-constexpr int scored_ctas(int row_tiles) { return row_tiles > 1 ? 2 : 4; }
+constexpr int scored_ctas(int row_tiles, bool big) { return row_tiles > 1 ? 2 : (big ? 3 : 4); }
 // A warp's run is at least this many tiles: below it the start of a run and the
 // join of its result cost more than the tiles.
 constexpr int kMinTiles = 2;
 
 // Shapes per cache format, head size D and row tiles (8 queries each).
-template <int FMT_, int D_, int NR_>
+template <int FMT_, int D_, int NR_, bool BIG_>
 struct DCfg {
   static constexpr int FMT = FMT_, D = D_, NR = NR_;
   static constexpr int ES = FMT_ == kCacheBf16 ? 2 : 1;
   static constexpr int RB = D_ * ES;               // bytes of a cache row
   static constexpr int BB = RB < 128 ? RB : 128;   // bytes of a row in one TMA box
   static constexpr int NB = RB / BB;               // boxes per tile
-  static constexpr int KT = scored_tile_keys(RB);
+  static constexpr int KT = scored_tile_keys(RB, BIG_);
   static constexpr uint32_t TILE = KT * RB;        // a tile of keys (or of values)
   static constexpr uint32_t BOX = KT * BB;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = BIG_ ? 2 : 3;
   static constexpr int NT = KT / 8;   // 8-key column tiles of S
   static constexpr int NG = KT / 16;  // 16-key groups (one k step of O^T)
   // K: a lane's quarter of a row, in loads of KV bytes
@@ -187,7 +192,7 @@ struct DCfg {
   static constexpr int MT = D_ / 16;                // 16-row tiles of O^T
   static constexpr int MQ = NR_ > 1 ? NR_ / 2 : 1;  // 16-query tiles of S
   static constexpr uint32_t RING = STAGES * 2 * TILE;  // shared memory of a warp
-  static constexpr int CTAS = scored_ctas(NR_);
+  static constexpr int CTAS = scored_ctas(NR_, BIG_);
   // Rows shorter than 128 bytes whose cache rows lie side by side are copied as
   // one run of bytes: a tiled copy takes about four cycles of the SM's copy
   // engine per box row, which for 64-byte rows is the time of 16 bytes a cycle,
@@ -220,8 +225,8 @@ __device__ __forceinline__ int val_elem(int e, int g) {
 struct SeqTiles {
   int L;      // tokens in the cache
   int key0;   // first key that any of the queries sees
-  int base0;  // where its tiles begin: a 16-key boundary, so that no 16-key group
-              // crosses a scale block
+  int base0;  // where its tiles begin: a tile boundary, so that no tile (or no 16-key
+              // group of it) crosses a scale block
   int tiles;
 };
 template <int KT>
@@ -230,7 +235,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const ScoredDecParams& p, int b) {
   s.L = p.L_max;
   if (p.cache_lens != nullptr) s.L = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
   s.key0 = p.window >= 0 ? max(s.L - p.n_q - p.window, 0) : 0;
-  s.base0 = s.key0 & ~15;
+  s.base0 = s.key0 & ~(KT - 1);
   s.tiles = (s.L - s.base0 + KT - 1) / KT;
   return s;
 }
@@ -270,11 +275,11 @@ __device__ __forceinline__ unsigned share_of(unsigned total, int warps) {
   return each < kMinTiles ? kMinTiles : each;
 }
 
-template <int FMT, int D, int NR>
-__global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
+template <int FMT, int D, int NR, bool BIG>
+__global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
     attn_decode_scored_kernel(const __grid_constant__ CUtensorMap tmk,
                               const __grid_constant__ CUtensorMap tmv, const ScoredDecParams p) {
-  using C = DCfg<FMT, D, NR>;
+  using C = DCfg<FMT, D, NR, BIG>;
   constexpr int KT = C::KT, NT = C::NT, NG = C::NG, MQ = C::MQ;
   constexpr bool Q8 = FMT != kCacheBf16;
   constexpr int ROWS = NR * 8;
@@ -424,17 +429,17 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR>::CTAS)
   const long long bk = static_cast<long long>(b) * p.HK + hk;
   const float* ksp = Q8 ? p.k_scale + bk * p.num_blocks : nullptr;
   const float* vsp = Q8 ? p.v_scale + bk * p.num_blocks : nullptr;
-  // one scale per 16-key group; a tile that lies in one block reads it once
-  const bool one_block = (1 << p.T_log2) >= KT && (base0 & (KT - 1)) == 0;
+  // one scale per 16-key group; where blocks are no smaller than tiles, one per tile
+  const bool one_block = (1 << p.T_log2) >= KT;
   auto load_scales = [&](const float* from, int base, float (&to)[NG]) {
+    to[0] = __ldg(from + (base >> p.T_log2));
     if (one_block) {
-      const float x = __ldg(from + (base >> p.T_log2));
 #pragma unroll
-      for (int n = 0; n < NG; ++n) to[n] = x;
+      for (int n = 1; n < NG; ++n) to[n] = to[0];
     } else {
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
-        to[n] = base + 16 * n < L ? __ldg(from + ((base + 16 * n) >> p.T_log2)) : 0.f;
+      for (int n = 1; n < NG; ++n)
+        to[n] = __ldg(from + (min(base + 16 * n, L - 1) >> p.T_log2));
     }
   };
   float ks[NG], vs[NG];
@@ -902,11 +907,11 @@ __global__ void __launch_bounds__(256)
         ll > 0.f ? (mm + __log2f(ll)) * kLn2 : -INFINITY;
 }
 
-template <int FMT, int D, int NR>
+template <int FMT, int D, int NR, bool BIG>
 cudaError_t launch_scored_decode_rows(const ScoredDecParams& p, const CUtensorMap* maps,
                                       const LaunchCtx& ctx) {
-  const size_t smem = DW * DCfg<FMT, D, NR>::RING + 1024;
-  auto* kernel = attn_decode_scored_kernel<FMT, D, NR>;
+  const size_t smem = DW * DCfg<FMT, D, NR, BIG>::RING + 1024;
+  auto* kernel = attn_decode_scored_kernel<FMT, D, NR, BIG>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
@@ -925,10 +930,15 @@ cudaError_t launch_scored_decode_rows(const ScoredDecParams& p, const CUtensorMa
 template <int FMT, int D>
 cudaError_t launch_scored_decode_d(const ScoredDecParams& p, const CUtensorMap* maps, int row_tile,
                                    const LaunchCtx& ctx) {
+  constexpr int rb = D * (FMT == kCacheBf16 ? 2 : 1);
   switch (row_tile) {
-    case 8: return launch_scored_decode_rows<FMT, D, 1>(p, maps, ctx);
-    case 16: return launch_scored_decode_rows<FMT, D, 2>(p, maps, ctx);
-    default: return launch_scored_decode_rows<FMT, D, 4>(p, maps, ctx);
+    case 8:
+      if constexpr (scored_big_tiles(rb, 1, false)) {
+        if (!p.whole) return launch_scored_decode_rows<FMT, D, 1, true>(p, maps, ctx);
+      }
+      return launch_scored_decode_rows<FMT, D, 1, false>(p, maps, ctx);
+    case 16: return launch_scored_decode_rows<FMT, D, 2, false>(p, maps, ctx);
+    default: return launch_scored_decode_rows<FMT, D, 4, false>(p, maps, ctx);
   }
 }
 

@@ -264,14 +264,17 @@ struct ScoredDecodeProblem {
 struct ScoredDecodePlan {
   int row_tile, row_tiles;  // query rows of one key head per CTA, and how many such tiles
   bool whole;  // a warp takes whole units (sequence, key head, row tile)
+  int tile_keys;
   int warps;   // that share the units, or the list of their tiles
   size_t part_off;  // floats before the partial results in the workspace
   size_t workspace_bytes;
 };
-// The kernel's shapes: keys of one tile, for cache rows of `row_bytes`; resident
-// warps per SM and least tiles per warp, for `row_tile` query rows.
-int scored_decode_tile_keys(int row_bytes);
-int scored_decode_warps(int row_tile);
+// The kernel's shapes, for cache rows of `row_bytes` and `row_tile` query rows:
+// whether it uses big tiles, keys of one tile, resident warps per SM, least
+// tiles per warp.
+bool scored_decode_big(int row_bytes, int row_tile, bool whole);
+int scored_decode_tile_keys(int row_bytes, bool big);
+int scored_decode_warps(int row_tile, bool big);
 int scored_decode_min_tiles();
 // maps[0..1]: the key and the value cache as 4-D (row bytes, L_max, HK, B) byte
 // tensors with a (min(row bytes, 128), tile keys, 1, 1) box, with the 128-byte
