@@ -130,6 +130,9 @@ def test_decode_scored_ignores_what_lies_before_the_window(dtype):
     kc, ks, k = _cache(B, h, L, d, dtype, block, 2)
     vc, vs, v = _cache(B, h, L, d, dtype, block, 4)
     first = L - 1 - window
+    if ks is not None:   # nor the scales of the blocks before it
+        ks[:, :, :first // block] = float("inf")
+        vs[:, :, :first // block] = float("nan")
     for c in (kc, vc):
         c[:, :, :first] = float("nan") if dtype == BF16 else torch.full(
             (), 0x7f, dtype=torch.uint8, device="cuda").view(dtype)
@@ -171,6 +174,19 @@ def test_decode_scored_tiny_values_and_equal_scales_of_zero():
     got = binding.attn_decode_scored(torch.zeros_like(q), kc, vc, k_scale=ks, v_scale=vs,
                                      block_tokens=block)
     _check(got, torch.zeros_like(q), k, v, [L], 0.125, 0.0, None, None, INT8)
+
+
+@pytest.mark.parametrize("cap", [1e-6, 0.01, 1.0, 300.0, 1e6])
+@pytest.mark.parametrize("dtype", [E4M3, BF16], ids=["e4m3", "bf16"])
+def test_decode_scored_caps_from_tiny_to_idle(dtype, cap):
+    B, h, L, d, block = 2, 2, 200, 64, 32
+    q = _random((B, h, 1, d), 1, 2.0).to(BF16)
+    kc, ks, k = _cache(B, h, L, d, dtype, block, 2)
+    vc, vs, v = _cache(B, h, L, d, dtype, block, 4)
+    got = binding.attn_decode_scored(q, kc, vc, k_scale=ks, v_scale=vs, block_tokens=block,
+                                     softcap=cap)
+    binding.check()
+    _check(got, q, k, v, [L] * B, 0.125, cap, None, None, dtype)
 
 
 def test_decode_scored_reads_past_32_bit_offsets():

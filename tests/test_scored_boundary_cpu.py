@@ -69,7 +69,7 @@ def test_decode_scored_arguments_rejected_on_host(lib):
     assert call(window=-2) == INV
     for bad in (0.0, -1.0, math.nan, math.inf):
         assert call(scale=bad) == INV
-    for bad in (-1.0, math.nan, math.inf):
+    for bad in (-1.0, math.nan, math.inf, 1e-40):
         assert call(cap=bad) == INV
     for at in range(12):
         s = [64] * 12
@@ -112,7 +112,7 @@ def _scored_refusals(call, tensors, strides):
     assert call(slopes=A + 2) == INV and call(lse=A + 2) == INV
     for bad in (0.0, -1.0, math.nan, math.inf):
         assert call(scale=bad) == INV
-    for bad in (-1.0, math.nan, math.inf):
+    for bad in (-1.0, math.nan, math.inf, 1e-40):
         assert call(cap=bad) == INV
     assert call(plan=A + 8) == INV
     assert call(plan=A, plan_bytes=100) == INV    # too small for these sizes

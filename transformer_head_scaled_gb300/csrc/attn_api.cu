@@ -819,6 +819,12 @@ bool read_strides(Strides* st, const int64_t* in, int count, const int* heads, c
   return true;
 }
 
+// 0 (none), or large enough that the tanh's argument per unit of q.k is finite.
+bool softcap_ok(float softcap, float scale) {
+  return std::isfinite(softcap) && softcap >= 0.f &&
+         (softcap == 0.f || std::isfinite(4.f * scale / softcap));
+}
+
 bool int_ptr_ok(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A cache as 4-D (row bytes, L_max, h, B) bytes with a (min(row bytes, 128),
@@ -930,7 +936,7 @@ int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
   int rc = scored_decode_sizes(B, h, h_kv, n_q, L_max, d_k, cache_format, window);
   if (rc == ATTN_ERR_INVALID_ARG) return rc;
   if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID_ARG;
-  if (!(std::isfinite(softcap) && softcap >= 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (!softcap_ok(softcap, scale)) return ATTN_ERR_INVALID_ARG;
   const bool q8 = cache_format != ATTN_CACHE_BF16;
   if (q8 && (!k_scale || !v_scale || !block_tokens_ok(block_tokens))) return ATTN_ERR_INVALID_ARG;
   const int e1 = elem_bytes(cache_format);
@@ -1027,7 +1033,7 @@ int check_scored(const void* q, const void* k, const void* v, const void* o, con
   int rc = check_common(q, k, v, o, lse, B, h, n_q, n_k, d_k, scale, ATTN_MASK_NONE, nullptr, 2);
   if (rc != ATTN_OK) return rc;
   if (h_kv < 1 || h % h_kv != 0) return ATTN_ERR_INVALID_ARG;
-  if (!(std::isfinite(softcap) && softcap >= 0.f) || !int_ptr_ok(slopes))
+  if (!softcap_ok(softcap, scale) || !int_ptr_ok(slopes))
     return ATTN_ERR_INVALID_ARG;
   if ((rc = check_mask_sizes(B, n_q, n_k)) != ATTN_OK) return rc;
   // one work item per 256 queries, or per 128 keys, of a head

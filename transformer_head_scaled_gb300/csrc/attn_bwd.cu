@@ -158,6 +158,7 @@ struct Params {
   float cap_log2;         // softcap * log2(e); 0: no cap
   float cap_in;           // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
   const float* slopes;    // distance bias per query head, or null
+  CapPoly cap;            // kWide
   const float* lse_log2;  // with a cap: [B * H][num_qt * 128]
   bool masked;
   MaskPlan plan;
@@ -344,10 +345,11 @@ __device__ __forceinline__ uint64_t sdesc_swz(uint32_t smem_addr, uint32_t lbo_b
 //
 // With a cap, from r = 1 / (1 + 2^(2 y log2(e))): tanh(y) = 1 - 2 r, 1 -
 // tanh^2(y) = 4 r (1 - r).  LSE comes off after the tanh, from shared memory (it
-// is a constant of the column, not of the thread).  (Polynomials for small
-// arguments, as in the forward, were slower here: registers bound this loop, not
-// the special-function unit.)
-template <int MODE, bool SLOW, class Emit>
+// is a constant of the column, not of the thread).  POLY: small arguments under a
+// wide cap, by the polynomials of CapPoly.  (Under the usual caps these are slower
+// here, 487 against 403 us on packed documents of 4 x 4096 tokens: registers bound
+// this loop, not the special-function unit.)
+template <int MODE, bool SLOW, bool POLY, class Emit>
 __device__ __forceinline__ void scored_probabilities(const Params& p, const uint32_t (&s0)[32],
                                                      const uint32_t (&s1)[32], float (&pf)[64],
                                                      int lim, int hi, float bias, float ahead,
@@ -359,7 +361,17 @@ __device__ __forceinline__ void scored_probabilities(const Params& p, const uint
   for (int c0 = 0; c0 < 64; c0 += 8) {
     const uint32_t* src = c0 < 32 ? s0 + c0 : s1 + (c0 - 32);
     float x[8];
-    if constexpr (CAP) {
+    if constexpr (CAP && POLY) {
+      const float4 l0 = *reinterpret_cast<const float4*>(lse + c0),
+                   l1 = *reinterpret_cast<const float4*>(lse + c0 + 4);
+      const float ln[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a = __uint_as_float(src[e]), z = a * a;
+        x[e] = fmaf(a, fmaf(z, fmaf(z, p.cap.poly[2], p.cap.poly[1]), p.cap.poly[0]), bias - ln[e]);
+        pf[c0 + e] = fmaf(z, fmaf(z, p.cap.slope[2], p.cap.slope[1]), p.cap.slope[0]);
+      }
+    } else if constexpr (CAP) {
       float r[8];
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
@@ -933,12 +945,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             tmem_st4(tPT + i, a0, a1, a2, a3);
           };
-          if (slow)
-            scored_probabilities<MODE, true>(p, s0, s1, pf, lim, hi, bias,
-                                             static_cast<float>(ahead), f, lse, emit);
+          const float fahead = static_cast<float>(ahead);
+          bool poly = false;
+          if constexpr ((MODE & kWide) != 0) {
+            float big = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              big = max3(big, fabsf(__uint_as_float(s0[e])), fabsf(__uint_as_float(s1[e])));
+            poly = __all_sync(0xffffffffu, big <= p.cap.small);
+            if (poly)
+              scored_probabilities<MODE, true, true>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
+                                                     emit);
+          }
+          if ((MODE & kWide) != 0 && poly)
+            ;  // done
+          else if (slow)
+            scored_probabilities<MODE, true, false>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
+                                                    emit);
           else
-            scored_probabilities<MODE, false>(p, s0, s1, pf, lim, hi, bias,
-                                              static_cast<float>(ahead), f, lse, emit);
+            scored_probabilities<MODE, false, false>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
+                                                     emit);
           if (!ok) break;
         } else {
 #pragma unroll
@@ -1289,11 +1315,15 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
     p.cap_log2 = mod->softcap * LOG2E;
     p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
     p.slopes = mod->slopes;
+    p.cap = cap_poly(pb.scale, mod->softcap);
     p.lse_log2 = lse_log2;
     p.masked = mod->masked;
     p.plan = mod->plan;
     const bool cap = mod->softcap > 0.f, bias = mod->slopes != nullptr;
-    err = cap && bias ? launch_bwd_main<kScored | kCap | kBias, D>(p, maps, ctx)
+    const bool wide = mod->softcap > kWideCap;
+    err = wide && bias  ? launch_bwd_main<kScored | kCap | kWide | kBias, D>(p, maps, ctx)
+          : wide        ? launch_bwd_main<kScored | kCap | kWide, D>(p, maps, ctx)
+          : cap && bias ? launch_bwd_main<kScored | kCap | kBias, D>(p, maps, ctx)
           : cap       ? launch_bwd_main<kScored | kCap, D>(p, maps, ctx)
           : bias      ? launch_bwd_main<kScored | kBias, D>(p, maps, ctx)
                       : launch_bwd_main<kScored, D>(p, maps, ctx);

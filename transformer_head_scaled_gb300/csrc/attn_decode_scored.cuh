@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   // this lane's rows of an 8-key tile: one as a key, two (a column pair) as values
   const int krow = C::key_of(g), vrow0 = C::key_of(2 * t), vrow1 = C::key_of(2 * t + 1);
   const bool capped = p.softcap > 0.f, biased = p.slopes != nullptr;
+  const bool wide_cap = p.softcap > kWideCap;
   const float cap2 = p.softcap * kLog2e;
   // a product times this is the score in log2 units, or the cap's exponent
   const float unit_scale = p.scale * kLog2e * (capped ? 2.f / p.softcap : 1.f);
@@ -432,14 +433,15 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   // one scale per 16-key group; where blocks are no smaller than tiles, one per tile
   const bool one_block = (1 << p.T_log2) >= KT;
   auto load_scales = [&](const float* from, int base, float (&to)[NG]) {
-    to[0] = __ldg(from + (base >> p.T_log2));
+    // (never a block outside the visible keys: its scale may be anything)
+    to[0] = __ldg(from + (max(base, key0) >> p.T_log2));
     if (one_block) {
 #pragma unroll
       for (int n = 1; n < NG; ++n) to[n] = to[0];
     } else {
 #pragma unroll
       for (int n = 1; n < NG; ++n)
-        to[n] = __ldg(from + (min(base + 16 * n, L - 1) >> p.T_log2));
+        to[n] = __ldg(from + (max(min(base + 16 * n, L - 1), key0) >> p.T_log2));
     }
   };
   float ks[NG], vs[NG];
@@ -582,8 +584,17 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                s[m][n][2 * r + c] = fmaf(-2.f * cap2, rcp(1.f + ex2(s[m][n][2 * r + c])), cap2);
+              for (int c = 0; c < 2; ++c) {
+                // (a in exponent units: y = a / (2 log2(e)))
+                const float a = s[m][n][2 * r + c];
+                float x = fmaf(-2.f * cap2, rcp(1.f + ex2(a)), cap2);
+                if (wide_cap && fabsf(a) <= 2.f * kLog2e * static_cast<float>(kTanhSmall)) {
+                  const float y = a * (0.5f / kLog2e), z = y * y;
+                  x = cap2 * y * fmaf(z, fmaf(z, static_cast<float>(kTanh2), static_cast<float>(kTanh1)),
+                                      static_cast<float>(kTanh0));
+                }
+                s[m][n][2 * r + c] = x;
+              }
           }
           if (biased) {
 #pragma unroll

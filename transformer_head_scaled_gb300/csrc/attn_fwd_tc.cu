@@ -117,28 +117,6 @@ struct __align__(1024) Smem {
   alignas(128) uint8_t slope[QT][MODE & kBias ? 128 : 16];
 };
 
-// tanh for small arguments: y (kTanh[0] + kTanh[1] y^2 + kTanh[2] y^4), within
-// 1.8e-7 of it for |y| <= kTanhSmall (a least-maximum fit over that interval,
-// made for this file).  Scores seldom reach 0.3 of a cap, and then a tile needs
-// no second exponential and no reciprocal per score.
-constexpr double kTanhSmall = 0.3;
-constexpr double kTanh[3] = {0.99999601, -0.3329748, 0.12522591};
-
-// The cap in units of q.k (x) and log2: softcap * log2(e) * tanh(scale * x /
-// softcap) = x (poly[0] + poly[1] x^2 + poly[2] x^4) for |x| <= small.
-struct CapPoly {
-  float small, poly[3];
-};
-CapPoly cap_poly(float scale, float softcap) {
-  CapPoly c{};
-  if (!(softcap > 0.f)) return c;
-  const double k = static_cast<double>(scale) / softcap;
-  c.small = static_cast<float>(kTanhSmall / k);
-  double f = scale * 1.4426950408889634;
-  for (int i = 0; i < 3; ++i, f *= k * k) c.poly[i] = static_cast<float>(kTanh[i] * f);
-  return c;
-}
-
 struct Params {
   __nv_bfloat16* o;
   float* lse;

@@ -75,9 +75,9 @@ struct ScoreMod {
 
 // Instantiations of the tensor-core kernels: the masks given by lengths (none,
 // causal, key padding), the restricted window, and changed scores under a mask
-// plan, with a cap and a distance bias or without; each keeps its code out of
-// the others'.
-enum Mode : int { kPlain = 0, kBand = 1, kScored = 2, kCap = 4, kBias = 8 };
+// plan, with a cap (kWide: the backward's for caps above kWideCap) and a distance
+// bias or without; each keeps its code out of the others'.
+enum Mode : int { kPlain = 0, kBand = 1, kScored = 2, kCap = 4, kBias = 8, kWide = 16 };
 
 // One forward problem, device pointers, [B, H, n, d] contiguous.
 struct Problem {
@@ -96,6 +96,41 @@ struct Problem {
 bool mask_plan_ordered(const MaskProblem& pb);
 struct LaunchCtx;
 cudaError_t launch_mask_plan(const MaskProblem& pb, void* plan, const LaunchCtx& ctx);
+
+// tanh for small arguments: y (kTanh0 + kTanh1 y^2 + kTanh2 y^4), within
+// 1.8e-7 of it for |y| <= kTanhSmall, and its derivative kSech0 + kSech1 y^2 +
+// kSech2 y^4, within 8e-6 (least-maximum fits over that interval, made for
+// this library).  Scores seldom reach 0.3 of a cap, and then need no second
+// exponential and no reciprocal.
+constexpr double kTanhSmall = 0.3;
+constexpr double kTanh0 = 0.99999601, kTanh1 = -0.3329748, kTanh2 = 0.12522591;
+constexpr double kSech0 = 0.99999215, kSech1 = -0.99840603, kSech2 = 0.61841958;
+// The general form, cap - 2 cap / (1 + e^2y), errs by up to 3e-7 of the cap: above
+// this cap that is more than 1e-4 of a score, and small arguments have to take
+// the polynomial.
+constexpr float kWideCap = 256.f;
+
+// The cap in units of q.k (x) and log2: softcap * log2(e) * tanh(scale * x /
+// softcap) = x (poly[0] + poly[1] x^2 + poly[2] x^4) for |x| <= small, and the
+// derivative of tanh likewise.
+struct CapPoly {
+  float small, poly[3], slope[3];
+};
+inline CapPoly cap_poly(float scale, float softcap) {
+  CapPoly c{};
+  c.small = -1.f;
+  if (!(softcap > 0.f)) return c;
+  const double k = static_cast<double>(scale) / softcap;
+  const double tanh_of[3] = {kTanh0, kTanh1, kTanh2}, sech_of[3] = {kSech0, kSech1, kSech2};
+  double f = 1.0;
+  for (int i = 0; i < 3; ++i, f *= k * k) {
+    c.poly[i] = static_cast<float>(tanh_of[i] * f * scale * 1.4426950408889634);
+    c.slope[i] = static_cast<float>(sech_of[i] * f);
+  }
+  // (a cap so small that the coefficients overflow is left to the general form)
+  if (f < 1e30) c.small = static_cast<float>(kTanhSmall / k);
+  return c;
+}
 
 // Launch context shared by every launcher.
 struct LaunchCtx {
