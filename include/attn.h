@@ -316,18 +316,21 @@ int attn_fwd_scored(const void* q, const void* k, const void* v, void* o, float*
  *   dV = P^T dO,  dP = dO V^T,  D_i = sum_c dO[i,c] O[i,c],
  *   dS = P * (dP - D_i) * (1 - tanh^2(s / softcap)),
  *   dQ = scale dS K,  dK = scale dS^T Q,
- * dK and dV summed over the query heads that share a key head (inside one
- * accumulator, in head order).  The slopes are constants: they get no gradient.
+ * dK and dV summed over the query heads that share a key head, in fp32 and in
+ * head order.  The slopes are constants: they get no gradient.
  *   strides  : host array of 24 element counts, three (b, h, row) per tensor in
  *              the order q, k, v, o, dout, dq, dk, dv (k, v, dk, dv have h_kv
  *              heads), each > 0 and a multiple of 8; NULL: contiguous.
  *   workspace, workspace_bytes : at least attn_bwd_scored_workspace_bytes(B, h,
- *              n_q, d_k) bytes, 16-byte aligned; contents on entry do not matter.
+ *              h_kv, n_q, n_k, d_k) bytes, 16-byte aligned; contents on entry do
+ *              not matter.
  * d_k in {16, 32, 64} (else ATTN_ERR_UNSUPPORTED).  Queries that see no key get
  * dq = 0, keys that no query sees dk = dv = 0.  dq, dk, dv must not overlap the
  * inputs; dout must be finite, in rows that see no key too.  dQ is summed over
  * key tiles in fp32 in the order in which they finish.  Other arguments,
- * roundings and status codes as attn_bwd and attn_fwd_scored.  Three kernels.
+ * roundings and status codes as attn_bwd and attn_fwd_scored.  Three kernels, a
+ * fourth where few key tiles make it worth to work on a key head's query heads
+ * apart.
  */
 int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout,
                     const float* lse, void* dq, void* dk, void* dv, int B, int h, int h_kv,
@@ -336,7 +339,7 @@ int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, 
                     size_t workspace_bytes, struct CUstream_st* stream);
 
 /* Scratch bytes attn_bwd_scored needs (0 for unsupported sizes). */
-size_t attn_bwd_scored_workspace_bytes(int B, int h, int n_q, int d_k);
+size_t attn_bwd_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int n_k, int d_k);
 
 /* What the rows of a key/value cache hold. */
 typedef enum {

@@ -142,9 +142,10 @@ def test_bwd_scored_arguments_rejected_on_host(lib):
                                            ws_bytes, None)
     _scored_refusals(call, ("q", "k", "v", "o", "dout", "dq", "dk", "dv", "ws"), 24)
     assert call(lse=None) == INV
-    assert call(ws_bytes=lib.attn_bwd_scored_workspace_bytes(1, 2, 8, 64) - 1) == INV
+    assert call(ws_bytes=lib.attn_bwd_scored_workspace_bytes(1, 2, 1, 8, 8, 64) - 1) == INV
     assert call(d=128) == UNS
-    assert lib.attn_bwd_scored_workspace_bytes(1, 2, 8, 128) == 0
+    assert lib.attn_bwd_scored_workspace_bytes(1, 2, 1, 8, 8, 128) == 0
+    assert lib.attn_bwd_scored_workspace_bytes(1, 3, 2, 8, 8, 64) == 0
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_types():

@@ -130,7 +130,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                                ctypes.c_size_t, vp,
                                                                ctypes.c_size_t, vp]
         lib.attn_bwd_scored_workspace_bytes.restype = ctypes.c_size_t
-        lib.attn_bwd_scored_workspace_bytes.argtypes = [i32] * 4
+        lib.attn_bwd_scored_workspace_bytes.argtypes = [i32] * 6
         lib.attn_check.restype = i32
         lib.attn_check.argtypes = [vp]
         lib.attn_status_string.restype = ctypes.c_char_p
@@ -966,9 +966,9 @@ def attn_fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 
 
 @functools.lru_cache(maxsize=256)
-def bwd_scored_workspace_bytes(B: int, h: int, n_q: int, d: int = 64) -> int:
+def bwd_scored_workspace_bytes(B: int, h: int, h_kv: int, n_q: int, n_k: int, d: int = 64) -> int:
     """Scratch bytes attn_bwd_scored needs (0 for unsupported sizes)."""
-    return int(load().attn_bwd_scored_workspace_bytes(B, h, n_q, d))
+    return int(load().attn_bwd_scored_workspace_bytes(B, h, h_kv, n_q, n_k, d))
 
 
 def attn_bwd_scored_raw(q_ptr, k_ptr, v_ptr, o_ptr, dout_ptr, lse_ptr, dq_ptr, dk_ptr, dv_ptr, B, h,
@@ -1012,7 +1012,7 @@ def attn_bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
             dk = torch.empty((B, h_kv, n_k, d), dtype=q.dtype, device=dev)
         if dv is None:
             dv = torch.empty((B, h_kv, n_k, d), dtype=q.dtype, device=dev)
-        workspace = _workspace(max(bwd_scored_workspace_bytes(B, h, n_q, d), 16), workspace, dev)
+        workspace = _workspace(max(bwd_scored_workspace_bytes(B, h, h_kv, n_q, n_k, d), 16), workspace, dev)
         rc = attn_bwd_scored_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
                                  _ptr(dq), _ptr(dk), _ptr(dv), B, h, h_kv, n_q, n_k, d,
                                  _strides(q, k, v, o, dout, dq, dk, dv), scale, softcap,

@@ -661,7 +661,7 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* o, 
   const Strides sq = st ? st[0] : rq, sk = st ? st[1] : rk, sv = st ? st[2] : rk,
                 so = st ? st[3] : rq, sdo = st ? st[4] : rq, sdq = st ? st[5] : rq,
                 sdk = st ? st[6] : rk, sdv = st ? st[7] : rk;
-  CUtensorMap maps[7];
+  CUtensorMap maps[8];
   if ((rc = encode_4d(&maps[0], q, d_k, n_q, h, B, sq, 128)) != ATTN_OK) return rc;
   if ((rc = encode_4d(&maps[1], k, d_k, n_k, h, B, sk, 128)) != ATTN_OK) return rc;
   if ((rc = encode_4d(&maps[2], v, d_k, n_k, h, B, sv, 128)) != ATTN_OK) return rc;
@@ -671,6 +671,7 @@ static int bwd_impl(const void* q, const void* k, const void* v, const void* o, 
   if ((rc = encode_3d_f32(&maps[6], static_cast<uint8_t*>(workspace) + lay.dq_acc_off, d_k, n_q,
                           bh)) != ATTN_OK)
     return rc;
+  maps[7] = maps[6];  // used with changed scores only
   const int reach = n_q + n_k;
   BwdProblem pb{q, k, v, o, dout, lse, dq, dk, dv, B, h, n_q, n_k, d_k, scale, mask_kind,
                 mask_kind == ATTN_MASK_KEY_PADDING ? key_lens : nullptr,
@@ -1046,7 +1047,7 @@ int check_scored(const void* q, const void* k, const void* v, const void* o, con
 
 ScoreMod score_mod(float softcap, const float* slopes, int h, int h_kv, const void* plan, int B,
                    int n_q, int n_k, const Strides* st) {
-  ScoreMod mod{softcap, slopes, h / h_kv, {}, plan != nullptr, st[0], st[1], st[2]};
+  ScoreMod mod{softcap, slopes, h / h_kv, {}, plan != nullptr, st[0], st[1], st[2], {}, {}, 1};
   if (plan != nullptr) mod.plan = mask_plan_at(plan, B, n_q, n_k);
   return mod;
 }
@@ -1117,10 +1118,11 @@ int attn_fwd_scored(const void* q, const void* k, const void* v, void* o, float*
   return ATTN_OK;
 }
 
-size_t attn_bwd_scored_workspace_bytes(int B, int h, int n_q, int d_k) {
-  if (B < 1 || h < 1 || n_q < 1 || !bwd_head_size_ok(d_k)) return 0;
-  if (static_cast<long long>(B) * h > 0x7fffffffLL) return 0;
-  return bwd_layout(B, h, n_q, d_k).scored_bytes;
+size_t attn_bwd_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int n_k, int d_k) {
+  if (h < 1 || h_kv < 1 || h % h_kv != 0 || check_mask_sizes(B, n_q, n_k) != ATTN_OK ||
+      !bwd_head_size_ok(d_k) || static_cast<long long>(B) * h > 0x7fffffffLL)
+    return 0;
+  return bwd_scored_layout(B, h, h_kv, n_q, n_k, d_k).scored_bytes;
 }
 
 int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout,
@@ -1141,11 +1143,13 @@ int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, 
             rows[8] = {n_q, n_k, n_k, n_q, n_q, n_q, n_k, n_k}, elem[8] = {2, 2, 2, 2, 2, 2, 2, 2};
   Strides st[8];
   if (!read_strides(st, strides, 8, heads, rows, d_k, elem)) return ATTN_ERR_INVALID_ARG;
-  const BwdLayout lay = bwd_layout(B, h, n_q, d_k);
+  const BwdLayout lay = bwd_scored_layout(B, h, h_kv, n_q, n_k, d_k);
   if (workspace_bytes < lay.scored_bytes) return ATTN_ERR_INVALID_ARG;
+  // (the parts of dK and dV are one tensor of 2^31 - 1 heads at most)
+  if (2LL * lay.parts * B * h_kv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di)) != ATTN_OK) return rc;
-  CUtensorMap maps[7];
+  CUtensorMap maps[8];
   if ((rc = encode_4d(&maps[0], q, d_k, n_q, h, B, st[0], 128)) != ATTN_OK) return rc;
   if ((rc = encode_4d(&maps[1], k, d_k, n_k, h_kv, B, st[1], 128)) != ATTN_OK) return rc;
   if ((rc = encode_4d(&maps[2], v, d_k, n_k, h_kv, B, st[2], 128)) != ATTN_OK) return rc;
@@ -1157,10 +1161,18 @@ int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, 
     return rc;
   const BwdProblem pb{q, k, v, o, dout, lse, dq, dk, dv, B, h, n_q, n_k, d_k, scale,
                       kMaskNone, nullptr, 0, 0, st[3], st[4], st[5]};
-  const ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k, st);
+  ScoreMod mod = score_mod(softcap, slopes, h, h_kv, plan, B, n_q, n_k, st);
+  mod.sdk = st[6];
+  mod.sdv = st[7];
+  mod.parts = lay.parts;
+  maps[7] = maps[6];
+  if (lay.parts > 1 &&
+      (rc = encode_3d_f32(&maps[7], static_cast<uint8_t*>(workspace) + lay.part_off, d_k, n_k,
+                          2LL * lay.parts * B * h_kv)) != ATTN_OK)
+    return rc;
   const cudaError_t e = launch_bwd(pb, maps, workspace, make_ctx(*di, stream), &mod);
   if (e != cudaSuccess) return cuda_fail(e);
-  g_launches.fetch_add(3);
+  g_launches.fetch_add(lay.parts > 1 ? 4 : 3);
   return ATTN_OK;
 }
 

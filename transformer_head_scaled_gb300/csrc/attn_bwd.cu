@@ -10,7 +10,8 @@
 //   dV = P^T dO,   dP = dO V^T,   D_i = sum_c dO_ic O_ic,
 //   dS = P * (dP - D_i)  (elementwise),   dQ = scale dS K,   dK = scale dS^T Q.
 //
-// Three launches:
+// Three launches (changed scores add attn_bwd_few_kernel beside the first and, for
+// shared key heads worked on in parts, attn_bwd_dkv_kernel after the last):
 //   1. attn_bwd_pre_kernel: per query row, the two per-query constants the
 //      elementwise steps need, b_i = -LSE_i / scale and -D_i, each split into
 //      three bf16 parts (hi + mid + lo) and written as [128 x 16] bf16 tiles;
@@ -155,6 +156,7 @@ struct Params {
   float scale;
   // changed scores (kScored): BH counts key heads then
   int group;              // query heads per key head
+  int parts;              // items that share a key tile, group / parts query heads each
   float cap_log2;         // softcap * log2(e); 0: no cap
   float cap_in;           // 2 log2(e) scale / softcap: tanh's exponent per unit of q.k
   const float* slopes;    // distance bias per query head, or null
@@ -173,12 +175,16 @@ struct Params {
 struct Item {
   int bh, kt, qt0, n, key_limit;
   int nq;
+  int part;  // kScored: which of the parts of the query heads
 };
 
-// An item of changed scores: the plan's, for every key head in turn.
+// An item of changed scores: the plan's, for every key head and part in turn.
 __device__ __forceinline__ Item bwd_item_planned(const Params& p, int t) {
   Item it;
-  const int heads = p.H / p.group, e = t / heads, hk = t - e * heads;
+  const int heads = p.H / p.group;
+  const int whole = p.parts == 1 ? t : t / p.parts;
+  it.part = t - whole * p.parts;
+  const int e = whole / heads, hk = whole - e * heads;
   it.key_limit = p.n_k;
   if (p.masked) {
     const int4 k = __ldg(reinterpret_cast<const int4*>(p.plan.key_items + e));
@@ -192,7 +198,7 @@ __device__ __forceinline__ Item bwd_item_planned(const Params& p, int t) {
     it.qt0 = 0;
     it.nq = p.num_qt;
   }
-  it.n = it.nq * p.group;
+  it.n = it.nq * (p.group / p.parts);
   return it;
 }
 
@@ -235,6 +241,7 @@ __device__ __forceinline__ Item bwd_item(const Params& p, int t) {
     }
   }
   it.nq = it.n;
+  it.part = 0;
   return it;
 }
 
@@ -428,7 +435,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                        const __grid_constant__ CUtensorMap tmdo,
                        const __grid_constant__ CUtensorMap tmdk,
                        const __grid_constant__ CUtensorMap tmdv,
-                       const __grid_constant__ CUtensorMap tmdq, const Params p) {
+                       const __grid_constant__ CUtensorMap tmdq,
+                       const __grid_constant__ CUtensorMap tmpart, const Params p) {
   using C = BCfg<D_>;
   using S = Smem<D_, MODE>;
   constexpr int D = D_;
@@ -515,9 +523,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   }
-  // heads of K, V, dK and dV, and the query head of a key head's g-th group member
+  // heads of K, V, dK and dV, and the query head of an item's g-th group member
   const int kv_heads = SCORED ? p.H / p.group : p.H;
-  auto q_head = [&](int bh, int g) { return SCORED ? bh % kv_heads * p.group + g : bh % p.H; };
+  auto q_head = [&](const Item& item, int g) {
+    return SCORED ? item.bh % kv_heads * p.group + item.part * (p.group / p.parts) + g
+                  : item.bh % p.H;
+  };
   // the item's next tile pair: the next query tile, then the next query head
   auto step = [](const Item& item, int& qt, int& g) {
     if (++qt == item.qt0 + item.nq) {
@@ -542,7 +553,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++it;
         int qt = item.qt0, g = 0;
         for (int i = 0; i < item.n && ok; ++i, step(item, qt, g)) {
-          const int hq = q_head(item.bh, g);
+          const int hq = q_head(item, g);
           const uint32_t st = nq % QSTAGES;
           ok = mbar_wait(smem_u32(&sm.q_empty[st]), ((nq / QSTAGES) & 1) ^ 1, p.limit_ns, abort);
           if (!ok) break;
@@ -774,6 +785,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       fence_proxy_async_smem();
       named_bar_sync(bar_id, 64);
     };
+    // kScored with parts: this part's dV (which = 0) or dK as fp32 rows into the
+    // workspace, [dV, dK][part][B * key heads]; attn_bwd_dkv_kernel adds the parts up
+    auto store_part = [&](const Item& item, int which, uint32_t (&lo)[32], uint32_t (&hi)[32],
+                          float sc) {
+      const int z = (which * p.parts + item.part) * p.BH + item.bh;
+      const int key_row0 = item.kt * BN + 64 * g;
+#pragma unroll
+      for (int half = 0; half < (D > 32 ? 2 : 1); ++half) {
+        uint32_t(&w)[32] = half == 0 ? lo : hi;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * sc);
+        stage_acquire();
+        st_row_swz<C::QRB>(stage, rg, w);
+        stage_release();
+        if (leader && key_row0 < p.n_k) {
+          tma_store_3d(&tmpart, stage, 32 * half, key_row0, z);
+          bulk_commit_group();
+        }
+      }
+    };
     uint32_t it = 0, t = 0;
     for (Walk<MODE> at; at.x < num_items && ok; at.next()) {
       const Item item = bwd_item<MODE>(p, at.x);
@@ -784,6 +815,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t w[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) w[i] = 0u;
+        if (SCORED && p.parts > 1) {
+          store_part(item, 0, w, w, 1.f);
+          store_part(item, 1, w, w, 1.f);
+          continue;
+        }
         stage_acquire();
         st_row_swz<C::RB>(stage, rg, w);
         stage_release();
@@ -808,7 +844,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // fp32 boxes of min(d, 32) columns x 64 rows per group, each added
         // into the accumulator by one TMA reduce; rows past n_q are not touched
         const int q_row0 = qt * BM + 64 * g;
-        const int qbh = SCORED ? b * p.H + q_head(item.bh, member) : item.bh;
+        const int qbh = SCORED ? b * p.H + q_head(item, member) : item.bh;
         stage_acquire();
         st_row_swz<C::QRB>(stage, rg, a);
         stage_release();
@@ -842,6 +878,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (which == 1) {
           tc_fence_before();
           mbar_arrive(smem_u32(&sm.dkv_free));
+        }
+        if constexpr (SCORED) {
+          if (p.parts > 1) {
+            store_part(item, which, a, a2, sc);
+            continue;
+          }
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -929,7 +971,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int ahead = j - qt * BM - 64 * half;
           bool slow = __any_sync(0xffffffffu, lim > 0 || hi < 64);
           if constexpr ((MODE & kBias) != 0) {
-            const float slope2 = LOG2E * __ldg(p.slopes + q_head(item.bh, member));
+            const float slope2 = LOG2E * __ldg(p.slopes + q_head(item, member));
             bias = slope2 * static_cast<float>(j - qt * BM);
             f = -2.f * slope2;
             // a query of this half that sees this key and comes before it
@@ -957,14 +999,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               scored_probabilities<MODE, true, true>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
                                                      emit);
           }
-          if ((MODE & kWide) != 0 && poly)
-            ;  // done
-          else if (slow)
-            scored_probabilities<MODE, true, false>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
-                                                    emit);
-          else
-            scored_probabilities<MODE, false, false>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
-                                                     emit);
+          if ((MODE & kWide) == 0 || !poly) {
+            if (slow)
+              scored_probabilities<MODE, true, false>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
+                                                      emit);
+            else
+              scored_probabilities<MODE, false, false>(p, s0, s1, pf, lim, hi, bias, fahead, f,
+                                                       lse, emit);
+          }
           if (!ok) break;
         } else {
 #pragma unroll
@@ -1051,21 +1093,6 @@ __device__ __forceinline__ uint2 split3_bf16(float x) {
   return w;
 }
 
-// Per query row (d/8 threads a row, 8 elements each): D = sum_c dO_c O_c, the constant tile's
-// row for this query (b = -LSE/scale and -D, three bf16 parts each), and the
-// dQ accumulator row set to zero.  Rows n_q .. of the last query tile get zero
-// constants (their Q and dO rows are zero-filled by the tile loads, so every
-// product they enter is zero).
-//
-// SCORED (changed scores): D of a query that sees at most kFewKeys keys is
-// summed from its P and dP in fp32 instead.  The O it would come from is rounded
-// to bf16, which errs by up to 2^-8 |dO| |O|; with few keys |O| is as large as a
-// value and dP - D cancels, so that this rounding alone took the gradients of
-// short documents (2 to 9 in 17 to 48 tokens) to 6e-3 relative error in an
-// emulation with the kernels' roundings; with up to 16 keys summed so they stay
-// below 3.1e-3, with up to 32 below 3.0e-3, at any length.
-constexpr int kFewKeys = 16;
-
 struct PreMod {
   const __nv_bfloat16* q;
   const __nv_bfloat16* k;
@@ -1093,12 +1120,125 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return acc;
 }
 
+// D of the queries that see 2 to kFewKeys keys, summed from P and dP in fp32,
+// put in the place of the one from O.  That O is rounded to bf16, which errs by
+// up to 2^-8 |dO| |O|; with few keys |O| is as large as a value and dP - D
+// cancels, so that this rounding alone took the gradients of short documents (2
+// to 9 in 17 to 48 tokens) to 6e-3 relative error in an emulation with the
+// kernels' roundings; with up to 16 keys summed so they stay below 3.1e-3, with
+// up to 32 below 3.0e-3, at any length.  (With one key O is that value exactly.)
+//
+// A CTA looks at 256 queries of a head, lists those it has work for, and gives
+// each d / 8 threads.  A kernel of its own: the sums want 64 registers, which as
+// part of the pre-kernel halved the warps in flight there (4 x 4096 tokens, 16
+// heads, d = 64, causal: 45 us in one kernel; 27 us, with these 18 us beside it, in
+// two).
+constexpr int kFewKeys = 16;
+
+template <int D>
+__global__ void __launch_bounds__(256)
+    attn_bwd_few_kernel(const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
+                        uint8_t* __restrict__ cst, int H, int n_q, int num_qt, RowStrides sdo,
+                        const PreMod mod) {
+  grid_launch_dependents();
+  constexpr int TPR = D / 8;  // threads a row
+  __shared__ int s_row[256], s_first[256], s_seen[256], s_n;
+  const int rows = (n_q + 255) / 256;  // CTAs a head
+  const int bh = blockIdx.x / rows;
+  const int i0 = (blockIdx.x - bh * rows) * 256;
+  const long long bb = bh / H, hh = bh % H;
+  if (threadIdx.x == 0) s_n = 0;
+  __syncthreads();
+  {
+    const int i = i0 + threadIdx.x;
+    int2 keys = make_int2(0, mod.n_k);
+    if (mod.row_keys != nullptr) {
+      const int4 h = __ldg(mod.header);
+      const bool fits = h.x == n_q && h.y == mod.n_k && h.z == mod.B;  // else the main kernel reports it
+      keys = i < n_q && fits ? __ldg(mod.row_keys + bb * n_q + i) : make_int2(0, 0);
+    }
+    const int seen = keys.y - keys.x;
+    if (i < n_q && seen > 1 && seen <= kFewKeys) {
+      const int at = atomicAdd(&s_n, 1);  // in any order: the rows are apart
+      s_row[at] = i;
+      s_first[at] = keys.x;
+      s_seen[at] = seen;
+    }
+  }
+  __syncthreads();
+  const int n = s_n, sub = threadIdx.x % TPR;
+  if (n > 0) {
+    const long long hk = hh / mod.group;
+    const float slope = mod.slopes != nullptr ? __ldg(mod.slopes + hh) : 0.f;
+    const __nv_bfloat16* kp = mod.k + bb * mod.sk.b + hk * mod.sk.h + sub * 8;
+    const __nv_bfloat16* vp = mod.v + bb * mod.sv.b + hk * mod.sv.h + sub * 8;
+    for (int w0 = 0; w0 < n; w0 += 256 / TPR) {
+      const int at = w0 + threadIdx.x / TPR;
+      const int i = at < n ? s_row[at] : 0, j0 = at < n ? s_first[at] : 0;
+      const int seen = at < n ? s_seen[at] : 0;
+      uint4 qv = make_uint4(0u, 0u, 0u, 0u), a = qv;
+      float l = 0.f;
+      if (at < n) {
+        qv = *reinterpret_cast<const uint4*>(mod.q + bb * mod.sq.b + hh * mod.sq.h +
+                                             i * mod.sq.n + sub * 8);
+        a = *reinterpret_cast<const uint4*>(dout + bb * sdo.b + hh * sdo.h + i * sdo.n + sub * 8);
+        l = lse[static_cast<size_t>(bh) * n_q + i];
+      }
+      const int most = __reduce_max_sync(0xffffffffu, seen);
+      float exact = 0.f;
+      // four keys' loads in flight at a time
+      for (int x0 = 0; x0 < most; x0 += 4) {
+        float s[4], dp[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          s[y] = dp[y] = 0.f;
+          if (x0 + y < seen) {
+            const long long j = j0 + x0 + y;
+            s[y] = dot8(qv, *reinterpret_cast<const uint4*>(kp + j * mod.sk.n));
+            dp[y] = dot8(a, *reinterpret_cast<const uint4*>(vp + j * mod.sv.n));
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+#pragma unroll
+          for (int m = TPR / 2; m > 0; m >>= 1) {
+            s[y] += __shfl_xor_sync(0xffffffffu, s[y], m);
+            dp[y] += __shfl_xor_sync(0xffffffffu, dp[y], m);
+          }
+          s[y] *= mod.scale;
+          if (mod.softcap > 0.f) s[y] = mod.softcap * tanhf(s[y] / mod.softcap);
+          s[y] -= slope * fabsf(static_cast<float>(i - (j0 + x0 + y)));
+          if (x0 + y < seen) exact = fmaf(expf(s[y] - l), dp[y], exact);
+        }
+      }
+      if (at < n && sub == 0 && isfinite(l)) {
+        const int qt = i / BM, r = i % BM;
+        uint8_t* row = cst +
+                       (static_cast<size_t>(bh) * num_qt + qt) * static_cast<size_t>(CONST_TILE_BYTES) +
+                       (r & 7) * 16 + (r >> 3) * 256;
+        const uint2 pd = split3_bf16(-exact);
+        *reinterpret_cast<uint16_t*>(row + 6) = static_cast<uint16_t>(pd.x);
+        *reinterpret_cast<uint32_t*>(row + 8) = (pd.x >> 16) | (pd.y << 16);
+      }
+    }
+  }
+}
+
+// Per query row (d/8 threads a row, 8 elements each): D = sum_c dO_c O_c, the constant tile's
+// row for this query (b = -LSE/scale and -D, three bf16 parts each), and the
+// dQ accumulator row set to zero.  Rows n_q .. of the last query tile get zero
+// constants (their Q and dO rows are zero-filled by the tile loads, so every
+// product they enter is zero).
+//
+// SCORED (changed scores): the D of queries that attn_bwd_few_kernel takes is left
+// to it (`few`); the two run side by side, and the last CTA here ends after it, so
+// that what waits for this grid waits for both.
 template <int D, bool SCORED>
 __global__ void __launch_bounds__(256)
     attn_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                         const float* __restrict__ lse, uint8_t* __restrict__ cst,
                         float* __restrict__ dq_acc, int H, int n_q, int num_qt, float inv_scale,
-                        long long rows, RowStrides so, RowStrides sdo, const PreMod mod) {
+                        long long rows, RowStrides so, RowStrides sdo, const PreMod mod, bool few) {
   // the main kernel may start launching now: it waits for this grid to
   // complete before it reads the constants or adds into dq_acc
   grid_launch_dependents();
@@ -1112,10 +1252,22 @@ __global__ void __launch_bounds__(256)
   const bool valid = in && i < n_q;
   const size_t src = (static_cast<size_t>(bh) * n_q + i) * D + sub * 8;  // accumulator row
   const long long bb = bh / H, hh = bh % H;
+  // does the other kernel write this query's D?
+  bool skip = false;
+  if (SCORED && few) {
+    int seen = mod.n_k;
+    if (mod.row_keys != nullptr) {
+      const int4 h = __ldg(mod.header);
+      const bool fits = h.x == n_q && h.y == mod.n_k && h.z == mod.B;  // else the main kernel reports it
+      const int2 keys = valid && fits ? __ldg(mod.row_keys + bb * n_q + i) : make_int2(0, 0);
+      seen = keys.y - keys.x;
+    }
+    skip = seen > 1 && seen <= kFewKeys;
+  }
   float acc = 0.f;
-  uint4 a = make_uint4(0u, 0u, 0u, 0u);
   if (valid) {
-    a = *reinterpret_cast<const uint4*>(dout + bb * sdo.b + hh * sdo.h + i * sdo.n + sub * 8);
+    const uint4 a =
+        *reinterpret_cast<const uint4*>(dout + bb * sdo.b + hh * sdo.h + i * sdo.n + sub * 8);
     const uint4 b = *reinterpret_cast<const uint4*>(o + bb * so.b + hh * so.h + i * so.n + sub * 8);
     acc = dot8(a, b);
     float4* z = reinterpret_cast<float4*>(dq_acc + src);
@@ -1124,47 +1276,6 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int m = TPR / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-  if constexpr (SCORED) {
-    int2 keys = make_int2(0, mod.n_k);
-    if (mod.row_keys != nullptr) {
-      const int4 h = __ldg(mod.header);
-      const bool fits = h.x == n_q && h.y == mod.n_k && h.z == mod.B;  // else the main kernel reports it
-      keys = valid && fits ? __ldg(mod.row_keys + bb * n_q + i) : make_int2(0, 0);
-    }
-    const float l = valid ? lse[static_cast<size_t>(bh) * n_q + i] : 0.f;
-    const int seen = valid && keys.y - keys.x <= kFewKeys && isfinite(l) ? keys.y - keys.x : 0;
-    // (one key: O is that value exactly)
-    const int most = __reduce_max_sync(0xffffffffu, seen > 1 ? seen : 0);
-    if (most > 0) {
-      const long long hk = hh / mod.group;
-      uint4 qv = make_uint4(0u, 0u, 0u, 0u);
-      if (valid)
-        qv = *reinterpret_cast<const uint4*>(mod.q + bb * mod.sq.b + hh * mod.sq.h +
-                                             i * mod.sq.n + sub * 8);
-      const float slope = mod.slopes != nullptr && valid ? __ldg(mod.slopes + hh) : 0.f;
-      float exact = 0.f;
-      for (int x = 0; x < most; ++x) {
-        const int j = keys.x + x;
-        float s = 0.f, dp = 0.f;
-        if (x < seen) {
-          s = dot8(qv, *reinterpret_cast<const uint4*>(mod.k + bb * mod.sk.b + hk * mod.sk.h +
-                                                       j * mod.sk.n + sub * 8));
-          dp = dot8(a, *reinterpret_cast<const uint4*>(mod.v + bb * mod.sv.b + hk * mod.sv.h +
-                                                       j * mod.sv.n + sub * 8));
-        }
-#pragma unroll
-        for (int m = TPR / 2; m > 0; m >>= 1) {
-          s += __shfl_xor_sync(0xffffffffu, s, m);
-          dp += __shfl_xor_sync(0xffffffffu, dp, m);
-        }
-        s *= mod.scale;
-        if (mod.softcap > 0.f) s = mod.softcap * tanhf(s / mod.softcap);
-        s -= slope * fabsf(static_cast<float>(i - j));
-        if (x < seen) exact = fmaf(expf(s - l), dp, exact);
-      }
-      if (seen > 1) acc = exact;
-    }
-  }
   if (in && sub < 2) {
     // sub 0: columns 0-7 of this query's row (b in 0-2, -D in 3-5); sub 1:
     // columns 8-15, zero
@@ -1185,7 +1296,14 @@ __global__ void __launch_bounds__(256)
       w.y = pb.y | (pd.x << 16);          // b_lo, -D_hi
       w.z = (pd.x >> 16) | (pd.y << 16);  // -D_mid, -D_lo
     }
-    *reinterpret_cast<uint4*>(tile + (n & 7) * 16 + (n >> 3) * 256 + sub * 128) = w;
+    uint8_t* dst = tile + (n & 7) * 16 + (n >> 3) * 256 + sub * 128;
+    if (SCORED && skip && valid && sub == 0) {
+      *reinterpret_cast<uint32_t*>(dst) = w.x;
+      *reinterpret_cast<uint16_t*>(dst + 4) = static_cast<uint16_t>(w.y);
+      *reinterpret_cast<uint32_t*>(dst + 12) = 0u;
+    } else {
+      *reinterpret_cast<uint4*>(dst) = w;
+    }
     if (SCORED && mod.lse_log2 != nullptr && sub == 0) {
       const float l = valid ? lse[static_cast<size_t>(bh) * n_q + i] : 0.f;
       const float far = mod.slopes != nullptr ? __ldg(mod.slopes + hh) * static_cast<float>(n) : 0.f;
@@ -1193,6 +1311,7 @@ __global__ void __launch_bounds__(256)
           ((isfinite(l) ? l : 0.f) + far) * LOG2E;
     }
   }
+  if (SCORED && few && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
 // dQ = scale * accumulator, rounded to bf16, written through dq's strides;
@@ -1217,7 +1336,55 @@ __global__ void __launch_bounds__(256)
   *reinterpret_cast<uint4*>(dq + dst) = out;
 }
 
+// dK and dV of key heads whose query heads were worked on in parts: the parts'
+// fp32 sums added up in order and rounded to bf16, 8 elements a thread.
+// grid.y: 0 dV, 1 dK.
+__global__ void __launch_bounds__(256)
+    attn_bwd_dkv_kernel(const float* __restrict__ acc, __nv_bfloat16* __restrict__ dk,
+                        __nv_bfloat16* __restrict__ dv, int parts, long long n8, int d8, int HK,
+                        int n_k, RowStrides sdk, RowStrides sdv) {
+  grid_dependency_wait();  // the parts are complete
+  const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i >= n8) return;
+  const long long r = i / d8;  // row (b * HK + head) * n_k + key
+  const long long bh = r / n_k;
+  const bool is_k = blockIdx.y == 1;
+  const RowStrides st = is_k ? sdk : sdv;
+  const long long dst =
+      (bh / HK) * st.b + (bh % HK) * st.h + (r - bh * n_k) * st.n + (i - r * d8) * 8;
+  const float4* src = reinterpret_cast<const float4*>(acc) + (is_k ? parts * n8 * 2 : 0) + 2 * i;
+  float4 a = src[0], b = src[1];
+  for (int x = 1; x < parts; ++x) {
+    const float4 c = src[x * n8 * 2], e = src[x * n8 * 2 + 1];
+    a = make_float4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w);
+    b = make_float4(b.x + e.x, b.y + e.y, b.z + e.z, b.w + e.w);
+  }
+  uint4 out;
+  out.x = pack_bf16x2(a.x, a.y);
+  out.y = pack_bf16x2(a.z, a.w);
+  out.z = pack_bf16x2(b.x, b.y);
+  out.w = pack_bf16x2(b.z, b.w);
+  *reinterpret_cast<uint4*>((is_k ? dk : dv) + dst) = out;
+}
+
 }  // namespace
+
+// A key head's query heads are worked on in parts, each an item of its own, when
+// there are too few (key tile, key head) items to even out over the SMs: in as
+// many as make kPartItems of them.  Parts cost their dK and dV in fp32 once more
+// through memory, so there are no more than that.  Packed documents in 2 x 333
+// tokens, 8 query heads on 2, d = 32, 12 items: 41.6 us in one part, 28.6 us in
+// four.  4 x 4096 tokens, 16 query heads on 4, d = 64, 512 items: 350 us in one
+// part, 350 us in two, 375 us in four.
+constexpr long long kPartItems = 512;
+
+int bwd_parts(int B, int H, int HK, int n_k) {
+  const int group = H / HK;
+  const long long items = static_cast<long long>(B) * HK * ((n_k + BN - 1) / BN);
+  for (int parts = 1; parts < group; ++parts)
+    if (group % parts == 0 && items * parts >= kPartItems) return parts;
+  return group;
+}
 
 BwdLayout bwd_layout(int B, int H, int n_q, int d) {
   BwdLayout l;
@@ -1227,7 +1394,16 @@ BwdLayout bwd_layout(int B, int H, int n_q, int d) {
   l.dq_acc_off = bh * l.num_qt * CONST_TILE_BYTES;
   l.lse_off = l.dq_acc_off + bh * static_cast<size_t>(n_q) * d * 4;
   l.bytes = l.lse_off;
-  l.scored_bytes = l.lse_off + bh * l.num_qt * BM * 4;
+  l.part_off = l.lse_off + bh * l.num_qt * BM * 4;
+  l.scored_bytes = l.part_off;
+  return l;
+}
+
+BwdLayout bwd_scored_layout(int B, int H, int HK, int n_q, int n_k, int d) {
+  BwdLayout l = bwd_layout(B, H, n_q, d);
+  l.parts = bwd_parts(B, H, HK, n_k);
+  if (l.parts > 1)
+    l.scored_bytes += 2 * static_cast<size_t>(l.parts) * B * HK * n_k * d * 4;
   return l;
 }
 
@@ -1244,7 +1420,7 @@ cudaError_t launch_bwd_main(const Params& p, const CUtensorMap* maps, const Laun
   const int grid = p.num_items < ctx.num_sms ? p.num_items : ctx.num_sms;
   return launch_dependent(attn_bwd_tc_kernel<MODE, D>, dim3(grid), dim3(NUM_THREADS), smem,
                           ctx.stream, maps[0], maps[1], maps[2], maps[3], maps[4], maps[5],
-                          maps[6], p);
+                          maps[6], maps[7], p);
 }
 
 template <int D>
@@ -1280,12 +1456,27 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
     pm.B = pb.B;
     pm.lse_log2 = lse_log2;
   }
-  auto* pre = mod != nullptr ? attn_bwd_pre_kernel<D, true> : attn_bwd_pre_kernel<D, false>;
-  pre<<<static_cast<unsigned>(pre_blocks), 256, 0, ctx.stream>>>(
-      static_cast<const __nv_bfloat16*>(pb.o), static_cast<const __nv_bfloat16*>(pb.dout), pb.lse,
-      cst, dq_acc, pb.H, pb.n_q, static_cast<int>(lay.num_qt), 1.f / pb.scale, rows, pb.so,
-      pb.sdo, pm);
-  cudaError_t err = cudaGetLastError();
+  const auto* o = static_cast<const __nv_bfloat16*>(pb.o);
+  const auto* dout = static_cast<const __nv_bfloat16*>(pb.dout);
+  const int num_qt = static_cast<int>(lay.num_qt);
+  const bool few = mod != nullptr && (mod->masked || pb.n_k <= kFewKeys);
+  cudaError_t err = cudaSuccess;
+  if (few) {
+    const long long blocks = bh * ((pb.n_q + 255) / 256);  // no more than pre_blocks
+    attn_bwd_few_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, ctx.stream>>>(
+        dout, pb.lse, cst, pb.H, pb.n_q, num_qt, pb.sdo, pm);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    err = launch_dependent(attn_bwd_pre_kernel<D, true>, dim3(static_cast<unsigned>(pre_blocks)),
+                           dim3(256), 0, ctx.stream, o, dout, pb.lse, cst, dq_acc, pb.H, pb.n_q,
+                           num_qt, 1.f / pb.scale, rows, pb.so, pb.sdo, pm, true);
+  } else {
+    auto* pre = mod != nullptr ? attn_bwd_pre_kernel<D, true> : attn_bwd_pre_kernel<D, false>;
+    pre<<<static_cast<unsigned>(pre_blocks), 256, 0, ctx.stream>>>(
+        o, dout, pb.lse, cst, dq_acc, pb.H, pb.n_q, num_qt, 1.f / pb.scale, rows, pb.so, pb.sdo,
+        pm, false);
+    err = cudaGetLastError();
+  }
   if (err != cudaSuccess) return err;
 
   Params p{};
@@ -1310,8 +1501,9 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   if (mod != nullptr) {
     p.mask = kMaskNone;
     p.group = mod->group;
+    p.parts = mod->parts;
     p.BH = p.BH / mod->group;
-    p.num_items = p.BH * p.num_kt;
+    p.num_items = p.BH * p.num_kt * p.parts;
     p.cap_log2 = mod->softcap * LOG2E;
     p.cap_in = mod->softcap > 0.f ? 2.f * p.scale_log2 / mod->softcap : 0.f;
     p.slopes = mod->slopes;
@@ -1335,10 +1527,18 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   if (err != cudaSuccess) return err;
 
   const long long n8 = bh * pb.n_q * (D / 8);
-  return launch_dependent(attn_bwd_dq_kernel, dim3(static_cast<unsigned>((n8 + 255) / 256)),
-                          dim3(256), 0, ctx.stream, static_cast<const float*>(dq_acc),
-                          static_cast<__nv_bfloat16*>(pb.dq), pb.scale, n8, D / 8, pb.H, pb.n_q,
-                          pb.sdq);
+  err = launch_dependent(attn_bwd_dq_kernel, dim3(static_cast<unsigned>((n8 + 255) / 256)),
+                         dim3(256), 0, ctx.stream, static_cast<const float*>(dq_acc),
+                         static_cast<__nv_bfloat16*>(pb.dq), pb.scale, n8, D / 8, pb.H, pb.n_q,
+                         pb.sdq);
+  if (err != cudaSuccess || mod == nullptr || mod->parts == 1) return err;
+  const int HK = pb.H / mod->group;
+  const long long k8 = static_cast<long long>(pb.B) * HK * pb.n_k * (D / 8);
+  return launch_dependent(attn_bwd_dkv_kernel, dim3(static_cast<unsigned>((k8 + 255) / 256), 2),
+                          dim3(256), 0, ctx.stream,
+                          reinterpret_cast<const float*>(ws + lay.part_off),
+                          static_cast<__nv_bfloat16*>(pb.dk), static_cast<__nv_bfloat16*>(pb.dv),
+                          mod->parts, k8, D / 8, HK, pb.n_k, mod->sdk, mod->sdv);
 }
 
 }  // namespace

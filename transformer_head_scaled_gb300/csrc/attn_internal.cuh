@@ -70,7 +70,10 @@ struct ScoreMod {
   int group;            // query heads per key head
   MaskPlan plan;
   bool masked;          // whether there is a plan
-  RowStrides sq, sk, sv;  // of q, k, v (the backward reads a few rows with plain loads)
+  // the backward: of q, k, v (a few rows are read with plain loads), dk and dv, and
+  // the parts that a key head's query heads are worked on in
+  RowStrides sq, sk, sv, sdk, sdv;
+  int parts;
 };
 
 // Instantiations of the tensor-core kernels: the masks given by lengths (none,
@@ -249,13 +252,19 @@ struct BwdLayout {
   size_t num_qt, cst_off, dq_acc_off, bytes;
   // with changed scores: LSE * log2(e), padded to whole query tiles, behind them
   size_t lse_off, scored_bytes;
+  // and, where key heads' query heads are worked on in parts, those parts' dV and
+  // dK in fp32, [dV, dK][part][B, HK, n_k, d]
+  size_t part_off;
+  int parts = 1;
 };
 BwdLayout bwd_layout(int B, int H, int n_q, int d);
+BwdLayout bwd_scored_layout(int B, int H, int HK, int n_q, int n_k, int d);
 bool bwd_head_size_ok(int d);
 // maps: Q, K, V, dO as 4-D (d, n, H, B) bf16 with a (d, 128, 1, 1) box; dK,
 // dV the same with a (d, 64, 1, 1) box (any strides); the dQ accumulator as 3-D (d, n_q, B*H)
 // fp32 with a (min(d, 32), 64, 1) box; each in the swizzle of its box's row
-// bytes.  Three launches (preprocess, main, dQ convert).
+// bytes; with `mod`, the parts of dV and dK the same as 3-D (d, n_k, 2 * parts *
+// B*HK).  Three launches (preprocess, main, dQ convert), four with parts.
 // With `mod`: changed scores, under its plan instead of pb's mask; the K, V, dK
 // and dV maps then have H / mod->group heads.
 cudaError_t launch_bwd(const BwdProblem& pb, const CUtensorMap* maps, void* workspace,
