@@ -164,6 +164,8 @@ struct Params {
   const float* lse_log2;  // with a cap: [B * H][num_qt * 128]
   bool masked;
   MaskPlan plan;
+  const int* next;  // the items dealt out by load: after each the next one of its CTA,
+                    // then every CTA's first; or null
   uint64_t limit_ns;
   int* status;
 };
@@ -246,13 +248,29 @@ __device__ __forceinline__ Item bwd_item(const Params& p, int t) {
 }
 
 // The items of this CTA, one after the other: every gridDim.x-th, or, of planned
-// ones, back and forth.
+// ones, those that attn_bwd_few_kernel dealt it, else back and forth.
 template <int MODE>
 struct Walk {
-  int x, step;
-  __device__ __forceinline__ Walk()
-      : x(blockIdx.x), step((MODE & kScored) ? first_step() : static_cast<int>(gridDim.x)) {}
-  __device__ __forceinline__ void next() {
+  int x, step;  // step 0: the dealt ones
+  __device__ __forceinline__ explicit Walk(const Params& p)
+      : x(blockIdx.x), step((MODE & kScored) ? first_step() : static_cast<int>(gridDim.x)) {
+    if constexpr ((MODE & kScored) != 0) {
+      if (p.next != nullptr) {
+        const int first = p.next[p.num_items + blockIdx.x];
+        if (first >= 0) {
+          x = first;
+          step = 0;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void next(const Params& p) {
+    if constexpr ((MODE & kScored) != 0) {
+      if (step == 0) {
+        x = max(p.next[x], x + 1);  // (always larger; so that every walk ends)
+        return;
+      }
+    }
     x += step;
     if (MODE & kScored) step = 2 * gridDim.x - step;
   }
@@ -262,7 +280,7 @@ struct Walk {
 template <int MODE>
 __device__ __forceinline__ bool find_item(const Params& p, int num_items, Walk<MODE>& at,
                                           Item& out) {
-  for (; at.x < num_items; at.next()) {
+  for (; at.x < num_items; at.next(p)) {
     out = bwd_item<MODE>(p, at.x);
     if (out.n > 0) return true;
   }
@@ -543,7 +561,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t it = 0, nv = 0, nq = 0, no = 0;  // K, V, Q and dO loads issued
       bool ok = true;
       Item item;
-      for (Walk<MODE> at; ok && find_item(p, num_items, at, item); at.next()) {
+      for (Walk<MODE> at(p); ok && find_item(p, num_items, at, item); at.next(p)) {
         const uint32_t slot = it & 1;
         ok = mbar_wait(smem_u32(&sm.k_empty[slot]), ((it >> 1) & 1) ^ 1, p.limit_ns, abort);
         if (!ok) break;
@@ -667,7 +685,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     uint32_t it = 0, t = 0;
     Item cur;
-    Walk<MODE> at;
+    Walk<MODE> at(p);
     const bool any = find_item(p, num_items, at, cur);
     int ci = 0;  // index of tile t inside its item
     if (any && wait(&sm.k_full[0], 0) && wait(&sm.q_full[0], 0) && wait(&sm.v_full, 0) &&
@@ -683,7 +701,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t nit = it;
         bool has_next = true;
         if (ni >= cur.n) {
-          at.next();
+          at.next(p);
           has_next = find_item(p, num_items, at, nx);
           ni = 0;
           nit = it + 1;
@@ -806,7 +824,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     };
     uint32_t it = 0, t = 0;
-    for (Walk<MODE> at; at.x < num_items && ok; at.next()) {
+    for (Walk<MODE> at(p); at.x < num_items && ok; at.next(p)) {
       const Item item = bwd_item<MODE>(p, at.x);
       const int key_row0 = item.kt * BN + 64 * g;
       const int b = item.bh / kv_heads, hk = item.bh % kv_heads;
@@ -922,7 +940,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     };
     uint32_t t = 0;
     Item item;
-    for (Walk<MODE> at; ok && find_item(p, num_items, at, item); at.next()) {
+    for (Walk<MODE> at(p); ok && find_item(p, num_items, at, item); at.next(p)) {
       const int j = item.kt * BN + r;  // this thread's key
       const bool row_valid = j < item.key_limit;
       int2 rows = make_int2(0, row_valid ? p.n_q : 0);  // kScored: this key's queries
@@ -1100,6 +1118,7 @@ struct PreMod {
   RowStrides sq, sk, sv;
   const int2* row_keys;  // [B][n_q], or null: every key
   const int4* header;    // the plan's sizes, or null
+  const KeyItem* key_items;
   const float* slopes;
   float scale, softcap;
   int group, n_k, B;
@@ -1135,17 +1154,90 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 // two).
 constexpr int kFewKeys = 16;
 
+// The items dealt out by load: each, heaviest first, to the CTA with the least
+// work so far.  Run by one CTA more of attn_bwd_few_kernel, in the time of the
+// pre-kernel, for a plan with documents.  Back and forth is as even where a CTA
+// gets many items, or items whose weights fall steadily; with few uneven ones, the
+// heaviest nearly a CTA's share, it gives every CTA as many.  Measured on 4 x 4096
+// tokens, 16 query heads on 4, d = 64, caps, by the documents in a row, 512 items:
+// three 416 -> 381 us, six 337 -> 297, twelve 272 -> 249; on 1 x 8192, 16 heads on
+// one, 512 items: 339 -> 306, 285 -> 262, 212 -> 201; with 1024 items and more no
+// difference.  It takes 8 us for 512 items, which the pre-kernel hides where it has
+// kDealBytes to move: below, 8 x 1000 tokens, d = 32, 59 us became 67.
+struct Deal {
+  int* next;  // [items], then [ctas] the first ones; null: nothing to do
+  int items, ctas, shares, heads;  // shares: items of one key tile; heads: query heads of each
+};
+constexpr int kMostDealt = 1024, kMostCtas = 256;
+constexpr long long kDealPerCta = 4, kDealBytes = 1ll << 26;
+
+__device__ __forceinline__ void deal_items(const Deal& d, const KeyItem* key_items, bool uneven) {
+  if (!uneven) {
+    for (int c = threadIdx.x; c < d.ctas; c += 256) d.next[d.items + c] = -1;
+    return;
+  }
+  // load << 8 | CTA in 32 bits: a sum of kMostDealt weights stays below 2^24
+  constexpr int MOST = (1 << 24) / kMostDealt - 1;
+  const int most = max(MOST / d.heads - 1, 0);
+  __shared__ uint32_t work[kMostDealt];
+  __shared__ uint8_t owner[kMostDealt];
+  for (int x = threadIdx.x; x < d.items; x += 256)
+    work[x] = static_cast<uint32_t>(min(key_items[x / d.shares].count, most) * d.heads + 1) << 8;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;  // has the CTAs lane, lane + 32, ..
+    uint32_t load[kMostCtas / 32];
+#pragma unroll
+    for (int k = 0; k < kMostCtas / 32; ++k) {
+      const int c = lane + 32 * k;  // one each to begin with
+      load[k] = c < d.ctas ? work[c] | c : 0xffffffffu;
+    }
+#pragma unroll 4
+    for (int x = d.ctas; x < d.items; ++x) {
+      const uint32_t w = work[x];
+      uint32_t least = load[0];
+#pragma unroll
+      for (int k = 1; k < kMostCtas / 32; ++k) least = min(least, load[k]);
+      least = __reduce_min_sync(0xffffffffu, least);
+#pragma unroll
+      for (int k = 0; k < kMostCtas / 32; ++k)
+        if (load[k] == least) load[k] = least + w;
+      if (lane == 0) owner[x] = static_cast<uint8_t>(least);
+    }
+  }
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < d.ctas) {
+    int last = c;
+    for (int x = d.ctas; x < d.items; ++x) {
+      if (owner[x] == c) {
+        d.next[last] = x;
+        last = x;
+      }
+    }
+    d.next[last] = d.items;
+    d.next[d.items + c] = c;
+  }
+}
+static_assert(kMostCtas == 256, "a thread a CTA; a CTA's number in a byte");
+
 template <int D>
 __global__ void __launch_bounds__(256)
     attn_bwd_few_kernel(const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
                         uint8_t* __restrict__ cst, int H, int n_q, int num_qt, RowStrides sdo,
-                        const PreMod mod) {
+                        const PreMod mod, const Deal deal) {
   grid_launch_dependents();
+  if (deal.next != nullptr && blockIdx.x == 0) {
+    const int4 h = __ldg(mod.header);
+    deal_items(deal, mod.key_items, h.x == n_q && h.y == mod.n_k && h.z == mod.B && h.w != 0);
+    return;
+  }
+  const int block = blockIdx.x - (deal.next != nullptr);
   constexpr int TPR = D / 8;  // threads a row
   __shared__ int s_row[256], s_first[256], s_seen[256], s_n;
   const int rows = (n_q + 255) / 256;  // CTAs a head
-  const int bh = blockIdx.x / rows;
-  const int i0 = (blockIdx.x - bh * rows) * 256;
+  const int bh = block / rows;
+  const int i0 = (block - bh * rows) * 256;
   const long long bb = bh / H, hh = bh % H;
   if (threadIdx.x == 0) s_n = 0;
   __syncthreads();
@@ -1394,7 +1486,8 @@ BwdLayout bwd_layout(int B, int H, int n_q, int d) {
   l.dq_acc_off = bh * l.num_qt * CONST_TILE_BYTES;
   l.lse_off = l.dq_acc_off + bh * static_cast<size_t>(n_q) * d * 4;
   l.bytes = l.lse_off;
-  l.part_off = l.lse_off + bh * l.num_qt * BM * 4;
+  l.deal_off = l.lse_off + bh * l.num_qt * BM * 4;
+  l.part_off = l.deal_off + (kMostDealt + kMostCtas) * 4;
   l.scored_bytes = l.part_off;
   return l;
 }
@@ -1448,6 +1541,7 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
     pm.sv = mod->sv;
     pm.row_keys = mod->masked ? mod->plan.row_keys : nullptr;
     pm.header = mod->plan.header;
+    pm.key_items = mod->plan.key_items;
     pm.slopes = mod->slopes;
     pm.scale = pb.scale;
     pm.softcap = mod->softcap;
@@ -1461,10 +1555,22 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   const int num_qt = static_cast<int>(lay.num_qt);
   const bool few = mod != nullptr && (mod->masked || pb.n_k <= kFewKeys);
   cudaError_t err = cudaSuccess;
+  Deal deal{};
   if (few) {
-    const long long blocks = bh * ((pb.n_q + 255) / 256);  // no more than pre_blocks
+    long long blocks = bh * ((pb.n_q + 255) / 256);  // no more than pre_blocks
+    const long long items = bh / mod->group * ((pb.n_k + BN - 1) / BN) * mod->parts;
+    if (mod->masked && items > ctx.num_sms && items <= kDealPerCta * ctx.num_sms &&
+        items <= kMostDealt && ctx.num_sms <= kMostCtas &&
+        rows * (8 * D + 36) >= kDealBytes) {
+      deal.next = reinterpret_cast<int*>(ws + lay.deal_off);
+      deal.items = static_cast<int>(items);
+      deal.ctas = ctx.num_sms;
+      deal.shares = pb.H / mod->group * mod->parts;
+      deal.heads = mod->group / mod->parts;
+      ++blocks;
+    }
     attn_bwd_few_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, ctx.stream>>>(
-        dout, pb.lse, cst, pb.H, pb.n_q, num_qt, pb.sdo, pm);
+        dout, pb.lse, cst, pb.H, pb.n_q, num_qt, pb.sdo, pm, deal);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     err = launch_dependent(attn_bwd_pre_kernel<D, true>, dim3(static_cast<unsigned>(pre_blocks)),
@@ -1511,6 +1617,7 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
     p.lse_log2 = lse_log2;
     p.masked = mod->masked;
     p.plan = mod->plan;
+    p.next = deal.next;
     const bool cap = mod->softcap > 0.f, bias = mod->slopes != nullptr;
     const bool wide = mod->softcap > kWideCap;
     err = wide && bias  ? launch_bwd_main<kScored | kCap | kWide | kBias, D>(p, maps, ctx)

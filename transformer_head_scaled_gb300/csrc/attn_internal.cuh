@@ -29,7 +29,7 @@ struct __align__(16) KeyItem {
   int b, tile, first, count;
 };
 struct MaskPlan {
-  const int4* header;    // n_q, n_k, B
+  const int4* header;    // n_q, n_k, B, are the items ordered by their work?
   const int2* row_keys;  // [B][n_q] keys of a query
   const int2* key_rows;  // [B][n_k] queries of a key
   // in the order in which they are dealt out, for every head alike
@@ -250,8 +250,9 @@ struct BwdProblem {
 // accumulator [B, H, n_q, d].
 struct BwdLayout {
   size_t num_qt, cst_off, dq_acc_off, bytes;
-  // with changed scores: LSE * log2(e), padded to whole query tiles, behind them
-  size_t lse_off, scored_bytes;
+  // with changed scores: LSE * log2(e), padded to whole query tiles, behind them,
+  // and who works on which item
+  size_t lse_off, deal_off, scored_bytes;
   // and, where key heads' query heads are worked on in parts, those parts' dV and
   // dK in fp32, [dV, dK][part][B, HK, n_k, d]
   size_t part_off;

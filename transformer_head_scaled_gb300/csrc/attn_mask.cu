@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(BLOCK) attn_mask_plan_kernel(const MaskParams 
   const int blocks = max(p.qb, p.kb);
   const int b = blockIdx.x / blocks, block = blockIdx.x - b * blocks;
   const int i = block * BLOCK + threadIdx.x;  // as a query and as a key
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.header = make_int4(p.n_q, p.n_k, p.B, 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.header = make_int4(p.n_q, p.n_k, p.B, p.ordered);
   int run0 = 0, run1 = 0x7fffffff;  // this token's document
   if (p.doc_ids != nullptr) {
     const int* ids = p.doc_ids + static_cast<size_t>(b) * p.n_q;
