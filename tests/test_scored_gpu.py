@@ -332,6 +332,36 @@ def test_long_packed_row_by_parts():
         at += x
 
 
+@pytest.mark.parametrize("B,h,hk", [(1, 32, 2), (2, 32, 16)])
+def test_documents_dealt_out_by_load(B, h, hk):
+    """Few, uneven key tiles with enough rows to be dealt out by load, the query
+    heads of a key head in parts and in one; every document against itself alone."""
+    n, d = 4096 if B == 1 else 2048, 64
+    lens = [[n // 2 + 1, 1, 300, n // 2 - 302], [5, n - 700, 695]][:B]
+    ids = [sum(([i] * x for i, x in enumerate(row)), []) for row in lens]
+    q, k, v, dout = (_random((B, x, n, d), s) for x, s in ((h, 1), (hk, 2), (hk, 3), (h, 4)))
+    plan = binding.attn_mask_plan(B, n, n, right=0, doc_ids=_ints(ids))
+    o, lse = binding.attn_fwd_scored(q, k, v, plan=plan, softcap=30.0)
+    grads = binding.attn_bwd_scored(q, k, v, o, lse, dout, plan=plan, softcap=30.0)
+    again = binding.attn_bwd_scored(q, k, v, o, lse, dout, plan=plan, softcap=30.0)
+    binding.check()
+    assert torch.equal(grads[1], again[1]) and torch.equal(grads[2], again[2])
+    for b, row in enumerate(lens):
+        at = 0
+        for x in row:
+            part = [t[b:b + 1, :, at:at + x].contiguous() for t in (q, k, v)]
+            own = binding.attn_mask_plan(1, x, x, right=0, device="cuda")
+            po, pl = binding.attn_fwd_scored(*part, plan=own, softcap=30.0)
+            pg = binding.attn_bwd_scored(*part, po, pl, dout[b:b + 1, :, at:at + x], plan=own,
+                                         softcap=30.0)
+            binding.check()
+            for g, w in zip(grads, pg):
+                g, w = g[b:b + 1, :, at:at + x].float(), w.float()
+                # (as above: each within half a step of bf16 and the roundings of P and dS)
+                assert (g - w).norm() <= 1e-2 * w.norm() + 1e-4 * math.sqrt(w.numel())
+            at += x
+
+
 def test_training_step_as_a_captured_graph():
     """Plan, two layers forward and backward captured once and replayed on new
     inputs and documents; dK, dV and O are the eager calls' bit for bit."""
