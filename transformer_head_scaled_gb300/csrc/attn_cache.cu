@@ -56,10 +56,13 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   }
-  auto one = [](float x) {
-    return static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x)))) & 0xffu;
-  };
-  return one(a) | (one(b) << 8) | (one(c) << 16) | (one(d) << 24);
+  // (a magnitude over 127 cannot come of a product with a block's reciprocal; -128
+  // times a ratio can, from a cache that something else wrote)
+  auto one = [](float x) { return max(-127, __float2int_rn(x)); };
+  uint32_t w;
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(w) : "r"(one(d)), "r"(one(c)));
+  asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(w) : "r"(one(b)), "r"(one(a)), "r"(w));
+  return w;
 }
 
 template <bool E4M3>
@@ -99,29 +102,29 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   uint8_t* dst = p.dst[kv] + b * p.sd[kv].b + hh * p.sd[kv].h;
   const int chunks = (last - first) << cpr_log2;  // 8-element chunks, a row's side by side
 
+  // a thread's chunks stand in one column, `rows` rows apart
+  const int rows = THREADS >> cpr_log2, row = tid >> cpr_log2;
+  const int col = (tid - (row << cpr_log2)) * 8;
   uint4 w[CHUNKS];
-  float top = 0.f;
+  {
+    const __nv_bfloat16* at = src + row * p.ss[kv].n + col;
+    const long long step = rows * p.ss[kv].n;
 #pragma unroll
-  for (int i = 0; i < CHUNKS; ++i) {
-    const int c = tid + i * THREADS;
-    if (c < chunks) {
-      const int r = c >> cpr_log2;
-      w[i] = __ldg(reinterpret_cast<const uint4*>(src + r * p.ss[kv].n) + (c - (r << cpr_log2)));
-    } else {
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
+    for (int i = 0; i < CHUNKS; ++i, at += step)
+      w[i] = tid + i * THREADS < chunks ? __ldg(reinterpret_cast<const uint4*>(at))
+                                        : make_uint4(0u, 0u, 0u, 0u);
   }
   float* scale_at = p.scale[kv] + static_cast<long long>(bh) * p.num_blocks + blk;
   const float held = first > row0 ? *scale_at : 0.f;
+  // (the larger of two bf16 magnitudes, exactly; a NaN gives way to a number)
+  __nv_bfloat162 most = __halves2bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
 #pragma unroll
   for (int i = 0; i < CHUNKS; ++i) {
     const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = __bfloat1622float2(x[e]);
-      top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-    }
+    for (int e = 0; e < 4; ++e) most = __hmax2(most, __habs2(x[e]));
   }
+  float top = fmaxf(__low2float(most), __high2float(most));
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
   if (!WARP) {
@@ -134,19 +137,23 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   }
   const float scale = fmaxf(fmaxf(held, __fdiv_rn(top, code_max<E4M3>())), kScaleMin);
   const float inv = __frcp_rn(scale);
+  {
+    uint8_t* at = dst + (first + row) * p.sd[kv].n + col;
+    const long long step = rows * p.sd[kv].n;
 #pragma unroll
-  for (int i = 0; i < CHUNKS; ++i) {
-    const int c = tid + i * THREADS;
-    if (c >= chunks) break;
-    const int r = c >> cpr_log2;
-    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-    const float2 f0 = __bfloat1622float2(x[0]), f1 = __bfloat1622float2(x[1]),
-                 f2 = __bfloat1622float2(x[2]), f3 = __bfloat1622float2(x[3]);
-    uint2 out;
-    out.x = encode4<E4M3>(f0.x * inv, f0.y * inv, f1.x * inv, f1.y * inv);
-    out.y = encode4<E4M3>(f2.x * inv, f2.y * inv, f3.x * inv, f3.y * inv);
-    *(reinterpret_cast<uint2*>(dst + static_cast<long long>(first + r) * p.sd[kv].n) +
-      (c - (r << cpr_log2))) = out;
+    for (int i = 0; i < CHUNKS; ++i, at += step) {
+      if (tid + i * THREADS >= chunks) break;
+      const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 y = __bfloat1622float2(x[e]);
+        f[2 * e] = y.x * inv;
+        f[2 * e + 1] = y.y * inv;
+      }
+      *reinterpret_cast<uint2*>(at) = make_uint2(encode4<E4M3>(f[0], f[1], f[2], f[3]),
+                                                 encode4<E4M3>(f[4], f[5], f[6], f[7]));
+    }
   }
   if (scale != held) {
     if (tid == 0) *scale_at = scale;
