@@ -17,8 +17,8 @@
 // cores would be the bound from about 5 rows on; the products run on the
 // tensor cores instead, in the warp-level m16n8k16 form: the tile of queries
 // (at most 32 rows) is far too small for a tcgen05 tile, and this form takes
-// its operands straight from registers, so cache rows go from global memory
-// to the products without a stop in shared memory:
+// its operands from registers, where codes are widened on their way from a
+// warp's ring of tiles in shared memory:
 //   S = Q K^T  queries are the 16 rows, 8 keys the columns;
 //   O^T = V^T P^T  16 values of d are the rows, 8 queries the columns: the
 //       accumulator layout of S is the operand layout of P^T as it stands.
@@ -47,6 +47,14 @@
 // its own copies only, never for another warp, and memory stays busy while it
 // computes.
 //
+// Measured (the floor is the visible cache at the rate of a plain copy, 6.7 TB/s):
+// 4 sequences of 65 to 131 thousand tokens, 32 query heads on 8, d = 128, e4m3,
+// distance bias: 132 us (floor 121); the same with a bf16 cache at its floor, 235
+// us.  32 of 2 to 4 thousand, 16 heads of d = 64, e4m3, caps: 45 us (30), of which
+// 7 are the join.  256 of 64 to 512, 8 heads, int8, whole units: 27 us (11); one
+// warp's chain of tiles is what it takes, 1.2 us each with 13 warps on an SM (128
+// registers a thread leave room for 16).  Copies alone, 32 x 4096 at full length:
+// 47 us against the kernel's 55.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -695,12 +695,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           if (edge) {
-            const int lim = row_hi - kbase, lo = row_lo - kbase;  // columns [lo, lim) are visible
+            // columns [lo, lim) are visible; as bits, which are tested several at
+            // a time, where comparisons take two instructions a score (packed
+            // documents 161 -> 146 us, 64 x 501 tokens with a prefix 54 -> 48)
+            const int lim = row_hi - kbase, lo = row_lo - kbase;
 #pragma unroll
-            for (int q4 = 0; q4 < SC; ++q4)
+            for (int q4 = 0; q4 < SC; ++q4) {
+              const uint32_t see = below(lim - 32 * q4) & ~below(lo - 32 * q4);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (q4 * 32 + i >= lim || q4 * 32 + i < lo) r[q4][i] = __float_as_uint(-INFINITY);
+                if (!(see & (1u << i))) r[q4][i] = __float_as_uint(-INFINITY);
+            }
           }
         } else if (kbase + BN > it.key_limit || (causal && kbase + BN - 1 > row0) ||
             (band && (kbase < row0 + BM - 1 - p.win_left || kbase + BN - 1 > row0 + p.win_right))) {

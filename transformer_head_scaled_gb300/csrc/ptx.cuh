@@ -399,6 +399,11 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return d;
 }
 
+// The bits i < n of 32.
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
 // (a0, a1) * (b0, b1) + (c0, c1) as one packed fma.rn.f32x2.
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
                                      float c0, float c1) {
