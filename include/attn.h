@@ -274,7 +274,7 @@ int attn_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
  *   plan, plan_bytes : caller-owned device memory of at least
  *              attn_mask_plan_bytes(B, n_q, n_k) bytes, 16-byte aligned.
  *   B, n_q, n_k >= 1, at most 2^30 tokens (else ATTN_ERR_UNSUPPORTED).
- * One kernel on `stream`, two with doc_ids.
+ * One kernel on `stream`, up to three with doc_ids.
  */
 int attn_mask_plan(int B, int n_q, int n_k, int window_left, int window_right,
                    const int* key_lens, const int* doc_ids, const int* prefix_lens, void* plan,
@@ -317,20 +317,20 @@ int attn_fwd_scored(const void* q, const void* k, const void* v, void* o, float*
  *   dS = P * (dP - D_i) * (1 - tanh^2(s / softcap)),
  *   dQ = scale dS K,  dK = scale dS^T Q,
  * dK and dV summed over the query heads that share a key head, in fp32 and in
- * head order.  The slopes are constants: they get no gradient.
+ * an order that depends on the sizes alone.  The slopes are constants: they get no gradient.
  *   strides  : host array of 24 element counts, three (b, h, row) per tensor in
  *              the order q, k, v, o, dout, dq, dk, dv (k, v, dk, dv have h_kv
  *              heads), each > 0 and a multiple of 8; NULL: contiguous.
  *   workspace, workspace_bytes : at least attn_bwd_scored_workspace_bytes(B, h,
  *              h_kv, n_q, n_k, d_k) bytes, 16-byte aligned; contents on entry do
- *              not matter.
+ *              not matter; calls that may overlap need one each.
  * d_k in {16, 32, 64} (else ATTN_ERR_UNSUPPORTED).  Queries that see no key get
  * dq = 0, keys that no query sees dk = dv = 0.  dq, dk, dv must not overlap the
  * inputs; dout must be finite, in rows that see no key too.  dQ is summed over
  * key tiles in fp32 in the order in which they finish.  Other arguments,
- * roundings and status codes as attn_bwd and attn_fwd_scored.  Three kernels, a
- * fourth where few key tiles make it worth to work on a key head's query heads
- * apart.
+ * roundings and status codes as attn_bwd and attn_fwd_scored.  Three kernels, one
+ * more under a plan, one more where few key tiles make it worth to work on a key
+ * head's query heads apart.
  */
 int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, const void* dout,
                     const float* lse, void* dq, void* dk, void* dv, int B, int h, int h_kv,

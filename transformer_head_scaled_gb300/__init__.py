@@ -11,6 +11,9 @@ from .inputs import MASK_CAUSAL, MASK_KEY_PADDING, MASK_NONE  # noqa: F401
 def __getattr__(name):
     if name in ("attn_fwd", "attn_fwd_f32", "attn_fwd_raw", "attn_fwd_f32_raw", "attn_decode",
                 "decode_workspace_bytes",
+                "attn_mask_plan", "attn_fwd_scored", "attn_bwd_scored", "attn_cache_append",
+                "attn_decode_scored", "mask_plan_bytes", "bwd_scored_workspace_bytes",
+                "decode_scored_workspace_bytes",
                 "load", "AttnError", "status_string", "check"):
         from . import binding
         return getattr(binding, name)

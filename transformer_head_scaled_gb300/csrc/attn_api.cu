@@ -1172,7 +1172,7 @@ int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, 
     return rc;
   const cudaError_t e = launch_bwd(pb, maps, workspace, make_ctx(*di, stream), &mod);
   if (e != cudaSuccess) return cuda_fail(e);
-  g_launches.fetch_add(lay.parts > 1 ? 4 : 3);
+  g_launches.fetch_add(3 + (bwd_few_possible(mod.masked, n_k) ? 1 : 0) + (lay.parts > 1 ? 1 : 0));
   return ATTN_OK;
 }
 

@@ -1159,7 +1159,6 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 // part of the pre-kernel halved the warps in flight there (4 x 4096 tokens, 16
 // heads, d = 64, causal: 45 us in one kernel; 27 us, with these 18 us beside it, in
 // two).
-constexpr int kFewKeys = 16;
 
 // The items dealt out by load: each, heaviest first, to the CTA with the least
 // work so far.  Run by one CTA more of attn_bwd_few_kernel, in the time of the
@@ -1560,7 +1559,7 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   const auto* o = static_cast<const __nv_bfloat16*>(pb.o);
   const auto* dout = static_cast<const __nv_bfloat16*>(pb.dout);
   const int num_qt = static_cast<int>(lay.num_qt);
-  const bool few = mod != nullptr && (mod->masked || pb.n_k <= kFewKeys);
+  const bool few = mod != nullptr && bwd_few_possible(mod->masked, pb.n_k);
   cudaError_t err = cudaSuccess;
   Deal deal{};
   if (few) {

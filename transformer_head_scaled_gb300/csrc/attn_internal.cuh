@@ -261,6 +261,10 @@ struct BwdLayout {
 BwdLayout bwd_layout(int B, int H, int n_q, int d);
 BwdLayout bwd_scored_layout(int B, int H, int HK, int n_q, int n_k, int d);
 bool bwd_head_size_ok(int d);
+// With changed scores, D of queries that see at most this many keys comes from P
+// and dP, in a kernel of its own, which runs where there may be such queries.
+constexpr int kFewKeys = 16;
+inline bool bwd_few_possible(bool masked, int n_k) { return masked || n_k <= kFewKeys; }
 // maps: Q, K, V, dO as 4-D (d, n, H, B) bf16 with a (d, 128, 1, 1) box; dK,
 // dV the same with a (d, 64, 1, 1) box (any strides); the dQ accumulator as 3-D (d, n_q, B*H)
 // fp32 with a (min(d, 32), 64, 1) box; each in the swizzle of its box's row
