@@ -696,7 +696,13 @@ def _strides_of(layouts):
 
 def _strides(*tensors):
     """The (b, h, row) element strides of [B, h, n, d] views.  The stride of a
-    dimension of one entry is never stepped over, whatever the view says."""
+    dimension of one entry is never stepped over, whatever the view says.  None
+    when all are contiguous, which needs no strides."""
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
+        return None
     return _strides_of(tuple([(t.stride(), t.shape) for t in tensors]))
 
 
