@@ -718,6 +718,11 @@ def _workspace(need: int, given, device):
     return torch.empty(need, dtype=torch.uint8, device=device)
 
 
+def _contiguous_like(t):
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -831,13 +836,13 @@ def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         scale = 1.0 / math.sqrt(d)
     with _call_on(dev, stream) as ptr:
         if out is None:
-            out = torch.empty((B, h, n_q, d), dtype=q.dtype, device=dev)
+            out = _contiguous_like(q)
         else:
             _views("q and out", torch.bfloat16, q, out)
             if out.shape != q.shape:
                 raise ValueError("out must be shaped like q")
         if lse is None:
-            lse = torch.empty((B, h, n_q), dtype=torch.float32, device=dev)
+            lse = q.new_empty((B, h, n_q), dtype=torch.float32)
         else:
             _vector("lse", lse, torch.float32, B * h * n_q, dev)
         window = -1 if window is None else window
@@ -954,13 +959,13 @@ def attn_fwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         scale = 1.0 / math.sqrt(d)
     with _call_on(dev, stream) as ptr:
         if out is None:
-            out = torch.empty((B, h, n_q, d), dtype=q.dtype, device=dev)
+            out = _contiguous_like(q)
         else:
             _views("q and out", torch.bfloat16, q, out)
             if out.shape != q.shape:
                 raise ValueError("out must be shaped like q")
         if lse is None:
-            lse = torch.empty((B, h, n_q), dtype=torch.float32, device=dev)
+            lse = q.new_empty((B, h, n_q), dtype=torch.float32)
         else:
             _vector("lse", lse, torch.float32, B * h * n_q, dev)
         rc = attn_fwd_scored_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, h, h_kv, n_q,
@@ -1013,12 +1018,13 @@ def attn_bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
                 raise ValueError(f"{name} must be shaped like {name[1]}")
     with _call_on(dev, stream) as ptr:
         if dq is None:
-            dq = torch.empty((B, h, n_q, d), dtype=q.dtype, device=dev)
+            dq = _contiguous_like(q)
         if dk is None:
-            dk = torch.empty((B, h_kv, n_k, d), dtype=q.dtype, device=dev)
+            dk = _contiguous_like(k)
         if dv is None:
-            dv = torch.empty((B, h_kv, n_k, d), dtype=q.dtype, device=dev)
-        workspace = _workspace(max(bwd_scored_workspace_bytes(B, h, h_kv, n_q, n_k, d), 16), workspace, dev)
+            dv = _contiguous_like(v)
+        workspace = _workspace(max(bwd_scored_workspace_bytes(B, h, h_kv, n_q, n_k, d), 16),
+                               workspace, dev)
         rc = attn_bwd_scored_raw(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse),
                                  _ptr(dq), _ptr(dk), _ptr(dv), B, h, h_kv, n_q, n_k, d,
                                  _strides(q, k, v, o, dout, dq, dk, dv), scale, softcap,
