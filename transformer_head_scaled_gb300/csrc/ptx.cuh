@@ -399,6 +399,13 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   return d;
 }
 
+// max(|a|, |b|, |c|) in one instruction.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The bits i < n of 32.
 __device__ __forceinline__ uint32_t below(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
