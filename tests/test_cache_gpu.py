@@ -344,3 +344,14 @@ def test_two_steps_at_once_on_two_streams():
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.parametrize("window", [63, 64, 2 ** 31 - 1, 2 ** 32, 2 ** 40])
+def test_decode_scored_window_longer_than_the_cache(window):
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(s, generator=g).to(torch.bfloat16).cuda()
+               for s in ((2, 4, 2, 64), (2, 2, 64, 64), (2, 2, 64, 64)))
+    for a, b in zip(binding.attn_decode_scored(q, k, v, window=window),
+                    binding.attn_decode_scored(q, k, v)):
+        assert torch.equal(a, b)
+    binding.check()

@@ -362,6 +362,19 @@ def test_documents_dealt_out_by_load(B, h, hk):
             at += x
 
 
+@pytest.mark.parametrize("n", [5, 300])
+def test_sides_longer_than_the_sequence_bound_nothing(n):
+    whole = binding.attn_mask_plan(2, n, n, device="cuda").clone()
+    for far in (n - 1, n, 2 * n, 2 ** 31 - 1, 2 ** 32, 2 ** 40):
+        assert scored.visible(n, n, left=far, right=far).all()
+        plan = binding.attn_mask_plan(2, n, n, left=far, right=far, device="cuda")
+        q, k, v = (_random((2, 2, n, 16), s) for s in (1, 2, 3))
+        for a, b in zip(binding.attn_fwd_scored(q, k, v, plan=plan),
+                        binding.attn_fwd_scored(q, k, v, plan=whole)):
+            assert torch.equal(a, b), far
+    binding.check()
+
+
 def test_training_step_as_a_captured_graph():
     """Plan, two layers forward and backward captured once and replayed on new
     inputs and documents; dK, dV and O are the eager calls' bit for bit."""

@@ -672,6 +672,8 @@ def _vector(name: str, t, dtype, count: int, device) -> None:
                          f"{device}")
 
 
+_INT_MAX = 0x7fffffff  # what fits the C calls' sizes
+
 _INT64S = {n: ctypes.c_int64 * n for n in (12, 24)}
 
 
@@ -755,6 +757,8 @@ def attn_cache_append(k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torch.T
     if (v_new.shape != k_new.shape or tuple(k_cache.shape) != (B, h, L_max, d)
             or v_cache.shape != k_cache.shape or k_cache.device != k_new.device):
         raise ValueError("k_new, v_new must be [B, h, n_new, d] and the caches [B, h, L_max, d]")
+    if n_new > _INT_MAX or L_max > _INT_MAX:
+        raise ValueError("caches of 2^31 tokens and more are not supported")
     if block_tokens not in (16, 32, 64, 128):
         raise ValueError("block_tokens must be 16, 32, 64 or 128")
     dev = k_new.device
@@ -782,7 +786,8 @@ def decode_scored_workspace_bytes(B: int, h: int, h_kv: int, n_q: int, L_max: in
                                   window: int | None = None) -> int:
     """Scratch bytes attn_decode_scored needs on the current device (0: none)."""
     return int(load().attn_decode_scored_workspace_bytes(
-        B, h, h_kv, n_q, L_max, d, cache_format, -1 if window is None else int(window)))
+        B, h, h_kv, n_q, L_max, d, cache_format,
+        -1 if window is None else min(int(window), _INT_MAX)))
 
 
 def attn_decode_scored_raw(q_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, o_ptr, lse_ptr, B, h, h_kv, n_q,
@@ -818,6 +823,8 @@ def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     if (tuple(k_cache.shape) != (B, h_kv, L_max, d) or v_cache.shape != k_cache.shape
             or h_kv < 1 or h % h_kv != 0 or k_cache.device != q.device):
         raise ValueError("caches must be [B, h_kv, L_max, d] with q's B and d, h a multiple of h_kv")
+    if L_max > _INT_MAX:
+        raise ValueError("caches of 2^31 tokens and more are not supported")
     dev = q.device
     if fmt == CACHE_BF16:
         k_scale = v_scale = None
@@ -845,7 +852,7 @@ def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
             lse = q.new_empty((B, h, n_q), dtype=torch.float32)
         else:
             _vector("lse", lse, torch.float32, B * h * n_q, dev)
-        window = -1 if window is None else window
+        window = -1 if window is None else min(int(window), _INT_MAX)
         workspace = _workspace(
             _decode_scored_bytes(dev.index, B, h, h_kv, n_q, L_max, d, fmt, window), workspace, dev)
         rc = attn_decode_scored_raw(
@@ -861,7 +868,7 @@ def attn_decode_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
 def _not_negative(name: str, x: int) -> int:
     if x < 0:
         raise ValueError(f"{name} must be >= 0 (None: unbounded)")
-    return x
+    return min(int(x), _INT_MAX)
 
 
 @functools.lru_cache(maxsize=256)
@@ -908,6 +915,8 @@ def attn_mask_plan(B: int, n_q: int, n_k: int, left: int | None = None, right: i
         _vector("doc_ids", doc_ids, torch.int32, B * n_q, dev)
         if n_q != n_k:
             raise ValueError("documents need n_q == n_k")
+    if max(B, n_q, n_k) > _INT_MAX:
+        raise ValueError("sequences of 2^31 tokens and more are not supported")
     need = mask_plan_bytes(B, n_q, n_k)
     if plan is not None and (plan.device != dev or not plan.is_contiguous()
                              or _nbytes(plan) < need):
@@ -929,6 +938,8 @@ def _scored_shapes(q, k, v, slopes, plan):
     h_kv, n_k = k.shape[1:3]
     if (tuple(k.shape) != (B, h_kv, n_k, d) or v.shape != k.shape or h_kv < 1 or h % h_kv != 0):
         raise ValueError("k and v must be [B, h_kv, n_k, d] with q's B and d, h a multiple of h_kv")
+    if n_q > _INT_MAX or n_k > _INT_MAX:
+        raise ValueError("sequences of 2^31 tokens and more are not supported")
     _vector("slopes", slopes, torch.float32, h, q.device)
     if plan is not None and (plan.device != q.device or not plan.is_contiguous()
                              or _nbytes(plan) < mask_plan_bytes(B, n_q, n_k)):

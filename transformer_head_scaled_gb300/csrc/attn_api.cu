@@ -1017,7 +1017,7 @@ ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int
 namespace attn {
 namespace {
 
-constexpr int kMostTokens = 1 << 30;  // tokens of a sequence, so that sums of two stay in int
+constexpr int kMostTokens = 1 << 30;  // of a sequence: a place and a side of a mask add up in int
 
 int check_mask_sizes(int B, int n_q, int n_k) {
   if (B < 1 || n_q < 1 || n_k < 1) return ATTN_ERR_INVALID_ARG;
@@ -1076,12 +1076,11 @@ int attn_mask_plan(int B, int n_q, int n_k, int window_left, int window_right,
   if (plan_bytes < mask_layout(B, n_q, n_k).bytes) return ATTN_ERR_INVALID_ARG;
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di)) != ATTN_OK) return rc;
-  const int reach = n_q + n_k;  // a side longer than both sequences bounds nothing
   const MaskProblem pb{B,
                        n_q,
                        n_k,
-                       window_left < reach ? window_left : -1,
-                       window_right < reach ? window_right : -1,
+                       window_left < n_q ? window_left : -1,  // a longer side bounds nothing
+                       window_right < n_k ? window_right : -1,
                        key_lens,
                        doc_ids,
                        prefix_lens};

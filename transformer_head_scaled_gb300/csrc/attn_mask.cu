@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(BLOCK) attn_mask_plan_kernel(const MaskParams 
   const int limit = p.key_lens != nullptr ? min(max(__ldg(p.key_lens + b), 0), p.n_k) : p.n_k;
   const int prefix = p.prefix_lens != nullptr ? min(max(__ldg(p.prefix_lens + b), 0), p.n_k) : 0;
   const bool later_heavier = p.right >= 0;
-  // (left and right are at most n_q + n_k, so nothing here leaves int)
+  // (left < n_q and right < n_k, 2^30 tokens at most, so nothing here leaves int)
   if (block < p.qb) {
     int2 v = make_int2(0, 0);
     if (i < p.n_q) {
