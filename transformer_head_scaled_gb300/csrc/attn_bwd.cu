@@ -66,8 +66,10 @@
 // the query tiles of its whole group (or of a part of it), so that dK and dV of
 // shared heads are sums in tensor memory.  Bound by the chain of a tile pair, as
 // the plain kernel; with caps by registers.  8 x 16 x 4096, d = 64, causal, on one
-// GPU: plain 921 us, by plan 918, with bias 937, with cap 1088, with both 1164.
+// GPU: plain 919 us, by plan 912, with bias 930, with cap 1081, with both 1158.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "attn_internal.cuh"
 #include "ptx.cuh"
@@ -1161,10 +1163,10 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 // kernels' roundings; with up to 16 keys summed so they stay below 3.1e-3, with
 // up to 32 below 3.0e-3, at any length.  (With one key O is that value exactly.)
 //
-// A CTA looks at 256 queries of a head, lists those it has work for, and gives
-// each d / 8 threads.  A kernel of its own: the sums want 64 registers, which as
+// A CTA looks at 256 queries, lists those it has work for, and gives each of them,
+// head by head, d / 8 threads.  A kernel of its own: the sums want 64 registers, which as
 // part of the pre-kernel halved the warps in flight there (4 x 4096 tokens, 16
-// heads, d = 64, causal: 45 us in one kernel; 27 us, with these 18 us beside it, in
+// heads, d = 64, causal: 45 us in one kernel; 26 us, with these 17 us beside it, in
 // two).
 
 // The items dealt out by load: each, heaviest first, to the CTA with the least
@@ -1173,9 +1175,9 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
 // gets many items, or items whose weights fall steadily; with few uneven ones, the
 // heaviest nearly a CTA's share, it gives every CTA as many.  Measured on 4 x 4096
 // tokens, 16 query heads on 4, d = 64, caps, by the documents in a row, 512 items:
-// three 416 -> 381 us, six 337 -> 297, twelve 272 -> 249; on 1 x 8192, 16 heads on
-// one, 512 items: 339 -> 306, 285 -> 262, 212 -> 201; with 1024 items and more no
-// difference.  It takes 8 us for 512 items, which the pre-kernel hides where it has
+// three 416 -> 381 us, six 337 -> 297, twelve 272 -> 249 (with the masks as bits
+// 338, 252 and 219); on 1 x 8192, 16 heads on one, 512 items: 339 -> 306, 285 ->
+// 262, 212 -> 201; with 1024 items and more no difference.  It takes 8 us for 512 items, which the pre-kernel hides where it has
 // kDealBytes to move: below, 8 x 1000 tokens, d = 32, 59 us became 67.
 struct Deal {
   int* next;  // [items], then [ctas] the first ones; null: nothing to do
@@ -1238,7 +1240,7 @@ template <int D>
 __global__ void __launch_bounds__(256)
     attn_bwd_few_kernel(const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,
                         uint8_t* __restrict__ cst, int H, int n_q, int num_qt, RowStrides sdo,
-                        const PreMod mod, const Deal deal) {
+                        const PreMod mod, int heads, const Deal deal) {
   grid_launch_dependents();
   if (deal.next != nullptr && blockIdx.x == 0) {
     const int4 h = __ldg(mod.header);
@@ -1248,10 +1250,13 @@ __global__ void __launch_bounds__(256)
   const int block = blockIdx.x - (deal.next != nullptr);
   constexpr int TPR = D / 8;  // threads a row
   __shared__ int s_row[256], s_first[256], s_seen[256], s_n;
-  const int rows = (n_q + 255) / 256;  // CTAs a head
-  const int bh = block / rows;
-  const int i0 = (block - bh * rows) * 256;
-  const long long bb = bh / H, hh = bh % H;
+  // the CTA's 256 rows, of one batch entry, and its heads
+  const int rows = (n_q + 255) / 256, groups = (H + heads - 1) / heads;
+  const unsigned rest = static_cast<unsigned>(block) / groups;
+  const int h0 = (block - rest * groups) * heads, hn = min(heads, H - h0);
+  const unsigned b32 = rest / rows;
+  const int i0 = (rest - b32 * rows) * 256;
+  const long long bb = b32;
   if (threadIdx.x == 0) s_n = 0;
   __syncthreads();
   {
@@ -1271,60 +1276,65 @@ __global__ void __launch_bounds__(256)
     }
   }
   __syncthreads();
-  const int n = s_n, sub = threadIdx.x % TPR;
-  if (n > 0) {
-    const long long hk = hh / mod.group;
+  // the rows found, of every head
+  const int n = s_n * hn, sub = threadIdx.x % TPR;
+  for (int w0 = 0; w0 < n; w0 += 256 / TPR) {
+    const int item = w0 + threadIdx.x / TPR;
+    const bool own = item < n;
+    const int at = own ? item / hn : 0, hh = h0 + (own ? item - at * hn : 0);
+    const int i = own ? s_row[at] : 0, j0 = own ? s_first[at] : 0;
+    const int seen = own ? s_seen[at] : 0;
+    const long long bh = bb * H + hh, hk = hh / mod.group;
     const float slope = mod.slopes != nullptr ? __ldg(mod.slopes + hh) : 0.f;
     const __nv_bfloat16* kp = mod.k + bb * mod.sk.b + hk * mod.sk.h + sub * 8;
     const __nv_bfloat16* vp = mod.v + bb * mod.sv.b + hk * mod.sv.h + sub * 8;
-    for (int w0 = 0; w0 < n; w0 += 256 / TPR) {
-      const int at = w0 + threadIdx.x / TPR;
-      const int i = at < n ? s_row[at] : 0, j0 = at < n ? s_first[at] : 0;
-      const int seen = at < n ? s_seen[at] : 0;
-      uint4 qv = make_uint4(0u, 0u, 0u, 0u), a = qv;
-      float l = 0.f;
-      if (at < n) {
-        qv = *reinterpret_cast<const uint4*>(mod.q + bb * mod.sq.b + hh * mod.sq.h +
-                                             i * mod.sq.n + sub * 8);
-        a = *reinterpret_cast<const uint4*>(dout + bb * sdo.b + hh * sdo.h + i * sdo.n + sub * 8);
-        l = lse[static_cast<size_t>(bh) * n_q + i];
-      }
-      const int most = __reduce_max_sync(0xffffffffu, seen);
-      float exact = 0.f;
-      // four keys' loads in flight at a time
-      for (int x0 = 0; x0 < most; x0 += 4) {
-        float s[4], dp[4];
+    uint4 qv = make_uint4(0u, 0u, 0u, 0u), a = qv;
+    float l = 0.f;
+    if (own) {
+      qv = *reinterpret_cast<const uint4*>(mod.q + bb * mod.sq.b + hh * mod.sq.h +
+                                           i * mod.sq.n + sub * 8);
+      a = *reinterpret_cast<const uint4*>(dout + bb * sdo.b + hh * sdo.h + i * sdo.n + sub * 8);
+      l = lse[static_cast<size_t>(bh) * n_q + i];
+    }
+    const int most = __reduce_max_sync(0xffffffffu, seen);
+    float exact = 0.f;
+    // four keys' loads in flight at a time
+    for (int x0 = 0; x0 < most; x0 += 4) {
+      uint4 kk[4], vv[4];
+      float s[4], dp[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          s[y] = dp[y] = 0.f;
-          if (x0 + y < seen) {
-            const long long j = j0 + x0 + y;
-            s[y] = dot8(qv, *reinterpret_cast<const uint4*>(kp + j * mod.sk.n));
-            dp[y] = dot8(a, *reinterpret_cast<const uint4*>(vp + j * mod.sv.n));
-          }
+      for (int y = 0; y < 4; ++y) {
+        // (past the last key: the last one again, not counted below)
+        const long long j = j0 + max(min(x0 + y, seen - 1), 0);
+        kk[y] = *reinterpret_cast<const uint4*>(kp + j * mod.sk.n);
+        vv[y] = *reinterpret_cast<const uint4*>(vp + j * mod.sv.n);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        s[y] = dot8(qv, kk[y]);
+        dp[y] = dot8(a, vv[y]);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+#pragma unroll
+        for (int m = TPR / 2; m > 0; m >>= 1) {
+          s[y] += __shfl_xor_sync(0xffffffffu, s[y], m);
+          dp[y] += __shfl_xor_sync(0xffffffffu, dp[y], m);
         }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-#pragma unroll
-          for (int m = TPR / 2; m > 0; m >>= 1) {
-            s[y] += __shfl_xor_sync(0xffffffffu, s[y], m);
-            dp[y] += __shfl_xor_sync(0xffffffffu, dp[y], m);
-          }
-          s[y] *= mod.scale;
-          if (mod.softcap > 0.f) s[y] = mod.softcap * tanhf(s[y] / mod.softcap);
-          s[y] -= slope * fabsf(static_cast<float>(i - (j0 + x0 + y)));
-          if (x0 + y < seen) exact = fmaf(expf(s[y] - l), dp[y], exact);
-        }
+        s[y] *= mod.scale;
+        if (mod.softcap > 0.f) s[y] = mod.softcap * tanhf(s[y] / mod.softcap);
+        s[y] -= slope * fabsf(static_cast<float>(i - (j0 + x0 + y)));
+        if (x0 + y < seen) exact = fmaf(expf(s[y] - l), dp[y], exact);
       }
-      if (at < n && sub == 0 && isfinite(l)) {
-        const int qt = i / BM, r = i % BM;
-        uint8_t* row = cst +
-                       (static_cast<size_t>(bh) * num_qt + qt) * static_cast<size_t>(CONST_TILE_BYTES) +
-                       (r & 7) * 16 + (r >> 3) * 256;
-        const uint2 pd = split3_bf16(-exact);
-        *reinterpret_cast<uint16_t*>(row + 6) = static_cast<uint16_t>(pd.x);
-        *reinterpret_cast<uint32_t*>(row + 8) = (pd.x >> 16) | (pd.y << 16);
-      }
+    }
+    if (own && sub == 0 && isfinite(l)) {
+      const int qt = i / BM, r = i % BM;
+      uint8_t* row = cst +
+                     (static_cast<size_t>(bh) * num_qt + qt) * static_cast<size_t>(CONST_TILE_BYTES) +
+                     (r & 7) * 16 + (r >> 3) * 256;
+      const uint2 pd = split3_bf16(-exact);
+      *reinterpret_cast<uint16_t*>(row + 6) = static_cast<uint16_t>(pd.x);
+      *reinterpret_cast<uint32_t*>(row + 8) = (pd.x >> 16) | (pd.y << 16);
     }
   }
 }
@@ -1343,20 +1353,20 @@ __global__ void __launch_bounds__(256)
     attn_bwd_pre_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                         const float* __restrict__ lse, uint8_t* __restrict__ cst,
                         float* __restrict__ dq_acc, int H, int n_q, int num_qt, float inv_scale,
-                        long long rows, RowStrides so, RowStrides sdo, const PreMod mod, bool few) {
+                        RowStrides so, RowStrides sdo, const PreMod mod, bool few) {
   // the main kernel may start launching now: it waits for this grid to
   // complete before it reads the constants or adds into dq_acc
   grid_launch_dependents();
   constexpr int TPR = D / 8;  // threads a row
-  const long long row = static_cast<long long>(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR;
+  // a CTA's rows are of one head (whole tiles of 128 rows, 256 / TPR of them divides)
+  const unsigned per_head = static_cast<unsigned>(num_qt) * (BM / (256 / TPR));
+  const unsigned bh = blockIdx.x / per_head;
+  const int i = static_cast<int>((blockIdx.x - bh * per_head) * (256 / TPR) + threadIdx.x / TPR);
   const int sub = threadIdx.x % TPR;
-  const bool in = row < rows;
-  const long long per_head = static_cast<long long>(num_qt) * BM;
-  const long long bh = in ? row / per_head : 0;
-  const int i = in ? static_cast<int>(row - bh * per_head) : 0;  // query index
-  const bool valid = in && i < n_q;
+  const bool valid = i < n_q;
   const size_t src = (static_cast<size_t>(bh) * n_q + i) * D + sub * 8;  // accumulator row
-  const long long bb = bh / H, hh = bh % H;
+  const unsigned b32 = bh / static_cast<unsigned>(H);
+  const long long bb = b32, hh = bh - b32 * H;
   // does the other kernel write this query's D?
   bool skip = false;
   if (SCORED && few) {
@@ -1381,7 +1391,7 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int m = TPR / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-  if (in && sub < 2) {
+  if (sub < 2) {
     // sub 0: columns 0-7 of this query's row (b in 0-2, -D in 3-5); sub 1:
     // columns 8-15, zero
     const int qt = i / BM, n = i % BM;
@@ -1570,7 +1580,13 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   cudaError_t err = cudaSuccess;
   Deal deal{};
   if (few) {
-    long long blocks = bh * ((pb.n_q + 255) / 256);  // no more than pre_blocks
+    // four CTAs an SM are resident: heads of the same rows share one as far as it
+    // takes for all to be
+    const long long tiles = static_cast<long long>(pb.B) * ((pb.n_q + 255) / 256);
+    const long long shares = std::min<long long>(
+        pb.H, std::max<long long>(1, 4LL * ctx.num_sms / tiles));  // CTAs of the same rows
+    const int heads = static_cast<int>((pb.H + shares - 1) / shares);
+    long long blocks = tiles * ((pb.H + heads - 1) / heads);  // no more than pre_blocks
     const long long items = bh / mod->group * ((pb.n_k + BN - 1) / BN) * mod->parts;
     if (mod->masked && items > ctx.num_sms && items <= kDealPerCta * ctx.num_sms &&
         items <= kMostDealt && ctx.num_sms <= kMostCtas &&
@@ -1583,17 +1599,16 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
       ++blocks;
     }
     attn_bwd_few_kernel<D><<<static_cast<unsigned>(blocks), 256, 0, ctx.stream>>>(
-        dout, pb.lse, cst, pb.H, pb.n_q, num_qt, pb.sdo, pm, deal);
+        dout, pb.lse, cst, pb.H, pb.n_q, num_qt, pb.sdo, pm, heads, deal);
     err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     err = launch_dependent(attn_bwd_pre_kernel<D, true>, dim3(static_cast<unsigned>(pre_blocks)),
                            dim3(256), 0, ctx.stream, o, dout, pb.lse, cst, dq_acc, pb.H, pb.n_q,
-                           num_qt, 1.f / pb.scale, rows, pb.so, pb.sdo, pm, true);
+                           num_qt, 1.f / pb.scale, pb.so, pb.sdo, pm, true);
   } else {
     auto* pre = mod != nullptr ? attn_bwd_pre_kernel<D, true> : attn_bwd_pre_kernel<D, false>;
     pre<<<static_cast<unsigned>(pre_blocks), 256, 0, ctx.stream>>>(
-        o, dout, pb.lse, cst, dq_acc, pb.H, pb.n_q, num_qt, 1.f / pb.scale, rows, pb.so, pb.sdo,
-        pm, false);
+        o, dout, pb.lse, cst, dq_acc, pb.H, pb.n_q, num_qt, 1.f / pb.scale, pb.so, pb.sdo, pm, false);
     err = cudaGetLastError();
   }
   if (err != cudaSuccess) return err;
