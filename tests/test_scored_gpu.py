@@ -223,6 +223,25 @@ def test_gradients_of_short_documents(n, docs):
     _check_grads(got, want)
 
 
+@pytest.mark.parametrize("B,h,hk,n_q,n_k,d", [(2, 2, 1, 40, 2, 64), (2, 2, 2, 300, 7, 32),
+                                              (1, 4, 2, 5, 16, 16), (2, 2, 1, 40, 17, 64),
+                                              (80, 16, 4, 20, 20, 16), (90, 7, 7, 9, 9, 64)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_gradients_of_queries_with_few_keys(B, h, hk, n_q, n_k, d, masked):
+    """Without a plan and with one, few heads and many, capped and biased."""
+    plan = binding.attn_mask_plan(B, n_q, n_k, right=0, device="cuda") if masked else None
+    see = [scored.visible(n_q, n_k, right=0 if masked else None)] * B
+    q, dout = _random((B, h, n_q, d), 1, 2.0), _random((B, h, n_q, d), 4)
+    k, v = _random((B, hk, n_k, d), 2), _random((B, hk, n_k, d), 3)
+    kw = dict(softcap=20.0, slopes=_slopes(h), plan=plan)
+    o, lse = binding.attn_fwd_scored(q, k, v, **kw)
+    got = binding.attn_bwd_scored(q, k, v, o, lse, dout, **kw)
+    binding.check()
+    want = scored.gradients(_f64(q), _f64(k), _f64(v), _f64(dout), see, 1 / math.sqrt(d), 20.0,
+                            _f64(_slopes(h)))
+    _check_grads(got, want)
+
+
 def test_gradients_are_those_of_finite_differences():
     """Along random directions, in float64, of the reference's forward."""
     B, h, hk, n, d, cap = 1, 4, 2, 40, 16, 5.0
