@@ -66,7 +66,7 @@
 // the query tiles of its whole group (or of a part of it), so that dK and dV of
 // shared heads are sums in tensor memory.  Bound by the chain of a tile pair, as
 // the plain kernel; with caps by registers.  8 x 16 x 4096, d = 64, causal, on one
-// GPU: plain 919 us, by plan 912, with bias 930, with cap 1081, with both 1158.
+// GPU: plain 919 us, by plan 912, with bias 930, with cap 1081, with both 1190.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -374,7 +374,9 @@ __device__ __forceinline__ uint64_t sdesc_swz(uint32_t smem_addr, uint32_t lbo_b
 // thread's.  Keys after their query get 2 slope (j - i) less; SLOW: some visible
 // key is, or some query of the warp's tile does not see some key (two loops
 // instead of branches in one, which would keep its instructions from being
-// interleaved).  `ahead` = j - the first of the 64 queries, f = -2 slope in log2
+// interleaved).  LINE: every key of the warp's is visible and at or after all of its
+// queries, so that the correction is linear too (f * ahead is in `bias` then).
+// `ahead` = j - the first of the 64 queries, f = -2 slope in log2
 // units; columns outside [lim, hi) are forbidden for this key.
 //
 // With a cap, from r = 1 / (1 + 2^(2 y log2(e))): tanh(y) = 1 - 2 r, 1 -
@@ -383,7 +385,7 @@ __device__ __forceinline__ uint64_t sdesc_swz(uint32_t smem_addr, uint32_t lbo_b
 // wide cap, by the polynomials of CapPoly.  (Under the usual caps these are slower
 // here, 487 against 403 us on packed documents of 4 x 4096 tokens: registers bound
 // this loop, not the special-function unit.)
-template <int MODE, bool SLOW, bool POLY, class Emit>
+template <int MODE, bool SLOW, bool POLY, bool LINE, class Emit>
 __device__ __forceinline__ void scored_probabilities(const Params& p, const uint32_t (&s0)[32],
                                                      const uint32_t (&s1)[32], float (&pf)[64],
                                                      int lim, int hi, float bias, float ahead,
@@ -394,7 +396,7 @@ __device__ __forceinline__ void scored_probabilities(const Params& p, const uint
   // The visible columns as bits, which are tested several at a time, where
   // comparisons take two instructions a score (packed documents with caps 308 ->
   // 272 us); not with caps and bias, where registers are short (big causal 1164
-  // us by comparisons, 1200 by bits).
+  // us by comparisons, 1200 by bits, without LINE).
   constexpr bool BITS = !(CAP && BIAS);
   const uint32_t see[2] = {below(hi) & ~below(lim), below(hi - 32) & ~below(lim - 32)};
 #pragma unroll
@@ -438,6 +440,12 @@ __device__ __forceinline__ void scored_probabilities(const Params& p, const uint
       for (int e = 0; e < 8; e += 2)
         fma2(x[e], x[e + 1], __uint_as_float(src[e]), __uint_as_float(src[e + 1]), c, c, bias,
              bias);
+    }
+    if constexpr (LINE) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2)
+        fma2(x[e], x[e + 1], static_cast<float>(c0 + e), static_cast<float>(c0 + e + 1), -f, -f,
+             x[e], x[e + 1]);
     }
     if constexpr (SLOW) {
 #pragma unroll
@@ -1004,10 +1012,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           float bias = 0.f, f = 0.f;
           const int ahead = j - qt * BM - 64 * half;
           bool slow = __any_sync(0xffffffffu, lim > 0 || hi < 64);
+          bool line = false;
           if constexpr ((MODE & kBias) != 0) {
             const float slope2 = LOG2E * __ldg(p.slopes + q_head(item, member));
             bias = slope2 * static_cast<float>(j - qt * BM);
             f = -2.f * slope2;
+            // (with caps only: no mask 2767 -> 2211 us for 8 x 16 x 4096, causal 1155 ->
+            // 1190, a third loop; without caps 1620 -> 1587, short causal 152 -> 156)
+            line = CAP && !slow && __all_sync(0xffffffffu, ahead >= 63);
             // a query of this half that sees this key and comes before it
             slow = slow || __any_sync(0xffffffffu, lim < hi && lim < ahead);
           }
@@ -1030,16 +1042,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               big = max3(big, fabsf(__uint_as_float(s0[e])), fabsf(__uint_as_float(s1[e])));
             poly = __all_sync(0xffffffffu, big <= p.cap.small);
             if (poly)
-              scored_probabilities<MODE, true, true>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
-                                                     emit);
+              scored_probabilities<MODE, true, true, false>(p, s0, s1, pf, lim, hi, bias, fahead, f,
+                                                            lse, emit);
           }
           if ((MODE & kWide) == 0 || !poly) {
-            if (slow)
-              scored_probabilities<MODE, true, false>(p, s0, s1, pf, lim, hi, bias, fahead, f, lse,
-                                                      emit);
+            if (CAP && (MODE & kBias) != 0 && line)
+              scored_probabilities<MODE, false, false, CAP && (MODE & kBias) != 0>(
+                  p, s0, s1, pf, lim, hi, fmaf(f, fahead, bias), fahead, f, lse, emit);
+            else if (slow)
+              scored_probabilities<MODE, true, false, false>(p, s0, s1, pf, lim, hi, bias, fahead,
+                                                             f, lse, emit);
             else
-              scored_probabilities<MODE, false, false>(p, s0, s1, pf, lim, hi, bias, fahead, f,
-                                                       lse, emit);
+              scored_probabilities<MODE, false, false, false>(p, s0, s1, pf, lim, hi, bias, fahead,
+                                                              f, lse, emit);
           }
           if (!ok) break;
         } else {
