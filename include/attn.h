@@ -412,8 +412,10 @@ int attn_cache_append(const void* k_new, const void* v_new, void* k_cache, void*
  *   d_k      : 16, 32, 64 or 128, B*h*n_q <= 2^24, L_max <= 2^30 and fewer than
  *              2^31 groups of 16 keys over all sequences and key heads (else
  *              ATTN_ERR_UNSUPPORTED).
- * 8-bit codes enter the products exactly; probabilities are rounded to f16
- * (8-bit caches) or bf16 before the second product.
+ * 8-bit codes enter the products exactly; before the second product a bf16
+ * cache's probabilities are rounded to bf16, an 8-bit cache's probabilities times
+ * their value scales to f16, relative to the row's largest such product (normal
+ * numbers down to 2^-21 of it), whatever the scales of other blocks are.
  */
 int attn_decode_scored(const void* q, const void* k_cache, const void* v_cache,
                        const float* k_scale, const float* v_scale, void* o, float* lse, int B,

@@ -1008,7 +1008,7 @@ ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int
   // the sequences' first tiles, then two partial results per warp
   plan.part_off = (static_cast<size_t>(B) + 1 + 3) / 4 * 4;
   plan.workspace_bytes = (plan.part_off + static_cast<size_t>(plan.warps) * 2 * plan.row_tile *
-                                              (d + 2)) * sizeof(float);
+                                              (d + kPartTail)) * sizeof(float);
   return plan;
 }
 

@@ -27,11 +27,18 @@
 // rows of O^T likewise, so a lane's 16 consecutive bytes of a value row are.
 //
 // 8-bit codes are widened to f16, which holds both kinds exactly; q is
-// brought to f16 by a power of two per row (exact down to 2^-25 of the row's
-// largest entry), P and the value scales are multiplied in fp32 (relative to
-// the largest value scale so far) before the rounding to f16.  A bf16 cache
-// multiplies in bf16, P rounded to bf16 as in the forward.  Softmax
-// statistics, scores and accumulators are fp32.
+// brought to f16 by a power of two per row (within 2^-25 of the row's
+// largest entry), and P times the value scale is rounded to f16 as the operand of
+// the second product:
+//   2^(x_j + log2 v_j - m' + 7),  m' a running maximum of x_j + log2 v_j of its own,
+// so that its precision follows what a key adds to the output, whatever the scales
+// of keys without weight are, and 2^-21 of the largest of them is still a normal
+// f16 number.  The row sum takes exponentials relative to the scores' maximum,
+// in fp32.  (With one exponential for both, relative to the largest scale so far, a
+// block of large values and no weight took the others' P out of f16's range: O off
+// by 1 % at 2^14 times their scale, by 20 % at 2^18.)  A bf16 cache multiplies in
+// bf16, P rounded to bf16 as in the forward.  Softmax statistics, scores and
+// accumulators are fp32.
 //
 // Work split, two ways (scored_decode_plan chooses):
 //  * whole: every warp takes whole units (a unit is one sequence, key head and
@@ -76,6 +83,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A running maximum is kept until a score exceeds it by more than this (log2
 // units): P stays below 2^8, harmless for f16 and the fp32 accumulators.
 constexpr float kRescale = 8.0f;
+// 8-bit caches: the operand of the second product is 2^7 at its running maximum,
+// below 2^15 with the above, inside f16's range.
+constexpr float kLift = 7.0f;
 
 struct ScoredDecParams {
   const __nv_bfloat16* q;
@@ -83,7 +93,7 @@ struct ScoredDecParams {
   const float* v_scale;
   __nv_bfloat16* o;
   float* lse;
-  float* part;        // [warp][2][query rows][D + 2]: O, running maximum, row sum
+  float* part;        // [warp][2][query rows][D + kPartTail]: a part of a row's result
   unsigned* first;  // split: [B + 1], the list index of each sequence's first tile, and the total
   const int* cache_lens;
   const float* slopes;
@@ -276,6 +286,12 @@ struct Cursor {
     return true;
   }
 };
+
+// Accumulators relative to 2^from, over a row sum relative to 2^m: times this
+// factor twice (its square may leave fp32 where the result does not).
+__device__ __forceinline__ float value_factor(float from, float m) {
+  return from == -INFINITY ? 0.f : ex2(0.5f * (from - m));
+}
 
 // Tiles per warp: an equal share, kMinTiles at least.
 __device__ __forceinline__ unsigned share_of(unsigned total, int warps) {
@@ -507,19 +523,19 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
       nslope[m][r] = p.slopes != nullptr && in ? -__ldg(p.slopes + head) * kLog2e : 0.f;
     }
   }
-  float m_run[MQ][2], l_run[MQ][2];
+  // maximum and sum of a row; mv_run: maximum of the scores times their value scales
+  float m_run[MQ][2], l_run[MQ][2], mv_run[MQ][2];
   float acc[C::MT][NR][4];
 #pragma unroll
   for (int m = 0; m < MQ; ++m)
 #pragma unroll
-    for (int r = 0; r < 2; ++r) m_run[m][r] = -INFINITY, l_run[m][r] = 0.f;
+    for (int r = 0; r < 2; ++r) m_run[m][r] = mv_run[m][r] = -INFINITY, l_run[m][r] = 0.f;
 #pragma unroll
   for (int i = 0; i < C::MT; ++i)
 #pragma unroll
     for (int n = 0; n < NR; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.f;
-  float vref = 0.f, inv_vref = 0.f;  // the value scale that P is held relative to
 
   for (int k = 0; k < seg; ++k, ++it) {
     const int base = base0 + k * KT;
@@ -568,9 +584,13 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
     // or of the window
     const bool edge = base + KT > L - p.n_q + 1 || base < last_lo;
 
+    float lv[NG];  // the groups' value scales in log2 units (a scale of 0: -inf)
+#pragma unroll
+    for (int n = 0; n < NG; ++n) lv[n] = Q8 ? __log2f(vs[n]) : 0.f;
+
     // ---- scores in log2 units are s * f (f = 1 once the cap or the bias is
-    // in), masked; mx: this lane's largest of a row
-    float mx[MQ][2], f[MQ][2][NG];
+    // in), masked; mx: this lane's largest of a row, mxv: with their value scales
+    float mx[MQ][2], mxv[MQ][2], f[MQ][2][NG];
 #pragma unroll
     for (int m = 0; m < MQ; ++m) {
 #pragma unroll
@@ -628,31 +648,26 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
               if (col >= hi || col < lo) s[m][n][2 * r + c] = -INFINITY;
             }
         }
-        mx[m][r] = -INFINITY;
+        mx[m][r] = mxv[m][r] = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
-          mx[m][r] = fmaxf(mx[m][r], f[m][r][n] * fmaxf(fmaxf(s[m][2 * n][2 * r], s[m][2 * n][2 * r + 1]),
-                                                        fmaxf(s[m][2 * n + 1][2 * r],
-                                                              s[m][2 * n + 1][2 * r + 1])));
+        for (int n = 0; n < NG; ++n) {
+          const float top = f[m][r][n] * fmaxf(fmaxf(s[m][2 * n][2 * r], s[m][2 * n][2 * r + 1]),
+                                               fmaxf(s[m][2 * n + 1][2 * r],
+                                                     s[m][2 * n + 1][2 * r + 1]));
+          mx[m][r] = fmaxf(mx[m][r], top);
+          if (Q8) mxv[m][r] = fmaxf(mxv[m][r], top + lv[n]);
+        }
       }
     }
     bool grow = false;
 #pragma unroll
     for (int m = 0; m < MQ; ++m)
 #pragma unroll
-      for (int r = 0; r < RS; ++r) grow |= mx[m][r] > m_run[m][r] + kRescale;
-    float vtop = 0.f;
-    if (Q8) {
-#pragma unroll
-      for (int n = 0; n < NG; ++n) vtop = fmaxf(vtop, vs[n]);
-    }
-    if (__any_sync(0xffffffffu, grow || (Q8 && vtop > vref))) {
-      float vfac = 1.f;
-      if (Q8 && vtop > vref) {
-        vfac = vref / (2.f * vtop);  // 0 the first time; room for the scales to come
-        vref = 2.f * vtop;
-        inv_vref = 1.f / vref;
+      for (int r = 0; r < RS; ++r) {
+        grow |= mx[m][r] > m_run[m][r] + kRescale;
+        if (Q8) grow |= mxv[m][r] > mv_run[m][r] + kRescale;
       }
+    if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
       for (int m = 0; m < MQ; ++m) {
 #pragma unroll
@@ -665,7 +680,16 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
             m_run[m][r] = top;
             l_run[m][r] *= alpha;
           }
-          alpha *= vfac;
+          if (Q8) {  // the accumulators follow the other maximum
+            alpha = 1.f;
+            top = mxv[m][r];
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            if (top > mv_run[m][r] + kRescale) {
+              alpha = ex2(mv_run[m][r] - top);
+              mv_run[m][r] = top;
+            }
+          }
           // this lane's accumulator columns are queries 2t and 2t + 1
           const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t);
           const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);
@@ -679,38 +703,29 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
         }
       }
     }
-    // ---- P, its row sums, and P^T as the operand of O^T.  A group's value
-    // scale rides in the exponent (down to 2^-100 of the reference, so that the
-    // group's share of the row sum can be had back).
-    float lv[NG], unlv[NG];
-    if (Q8) {
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        lv[n] = fmaxf(__log2f(vs[n] * inv_vref), -100.f);
-        unlv[n] = ex2(-lv[n]);
-      }
-    }
+    // ---- P, its row sums, and P^T (times the value scales) as the operand of O^T
     uint32_t pb[NG][NR][2];
 #pragma unroll
     for (int m = 0; m < MQ; ++m) {
 #pragma unroll
       for (int r = 0; r < RS; ++r) {
         const float neg_m = m_run[m][r] == -INFINITY ? 0.f : -m_run[m][r];
+        const float neg_mv = mv_run[m][r] == -INFINITY ? 0.f : kLift - mv_run[m][r];
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
-          const float off = Q8 ? neg_m + lv[n] : neg_m, fn = f[m][r][n];
-          const float p0 = ex2(fmaf(s[m][2 * n][2 * r], fn, off)),
-                      p1 = ex2(fmaf(s[m][2 * n][2 * r + 1], fn, off)),
-                      p2 = ex2(fmaf(s[m][2 * n + 1][2 * r], fn, off)),
-                      p3 = ex2(fmaf(s[m][2 * n + 1][2 * r + 1], fn, off));
-          const float sum = (p0 + p1) + (p2 + p3);
+          const float fn = f[m][r][n];
+          const float s0 = s[m][2 * n][2 * r], s1 = s[m][2 * n][2 * r + 1],
+                      s2 = s[m][2 * n + 1][2 * r], s3 = s[m][2 * n + 1][2 * r + 1];
+          const float p0 = ex2(fmaf(s0, fn, neg_m)), p1 = ex2(fmaf(s1, fn, neg_m)),
+                      p2 = ex2(fmaf(s2, fn, neg_m)), p3 = ex2(fmaf(s3, fn, neg_m));
+          l_run[m][r] += (p0 + p1) + (p2 + p3);
           if (Q8) {
-            l_run[m][r] = fmaf(sum, unlv[n], l_run[m][r]);
-            const __half2 y = __floats2half2_rn(p0, p1), z = __floats2half2_rn(p2, p3);
+            const float off = neg_mv + lv[n];
+            const __half2 y = __floats2half2_rn(ex2(fmaf(s0, fn, off)), ex2(fmaf(s1, fn, off))),
+                          z = __floats2half2_rn(ex2(fmaf(s2, fn, off)), ex2(fmaf(s3, fn, off)));
             pb[n][2 * m + r][0] = *reinterpret_cast<const uint32_t*>(&y);
             pb[n][2 * m + r][1] = *reinterpret_cast<const uint32_t*>(&z);
           } else {
-            l_run[m][r] += sum;
             pb[n][2 * m + r][0] = pack_bf16x2(p0, p1);
             pb[n][2 * m + r][1] = pack_bf16x2(p2, p3);
           }
@@ -801,7 +816,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
       l_run[m][r] += __shfl_xor_sync(0xffffffffu, l_run[m][r], 2);
     }
   const bool whole_unit = it - seg_it == cur.s.tiles;
-  float* part = p.part + (static_cast<long long>(w) * 2 + (leads ? 0 : 1)) * ROWS * (D + 2);
+  float* part = p.part + (static_cast<long long>(w) * 2 + (leads ? 0 : 1)) * ROWS * (D + kPartTail);
 #pragma unroll
   for (int x = 0; x < NR; ++x) {
 #pragma unroll
@@ -809,18 +824,21 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
       // this lane's accumulators hold query rows 2t + c of the 8-row tile x
       const float mm = __shfl_sync(0xffffffffu, m_run[x / 2][x & 1], 8 * t + 4 * c);
       const float ll = __shfl_sync(0xffffffffu, l_run[x / 2][x & 1], 8 * t + 4 * c);
+      // what the accumulators are relative to
+      const float from = Q8 ? __shfl_sync(0xffffffffu, mv_run[x / 2][x & 1], 8 * t + 4 * c) - kLift : mm;
       const int row = x * 8 + 2 * t + c;
       if (row >= rows) continue;
       if (whole_unit) {
         const int gr = rt * ROWS + row;
         const int in_group = p.n_q == 1 ? gr : gr / p.n_q, qi = gr - in_group * p.n_q;
         const int head = hk * p.G + in_group;
-        const float inv = (ll > 0.f ? 1.f / ll : 0.f) * (Q8 ? vref : 1.f);
+        const float fac = Q8 ? value_factor(from, mm) : 1.f;
+        const float inv = (ll > 0.f ? 1.f / ll : 0.f) * fac;
         __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
         uint32_t word[C::MT];
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
-          word[i] = pack_bf16x2(acc[i][x][c] * inv, acc[i][x][2 + c] * inv);
+          word[i] = pack_bf16x2(acc[i][x][c] * fac * inv, acc[i][x][2 + c] * fac * inv);
         constexpr int V = C::VE / 2 < 4 ? C::VE / 2 : 4;  // words side by side
 #pragma unroll
         for (int i = 0; i < C::MT; i += V) {
@@ -836,13 +854,12 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
           p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
               ll > 0.f ? (mm + __log2f(ll)) * kLn2 : -INFINITY;
       } else {
-        float* at = part + row * (D + 2);
-        const float f = Q8 ? vref : 1.f;
+        float* at = part + row * (D + kPartTail);
 #pragma unroll
         for (int i = 0; i < C::MT; ++i)
           *reinterpret_cast<float2*>(at + val_elem<C>(2 * i, g)) =
-              make_float2(acc[i][x][c] * f, acc[i][x][2 + c] * f);
-        if (g == 0) *reinterpret_cast<float2*>(at + D) = make_float2(mm, ll);
+              make_float2(acc[i][x][c], acc[i][x][2 + c]);
+        if (g == 0) *reinterpret_cast<float4*>(at + D) = make_float4(mm, ll, from, 0.f);
       }
     }
   }
@@ -880,26 +897,55 @@ __global__ void __launch_bounds__(256)
   const int n = tiles > 0 ? static_cast<int>((u0 + tiles - 1) / share - w0) + 1 : 0;
   if (n == 1) return;
   // part i: the first warp's run may have begun before the unit
-  const float* part = p.part + (static_cast<long long>(w0) * 2 * ROWS + row) * (D + 2);
-  constexpr int NEXT = 2 * ROWS * (D + 2);
-  const int late = share * w0 < u0 ? ROWS * (D + 2) : 0;
+  const float* part = p.part + (static_cast<long long>(w0) * 2 * ROWS + row) * (D + kPartTail);
+  constexpr int NEXT = 2 * ROWS * (D + kPartTail);
+  const int late = share * w0 < u0 ? ROWS * (D + kPartTail) : 0;
   auto part_at = [&](int i) { return part + static_cast<long long>(i) * NEXT + (i == 0 ? late : 0); };
   const int first = ONE_WARP ? 0 : warp;
   constexpr int STEP = ONE_WARP ? 1 : 8;
-  float mm = -INFINITY, ll = 0.f, a[E] = {};
-  for (int i = lane; i < n; i += 32) mm = fmaxf(mm, part_at(i)[D]);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-  const float mb = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 8
-  for (int i = first; i < n; i += STEP) {
-    const float* at = part_at(i);
-    const float f = ex2(at[D] - mb);
-    ll += f * at[D + 1];
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (lane + 32 * e < D) a[e] += f * at[lane + 32 * e];
+  float mm = -INFINITY, from = -INFINITY, ll = 0.f, a[E] = {};
+  // {maximum, sum, what the values are relative to}
+  auto tail_of = [](const float* at) { return *reinterpret_cast<const float4*>(at + D); };
+  for (int i = lane; i < n; i += 32) {
+    const float4 x = tail_of(part_at(i));
+    mm = fmaxf(mm, x.x);
+    from = fmaxf(from, x.z);
   }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) {
+    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+    from = fmaxf(from, __shfl_xor_sync(0xffffffffu, from, x));
+  }
+  const float mb = mm == -INFINITY ? 0.f : mm, fb = from == -INFINITY ? 0.f : from;
+  // 32 of this warp's parts at a time: their weights in the lanes, then their values
+  for (int c = first; c < n; c += 32 * STEP) {
+    const int own = c + lane * STEP;
+    float f = 0.f;
+    if (own < n) {
+      const float4 x = tail_of(part_at(own));
+      f = ex2(x.z - fb);
+      ll += ex2(x.x - mb) * x.y;
+    }
+    const int here_n = min((n - c + STEP - 1) / STEP, 32);
+    for (int y0 = 0; y0 < here_n; y0 += 4) {  // four parts' loads in flight
+      float x[4][E];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        // (past the last part: the last one again, at weight 0)
+        const float* at = part_at(c + min(y0 + y, here_n - 1) * STEP);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[y][e] = lane + 32 * e < D ? at[lane + 32 * e] : 0.f;
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const float fy = __shfl_sync(0xffffffffu, f, y0 + y);
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[e] = fmaf(fy, x[y][e], a[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, x);
   if (!ONE_WARP) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -917,10 +963,10 @@ __global__ void __launch_bounds__(256)
   }
   const int head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
   __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
-  const float inv = ll > 0.f ? 1.f / ll : 0.f;
+  const float fac = value_factor(from, mb), inv = (ll > 0.f ? 1.f / ll : 0.f) * fac;
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    if (lane + 32 * e < D) out[lane + 32 * e] = __float2bfloat16_rn(a[e] * inv);
+    if (lane + 32 * e < D) out[lane + 32 * e] = __float2bfloat16_rn(a[e] * fac * inv);
   if (lane == 0 && p.lse != nullptr)
     p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
         ll > 0.f ? (mm + __log2f(ll)) * kLn2 : -INFINITY;

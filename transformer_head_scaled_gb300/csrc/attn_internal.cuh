@@ -310,6 +310,10 @@ struct ScoredDecodeProblem {
   int window;  // -1: every key up to the query
   RowStrides sq, sk, sv, so;
 };
+// Behind the d values of a row's part in the workspace: the scores' maximum, the
+// row sum relative to it, what the values are relative to, and one to make them a
+// 16-byte load.
+constexpr int kPartTail = 4;
 struct ScoredDecodePlan {
   int row_tile, row_tiles;  // query rows of one key head per CTA, and how many such tiles
   bool whole;  // a warp takes whole units (sequence, key head, row tile)
