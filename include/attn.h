@@ -299,7 +299,8 @@ size_t attn_mask_plan_bytes(int B, int n_q, int n_k);
  *   plan, plan_bytes : what attn_mask_plan wrote for (B, n_q, n_k), on this
  *              stream or ordered before it; NULL: every query sees every key.
  *              A plan of other sizes is found on the device: nothing is
- *              computed and attn_check reports ATTN_ERR_WRONG_PLAN.
+ *              computed, the outputs (of attn_bwd_scored: the gradients) keep what
+ *              they held, and attn_check reports ATTN_ERR_WRONG_PLAN.
  * d_k in {16, 32, 64, 128}.  A query that sees no key gets O = 0, LSE = -inf.
  * Values that a mask hides must be finite, as for attn_fwd.  Scores, cap, bias
  * and softmax are computed in fp32; P is rounded to bf16 before the second

@@ -1,0 +1,99 @@
+"""Attention with changed scores where its arguments end: caps from wide to idle,
+scores past the polynomials' range in some tiles and not in others, plans of other
+sizes, workspaces with anything in them, the default stream by its number.
+
+Tolerances as in test_scored_gpu, and with the general form of the tanh 3e-7 of the
+cap more for scores and LSE.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import scored
+from transformer_head_scaled_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+SCORE_TOL = 5e-4
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from transformer_head_scaled_gb300.build import build
+    build()
+    return binding.load()
+
+
+def _random(shape, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(BF16)
+
+
+def _slopes(h):
+    return torch.tensor([2.0 ** (-8.0 * (i + 1) / h) for i in range(h)], device="cuda")
+
+
+def _f64(t):
+    return None if t is None else t.double().cpu().numpy()
+
+
+def _check_fwd(got, want, weight, tol=SCORE_TOL):
+    o, lse = _f64(got[0]), _f64(got[1])
+    ro, rl = want
+    assert np.isfinite(o).all()
+    err = np.abs(o - ro) / (2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2 * tol) * weight + 1e-6)
+    assert (err <= 1).all(), err.max()
+    none = np.isinf(rl)
+    assert np.array_equal(np.isinf(lse), none) and (lse[none] < 0).all()
+    assert (np.abs(lse[~none] - rl[~none]) <= tol).all(), np.abs(lse[~none] - rl[~none]).max()
+
+
+def _check_grads(got, want):
+    for name, a, b in zip(("dq", "dk", "dv"), got, want):
+        a = _f64(a)
+        assert np.isfinite(a).all(), name
+        rel, worst = np.linalg.norm(a - b) / np.linalg.norm(b), np.abs(a - b).max() / np.abs(b).max()
+        assert rel <= 5e-3 and worst <= 1.5e-2, (name, rel, worst)
+
+
+def _both_ways(h, hk, n, d, mask, cap, slopes, q, k, v, tol=SCORE_TOL, gradients=True):
+    """Forward, and gradients where d has them, of one batch entry against the reference."""
+    see = [scored.visible(n, n, **mask)]
+    plan = binding.attn_mask_plan(1, n, n, device="cuda", **mask)
+    kw = dict(plan=plan, softcap=cap, slopes=slopes)
+    o, lse = binding.attn_fwd_scored(q, k, v, **kw)
+    binding.check()
+    scale = 1 / math.sqrt(d)
+    ref = (_f64(q), _f64(k), _f64(v))
+    want = scored.attention(*ref, see, scale, cap, _f64(slopes))
+    weight, _ = scored.attention(*ref[:2], np.abs(ref[2]), see, scale, cap, _f64(slopes))
+    _check_fwd((o, lse), want, weight, tol)
+    if d == 128 or not gradients:
+        return
+    dout = _random(q.shape, 4)
+    got = binding.attn_bwd_scored(q, k, v, o, lse, dout, **kw)
+    binding.check()
+    _check_grads(got, scored.gradients(*ref, _f64(dout), see, scale, cap, _f64(slopes)))
+
+
+@pytest.mark.parametrize("h,hk", [(2, 2), (4, 1)])
+def test_a_plan_of_other_sizes_writes_nothing(h, hk):
+    """Outputs and gradients keep what they held, those of key heads whose query heads
+    are worked on in parts too."""
+    q, k, v = (_random((1, x, 100, 64), s) for x, s in ((h, 1), (hk, 2), (hk, 3)))
+    other = binding.attn_mask_plan(1, 101, 101, right=0, device="cuda")
+    out, lse = torch.full_like(q, 5.0), torch.full((1, h, 100), 5.0, device="cuda")
+    grads = [torch.full_like(t, 5.0) for t in (q, k, v)]
+    binding.attn_fwd_scored(q, k, v, plan=other, out=out, lse=lse)
+    binding.attn_bwd_scored(q, k, v, q, torch.zeros_like(lse), q, plan=other, dq=grads[0],
+                            dk=grads[1], dv=grads[2])
+    with pytest.raises(binding.AttnError) as e:
+        binding.check()
+    assert e.value.status == binding.ATTN_ERR_WRONG_PLAN
+    for t in (out, lse, *grads):
+        assert (t == 5.0).all()

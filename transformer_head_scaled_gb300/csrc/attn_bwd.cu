@@ -1444,14 +1444,28 @@ __global__ void __launch_bounds__(256)
   if (SCORED && few && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
+// The sizes that a call's plan has to be of; header null: there is no plan.  Under a
+// plan of others the main kernel computes nothing and reports it, and the kernels
+// after it write no gradients.
+struct PlanSizes {
+  const int4* header;
+  int n_q, n_k, B;
+  __device__ __forceinline__ bool fit() const {
+    if (header == nullptr) return true;
+    const int4 h = __ldg(header);
+    return h.x == n_q && h.y == n_k && h.z == B;
+  }
+};
+
 // dQ = scale * accumulator, rounded to bf16, written through dq's strides;
 // 8 elements a thread (d8 = d / 8 threads a row).
 __global__ void __launch_bounds__(256)
     attn_bwd_dq_kernel(const float* __restrict__ dq_acc, __nv_bfloat16* __restrict__ dq,
-                       float scale, long long n8, int d8, int H, int n_q, RowStrides sdq) {
+                       float scale, long long n8, int d8, int H, int n_q, RowStrides sdq,
+                       const PlanSizes plan) {
   grid_dependency_wait();  // the main kernel's additions into dq_acc are complete
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n8) return;
+  if (i >= n8 || !plan.fit()) return;
   const long long r = i / d8;  // row (b * H + hh) * n_q + qi of the accumulator
   const long long bh = r / n_q;
   const long long dst =
@@ -1472,10 +1486,10 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     attn_bwd_dkv_kernel(const float* __restrict__ acc, __nv_bfloat16* __restrict__ dk,
                         __nv_bfloat16* __restrict__ dv, int parts, long long n8, int d8, int HK,
-                        int n_k, RowStrides sdk, RowStrides sdv) {
+                        int n_k, RowStrides sdk, RowStrides sdv, const PlanSizes plan) {
   grid_dependency_wait();  // the parts are complete
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n8) return;
+  if (i >= n8 || !plan.fit()) return;
   const long long r = i / d8;  // row (b * HK + head) * n_k + key
   const long long bh = r / n_k;
   const bool is_k = blockIdx.y == 1;
@@ -1676,11 +1690,13 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
   }
   if (err != cudaSuccess) return err;
 
+  const PlanSizes sizes{mod != nullptr && mod->masked ? mod->plan.header : nullptr, pb.n_q, pb.n_k,
+                        pb.B};
   const long long n8 = bh * pb.n_q * (D / 8);
   err = launch_dependent(attn_bwd_dq_kernel, dim3(static_cast<unsigned>((n8 + 255) / 256)),
                          dim3(256), 0, ctx.stream, static_cast<const float*>(dq_acc),
                          static_cast<__nv_bfloat16*>(pb.dq), pb.scale, n8, D / 8, pb.H, pb.n_q,
-                         pb.sdq);
+                         pb.sdq, sizes);
   if (err != cudaSuccess || mod == nullptr || mod->parts == 1) return err;
   const int HK = pb.H / mod->group;
   const long long k8 = static_cast<long long>(pb.B) * HK * pb.n_k * (D / 8);
@@ -1688,7 +1704,7 @@ cudaError_t launch_bwd_d(const BwdProblem& pb, const CUtensorMap* maps, void* wo
                           dim3(256), 0, ctx.stream,
                           reinterpret_cast<const float*>(ws + lay.part_off),
                           static_cast<__nv_bfloat16*>(pb.dk), static_cast<__nv_bfloat16*>(pb.dv),
-                          mod->parts, k8, D / 8, HK, pb.n_k, mod->sdk, mod->sdv);
+                          mod->parts, k8, D / 8, HK, pb.n_k, mod->sdk, mod->sdv, sizes);
 }
 
 }  // namespace
