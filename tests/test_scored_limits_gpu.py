@@ -97,3 +97,26 @@ def test_a_plan_of_other_sizes_writes_nothing(h, hk):
     assert e.value.status == binding.ATTN_ERR_WRONG_PLAN
     for t in (out, lse, *grads):
         assert (t == 5.0).all()
+
+
+@pytest.mark.parametrize("lost", [False, True])
+def test_gradients_do_not_depend_on_what_the_workspace_held(lost):
+    """Queries with few keys among them; and (lost) with an LSE of -inf for one that
+    sees keys, as scores of -inf leave it."""
+    h, n, d = 2, 140, 64
+    q, k, v, dout = (_random((1, h, n, d), s) for s in (1, 2, 3, 4))
+    plan = binding.attn_mask_plan(1, n, n, left=5, right=0, device="cuda")
+    o, lse = binding.attn_fwd_scored(q, k, v, plan=plan)
+    if lost:
+        lse[:, :, 7] = -math.inf
+        o[:, :, 7] = 0
+    need = binding.bwd_scored_workspace_bytes(1, h, h, n, n, d)
+    got = []
+    for fill in (0, 0xff, 0x7f):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        got.append(binding.attn_bwd_scored(q, k, v, o, lse, dout, plan=plan, workspace=ws))
+    binding.check()
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert torch.isfinite(b.float()).all()
+            assert (a.float() - b.float()).abs().max() <= 1e-2 * a.float().abs().max()

@@ -1342,12 +1342,13 @@ __global__ void __launch_bounds__(256)
         if (x0 + y < seen) exact = fmaf(expf(s[y] - l), dp[y], exact);
       }
     }
-    if (own && sub == 0 && isfinite(l)) {
+    if (own && sub == 0) {
       const int qt = i / BM, r = i % BM;
       uint8_t* row = cst +
                      (static_cast<size_t>(bh) * num_qt + qt) * static_cast<size_t>(CONST_TILE_BYTES) +
                      (r & 7) * 16 + (r >> 3) * 256;
-      const uint2 pd = split3_bf16(-exact);
+      // (without a finite LSE D is 0, not what the workspace held)
+      const uint2 pd = split3_bf16(isfinite(l) ? -exact : 0.f);
       *reinterpret_cast<uint16_t*>(row + 6) = static_cast<uint16_t>(pd.x);
       *reinterpret_cast<uint32_t*>(row + 8) = (pd.x >> 16) | (pd.y << 16);
     }
