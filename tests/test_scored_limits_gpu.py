@@ -120,3 +120,21 @@ def test_gradients_do_not_depend_on_what_the_workspace_held(lost):
         for a, b in zip(got[0], other):
             assert torch.isfinite(b.float()).all()
             assert (a.float() - b.float()).abs().max() <= 1e-2 * a.float().abs().max()
+
+
+def test_the_default_stream_by_its_number():
+    """stream=0 is the default stream: the call waits for what was put there before."""
+    q, k, v = (_random((1, 2, 100, 64), s) for s in (1, 2, 3))
+    cache = [t.contiguous() for t in (k, v)]
+    want = [*binding.attn_fwd_scored(q, k, v), *binding.attn_decode_scored(q[:, :, :1], *cache)]
+    late = torch.zeros_like(q)
+    torch.cuda.Stream()   # (making a process's first one waits for the device)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.default_stream()):
+        torch.cuda._sleep(200_000_000)   # a tenth of a second
+        late.copy_(q)
+    got = [*binding.attn_fwd_scored(late, k, v, stream=0),
+           *binding.attn_decode_scored(late[:, :, :1], *cache, stream=0)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

@@ -626,7 +626,8 @@ class _call_on:
     """Makes the tensors' device current for a call, and the call's stream too,
     so that what is allocated for it belongs to that stream; gives the stream's
     pointer.  Nothing has to be switched for a call on the current stream of the
-    current device."""
+    current device.  `stream`: a torch stream of the tensors' device, or a
+    cudaStream_t as a number (0: the default stream)."""
 
     __slots__ = ("_device", "_stream")
 
@@ -644,7 +645,9 @@ class _call_on:
         if stream is None:
             stream = torch.cuda.current_stream()
         elif not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
+            # (ExternalStream(0) would be a new stream)
+            stream = (torch.cuda.ExternalStream(int(stream)) if int(stream)
+                      else torch.cuda.default_stream())
         self._stream = torch.cuda.stream(stream)
         self._stream.__enter__()
         return int(stream.cuda_stream)
