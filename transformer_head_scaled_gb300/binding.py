@@ -633,6 +633,8 @@ class _call_on:
 
     def __init__(self, device: torch.device, stream):
         self._device = None
+        if stream is not None and getattr(stream, "device", device) != device:
+            raise ValueError(f"stream must be one of the tensors' device, {device}")
         if stream is not None or device.index != torch.cuda.current_device():
             self._device = torch.cuda.device(device)
         self._stream = stream if self._device is not None else device.index
