@@ -375,7 +375,7 @@ typedef enum {
  *              new_lens[b] of the n_new tokens are written (a padded batch of
  *              prompts); NULL: all.  Tokens that would land past L_max are
  *              dropped.
- *   d_k      : 16, 32, 64 or 128 (else ATTN_ERR_UNSUPPORTED).
+ *   d_k      : 16, 32, 64 or 128, L_max <= 2^30 (else ATTN_ERR_UNSUPPORTED).
  * One kernel on `stream`; nothing is allocated.  The caches must not overlap
  * the new tokens, and two calls on one cache must be ordered on one stream.
  */

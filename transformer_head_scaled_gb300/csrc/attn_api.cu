@@ -805,6 +805,8 @@ bool stride16_ok(long long elems, int elem) {
   return elems > 0 && elems < (1LL << 40) / elem && (elems * elem) % 16 == 0;
 }
 
+constexpr int kMostCached = 1 << 30;  // tokens of a sequence in a cache
+
 bool block_tokens_ok(int t) { return t == 16 || t == 32 || t == 64 || t == 128; }
 
 // Strides of `count` [B, h, n, d] tensors from a host array of 3 * count
@@ -867,7 +869,7 @@ int scored_decode_sizes(int B, int h, int h_kv, int n_q, int L_max, int d_k, int
   if (!tc_head_size(d_k) || n_q > kDecodeMaxQueries) return ATTN_ERR_UNSUPPORTED;
   // the kernel counts the visible cache's tiles of 16 keys or more, over all
   // sequences and key heads (and tiles of query rows), in 31 bits
-  if (static_cast<long long>(B) * h * n_q > (1LL << 24) || L_max > (1 << 30) ||
+  if (static_cast<long long>(B) * h * n_q > (1LL << 24) || L_max > kMostCached ||
       static_cast<long long>(B) * h_kv * ((h / h_kv * n_q + 31) / 32) * (L_max / 16 + 2LL) >
           0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
@@ -897,6 +899,8 @@ int attn_cache_append(const void* k_new, const void* v_new, void* k_cache, void*
     return ATTN_ERR_INVALID_ARG;
   if (static_cast<long long>(B) * h > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   if (!tc_head_size(d_k)) return ATTN_ERR_UNSUPPORTED;
+  // (a row's number and its block's end stay inside int)
+  if (L_max > kMostCached) return ATTN_ERR_UNSUPPORTED;
   // one block of threads at most per cache block that can be touched
   if (static_cast<double>(B) * h * cache_blocks_touched(n_new, L_max, block_tokens) * 2.0 >
       2147483647.0)

@@ -94,8 +94,10 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   const int b = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(b) * p.H;
   const int len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
   const int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
-  const int end = min(len + more, p.L_max);  // tokens that do not fit are dropped
+  const int end = len + min(more, p.L_max - len);  // tokens that do not fit are dropped
   const int blk = len / p.T + static_cast<int>(rest - bh * p.touched);
+  if (blk >= p.num_blocks) return;
+  // (L_max is 2^30 at most, so that nothing here leaves int)
   const int row0 = blk * p.T;
   const int first = max(len, row0), last = min(end, row0 + p.T);  // new rows of this block
   if (first >= last) return;  // the same for every thread of the unit
