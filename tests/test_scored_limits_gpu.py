@@ -81,6 +81,19 @@ def _both_ways(h, hk, n, d, mask, cap, slopes, q, k, v, tol=SCORE_TOL, gradients
     _check_grads(got, scored.gradients(*ref, _f64(dout), see, scale, cap, _f64(slopes)))
 
 
+@pytest.mark.parametrize("mask", [dict(), dict(right=0)], ids=["none", "causal"])
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("cap", [1e8, 1e9, 1e10, 1e12])
+def test_large_scores_under_an_idle_cap(cap, d, mask):
+    """Scores of up to 150, where the running maximum must not carry the general
+    form's error of 3e-7 of the cap (forward)."""
+    h, hk, n = 2, 1, 300
+    q, k, v = _random((1, h, n, d), 1, 40.0), _random((1, hk, n, d), 2), _random((1, hk, n, d), 3)
+    sums = (np.abs(_f64(q)) @ np.abs(_f64(k)).swapaxes(2, 3)).max() / math.sqrt(d)
+    _both_ways(h, hk, n, d, mask, cap, None, q, k, v, SCORE_TOL + (d + 8) * 2.0 ** -24 * sums,
+               gradients=False)
+
+
 @pytest.mark.parametrize("h,hk", [(2, 2), (4, 1)])
 def test_a_plan_of_other_sizes_writes_nothing(h, hk):
     """Outputs and gradients keep what they held, those of key heads whose query heads

@@ -772,8 +772,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
         float mt;  // the row's largest score of this tile, in log2 units
         if (CAP && !BIAS && !edge) {
-          // the cap is monotone: its maximum is that of the largest raw score
-          mt = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(top_raw * p.cap_in)), p.cap_log2);
+          // the cap is monotone: its maximum is that of the largest raw score, by the
+          // form that the scores take (the general one errs by 3e-7 of the cap, which
+          // may be any number of powers of two)
+          const float z = top_raw * top_raw;
+          mt = merged ? top_raw * fmaf(z, fmaf(z, p.cap.poly[2], p.cap.poly[1]), p.cap.poly[0])
+                      : fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(top_raw * p.cap_in)), p.cap_log2);
         } else {
         float mx[4];
 #pragma unroll
