@@ -294,7 +294,7 @@ size_t attn_mask_plan_bytes(int B, int n_q, int n_k);
  *   strides  : host array of 12 element counts, three (b, h, row) per tensor in
  *              the order q, k, v, o, each > 0 and a multiple of 8; NULL:
  *              contiguous.
- *   softcap  : > 0 (scale / softcap finite), or 0 for none.
+ *   softcap  : > 0 and <= 2^64 (scale / softcap finite), or 0 for none.
  *   slopes   : device float[h], or NULL for none.
  *   plan, plan_bytes : what attn_mask_plan wrote for (B, n_q, n_k), on this
  *              stream or ordered before it; NULL: every query sees every key.
@@ -403,7 +403,7 @@ int attn_cache_append(const void* k_new, const void* v_new, void* k_cache, void*
  *              ignored for ATTN_CACHE_BF16.
  *   strides  : host array of 12 element counts (q, k_cache, v_cache, o; three
  *              each, > 0 and a multiple of 16 bytes), or NULL: contiguous.
- *   softcap  : > 0 (scale / softcap finite), or 0 for none.
+ *   softcap  : > 0 and <= 2^64 (scale / softcap finite), or 0 for none.
  *   slopes   : device float[h], or NULL for none.
  *   cache_lens : device int32[B] (clamped to [0, L_max]), or NULL: all L_max.
  *   window   : >= 0, or -1 for none.

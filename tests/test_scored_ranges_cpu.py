@@ -34,3 +34,18 @@ def test_append_to_caches_past_the_index_arithmetic_is_refused(lib):
     for L in ((1 << 30) + 1, 2 ** 31 - 1):
         assert call(L) == binding.ATTN_ERR_UNSUPPORTED, L
         assert call(L, n_new=L) == binding.ATTN_ERR_UNSUPPORTED, L
+
+
+@pytest.mark.parametrize("cap,ok", [(2.0 ** 64, True), (2.0 ** 64 * (1 + 2.0 ** -23), False),
+                                    (1e30, False), (3e38, False)])
+def test_caps_above_2_to_the_64_are_refused(lib, cap, ok):
+    """(2^64 itself gets past this check, to that of the head size or the queries.)"""
+    got = (binding.attn_fwd_scored_raw(A, A, A, A, None, 1, 2, 1, 8, 8, 48, None, 0.125, cap, None,
+                                       None, 0, None),
+           binding.attn_bwd_scored_raw(A, A, A, A, A, A, A, A, A, 1, 2, 1, 8, 8, 48, None, 0.125, cap,
+                                       None, None, 0, A, 1 << 40, None),
+           binding.attn_decode_scored_raw(A, A, A, A, A, A, None, 1, 2, 1, 9, 64, 64, None,
+                                          binding.CACHE_E4M3, 64, 0.125, cap, None, None, -1, None,
+                                          0, None))
+    want = binding.ATTN_ERR_UNSUPPORTED if ok else binding.ATTN_ERR_INVALID_ARG
+    assert all(rc == want for rc in got), got

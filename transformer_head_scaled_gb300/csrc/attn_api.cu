@@ -822,9 +822,11 @@ bool read_strides(Strides* st, const int64_t* in, int count, const int* heads, c
   return true;
 }
 
-// 0 (none), or large enough that the tanh's argument per unit of q.k is finite.
+// 0 (none), or large enough that the tanh's argument per unit of q.k is finite, and
+// no larger than 2^64, so that this argument times a code's scale and the cap in log2
+// units stay normal numbers (at 1e36 and above scores of 8-bit caches were wrong).
 bool softcap_ok(float softcap, float scale) {
-  return std::isfinite(softcap) && softcap >= 0.f &&
+  return softcap >= 0.f && softcap <= 0x1p64f &&
          (softcap == 0.f || std::isfinite(4.f * scale / softcap));
 }
 
