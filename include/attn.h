@@ -295,7 +295,7 @@ size_t attn_mask_plan_bytes(int B, int n_q, int n_k);
  *              the order q, k, v, o, each > 0 and a multiple of 8; NULL:
  *              contiguous.
  *   softcap  : > 0 and <= 2^64 (scale / softcap finite), or 0 for none.
- *   slopes   : device float[h], or NULL for none.
+ *   slopes   : device float[h], or NULL for none; with them scale >= 2^-64.
  *   plan, plan_bytes : what attn_mask_plan wrote for (B, n_q, n_k), on this
  *              stream or ordered before it; NULL: every query sees every key.
  *              A plan of other sizes is found on the device: nothing is
@@ -325,7 +325,7 @@ int attn_fwd_scored(const void* q, const void* k, const void* v, void* o, float*
  *   workspace, workspace_bytes : at least attn_bwd_scored_workspace_bytes(B, h,
  *              h_kv, n_q, n_k, d_k) bytes, 16-byte aligned; contents on entry do
  *              not matter; calls that may overlap need one each.
- * d_k in {16, 32, 64} (else ATTN_ERR_UNSUPPORTED).  Queries that see no key get
+ * d_k in {16, 32, 64} (else ATTN_ERR_UNSUPPORTED), scale >= 2^-64.  Queries that see no key get
  * dq = 0, keys that no query sees dk = dv = 0.  dq, dk, dv must not overlap the
  * inputs; dout must be finite, in rows that see no key too.  dQ is summed over
  * key tiles in fp32 in the order in which they finish.  Other arguments,

@@ -61,14 +61,15 @@ def _check_grads(got, want):
         assert rel <= 5e-3 and worst <= 1.5e-2, (name, rel, worst)
 
 
-def _both_ways(h, hk, n, d, mask, cap, slopes, q, k, v, tol=SCORE_TOL, gradients=True):
+def _both_ways(h, hk, n, d, mask, cap, slopes, q, k, v, tol=SCORE_TOL, gradients=True,
+               scale=None):
     """Forward, and gradients where d has them, of one batch entry against the reference."""
     see = [scored.visible(n, n, **mask)]
     plan = binding.attn_mask_plan(1, n, n, device="cuda", **mask)
-    kw = dict(plan=plan, softcap=cap, slopes=slopes)
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    kw = dict(plan=plan, softcap=cap, slopes=slopes, scale=scale)
     o, lse = binding.attn_fwd_scored(q, k, v, **kw)
     binding.check()
-    scale = 1 / math.sqrt(d)
     ref = (_f64(q), _f64(k), _f64(v))
     want = scored.attention(*ref, see, scale, cap, _f64(slopes))
     weight, _ = scored.attention(*ref[:2], np.abs(ref[2]), see, scale, cap, _f64(slopes))
@@ -151,3 +152,13 @@ def test_the_default_stream_by_its_number():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -64, 2.0 ** -20])
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_the_least_scales(d, alibi, scale):
+    """What is divided by the scale (the bias, LSE) keeps its precision."""
+    h, hk, n = 2, 1, 300
+    q, k, v = _random((1, h, n, d), 1, 2.0), _random((1, hk, n, d), 2), _random((1, hk, n, d), 3)
+    _both_ways(h, hk, n, d, dict(right=0), 0.0, _slopes(h) if alibi else None, q, k, v, scale=scale)

@@ -49,3 +49,16 @@ def test_caps_above_2_to_the_64_are_refused(lib, cap, ok):
                                           0, None))
     want = binding.ATTN_ERR_UNSUPPORTED if ok else binding.ATTN_ERR_INVALID_ARG
     assert all(rc == want for rc in got), got
+
+
+def test_scales_that_something_is_divided_by_are_refused_below_2_to_the_minus_64(lib):
+    def fwd(scale, slopes):
+        return binding.attn_fwd_scored_raw(A, A, A, A, None, 1, 2, 1, 8, 8, 48, None, scale, 0.0,
+                                           slopes, None, 0, None)
+
+    def bwd(scale):
+        return binding.attn_bwd_scored_raw(A, A, A, A, A, A, A, A, A, 1, 2, 1, 8, 8, 48, None, scale,
+                                           0.0, None, None, 0, A, 1 << 40, None)
+    assert fwd(2.0 ** -65, A) == bwd(2.0 ** -65) == binding.ATTN_ERR_INVALID_ARG
+    assert fwd(2.0 ** -64, A) == bwd(2.0 ** -64) == binding.ATTN_ERR_UNSUPPORTED
+    assert fwd(2.0 ** -65, None) == binding.ATTN_ERR_UNSUPPORTED

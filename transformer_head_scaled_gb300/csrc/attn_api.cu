@@ -1025,6 +1025,8 @@ namespace {
 
 constexpr int kMostTokens = 1 << 30;  // of a sequence: a place and a side of a mask add up in int
 
+constexpr float kLeastScale = 0x1p-64f;  // where something is divided by it
+
 int check_mask_sizes(int B, int n_q, int n_k) {
   if (B < 1 || n_q < 1 || n_k < 1) return ATTN_ERR_INVALID_ARG;
   const long long n = n_q > n_k ? n_q : n_k;
@@ -1042,6 +1044,8 @@ int check_scored(const void* q, const void* k, const void* v, const void* o, con
   if (h_kv < 1 || h % h_kv != 0) return ATTN_ERR_INVALID_ARG;
   if (!softcap_ok(softcap, scale) || !int_ptr_ok(slopes))
     return ATTN_ERR_INVALID_ARG;
+  // the bias is added in units of q.k: slope / scale
+  if (slopes != nullptr && scale < kLeastScale) return ATTN_ERR_INVALID_ARG;
   if ((rc = check_mask_sizes(B, n_q, n_k)) != ATTN_OK) return rc;
   // one work item per 256 queries, or per 128 keys, of a head
   const long long n = n_q > n_k ? n_q : n_k;
@@ -1142,6 +1146,7 @@ int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, 
   if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
       !aligned16(workspace))
     return ATTN_ERR_INVALID_ARG;
+  if (scale < kLeastScale) return ATTN_ERR_INVALID_ARG;  // LSE comes off in units of q.k
   if (!bwd_head_size_ok(d_k)) return ATTN_ERR_UNSUPPORTED;
   // order: q, k, v, o, dout, dq, dk, dv
   const int heads[8] = {h, h_kv, h_kv, h, h, h, h_kv, h_kv},
