@@ -145,3 +145,21 @@ def test_a_key_without_values_takes_nearly_all_the_weight(dtype):
     got = binding.attn_decode_scored(q, kc, vc, k_scale=ks, v_scale=vs, block_tokens=block)
     binding.check()
     _check(got, q, k, v, [L])
+
+
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (BF16, 64), (E4M3, 128), (INT8, 64)])
+@pytest.mark.parametrize("rows", [1, 16, 32])
+def test_the_parts_of_a_split_cache_are_those_of_resident_warps(dtype, d, rows):
+    """Two parts of d values and four more floats a row, at most, for each warp that
+    228 KB of shared memory an SM have room for: two or more stages of 4 KB of keys and
+    values, or three of 2 KB, a warp, and 3 KB a CTA of four."""
+    fmt = {BF16: binding.CACHE_BF16, E4M3: binding.CACHE_E4M3, INT8: binding.CACHE_INT8}[dtype]
+    row_bytes = d * (2 if dtype == BF16 else 1)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    need = binding.decode_scored_workspace_bytes(1, 8 * rows, 8, 1, 1 << 20, d, fmt)
+    tile = 16 * row_bytes if row_bytes >= 128 else 2048   # the least
+    ring = 3 * 2 * max(tile, 2048)
+    fit = 228 * 1024 // (4 * ring + 3 * 1024)
+    warps = sms * 4 * fit
+    row_tile = 8 if rows <= 8 else (16 if rows <= 16 else 32)
+    assert 0 < need <= 4 * (4 + warps * 2 * row_tile * (d + 4))

@@ -996,7 +996,7 @@ ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int
   // whole units per warp when there are enough of them to occupy the SMs and the
   // longest is at most 32 small tiles (about 20 us of one warp)
   int kt = scored_decode_tile_keys(row_bytes, false);
-  const long long small = static_cast<long long>(num_sms) * scored_decode_warps(plan.row_tile, false);
+  const long long small = static_cast<long long>(num_sms) * scored_decode_warps(row_bytes, plan.row_tile, false);
   plan.whole = units * 2 >= small && tiles_of(kt) <= 32;
   plan.tile_keys = kt;
   if (plan.whole) {
@@ -1007,7 +1007,7 @@ ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int
   // every resident warp takes a share of the tiles, if there are that many
   const bool big = scored_decode_big(row_bytes, plan.row_tile, false);
   plan.tile_keys = kt = scored_decode_tile_keys(row_bytes, big);
-  const long long resident = static_cast<long long>(num_sms) * scored_decode_warps(plan.row_tile, big);
+  const long long resident = static_cast<long long>(num_sms) * scored_decode_warps(row_bytes, plan.row_tile, big);
   const long long useful =
       (units * tiles_of(kt) + scored_decode_min_tiles() - 1) / scored_decode_min_tiles();
   plan.warps = static_cast<int>(useful < resident ? useful : resident);

@@ -176,8 +176,19 @@ constexpr bool scored_big_tiles(int row_bytes, int row_tiles, bool whole) {
 constexpr int scored_tile_keys(int row_bytes, bool big) {
   return (row_bytes >= 128 ? 16 : (row_bytes >= 64 ? 32 : 64)) * (big ? 2 : 1);
 }
-// Resident CTAs per SM that the registers allow, by row tiles.
-constexpr int scored_ctas(int row_tiles, bool big) { return row_tiles > 1 ? 2 : (big ? 3 : 4); }
+constexpr int scored_stages(bool big) { return big ? 2 : 3; }
+// Bytes of a warp's ring: keys and values of its stages.
+constexpr int scored_ring(int row_bytes, bool big) {
+  return scored_stages(big) * 2 * scored_tile_keys(row_bytes, big) * row_bytes;
+}
+// Resident CTAs per SM: what the registers allow, by row tiles, and what 228 KB of
+// shared memory do (a CTA's rings, 1 KB to align them, 1 KB of its own and 1 KB that
+// the system takes): two for the 256-byte rows of a bf16 cache at d = 128.
+constexpr int scored_ctas(int row_bytes, int row_tiles, bool big) {
+  const int regs = row_tiles > 1 ? 2 : (big ? 3 : 4);
+  const int smem = 228 * 1024 / (DW * scored_ring(row_bytes, big) + 3 * 1024);
+  return regs < smem ? regs : smem;
+}
 // A warp's run is at least this many tiles: below it the start of a run and the
 // join of its result cost more than the tiles.
 constexpr int kMinTiles = 2;
@@ -193,7 +204,7 @@ struct DCfg {
   static constexpr int KT = scored_tile_keys(RB, BIG_);
   static constexpr uint32_t TILE = KT * RB;        // a tile of keys (or of values)
   static constexpr uint32_t BOX = KT * BB;
-  static constexpr int STAGES = BIG_ ? 2 : 3;
+  static constexpr int STAGES = scored_stages(BIG_);
   static constexpr int NT = KT / 8;   // 8-key column tiles of S
   static constexpr int NG = KT / 16;  // 16-key groups (one k step of O^T)
   // K: a lane's quarter of a row, in loads of KV bytes
@@ -209,8 +220,8 @@ struct DCfg {
   static constexpr int VE = VV / ES;
   static constexpr int MT = D_ / 16;                // 16-row tiles of O^T
   static constexpr int MQ = NR_ > 1 ? NR_ / 2 : 1;  // 16-query tiles of S
-  static constexpr uint32_t RING = STAGES * 2 * TILE;  // shared memory of a warp
-  static constexpr int CTAS = scored_ctas(NR_, BIG_);
+  static constexpr uint32_t RING = scored_ring(RB, BIG_);  // shared memory of a warp
+  static constexpr int CTAS = scored_ctas(RB, NR_, BIG_);
   // Rows shorter than 128 bytes whose cache rows lie side by side are copied as
   // one run of bytes: a tiled copy takes about four cycles of the SM's copy
   // engine per box row, which for 64-byte rows is the time of 16 bytes a cycle,

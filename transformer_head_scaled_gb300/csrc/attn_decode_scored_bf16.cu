@@ -14,7 +14,9 @@ bool scored_decode_big(int row_bytes, int row_tile, bool whole) {
   return scored_big_tiles(row_bytes, row_tile / 8, whole);
 }
 int scored_decode_tile_keys(int row_bytes, bool big) { return scored_tile_keys(row_bytes, big); }
-int scored_decode_warps(int row_tile, bool big) { return DW * scored_ctas(row_tile / 8, big); }
+int scored_decode_warps(int row_bytes, int row_tile, bool big) {
+  return DW * scored_ctas(row_bytes, row_tile / 8, big);
+}
 int scored_decode_min_tiles() { return kMinTiles; }
 
 }  // namespace attn

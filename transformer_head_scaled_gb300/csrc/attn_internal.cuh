@@ -327,7 +327,7 @@ struct ScoredDecodePlan {
 // tiles per warp.
 bool scored_decode_big(int row_bytes, int row_tile, bool whole);
 int scored_decode_tile_keys(int row_bytes, bool big);
-int scored_decode_warps(int row_tile, bool big);
+int scored_decode_warps(int row_bytes, int row_tile, bool big);
 int scored_decode_min_tiles();
 // maps[0..1]: the key and the value cache as 4-D (row bytes, L_max, HK, B) byte
 // tensors with a (min(row bytes, 128), tile keys, 1, 1) box, with the 128-byte
