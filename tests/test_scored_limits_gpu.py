@@ -82,6 +82,18 @@ def _both_ways(h, hk, n, d, mask, cap, slopes, q, k, v, tol=SCORE_TOL, gradients
     _check_grads(got, scored.gradients(*ref, _f64(dout), see, scale, cap, _f64(slopes)))
 
 
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("mask", [dict(), dict(right=0), dict(left=40, right=0)],
+                         ids=["none", "causal", "window"])
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("cap", [300.0, 1e6, 1e9, 1e12, 2.0 ** 64])
+def test_wide_and_idle_caps(cap, d, mask, alibi):
+    """A cap far above every score changes nothing."""
+    h, hk, n = 2, 1, 300
+    q, k, v = _random((1, h, n, d), 1, 2.0), _random((1, hk, n, d), 2), _random((1, hk, n, d), 3)
+    _both_ways(h, hk, n, d, mask, cap, _slopes(h) if alibi else None, q, k, v)
+
+
 @pytest.mark.parametrize("mask", [dict(), dict(right=0)], ids=["none", "causal"])
 @pytest.mark.parametrize("d", [16, 64, 128])
 @pytest.mark.parametrize("cap", [1e8, 1e9, 1e10, 1e12])
@@ -93,6 +105,88 @@ def test_large_scores_under_an_idle_cap(cap, d, mask):
     sums = (np.abs(_f64(q)) @ np.abs(_f64(k)).swapaxes(2, 3)).max() / math.sqrt(d)
     _both_ways(h, hk, n, d, mask, cap, None, q, k, v, SCORE_TOL + (d + 8) * 2.0 ** -24 * sums,
                gradients=False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.int8, torch.float8_e4m3fn],
+                         ids=["bf16", "int8", "e4m3"])
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("cap", [300.0, 1e9, 1e12, 2.0 ** 64])
+def test_decode_under_wide_and_idle_caps(cap, alibi, dtype):
+    h, L, d = 2, 400, 64
+    q = _random((1, h, 1, d), 1, 2.0)
+    k, v = (_random((1, h, L, d), s, 1.0 if dtype == BF16 else 40.0).to(dtype) for s in (2, 3))
+    ks = None if dtype == BF16 else torch.full((1, h, 25), 1 / 40, device="cuda")
+    unit = 1.0 if ks is None else float(ks[0, 0, 0])
+    slopes = _slopes(h) if alibi else None
+    o, lse = binding.attn_decode_scored(q, k, v, k_scale=ks, v_scale=ks, block_tokens=16,
+                                        softcap=cap, slopes=slopes)
+    binding.check()
+    kw = dict(lens=[L], scale=0.125, softcap=cap, slopes=_f64(slopes))
+    kd, vd = _f64(k.float()) * unit, _f64(v.float()) * unit
+    want = scored.decode(_f64(q), kd, vd, **kw)
+    _check_fwd((o, lse), want, scored.decode(_f64(q), kd, np.abs(vd), **kw)[0])
+
+
+@pytest.mark.parametrize("sign", [-1, 1], ids=["against", "toward"])
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("cap", [300.0, 1000.0])
+def test_scores_past_the_polynomials_in_some_tiles(cap, d, alibi, sign):
+    """Under a wide cap, key tiles whose scores stay within 0.3 caps and others that
+    hold one of 0.6 caps, against every query (its tile's other keys keep their
+    weights) or toward it (forward alone: it takes all the weight)."""
+    h, hk, n = 2, 1, 420
+    q, k, v = _random((1, h, n, d), 1), _random((1, hk, n, d), 2), _random((1, hk, n, d), 3)
+    q = (q.float() + 2).to(BF16)   # q . (1, 1, ..) is 2 d, give or take sqrt(d)
+    k[0, 0, 130] = sign * 0.3 * cap / math.sqrt(d)
+    s = _f64(q[0]) @ _f64(k[0, 0]).T / math.sqrt(d)
+    assert (np.abs(s[:, :, 130]) > 0.3 * cap).all()
+    assert np.abs(np.delete(s, 130, 2)).max() < 0.3 * cap
+    tol = SCORE_TOL + 3e-7 * cap
+    if sign > 0:   # sums of products as large as the cap have the weight
+        tol += (d + 8) * 2.0 ** -24 * cap
+    _both_ways(h, hk, n, d, dict(right=0), cap, _slopes(h) if alibi else None, q, k, v, tol,
+               gradients=sign < 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.float8_e4m3fn], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("sign", [-1, 1], ids=["against", "toward"])
+@pytest.mark.parametrize("cap", [300.0, 1000.0])
+def test_decode_scores_past_the_polynomials(cap, sign, dtype):
+    """The same in the decoding step: one key of 0.6 caps among ordinary ones."""
+    h, L, d = 2, 300, 64
+    q = (_random((1, h, 1, d), 1).float() + 2).to(BF16)
+    x = _random((1, h, L, d), 2).float().clamp(-3.5, 3.5)
+    x[:, :, 130] = sign * 0.3 * cap / math.sqrt(d)
+    v = _random((1, h, L, d), 3).float().clamp(-3.5, 3.5)
+    if dtype == BF16:
+        codes, scales = [x.to(BF16), v.to(BF16)], [None, None]
+        unit = [1.0, 1.0]
+    else:   # a block of 16 tokens holds the large key: its scale is its own
+        scales = [t.reshape(1, h, 20, 16 * d).abs().amax(-1) / 448 for t in (
+            torch.cat([t, t[:, :, :20]], 2) for t in (x, v))]
+        wide = [s.repeat_interleave(16, 2)[:, :, :L, None] for s in scales]
+        codes = [(t / s).to(dtype) for t, s in zip((x, v), wide)]
+        scales = [s[:, :, :19].contiguous() for s in scales]
+        unit = [_f64(s) for s in wide]
+    o, lse = binding.attn_decode_scored(q, *codes, k_scale=scales[0], v_scale=scales[1],
+                                        block_tokens=16, softcap=cap)
+    binding.check()
+    k, v = (_f64(c.float()) * u for c, u in zip(codes, unit))
+    kw = dict(lens=[L], scale=0.125, softcap=cap)
+    tol = SCORE_TOL + 3e-7 * cap + ((d + 8) * 2.0 ** -24 * cap if sign > 0 else 0.0)
+    _check_fwd((o, lse), scored.decode(_f64(q), k, v, **kw),
+               scored.decode(_f64(q), k, np.abs(v), **kw)[0], tol)
+
+
+@pytest.mark.parametrize("mask", [dict(), dict(right=0), dict(left=70, right=0), dict(right=60)],
+                         ids=["none", "causal", "window", "ahead"])
+@pytest.mark.parametrize("cap,alibi", [(50.0, False), (2.0, False), (0.0, True)])
+@pytest.mark.parametrize("h,hk,n", [(2, 1, 200), (3, 3, 513)])
+def test_heads_of_128_with_a_cap_or_a_bias_alone(h, hk, n, cap, alibi, mask):
+    d = 128
+    q, k, v = _random((1, h, n, d), 1, 2.0), _random((1, hk, n, d), 2), _random((1, hk, n, d), 3)
+    _both_ways(h, hk, n, d, mask, cap, _slopes(h) if alibi else None, q, k, v)
 
 
 @pytest.mark.parametrize("h,hk", [(2, 2), (4, 1)])
