@@ -256,3 +256,31 @@ def test_the_least_scales(d, alibi, scale):
     h, hk, n = 2, 1, 300
     q, k, v = _random((1, h, n, d), 1, 2.0), _random((1, hk, n, d), 2), _random((1, hk, n, d), 3)
     _both_ways(h, hk, n, d, dict(right=0), 0.0, _slopes(h) if alibi else None, q, k, v, scale=scale)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("cap", [0.0, 50.0, 3000.0])
+@pytest.mark.parametrize("d", [16, 64])
+def test_gradients_of_two_keys_of_which_one_has_all_but_the_weight(d, cap, masked):
+    """Weights of 1 - p and p, p about e^-9: dP - D is p of dP, so that an error of the
+    LSE of 4e-6 (a score of 20 by the cap's polynomial) must not reach D: it would be
+    3 % of p.  What does reach it is fp32 rounding, 2^-23 / p = 1e-3, beside the three
+    of bf16."""
+    B, h, n = 2, 2, 60
+    k, v = _random((B, h, 2, d), 2), _random((B, h, 2, d), 3)
+    a, z = k[:, :, :1].float(), k[:, :, 1:].float()
+    unit = (a - z) / (a - z).square().sum(-1, keepdim=True)
+    side = (a + z) - ((a + z) * unit).sum(-1, keepdim=True) * (a - z)
+    side = side / (side * (a + z)).sum(-1, keepdim=True)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    gap = 8.5 + torch.rand((B, h, n, 1), generator=g, device="cuda")
+    q = (math.sqrt(d) * (gap * unit + 30 * side)).to(BF16)   # scores of 15 + gap / 2, 15 - gap / 2
+    dout = _random((B, h, n, d), 4)
+    plan = binding.attn_mask_plan(B, n, 2, device="cuda") if masked else None
+    kw = dict(plan=plan, softcap=cap)
+    o, lse = binding.attn_fwd_scored(q, k, v, **kw)
+    got = binding.attn_bwd_scored(q, k, v, o, lse, dout, **kw)
+    binding.check()
+    see = [np.ones((n, 2), bool)] * B
+    ref = scored.gradients(_f64(q), _f64(k), _f64(v), _f64(dout), see, 1 / math.sqrt(d), cap)
+    _check_grads(got, ref)

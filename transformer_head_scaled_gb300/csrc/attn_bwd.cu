@@ -1312,7 +1312,7 @@ __global__ void __launch_bounds__(256)
       l = lse[static_cast<size_t>(bh) * n_q + i];
     }
     const int most = __reduce_max_sync(0xffffffffu, seen);
-    float exact = 0.f;
+    float exact = 0.f, total = 0.f;
     // four keys' loads in flight at a time
     for (int x0 = 0; x0 < most; x0 += 4) {
       uint4 kk[4], vv[4];
@@ -1339,7 +1339,11 @@ __global__ void __launch_bounds__(256)
         s[y] *= mod.scale;
         if (mod.softcap > 0.f) s[y] = mod.softcap * tanhf(s[y] / mod.softcap);
         s[y] -= slope * fabsf(static_cast<float>(i - (j0 + x0 + y)));
-        if (x0 + y < seen) exact = fmaf(expf(s[y] - l), dp[y], exact);
+        if (x0 + y < seen) {
+          const float e = expf(s[y] - l);
+          total += e;
+          exact = fmaf(e, dp[y], exact);
+        }
       }
     }
     if (own && sub == 0) {
@@ -1347,8 +1351,11 @@ __global__ void __launch_bounds__(256)
       uint8_t* row = cst +
                      (static_cast<size_t>(bh) * num_qt + qt) * static_cast<size_t>(CONST_TILE_BYTES) +
                      (r & 7) * 16 + (r >> 3) * 256;
+      // Over the sum of these P, which LSE's error keeps from 1 (by 4e-6 of a score of
+      // 20 under a wide cap): where one key has nearly all the weight, dP - D is next to
+      // nothing and would be that error (30 % off with a second key at e^-9).
       // (without a finite LSE D is 0, not what the workspace held)
-      const uint2 pd = split3_bf16(isfinite(l) ? -exact : 0.f);
+      const uint2 pd = split3_bf16(isfinite(l) && total > 0.f ? -exact / total : 0.f);
       *reinterpret_cast<uint16_t*>(row + 6) = static_cast<uint16_t>(pd.x);
       *reinterpret_cast<uint32_t*>(row + 8) = (pd.x >> 16) | (pd.y << 16);
     }
