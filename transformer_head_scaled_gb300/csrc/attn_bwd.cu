@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   };
   // the item's next tile pair: the next query tile, then the next query head
   auto step = [](const Item& item, int& qt, int& g) {
-    if (++qt == item.qt0 + item.nq) {
+    ++qt;
+    if (SCORED && qt == item.qt0 + item.nq) {
       qt = item.qt0;
       ++g;
     }
@@ -602,7 +603,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const uint32_t qb = smem_u32(&sm.q_full[st]);
           mbar_arrive_expect_tx(qb, C::TILE + CONST_TILE_BYTES + (CAP ? BM * 4 : 0));
           tma_load_4d(smem_u32(sm.q[st]), &tmq, qb, 0, qt * BM, hq, b);
-          const size_t tile = (static_cast<size_t>(b) * p.H + hq) * p.num_qt + qt;
+          const size_t tile =
+              (SCORED ? static_cast<size_t>(b) * p.H + hq : static_cast<size_t>(item.bh)) * p.num_qt + qt;
           bulk_load(smem_u32(sm.cst[st]), p.cst + tile * CONST_TILE_BYTES, CONST_TILE_BYTES, qb);
           if constexpr (CAP)
             bulk_load(smem_u32(sm.lse[st]), p.lse_log2 + tile * BM, BM * 4, qb);
