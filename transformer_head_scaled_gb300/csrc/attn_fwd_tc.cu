@@ -810,7 +810,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                           mbar_wait(smem_u32(&sm.turn[s]), turns & 1, p.limit_ns, abort));
           if (!ok) break;
         }
-        const float neg_m = ((m == -INFINITY) ? 0.f : -m) + (BIAS ? offset : 0.f);
+        float neg_m = (m == -INFINITY) ? 0.f : -m;
+        if (BIAS) neg_m += offset;
         float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
         uint32_t pk[SC / 2][32];
         if (CAP && merged) {
