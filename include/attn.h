@@ -301,7 +301,10 @@ size_t attn_mask_plan_bytes(int B, int n_q, int n_k);
  *              A plan of other sizes is found on the device: nothing is
  *              computed, the outputs (of attn_bwd_scored: the gradients) keep what
  *              they held, and attn_check reports ATTN_ERR_WRONG_PLAN.
- * d_k in {16, 32, 64, 128}.  A query that sees no key gets O = 0, LSE = -inf.
+ * d_k in {16, 32, 64, 128} (attn_bwd_scored: to 64).  Query i stands at position i and
+ * key j at position j, for the plan's window and for the bias, whatever n_q and n_k are:
+ * queries that follow a cache of earlier tokens are attn_decode_scored's, up to 8 of
+ * them.  A query that sees no key gets O = 0, LSE = -inf.
  * Values that a mask hides must be finite, as for attn_fwd.  Scores, cap, bias
  * and softmax are computed in fp32; P is rounded to bf16 before the second
  * product.  Other arguments and status codes as attn_fwd.
@@ -407,6 +410,8 @@ int attn_cache_append(const void* k_new, const void* v_new, void* k_cache, void*
  *   slopes   : device float[h], or NULL for none.
  *   cache_lens : device int32[B] (clamped to [0, L_max]), or NULL: all L_max.
  *   window   : >= 0, or -1 for none.
+ *   (h / h_kv) * n_q : the query rows that a key head's cache is read for at once, 32 at
+ *              most; more rows read it again.
  *   workspace, workspace_bytes : at least attn_decode_scored_workspace_bytes(...)
  *              bytes, 16-byte aligned; may be NULL when that is 0.  Its contents
  *              on entry do not matter; calls that may overlap need one each.

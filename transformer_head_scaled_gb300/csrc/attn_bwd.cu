@@ -1172,20 +1172,6 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return acc;
 }
 
-// D of the queries that see 2 to kFewKeys keys, summed from P and dP in fp32,
-// put in the place of the one from O.  That O is rounded to bf16, which errs by
-// up to 2^-8 |dO| |O|; with few keys |O| is as large as a value and dP - D
-// cancels, so that this rounding alone took the gradients of short documents (2
-// to 9 in 17 to 48 tokens) to 6e-3 relative error in an emulation with the
-// kernels' roundings; with up to 16 keys summed so they stay below 3.1e-3, with
-// up to 32 below 3.0e-3, at any length.  (With one key O is that value exactly.)
-//
-// A CTA looks at 256 queries, lists those it has work for, and gives each of them,
-// head by head, d / 8 threads.  A kernel of its own: the sums want 64 registers, which as
-// part of the pre-kernel halved the warps in flight there (4 x 4096 tokens, 16
-// heads, d = 64, causal: 45 us in one kernel; 26 us, with these 17 us beside it, in
-// two).
-
 // The items dealt out by load: each, heaviest first, to the CTA with the least
 // work so far.  Run by one CTA more of attn_bwd_few_kernel, in the time of the
 // pre-kernel, for a plan with documents.  Back and forth is as even where a CTA
@@ -1253,6 +1239,21 @@ __device__ __forceinline__ void deal_items(const Deal& d, const KeyItem* key_ite
 }
 static_assert(kMostCtas == 256, "a thread a CTA; a CTA's number in a byte");
 
+// D of the queries that see 2 to kFewKeys keys, summed from P and dP in fp32,
+// put in the place of the one from O.  That O is rounded to bf16, which errs by
+// up to 2^-8 |dO| |O|; with few keys |O| is as large as a value and dP - D
+// cancels, so that this rounding alone took the gradients of short documents (2
+// to 9 in 17 to 48 tokens) to 6e-3 relative error in an emulation with the
+// kernels' roundings; with up to 16 keys summed so they stay below 3.1e-3, with
+// up to 32 below 3.0e-3, at any length.  (With one key O is that value exactly.)
+//
+// A CTA looks at 256 queries, lists those it has work for, and gives each of them,
+// head by head, d / 8 threads.  A kernel of its own: the sums want 64 registers, which as
+// part of the pre-kernel halved the warps in flight there (4 x 4096 tokens, 16
+// heads, d = 64, causal: 45 us in one kernel; 26 us, with these 17 us beside it, in
+// two).  Where every query sees few keys it has every row to sum: a window of 16 keys
+// takes 510 us in all on 8 x 16 x 4096 tokens, d = 64, where attn_bwd_window, whose D
+// is from the rounded O, takes 212.
 template <int D>
 __global__ void __launch_bounds__(256)
     attn_bwd_few_kernel(const __nv_bfloat16* __restrict__ dout, const float* __restrict__ lse,

@@ -12,7 +12,10 @@
 // over the keys j <= p_i (and j >= p_i - window).  Without a cap the first
 // term is the plain score.
 //
-// Bound by HBM: every visible cache byte is read once.  An 8-bit cache leaves
+// Bound by HBM: every visible cache byte is read once for each 32 query rows of a
+// key head (G * n_q of them; with more, the tiles of rows each copy the cache in, a
+// part of it from L2: 4 x 65536 tokens, d = 128, e4m3, group of 8, 4 queries 93 us, 8
+// queries 162).  An 8-bit cache leaves
 // 4 FLOPs per byte and query row, so with G * n_q rows per key head the CUDA
 // cores would be the bound from about 5 rows on; the products run on the
 // tensor cores instead, in the warp-level m16n8k16 form: the tile of queries

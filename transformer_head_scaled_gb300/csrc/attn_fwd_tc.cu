@@ -36,7 +36,10 @@
 // exponential's argument where a warp's scores stay within 0.3 caps, else 1 - 2 /
 // (1 + 2^x).  Bound by the softmax warps, as the plain kernel: 8 x 16 x 4096, d =
 // 64, causal, on one GPU: plain 295 us, the same by plan 292, with bias 331, with
-// cap 441, with both 541; without caps' small arguments (cap 2) 682.
+// cap 441, with both 541; without caps' small arguments (cap 2) 682.  These
+// instantiations spill 64 to 76 bytes a thread, 150 with a cap at d = 16 and 32 (the
+// plain one 4): they are compiled for 168 registers, of which the softmax warps have
+// 184 when they run.  What that costs was not measured.
 #include <cuda_bf16.h>
 
 #include "attn_internal.cuh"
