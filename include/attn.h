@@ -436,6 +436,129 @@ size_t attn_decode_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int L
                                           int cache_format, int window);
 
 /*
+ * Drafted tokens.  A decoding step may try several tokens at once: a draft
+ * proposes a tree of them, the target model scores all nodes in one pass
+ * (attn_decode_tree in every layer), attn_tree_verify tells which of them stand
+ * and what follows, and attn_cache_append_tree puts the accepted path into the
+ * cache.  The tree of sequence b is parents[b][0 .. n-1], n <= 128: the parent of
+ * node i is an earlier node, 0 <= parents[b][i] < i, or -1 for a root; any other
+ * value, or a parent that is no node, makes place i no node (trees of
+ * different sizes in one batch).
+ */
+
+/*
+ * attn_decode_tree -- attention of a tree's nodes over a cache and their
+ * ancestors, with the caches, changed scores and shared key heads of
+ * attn_decode_scored.  Node i of sequence b stands at position p_i =
+ * cache_lens[b] + depth_i (a root's depth is 0).  It sees the cached keys j <
+ * cache_lens[b] (at position j) and its own ancestors and itself (at theirs),
+ * with a window only those at positions p_i - window and later:
+ *   s_j = scale * q_i.k_j;   capped: softcap * tanh(s_j / softcap);
+ *   biased: minus slopes[head] * (p_i - p_j);   O = softmax(s) V,  LSE = ln sum e^s.
+ * A place that is no node gets O = 0 and LSE = -inf and is not seen.
+ *   q, o     : bf16 [B, h, n, d_k], 1 <= n <= 128; lse float [B, h, n] or NULL.
+ *   k_tree, v_tree : the nodes' own keys and values, bf16 [B, h_kv, n, d_k].  They
+ *              are not in the cache; those of places that are no node are never
+ *              used, whatever they hold.
+ *   k_cache, v_cache, k_scale, v_scale, cache_format, block_tokens, cache_lens,
+ *   softcap, slopes, window : as for attn_decode_scored; cache rows that no node
+ *              sees are never used, whatever they hold.
+ *   parents  : device int32 [B, n].
+ *   strides  : host array of 18 element counts, three (b, h, row) per tensor in
+ *              the order q, k_tree, v_tree, k_cache, v_cache, o, each > 0 and a
+ *              multiple of 16 bytes; NULL: contiguous.
+ *   workspace, workspace_bytes : at least attn_decode_tree_workspace_bytes(...)
+ *              bytes, 16-byte aligned; may be NULL when that is 0.  Its contents
+ *              on entry do not matter; calls that may overlap need one each.
+ *   d_k      : 16, 32, 64 or 128, B*h*n <= 2^24, L_max <= 2^30 (else
+ *              ATTN_ERR_UNSUPPORTED).
+ * Scores, cap, bias and softmax are computed in fp32; 8-bit codes enter the
+ * products exactly; P (times the value scale) is rounded to bf16 before the
+ * second product.
+ */
+int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* k_cache,
+                     const void* v_cache, const float* k_scale, const float* v_scale,
+                     const int* parents, void* o, float* lse, int B, int h, int h_kv, int n,
+                     int L_max, int d_k, const int64_t* strides, int cache_format,
+                     int block_tokens, float scale, float softcap, const float* slopes,
+                     const int* cache_lens, int window, void* workspace, size_t workspace_bytes,
+                     struct CUstream_st* stream);
+
+/* Scratch bytes attn_decode_tree needs on the current device (0 when none is
+ * needed, or for unsupported sizes). */
+size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int L_max, int d_k,
+                                        int cache_format, int window);
+
+/* What probabilities are held in. */
+typedef enum { ATTN_PROB_F32 = 0, ATTN_PROB_BF16 = 1 } attn_prob_type;
+
+/*
+ * attn_tree_verify -- which drafted tokens stand, so that the tokens kept and
+ * the one after them are distributed as if drawn from the target alone.  Node 0
+ * is the newest token that stands already; the walk begins there.  At a node
+ * its children c are tried in order, with p = the target's probabilities at the
+ * node, q = the draft's, x = tokens[b][c], u = uniforms[b][c]:
+ *   c stands if  u Z q(x) < r(x);  at first r = p, Z = 1, C = 0, and after each child
+ *   that does not  C += Z,  r(v) = max(p(v) - C q(v), 0),  Z = sum_v r(v).
+ * The walk goes on from a child that stands, and ends where none does; there the
+ * next token is drawn from r: the lowest v with r(0) + ... + r(v) > uniforms[b][0]
+ * sum_v r(v).  (If nothing is left of r, from p; -1 if p holds nothing either.)
+ * This holds for children drawn independently from q.  Without a draft (children
+ * chosen without chance, such as the draft's likeliest tokens) q(x) = 1, r is p
+ * without the tokens that did not stand, and Z is 1 less their probabilities.
+ *   target   : probabilities [B, n, V] in prob_type, row i those of the token
+ *              after node i; rows sum to 1 (up to 15 is harmless), values in
+ *              [0, 1], NaN counts as 0.
+ *   draft    : likewise, row i what the children of node i were drawn from; or
+ *              NULL.
+ *   tokens, parents : device int32 [B, n]; a token outside [0, V) does not stand.
+ *              tokens[b][0] and parents[b][0] are not used.
+ *   uniforms : device float [B, n], random numbers in [0, 1).
+ *   path     : device int32 [B, n], written: the nodes from node 0 to where the
+ *              walk ends, then -1.
+ *   path_lens : device int32 [B], written: how many (1 at least).
+ *   next_tokens : device int32 [B], written.
+ *   strides  : host array of 4 element counts >= 0: target's from batch entry to
+ *              batch entry and from row to row, then draft's (those two are not
+ *              read without one); NULL: contiguous.  V is contiguous.
+ *   n <= 128, V <= 2^24, B <= 2^24 (else ATTN_ERR_UNSUPPORTED).
+ * r is rounded to fp32 and summed exactly in multiples of 2^-60: the answer does
+ * not depend on the order of the sums.  One kernel on `stream`.
+ */
+int attn_tree_verify(const void* target, const void* draft, const int* tokens,
+                     const int* parents, const float* uniforms, int* path, int* path_lens,
+                     int* next_tokens, int B, int n, int V, const int64_t* strides, int prob_type,
+                     struct CUstream_st* stream);
+
+/*
+ * attn_cache_append_tree -- the keys and values of an accepted path into the
+ * caches of all layers: token i of the path goes to row cache_lens[b] + i, from
+ * row path[b][i] of the tree's own keys and values.  8-bit caches as for
+ * attn_cache_append; a bf16 cache gets copies.
+ *   k_tree, v_tree : bf16 [layers, B, h, n, d_k], 1 <= n <= 128.
+ *   path, path_lens : device int32 [B, n] and [B] as attn_tree_verify writes them
+ *              (the same for every layer); path_lens is clamped to [0, n], and a
+ *              path ends before its first entry outside [0, n).
+ *   k_cache, v_cache : [layers, B, h, L_max, d_k] in cache_format.
+ *   k_scale, v_scale : float [layers, B, h, ceil(L_max / block_tokens)], contiguous;
+ *              ignored for ATTN_CACHE_BF16, with block_tokens.
+ *   strides  : host array of 16 element counts, four (layer, b, h, row) per tensor
+ *              in the order k_tree, v_tree, k_cache, v_cache, each > 0 and a
+ *              multiple of 16 bytes; NULL for contiguous tensors.
+ *   cache_lens : device int32[B] (clamped to [0, L_max]), or NULL when the
+ *              caches are empty.  Not changed: the caller adds path_lens.  Tokens
+ *              that would land past L_max are dropped.
+ *   d_k      : 16, 32, 64 or 128, L_max <= 2^30 (else ATTN_ERR_UNSUPPORTED).
+ * One kernel on `stream`; nothing is allocated.  The caches must not overlap the
+ * tree's keys and values, and two calls on one cache must be ordered on one stream.
+ */
+int attn_cache_append_tree(const void* k_tree, const void* v_tree, const int* path,
+                           const int* path_lens, void* k_cache, void* v_cache, float* k_scale,
+                           float* v_scale, int layers, int B, int h, int n, int L_max, int d_k,
+                           const int64_t* strides, int cache_format, int block_tokens,
+                           const int* cache_lens, struct CUstream_st* stream);
+
+/*
  * attn_bwd -- gradients of attn_fwd: given dout = dLoss/dO, writes
  *   dq = dLoss/dQ, dk = dLoss/dK, dv = dLoss/dV
  * for the same (q, k, v, scale, mask_kind, key_lens).  Per (b, h), with

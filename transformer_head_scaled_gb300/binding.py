@@ -29,6 +29,8 @@ ATTN_ERR_SCRATCH_TOO_SMALL = -5
 ATTN_ERR_WRONG_PLAN = -6
 MASK_WINDOW = 3  # attn_fwd_strided: the window of attn_fwd_window
 CACHE_BF16, CACHE_E4M3, CACHE_INT8 = 0, 1, 2  # attn_cache_format
+PROB_F32, PROB_BF16 = 0, 1  # attn_prob_type
+MOST_NODES = 128  # of a tree of drafted tokens
 _CACHE_FORMATS = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3,
                   torch.int8: CACHE_INT8}
 DECODE_NOALLOC_SCRATCH_BYTES = 1 << 20
@@ -41,6 +43,8 @@ EXPORTS = ("attn_fwd", "attn_fwd_f32", "attn_fwd_window", "attn_fwd_strided", "a
            "attn_bwd_workspace_bytes", "attn_cache_append", "attn_decode_scored",
            "attn_decode_scored_workspace_bytes", "attn_mask_plan", "attn_mask_plan_bytes",
            "attn_fwd_scored", "attn_bwd_scored", "attn_bwd_scored_workspace_bytes",
+           "attn_decode_tree", "attn_decode_tree_workspace_bytes", "attn_tree_verify",
+           "attn_cache_append_tree",
            "attn_check", "attn_status_string",
            "attn_last_cuda_error", "attn_set_wait_limit_ns", "attn_launch_count",
            "attn_diag_tile", "attn_diag_wait_timeout")
@@ -131,6 +135,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                                                ctypes.c_size_t, vp]
         lib.attn_bwd_scored_workspace_bytes.restype = ctypes.c_size_t
         lib.attn_bwd_scored_workspace_bytes.argtypes = [i32] * 6
+        lib.attn_decode_tree.restype = i32
+        lib.attn_decode_tree.argtypes = ([vp] * 10 + [i32] * 6
+                                         + [vp, i32, i32, f32, f32, vp, vp, i32, vp,
+                                            ctypes.c_size_t, vp])
+        lib.attn_decode_tree_workspace_bytes.restype = ctypes.c_size_t
+        lib.attn_decode_tree_workspace_bytes.argtypes = [i32] * 8
+        lib.attn_tree_verify.restype = i32
+        lib.attn_tree_verify.argtypes = [vp] * 8 + [i32] * 3 + [vp, i32, vp]
+        lib.attn_cache_append_tree.restype = i32
+        lib.attn_cache_append_tree.argtypes = [vp] * 8 + [i32] * 6 + [vp, i32, i32, vp, vp]
         lib.attn_check.restype = i32
         lib.attn_check.argtypes = [vp]
         lib.attn_status_string.restype = ctypes.c_char_p
@@ -679,7 +693,7 @@ def _vector(name: str, t, dtype, count: int, device) -> None:
 
 _INT_MAX = 0x7fffffff  # what fits the C calls' sizes
 
-_INT64S = {n: ctypes.c_int64 * n for n in (12, 24)}
+_INT64S = {n: ctypes.c_int64 * n for n in (4, 12, 16, 18, 24)}
 
 
 def _strides_array(strides):
@@ -1049,6 +1063,249 @@ def attn_bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_bwd_scored")
     return dq, dk, dv
+
+
+def _cache_scales(fmt, k_scale, v_scale, block_tokens, count, device):
+    """The scales of a cache, checked (bf16: none); count: tokens to entries."""
+    if fmt == CACHE_BF16:
+        return None, None
+    if block_tokens not in (16, 32, 64, 128):
+        raise ValueError("block_tokens must be 16, 32, 64 or 128")
+    if k_scale is None or v_scale is None:
+        raise ValueError("an 8-bit cache needs k_scale and v_scale")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _vector(name, t, torch.float32, count, device)
+    return k_scale, v_scale
+
+
+def _nodes(name: str, t, dtype, B: int, n: int, device) -> None:
+    if t is None or tuple(t.shape) != (B, n):
+        raise ValueError(f"{name} must be [B, n] = [{B}, {n}]")
+    _vector(name, t, dtype, B * n, device)
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_tree_bytes(device: int, *sizes) -> int:
+    """The workspace size follows from the sizes and the device alone."""
+    return int(load().attn_decode_tree_workspace_bytes(*sizes))
+
+
+def decode_tree_workspace_bytes(B: int, h: int, h_kv: int, n: int, L_max: int, d: int,
+                                cache_format: int = CACHE_BF16, window: int | None = None) -> int:
+    """Scratch bytes attn_decode_tree needs on the current device (0: none)."""
+    return int(load().attn_decode_tree_workspace_bytes(
+        B, h, h_kv, n, L_max, d, cache_format,
+        -1 if window is None else min(int(window), _INT_MAX)))
+
+
+def attn_decode_tree_raw(q_ptr, kt_ptr, vt_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, parents_ptr, o_ptr,
+                         lse_ptr, B, h, h_kv, n, L_max, d, strides, cache_format, block_tokens,
+                         scale, softcap, slopes_ptr, lens_ptr, window, ws_ptr, ws_bytes,
+                         stream_ptr) -> int:
+    """The C call itself, on raw device pointers; ``strides`` = 18 element counts or None."""
+    return load().attn_decode_tree(
+        q_ptr, kt_ptr, vt_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, parents_ptr, o_ptr, lse_ptr, B, h,
+        h_kv, n, L_max, d, _strides_array(strides), cache_format, block_tokens, scale, softcap,
+        slopes_ptr, lens_ptr, window, ws_ptr, ws_bytes, stream_ptr)
+
+
+def attn_decode_tree(q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor,
+                     parents: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     cache_lens: torch.Tensor | None = None, k_scale: torch.Tensor | None = None,
+                     v_scale: torch.Tensor | None = None, block_tokens: int = 64,
+                     scale: float | None = None, softcap: float = 0.0,
+                     slopes: torch.Tensor | None = None, window: int | None = None,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """n <= 128 nodes of a tree of drafted tokens, queries q [B, h, n, d] and keys
+    and values k_tree, v_tree [B, h_kv, n, d] (bf16), over a cache [B, h_kv, L_max, d]
+    of bf16 rows or of 8-bit codes with scales (see attn_cache_append): node i
+    sees the first cache_lens[b] cached tokens (None: all), its ancestors and
+    itself.  parents [B, n] (int32): an earlier node, -1 for a root, anything else
+    for no node.  softcap > 0 caps the scores by a tanh, slopes [h] (float32) bias
+    them by distance, ``window`` hides what lies more than that many positions
+    back (a node stands cache_lens[b] + its depth).  Returns (o, lse)."""
+    _views("q, k_tree and v_tree", torch.bfloat16, q, k_tree, v_tree)
+    fmt = _CACHE_FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise ValueError("the caches must be bf16, torch.float8_e4m3fn or torch.int8")
+    _views("k_cache and v_cache", k_cache.dtype, k_cache, v_cache)
+    B, h, n, d = q.shape
+    h_kv, L_max = k_cache.shape[1:3]
+    if (tuple(k_cache.shape) != (B, h_kv, L_max, d) or v_cache.shape != k_cache.shape
+            or h_kv < 1 or h % h_kv != 0 or k_cache.device != q.device):
+        raise ValueError("caches must be [B, h_kv, L_max, d] with q's B and d, h a multiple of h_kv")
+    if tuple(k_tree.shape) != (B, h_kv, n, d) or v_tree.shape != k_tree.shape:
+        raise ValueError("k_tree and v_tree must be [B, h_kv, n, d] with q's B, n and d")
+    if L_max > _INT_MAX:
+        raise ValueError("caches of 2^31 tokens and more are not supported")
+    dev = q.device
+    k_scale, v_scale = _cache_scales(fmt, k_scale, v_scale, block_tokens,
+                                     B * h_kv * -(-L_max // block_tokens), dev)
+    _nodes("parents", parents, torch.int32, B, n, dev)
+    _vector("cache_lens", cache_lens, torch.int32, B, dev)
+    _vector("slopes", slopes, torch.float32, h, dev)
+    if window is not None and window < 0:
+        raise ValueError("window must be >= 0 (None for none)")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _call_on(dev, stream) as ptr:
+        if out is None:
+            out = _contiguous_like(q)
+        else:
+            _views("q and out", torch.bfloat16, q, out)
+            if out.shape != q.shape:
+                raise ValueError("out must be shaped like q")
+        if lse is None:
+            lse = q.new_empty((B, h, n), dtype=torch.float32)
+        else:
+            _vector("lse", lse, torch.float32, B * h * n, dev)
+        window = -1 if window is None else min(int(window), _INT_MAX)
+        workspace = _workspace(
+            _decode_tree_bytes(dev.index, B, h, h_kv, n, L_max, d, fmt, window), workspace, dev)
+        rc = attn_decode_tree_raw(
+            _ptr(q), _ptr(k_tree), _ptr(v_tree), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(parents), _ptr(out), _ptr(lse), B, h, h_kv, n, L_max, d,
+            _strides(q, k_tree, v_tree, k_cache, v_cache, out), fmt, block_tokens, scale, softcap,
+            _ptr(slopes), _ptr(cache_lens), window, _ptr(workspace), _nbytes(workspace), ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_tree")
+    return out, lse
+
+
+def attn_tree_verify_raw(target_ptr, draft_ptr, tokens_ptr, parents_ptr, uniforms_ptr, path_ptr,
+                         lens_ptr, next_ptr, B, n, V, strides, prob_type, stream_ptr) -> int:
+    """The C call itself, on raw device pointers; ``strides`` = 4 element counts or None."""
+    return load().attn_tree_verify(target_ptr, draft_ptr, tokens_ptr, parents_ptr, uniforms_ptr,
+                                   path_ptr, lens_ptr, next_ptr, B, n, V, _strides_array(strides),
+                                   prob_type, stream_ptr)
+
+
+def attn_tree_verify(target: torch.Tensor, tokens: torch.Tensor, parents: torch.Tensor,
+                     uniforms: torch.Tensor, draft: torch.Tensor | None = None,
+                     path: torch.Tensor | None = None, path_lens: torch.Tensor | None = None,
+                     next_tokens: torch.Tensor | None = None, stream=None):
+    """Which nodes of trees of drafted tokens stand.  target [B, n, V] (float32 or
+    bf16): the target's probabilities of the token after each node; draft,
+    likewise: what each node's children were drawn from (None: children chosen
+    without chance); tokens, parents [B, n] (int32), node 0 the newest token that
+    stands already; uniforms [B, n] (float32) in [0, 1): uniforms[b, c] decides on
+    node c, uniforms[b, 0] draws the next token.  Returns (path, path_lens,
+    next_tokens), int32 [B, n], [B], [B]: the nodes of the accepted path from node
+    0 on, then -1; how many; and the token after them."""
+    if target.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("target must be float32 or bfloat16")
+    for name, t in (("target", target), ("draft", draft)):
+        if t is not None and (t.dim() != 3 or t.dtype != target.dtype or not t.is_cuda
+                              or t.device != target.device or t.shape != target.shape
+                              or (t.shape[2] > 1 and t.stride(2) != 1)):
+            raise ValueError(f"{name} must be a CUDA [B, n, V] tensor of target's type, shape and "
+                             "device with unit last stride")
+    B, n, V = target.shape
+    if max(B, n, V) > _INT_MAX:
+        raise ValueError("sizes of 2^31 and more are not supported")
+    dev = target.device
+    _nodes("tokens", tokens, torch.int32, B, n, dev)
+    _nodes("parents", parents, torch.int32, B, n, dev)
+    _nodes("uniforms", uniforms, torch.float32, B, n, dev)
+    if path is not None:
+        _nodes("path", path, torch.int32, B, n, dev)
+    _vector("path_lens", path_lens, torch.int32, B, dev)
+    _vector("next_tokens", next_tokens, torch.int32, B, dev)
+    strides = None
+    if not target.is_contiguous() or (draft is not None and not draft.is_contiguous()):
+        strides = [*target.stride()[:2], *(target if draft is None else draft).stride()[:2]]
+        strides = _strides_array(strides)
+    with _call_on(dev, stream) as ptr:
+        if path is None:
+            path = tokens.new_empty((B, n))
+        if path_lens is None:
+            path_lens = tokens.new_empty(B)
+        if next_tokens is None:
+            next_tokens = tokens.new_empty(B)
+        rc = attn_tree_verify_raw(
+            _ptr(target), _ptr(draft), _ptr(tokens), _ptr(parents), _ptr(uniforms), _ptr(path),
+            _ptr(path_lens), _ptr(next_tokens), B, n, V, strides,
+            PROB_F32 if target.dtype == torch.float32 else PROB_BF16, ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_tree_verify")
+    return path, path_lens, next_tokens
+
+
+def attn_cache_append_tree_raw(kt_ptr, vt_ptr, path_ptr, path_lens_ptr, k_ptr, v_ptr, ks_ptr,
+                               vs_ptr, layers, B, h, n, L_max, d, strides, cache_format,
+                               block_tokens, lens_ptr, stream_ptr) -> int:
+    """The C call itself, on raw device pointers; ``strides`` = 16 element counts or None."""
+    return load().attn_cache_append_tree(
+        kt_ptr, vt_ptr, path_ptr, path_lens_ptr, k_ptr, v_ptr, ks_ptr, vs_ptr, layers, B, h, n,
+        L_max, d, _strides_array(strides), cache_format, block_tokens, lens_ptr, stream_ptr)
+
+
+def _layer_strides(*tensors):
+    """The (layer, b, h, row) element strides of [layers, B, h, n, d] views; None
+    when all are contiguous.  The stride of a dimension of one entry is never
+    stepped over, whatever the view says."""
+    for t in tensors:
+        if not t.is_contiguous():
+            break
+    else:
+        return None
+    flat = []
+    for t in tensors:
+        step, shape = t.stride(), t.shape
+        room = -(-max(*step, shape[3] * shape[4]) // 16) * 16
+        flat += [step[i] if shape[i] > 1 else room for i in range(4)]
+    return _strides_array(flat)
+
+
+def attn_cache_append_tree(k_tree: torch.Tensor, v_tree: torch.Tensor, path: torch.Tensor,
+                           path_lens: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           cache_lens: torch.Tensor | None, k_scale: torch.Tensor | None = None,
+                           v_scale: torch.Tensor | None = None, block_tokens: int = 64,
+                           stream=None) -> None:
+    """Writes the accepted path of a tree of drafted tokens into the caches of all
+    layers: rows path[b, :path_lens[b]] of bf16 k_tree, v_tree [layers, B, h, n, d]
+    behind the first cache_lens[b] tokens (None: empty) of k_cache, v_cache [layers,
+    B, h, L_max, d] (bf16 rows, or codes with scales [layers, B, h, ceil(L_max /
+    block_tokens)] as attn_cache_append writes them).  Without the layers'
+    dimension: one layer.  path and path_lens are attn_tree_verify's; cache_lens
+    is not changed."""
+    if k_tree.dim() == 4:
+        k_tree, v_tree, k_cache, v_cache = (t.unsqueeze(0)
+                                            for t in (k_tree, v_tree, k_cache, v_cache))
+    fmt = _CACHE_FORMATS.get(k_cache.dtype)
+    if fmt is None:
+        raise ValueError("the caches must be bf16, torch.float8_e4m3fn or torch.int8")
+    dev = k_tree.device
+    for t, dtype in ((k_tree, torch.bfloat16), (v_tree, torch.bfloat16),
+                     (k_cache, k_cache.dtype), (v_cache, k_cache.dtype)):
+        if (t.dim() != 5 or t.dtype != dtype or not t.is_cuda or t.device != dev
+                or t.stride(4) != 1):
+            raise ValueError("k_tree and v_tree must be bf16, the caches of one type, CUDA "
+                             "[layers, B, h, n, d] views on one device with unit last stride")
+    layers, B, h, n, d = k_tree.shape
+    L_max = k_cache.shape[3]
+    if (v_tree.shape != k_tree.shape or tuple(k_cache.shape) != (layers, B, h, L_max, d)
+            or v_cache.shape != k_cache.shape):
+        raise ValueError("k_tree, v_tree must be [layers, B, h, n, d] and the caches "
+                         "[layers, B, h, L_max, d]")
+    if L_max > _INT_MAX:
+        raise ValueError("caches of 2^31 tokens and more are not supported")
+    k_scale, v_scale = _cache_scales(fmt, k_scale, v_scale, block_tokens,
+                                     layers * B * h * -(-L_max // block_tokens), dev)
+    _nodes("path", path, torch.int32, B, n, dev)
+    if path_lens is None:
+        raise ValueError("path_lens must be given")
+    _vector("path_lens", path_lens, torch.int32, B, dev)
+    _vector("cache_lens", cache_lens, torch.int32, B, dev)
+    with _call_on(dev, stream) as ptr:
+        rc = attn_cache_append_tree_raw(
+            _ptr(k_tree), _ptr(v_tree), _ptr(path), _ptr(path_lens), _ptr(k_cache), _ptr(v_cache),
+            _ptr(k_scale), _ptr(v_scale), layers, B, h, n, L_max, d,
+            _layer_strides(k_tree, v_tree, k_cache, v_cache), fmt, block_tokens, _ptr(cache_lens),
+            ptr)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_append_tree")
 
 
 def check(stream=None) -> None:

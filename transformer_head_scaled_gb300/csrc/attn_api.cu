@@ -1187,3 +1187,147 @@ int attn_bwd_scored(const void* q, const void* k, const void* v, const void* o, 
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- drafted tokens
+
+namespace attn {
+namespace {
+// Sizes of attn_decode_tree, shared with its workspace query.
+int tree_decode_sizes(int B, int h, int h_kv, int n, int L_max, int d_k, int cache_format,
+                      int window) {
+  if (B < 1 || h < 1 || h_kv < 1 || n < 1 || L_max < 1 || d_k < 1 || h % h_kv != 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (cache_format < ATTN_CACHE_BF16 || cache_format > ATTN_CACHE_INT8 || window < -1)
+    return ATTN_ERR_INVALID_ARG;
+  if (!tc_head_size(d_k) || n > kMostNodes || L_max > kMostCached) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * h > (1LL << 24) / n) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+}  // namespace
+}  // namespace attn
+
+extern "C" {
+
+size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int L_max, int d_k,
+                                        int cache_format, int window) {
+  (void)B, (void)h, (void)h_kv, (void)n, (void)L_max, (void)d_k, (void)cache_format, (void)window;
+  return 0;
+}
+
+int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* k_cache,
+                     const void* v_cache, const float* k_scale, const float* v_scale,
+                     const int* parents, void* o, float* lse, int B, int h, int h_kv, int n,
+                     int L_max, int d_k, const int64_t* strides, int cache_format,
+                     int block_tokens, float scale, float softcap, const float* slopes,
+                     const int* cache_lens, int window, void* workspace, size_t workspace_bytes,
+                     struct CUstream_st* stream) {
+  (void)workspace, (void)workspace_bytes;
+  if (!q || !k_tree || !v_tree || !k_cache || !v_cache || !parents || !o)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_cache) ||
+      !aligned16(v_cache) || !aligned16(o) || !int_ptr_ok(parents) || !int_ptr_ok(k_scale) ||
+      !int_ptr_ok(v_scale) || !int_ptr_ok(lse) || !int_ptr_ok(slopes) || !int_ptr_ok(cache_lens))
+    return ATTN_ERR_INVALID_ARG;
+  int rc = tree_decode_sizes(B, h, h_kv, n, L_max, d_k, cache_format, window);
+  if (rc == ATTN_ERR_INVALID_ARG) return rc;
+  if (!(std::isfinite(scale) && scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if (!softcap_ok(softcap, scale)) return ATTN_ERR_INVALID_ARG;
+  const bool q8 = cache_format != ATTN_CACHE_BF16;
+  if (q8 && (!k_scale || !v_scale || !block_tokens_ok(block_tokens))) return ATTN_ERR_INVALID_ARG;
+  const int e1 = elem_bytes(cache_format);
+  const int heads[6] = {h, h_kv, h_kv, h_kv, h_kv, h}, rows[6] = {n, n, n, L_max, L_max, n},
+            elem[6] = {2, 2, 2, e1, e1, 2};
+  Strides st[6];
+  if (rc == ATTN_OK && !read_strides(st, strides, 6, heads, rows, d_k, elem))
+    return ATTN_ERR_INVALID_ARG;
+  if (rc != ATTN_OK) return rc;
+  DeviceInfo* di = nullptr;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  TreeDecodeProblem pb{q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, parents, o, lse, B, h,
+                       h_kv, n, L_max, d_k, cache_format, q8 ? block_tokens : 128, scale, softcap,
+                       slopes, cache_lens, window, st[0], st[1], st[2], st[3], st[4], st[5]};
+  const cudaError_t e = launch_decode_tree(pb, make_ctx(*di, stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1);
+  return ATTN_OK;
+}
+
+int attn_tree_verify(const void* target, const void* draft, const int* tokens,
+                     const int* parents, const float* uniforms, int* path, int* path_lens,
+                     int* next_tokens, int B, int n, int V, const int64_t* strides, int prob_type,
+                     struct CUstream_st* stream) {
+  if (!target || !tokens || !parents || !uniforms || !path || !path_lens || !next_tokens)
+    return ATTN_ERR_INVALID_ARG;
+  if (prob_type != ATTN_PROB_F32 && prob_type != ATTN_PROB_BF16) return ATTN_ERR_INVALID_ARG;
+  const uintptr_t off = prob_type == ATTN_PROB_BF16 ? 1u : 3u;
+  if ((reinterpret_cast<uintptr_t>(target) & off) || (reinterpret_cast<uintptr_t>(draft) & off) ||
+      !int_ptr_ok(tokens) || !int_ptr_ok(parents) || !int_ptr_ok(uniforms) || !int_ptr_ok(path) ||
+      !int_ptr_ok(path_lens) || !int_ptr_ok(next_tokens))
+    return ATTN_ERR_INVALID_ARG;
+  if (B < 1 || n < 1 || V < 1) return ATTN_ERR_INVALID_ARG;
+  if (n > kMostNodes || V > (1 << 24) || B > (1 << 24)) return ATTN_ERR_UNSUPPORTED;
+  long long st[4] = {static_cast<long long>(n) * V, V, static_cast<long long>(n) * V, V};
+  for (int i = 0; strides != nullptr && i < (draft ? 4 : 2); ++i) {
+    if (strides[i] < 0 || strides[i] >= (1LL << 40)) return ATTN_ERR_INVALID_ARG;
+    st[i] = strides[i];
+  }
+  DeviceInfo* di = nullptr;
+  int rc;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  TreeVerifyProblem pb{target, draft, tokens, parents, uniforms, path, path_lens, next_tokens, B, n,
+                       V, st[0], st[1], st[2], st[3], prob_type == ATTN_PROB_BF16};
+  const cudaError_t e = launch_tree_verify(pb, make_ctx(*di, stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1);
+  return ATTN_OK;
+}
+
+int attn_cache_append_tree(const void* k_tree, const void* v_tree, const int* path,
+                           const int* path_lens, void* k_cache, void* v_cache, float* k_scale,
+                           float* v_scale, int layers, int B, int h, int n, int L_max, int d_k,
+                           const int64_t* strides, int cache_format, int block_tokens,
+                           const int* cache_lens, struct CUstream_st* stream) {
+  if (!k_tree || !v_tree || !path || !path_lens || !k_cache || !v_cache)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !int_ptr_ok(path) || !int_ptr_ok(path_lens) || !int_ptr_ok(k_scale) ||
+      !int_ptr_ok(v_scale) || !int_ptr_ok(cache_lens))
+    return ATTN_ERR_INVALID_ARG;
+  if (layers < 1 || B < 1 || h < 1 || n < 1 || L_max < 1 || d_k < 1) return ATTN_ERR_INVALID_ARG;
+  if (cache_format < ATTN_CACHE_BF16 || cache_format > ATTN_CACHE_INT8)
+    return ATTN_ERR_INVALID_ARG;
+  const bool q8 = cache_format != ATTN_CACHE_BF16;
+  if (q8 && (!k_scale || !v_scale || !block_tokens_ok(block_tokens))) return ATTN_ERR_INVALID_ARG;
+  if (!tc_head_size(d_k) || n > kMostNodes || L_max > kMostCached) return ATTN_ERR_UNSUPPORTED;
+  const int e1 = elem_bytes(cache_format);
+  LayerStrides st[4];
+  for (int i = 0; i < 4; ++i) {
+    const int rows = i < 2 ? n : L_max, es = i < 2 ? 2 : e1;
+    if (strides != nullptr) {
+      st[i].layer = strides[4 * i];
+      st[i].row = Strides{strides[4 * i + 1], strides[4 * i + 2], strides[4 * i + 3]};
+    } else {
+      st[i].row = bhsd(h, rows, d_k);
+      st[i].layer = st[i].row.b * B;
+    }
+    if (!stride16_ok(st[i].layer, es) || !stride16_ok(st[i].row.b, es) ||
+        !stride16_ok(st[i].row.h, es) || !stride16_ok(st[i].row.n, es))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  // one block of threads at most per cache block that can be touched
+  const int touched = q8 ? cache_blocks_touched(n, L_max, block_tokens) : 1;
+  if (static_cast<double>(layers) * B * h * touched * 2.0 > 2147483647.0)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceInfo* di = nullptr;
+  int rc;
+  if ((rc = device_info(&di)) != ATTN_OK) return rc;
+  CacheTreeProblem pb{k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, layers, B, h, n, L_max,
+                      d_k, !q8, cache_format == ATTN_CACHE_E4M3, q8 ? block_tokens : 128, path,
+                      path_lens, cache_lens, {st[0], st[1]}, {st[2], st[3]}};
+  const cudaError_t e = launch_cache_append_tree(pb, make_ctx(*di, stream));
+  if (e != cudaSuccess) return cuda_fail(e);
+  g_launches.fetch_add(1);
+  return ATTN_OK;
+}
+
+}  // extern "C"

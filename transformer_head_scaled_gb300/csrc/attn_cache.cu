@@ -25,6 +25,10 @@
 // TB/s, the rate of a plain copy), 50 us with blocks of 16; to int8 48 us.  Twice
 // the threads with half the loads each: 54, 50 and 79 us.  One token for 256
 // sequences, 8 heads: 3 us, the launch.
+//
+// The accepted path of a tree of drafted tokens (attn_cache_append_tree) goes
+// the same way: token i of it is row path[b][i] of the tree's keys and values,
+// and one launch does it for all layers.  Into a cache of bf16 rows it is a copy.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -41,7 +45,23 @@ struct CacheParams {
   const int* new_lens;  // new tokens per sequence, or null (n_new each)
   RowStrides ss[2], sd[2];
   int H, n_new, L_max, T, num_blocks, touched;
+  // TREE: token i of sequence b is row path[b][i] of n; B sequences in each of
+  // the layers, whose strides these are
+  const int* path;
+  int B, n;
+  long long sl[2], dl[2];
 };
+
+// How many of a path's first `len` nodes stand before one outside [0, n); by a
+// whole warp.
+__device__ __forceinline__ int path_length(const int* path, int len, int n, int lane) {
+  for (int at = 0; at < len; at += 32) {
+    const int node = at + lane < len ? __ldg(path + at + lane) : 0;
+    const unsigned bad = __ballot_sync(0xffffffffu, node < 0 || node >= n);
+    if (bad != 0) return at + __ffs(bad) - 1;
+  }
+  return len;
+}
 
 constexpr float kScaleMin = 0x1p-100f;
 
@@ -80,7 +100,8 @@ __device__ __forceinline__ float decode1(uint32_t byte) {
 // THREADS threads work on one block of one (b, head) and of keys or values;
 // CHUNKS chunks of 8 elements each wait in a thread's registers.  WARP: one
 // warp per block, eight blocks to a CTA and no barrier; else one CTA per block.
-template <bool E4M3, bool WARP, int THREADS, int CHUNKS>
+// TREE: the new tokens are a path through a tree's, in every layer.
+template <bool E4M3, bool WARP, int THREADS, int CHUNKS, bool TREE>
 __global__ void __launch_bounds__(WARP ? 256 : THREADS)
     attn_cache_append_kernel(const CacheParams p, unsigned units, int cpr_log2) {
   __shared__ float red[WARP ? 1 : THREADS / 32];
@@ -91,9 +112,12 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   const int kv = unit & 1u;
   const unsigned rest = unit >> 1;
   const unsigned bh = rest / static_cast<unsigned>(p.touched);
-  const int b = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(b) * p.H;
+  const int bl = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(bl) * p.H;
+  const int layer = TREE ? bl / p.B : 0, b = TREE ? bl - layer * p.B : bl;
   const int len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
-  const int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
+  int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
+  const int* path = TREE ? p.path + static_cast<long long>(b) * p.n_new : nullptr;
+  if (TREE) more = path_length(path, more, p.n, threadIdx.x & 31);
   const int end = len + min(more, p.L_max - len);  // tokens that do not fit are dropped
   const int blk = len / p.T + static_cast<int>(rest - bh * p.touched);
   if (blk >= p.num_blocks) return;
@@ -102,16 +126,29 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   const int first = max(len, row0), last = min(end, row0 + p.T);  // new rows of this block
   if (first >= last) return;  // the same for every thread of the unit
 
-  const __nv_bfloat16* src = p.src[kv] + b * p.ss[kv].b + hh * p.ss[kv].h +
-                             static_cast<long long>(first - len) * p.ss[kv].n;
+  const __nv_bfloat16* src = p.src[kv] + b * p.ss[kv].b + hh * p.ss[kv].h;
+  if (TREE)
+    src += layer * p.sl[kv];
+  else
+    src += static_cast<long long>(first - len) * p.ss[kv].n;
   uint8_t* dst = p.dst[kv] + b * p.sd[kv].b + hh * p.sd[kv].h;
+  if (TREE) dst += layer * p.dl[kv];
   const int chunks = (last - first) << cpr_log2;  // 8-element chunks, a row's side by side
 
   // a thread's chunks stand in one column, `rows` rows apart
   const int rows = THREADS >> cpr_log2, row = tid >> cpr_log2;
   const int col = (tid - (row << cpr_log2)) * 8;
   uint4 w[CHUNKS];
-  {
+  if constexpr (TREE) {
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (tid + i * THREADS < chunks) {
+        const int node = __ldg(path + (first - len) + row + i * rows);
+        w[i] = __ldg(reinterpret_cast<const uint4*>(src + node * p.ss[kv].n + col));
+      }
+    }
+  } else {
     const __nv_bfloat16* at = src + row * p.ss[kv].n + col;
     const long long step = rows * p.ss[kv].n;
 #pragma unroll
@@ -182,30 +219,62 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   }
 }
 
-template <bool E4M3>
+template <bool E4M3, bool TREE>
 cudaError_t launch_append(const CacheParams& p, unsigned units, int cpr_log2, cudaStream_t stream) {
   // most 8-element chunks of new tokens that one block can get
   const int most = (p.n_new < p.T ? p.n_new : p.T) << cpr_log2;
   if (most <= 4 * 32) {
-    attn_cache_append_kernel<E4M3, true, 32, 4>
+    attn_cache_append_kernel<E4M3, true, 32, 4, TREE>
         <<<(units + 7) / 8, 256, 0, stream>>>(p, units, cpr_log2);
   } else if (most <= 8 * 32) {
-    attn_cache_append_kernel<E4M3, true, 32, 8>
+    attn_cache_append_kernel<E4M3, true, 32, 8, TREE>
         <<<(units + 7) / 8, 256, 0, stream>>>(p, units, cpr_log2);
   } else if (most <= 8 * 64) {
-    attn_cache_append_kernel<E4M3, false, 64, 8><<<units, 64, 0, stream>>>(p, units, cpr_log2);
+    attn_cache_append_kernel<E4M3, false, 64, 8, TREE>
+        <<<units, 64, 0, stream>>>(p, units, cpr_log2);
   } else if (most <= 8 * 128) {
-    attn_cache_append_kernel<E4M3, false, 128, 8><<<units, 128, 0, stream>>>(p, units, cpr_log2);
+    attn_cache_append_kernel<E4M3, false, 128, 8, TREE>
+        <<<units, 128, 0, stream>>>(p, units, cpr_log2);
   } else {
-    attn_cache_append_kernel<E4M3, false, 256, 8><<<units, 256, 0, stream>>>(p, units, cpr_log2);
+    attn_cache_append_kernel<E4M3, false, 256, 8, TREE>
+        <<<units, 256, 0, stream>>>(p, units, cpr_log2);
   }
   return cudaGetLastError();
+}
+
+// The path's rows of a bf16 cache: a warp per (layer, sequence, head, keys or
+// values), 16-byte chunks of its rows side by side.  Bound by the latency of
+// three loads in a row (lengths, path, rows).
+__global__ void __launch_bounds__(256)
+    attn_cache_copy_tree_kernel(const CacheParams p, unsigned units, int cpr_log2) {
+  const unsigned unit = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 31;
+  const int kv = unit & 1u;
+  const unsigned bh = unit >> 1;
+  const int bl = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(bl) * p.H;
+  const int layer = bl / p.B, b = bl - layer * p.B;
+  const int len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
+  int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
+  const int* path = p.path + static_cast<long long>(b) * p.n_new;
+  more = min(path_length(path, more, p.n, lane), p.L_max - len);
+  const __nv_bfloat16* src = p.src[kv] + layer * p.sl[kv] + b * p.ss[kv].b + hh * p.ss[kv].h;
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.dst[kv]) + layer * p.dl[kv] +
+                       b * p.sd[kv].b + hh * p.sd[kv].h + len * p.sd[kv].n;
+  const int chunks = more << cpr_log2;
+#pragma unroll 4
+  for (int c = lane; c < chunks; c += 32) {
+    const int row = c >> cpr_log2, col = (c - (row << cpr_log2)) * 8;
+    const int node = __ldg(path + row);
+    *reinterpret_cast<uint4*>(dst + row * p.sd[kv].n + col) =
+        __ldg(reinterpret_cast<const uint4*>(src + node * p.ss[kv].n + col));
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheAppendProblem& pb, const LaunchCtx& ctx) {
-  CacheParams p;
+  CacheParams p{};
   p.src[0] = static_cast<const __nv_bfloat16*>(pb.k_new);
   p.src[1] = static_cast<const __nv_bfloat16*>(pb.v_new);
   p.dst[0] = static_cast<uint8_t*>(pb.k_cache);
@@ -227,8 +296,45 @@ cudaError_t launch_cache_append(const CacheAppendProblem& pb, const LaunchCtx& c
   const unsigned units = 2u * pb.B * pb.H * p.touched;  // the caller keeps it below 2^31
   int cpr_log2 = 1;  // 8-element chunks of a row
   while ((8 << cpr_log2) < pb.d) ++cpr_log2;
-  return pb.e4m3 ? launch_append<true>(p, units, cpr_log2, ctx.stream)
-                 : launch_append<false>(p, units, cpr_log2, ctx.stream);
+  return pb.e4m3 ? launch_append<true, false>(p, units, cpr_log2, ctx.stream)
+                 : launch_append<false, false>(p, units, cpr_log2, ctx.stream);
+}
+
+cudaError_t launch_cache_append_tree(const CacheTreeProblem& pb, const LaunchCtx& ctx) {
+  CacheParams p{};
+  p.src[0] = static_cast<const __nv_bfloat16*>(pb.k_tree);
+  p.src[1] = static_cast<const __nv_bfloat16*>(pb.v_tree);
+  p.dst[0] = static_cast<uint8_t*>(pb.k_cache);
+  p.dst[1] = static_cast<uint8_t*>(pb.v_cache);
+  p.scale[0] = pb.k_scale;
+  p.scale[1] = pb.v_scale;
+  p.lens = pb.cache_lens;
+  p.new_lens = pb.path_lens;
+  p.path = pb.path;
+  for (int i = 0; i < 2; ++i) {
+    p.ss[i] = pb.src[i].row;
+    p.sl[i] = pb.src[i].layer;
+    p.sd[i] = pb.dst[i].row;
+    p.dl[i] = pb.dst[i].layer;
+  }
+  p.B = pb.B;
+  p.H = pb.H;
+  p.n = pb.n;
+  p.n_new = pb.n;
+  p.L_max = pb.L_max;
+  int cpr_log2 = 1;
+  while ((8 << cpr_log2) < pb.d) ++cpr_log2;
+  const unsigned rows = 2u * pb.layers * pb.B * pb.H;
+  if (pb.bf16) {
+    attn_cache_copy_tree_kernel<<<(rows + 7) / 8, 256, 0, ctx.stream>>>(p, rows, cpr_log2);
+    return cudaGetLastError();
+  }
+  p.T = pb.block_tokens;
+  p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
+  p.touched = cache_blocks_touched(pb.n, pb.L_max, pb.block_tokens);
+  const unsigned units = rows * p.touched;  // the caller keeps it below 2^31
+  return pb.e4m3 ? launch_append<true, true>(p, units, cpr_log2, ctx.stream)
+                 : launch_append<false, true>(p, units, cpr_log2, ctx.stream);
 }
 
 int cache_blocks_touched(int n_new, int L_max, int block_tokens) {

@@ -294,6 +294,68 @@ cudaError_t launch_cache_append(const CacheAppendProblem& pb, const LaunchCtx& c
 // Blocks that the new tokens of one sequence can fall into.
 int cache_blocks_touched(int n_new, int L_max, int block_tokens);
 
+// The accepted path of a tree of drafted tokens into the caches of all layers.
+struct LayerStrides {
+  long long layer;
+  RowStrides row;
+};
+struct CacheTreeProblem {
+  const void* k_tree;  // bf16 [layers, B, H, n, d]
+  const void* v_tree;
+  void* k_cache;  // [layers, B, H, L_max, d]: bf16 rows or 8-bit codes
+  void* v_cache;
+  float* k_scale;  // [layers, B, H, ceil(L_max / block_tokens)]; unused for bf16
+  float* v_scale;
+  int layers, B, H, n, L_max, d;
+  bool bf16, e4m3;
+  int block_tokens;
+  const int* path;        // [B, n] nodes
+  const int* path_lens;   // [B]
+  const int* cache_lens;  // device int32[B] or null (empty caches)
+  LayerStrides src[2], dst[2];  // of keys and values
+};
+cudaError_t launch_cache_append_tree(const CacheTreeProblem& pb, const LaunchCtx& ctx);
+
+// A tree of drafted tokens: nodes at most.
+constexpr int kMostNodes = 128;
+
+// Which drafted tokens stand, and the token after them.
+struct TreeVerifyProblem {
+  const void* target;  // probabilities [B, n, V], f32 or bf16
+  const void* draft;   // likewise, or null
+  const int* tokens;   // [B, n]
+  const int* parents;
+  const float* uniforms;
+  int* path;  // [B, n]
+  int* path_lens;
+  int* next_tokens;
+  int B, n, V;
+  long long tb, tn, db, dn;  // element strides of batch entries and nodes
+  bool bf16;
+};
+cudaError_t launch_tree_verify(const TreeVerifyProblem& pb, const LaunchCtx& ctx);
+
+// Attention of a tree's nodes over a cache and their ancestors.
+struct TreeDecodeProblem {
+  const void* q;  // bf16 [B, H, n, d]
+  const void* k_tree;  // bf16 [B, HK, n, d]
+  const void* v_tree;
+  const void* k_cache;  // [B, HK, L_max, d]
+  const void* v_cache;
+  const float* k_scale;  // [B, HK, ceil(L_max / block_tokens)]; unused for bf16
+  const float* v_scale;
+  const int* parents;  // [B, n]
+  void* o;
+  float* lse;  // or null
+  int B, H, HK, n, L_max, d, format, block_tokens;
+  float scale, softcap;  // softcap <= 0: none
+  const float* slopes;   // device float[H] or null
+  const int* cache_lens;  // device int32[B] or null
+  int window;  // -1: none
+  RowStrides sq, skt, svt, sk, sv, so;
+};
+cudaError_t launch_decode_tree(const TreeDecodeProblem& pb, const LaunchCtx& ctx);
+
 // Decoding with changed scores against a bf16, e4m3 or int8 cache.
 struct ScoredDecodeProblem {
   const void* q;  // bf16 [B, H, n_q, d]
