@@ -116,6 +116,7 @@ CASES = [
     (2, 2, 2, 65, 128, 128, 128, 0.0, False, None, "roots", [128, 127]),
     (1, 2, 1, 9, 9000, 64, 128, 0.0, True, None, "random", [8999]),  # the cache is split
     (1, 2, 2, 12, 5000, 128, 16, 30.0, False, 2100, "random", [4996]),
+    (2, 2, 1, 70, 3, 64, 16, 0.0, True, 5, "chain", [3, 0]),  # a window wider than the cache
     (5, 2, 1, 3, 640, 16, 64, 0.0, False, None, "holes", [640, 1, 0, 333, 64]),
 ]
 

@@ -1201,17 +1201,46 @@ int tree_decode_sizes(int B, int h, int h_kv, int n, int L_max, int d_k, int cac
     return ATTN_ERR_INVALID_ARG;
   if (!tc_head_size(d_k) || n > kMostNodes || L_max > kMostCached) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * h > (1LL << 24) / n) return ATTN_ERR_UNSUPPORTED;
+  // the kernel counts the visible cache's tiles over all sequences and key heads
+  // (and blocks of query rows) in 31 bits
+  const long long blocks = (static_cast<long long>(h / h_kv) * n + 255) / 256;
+  if (static_cast<long long>(B) * h_kv * blocks * (L_max / tree_tile_keys(d_k) + 4LL) > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 }  // namespace
+
+TreePlan tree_plan(int B, int HK, int rows, int n, int L_max, int d, int window, int num_sms) {
+  TreePlan plan;
+  plan.blocks = (rows + 255) / 256;
+  plan.block_rows = rows < 256 ? rows : 256;
+  const int kt = tree_tile_keys(d);
+  plan.tree_tiles = (n + kt - 1) / kt;
+  const long long units = static_cast<long long>(B) * HK * plan.blocks;
+  // most tiles of a unit (a window may begin inside one)
+  const long long seen = window >= 0 && window < L_max ? window + kt - 1LL : L_max;
+  const long long tiles = (seen + kt - 1) / kt + plan.tree_tiles;
+  plan.whole = tiles <= 8;
+  const long long useful = plan.whole ? units : (units * tiles + tree_min_tiles() - 1) / tree_min_tiles();
+  plan.ctas = static_cast<int>(useful < num_sms ? useful : num_sms);
+  plan.part_off = plan.workspace_bytes = 0;
+  if (plan.whole) return plan;
+  // the sequences' first tiles, then two parts per CTA
+  plan.part_off = (static_cast<size_t>(B) + 1 + 3) / 4 * 4;
+  plan.workspace_bytes = (plan.part_off + static_cast<size_t>(plan.ctas) * 2 * plan.block_rows *
+                                              (d + kPartTail)) * sizeof(float);
+  return plan;
+}
 }  // namespace attn
 
 extern "C" {
 
 size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int L_max, int d_k,
                                         int cache_format, int window) {
-  (void)B, (void)h, (void)h_kv, (void)n, (void)L_max, (void)d_k, (void)cache_format, (void)window;
-  return 0;
+  if (tree_decode_sizes(B, h, h_kv, n, L_max, d_k, cache_format, window) != ATTN_OK) return 0;
+  DeviceInfo* di = nullptr;
+  if (device_info(&di) != ATTN_OK) return 0;
+  return tree_plan(B, h_kv, h / h_kv * n, n, L_max, d_k, window, di->num_sms).workspace_bytes;
 }
 
 int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* k_cache,
@@ -1221,7 +1250,6 @@ int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, cons
                      int block_tokens, float scale, float softcap, const float* slopes,
                      const int* cache_lens, int window, void* workspace, size_t workspace_bytes,
                      struct CUstream_st* stream) {
-  (void)workspace, (void)workspace_bytes;
   if (!q || !k_tree || !v_tree || !k_cache || !v_cache || !parents || !o)
     return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_cache) ||
@@ -1245,10 +1273,31 @@ int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, cons
   if ((rc = device_info(&di)) != ATTN_OK) return rc;
   TreeDecodeProblem pb{q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, parents, o, lse, B, h,
                        h_kv, n, L_max, d_k, cache_format, q8 ? block_tokens : 128, scale, softcap,
-                       slopes, cache_lens, window, st[0], st[1], st[2], st[3], st[4], st[5]};
-  const cudaError_t e = launch_decode_tree(pb, make_ctx(*di, stream));
+                       slopes, cache_lens,
+                       window < L_max + n ? window : -1,  // (the tree's own keys are that far back too)
+                       st[0], st[1], st[2], st[3], st[4], st[5]};
+  const TreePlan plan = tree_plan(B, h_kv, h / h_kv * n, n, L_max, d_k, window, di->num_sms);
+  if (plan.workspace_bytes > 0 &&
+      (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
+    return ATTN_ERR_INVALID_ARG;
+  CUtensorMap maps[4];
+  const int kt = tree_tile_keys(d_k);
+  for (int i = 0; i < 2; ++i) {
+    const void* cache = i ? v_cache : k_cache;
+    rc = q8 ? encode_4d_bytes(&maps[i], cache, d_k, L_max, h_kv, B, st[3 + i], 1, kt)
+            : encode_4d(&maps[i], cache, d_k, L_max, h_kv, B, st[3 + i], kt);
+    if (rc != ATTN_OK) return rc;
+    if ((rc = encode_4d(&maps[2 + i], i ? v_tree : k_tree, d_k, n, h_kv, B, st[1 + i], kt)) !=
+        ATTN_OK)
+      return rc;
+  }
+  const LaunchCtx ctx = make_ctx(*di, stream);
+  const cudaError_t e =
+      cache_format == ATTN_CACHE_BF16   ? launch_decode_tree_bf16(pb, maps, plan, workspace, ctx)
+      : cache_format == ATTN_CACHE_E4M3 ? launch_decode_tree_e4m3(pb, maps, plan, workspace, ctx)
+                                        : launch_decode_tree_int8(pb, maps, plan, workspace, ctx);
   if (e != cudaSuccess) return cuda_fail(e);
-  g_launches.fetch_add(1);
+  g_launches.fetch_add(plan.whole ? 1 : 2);
   return ATTN_OK;
 }
 

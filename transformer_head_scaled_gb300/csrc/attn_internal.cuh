@@ -354,7 +354,26 @@ struct TreeDecodeProblem {
   int window;  // -1: none
   RowStrides sq, skt, svt, sk, sv, so;
 };
-cudaError_t launch_decode_tree(const TreeDecodeProblem& pb, const LaunchCtx& ctx);
+struct TreePlan {
+  int ctas;
+  bool whole;      // a CTA takes whole units (sequence, key head, block of query rows)
+  int blocks;      // of query rows of a key head
+  int block_rows;  // rows of a part in the workspace
+  int tree_tiles;  // tiles of the tree's own keys
+  size_t part_off;  // floats before the parts in the workspace
+  size_t workspace_bytes;
+};
+TreePlan tree_plan(int B, int HK, int rows, int n, int L_max, int d, int window, int num_sms);
+int tree_tile_keys(int d);
+int tree_min_tiles();
+// maps: the key and the value cache with a box of a tile's rows (bf16: swizzled as
+// the operand of a product; 8 bits: as bytes), then the tree's keys and values.
+cudaError_t launch_decode_tree_bf16(const TreeDecodeProblem& pb, const CUtensorMap* maps,
+                                    const TreePlan& plan, void* workspace, const LaunchCtx& ctx);
+cudaError_t launch_decode_tree_e4m3(const TreeDecodeProblem& pb, const CUtensorMap* maps,
+                                    const TreePlan& plan, void* workspace, const LaunchCtx& ctx);
+cudaError_t launch_decode_tree_int8(const TreeDecodeProblem& pb, const CUtensorMap* maps,
+                                    const TreePlan& plan, void* workspace, const LaunchCtx& ctx);
 
 // Decoding with changed scores against a bf16, e4m3 or int8 cache.
 struct ScoredDecodeProblem {

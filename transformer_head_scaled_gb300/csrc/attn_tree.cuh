@@ -1,0 +1,1270 @@
+// attn_tree.cuh -- attention of a tree of drafted tokens over a key/value cache
+// in bf16 or in 8 bits.  Included by one source file per cache format.
+//
+// Node i of sequence b stands at position p_i = L + depth_i behind the L tokens
+// of its cache and sees them and its own ancestors (itself among them):
+//   x_j = cap * tanh(scale * q_i . k_j / cap) - slope_h * (p_i - p_j)
+//   O_i = sum_j softmax_j(x) v_j,   LSE_i = ln sum_j exp(x_j)
+// over the cached keys j (p_j = j >= p_i - window) from the cache and the
+// ancestors a (p_a = L + depth_a >= p_i - window) from the tree's own keys.
+//
+// Bound by HBM (the visible cache, read once for each 256 query rows of a key
+// head) while the rows are few, by the exponentials and the tensor cores from
+// about 200 rows on.  The G * n query rows of a key head (G query heads share
+// it) are the rows of tcgen05 tiles of 128, so that a cache tile is multiplied
+// for all of them while it is in shared memory.
+//
+// Work split: the visible cache of all sequences and key heads, and behind each
+// its tree's own keys, are one list of tiles of BN keys; a unit is a sequence,
+// key head and block of 256 query rows.  Every CTA (one per SM) takes an equal
+// run of the list, whatever the lengths are; units that several CTAs share go
+// through the workspace to a second kernel.  Where units are short every CTA
+// takes whole ones instead, and there is no second kernel.
+//
+// Inside a CTA two streams (a softmax warpgroup and an MMA warp each) overlap
+// one's exponentials with the other's products.  With more than 128 rows a stream
+// takes one tile of rows and both see every key tile; with at most 128 they take
+// every second key tile with the same rows.  With at most 64 (32) rows the tile
+// of 128 holds them two (four) times, and each copy takes a half (a quarter) of a
+// tile's keys: its probabilities of the others stay zero.  Exponentials cost a
+// warp the same for one row as for 32, and only so do all four warps of a
+// stream share them.  The parts of a row are joined at its end.
+//
+// Warps 0-3, 4-7: softmax of stream 0 and 1; 8-11: the query rows, the nodes'
+// ancestors, and for 8-bit caches the widening of codes to bf16 (exact, both
+// kinds); 12, 13: copies of keys and of values; 14, 15: MMA of stream 0 and 1.
+// Every wait is bounded; on timeout the kernel records kDevTimeout, all roles
+// drain and the CTA returns.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "attn_internal.cuh"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+using namespace ptx;
+
+enum CacheFormat : int { kCacheBf16 = 0, kCacheE4M3 = 1, kCacheInt8 = 2 };
+
+constexpr int BM = 128;        // query rows per tile (= tensor-memory lanes)
+constexpr int kBlockRows = 2 * BM;
+constexpr int AUX_WARP = 8;
+constexpr int KLOAD_WARP = 12;
+constexpr int VLOAD_WARP = 13;
+constexpr int MMA_WARP = 14;   // and 15
+constexpr int NUM_THREADS = 512;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr float kRescale = 8.0f;  // a running maximum is kept until a score exceeds it by 2^8
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMergeStride = 20;  // floats: 16 columns of a part's row, four apart in the banks
+
+template <int FMT_, int D_>
+struct TCfg {
+  static constexpr int FMT = FMT_, D = D_;
+  static constexpr bool Q8 = FMT_ != kCacheBf16;
+  static constexpr int BN = D_ == 128 ? 64 : 128;          // keys per tile
+  static constexpr uint32_t RB = (D_ < 64 ? D_ : 64) * 2;  // bytes of a row in one block
+  static constexpr int NB = D_ > 64 ? D_ / 64 : 1;
+  static constexpr uint32_t SWZ = RB == 128 ? 2u : (RB == 64 ? 4u : 6u);
+  static constexpr int KPB = RB / 32;
+  static constexpr int CPB = RB / 16;  // 16-byte chunks of a block row
+  static constexpr int QSLOTS = D_ == 128 ? 1 : 2;
+  static constexpr uint32_t Q_TILE = BM * D_ * 2, Q_BLOCK = BM * RB;
+  static constexpr uint32_t KV_TILE = BN * D_ * 2, KV_BLOCK = BN * RB;
+  static constexpr uint32_t RAW_TILE = BN * D_;  // codes
+  static constexpr int KSTAGES = D_ >= 64 ? (Q8 ? 2 : 4) : (Q8 ? 4 : 6);  // of bf16 tiles
+  static constexpr int VSTAGES = D_ >= 64 && Q8 ? 3 : KSTAGES;
+  static constexpr int RAWS = Q8 ? (D_ >= 64 ? 3 : 6) : 1;  // of tiles of codes
+  static constexpr uint32_t OW = D_ < 32 ? 32 : D_;
+  static constexpr int MOST_SPLIT = BN / 32;  // copies of a row in a tile
+  __host__ __device__ static constexpr uint32_t col_s(int s) { return BN * s; }
+  __host__ __device__ static constexpr uint32_t col_o(int s) { return 2 * BN + OW * s; }
+  __host__ __device__ static constexpr uint32_t col_p(int s) {
+    return 2 * BN + 2 * OW + (BN / 2) * s;
+  }
+  __host__ __device__ static constexpr uint32_t swz(uint32_t r) {
+    return ((r * RB) >> 7) & (RB / 16 - 1);
+  }
+  static_assert(col_p(2) <= TMEM_COLS, "tensor memory");
+};
+
+// A run of a unit's tiles.
+struct TreeItem {
+  int more;        // 0: the CTA's work has ended
+  int b, hk;
+  int row0, rows;  // of the key head's query rows
+  int split;       // copies of each row in a tile; 0: two tiles of rows
+  int L, key0;     // cached tokens, and the first one that any node sees
+  int base0, ctx;  // key of the unit's first cache tile, and how many there are
+  int t0, n;       // this run of its tiles
+  int whole, slot;
+};
+
+struct TreeParams {
+  const __nv_bfloat16* q;
+  const int* parents;
+  const float* k_scale;
+  const float* v_scale;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part;      // [CTA][2][block rows][D + kPartTail]
+  unsigned* first;  // [B + 1], the list index of each sequence's first tile, and the total
+  const int* cache_lens;
+  const float* slopes;
+  RowStrides sq, so;
+  const uint8_t* k;  // 8-bit caches whose rows lie side by side are copied in runs
+  const uint8_t* v;
+  RowStrides sk, sv;
+  bool run_k, run_v, whole;
+  uint64_t limit_ns;
+  int* status;
+  int B, H, HK, G, n, L_max, T_log2, num_blocks, window;
+  int rows, blocks, block_rows;  // query rows of a key head, their blocks, rows of a part
+  int tree_tiles, rounds;
+  float scale_log2, cap_log2, cap_in;
+  CapPoly cap;
+  bool capped, wide;
+};
+
+template <class C>
+struct __align__(1024) TreeSmem {
+  uint8_t q[C::QSLOTS][2][C::Q_TILE];
+  uint8_t k[C::KSTAGES][C::KV_TILE];
+  uint8_t v[C::VSTAGES][C::KV_TILE];
+  uint8_t raw_k[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
+  uint8_t raw_v[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
+  float merge[2 * BM][kMergeStride];
+  float2 stat[2 * BM];
+  uint32_t line[2][kMostNodes][4];  // what a node sees of the tree
+  int depth[2][kMostNodes];         // -1: no node
+  int up[2][kMostNodes];            // scratch: parents, and 2^k-th ancestors
+  TreeItem item[2];
+  uint64_t item_full[2], item_empty[2], q_empty[C::QSLOTS];
+  uint64_t k_full[C::KSTAGES], k_empty[C::KSTAGES], v_full[C::VSTAGES], v_empty[C::VSTAGES];
+  uint64_t raw_full[2][C::RAWS], raw_empty[2][C::RAWS];  // keys, values
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain[2];
+  uint64_t aux_sync, join_sync;  // barriers of the auxiliary and of the softmax threads
+  unsigned warp_sum[NUM_THREADS / 32];
+  unsigned total;
+  int start_b;
+  unsigned start_off;
+  uint32_t tmem_base;
+  int abort;
+};
+
+// The tiles of a sequence's visible cache and of its tree.
+struct TreeSeq {
+  int L, key0, base0, ctx, tiles;
+};
+template <int BN>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+  TreeSeq s;
+  s.L = p.L_max;
+  if (p.cache_lens != nullptr) s.L = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
+  // (a root, at position L, sees furthest back)
+  s.key0 = p.window >= 0 ? max(s.L - p.window, 0) : 0;
+  s.base0 = s.key0 & ~(BN - 1);
+  s.ctx = s.key0 < s.L ? (s.L - s.base0 + BN - 1) / BN : 0;
+  s.tiles = s.ctx + p.tree_tiles;
+  return s;
+}
+
+constexpr int kMinTreeTiles = 2;  // of a CTA's run
+__host__ __device__ __forceinline__ unsigned tree_share(unsigned total, int ctas) {
+  const unsigned each = total / static_cast<unsigned>(ctas) + 1;
+  return each < kMinTreeTiles ? kMinTreeTiles : each;
+}
+
+// A CTA's place in its work.
+template <int BN>
+struct TreeCursor {
+  TreeSeq s;
+  int b, sub, tile;
+  unsigned left;  // tiles (split), units (whole)
+  __device__ __forceinline__ void begin(const TreeParams& p, int start_b, unsigned off,
+                                        unsigned count) {
+    const int subs = p.HK * p.blocks;
+    left = count;
+    if (p.whole) {
+      b = blockIdx.x / subs;
+      sub = blockIdx.x - b * subs;
+      tile = 0;
+      if (left > 0) s = tree_seq<BN>(p, b);
+      return;
+    }
+    b = start_b;
+    if (left == 0) return;
+    s = tree_seq<BN>(p, b);
+    sub = off / static_cast<unsigned>(s.tiles);
+    tile = off - static_cast<unsigned>(sub) * s.tiles;
+  }
+  // the next run, or false at the end
+  __device__ __forceinline__ bool next(const TreeParams& p, TreeItem& it) {
+    if (left == 0) {
+      it.more = 0;
+      return false;
+    }
+    const int rb = sub % p.blocks;
+    it.more = 1;
+    it.b = b;
+    it.hk = sub / p.blocks;
+    it.row0 = rb * kBlockRows;
+    it.rows = min(p.rows - it.row0, kBlockRows);
+    it.split = it.rows > BM ? 0 : (it.rows > BM / 2 ? 1 : (it.rows > BM / 4 ? 2 : BN / 32));
+    it.L = s.L;
+    it.key0 = s.key0;
+    it.base0 = s.base0;
+    it.ctx = s.ctx;
+    it.t0 = tile;
+    const int subs = p.HK * p.blocks;
+    if (p.whole) {
+      it.n = s.tiles;
+      it.whole = 1;
+      it.slot = 0;
+      --left;
+      const int was = b;
+      const int u = b * subs + sub + gridDim.x;
+      if (left > 0) {
+        b = u / subs;
+        sub = u - b * subs;
+        if (b != was) s = tree_seq<BN>(p, b);
+      }
+      return true;
+    }
+    it.n = min(static_cast<unsigned>(s.tiles - tile), left);
+    it.whole = it.n == s.tiles;
+    // a CTA's run begins in its first unit and ends in its last
+    it.slot = 0;
+    left -= it.n;
+    tile = 0;
+    if (left > 0 && ++sub == subs) {
+      sub = 0;
+      s = tree_seq<BN>(p, ++b);
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ uint64_t tree_sdesc(uint32_t smem_addr, uint32_t lbo_bytes,
+                                               uint32_t sbo_bytes, uint32_t swz) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo_bytes >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo_bytes >> 4) & 0x3FFFu) << 32;
+  d |= 1ull << 46;
+  d |= static_cast<uint64_t>(swz) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Two of a word's four codes (bytes 2 * HI and 2 * HI + 1) as a bf16 pair, exactly.
+template <int FMT, int HI>
+__device__ __forceinline__ uint32_t widen2(uint32_t w) {
+  uint32_t t, y;
+  if (FMT == kCacheE4M3) {
+    // sign, four exponent and three mantissa bits to their places in a bf16, whose
+    // exponent is then 120 too small (the smallest codes are subnormal numbers in both)
+    t = __byte_perm(w, 0u, HI ? 0x3424 : 0x1404);
+    y = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+    const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7b80));  // 2^120
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), up);
+    return *reinterpret_cast<const uint32_t*>(&x);
+  }
+  // the low seven bits c as 128 + c, less 128, or 256 for a negative code
+  t = __byte_perm(w, 0x43434343u, HI ? 0x4342 : 0x4140);
+  const uint32_t a = t & 0xff7fff7fu, b = t & 0xff80ff80u;
+  const __nv_bfloat162 x = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+// A tile of codes to bf16 in the layout of a swizzled copy, by the 128 threads of
+// the auxiliary warps; rows outside [lo, hi) become zeros.
+template <class C>
+__device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int tid, int lo,
+                                           int hi) {
+  constexpr int CPR = C::D / 16;  // 16-code chunks of a row
+#pragma unroll 2
+  for (int i = tid; i < C::BN * CPR; i += 128) {
+    const int row = i / CPR, c = i % CPR;
+    const int at = C::D == 128 ? c ^ (row & 7) : c;
+    const uint4 w = *reinterpret_cast<const uint4*>(raw + row * C::D + at * 16);
+    uint4 a = make_uint4(widen2<C::FMT, 0>(w.x), widen2<C::FMT, 1>(w.x), widen2<C::FMT, 0>(w.y),
+                         widen2<C::FMT, 1>(w.y));
+    uint4 b = make_uint4(widen2<C::FMT, 0>(w.z), widen2<C::FMT, 1>(w.z), widen2<C::FMT, 0>(w.w),
+                         widen2<C::FMT, 1>(w.w));
+    if (row < lo || row >= hi) a = b = make_uint4(0u, 0u, 0u, 0u);
+    uint8_t* to = out + (2 * c / C::CPB) * C::KV_BLOCK + row * C::RB;
+    const int c0 = 2 * c % C::CPB, x = C::swz(row);
+    // (the two halves of a 256-byte row would meet in the same banks)
+    const bool turn = C::D == 128 && (c & 4);
+    *reinterpret_cast<uint4*>(to + (((turn ? c0 + 1 : c0) ^ x) << 4)) = turn ? b : a;
+    *reinterpret_cast<uint4*>(to + (((turn ? c0 : c0 + 1) ^ x) << 4)) = turn ? a : b;
+  }
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    attn_tree_kernel(const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv,
+                     const __grid_constant__ CUtensorMap tmkt,
+                     const __grid_constant__ CUtensorMap tmvt, const TreeParams p) {
+  using C = TCfg<FMT, D>;
+  using S = TreeSmem<C>;
+  constexpr int BN = C::BN, KSTAGES = C::KSTAGES, VSTAGES = C::VSTAGES, RAWS = C::RAWS;
+  constexpr bool Q8 = C::Q8;
+  extern __shared__ uint8_t smem_raw[];
+  S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const volatile int* abort = &sm.abort;
+  grid_launch_dependents();
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sm.item_full[i]), 128);
+      mbar_init(smem_u32(&sm.item_empty[i]), 2 * BM + 2);  // softmax threads, MMA warps
+      mbar_init(smem_u32(&sm.s_full[i]), 1);
+      mbar_init(smem_u32(&sm.s_free[i]), BM);
+      mbar_init(smem_u32(&sm.p_full[i]), BM);
+      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+      mbar_init(smem_u32(&sm.drain[i]), 1);
+      for (int r = 0; r < RAWS; ++r) {
+        mbar_init(smem_u32(&sm.raw_full[i][r]), 1);
+        mbar_init(smem_u32(&sm.raw_empty[i][r]), 4);
+      }
+    }
+    mbar_init(smem_u32(&sm.aux_sync), 128);
+    mbar_init(smem_u32(&sm.join_sync), 2 * BM);
+    for (int i = 0; i < C::QSLOTS; ++i) mbar_init(smem_u32(&sm.q_empty[i]), 2);
+    for (int i = 0; i < KSTAGES; ++i) {
+      mbar_init(smem_u32(&sm.k_full[i]), Q8 ? 4 : 1);
+      mbar_init(smem_u32(&sm.k_empty[i]), 2);  // both streams
+    }
+    for (int i = 0; i < VSTAGES; ++i) {
+      mbar_init(smem_u32(&sm.v_full[i]), Q8 ? 4 : 1);
+      mbar_init(smem_u32(&sm.v_empty[i]), 2);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == KLOAD_WARP && lane == 0) {
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmkt);
+  }
+  if (warp == VLOAD_WARP && lane == 0) {
+    prefetch_tmap(&tmv);
+    prefetch_tmap(&tmvt);
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
+    tmem_relinquish();
+  }
+
+  // ---- where this CTA's work begins, and how much it is
+  unsigned count = 0;
+  const int subs = p.HK * p.blocks;
+  if (p.whole) {
+    const int units = p.B * subs;  // (the caller keeps it below 2^24)
+    if (static_cast<int>(blockIdx.x) < units) count = (units - 1 - blockIdx.x) / gridDim.x + 1;
+  } else {
+    const int per = (p.B + NUM_THREADS - 1) / NUM_THREADS;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
+    unsigned sum = 0;
+    for (int b = b0; b < b1; ++b) sum += tree_seq<BN>(p, b).tiles;
+    sum *= subs;
+    unsigned run = sum;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const unsigned x = __shfl_up_sync(0xffffffffu, run, m);
+      if (lane >= m) run += x;
+    }
+    if (lane == 31) sm.warp_sum[warp] = run;
+    __syncthreads();
+    unsigned total = 0;
+#pragma unroll
+    for (int i = 0; i < NUM_THREADS / 32; ++i) {
+      const unsigned x = sm.warp_sum[i];
+      if (i < warp) run += x;
+      total += x;
+    }
+    const unsigned share = tree_share(total, gridDim.x);
+    // (share * CTAs stays below 2^32: total < 2^31)
+    const unsigned begin = share * blockIdx.x;
+    count = begin < total ? min(share, total - begin) : 0;
+    unsigned at = run - sum;
+    if (blockIdx.x == 0) {  // for the second kernel
+      unsigned a = at;
+      for (int b = b0; b < b1; ++b) {
+        p.first[b] = a;
+        a += tree_seq<BN>(p, b).tiles * subs;
+      }
+      if (threadIdx.x == 0) p.first[p.B] = total;
+    }
+    if (count > 0 && begin >= at && begin < run) {
+      for (int b = b0; b < b1; ++b) {
+        const unsigned t = tree_seq<BN>(p, b).tiles * subs;
+        if (begin - at < t) {
+          sm.start_b = b;
+          sm.start_off = begin - at;
+          break;
+        }
+        at += t;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  const int start_b = sm.start_b;
+  const unsigned start_off = sm.start_off;
+
+  bool ok = true;
+  auto fail = [&]() {
+    atomicCAS(p.status, kDevOk, kDevTimeout);
+    *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+  };
+
+  if (warp >= MMA_WARP) {
+    // ---------------------------------------------------------------- MMA issuers
+    // A stream runs through its own tiles in the order S(0), S(1), PV(0), S(2), ...;
+    // a ring slot is released by one arrival per stream: a commit by a stream that
+    // used the tile, a plain arrival by one that did not.
+    const int s = warp - MMA_WARP;
+    constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, false, false);
+    constexpr uint32_t IDESC_O = idesc_bf16_f32(BM, D, false, true);
+    constexpr uint32_t KV16 = C::KV_TILE >> 4;
+    const uint64_t dk = tree_sdesc(smem_u32(sm.k[0]), 16, 8 * C::RB, C::SWZ);
+    const uint64_t dv = tree_sdesc(smem_u32(sm.v[0]), C::KV_BLOCK, 8 * C::RB, C::SWZ);
+    auto qstep = [](int kk) {
+      return static_cast<uint32_t>((kk / C::KPB) * (C::Q_BLOCK >> 4) + (kk % C::KPB) * 2);
+    };
+    auto kstep = [](int kk) {
+      return static_cast<uint32_t>((kk / C::KPB) * (C::KV_BLOCK >> 4) + (kk % C::KPB) * 2);
+    };
+    const uint32_t t_s = tmem + C::col_s(s), t_o = tmem + C::col_o(s), t_p = tmem + C::col_p(s);
+    const bool leader = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
+      return ok;
+    };
+    auto k_wait = [&](uint32_t g) { return wait(&sm.k_full[g % KSTAGES], (g / KSTAGES) & 1); };
+    auto v_wait = [&](uint32_t g) { return wait(&sm.v_full[g % VSTAGES], (g / VSTAGES) & 1); };
+    uint32_t u = 0, npv = 0;  // products issued
+    bool pending = false;     // the last S'd tile still owes its PV product
+    uint32_t pg = 0;          // its ring index
+    bool pfirst = false;      // whether it is its item's first (of this stream)
+    TreeItem it = {};
+    int slot = 0;
+    // zeros in the rows of a value tile that nobody sees, whatever they hold
+    auto clear_rows = [&](uint32_t g, int tile) {
+      uint8_t* v = sm.v[g % VSTAGES];
+      auto clear = [&](int lo, int hi) {
+        for (int e = lo * C::CPB + lane; e < hi * C::CPB; e += 32)
+#pragma unroll
+          for (int nb = 0; nb < C::NB; ++nb)
+            *reinterpret_cast<uint4*>(v + nb * C::KV_BLOCK + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+      };
+      bool any = false;
+      if (tile < it.ctx) {
+        if (Q8) return;  // done where codes are widened
+        const int base = it.base0 + tile * BN;
+        const int lo = min(max(it.key0 - base, 0), BN), hi = min(max(it.L - base, 0), BN);
+        any = lo > 0 || hi < BN;
+        if (any) {
+          clear(0, lo);
+          clear(hi, BN);
+        }
+      } else {
+        const int base = (tile - it.ctx) * BN;
+        for (int r = 0; r < BN; r += 32) {
+          const int node = base + r + lane;
+          unsigned gone = __ballot_sync(0xffffffffu, node < p.n && sm.depth[slot][node] < 0);
+          any = any || gone != 0;
+          for (; gone != 0; gone &= gone - 1) {
+            const int row = r + __ffs(gone) - 1;
+            clear(row, row + 1);
+          }
+        }
+      }
+      if (any) {
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    };
+    int ptile = 0;
+    auto flush_pv = [&]() {
+      if (!pending) return;
+      if (!wait(&sm.p_full[s], npv & 1) || !v_wait(pg)) return;
+      clear_rows(pg, ptile);
+      tc_fence_after();
+      const uint64_t b = dv + (pg % VSTAGES) * KV16;
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(t_o, t_p + kk * 8, b + C::RB * kk, IDESC_O, (!pfirst || kk > 0) ? 1u : 0u);
+        tc_commit(smem_u32(&sm.pv_done[s]));
+        tc_commit(smem_u32(&sm.v_empty[pg % VSTAGES]));
+      }
+      __syncwarp();
+      ++npv;
+      pending = false;
+    };
+    uint32_t g0 = 0;
+    for (uint32_t items = 0; ok; ++items) {
+      if (!wait(&sm.item_full[items & 1], (items >> 1) & 1)) break;
+      it = sm.item[items & 1];
+      slot = items & 1;
+      if (it.more == 0) break;
+      const bool both = it.split == 0;
+      const uint64_t dq = tree_sdesc(smem_u32(sm.q[items % C::QSLOTS][both ? s : 0]), 16,
+                                     8 * C::RB, C::SWZ);
+      const int last = both ? it.n - 1 : (it.n - 1 - s) / 2 * 2 + s;  // (< 0: none)
+      bool first = true;
+      if (!both && it.n <= s && leader) mbar_arrive(smem_u32(&sm.q_empty[items % C::QSLOTS]));
+      for (int j = 0; j < it.n && ok; ++j) {
+        const uint32_t g = g0 + j;
+        if (!both && (j & 1) != s) {
+          // the other stream's tile
+          if (k_wait(g) && leader) mbar_arrive(smem_u32(&sm.k_empty[g % KSTAGES]));
+          if (v_wait(g) && leader) mbar_arrive(smem_u32(&sm.v_empty[g % VSTAGES]));
+          continue;
+        }
+        if (!k_wait(g)) break;
+        if (u > 0 && !wait(&sm.s_free[s], (u - 1) & 1)) break;
+        tc_fence_after();
+        const uint64_t b = dk + (g % KSTAGES) * KV16;
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(t_s, dq + qstep(kk), b + kstep(kk), IDESC_S, kk > 0 ? 1u : 0u);
+          tc_commit(smem_u32(&sm.s_full[s]));
+          tc_commit(smem_u32(&sm.k_empty[g % KSTAGES]));
+          if (j == last) tc_commit(smem_u32(&sm.q_empty[items % C::QSLOTS]));
+        }
+        __syncwarp();
+        ++u;
+        flush_pv();
+        pending = true;
+        pg = g;
+        ptile = it.t0 + j;
+        pfirst = first;
+        first = false;
+      }
+      // the item's last product before its tables go away
+      flush_pv();
+      g0 += it.n;
+      if (ok && leader) mbar_arrive(smem_u32(&sm.item_empty[slot]));
+      __syncwarp();
+    }
+    if (!ok && leader) fail();
+    // every product issued by this warp completes before tensor memory is freed
+    if (leader) tc_commit(smem_u32(&sm.drain[s]));
+    __syncwarp();
+    const int never = 0;
+    mbar_wait(smem_u32(&sm.drain[s]), 0, p.limit_ns, &never);
+  } else if (warp >= KLOAD_WARP) {
+    // ---------------------------------------------------------------- copies
+    if (lane == 0 && count > 0) {
+      const bool is_v = warp == VLOAD_WARP;
+      const uint32_t ST = Q8 ? RAWS : (is_v ? VSTAGES : KSTAGES);
+      uint64_t* full = Q8 ? sm.raw_full[is_v] : (is_v ? sm.v_full : sm.k_full);
+      uint64_t* empty = Q8 ? sm.raw_empty[is_v] : (is_v ? sm.v_empty : sm.k_empty);
+      uint8_t* ring = Q8 ? (is_v ? &sm.raw_v[0][0] : &sm.raw_k[0][0])
+                         : (is_v ? &sm.v[0][0] : &sm.k[0][0]);
+      const CUtensorMap* map = is_v ? &tmv : &tmk;
+      const CUtensorMap* tree_map = is_v ? &tmvt : &tmkt;
+      const bool runs = is_v ? p.run_v : p.run_k;
+      TreeCursor<BN> cur;
+      cur.begin(p, start_b, start_off, count);
+      TreeItem it;
+      uint32_t cnt = 0;
+      while (ok && cur.next(p, it)) {
+        const int stop = Q8 ? min(it.t0 + it.n, it.ctx) : it.t0 + it.n;
+        for (int t = it.t0; t < stop; ++t) {
+          const uint32_t at = cnt % ST;
+          ok = mbar_wait(smem_u32(&empty[at]), ((cnt / ST) & 1) ^ 1, p.limit_ns, abort);
+          if (!ok) break;
+          const uint32_t bar = smem_u32(&full[at]);
+          if constexpr (Q8) {
+            const uint32_t to = smem_u32(ring + at * C::RAW_TILE);
+            const int key = it.base0 + t * BN;
+            if (D < 128 && runs) {
+              const uint32_t bytes = min(BN, p.L_max - key) * D;
+              const RowStrides& st = is_v ? p.sv : p.sk;
+              mbar_arrive_expect_tx(bar, bytes);
+              bulk_copy_in(to, (is_v ? p.v : p.k) + it.b * st.b + it.hk * st.h +
+                                   static_cast<long long>(key) * D, bytes, bar);
+            } else {
+              mbar_arrive_expect_tx(bar, C::RAW_TILE);
+              tma_load_4d(to, map, bar, 0, key, it.hk, it.b);
+            }
+          } else {
+            const uint32_t to = smem_u32(ring + at * C::KV_TILE);
+            const bool tree = t >= it.ctx;
+            mbar_arrive_expect_tx(bar, C::KV_TILE);
+#pragma unroll
+            for (int nb = 0; nb < C::NB; ++nb)
+              tma_load_4d(to + nb * C::KV_BLOCK, tree ? tree_map : map, bar, 64 * nb,
+                          tree ? (t - it.ctx) * BN : it.base0 + t * BN, it.hk, it.b);
+          }
+          ++cnt;
+        }
+      }
+      if (!ok) {
+        fail();
+        const int never = 0;  // the copies under way land before shared memory goes away
+        for (uint32_t i = 0; i < ST; ++i) {
+          const uint32_t uses = cnt / ST + (i < cnt % ST ? 1u : 0u);
+          if (uses > 0) mbar_wait(smem_u32(&full[i]), (uses - 1) & 1, p.limit_ns, &never);
+        }
+      }
+    }
+  } else if (warp >= AUX_WARP) {
+    // ---------------------------------------------------------------- rows, trees, codes
+    const int tid = threadIdx.x - AUX_WARP * 32;
+    TreeCursor<BN> cur;
+    cur.begin(p, start_b, start_off, count);
+    int has[2] = {-1, -1};  // whose tree a slot's tables hold
+    uint32_t cnt = 0, raws = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = mbar_wait(smem_u32(bar), parity, p.limit_ns, abort);
+      return ok;
+    };
+    uint32_t syncs = 0;
+    auto sync = [&]() {
+      mbar_arrive(smem_u32(&sm.aux_sync));
+      return wait(&sm.aux_sync, syncs++ & 1);
+    };
+    uint32_t copied[2] = {}, filled[2] = {};  // ring slots last filled by a copy; tiles so far
+    for (uint32_t items = 0;; ++items) {
+      const int slot = items & 1;
+      if (!wait(&sm.item_empty[slot], ((items >> 1) & 1) ^ 1)) break;
+      TreeItem it;
+      const bool more = cur.next(p, it);
+      if (more && !it.whole) it.slot = items == 0 ? 0 : 1;
+      if (tid == 0) sm.item[slot] = it;
+      if (!more) {
+        mbar_arrive(smem_u32(&sm.item_full[slot]));
+        break;
+      }
+      if (has[slot] != it.b) {
+        has[slot] = it.b;
+        // ancestors by pointer doubling: after round k a node knows 2^k of them
+        int up = -2;
+        if (tid < p.n) {
+          up = __ldg(p.parents + static_cast<long long>(it.b) * p.n + tid);
+          if (up < -1 || up >= tid) up = -2;
+        }
+        const int parent = up;
+        uint32_t line[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) line[w] = tid >> 5 == w ? 1u << (tid & 31) : 0u;
+        for (int r = 0; r < p.rounds && ok; ++r) {
+          sm.up[0][tid] = up;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) sm.line[slot][tid][w] = line[w];
+          if (!sync()) break;
+          if (up >= 0) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) line[w] |= sm.line[slot][up][w];
+            up = sm.up[0][up];
+          }
+          sync();
+        }
+        const bool node = up == -1;
+        const int depth =
+            __popc(line[0]) + __popc(line[1]) + __popc(line[2]) + __popc(line[3]) - 1;
+        sm.up[1][tid] = parent;
+        if (!sync()) break;
+        if (node && p.window >= 0 && p.window < depth) {
+          // only the nearest ancestors
+#pragma unroll
+          for (int w = 0; w < 4; ++w) line[w] = 0u;
+          int a = tid;
+          for (int k = 0; k <= p.window; ++k) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              if (a >> 5 == w) line[w] |= 1u << (a & 31);
+            a = sm.up[1][a];
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sm.line[slot][tid][w] = node ? line[w] : 0u;
+        sm.depth[slot][tid] = node ? depth : -1;
+      }
+      // the query rows, each `split` times
+      const int qslot = items % C::QSLOTS;
+      if (!wait(&sm.q_empty[qslot], ((items / C::QSLOTS) & 1) ^ 1)) break;
+      constexpr int CPR = D / 8;  // 16-byte chunks of a row
+      const int tiles = it.split == 0 ? 2 : 1;
+      const int lanes = it.split == 0 ? BM : BM / it.split;
+      for (int s = 0; s < tiles; ++s) {
+#pragma unroll 8
+        for (int e = tid; e < BM * CPR; e += 128) {
+          const int at = e / CPR, c = e % CPR;
+          const int r = s * BM + at % lanes;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (r < it.rows) {
+            const int row = it.row0 + r, g = row / p.n, i = row - g * p.n;
+            x = __ldg(reinterpret_cast<const uint4*>(p.q + it.b * p.sq.b +
+                                                     (it.hk * p.G + g) * p.sq.h + i * p.sq.n) +
+                      c);
+          }
+          *reinterpret_cast<uint4*>(sm.q[qslot][s] + (c / C::CPB) * C::Q_BLOCK + at * C::RB +
+                                    (((c % C::CPB) ^ C::swz(at)) << 4)) = x;
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&sm.item_full[slot]));
+      if constexpr (Q8) {
+        for (int t = it.t0; t < it.t0 + it.n && ok; ++t, ++cnt) {
+          const uint32_t from = raws % RAWS, rph = (raws / RAWS) & 1;
+          const int key = it.base0 + t * BN;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const uint32_t stages = kv ? VSTAGES : KSTAGES, at = cnt % stages;
+            const uint32_t ph = ((cnt / stages) & 1) ^ 1;
+            uint64_t* full = kv ? sm.v_full : sm.k_full;
+            uint8_t* to = kv ? sm.v[at] : sm.k[at];
+            if (!wait(kv ? &sm.v_empty[at] : &sm.k_empty[at], ph)) break;
+            copied[kv] &= ~(1u << at);
+            ++filled[kv];
+            if (t < it.ctx) {
+              if (!wait(&sm.raw_full[kv][from], rph)) break;
+              widen_tile<C>(kv ? sm.raw_v[from] : sm.raw_k[from], to, tid,
+                            kv ? it.key0 - key : 0, kv ? it.L - key : BN);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(smem_u32(&sm.raw_empty[kv][from]));
+                mbar_arrive(smem_u32(&full[at]));
+              }
+            } else if (lane == 0) {
+              // the tree's own keys are bf16 already
+              if (tid == 0) {
+                const uint32_t bar = smem_u32(&full[at]);
+                mbar_arrive_expect_tx(bar, C::KV_TILE);
+#pragma unroll
+                for (int nb = 0; nb < C::NB; ++nb)
+                  tma_load_4d(smem_u32(to) + nb * C::KV_BLOCK, kv ? &tmvt : &tmkt, bar, 64 * nb,
+                              (t - it.ctx) * BN, it.hk, it.b);
+                copied[kv] |= 1u << at;
+              } else {
+                mbar_arrive(smem_u32(&full[at]));
+              }
+            }
+            __syncwarp();
+          }
+          if (t < it.ctx) ++raws;
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok && lane == 0) {
+      fail();
+      if (Q8 && tid == 0) {
+        const int never = 0;  // the copies under way land before shared memory goes away
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t stages = kv ? VSTAGES : KSTAGES;
+          for (uint32_t i = 0; i < stages; ++i) {
+            const uint32_t uses = filled[kv] / stages + (i < filled[kv] % stages ? 1u : 0u);
+            if ((copied[kv] >> i) & 1u)
+              mbar_wait(smem_u32(kv ? &sm.v_full[i] : &sm.k_full[i]), (uses - 1) & 1, p.limit_ns,
+                        &never);
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int s = warp >> 2, quarter = warp & 3;
+    const int at = quarter * 32 + lane;  // tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_off + C::col_s(s);
+    const uint32_t tO = tmem + lane_off + C::col_o(s);
+    const uint32_t tP = tmem + lane_off + C::col_p(s);
+    constexpr int OC = C::OW / 32;
+    uint32_t u = 0;  // tiles of this stream
+    int was_split = -1;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
+      return ok;
+    };
+    uint32_t joins = 0;
+    auto join = [&]() {
+      mbar_arrive(smem_u32(&sm.join_sync));
+      return wait(&sm.join_sync, joins++ & 1);
+    };
+    for (uint32_t items = 0; ok; ++items) {
+      const int slot = items & 1;
+      if (!wait(&sm.item_full[slot], (items >> 1) & 1)) break;
+      const TreeItem it = sm.item[slot];
+      if (it.more == 0) break;
+      const bool both = it.split == 0;
+      const int split = both ? 1 : it.split;
+      const int lanes = BM / split, cols = BN / split;
+      const int copy = at / lanes;
+      const int r = both ? s * BM + at : at - copy * lanes;
+      const bool valid = r < it.rows;
+      const bool active = __any_sync(0xffffffffu, valid);
+      const int row = it.row0 + (valid ? r : 0);
+      const int head = it.hk * p.G + row / p.n, node = row % p.n;
+      const int depth = sm.depth[slot][node];
+      const bool alive = valid && depth >= 0;
+      const float slope2 = p.slopes ? kLog2e * __ldg(p.slopes + head) : 0.f;
+      const int col0 = copy * cols;
+      const bool changed = p.capped || p.slopes != nullptr;
+      if (split != was_split) {
+        // columns that another copy of a row takes stay zero
+        was_split = split;
+        if (split > 1) {
+          uint32_t z[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) z[i] = 0u;
+          for (int c = 0; c < BN / 2; c += 16) tmem_st16(tP + c, z);
+          tmem_st_wait();
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+      const int step = both ? 1 : 2, j0 = both ? 0 : s;
+      bool first = true;
+      for (int j = j0; j < it.n; j += step, ++u) {
+        const int t = it.t0 + j;
+        const bool tree = t >= it.ctx;
+        const int base = tree ? (t - it.ctx) * BN : it.base0 + t * BN;
+        float sc = 1.f;  // lane i: the scale of the tile's i-th block of keys, 8 + i: of values
+        if constexpr (Q8) {
+          if (!tree) {
+            const int blk = (base >> p.T_log2) + (lane & 7);
+            sc = 0.f;
+            if (lane < 16 && (blk << p.T_log2) < min(it.L, base + BN) &&
+                ((blk + 1) << p.T_log2) > it.key0)
+              sc = __ldg((lane < 8 ? p.k_scale : p.v_scale) +
+                         (static_cast<long long>(it.b) * p.HK + it.hk) * p.num_blocks + blk);
+          }
+        }
+        if (!wait(&sm.s_full[s], u & 1)) break;
+        tc_fence_after();
+        bool rescale_o = false;
+        float alpha = 1.f;
+        if (active) {
+          // this row's keys of the tile: columns [lo, hi), or bits
+          const int hi = it.L - base;
+          const int lo = p.window >= 0 ? it.L + max(depth, 0) - p.window - base : 0;
+          const bool edge =
+              tree || hi < BN || (p.window >= 0 && __any_sync(0xffffffffu, lo > 0));
+          const float off = p.slopes ? (tree ? -slope2 * max(depth, 0)
+                                             : -slope2 * static_cast<float>(it.L + max(depth, 0) - base))
+                                     : 0.f;
+          // the finished scores of 32 columns from `c` on, less `off`, in log2 units
+          auto scores = [&](uint32_t(&x)[32], int c) {
+            float k0 = 1.f, k1 = 1.f;
+            if constexpr (Q8) {
+              if (!tree) {
+                k0 = __shfl_sync(0xffffffffu, sc, c >> p.T_log2);
+                k1 = __shfl_sync(0xffffffffu, sc, (c + 16) >> p.T_log2);
+              }
+            }
+            if (!changed) {
+              k0 *= p.scale_log2;
+              k1 *= p.scale_log2;
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float k = i < 16 ? k0 : k1;
+                float a, b;
+                fma2(a, b, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), k, k, 0.f, 0.f);
+                x[i] = __float_as_uint(a);
+                x[i + 1] = __float_as_uint(b);
+              }
+            } else {
+              if (p.capped) {
+                float big = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  if constexpr (Q8)
+                    x[i] = __float_as_uint(__uint_as_float(x[i]) * (i < 16 ? k0 : k1));
+                  big = fmaxf(big, fabsf(__uint_as_float(x[i])));
+                }
+                const bool small = __all_sync(0xffffffffu, big <= p.cap.small);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float y = __uint_as_float(x[i]), z = y * y;
+                  const float near =
+                      y * fmaf(z, fmaf(z, p.cap.poly[2], p.cap.poly[1]), p.cap.poly[0]);
+                  float w = near;
+                  if (!small) {
+                    w = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(y * p.cap_in)), p.cap_log2);
+                    if (p.wide && fabsf(y) <= p.cap.small) w = near;
+                  }
+                  x[i] = __float_as_uint(w);
+                }
+              } else {
+                k0 *= p.scale_log2;
+                k1 *= p.scale_log2;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  x[i] = __float_as_uint(__uint_as_float(x[i]) * (i < 16 ? k0 : k1));
+              }
+              if (p.slopes) {
+                if (tree) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const int a = min(base + c + i, kMostNodes - 1);
+                    x[i] = __float_as_uint(fmaf(slope2, static_cast<float>(sm.depth[slot][a]),
+                                                __uint_as_float(x[i])));
+                  }
+                } else {
+                  const float c0 = static_cast<float>(c);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    x[i] = __float_as_uint(fmaf(slope2, c0 + i, __uint_as_float(x[i])));
+                }
+              }
+            }
+            if (edge) {
+              const uint32_t see = tree ? sm.line[slot][node][(base + c) >> 5]
+                                        : below(hi - c) & ~below(lo - c);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(see & (1u << i))) x[i] = __float_as_uint(-INFINITY);
+            }
+          };
+          float mt = -INFINITY;
+#pragma unroll 1
+          for (int c = col0; c < col0 + cols; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(tS + c, x);
+            tmem_ld_wait(x);
+            scores(x, c);
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                m4[e] = max3(m4[e], __uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1]));
+            mt = fmaxf(mt, fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]));
+          }
+          mt += off;
+          if (mt > m + kRescale) {
+            alpha = ex2(m - mt);  // 0 when m = -inf
+            l *= alpha;
+            rescale_o = !first;
+            m = mt;
+          }
+          // P overwrites the last tile's, and O is rescaled, once that product is done
+          if (u > 0) {
+            if (!wait(&sm.pv_done[s], (u - 1) & 1)) break;
+            tc_fence_after();
+          }
+          if (__any_sync(0xffffffffu, rescale_o)) {
+            const float a = rescale_o ? alpha : 1.f;
+#pragma unroll
+            for (int h2 = 0; h2 < OC; ++h2) {
+              uint32_t oc[32];
+              tmem_ld32(tO + h2 * 32, oc);
+              tmem_ld_wait(oc);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) oc[i] = __float_as_uint(__uint_as_float(oc[i]) * a);
+              tmem_st32(tO + h2 * 32, oc);
+            }
+          }
+          const float neg_m = m == -INFINITY ? 0.f : off - m;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll 1
+          for (int c = col0; c < col0 + cols; c += 32) {
+            uint32_t x[32], pk[16];
+            tmem_ld32(tS + c, x);
+            tmem_ld_wait(x);
+            scores(x, c);
+            float v0 = 1.f, v1 = 1.f;
+            if constexpr (Q8) {
+              if (!tree) {
+                v0 = __shfl_sync(0xffffffffu, sc, 8 + (c >> p.T_log2));
+                v1 = __shfl_sync(0xffffffffu, sc, 8 + ((c + 16) >> p.T_log2));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float a, b;
+              add2(a, b, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), neg_m, neg_m);
+              a = ex2(a);
+              b = ex2(b);
+              add2(l0, l1, l0, l1, a, b);
+              if constexpr (Q8) {
+                const float v = i < 16 ? v0 : v1;
+                fma2(a, b, a, b, v, v, 0.f, 0.f);
+              }
+              pk[i >> 1] = pack_bf16x2(a, b);
+            }
+            tmem_st16(tP + c / 2, pk);
+          }
+          l += l0 + l1;
+          tmem_st_wait();
+        } else if (u > 0) {
+          if (!wait(&sm.pv_done[s], (u - 1) & 1)) break;
+        }
+        first = false;
+        tc_fence_before();
+        mbar_arrive(smem_u32(&sm.s_free[s]));
+        mbar_arrive(smem_u32(&sm.p_full[s]));
+      }
+      if (!ok) break;
+
+      // ---------------------------------------------------------- the run's result
+      if (!first) {
+        if (!wait(&sm.pv_done[s], (u - 1) & 1)) break;
+        tc_fence_after();
+      }
+      if (!alive) {
+        m = -INFINITY;
+        l = 0.f;
+      }
+      float* part = it.whole ? nullptr
+                             : p.part + (static_cast<size_t>(blockIdx.x) * 2 + it.slot) *
+                                            p.block_rows * (D + kPartTail);
+      float weight = alive ? 1.f : 0.f, most = m, sum = l;
+      if (!both) {
+        // the parts of a row: two streams, `split` copies each
+        sm.stat[threadIdx.x] = make_float2(m, l);
+        if (!join()) break;
+        most = -INFINITY;
+        for (int e = 0; e < 2 * split; ++e)
+          most = fmaxf(most, sm.stat[e / split * BM + e % split * lanes + r].x);
+        sum = 0.f;
+        for (int e = 0; e < 2 * split; ++e) {
+          const float2 x = sm.stat[e / split * BM + e % split * lanes + r];
+          if (x.y > 0.f) sum += x.y * ex2(x.x - most);
+        }
+        weight = l > 0.f ? ex2(m - most) : 0.f;
+      }
+      if (it.whole) weight = sum > 0.f ? weight / sum : 0.f;
+      if (valid && (both || (s == 0 && copy == 0))) {
+        if (!it.whole) {
+          float* tail = part + static_cast<size_t>(r) * (D + kPartTail) + D;
+          tail[0] = most;
+          tail[1] = sum;
+        } else if (p.lse != nullptr) {
+          p.lse[(static_cast<size_t>(it.b) * p.H + head) * p.n + node] =
+              sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
+        }
+      }
+#pragma unroll 1
+      for (int h2 = 0; h2 < OC; ++h2) {
+        uint32_t oc[32];
+        if (!first) {
+          tmem_ld32(tO + 32 * h2, oc);
+          tmem_ld_wait(oc);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          oc[i] = weight > 0.f && !first ? __float_as_uint(__uint_as_float(oc[i]) * weight) : 0u;
+#pragma unroll
+        for (int half = 0; half < (D < 32 ? 1 : 2); ++half) {
+          const int c = h2 * 32 + half * 16;
+          if (both) {
+            if (!valid) {
+            } else if (it.whole) {
+              uint4* to = reinterpret_cast<uint4*>(p.o + it.b * p.so.b + head * p.so.h +
+                                                   node * p.so.n + c);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t* x = oc + half * 16 + e * 8;
+                to[e] = make_uint4(
+                    pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
+                    pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
+                    pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
+                    pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
+              }
+            } else {
+              uint4* to = reinterpret_cast<uint4*>(part + static_cast<size_t>(r) * (D + kPartTail) + c);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t* x = oc + half * 16 + e * 4;
+                to[e] = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+            }
+            continue;
+          }
+          uint4* mine = reinterpret_cast<uint4*>(sm.merge[threadIdx.x]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t* x = oc + half * 16 + e * 4;
+            mine[e] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+          if (!join()) break;
+          for (int e = threadIdx.x; e < it.rows * 4; e += 2 * BM) {
+            const int rr = e >> 2, c4 = (e & 3) * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < 2 * split; ++w) {
+              const float4 x = *reinterpret_cast<const float4*>(
+                  &sm.merge[w / split * BM + w % split * lanes + rr][c4]);
+              y.x += x.x;
+              y.y += x.y;
+              y.z += x.z;
+              y.w += x.w;
+            }
+            if (it.whole) {
+              const int rw = it.row0 + rr, g = rw / p.n;
+              *reinterpret_cast<uint2*>(p.o + it.b * p.so.b + (it.hk * p.G + g) * p.so.h +
+                                        (rw - g * p.n) * p.so.n + c + c4) =
+                  make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+            } else {
+              *reinterpret_cast<float4*>(part + static_cast<size_t>(rr) * (D + kPartTail) + c +
+                                         c4) = y;
+            }
+          }
+          if (!join()) break;
+        }
+        if (!ok) break;
+      }
+      if (!ok) break;
+      tc_fence_before();
+      mbar_arrive(smem_u32(&sm.item_empty[slot]));
+    }
+    if (!ok) fail();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the parts of the units that several CTAs shared: a warp per query row.
+template <int D>
+__global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p, int ctas) {
+  grid_dependency_wait();
+  const long long at = blockIdx.x * 8LL + (threadIdx.x >> 5);
+  if (at >= static_cast<long long>(p.B) * p.HK * p.rows) return;
+  const int lane = threadIdx.x & 31;
+  const int row = at % p.rows;
+  const int hk = at / p.rows % p.HK, b = at / p.rows / p.HK;
+  const int subs = p.HK * p.blocks;
+  const unsigned f0 = p.first[b], f1 = p.first[b + 1];
+  const unsigned tiles = (f1 - f0) / subs;
+  const unsigned begin = f0 + (hk * p.blocks + row / kBlockRows) * tiles;
+  const unsigned share = tree_share(p.first[p.B], ctas);
+  const unsigned c0 = begin / share, c1 = (begin + tiles - 1) / share;
+  if (c0 == c1) return;
+  auto part = [&](unsigned c) {
+    const int slot = share * c >= begin ? 0 : 1;
+    return p.part + ((static_cast<size_t>(c) * 2 + slot) * p.block_rows + row % kBlockRows) *
+                        (D + kPartTail);
+  };
+  float most = -INFINITY;
+  for (unsigned c = c0 + lane; c <= c1; c += 32) most = fmaxf(most, part(c)[D]);
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
+  constexpr int E = D < 32 ? 1 : D / 32;
+  float y[E] = {}, sum = 0.f;
+#pragma unroll 4
+  for (unsigned c = c0; c <= c1; ++c) {
+    const float* x = part(c);
+    const float w = x[D + 1] > 0.f ? ex2(x[D] - most) : 0.f;
+    sum = fmaf(w, x[D + 1], sum);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (lane * E + e < D) y[e] = fmaf(w, x[lane * E + e], y[e]);
+  }
+  const int g = row / p.n, node = row - g * p.n;
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  __nv_bfloat16* out = p.o + b * p.so.b + (hk * p.G + g) * p.so.h + node * p.so.n;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (lane * E + e < D) out[lane * E + e] = __float2bfloat16_rn(y[e] * inv);
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[(static_cast<size_t>(b) * p.H + hk * p.G + g) * p.n + node] =
+        sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
+}
+
+template <int FMT, int D>
+cudaError_t launch_tree_d(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
+                          const LaunchCtx& ctx) {
+  using C = TCfg<FMT, D>;
+  static_assert(sizeof(TreeSmem<C>) + 1024 <= 232448, "dynamic shared memory per CTA");
+  const size_t smem = sizeof(TreeSmem<C>) + 1024;
+  cudaError_t err = cudaFuncSetAttribute(attn_tree_kernel<FMT, D>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem));
+  if (err != cudaSuccess) return err;
+  attn_tree_kernel<FMT, D><<<plan.ctas, NUM_THREADS, smem, ctx.stream>>>(maps[0], maps[1], maps[2],
+                                                                        maps[3], p);
+  if ((err = cudaGetLastError()) != cudaSuccess || plan.whole) return err;
+  const long long rows = static_cast<long long>(p.B) * p.HK * p.rows;
+  return launch_dependent(attn_tree_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)),
+                          dim3(256), 0, ctx.stream, p, plan.ctas);
+}
+
+template <int FMT>
+cudaError_t launch_tree_fmt(const TreeDecodeProblem& pb, const CUtensorMap* maps,
+                            const TreePlan& plan, void* workspace, const LaunchCtx& ctx) {
+  TreeParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(pb.q);
+  p.parents = pb.parents;
+  p.k_scale = pb.k_scale;
+  p.v_scale = pb.v_scale;
+  p.o = static_cast<__nv_bfloat16*>(pb.o);
+  p.lse = pb.lse;
+  p.first = static_cast<unsigned*>(workspace);
+  p.part = static_cast<float*>(workspace) + plan.part_off;
+  p.cache_lens = pb.cache_lens;
+  p.slopes = pb.slopes;
+  p.sq = pb.sq;
+  p.so = pb.so;
+  p.k = static_cast<const uint8_t*>(pb.k_cache);
+  p.v = static_cast<const uint8_t*>(pb.v_cache);
+  p.sk = pb.sk;
+  p.sv = pb.sv;
+  p.run_k = pb.sk.n == pb.d;
+  p.run_v = pb.sv.n == pb.d;
+  p.whole = plan.whole;
+  p.limit_ns = ctx.limit_ns;
+  p.status = ctx.status;
+  p.B = pb.B;
+  p.H = pb.H;
+  p.HK = pb.HK;
+  p.G = pb.H / pb.HK;
+  p.n = pb.n;
+  p.L_max = pb.L_max;
+  while ((1 << p.T_log2) < pb.block_tokens) ++p.T_log2;
+  p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
+  p.window = pb.window;
+  p.rows = p.G * pb.n;
+  p.blocks = plan.blocks;
+  p.block_rows = plan.block_rows;
+  p.tree_tiles = plan.tree_tiles;
+  while ((1 << p.rounds) < pb.n) ++p.rounds;
+  p.scale_log2 = pb.scale * kLog2e;
+  p.capped = pb.softcap > 0.f;
+  p.cap_log2 = pb.softcap * kLog2e;
+  p.cap_in = p.capped ? 2.f * p.scale_log2 / pb.softcap : 0.f;
+  p.cap = cap_poly(pb.scale, pb.softcap);
+  p.wide = pb.softcap > kWideCap;
+  switch (pb.d) {
+    case 16: return launch_tree_d<FMT, 16>(p, maps, plan, ctx);
+    case 32: return launch_tree_d<FMT, 32>(p, maps, plan, ctx);
+    case 64: return launch_tree_d<FMT, 64>(p, maps, plan, ctx);
+    case 128: return launch_tree_d<FMT, 128>(p, maps, plan, ctx);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+}  // namespace attn
