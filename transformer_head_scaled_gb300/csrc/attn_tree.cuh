@@ -24,11 +24,12 @@
 // Inside a CTA two streams (a softmax warpgroup and an MMA warp each) overlap
 // one's exponentials with the other's products.  With more than 128 rows a stream
 // takes one tile of rows and both see every key tile; with at most 128 they take
-// every second key tile with the same rows.  With at most 64 (32) rows the tile
-// of 128 holds them two (four) times, and each copy takes a half (a quarter) of a
-// tile's keys: its probabilities of the others stay zero.  Exponentials cost a
-// warp the same for one row as for 32, and only so do all four warps of a
-// stream share them.  The parts of a row are joined at its end.
+// every second 64 keys with the same rows.  With at most 64 rows the tile of 128
+// holds them twice, and each copy takes 32 of the 64 keys: its probabilities of
+// the others are zero.  Exponentials cost a warp the same for one row as for 32,
+// and so its four warps share them.  The parts of a row are joined at its end.
+// Scores go to one of two buffers of a stream in tensor memory, so that those of
+// the next 64 keys are there when a softmax is done; P takes its scores' place.
 //
 // Warps 0-3, 4-7: softmax of stream 0 and 1; 8-11: the query rows, the nodes'
 // ancestors, and for 8-bit caches the widening of codes to bf16 (exact, both
@@ -38,6 +39,8 @@
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "attn_internal.cuh"
 #include "ptx.cuh"
@@ -57,6 +60,7 @@ constexpr int VLOAD_WARP = 13;
 constexpr int MMA_WARP = 14;   // and 15
 constexpr int NUM_THREADS = 512;
 constexpr uint32_t TMEM_COLS = 512;
+constexpr int SN = 64;  // keys of one score product
 constexpr float kRescale = 8.0f;  // a running maximum is kept until a score exceeds it by 2^8
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -80,16 +84,13 @@ struct TCfg {
   static constexpr int VSTAGES = D_ >= 64 && Q8 ? 3 : KSTAGES;
   static constexpr int RAWS = Q8 ? (D_ >= 64 ? 3 : 6) : 1;  // of tiles of codes
   static constexpr uint32_t OW = D_ < 32 ? 32 : D_;
-  static constexpr int MOST_SPLIT = BN / 32;  // copies of a row in a tile
-  __host__ __device__ static constexpr uint32_t col_s(int s) { return BN * s; }
-  __host__ __device__ static constexpr uint32_t col_o(int s) { return 2 * BN + OW * s; }
-  __host__ __device__ static constexpr uint32_t col_p(int s) {
-    return 2 * BN + 2 * OW + (BN / 2) * s;
-  }
+  static constexpr int NSUB = BN / SN;
+  __host__ __device__ static constexpr uint32_t col_s(int s, int b) { return SN * (2 * s + b); }
+  __host__ __device__ static constexpr uint32_t col_o(int s) { return 4 * SN + OW * s; }
   __host__ __device__ static constexpr uint32_t swz(uint32_t r) {
     return ((r * RB) >> 7) & (RB / 16 - 1);
   }
-  static_assert(col_p(2) <= TMEM_COLS, "tensor memory");
+  static_assert(col_o(2) <= TMEM_COLS, "tensor memory");
 };
 
 // A run of a unit's tiles.
@@ -97,7 +98,7 @@ struct TreeItem {
   int more;        // 0: the CTA's work has ended
   int b, hk;
   int row0, rows;  // of the key head's query rows
-  int split;       // copies of each row in a tile; 0: two tiles of rows
+  int split;       // copies of each row in a tile (1 or 2); 0: two tiles of rows
   int L, key0;     // cached tokens, and the first one that any node sees
   int base0, ctx;  // key of the unit's first cache tile, and how many there are
   int t0, n;       // this run of its tiles
@@ -137,7 +138,7 @@ struct __align__(1024) TreeSmem {
   uint8_t v[C::VSTAGES][C::KV_TILE];
   uint8_t raw_k[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
   uint8_t raw_v[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
-  float merge[2 * BM][kMergeStride];
+  float merge[3 * BM / 2][kMergeStride];  // the parts of rows but the first
   float2 stat[2 * BM];
   uint32_t line[2][kMostNodes][4];  // what a node sees of the tree
   int depth[2][kMostNodes];         // -1: no node
@@ -146,7 +147,8 @@ struct __align__(1024) TreeSmem {
   uint64_t item_full[2], item_empty[2], q_empty[C::QSLOTS];
   uint64_t k_full[C::KSTAGES], k_empty[C::KSTAGES], v_full[C::VSTAGES], v_empty[C::VSTAGES];
   uint64_t raw_full[2][C::RAWS], raw_empty[2][C::RAWS];  // keys, values
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], drain[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // stream, buffer
+  uint64_t drain[2];
   uint64_t aux_sync, join_sync;  // barriers of the auxiliary and of the softmax threads
   unsigned warp_sum[NUM_THREADS / 32];
   unsigned total;
@@ -171,6 +173,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.ctx = s.key0 < s.L ? (s.L - s.base0 + BN - 1) / BN : 0;
   s.tiles = s.ctx + p.tree_tiles;
   return s;
+}
+
+// How many of a tile's parts of SN keys hold any (the unit's tile `t`).
+template <class C>
+__device__ __forceinline__ int parts_of(const TreeItem& it, int t, int n) {
+  if (C::NSUB == 1) return 1;
+  const int keys = t < it.ctx ? it.L - (it.base0 + t * C::BN) : n - (t - it.ctx) * C::BN;
+  return keys > SN ? 2 : 1;
 }
 
 constexpr int kMinTreeTiles = 2;  // of a CTA's run
@@ -214,7 +224,7 @@ struct TreeCursor {
     it.hk = sub / p.blocks;
     it.row0 = rb * kBlockRows;
     it.rows = min(p.rows - it.row0, kBlockRows);
-    it.split = it.rows > BM ? 0 : (it.rows > BM / 2 ? 1 : (it.rows > BM / 4 ? 2 : BN / 32));
+    it.split = it.rows > BM ? 0 : (it.rows > BM / 2 ? 1 : 2);
     it.L = s.L;
     it.key0 = s.key0;
     it.base0 = s.base0;
@@ -269,15 +279,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Two of a word's four codes (bytes 2 * HI and 2 * HI + 1) as a bf16 pair, exactly.
 template <int FMT, int HI>
 __device__ __forceinline__ uint32_t widen2(uint32_t w) {
   uint32_t t, y;
   if (FMT == kCacheE4M3) {
     // sign, four exponent and three mantissa bits to their places in a bf16, whose
-    // exponent is then 120 too small (the smallest codes are subnormal numbers in both)
-    t = __byte_perm(w, 0u, HI ? 0x3424 : 0x1404);
-    y = (t & 0x80008000u) | ((t >> 4) & 0x07f007f0u);
+    // exponent is then 120 too small (the smallest codes are subnormal numbers in both);
+    // bytes are spread with their sign in the byte above
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(t) : "r"(w), "n"(HI ? 0xb3a2 : 0x9180));
+    y = (t << 4) & 0x87f087f0u;
     const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7b80));  // 2^120
     const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&y), up);
     return *reinterpret_cast<const uint32_t*>(&x);
@@ -296,15 +319,21 @@ template <class C>
 __device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int tid, int lo,
                                            int hi) {
   constexpr int CPR = C::D / 16;  // 16-code chunks of a row
-#pragma unroll 2
-  for (int i = tid; i < C::BN * CPR; i += 128) {
-    const int row = i / CPR, c = i % CPR;
+  constexpr int N = C::BN * CPR / 128;
+  uint4 w[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int i = tid + e * 128, row = i / CPR, c = i % CPR;
     const int at = C::D == 128 ? c ^ (row & 7) : c;
-    const uint4 w = *reinterpret_cast<const uint4*>(raw + row * C::D + at * 16);
-    uint4 a = make_uint4(widen2<C::FMT, 0>(w.x), widen2<C::FMT, 1>(w.x), widen2<C::FMT, 0>(w.y),
-                         widen2<C::FMT, 1>(w.y));
-    uint4 b = make_uint4(widen2<C::FMT, 0>(w.z), widen2<C::FMT, 1>(w.z), widen2<C::FMT, 0>(w.w),
-                         widen2<C::FMT, 1>(w.w));
+    w[e] = *reinterpret_cast<const uint4*>(raw + row * C::D + at * 16);
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int i = tid + e * 128, row = i / CPR, c = i % CPR;
+    uint4 a = make_uint4(widen2<C::FMT, 0>(w[e].x), widen2<C::FMT, 1>(w[e].x),
+                         widen2<C::FMT, 0>(w[e].y), widen2<C::FMT, 1>(w[e].y));
+    uint4 b = make_uint4(widen2<C::FMT, 0>(w[e].z), widen2<C::FMT, 1>(w[e].z),
+                         widen2<C::FMT, 0>(w[e].w), widen2<C::FMT, 1>(w[e].w));
     if (row < lo || row >= hi) a = b = make_uint4(0u, 0u, 0u, 0u);
     uint8_t* to = out + (2 * c / C::CPB) * C::KV_BLOCK + row * C::RB;
     const int c0 = 2 * c % C::CPB, x = C::swz(row);
@@ -315,7 +344,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int
   }
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool CHANGED>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
@@ -336,10 +365,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.item_full[i]), 128);
       mbar_init(smem_u32(&sm.item_empty[i]), 2 * BM + 2);  // softmax threads, MMA warps
-      mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.s_free[i]), BM);
-      mbar_init(smem_u32(&sm.p_full[i]), BM);
-      mbar_init(smem_u32(&sm.pv_done[i]), 1);
+      for (int e = 0; e < 2; ++e) {
+        mbar_init(smem_u32(&sm.s_full[i][e]), 1);
+        mbar_init(smem_u32(&sm.p_full[i][e]), BM);
+        mbar_init(smem_u32(&sm.pv_done[i][e]), 1);
+      }
       mbar_init(smem_u32(&sm.drain[i]), 1);
       for (int r = 0; r < RAWS; ++r) {
         mbar_init(smem_u32(&sm.raw_full[i][r]), 1);
@@ -440,13 +470,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp >= MMA_WARP) {
     // ---------------------------------------------------------------- MMA issuers
-    // A stream runs through its own tiles in the order S(0), S(1), PV(0), S(2), ...;
-    // a ring slot is released by one arrival per stream: a commit by a stream that
-    // used the tile, a plain arrival by one that did not.
+    // A stream runs through its own parts u = 0, 1, ... of 64 keys (all items) in the
+    // order S(0), S(1), PV(0), S(2), PV(1), ...: S(u) goes to buffer u % 2 once PV(u - 2)
+    // has read P there, PV(u - 1) right after it, once its P is there.  A ring slot is
+    // released by one arrival per stream: a commit by a stream that used the tile, a
+    // plain arrival by one that did not.
     const int s = warp - MMA_WARP;
-    constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, BN, false, false);
+    constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, SN, false, false);
     constexpr uint32_t IDESC_O = idesc_bf16_f32(BM, D, false, true);
-    constexpr uint32_t KV16 = C::KV_TILE >> 4;
+    constexpr uint32_t KV16 = C::KV_TILE >> 4, SUB16 = SN * C::RB >> 4;
     const uint64_t dk = tree_sdesc(smem_u32(sm.k[0]), 16, 8 * C::RB, C::SWZ);
     const uint64_t dv = tree_sdesc(smem_u32(sm.v[0]), C::KV_BLOCK, 8 * C::RB, C::SWZ);
     auto qstep = [](int kk) {
@@ -455,23 +487,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     auto kstep = [](int kk) {
       return static_cast<uint32_t>((kk / C::KPB) * (C::KV_BLOCK >> 4) + (kk % C::KPB) * 2);
     };
-    const uint32_t t_s = tmem + C::col_s(s), t_o = tmem + C::col_o(s), t_p = tmem + C::col_p(s);
+    const uint32_t t_o = tmem + C::col_o(s);
     const bool leader = elect_one();
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
       return ok;
     };
-    auto k_wait = [&](uint32_t g) { return wait(&sm.k_full[g % KSTAGES], (g / KSTAGES) & 1); };
     auto v_wait = [&](uint32_t g) { return wait(&sm.v_full[g % VSTAGES], (g / VSTAGES) & 1); };
-    uint32_t u = 0, npv = 0;  // products issued
-    bool pending = false;     // the last S'd tile still owes its PV product
-    uint32_t pg = 0;          // its ring index
-    bool pfirst = false;      // whether it is its item's first (of this stream)
-    TreeItem it = {};
-    int slot = 0;
-    // zeros in the rows of a value tile that nobody sees, whatever they hold
-    auto clear_rows = [&](uint32_t g, int tile) {
-      uint8_t* v = sm.v[g % VSTAGES];
+    uint32_t u = 0;  // score products issued
+    // the last one still owes its PV product: of ring tile pg, part psub; whether it is
+    // its item's first, the last of its tile, the last of its item (then of pslot)
+    bool pending = false, pfirst = false, prelease = false, plast = false;
+    uint32_t pg = 0;
+    int psub = 0, pslot = 0, plo = 0, phi = 0, pnode = -1;
+    // zeros in the rows of a value tile that nobody sees, whatever they hold: rows of
+    // the part outside [plo, phi), of places that are no node
+    auto clear_rows = [&]() {
+      uint8_t* v = sm.v[pg % VSTAGES];
       auto clear = [&](int lo, int hi) {
         for (int e = lo * C::CPB + lane; e < hi * C::CPB; e += 32)
 #pragma unroll
@@ -479,20 +511,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             *reinterpret_cast<uint4*>(v + nb * C::KV_BLOCK + e * 16) = make_uint4(0u, 0u, 0u, 0u);
       };
       bool any = false;
-      if (tile < it.ctx) {
+      if (pnode < 0) {
         if (Q8) return;  // done where codes are widened
-        const int base = it.base0 + tile * BN;
-        const int lo = min(max(it.key0 - base, 0), BN), hi = min(max(it.L - base, 0), BN);
-        any = lo > 0 || hi < BN;
+        const int r0 = psub * SN, r1 = r0 + SN;
+        any = plo > r0 || phi < r1;
         if (any) {
-          clear(0, lo);
-          clear(hi, BN);
+          clear(r0, min(plo, r1));
+          clear(max(phi, r0), r1);
         }
       } else {
-        const int base = (tile - it.ctx) * BN;
-        for (int r = 0; r < BN; r += 32) {
-          const int node = base + r + lane;
-          unsigned gone = __ballot_sync(0xffffffffu, node < p.n && sm.depth[slot][node] < 0);
+        for (int r = psub * SN; r < psub * SN + SN; r += 32) {
+          const int node = pnode + r + lane;
+          unsigned gone = __ballot_sync(0xffffffffu, node < p.n && sm.depth[pslot][node] < 0);
           any = any || gone != 0;
           for (; gone != 0; gone &= gone - 1) {
             const int row = r + __ffs(gone) - 1;
@@ -505,71 +535,100 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
       }
     };
-    int ptile = 0;
     auto flush_pv = [&]() {
       if (!pending) return;
-      if (!wait(&sm.p_full[s], npv & 1) || !v_wait(pg)) return;
-      clear_rows(pg, ptile);
+      const uint32_t w = u - 1;
+      if (!v_wait(pg) || !wait(&sm.p_full[s][w & 1], (w >> 1) & 1)) return;
+      clear_rows();
       tc_fence_after();
-      const uint64_t b = dv + (pg % VSTAGES) * KV16;
+      const uint64_t b = dv + (pg % VSTAGES) * KV16 + psub * SUB16;
+      const uint32_t t_p = tmem + C::col_s(s, w & 1);
       if (leader) {
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
+        for (int kk = 0; kk < SN / 16; ++kk)
           mma_ts(t_o, t_p + kk * 8, b + C::RB * kk, IDESC_O, (!pfirst || kk > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&sm.pv_done[s]));
-        tc_commit(smem_u32(&sm.v_empty[pg % VSTAGES]));
+        tc_commit(smem_u32(&sm.pv_done[s][w & 1]));
+        if (prelease) tc_commit(smem_u32(&sm.v_empty[pg % VSTAGES]));
+        if (plast) mbar_arrive(smem_u32(&sm.item_empty[pslot]));
       }
       __syncwarp();
-      ++npv;
       pending = false;
+    };
+    // waits for a barrier, with what is pending done first where that takes time
+    auto next_wait = [&](uint64_t* bar, uint32_t parity) {
+      if (pending && __shfl_sync(0xffffffffu, mbar_test(smem_u32(bar), parity) ? 1 : 0, 0) == 0)
+        flush_pv();
+      return wait(bar, parity);
     };
     uint32_t g0 = 0;
     for (uint32_t items = 0; ok; ++items) {
-      if (!wait(&sm.item_full[items & 1], (items >> 1) & 1)) break;
-      it = sm.item[items & 1];
-      slot = items & 1;
+      const int slot = items & 1;
+      if (!next_wait(&sm.item_full[slot], (items >> 1) & 1)) break;
+      const TreeItem it = sm.item[slot];
       if (it.more == 0) break;
       const bool both = it.split == 0;
       const uint64_t dq = tree_sdesc(smem_u32(sm.q[items % C::QSLOTS][both ? s : 0]), 16,
                                      8 * C::RB, C::SWZ);
-      const int last = both ? it.n - 1 : (it.n - 1 - s) / 2 * 2 + s;  // (< 0: none)
       bool first = true;
-      if (!both && it.n <= s && leader) mbar_arrive(smem_u32(&sm.q_empty[items % C::QSLOTS]));
       for (int j = 0; j < it.n && ok; ++j) {
         const uint32_t g = g0 + j;
-        if (!both && (j & 1) != s) {
-          // the other stream's tile
-          if (k_wait(g) && leader) mbar_arrive(smem_u32(&sm.k_empty[g % KSTAGES]));
-          if (v_wait(g) && leader) mbar_arrive(smem_u32(&sm.v_empty[g % VSTAGES]));
+        const int t = it.t0 + j, parts = parts_of<C>(it, t, p.n);
+        int sub0 = 0, sub1 = parts;  // this stream's
+        if (!both) {
+          sub0 = C::NSUB == 1 ? 0 : s;
+          sub1 = C::NSUB == 1 ? ((j & 1) == s ? 1 : 0) : min(s + 1, parts);
+        }
+        if (!next_wait(&sm.k_full[g % KSTAGES], (g / KSTAGES) & 1)) break;
+        if (sub0 >= sub1) {
+          if (leader) mbar_arrive(smem_u32(&sm.k_empty[g % KSTAGES]));
+          if (next_wait(&sm.v_full[g % VSTAGES], (g / VSTAGES) & 1) && leader)
+            mbar_arrive(smem_u32(&sm.v_empty[g % VSTAGES]));
           continue;
         }
-        if (!k_wait(g)) break;
-        if (u > 0 && !wait(&sm.s_free[s], (u - 1) & 1)) break;
-        tc_fence_after();
-        const uint64_t b = dk + (g % KSTAGES) * KV16;
-        if (leader) {
+        for (int sub = sub0; sub < sub1 && ok; ++sub) {
+          if (u > 1 && !wait(&sm.pv_done[s][u & 1], ((u >> 1) - 1) & 1)) break;
+          tc_fence_after();
+          const uint64_t b = dk + (g % KSTAGES) * KV16 + sub * SUB16;
+          const uint32_t t_s = tmem + C::col_s(s, u & 1);
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(t_s, dq + qstep(kk), b + kstep(kk), IDESC_S, kk > 0 ? 1u : 0u);
-          tc_commit(smem_u32(&sm.s_full[s]));
-          tc_commit(smem_u32(&sm.k_empty[g % KSTAGES]));
-          if (j == last) tc_commit(smem_u32(&sm.q_empty[items % C::QSLOTS]));
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(t_s, dq + qstep(kk), b + kstep(kk), IDESC_S, kk > 0 ? 1u : 0u);
+            tc_commit(smem_u32(&sm.s_full[s][u & 1]));
+            if (sub + 1 == sub1) tc_commit(smem_u32(&sm.k_empty[g % KSTAGES]));
+          }
+          __syncwarp();
+          // (the pending one is u - 1 until u counts this one)
+          flush_pv();
+          if (!ok) break;
+          ++u;
+          pending = true;
+          pfirst = first;
+          first = false;
+          prelease = sub + 1 == sub1;
+          plast = false;
+          pg = g;
+          psub = sub;
+          pslot = slot;
+          const int base = it.base0 + t * BN;
+          plo = it.key0 - base;
+          phi = it.L - base;
+          pnode = t < it.ctx ? -1 : (t - it.ctx) * BN;
         }
-        __syncwarp();
-        ++u;
-        flush_pv();
-        pending = true;
-        pg = g;
-        ptile = it.t0 + j;
-        pfirst = first;
-        first = false;
       }
-      // the item's last product before its tables go away
-      flush_pv();
+      if (!ok) break;
+      if (leader) tc_commit(smem_u32(&sm.q_empty[items % C::QSLOTS]));
+      if (!first && pending) {
+        plast = true;
+      } else {
+        // nothing of this item is owed; what one before owes does not wait for more
+        if (leader) mbar_arrive(smem_u32(&sm.item_empty[slot]));
+        __syncwarp();
+        flush_pv();
+      }
       g0 += it.n;
-      if (ok && leader) mbar_arrive(smem_u32(&sm.item_empty[slot]));
-      __syncwarp();
     }
+    flush_pv();
     if (!ok && leader) fail();
     // every product issued by this warp completes before tensor memory is freed
     if (leader) tc_commit(smem_u32(&sm.drain[s]));
@@ -793,13 +852,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ---------------------------------------------------------------- softmax
     const int s = warp >> 2, quarter = warp & 3;
     const int at = quarter * 32 + lane;  // tensor-memory lane
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_off + C::col_s(s);
-    const uint32_t tO = tmem + lane_off + C::col_o(s);
-    const uint32_t tP = tmem + lane_off + C::col_p(s);
+    const uint32_t base_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tO = base_addr + C::col_o(s);
     constexpr int OC = C::OW / 32;
-    uint32_t u = 0;  // tiles of this stream
-    int was_split = -1;
+    uint32_t u = 0;  // parts of SN keys of this stream
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
       return ok;
@@ -814,42 +870,224 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!wait(&sm.item_full[slot], (items >> 1) & 1)) break;
       const TreeItem it = sm.item[slot];
       if (it.more == 0) break;
-      const bool both = it.split == 0;
-      const int split = both ? 1 : it.split;
-      const int lanes = BM / split, cols = BN / split;
-      const int copy = at / lanes;
-      const int r = both ? s * BM + at : at - copy * lanes;
+      const bool both = it.split == 0, twice = it.split == 2;
+      const int copy = twice ? at >> 6 : 0;
+      const int r = both ? s * BM + at : (twice ? at & 63 : at);
       const bool valid = r < it.rows;
       const bool active = __any_sync(0xffffffffu, valid);
       const int row = it.row0 + (valid ? r : 0);
-      const int head = it.hk * p.G + row / p.n, node = row % p.n;
-      const int depth = sm.depth[slot][node];
-      const bool alive = valid && depth >= 0;
-      const float slope2 = p.slopes ? kLog2e * __ldg(p.slopes + head) : 0.f;
-      const int col0 = copy * cols;
-      const bool changed = p.capped || p.slopes != nullptr;
-      if (split != was_split) {
-        // columns that another copy of a row takes stay zero
-        was_split = split;
-        if (split > 1) {
+      const int g = row / p.n, node = row - g * p.n, head = it.hk * p.G + g;
+      const int depth = max(sm.depth[slot][node], 0);
+      const bool alive = valid && sm.depth[slot][node] >= 0;
+      const float slope2 = CHANGED && p.slopes ? kLog2e * __ldg(p.slopes + head) : 0.f;
+      // position of the row's first visible key, for the window
+      const int first_key = p.window >= 0 ? it.L + depth - p.window : 0;
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+
+      // one part of a tile: NC of its 64 columns, from col0 on
+      auto part_of_tile = [&](auto nc, int t, int sub, float sc) {
+        constexpr int NC = decltype(nc)::value;
+        const int col0 = NC < SN ? copy * NC : 0;
+        const bool tree = t >= it.ctx;
+        // the key (or node) of column 0
+        const int base = (tree ? (t - it.ctx) * BN : it.base0 + t * BN) + sub * SN;
+        const uint32_t tS = base_addr + C::col_s(s, u & 1);
+        uint32_t x[NC / 32][32];
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) tmem_ld32(tS + col0 + 32 * c, x[c]);
+        // the scale of 16 columns: of the tile's block that they lie in
+        auto scale_at = [&](int col, int kv) {
+          return __shfl_sync(0xffffffffu, sc, kv * 8 + ((sub * SN + col0 + col) >> p.T_log2));
+        };
+        float factor[NC / 16];
+#pragma unroll
+        for (int c = 0; c < NC / 16; ++c)
+          factor[c] = (Q8 ? scale_at(16 * c, 0) : 1.f) * (CHANGED && p.capped ? 1.f : p.scale_log2);
+        // (a factor of zero would make NaN of masked scores)
+        if constexpr (Q8 && !CHANGED) {
+#pragma unroll
+          for (int c = 0; c < NC / 16; ++c) factor[c] = fmaxf(factor[c], 0x1p-126f);
+        }
+        const int hi = it.L - base, lo = first_key - base;
+        const bool edge = tree || hi < SN || (p.window >= 0 && __any_sync(0xffffffffu, lo > 0));
+        float off = 0.f;
+        tmem_ld_wait(x[0]);
+#pragma unroll
+        for (int c = 1; c < NC / 32; ++c) reg_fence(x[c]);
+        if constexpr (CHANGED) {
+          // finished scores in log2 units, but for `off`
+          if (p.capped) {
+            float big = 0.f;
+#pragma unroll
+            for (int c = 0; c < NC / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                if constexpr (Q8) {
+                  float a, b;
+                  fma2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]),
+                       factor[2 * c + i / 16], factor[2 * c + i / 16], 0.f, 0.f);
+                  x[c][i] = __float_as_uint(a);
+                  x[c][i + 1] = __float_as_uint(b);
+                }
+                big = max3_abs(big, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+              }
+            const bool small = __all_sync(0xffffffffu, big <= p.cap.small);
+            if (small) {
+#pragma unroll
+              for (int c = 0; c < NC / 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const float x0 = __uint_as_float(x[c][i]), x1 = __uint_as_float(x[c][i + 1]);
+                  float z0, z1, y0, y1;
+                  fma2(z0, z1, x0, x1, x0, x1, 0.f, 0.f);
+                  fma2(y0, y1, z0, z1, p.cap.poly[2], p.cap.poly[2], p.cap.poly[1], p.cap.poly[1]);
+                  fma2(y0, y1, z0, z1, y0, y1, p.cap.poly[0], p.cap.poly[0]);
+                  fma2(y0, y1, x0, x1, y0, y1, 0.f, 0.f);
+                  x[c][i] = __float_as_uint(y0);
+                  x[c][i + 1] = __float_as_uint(y1);
+                }
+            } else {
+              // cap * tanh(y) = cap - 2 cap / (1 + 2^(2 y log2(e))), in log2 units
+#pragma unroll
+              for (int c = 0; c < NC / 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float y = __uint_as_float(x[c][i]);
+                  float w = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(y * p.cap_in)), p.cap_log2);
+                  if (p.wide && fabsf(y) <= p.cap.small) {
+                    const float z = y * y;
+                    w = y * fmaf(z, fmaf(z, p.cap.poly[2], p.cap.poly[1]), p.cap.poly[0]);
+                  }
+                  x[c][i] = __float_as_uint(w);
+                }
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < NC / 32; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                x[c][i] = __float_as_uint(__uint_as_float(x[c][i]) * factor[2 * c + i / 16]);
+          }
+          if (p.slopes) {
+            if (tree) {
+              off = -slope2 * depth;
+#pragma unroll
+              for (int c = 0; c < NC / 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const int a = min(base + col0 + 32 * c + i, kMostNodes - 1);
+                  x[c][i] = __float_as_uint(fmaf(slope2, static_cast<float>(sm.depth[slot][a]),
+                                                 __uint_as_float(x[c][i])));
+                }
+            } else {
+              off = -slope2 * static_cast<float>(it.L + depth - base - col0);
+#pragma unroll
+              for (int c = 0; c < NC / 32; ++c)
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  const float col = static_cast<float>(32 * c + i);
+                  float a, b;
+                  fma2(a, b, col, col + 1.f, slope2, slope2, __uint_as_float(x[c][i]),
+                       __uint_as_float(x[c][i + 1]));
+                  x[c][i] = __float_as_uint(a);
+                  x[c][i + 1] = __float_as_uint(b);
+                }
+            }
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < NC / 32; ++c) {
+            const int at_col = col0 + 32 * c;
+            const uint32_t see = tree ? sm.line[slot][node][(base + at_col) >> 5]
+                                      : below(hi - at_col) & ~below(lo - at_col);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(see & (1u << i))) x[c][i] = __float_as_uint(-INFINITY);
+          }
+        }
+        // the largest score, 16 columns of one scale at a time
+        float mt = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NC / 16; ++c) {
+          float m2[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              m2[e] = max3(m2[e], __uint_as_float(x[c >> 1][(c & 1) * 16 + i + 2 * e]),
+                           __uint_as_float(x[c >> 1][(c & 1) * 16 + i + 2 * e + 1]));
+          mt = fmaxf(mt, fmaxf(m2[0], m2[1]) * (CHANGED ? 1.f : factor[c]));
+        }
+        mt += off;
+        float alpha = 1.f;
+        if (mt > m + kRescale) {
+          alpha = ex2(m - mt);  // 0 when m = -inf
+          l *= alpha;
+          m = mt;
+        }
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+          // O is rescaled once the last product is done
+          if (!wait(&sm.pv_done[s][(u - 1) & 1], ((u - 1) >> 1) & 1)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tO + c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(tO + c, o);
+          }
+        }
+        const float neg_m = m == -INFINITY ? 0.f : off - m;
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float f = factor[2 * c + half];
+            const float v = Q8 ? scale_at(32 * c + 16 * half, 1) : 1.f;
+#pragma unroll
+            for (int i = 16 * half; i < 16 * half + 16; i += 2) {
+              float a, b;
+              if constexpr (CHANGED)
+                add2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]), neg_m, neg_m);
+              else
+                fma2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]), f, f, neg_m,
+                     neg_m);
+              a = ex2(a);
+              b = ex2(b);
+              add2(l0, l1, l0, l1, a, b);
+              if constexpr (Q8) fma2(a, b, a, b, v, v, 0.f, 0.f);
+              pk[i >> 1] = pack_bf16x2(a, b);
+            }
+          }
+          tmem_st16(tS + (col0 >> 1) + 16 * c, pk);
+        }
+        l += l0 + l1;
+        if constexpr (NC < SN) {
           uint32_t z[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) z[i] = 0u;
-          for (int c = 0; c < BN / 2; c += 16) tmem_st16(tP + c, z);
-          tmem_st_wait();
+          tmem_st16(tS + (16 - (col0 >> 1)), z);  // the other copy's columns
         }
-      }
-      float m = -INFINITY, l = 0.f;
-      const int step = both ? 1 : 2, j0 = both ? 0 : s;
-      bool first = true;
-      for (int j = j0; j < it.n; j += step, ++u) {
-        const int t = it.t0 + j;
-        const bool tree = t >= it.ctx;
-        const int base = tree ? (t - it.ctx) * BN : it.base0 + t * BN;
+        tmem_st_wait();
+      };
+
+      for (int j = 0; j < it.n && ok; ++j) {
+        const int t = it.t0 + j, parts = parts_of<C>(it, t, p.n);
+        int sub0 = 0, sub1 = parts;
+        if (!both) {
+          sub0 = C::NSUB == 1 ? 0 : s;
+          sub1 = C::NSUB == 1 ? ((j & 1) == s ? 1 : 0) : min(s + 1, parts);
+        }
+        if (sub0 >= sub1) continue;
         float sc = 1.f;  // lane i: the scale of the tile's i-th block of keys, 8 + i: of values
         if constexpr (Q8) {
-          if (!tree) {
-            const int blk = (base >> p.T_log2) + (lane & 7);
+          if (t < it.ctx) {
+            const int base = it.base0 + t * BN, blk = (base >> p.T_log2) + (lane & 7);
             sc = 0.f;
             if (lane < 16 && (blk << p.T_log2) < min(it.L, base + BN) &&
                 ((blk + 1) << p.T_log2) > it.key0)
@@ -857,279 +1095,114 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                          (static_cast<long long>(it.b) * p.HK + it.hk) * p.num_blocks + blk);
           }
         }
-        if (!wait(&sm.s_full[s], u & 1)) break;
-        tc_fence_after();
-        bool rescale_o = false;
-        float alpha = 1.f;
-        if (active) {
-          // this row's keys of the tile: columns [lo, hi), or bits
-          const int hi = it.L - base;
-          const int lo = p.window >= 0 ? it.L + max(depth, 0) - p.window - base : 0;
-          const bool edge =
-              tree || hi < BN || (p.window >= 0 && __any_sync(0xffffffffu, lo > 0));
-          const float off = p.slopes ? (tree ? -slope2 * max(depth, 0)
-                                             : -slope2 * static_cast<float>(it.L + max(depth, 0) - base))
-                                     : 0.f;
-          // the finished scores of 32 columns from `c` on, less `off`, in log2 units
-          auto scores = [&](uint32_t(&x)[32], int c) {
-            float k0 = 1.f, k1 = 1.f;
-            if constexpr (Q8) {
-              if (!tree) {
-                k0 = __shfl_sync(0xffffffffu, sc, c >> p.T_log2);
-                k1 = __shfl_sync(0xffffffffu, sc, (c + 16) >> p.T_log2);
-              }
-            }
-            if (!changed) {
-              k0 *= p.scale_log2;
-              k1 *= p.scale_log2;
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float k = i < 16 ? k0 : k1;
-                float a, b;
-                fma2(a, b, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), k, k, 0.f, 0.f);
-                x[i] = __float_as_uint(a);
-                x[i + 1] = __float_as_uint(b);
-              }
-            } else {
-              if (p.capped) {
-                float big = 0.f;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  if constexpr (Q8)
-                    x[i] = __float_as_uint(__uint_as_float(x[i]) * (i < 16 ? k0 : k1));
-                  big = fmaxf(big, fabsf(__uint_as_float(x[i])));
-                }
-                const bool small = __all_sync(0xffffffffu, big <= p.cap.small);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float y = __uint_as_float(x[i]), z = y * y;
-                  const float near =
-                      y * fmaf(z, fmaf(z, p.cap.poly[2], p.cap.poly[1]), p.cap.poly[0]);
-                  float w = near;
-                  if (!small) {
-                    w = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(y * p.cap_in)), p.cap_log2);
-                    if (p.wide && fabsf(y) <= p.cap.small) w = near;
-                  }
-                  x[i] = __float_as_uint(w);
-                }
-              } else {
-                k0 *= p.scale_log2;
-                k1 *= p.scale_log2;
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  x[i] = __float_as_uint(__uint_as_float(x[i]) * (i < 16 ? k0 : k1));
-              }
-              if (p.slopes) {
-                if (tree) {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) {
-                    const int a = min(base + c + i, kMostNodes - 1);
-                    x[i] = __float_as_uint(fmaf(slope2, static_cast<float>(sm.depth[slot][a]),
-                                                __uint_as_float(x[i])));
-                  }
-                } else {
-                  const float c0 = static_cast<float>(c);
-#pragma unroll
-                  for (int i = 0; i < 32; ++i)
-                    x[i] = __float_as_uint(fmaf(slope2, c0 + i, __uint_as_float(x[i])));
-                }
-              }
-            }
-            if (edge) {
-              const uint32_t see = tree ? sm.line[slot][node][(base + c) >> 5]
-                                        : below(hi - c) & ~below(lo - c);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(see & (1u << i))) x[i] = __float_as_uint(-INFINITY);
-            }
-          };
-          float mt = -INFINITY;
-#pragma unroll 1
-          for (int c = col0; c < col0 + cols; c += 32) {
-            uint32_t x[32];
-            tmem_ld32(tS + c, x);
-            tmem_ld_wait(x);
-            scores(x, c);
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                m4[e] = max3(m4[e], __uint_as_float(x[i + 2 * e]), __uint_as_float(x[i + 2 * e + 1]));
-            mt = fmaxf(mt, fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]));
+        for (int sub = sub0; sub < sub1; ++sub) {
+          if (!wait(&sm.s_full[s][u & 1], (u >> 1) & 1)) break;
+          tc_fence_after();
+          if (active) {
+            if (twice)
+              part_of_tile(std::integral_constant<int, 32>(), t, sub, sc);
+            else
+              part_of_tile(std::integral_constant<int, 64>(), t, sub, sc);
+            if (!ok) break;
           }
-          mt += off;
-          if (mt > m + kRescale) {
-            alpha = ex2(m - mt);  // 0 when m = -inf
-            l *= alpha;
-            rescale_o = !first;
-            m = mt;
-          }
-          // P overwrites the last tile's, and O is rescaled, once that product is done
-          if (u > 0) {
-            if (!wait(&sm.pv_done[s], (u - 1) & 1)) break;
-            tc_fence_after();
-          }
-          if (__any_sync(0xffffffffu, rescale_o)) {
-            const float a = rescale_o ? alpha : 1.f;
-#pragma unroll
-            for (int h2 = 0; h2 < OC; ++h2) {
-              uint32_t oc[32];
-              tmem_ld32(tO + h2 * 32, oc);
-              tmem_ld_wait(oc);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) oc[i] = __float_as_uint(__uint_as_float(oc[i]) * a);
-              tmem_st32(tO + h2 * 32, oc);
-            }
-          }
-          const float neg_m = m == -INFINITY ? 0.f : off - m;
-          float l0 = 0.f, l1 = 0.f;
-#pragma unroll 1
-          for (int c = col0; c < col0 + cols; c += 32) {
-            uint32_t x[32], pk[16];
-            tmem_ld32(tS + c, x);
-            tmem_ld_wait(x);
-            scores(x, c);
-            float v0 = 1.f, v1 = 1.f;
-            if constexpr (Q8) {
-              if (!tree) {
-                v0 = __shfl_sync(0xffffffffu, sc, 8 + (c >> p.T_log2));
-                v1 = __shfl_sync(0xffffffffu, sc, 8 + ((c + 16) >> p.T_log2));
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float a, b;
-              add2(a, b, __uint_as_float(x[i]), __uint_as_float(x[i + 1]), neg_m, neg_m);
-              a = ex2(a);
-              b = ex2(b);
-              add2(l0, l1, l0, l1, a, b);
-              if constexpr (Q8) {
-                const float v = i < 16 ? v0 : v1;
-                fma2(a, b, a, b, v, v, 0.f, 0.f);
-              }
-              pk[i >> 1] = pack_bf16x2(a, b);
-            }
-            tmem_st16(tP + c / 2, pk);
-          }
-          l += l0 + l1;
-          tmem_st_wait();
-        } else if (u > 0) {
-          if (!wait(&sm.pv_done[s], (u - 1) & 1)) break;
+          first = false;
+          tc_fence_before();
+          mbar_arrive(smem_u32(&sm.p_full[s][u & 1]));
+          ++u;
         }
-        first = false;
-        tc_fence_before();
-        mbar_arrive(smem_u32(&sm.s_free[s]));
-        mbar_arrive(smem_u32(&sm.p_full[s]));
       }
       if (!ok) break;
 
       // ---------------------------------------------------------- the run's result
       if (!first) {
-        if (!wait(&sm.pv_done[s], (u - 1) & 1)) break;
+        if (!wait(&sm.pv_done[s][(u - 1) & 1], ((u - 1) >> 1) & 1)) break;
         tc_fence_after();
       }
       if (!alive) {
         m = -INFINITY;
         l = 0.f;
       }
-      float* part = it.whole ? nullptr
-                             : p.part + (static_cast<size_t>(blockIdx.x) * 2 + it.slot) *
-                                            p.block_rows * (D + kPartTail);
+      float* part = p.part + ((static_cast<size_t>(blockIdx.x) * 2 + it.slot) * p.block_rows + r) *
+                                 (D + kPartTail);
+      const int split = twice ? 2 : 1;
+      const int pidx = s * split + copy;  // which part of the row (not both)
       float weight = alive ? 1.f : 0.f, most = m, sum = l;
       if (!both) {
-        // the parts of a row: two streams, `split` copies each
         sm.stat[threadIdx.x] = make_float2(m, l);
         if (!join()) break;
         most = -INFINITY;
-        for (int e = 0; e < 2 * split; ++e)
-          most = fmaxf(most, sm.stat[e / split * BM + e % split * lanes + r].x);
+        const int step = twice ? 64 : BM, at0 = twice ? r : at;
+#pragma unroll 1
+        for (int e = at0; e < 2 * BM; e += step) most = fmaxf(most, sm.stat[e].x);
         sum = 0.f;
-        for (int e = 0; e < 2 * split; ++e) {
-          const float2 x = sm.stat[e / split * BM + e % split * lanes + r];
-          if (x.y > 0.f) sum += x.y * ex2(x.x - most);
+#pragma unroll 1
+        for (int e = at0; e < 2 * BM; e += step) {
+          const float2 x = sm.stat[e];
+          if (x.y > 0.f) sum = fmaf(x.y, ex2(x.x - most), sum);
         }
         weight = l > 0.f ? ex2(m - most) : 0.f;
       }
       if (it.whole) weight = sum > 0.f ? weight / sum : 0.f;
-      if (valid && (both || (s == 0 && copy == 0))) {
-        if (!it.whole) {
-          float* tail = part + static_cast<size_t>(r) * (D + kPartTail) + D;
-          tail[0] = most;
-          tail[1] = sum;
-        } else if (p.lse != nullptr) {
+      const bool writer = valid && (both || pidx == 0);
+      if (writer) {
+        if (!it.whole)
+          *reinterpret_cast<float2*>(part + D) = make_float2(most, sum);
+        else if (p.lse != nullptr)
           p.lse[(static_cast<size_t>(it.b) * p.H + head) * p.n + node] =
               sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
-        }
       }
+      __nv_bfloat16* out = p.o + it.b * p.so.b + head * p.so.h + node * p.so.n;
+      const int lanes = twice ? 64 : BM;
 #pragma unroll 1
-      for (int h2 = 0; h2 < OC; ++h2) {
-        uint32_t oc[32];
-        if (!first) {
-          tmem_ld32(tO + 32 * h2, oc);
-          tmem_ld_wait(oc);
-        }
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        if (!first) tmem_ld16(tO + c, o);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          oc[i] = weight > 0.f && !first ? __float_as_uint(__uint_as_float(oc[i]) * weight) : 0u;
+        for (int i = 0; i < 16; ++i)
+          o[i] = weight > 0.f && !first ? __float_as_uint(__uint_as_float(o[i]) * weight) : 0u;
+        if (!both) {
+          if (pidx > 0) {
+            uint4* to = reinterpret_cast<uint4*>(sm.merge[(pidx - 1) * lanes + r]);
 #pragma unroll
-        for (int half = 0; half < (D < 32 ? 1 : 2); ++half) {
-          const int c = h2 * 32 + half * 16;
-          if (both) {
-            if (!valid) {
-            } else if (it.whole) {
-              uint4* to = reinterpret_cast<uint4*>(p.o + it.b * p.so.b + head * p.so.h +
-                                                   node * p.so.n + c);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t* x = oc + half * 16 + e * 8;
-                to[e] = make_uint4(
-                    pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                    pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                    pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                    pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
-              }
-            } else {
-              uint4* to = reinterpret_cast<uint4*>(part + static_cast<size_t>(r) * (D + kPartTail) + c);
+            for (int e = 0; e < 4; ++e)
+              to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          if (!join()) break;
+          if (pidx == 0) {
+#pragma unroll 1
+            for (int w = 0; w < 2 * split - 1; ++w) {
+              const float4* from = reinterpret_cast<const float4*>(sm.merge[w * lanes + r]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint32_t* x = oc + half * 16 + e * 4;
-                to[e] = make_uint4(x[0], x[1], x[2], x[3]);
+                const float4 y = from[e];
+                o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) + y.x);
+                o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) + y.y);
+                o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) + y.z);
+                o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) + y.w);
               }
             }
-            continue;
           }
-          uint4* mine = reinterpret_cast<uint4*>(sm.merge[threadIdx.x]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t* x = oc + half * 16 + e * 4;
-            mine[e] = make_uint4(x[0], x[1], x[2], x[3]);
-          }
-          if (!join()) break;
-          for (int e = threadIdx.x; e < it.rows * 4; e += 2 * BM) {
-            const int rr = e >> 2, c4 = (e & 3) * 4;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < 2 * split; ++w) {
-              const float4 x = *reinterpret_cast<const float4*>(
-                  &sm.merge[w / split * BM + w % split * lanes + rr][c4]);
-              y.x += x.x;
-              y.y += x.y;
-              y.z += x.z;
-              y.w += x.w;
-            }
-            if (it.whole) {
-              const int rw = it.row0 + rr, g = rw / p.n;
-              *reinterpret_cast<uint2*>(p.o + it.b * p.so.b + (it.hk * p.G + g) * p.so.h +
-                                        (rw - g * p.n) * p.so.n + c + c4) =
-                  make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-            } else {
-              *reinterpret_cast<float4*>(part + static_cast<size_t>(rr) * (D + kPartTail) + c +
-                                         c4) = y;
-            }
-          }
-          if (!join()) break;
         }
-        if (!ok) break;
+        if (writer) {
+          if (it.whole) {
+            uint4* to = reinterpret_cast<uint4*>(out + c);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t* y = o + 8 * e;
+              to[e] = make_uint4(pack_bf16x2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                 pack_bf16x2(__uint_as_float(y[2]), __uint_as_float(y[3])),
+                                 pack_bf16x2(__uint_as_float(y[4]), __uint_as_float(y[5])),
+                                 pack_bf16x2(__uint_as_float(y[6]), __uint_as_float(y[7])));
+            }
+          } else {
+            uint4* to = reinterpret_cast<uint4*>(part + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (!both && !join()) break;
+        __syncwarp();
       }
       if (!ok) break;
       tc_fence_before();
@@ -1194,22 +1267,29 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p,
         sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool CHANGED>
 cudaError_t launch_tree_d(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
                           const LaunchCtx& ctx) {
   using C = TCfg<FMT, D>;
   static_assert(sizeof(TreeSmem<C>) + 1024 <= 232448, "dynamic shared memory per CTA");
   const size_t smem = sizeof(TreeSmem<C>) + 1024;
-  cudaError_t err = cudaFuncSetAttribute(attn_tree_kernel<FMT, D>,
+  cudaError_t err = cudaFuncSetAttribute(attn_tree_kernel<FMT, D, CHANGED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  attn_tree_kernel<FMT, D><<<plan.ctas, NUM_THREADS, smem, ctx.stream>>>(maps[0], maps[1], maps[2],
-                                                                        maps[3], p);
+  attn_tree_kernel<FMT, D, CHANGED>
+      <<<plan.ctas, NUM_THREADS, smem, ctx.stream>>>(maps[0], maps[1], maps[2], maps[3], p);
   if ((err = cudaGetLastError()) != cudaSuccess || plan.whole) return err;
   const long long rows = static_cast<long long>(p.B) * p.HK * p.rows;
   return launch_dependent(attn_tree_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)),
                           dim3(256), 0, ctx.stream, p, plan.ctas);
+}
+
+template <int FMT, int D>
+cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
+                             const LaunchCtx& ctx) {
+  return p.capped || p.slopes ? launch_tree_d<FMT, D, true>(p, maps, plan, ctx)
+                              : launch_tree_d<FMT, D, false>(p, maps, plan, ctx);
 }
 
 template <int FMT>
@@ -1258,10 +1338,10 @@ cudaError_t launch_tree_fmt(const TreeDecodeProblem& pb, const CUtensorMap* maps
   p.cap = cap_poly(pb.scale, pb.softcap);
   p.wide = pb.softcap > kWideCap;
   switch (pb.d) {
-    case 16: return launch_tree_d<FMT, 16>(p, maps, plan, ctx);
-    case 32: return launch_tree_d<FMT, 32>(p, maps, plan, ctx);
-    case 64: return launch_tree_d<FMT, 64>(p, maps, plan, ctx);
-    case 128: return launch_tree_d<FMT, 128>(p, maps, plan, ctx);
+    case 16: return launch_tree_mode<FMT, 16>(p, maps, plan, ctx);
+    case 32: return launch_tree_mode<FMT, 32>(p, maps, plan, ctx);
+    case 64: return launch_tree_mode<FMT, 64>(p, maps, plan, ctx);
+    case 128: return launch_tree_mode<FMT, 128>(p, maps, plan, ctx);
     default: return cudaErrorInvalidValue;
   }
 }
