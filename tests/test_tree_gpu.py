@@ -117,6 +117,10 @@ CASES = [
     (1, 2, 1, 9, 9000, 64, 128, 0.0, True, None, "random", [8999]),  # the cache is split
     (1, 2, 2, 12, 5000, 128, 16, 30.0, False, 2100, "random", [4996]),
     (2, 2, 1, 70, 3, 64, 16, 0.0, True, 5, "chain", [3, 0]),  # a window wider than the cache
+    (1, 4, 1, 16, 700, 64, 32, 0.0, True, 200, "holes", [650]),  # 64 query rows
+    (2, 1, 1, 33, 400, 128, 64, 20.0, False, None, "random", [400, 260]),
+    (1, 3, 1, 10, 9000, 32, 128, 0.0, False, None, "star", [8991]),
+    (2, 2, 2, 32, 260, 16, 16, 0.0, True, 64, "chain", [260, 30]),
     (5, 2, 1, 3, 640, 16, 64, 0.0, False, None, "holes", [640, 1, 0, 333, 64]),
 ]
 

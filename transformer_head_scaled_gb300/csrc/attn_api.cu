@@ -1204,7 +1204,7 @@ int tree_decode_sizes(int B, int h, int h_kv, int n, int L_max, int d_k, int cac
   // the kernel counts the visible cache's tiles over all sequences and key heads
   // (and blocks of query rows) in 31 bits
   const long long blocks = (static_cast<long long>(h / h_kv) * n + 255) / 256;
-  if (static_cast<long long>(B) * h_kv * blocks * (L_max / tree_tile_keys(d_k) + 4LL) > 0x7fffffffLL)
+  if (static_cast<long long>(B) * h_kv * blocks * (L_max / 64 + 4LL) > 0x7fffffffLL)
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
@@ -1214,7 +1214,8 @@ TreePlan tree_plan(int B, int HK, int rows, int n, int L_max, int d, int window,
   TreePlan plan;
   plan.blocks = (rows + 255) / 256;
   plan.block_rows = rows < 256 ? rows : 256;
-  const int kt = tree_tile_keys(d);
+  plan.few = rows <= tree_few_rows();
+  const int kt = tree_tile_keys(d, plan.few);
   plan.tree_tiles = (n + kt - 1) / kt;
   const long long units = static_cast<long long>(B) * HK * plan.blocks;
   // most tiles of a unit (a window may begin inside one)
@@ -1281,7 +1282,7 @@ int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, cons
       (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
     return ATTN_ERR_INVALID_ARG;
   CUtensorMap maps[4];
-  const int kt = tree_tile_keys(d_k);
+  const int kt = tree_tile_keys(d_k, plan.few);
   for (int i = 0; i < 2; ++i) {
     const void* cache = i ? v_cache : k_cache;
     rc = q8 ? encode_4d_bytes(&maps[i], cache, d_k, L_max, h_kv, B, st[3 + i], 1, kt)

@@ -356,6 +356,7 @@ struct TreeDecodeProblem {
 };
 struct TreePlan {
   int ctas;
+  bool few;        // the kernel for few query rows of a key head
   bool whole;      // a CTA takes whole units (sequence, key head, block of query rows)
   int blocks;      // of query rows of a key head
   int block_rows;  // rows of a part in the workspace
@@ -364,7 +365,8 @@ struct TreePlan {
   size_t workspace_bytes;
 };
 TreePlan tree_plan(int B, int HK, int rows, int n, int L_max, int d, int window, int num_sms);
-int tree_tile_keys(int d);
+int tree_tile_keys(int d, bool few);
+int tree_few_rows();  // of a key head, for the kernel for few rows
 int tree_min_tiles();
 // maps: the key and the value cache with a box of a tile's rows (bf16: swizzled as
 // the operand of a product; 8 bits: as bytes), then the tree's keys and values.

@@ -59,38 +59,47 @@ constexpr int KLOAD_WARP = 12;
 constexpr int VLOAD_WARP = 13;
 constexpr int MMA_WARP = 14;   // and 15
 constexpr int NUM_THREADS = 512;
-constexpr uint32_t TMEM_COLS = 512;
 constexpr int SN = 64;  // keys of one score product
 constexpr float kRescale = 8.0f;  // a running maximum is kept until a score exceeds it by 2^8
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMergeStride = 20;  // floats: 16 columns of a part's row, four apart in the banks
 
-template <int FMT_, int D_>
+// Shapes.  FEW: for key heads of at most kFewRows query rows (attn_tree_few.cuh).
+constexpr int kFewRows = 64;
+template <int FMT_, int D_, bool FEW_>
 struct TCfg {
   static constexpr int FMT = FMT_, D = D_;
-  static constexpr bool Q8 = FMT_ != kCacheBf16;
-  static constexpr int BN = D_ == 128 ? 64 : 128;          // keys per tile
-  static constexpr uint32_t RB = (D_ < 64 ? D_ : 64) * 2;  // bytes of a row in one block
+  static constexpr bool Q8 = FMT_ != kCacheBf16, FEW = FEW_;
+  static constexpr int BN = D_ == 128 && !FEW_ ? 64 : 128;  // keys per tile
+  static constexpr uint32_t RB = (D_ < 64 ? D_ : 64) * 2;   // bytes of a row in one block
   static constexpr int NB = D_ > 64 ? D_ / 64 : 1;
   static constexpr uint32_t SWZ = RB == 128 ? 2u : (RB == 64 ? 4u : 6u);
   static constexpr int KPB = RB / 32;
   static constexpr int CPB = RB / 16;  // 16-byte chunks of a block row
-  static constexpr int QSLOTS = D_ == 128 ? 1 : 2;
-  static constexpr uint32_t Q_TILE = BM * D_ * 2, Q_BLOCK = BM * RB;
+  static constexpr int QROWS = FEW_ ? kFewRows : BM, QTILES = FEW_ ? 1 : 2;
+  static constexpr int QSLOTS = D_ == 128 && (Q8 || !FEW_) ? 1 : 2;
+  static constexpr uint32_t Q_TILE = QROWS * D_ * 2, Q_BLOCK = QROWS * RB;
   static constexpr uint32_t KV_TILE = BN * D_ * 2, KV_BLOCK = BN * RB;
   static constexpr uint32_t RAW_TILE = BN * D_;  // codes
-  static constexpr int KSTAGES = D_ >= 64 ? (Q8 ? 2 : 4) : (Q8 ? 4 : 6);  // of bf16 tiles
-  static constexpr int VSTAGES = D_ >= 64 && Q8 ? 3 : KSTAGES;
-  static constexpr int RAWS = Q8 ? (D_ >= 64 ? 3 : 6) : 1;  // of tiles of codes
+  // ring stages: of bf16 tiles, and of tiles of codes
+  static constexpr int WIDE = KV_TILE >= 32768 ? 2 : (KV_TILE >= 16384 ? 4 : 6);
+  static constexpr int KSTAGES = Q8 ? (KV_TILE >= 32768 ? 1 : WIDE / 2) : WIDE;
+  static constexpr int VSTAGES = Q8 ? (KV_TILE >= 32768 ? 2 : (WIDE == 4 ? 3 : WIDE / 2)) : WIDE;
+  static constexpr int RAWS = Q8 ? (KV_TILE >= 32768 ? 2 : (WIDE == 4 ? 3 : WIDE)) : 1;
   static constexpr uint32_t OW = D_ < 32 ? 32 : D_;
-  static constexpr int NSUB = BN / SN;
-  __host__ __device__ static constexpr uint32_t col_s(int s, int b) { return SN * (2 * s + b); }
-  __host__ __device__ static constexpr uint32_t col_o(int s) { return 4 * SN + OW * s; }
+  static constexpr int NSUB = FEW_ ? 1 : BN / SN;
+  __host__ __device__ static constexpr uint32_t col_s(int s, int b) {
+    return (FEW_ ? 32 : SN) * (2 * s + b);
+  }
+  __host__ __device__ static constexpr uint32_t col_o(int s) {
+    return FEW_ ? 128 + 32 * s : 4 * SN + OW * s;
+  }
+  static constexpr uint32_t TMEM_COLS = FEW_ ? 256 : 512;
   __host__ __device__ static constexpr uint32_t swz(uint32_t r) {
     return ((r * RB) >> 7) & (RB / 16 - 1);
   }
-  static_assert(col_o(2) <= TMEM_COLS, "tensor memory");
+  static_assert((FEW_ ? 192 : col_o(2)) <= TMEM_COLS, "tensor memory");
 };
 
 // A run of a unit's tiles.
@@ -98,7 +107,7 @@ struct TreeItem {
   int more;        // 0: the CTA's work has ended
   int b, hk;
   int row0, rows;  // of the key head's query rows
-  int split;       // copies of each row in a tile (1 or 2); 0: two tiles of rows
+  int split;       // copies of each row in a tile (1 or 2); 0: rows for both streams
   int L, key0;     // cached tokens, and the first one that any node sees
   int base0, ctx;  // key of the unit's first cache tile, and how many there are
   int t0, n;       // this run of its tiles
@@ -131,15 +140,33 @@ struct TreeParams {
   bool capped, wide;
 };
 
+// What a stream knows of its query rows (few rows).
+struct FewTables {
+  alignas(16) float neg[32];    // less the running maximum; +inf before the first
+  alignas(16) float alpha[32];  // what sums are rescaled by
+  alignas(16) float zero[32];
+  alignas(16) float slope[32];  // log2 units
+  alignas(16) float offset[4][32];  // per warp: the bias's share of a row in this tile, less its maximum
+  alignas(16) float part[4][32];    // per warp: largest scores, sums
+  float m[32], sum[32];
+  long long out[32];  // where a row's result goes
+  int depth[32], node[32], first_key[32];
+  int flag[4];
+  uint64_t meet;  // barrier of the stream's 128 softmax threads
+};
+
 template <class C>
 struct __align__(1024) TreeSmem {
-  uint8_t q[C::QSLOTS][2][C::Q_TILE];
+  uint8_t q[C::QSLOTS][C::QTILES][C::Q_TILE];
   uint8_t k[C::KSTAGES][C::KV_TILE];
   uint8_t v[C::VSTAGES][C::KV_TILE];
   uint8_t raw_k[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
   uint8_t raw_v[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
-  float merge[3 * BM / 2][kMergeStride];  // the parts of rows but the first
-  float2 stat[2 * BM];
+  alignas(1024) uint8_t prob[2][C::FEW ? BM * 64 : 16];  // few rows: P of each stream, a key's 32 rows in 64 bytes
+  // many rows: the parts of rows but the first
+  alignas(16) float merge[C::FEW ? 1 : 3 * BM / 2][kMergeStride];
+  float2 stat[C::FEW ? 1 : 2 * BM];
+  FewTables few[C::FEW ? 2 : 1];
   uint32_t line[2][kMostNodes][4];  // what a node sees of the tree
   int depth[2][kMostNodes];         // -1: no node
   int up[2][kMostNodes];            // scratch: parents, and 2^k-th ancestors
@@ -190,7 +217,7 @@ __host__ __device__ __forceinline__ unsigned tree_share(unsigned total, int ctas
 }
 
 // A CTA's place in its work.
-template <int BN>
+template <int BN, bool FEW>
 struct TreeCursor {
   TreeSeq s;
   int b, sub, tile;
@@ -224,7 +251,7 @@ struct TreeCursor {
     it.hk = sub / p.blocks;
     it.row0 = rb * kBlockRows;
     it.rows = min(p.rows - it.row0, kBlockRows);
-    it.split = it.rows > BM ? 0 : (it.rows > BM / 2 ? 1 : 2);
+    it.split = FEW ? (it.rows > 32 ? 0 : 1) : (it.rows > BM ? 0 : (it.rows > BM / 2 ? 1 : 2));
     it.L = s.L;
     it.key0 = s.key0;
     it.base0 = s.base0;
@@ -291,6 +318,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Two of a word's four codes (bytes 2 * HI and 2 * HI + 1) as a bf16 pair, exactly.
 template <int FMT, int HI>
 __device__ __forceinline__ uint32_t widen2(uint32_t w) {
@@ -344,15 +381,60 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int
   }
 }
 
-template <int FMT, int D, bool CHANGED>
+// Zeros in the rows of a value tile that nobody sees, whatever they hold, by a warp:
+// of rows [r0, r1) those outside [lo, hi), or where `node` >= 0 (the tree's node of
+// row 0) the places that are no node.
+template <class C>
+__device__ __forceinline__ void clear_rows(const TreeParams& p, TreeSmem<C>& sm, uint8_t* v, int r0,
+                                           int r1, int lo, int hi, int node, int slot, int lane) {
+  auto clear = [&](int from, int to) {
+    for (int e = from * C::CPB + lane; e < to * C::CPB; e += 32)
+#pragma unroll
+      for (int nb = 0; nb < C::NB; ++nb)
+        *reinterpret_cast<uint4*>(v + nb * C::KV_BLOCK + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+  };
+  bool any = false;
+  if (node < 0) {
+    if (C::Q8) return;  // done where codes are widened
+    any = lo > r0 || hi < r1;
+    if (any) {
+      clear(r0, min(lo, r1));
+      clear(max(hi, r0), r1);
+    }
+  } else {
+    for (int r = r0; r < r1; r += 32) {
+      const int at = node + r + lane;
+      unsigned gone = __ballot_sync(0xffffffffu, at < p.n && sm.depth[slot][at] < 0);
+      any = any || gone != 0;
+      for (; gone != 0; gone &= gone - 1) {
+        const int row = r + __ffs(gone) - 1;
+        clear(row, row + 1);
+      }
+    }
+  }
+  if (any) {
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+}
+
+}  // namespace
+}  // namespace attn
+
+#include "attn_tree_few.cuh"
+#include "attn_tree_many.cuh"
+
+namespace attn {
+namespace {
+
+template <class C, bool CHANGED>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ CUtensorMap tmkt,
                      const __grid_constant__ CUtensorMap tmvt, const TreeParams p) {
-  using C = TCfg<FMT, D>;
   using S = TreeSmem<C>;
-  constexpr int BN = C::BN, KSTAGES = C::KSTAGES, VSTAGES = C::VSTAGES, RAWS = C::RAWS;
+  constexpr int D = C::D, BN = C::BN, KSTAGES = C::KSTAGES, VSTAGES = C::VSTAGES, RAWS = C::RAWS;
   constexpr bool Q8 = C::Q8;
   extern __shared__ uint8_t smem_raw[];
   S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -371,6 +453,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_init(smem_u32(&sm.pv_done[i][e]), 1);
       }
       mbar_init(smem_u32(&sm.drain[i]), 1);
+      if constexpr (C::FEW) mbar_init(smem_u32(&sm.few[i].meet), BM);
       for (int r = 0; r < RAWS; ++r) {
         mbar_init(smem_u32(&sm.raw_full[i][r]), 1);
         mbar_init(smem_u32(&sm.raw_empty[i][r]), 4);
@@ -399,7 +482,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     prefetch_tmap(&tmvt);
   }
   if (warp == MMA_WARP) {
-    tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
+    tmem_alloc(smem_u32(&sm.tmem_base), C::TMEM_COLS);
     tmem_relinquish();
   }
 
@@ -469,169 +552,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   };
 
   if (warp >= MMA_WARP) {
-    // ---------------------------------------------------------------- MMA issuers
-    // A stream runs through its own parts u = 0, 1, ... of 64 keys (all items) in the
-    // order S(0), S(1), PV(0), S(2), PV(1), ...: S(u) goes to buffer u % 2 once PV(u - 2)
-    // has read P there, PV(u - 1) right after it, once its P is there.  A ring slot is
-    // released by one arrival per stream: a commit by a stream that used the tile, a
-    // plain arrival by one that did not.
     const int s = warp - MMA_WARP;
-    constexpr uint32_t IDESC_S = idesc_bf16_f32(BM, SN, false, false);
-    constexpr uint32_t IDESC_O = idesc_bf16_f32(BM, D, false, true);
-    constexpr uint32_t KV16 = C::KV_TILE >> 4, SUB16 = SN * C::RB >> 4;
-    const uint64_t dk = tree_sdesc(smem_u32(sm.k[0]), 16, 8 * C::RB, C::SWZ);
-    const uint64_t dv = tree_sdesc(smem_u32(sm.v[0]), C::KV_BLOCK, 8 * C::RB, C::SWZ);
-    auto qstep = [](int kk) {
-      return static_cast<uint32_t>((kk / C::KPB) * (C::Q_BLOCK >> 4) + (kk % C::KPB) * 2);
-    };
-    auto kstep = [](int kk) {
-      return static_cast<uint32_t>((kk / C::KPB) * (C::KV_BLOCK >> 4) + (kk % C::KPB) * 2);
-    };
-    const uint32_t t_o = tmem + C::col_o(s);
-    const bool leader = elect_one();
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
-      return ok;
-    };
-    auto v_wait = [&](uint32_t g) { return wait(&sm.v_full[g % VSTAGES], (g / VSTAGES) & 1); };
-    uint32_t u = 0;  // score products issued
-    // the last one still owes its PV product: of ring tile pg, part psub; whether it is
-    // its item's first, the last of its tile, the last of its item (then of pslot)
-    bool pending = false, pfirst = false, prelease = false, plast = false;
-    uint32_t pg = 0;
-    int psub = 0, pslot = 0, plo = 0, phi = 0, pnode = -1;
-    // zeros in the rows of a value tile that nobody sees, whatever they hold: rows of
-    // the part outside [plo, phi), of places that are no node
-    auto clear_rows = [&]() {
-      uint8_t* v = sm.v[pg % VSTAGES];
-      auto clear = [&](int lo, int hi) {
-        for (int e = lo * C::CPB + lane; e < hi * C::CPB; e += 32)
-#pragma unroll
-          for (int nb = 0; nb < C::NB; ++nb)
-            *reinterpret_cast<uint4*>(v + nb * C::KV_BLOCK + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-      };
-      bool any = false;
-      if (pnode < 0) {
-        if (Q8) return;  // done where codes are widened
-        const int r0 = psub * SN, r1 = r0 + SN;
-        any = plo > r0 || phi < r1;
-        if (any) {
-          clear(r0, min(plo, r1));
-          clear(max(phi, r0), r1);
-        }
-      } else {
-        for (int r = psub * SN; r < psub * SN + SN; r += 32) {
-          const int node = pnode + r + lane;
-          unsigned gone = __ballot_sync(0xffffffffu, node < p.n && sm.depth[pslot][node] < 0);
-          any = any || gone != 0;
-          for (; gone != 0; gone &= gone - 1) {
-            const int row = r + __ffs(gone) - 1;
-            clear(row, row + 1);
-          }
-        }
-      }
-      if (any) {
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-    };
-    auto flush_pv = [&]() {
-      if (!pending) return;
-      const uint32_t w = u - 1;
-      if (!v_wait(pg) || !wait(&sm.p_full[s][w & 1], (w >> 1) & 1)) return;
-      clear_rows();
-      tc_fence_after();
-      const uint64_t b = dv + (pg % VSTAGES) * KV16 + psub * SUB16;
-      const uint32_t t_p = tmem + C::col_s(s, w & 1);
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < SN / 16; ++kk)
-          mma_ts(t_o, t_p + kk * 8, b + C::RB * kk, IDESC_O, (!pfirst || kk > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&sm.pv_done[s][w & 1]));
-        if (prelease) tc_commit(smem_u32(&sm.v_empty[pg % VSTAGES]));
-        if (plast) mbar_arrive(smem_u32(&sm.item_empty[pslot]));
-      }
-      __syncwarp();
-      pending = false;
-    };
-    // waits for a barrier, with what is pending done first where that takes time
-    auto next_wait = [&](uint64_t* bar, uint32_t parity) {
-      if (pending && __shfl_sync(0xffffffffu, mbar_test(smem_u32(bar), parity) ? 1 : 0, 0) == 0)
-        flush_pv();
-      return wait(bar, parity);
-    };
-    uint32_t g0 = 0;
-    for (uint32_t items = 0; ok; ++items) {
-      const int slot = items & 1;
-      if (!next_wait(&sm.item_full[slot], (items >> 1) & 1)) break;
-      const TreeItem it = sm.item[slot];
-      if (it.more == 0) break;
-      const bool both = it.split == 0;
-      const uint64_t dq = tree_sdesc(smem_u32(sm.q[items % C::QSLOTS][both ? s : 0]), 16,
-                                     8 * C::RB, C::SWZ);
-      bool first = true;
-      for (int j = 0; j < it.n && ok; ++j) {
-        const uint32_t g = g0 + j;
-        const int t = it.t0 + j, parts = parts_of<C>(it, t, p.n);
-        int sub0 = 0, sub1 = parts;  // this stream's
-        if (!both) {
-          sub0 = C::NSUB == 1 ? 0 : s;
-          sub1 = C::NSUB == 1 ? ((j & 1) == s ? 1 : 0) : min(s + 1, parts);
-        }
-        if (!next_wait(&sm.k_full[g % KSTAGES], (g / KSTAGES) & 1)) break;
-        if (sub0 >= sub1) {
-          if (leader) mbar_arrive(smem_u32(&sm.k_empty[g % KSTAGES]));
-          if (next_wait(&sm.v_full[g % VSTAGES], (g / VSTAGES) & 1) && leader)
-            mbar_arrive(smem_u32(&sm.v_empty[g % VSTAGES]));
-          continue;
-        }
-        for (int sub = sub0; sub < sub1 && ok; ++sub) {
-          if (u > 1 && !wait(&sm.pv_done[s][u & 1], ((u >> 1) - 1) & 1)) break;
-          tc_fence_after();
-          const uint64_t b = dk + (g % KSTAGES) * KV16 + sub * SUB16;
-          const uint32_t t_s = tmem + C::col_s(s, u & 1);
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(t_s, dq + qstep(kk), b + kstep(kk), IDESC_S, kk > 0 ? 1u : 0u);
-            tc_commit(smem_u32(&sm.s_full[s][u & 1]));
-            if (sub + 1 == sub1) tc_commit(smem_u32(&sm.k_empty[g % KSTAGES]));
-          }
-          __syncwarp();
-          // (the pending one is u - 1 until u counts this one)
-          flush_pv();
-          if (!ok) break;
-          ++u;
-          pending = true;
-          pfirst = first;
-          first = false;
-          prelease = sub + 1 == sub1;
-          plast = false;
-          pg = g;
-          psub = sub;
-          pslot = slot;
-          const int base = it.base0 + t * BN;
-          plo = it.key0 - base;
-          phi = it.L - base;
-          pnode = t < it.ctx ? -1 : (t - it.ctx) * BN;
-        }
-      }
-      if (!ok) break;
-      if (leader) tc_commit(smem_u32(&sm.q_empty[items % C::QSLOTS]));
-      if (!first && pending) {
-        plast = true;
-      } else {
-        // nothing of this item is owed; what one before owes does not wait for more
-        if (leader) mbar_arrive(smem_u32(&sm.item_empty[slot]));
-        __syncwarp();
-        flush_pv();
-      }
-      g0 += it.n;
-    }
-    flush_pv();
-    if (!ok && leader) fail();
+    if constexpr (C::FEW)
+      ok = mma_few<C>(p, sm, tmem, s, lane);
+    else
+      ok = mma_many<C>(p, sm, tmem, s, lane);
+    if (!ok && lane == 0) fail();
     // every product issued by this warp completes before tensor memory is freed
-    if (leader) tc_commit(smem_u32(&sm.drain[s]));
+    if (elect_one()) tc_commit(smem_u32(&sm.drain[s]));
     __syncwarp();
     const int never = 0;
     mbar_wait(smem_u32(&sm.drain[s]), 0, p.limit_ns, &never);
@@ -647,7 +575,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const CUtensorMap* map = is_v ? &tmv : &tmk;
       const CUtensorMap* tree_map = is_v ? &tmvt : &tmkt;
       const bool runs = is_v ? p.run_v : p.run_k;
-      TreeCursor<BN> cur;
+      TreeCursor<BN, C::FEW> cur;
       cur.begin(p, start_b, start_off, count);
       TreeItem it;
       uint32_t cnt = 0;
@@ -695,7 +623,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp >= AUX_WARP) {
     // ---------------------------------------------------------------- rows, trees, codes
     const int tid = threadIdx.x - AUX_WARP * 32;
-    TreeCursor<BN> cur;
+    TreeCursor<BN, C::FEW> cur;
     cur.begin(p, start_b, start_off, count);
     int has[2] = {-1, -1};  // whose tree a slot's tables hold
     uint32_t cnt = 0, raws = 0;
@@ -769,13 +697,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int qslot = items % C::QSLOTS;
       if (!wait(&sm.q_empty[qslot], ((items / C::QSLOTS) & 1) ^ 1)) break;
       constexpr int CPR = D / 8;  // 16-byte chunks of a row
-      const int tiles = it.split == 0 ? 2 : 1;
-      const int lanes = it.split == 0 ? BM : BM / it.split;
+      const int tiles = it.split == 0 ? C::QTILES : 1;
+      const int lanes = C::FEW || it.split == 0 ? C::QROWS : C::QROWS / it.split;
       for (int s = 0; s < tiles; ++s) {
 #pragma unroll 8
-        for (int e = tid; e < BM * CPR; e += 128) {
+        for (int e = tid; e < C::QROWS * CPR; e += 128) {
           const int at = e / CPR, c = e % CPR;
-          const int r = s * BM + at % lanes;
+          const int r = s * BM + (at & (lanes - 1));
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
           if (r < it.rows) {
             const int row = it.row0 + r, g = row / p.n, i = row - g * p.n;
@@ -849,365 +777,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else {
-    // ---------------------------------------------------------------- softmax
-    const int s = warp >> 2, quarter = warp & 3;
-    const int at = quarter * 32 + lane;  // tensor-memory lane
-    const uint32_t base_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t tO = base_addr + C::col_o(s);
-    constexpr int OC = C::OW / 32;
-    uint32_t u = 0;  // parts of SN keys of this stream
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
-      return ok;
-    };
-    uint32_t joins = 0;
-    auto join = [&]() {
-      mbar_arrive(smem_u32(&sm.join_sync));
-      return wait(&sm.join_sync, joins++ & 1);
-    };
-    for (uint32_t items = 0; ok; ++items) {
-      const int slot = items & 1;
-      if (!wait(&sm.item_full[slot], (items >> 1) & 1)) break;
-      const TreeItem it = sm.item[slot];
-      if (it.more == 0) break;
-      const bool both = it.split == 0, twice = it.split == 2;
-      const int copy = twice ? at >> 6 : 0;
-      const int r = both ? s * BM + at : (twice ? at & 63 : at);
-      const bool valid = r < it.rows;
-      const bool active = __any_sync(0xffffffffu, valid);
-      const int row = it.row0 + (valid ? r : 0);
-      const int g = row / p.n, node = row - g * p.n, head = it.hk * p.G + g;
-      const int depth = max(sm.depth[slot][node], 0);
-      const bool alive = valid && sm.depth[slot][node] >= 0;
-      const float slope2 = CHANGED && p.slopes ? kLog2e * __ldg(p.slopes + head) : 0.f;
-      // position of the row's first visible key, for the window
-      const int first_key = p.window >= 0 ? it.L + depth - p.window : 0;
-      float m = -INFINITY, l = 0.f;
-      bool first = true;
-
-      // one part of a tile: NC of its 64 columns, from col0 on
-      auto part_of_tile = [&](auto nc, int t, int sub, float sc) {
-        constexpr int NC = decltype(nc)::value;
-        const int col0 = NC < SN ? copy * NC : 0;
-        const bool tree = t >= it.ctx;
-        // the key (or node) of column 0
-        const int base = (tree ? (t - it.ctx) * BN : it.base0 + t * BN) + sub * SN;
-        const uint32_t tS = base_addr + C::col_s(s, u & 1);
-        uint32_t x[NC / 32][32];
-#pragma unroll
-        for (int c = 0; c < NC / 32; ++c) tmem_ld32(tS + col0 + 32 * c, x[c]);
-        // the scale of 16 columns: of the tile's block that they lie in
-        auto scale_at = [&](int col, int kv) {
-          return __shfl_sync(0xffffffffu, sc, kv * 8 + ((sub * SN + col0 + col) >> p.T_log2));
-        };
-        float factor[NC / 16];
-#pragma unroll
-        for (int c = 0; c < NC / 16; ++c)
-          factor[c] = (Q8 ? scale_at(16 * c, 0) : 1.f) * (CHANGED && p.capped ? 1.f : p.scale_log2);
-        // (a factor of zero would make NaN of masked scores)
-        if constexpr (Q8 && !CHANGED) {
-#pragma unroll
-          for (int c = 0; c < NC / 16; ++c) factor[c] = fmaxf(factor[c], 0x1p-126f);
-        }
-        const int hi = it.L - base, lo = first_key - base;
-        const bool edge = tree || hi < SN || (p.window >= 0 && __any_sync(0xffffffffu, lo > 0));
-        float off = 0.f;
-        tmem_ld_wait(x[0]);
-#pragma unroll
-        for (int c = 1; c < NC / 32; ++c) reg_fence(x[c]);
-        if constexpr (CHANGED) {
-          // finished scores in log2 units, but for `off`
-          if (p.capped) {
-            float big = 0.f;
-#pragma unroll
-            for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                if constexpr (Q8) {
-                  float a, b;
-                  fma2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]),
-                       factor[2 * c + i / 16], factor[2 * c + i / 16], 0.f, 0.f);
-                  x[c][i] = __float_as_uint(a);
-                  x[c][i + 1] = __float_as_uint(b);
-                }
-                big = max3_abs(big, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-              }
-            const bool small = __all_sync(0xffffffffu, big <= p.cap.small);
-            if (small) {
-#pragma unroll
-              for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const float x0 = __uint_as_float(x[c][i]), x1 = __uint_as_float(x[c][i + 1]);
-                  float z0, z1, y0, y1;
-                  fma2(z0, z1, x0, x1, x0, x1, 0.f, 0.f);
-                  fma2(y0, y1, z0, z1, p.cap.poly[2], p.cap.poly[2], p.cap.poly[1], p.cap.poly[1]);
-                  fma2(y0, y1, z0, z1, y0, y1, p.cap.poly[0], p.cap.poly[0]);
-                  fma2(y0, y1, x0, x1, y0, y1, 0.f, 0.f);
-                  x[c][i] = __float_as_uint(y0);
-                  x[c][i + 1] = __float_as_uint(y1);
-                }
-            } else {
-              // cap * tanh(y) = cap - 2 cap / (1 + 2^(2 y log2(e))), in log2 units
-#pragma unroll
-              for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const float y = __uint_as_float(x[c][i]);
-                  float w = fmaf(-2.f * p.cap_log2, rcp(1.f + ex2(y * p.cap_in)), p.cap_log2);
-                  if (p.wide && fabsf(y) <= p.cap.small) {
-                    const float z = y * y;
-                    w = y * fmaf(z, fmaf(z, p.cap.poly[2], p.cap.poly[1]), p.cap.poly[0]);
-                  }
-                  x[c][i] = __float_as_uint(w);
-                }
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                x[c][i] = __float_as_uint(__uint_as_float(x[c][i]) * factor[2 * c + i / 16]);
-          }
-          if (p.slopes) {
-            if (tree) {
-              off = -slope2 * depth;
-#pragma unroll
-              for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  const int a = min(base + col0 + 32 * c + i, kMostNodes - 1);
-                  x[c][i] = __float_as_uint(fmaf(slope2, static_cast<float>(sm.depth[slot][a]),
-                                                 __uint_as_float(x[c][i])));
-                }
-            } else {
-              off = -slope2 * static_cast<float>(it.L + depth - base - col0);
-#pragma unroll
-              for (int c = 0; c < NC / 32; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  const float col = static_cast<float>(32 * c + i);
-                  float a, b;
-                  fma2(a, b, col, col + 1.f, slope2, slope2, __uint_as_float(x[c][i]),
-                       __uint_as_float(x[c][i + 1]));
-                  x[c][i] = __float_as_uint(a);
-                  x[c][i + 1] = __float_as_uint(b);
-                }
-            }
-          }
-        }
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < NC / 32; ++c) {
-            const int at_col = col0 + 32 * c;
-            const uint32_t see = tree ? sm.line[slot][node][(base + at_col) >> 5]
-                                      : below(hi - at_col) & ~below(lo - at_col);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(see & (1u << i))) x[c][i] = __float_as_uint(-INFINITY);
-          }
-        }
-        // the largest score, 16 columns of one scale at a time
-        float mt = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NC / 16; ++c) {
-          float m2[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              m2[e] = max3(m2[e], __uint_as_float(x[c >> 1][(c & 1) * 16 + i + 2 * e]),
-                           __uint_as_float(x[c >> 1][(c & 1) * 16 + i + 2 * e + 1]));
-          mt = fmaxf(mt, fmaxf(m2[0], m2[1]) * (CHANGED ? 1.f : factor[c]));
-        }
-        mt += off;
-        float alpha = 1.f;
-        if (mt > m + kRescale) {
-          alpha = ex2(m - mt);  // 0 when m = -inf
-          l *= alpha;
-          m = mt;
-        }
-        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-          // O is rescaled once the last product is done
-          if (!wait(&sm.pv_done[s][(u - 1) & 1], ((u - 1) >> 1) & 1)) return;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tO + c, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(tO + c, o);
-          }
-        }
-        const float neg_m = m == -INFINITY ? 0.f : off - m;
-        float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC / 32; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float f = factor[2 * c + half];
-            const float v = Q8 ? scale_at(32 * c + 16 * half, 1) : 1.f;
-#pragma unroll
-            for (int i = 16 * half; i < 16 * half + 16; i += 2) {
-              float a, b;
-              if constexpr (CHANGED)
-                add2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]), neg_m, neg_m);
-              else
-                fma2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]), f, f, neg_m,
-                     neg_m);
-              a = ex2(a);
-              b = ex2(b);
-              add2(l0, l1, l0, l1, a, b);
-              if constexpr (Q8) fma2(a, b, a, b, v, v, 0.f, 0.f);
-              pk[i >> 1] = pack_bf16x2(a, b);
-            }
-          }
-          tmem_st16(tS + (col0 >> 1) + 16 * c, pk);
-        }
-        l += l0 + l1;
-        if constexpr (NC < SN) {
-          uint32_t z[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) z[i] = 0u;
-          tmem_st16(tS + (16 - (col0 >> 1)), z);  // the other copy's columns
-        }
-        tmem_st_wait();
-      };
-
-      for (int j = 0; j < it.n && ok; ++j) {
-        const int t = it.t0 + j, parts = parts_of<C>(it, t, p.n);
-        int sub0 = 0, sub1 = parts;
-        if (!both) {
-          sub0 = C::NSUB == 1 ? 0 : s;
-          sub1 = C::NSUB == 1 ? ((j & 1) == s ? 1 : 0) : min(s + 1, parts);
-        }
-        if (sub0 >= sub1) continue;
-        float sc = 1.f;  // lane i: the scale of the tile's i-th block of keys, 8 + i: of values
-        if constexpr (Q8) {
-          if (t < it.ctx) {
-            const int base = it.base0 + t * BN, blk = (base >> p.T_log2) + (lane & 7);
-            sc = 0.f;
-            if (lane < 16 && (blk << p.T_log2) < min(it.L, base + BN) &&
-                ((blk + 1) << p.T_log2) > it.key0)
-              sc = __ldg((lane < 8 ? p.k_scale : p.v_scale) +
-                         (static_cast<long long>(it.b) * p.HK + it.hk) * p.num_blocks + blk);
-          }
-        }
-        for (int sub = sub0; sub < sub1; ++sub) {
-          if (!wait(&sm.s_full[s][u & 1], (u >> 1) & 1)) break;
-          tc_fence_after();
-          if (active) {
-            if (twice)
-              part_of_tile(std::integral_constant<int, 32>(), t, sub, sc);
-            else
-              part_of_tile(std::integral_constant<int, 64>(), t, sub, sc);
-            if (!ok) break;
-          }
-          first = false;
-          tc_fence_before();
-          mbar_arrive(smem_u32(&sm.p_full[s][u & 1]));
-          ++u;
-        }
-      }
-      if (!ok) break;
-
-      // ---------------------------------------------------------- the run's result
-      if (!first) {
-        if (!wait(&sm.pv_done[s][(u - 1) & 1], ((u - 1) >> 1) & 1)) break;
-        tc_fence_after();
-      }
-      if (!alive) {
-        m = -INFINITY;
-        l = 0.f;
-      }
-      float* part = p.part + ((static_cast<size_t>(blockIdx.x) * 2 + it.slot) * p.block_rows + r) *
-                                 (D + kPartTail);
-      const int split = twice ? 2 : 1;
-      const int pidx = s * split + copy;  // which part of the row (not both)
-      float weight = alive ? 1.f : 0.f, most = m, sum = l;
-      if (!both) {
-        sm.stat[threadIdx.x] = make_float2(m, l);
-        if (!join()) break;
-        most = -INFINITY;
-        const int step = twice ? 64 : BM, at0 = twice ? r : at;
-#pragma unroll 1
-        for (int e = at0; e < 2 * BM; e += step) most = fmaxf(most, sm.stat[e].x);
-        sum = 0.f;
-#pragma unroll 1
-        for (int e = at0; e < 2 * BM; e += step) {
-          const float2 x = sm.stat[e];
-          if (x.y > 0.f) sum = fmaf(x.y, ex2(x.x - most), sum);
-        }
-        weight = l > 0.f ? ex2(m - most) : 0.f;
-      }
-      if (it.whole) weight = sum > 0.f ? weight / sum : 0.f;
-      const bool writer = valid && (both || pidx == 0);
-      if (writer) {
-        if (!it.whole)
-          *reinterpret_cast<float2*>(part + D) = make_float2(most, sum);
-        else if (p.lse != nullptr)
-          p.lse[(static_cast<size_t>(it.b) * p.H + head) * p.n + node] =
-              sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
-      }
-      __nv_bfloat16* out = p.o + it.b * p.so.b + head * p.so.h + node * p.so.n;
-      const int lanes = twice ? 64 : BM;
-#pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
-        uint32_t o[16];
-        if (!first) tmem_ld16(tO + c, o);
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          o[i] = weight > 0.f && !first ? __float_as_uint(__uint_as_float(o[i]) * weight) : 0u;
-        if (!both) {
-          if (pidx > 0) {
-            uint4* to = reinterpret_cast<uint4*>(sm.merge[(pidx - 1) * lanes + r]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-          if (!join()) break;
-          if (pidx == 0) {
-#pragma unroll 1
-            for (int w = 0; w < 2 * split - 1; ++w) {
-              const float4* from = reinterpret_cast<const float4*>(sm.merge[w * lanes + r]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 y = from[e];
-                o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) + y.x);
-                o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) + y.y);
-                o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) + y.z);
-                o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) + y.w);
-              }
-            }
-          }
-        }
-        if (writer) {
-          if (it.whole) {
-            uint4* to = reinterpret_cast<uint4*>(out + c);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t* y = o + 8 * e;
-              to[e] = make_uint4(pack_bf16x2(__uint_as_float(y[0]), __uint_as_float(y[1])),
-                                 pack_bf16x2(__uint_as_float(y[2]), __uint_as_float(y[3])),
-                                 pack_bf16x2(__uint_as_float(y[4]), __uint_as_float(y[5])),
-                                 pack_bf16x2(__uint_as_float(y[6]), __uint_as_float(y[7])));
-            }
-          } else {
-            uint4* to = reinterpret_cast<uint4*>(part + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-        }
-        if (!both && !join()) break;
-        __syncwarp();
-      }
-      if (!ok) break;
-      tc_fence_before();
-      mbar_arrive(smem_u32(&sm.item_empty[slot]));
-    }
+    if constexpr (C::FEW)
+      ok = softmax_few<C, CHANGED>(p, sm, tmem, warp >> 2, warp & 3, lane);
+    else
+      ok = softmax_many<C, CHANGED>(p, sm, tmem, warp >> 2, warp & 3, lane);
     if (!ok) fail();
   }
 
@@ -1216,7 +789,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == MMA_WARP) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -1267,29 +840,33 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p,
         sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <int FMT, int D, bool CHANGED>
+template <class C, bool CHANGED>
 cudaError_t launch_tree_d(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
                           const LaunchCtx& ctx) {
-  using C = TCfg<FMT, D>;
   static_assert(sizeof(TreeSmem<C>) + 1024 <= 232448, "dynamic shared memory per CTA");
   const size_t smem = sizeof(TreeSmem<C>) + 1024;
-  cudaError_t err = cudaFuncSetAttribute(attn_tree_kernel<FMT, D, CHANGED>,
+  cudaError_t err = cudaFuncSetAttribute(attn_tree_kernel<C, CHANGED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  attn_tree_kernel<FMT, D, CHANGED>
+  attn_tree_kernel<C, CHANGED>
       <<<plan.ctas, NUM_THREADS, smem, ctx.stream>>>(maps[0], maps[1], maps[2], maps[3], p);
   if ((err = cudaGetLastError()) != cudaSuccess || plan.whole) return err;
   const long long rows = static_cast<long long>(p.B) * p.HK * p.rows;
-  return launch_dependent(attn_tree_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)),
+  return launch_dependent(attn_tree_join_kernel<C::D>, dim3(static_cast<unsigned>((rows + 7) / 8)),
                           dim3(256), 0, ctx.stream, p, plan.ctas);
 }
 
 template <int FMT, int D>
 cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
                              const LaunchCtx& ctx) {
-  return p.capped || p.slopes ? launch_tree_d<FMT, D, true>(p, maps, plan, ctx)
-                              : launch_tree_d<FMT, D, false>(p, maps, plan, ctx);
+  using Few = TCfg<FMT, D, true>;
+  using Many = TCfg<FMT, D, false>;
+  if (p.capped || p.slopes)
+    return plan.few ? launch_tree_d<Few, true>(p, maps, plan, ctx)
+                    : launch_tree_d<Many, true>(p, maps, plan, ctx);
+  return plan.few ? launch_tree_d<Few, false>(p, maps, plan, ctx)
+                  : launch_tree_d<Many, false>(p, maps, plan, ctx);
 }
 
 template <int FMT>
