@@ -1201,21 +1201,30 @@ int tree_decode_sizes(int B, int h, int h_kv, int n, int L_max, int d_k, int cac
     return ATTN_ERR_INVALID_ARG;
   if (!tc_head_size(d_k) || n > kMostNodes || L_max > kMostCached) return ATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(B) * h > (1LL << 24) / n) return ATTN_ERR_UNSUPPORTED;
-  // the kernel counts the visible cache's tiles over all sequences and key heads
-  // (and blocks of query rows) in 31 bits
-  const long long blocks = (static_cast<long long>(h / h_kv) * n + 255) / 256;
-  if (static_cast<long long>(B) * h_kv * blocks * (L_max / 64 + 4LL) > 0x7fffffffLL)
+  // the kernels count the visible cache's tiles of 16 keys or more, over all sequences
+  // and key heads (and tiles of query rows), in 31 bits
+  const long long tiles = (static_cast<long long>(h / h_kv) * n + 31) / 32;
+  if (static_cast<long long>(B) * h_kv * tiles > 0x7fffffffLL / (L_max / 16 + 8LL))
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 }  // namespace
 
+ScoredDecodePlan tree_few_plan(int B, int H, int HK, int n, int seen, int d, int elem_bytes,
+                               int num_sms) {
+  ScoredDecodePlan plan = scored_decode_plan(B, H, HK, n, seen, d, elem_bytes, num_sms);
+  // behind what the plan needs: the results of units that one warp took
+  const size_t units = static_cast<size_t>(B) * HK * plan.row_tiles;
+  plan.done_off = (plan.workspace_bytes / sizeof(float) + 3) / 4 * 4;
+  plan.workspace_bytes = (plan.done_off + units * plan.row_tile * (d + kPartTail)) * sizeof(float);
+  return plan;
+}
+
 TreePlan tree_plan(int B, int HK, int rows, int n, int L_max, int d, int window, int num_sms) {
   TreePlan plan;
   plan.blocks = (rows + 255) / 256;
   plan.block_rows = rows < 256 ? rows : 256;
-  plan.few = rows <= tree_few_rows();
-  const int kt = tree_tile_keys(d, plan.few);
+  const int kt = tree_tile_keys(d);
   plan.tree_tiles = (n + kt - 1) / kt;
   const long long units = static_cast<long long>(B) * HK * plan.blocks;
   // most tiles of a unit (a window may begin inside one)
@@ -1241,6 +1250,10 @@ size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int L_max
   if (tree_decode_sizes(B, h, h_kv, n, L_max, d_k, cache_format, window) != ATTN_OK) return 0;
   DeviceInfo* di = nullptr;
   if (device_info(&di) != ATTN_OK) return 0;
+  if (h / h_kv * n <= kFewTreeRows)
+    return tree_few_plan(B, h, h_kv, n, scored_seen(n, L_max, window), d_k,
+                         elem_bytes(cache_format), di->num_sms)
+        .workspace_bytes;
   return tree_plan(B, h_kv, h / h_kv * n, n, L_max, d_k, window, di->num_sms).workspace_bytes;
 }
 
@@ -1272,17 +1285,41 @@ int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, cons
   if (rc != ATTN_OK) return rc;
   DeviceInfo* di = nullptr;
   if ((rc = device_info(&di)) != ATTN_OK) return rc;
-  TreeDecodeProblem pb{q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, parents, o, lse, B, h,
-                       h_kv, n, L_max, d_k, cache_format, q8 ? block_tokens : 128, scale, softcap,
-                       slopes, cache_lens,
-                       window < L_max + n ? window : -1,  // (the tree's own keys are that far back too)
-                       st[0], st[1], st[2], st[3], st[4], st[5]};
+  // (the tree's own keys are that far back too)
+  const int near = window < L_max + n ? window : -1;
+  const LaunchCtx ctx = make_ctx(*di, stream);
+  CUtensorMap maps[4];
+  if (h / h_kv * n <= kFewTreeRows) {
+    const ScoredDecodePlan plan = tree_few_plan(B, h, h_kv, n, scored_seen(n, L_max, window), d_k,
+                                                e1, di->num_sms);
+    if (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace))
+      return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i)
+      if ((rc = encode_4d_bytes(&maps[i], i ? v_cache : k_cache, d_k * e1, L_max, h_kv, B,
+                                st[3 + i], e1, plan.tile_keys)) != ATTN_OK)
+        return rc;
+    const ScoredDecodeProblem pb{q, k_cache, v_cache, k_scale, v_scale, o, lse, B, h, h_kv, n,
+                                 L_max, d_k, q8 ? block_tokens : 128, scale, softcap, slopes,
+                                 cache_lens, near, st[0], st[3], st[4], st[5]};
+    const TreeOwn tree{parents, k_tree, v_tree, st[1], st[2]};
+    float* ws = static_cast<float*>(workspace);
+    const cudaError_t e =
+        cache_format == ATTN_CACHE_BF16   ? launch_tree_few_bf16(pb, maps, plan, ws, ctx, tree)
+        : cache_format == ATTN_CACHE_E4M3 ? launch_tree_few_e4m3(pb, maps, plan, ws, ctx, tree)
+                                          : launch_tree_few_int8(pb, maps, plan, ws, ctx, tree);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches.fetch_add(2);
+    return ATTN_OK;
+  }
+  const TreeDecodeProblem pb{q, k_tree, v_tree, k_cache, v_cache, k_scale, v_scale, parents, o, lse,
+                             B, h, h_kv, n, L_max, d_k, cache_format, q8 ? block_tokens : 128,
+                             scale, softcap, slopes, cache_lens, near, st[0], st[1], st[2], st[3],
+                             st[4], st[5]};
   const TreePlan plan = tree_plan(B, h_kv, h / h_kv * n, n, L_max, d_k, window, di->num_sms);
   if (plan.workspace_bytes > 0 &&
       (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
     return ATTN_ERR_INVALID_ARG;
-  CUtensorMap maps[4];
-  const int kt = tree_tile_keys(d_k, plan.few);
+  const int kt = tree_tile_keys(d_k);
   for (int i = 0; i < 2; ++i) {
     const void* cache = i ? v_cache : k_cache;
     rc = q8 ? encode_4d_bytes(&maps[i], cache, d_k, L_max, h_kv, B, st[3 + i], 1, kt)
@@ -1292,7 +1329,6 @@ int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, cons
         ATTN_OK)
       return rc;
   }
-  const LaunchCtx ctx = make_ctx(*di, stream);
   const cudaError_t e =
       cache_format == ATTN_CACHE_BF16   ? launch_decode_tree_bf16(pb, maps, plan, workspace, ctx)
       : cache_format == ATTN_CACHE_E4M3 ? launch_decode_tree_e4m3(pb, maps, plan, workspace, ctx)

@@ -57,6 +57,12 @@
 // its own copies only, never for another warp, and memory stays busy while it
 // computes.
 //
+// TREE: the queries are the nodes of trees of drafted tokens (attn_decode_tree) with
+// few rows to a key head.  Node i stands at L + depth_i and sees the whole cache; what
+// it sees of its tree, its ancestors' own keys, is taken by the second kernel, which
+// needs nothing of the first for that and does it while the first still runs.  Every
+// unit's result therefore goes through the workspace.
+//
 // Measured (the floor is the visible cache at the rate of a plain copy, 6.7 TB/s):
 // 4 sequences of 65 to 131 thousand tokens, 32 query heads on 8, d = 128, e4m3,
 // distance bias: 132 us (floor 121); the same with a bf16 cache at its floor, 235
@@ -111,6 +117,12 @@ struct ScoredDecParams {
   int warps, units;
   bool whole;
   float scale, softcap;
+  // TREE
+  const int* parents;  // [B][n_q]
+  const __nv_bfloat16* k_tree;
+  const __nv_bfloat16* v_tree;
+  RowStrides skt, svt;
+  float* done;  // [unit][query rows][D + kPartTail]: results of units that one warp took
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -261,20 +273,21 @@ struct SeqTiles {
               // group of it) crosses a scale block
   int tiles;
 };
-template <int KT>
+template <int KT, bool TREE>
 __device__ __forceinline__ SeqTiles seq_tiles(const ScoredDecParams& p, int b) {
   SeqTiles s;
   s.L = p.L_max;
   if (p.cache_lens != nullptr) s.L = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
-  s.key0 = p.window >= 0 ? max(s.L - p.n_q - p.window, 0) : 0;
+  s.key0 = p.window >= 0 ? max(s.L - (TREE ? 0 : p.n_q) - p.window, 0) : 0;
   s.base0 = s.key0 & ~(KT - 1);
   s.tiles = (s.L - s.base0 + KT - 1) / KT;
+  if (TREE && s.key0 >= s.L) s.tiles = 0;  // (a window of no key before the tree)
   return s;
 }
 
 // A place in a warp's work: a tile of a unit = b * subs + sub, sub = key head *
 // row_tiles + row tile.
-template <int KT>
+template <int KT, bool TREE>
 struct Cursor {
   SeqTiles s;
   int unit, b, sub, tile;
@@ -285,7 +298,7 @@ struct Cursor {
     sub = u - nb * subs;
     if (nb != b) {
       b = nb;
-      s = seq_tiles<KT>(p, b);
+      s = seq_tiles<KT, TREE>(p, b);
     }
   }
   // the next unit of this warp; with skip, the next one that has tiles
@@ -313,7 +326,40 @@ __device__ __forceinline__ unsigned share_of(unsigned total, int warps) {
   return each < kMinTiles ? kMinTiles : each;
 }
 
-template <int FMT, int D, int NR, bool BIG>
+// The depths of a tree's nodes `lane` and `lane + 32` (0 where there is no node), by a
+// warp: after round k of pointer doubling a node knows how far its 2^k-th ancestor is.
+__device__ __forceinline__ int2 node_depths(const int* parents, int n, int lane) {
+  int up[2], depth[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = lane + 32 * e;
+    up[e] = i < n ? __ldg(parents + i) : -2;
+    if (up[e] < -1 || up[e] >= i) up[e] = -2;
+    depth[e] = up[e] >= 0 ? 1 : 0;
+  }
+  for (int r = 1; r < n; r *= 2) {
+    int far[2], further[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int from = max(up[e], 0);
+      const int d0 = __shfl_sync(0xffffffffu, depth[0], from & 31),
+                d1 = __shfl_sync(0xffffffffu, depth[1], from & 31),
+                u0 = __shfl_sync(0xffffffffu, up[0], from & 31),
+                u1 = __shfl_sync(0xffffffffu, up[1], from & 31);
+      far[e] = from < 32 ? d0 : d1;
+      further[e] = from < 32 ? u0 : u1;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (up[e] >= 0) {
+        depth[e] += far[e];
+        up[e] = further[e];
+      }
+  }
+  return make_int2(up[0] == -1 ? depth[0] : 0, up[1] == -1 ? depth[1] : 0);
+}
+
+template <int FMT, int D, int NR, bool BIG, bool TREE>
 __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
     attn_decode_scored_kernel(const __grid_constant__ CUtensorMap tmk,
                               const __grid_constant__ CUtensorMap tmv, const ScoredDecParams p) {
@@ -335,13 +381,13 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   const int w = blockIdx.x * DW + warp;
 
   // ---- where this warp's work begins, and how many tiles it is
-  Cursor<KT> cur;
+  Cursor<KT, TREE> cur;
   cur.b = -1;
   int count = 0;
   if (p.whole) {
     if (w >= p.warps) return;
     cur.at_unit(p, subs, w);
-    Cursor<KT> c = cur;
+    Cursor<KT, TREE> c = cur;
     do count += c.s.tiles;
     while (c.next(p, subs, false));
   } else {
@@ -351,7 +397,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
     const int per = (p.B + DW * 32 - 1) / (DW * 32);
     const int seq0 = min(static_cast<int>(threadIdx.x) * per, p.B), seq1 = min(seq0 + per, p.B);
     unsigned sum = 0;
-    for (int b = seq0; b < seq1; ++b) sum += seq_tiles<KT>(p, b).tiles;
+    for (int b = seq0; b < seq1; ++b) sum += seq_tiles<KT, TREE>(p, b).tiles;
     sum *= subs;
     unsigned run = sum;
 #pragma unroll
@@ -372,7 +418,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
       unsigned at = run - sum;
       for (int b = seq0; b < seq1; ++b) {
         p.first[b] = at;
-        at += seq_tiles<KT>(p, b).tiles * subs;
+        at += seq_tiles<KT, TREE>(p, b).tiles * subs;
       }
       if (threadIdx.x == 0) p.first[p.B] = total;
     }
@@ -389,7 +435,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
     unsigned at = chunk > 0 ? upto[chunk - 1] : 0u;
     int b = chunk * per;
     for (;; ++b) {
-      cur.s = seq_tiles<KT>(p, b);
+      cur.s = seq_tiles<KT, TREE>(p, b);
       const unsigned here = static_cast<unsigned>(cur.s.tiles) * subs;
       if (begin - at < here || b + 1 >= p.B) break;
       at += here;
@@ -405,7 +451,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   const uint32_t ring = smem_u32(ring_at);
   const uint32_t bars = smem_u32(&full[warp][0]);
   const int never = 0;
-  Cursor<KT> ahead = cur;  // where the next copy is from (lane 0)
+  Cursor<KT, TREE> ahead = cur;  // where the next copy is from (lane 0)
   if (ahead.s.tiles == 0) ahead.next(p, subs, true);
   auto fill = [&](uint32_t slot) {  // the next tile into a slot (one lane)
     const uint32_t bar = bars + 8 * slot;
@@ -464,7 +510,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   const int rows = min(p.G * p.n_q - rt * ROWS, ROWS);  // query rows of this unit
   const int L = cur.s.L, key0 = cur.s.key0, base0 = cur.s.base0 + cur.tile * KT;
   // first key that the last query sees
-  const int last_lo = p.window >= 0 ? max(L - 1 - p.window, 0) : 0;
+  const int last_lo = p.window >= 0 ? max(L - 1 + (TREE ? p.n_q : 0) - p.window, 0) : 0;
   const long long bk = static_cast<long long>(b) * p.HK + hk;
   const float* ksp = Q8 ? p.k_scale + bk * p.num_blocks : nullptr;
   const float* vsp = Q8 ? p.v_scale + bk * p.num_blocks : nullptr;
@@ -492,6 +538,9 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   uint32_t qa[MQ][C::KS][4];
   float qscale[MQ][2], nslope[MQ][2];
   int pos[MQ][2];
+  int2 depths = make_int2(0, 0);
+  if (TREE && (biased || p.window >= 0))
+    depths = node_depths(p.parents + static_cast<long long>(b) * p.n_q, p.n_q, lane);
 #pragma unroll
   for (int m = 0; m < MQ; ++m) {
 #pragma unroll
@@ -533,7 +582,13 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
           }
         }
       }
-      pos[m][r] = in ? L - p.n_q + qi : -1;
+      if (TREE) {
+        const int d0 = __shfl_sync(0xffffffffu, depths.x, qi & 31),
+                  d1 = __shfl_sync(0xffffffffu, depths.y, qi & 31);
+        pos[m][r] = L + (qi < 32 ? d0 : d1);
+      } else {
+        pos[m][r] = in ? L - p.n_q + qi : -1;
+      }
       nslope[m][r] = p.slopes != nullptr && in ? -__ldg(p.slopes + head) * kLog2e : 0.f;
     }
   }
@@ -596,7 +651,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
 
     // every row sees every key of the tile, unless it is an edge of the cache
     // or of the window
-    const bool edge = base + KT > L - p.n_q + 1 || base < last_lo;
+    const bool edge = base + KT > L - (TREE ? 0 : p.n_q - 1) || base < last_lo;
 
     float lv[NG];  // the groups' value scales in log2 units (a scale of 0: -inf)
 #pragma unroll
@@ -652,7 +707,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
         }
         if (edge) {
           // keys [lo, hi) of the tile are visible
-          const int hi = pos[m][r] + 1 - base;
+          const int hi = (TREE ? L : pos[m][r] + 1) - base;
           const int lo = p.window >= 0 ? max(pos[m][r] - p.window, key0) - base : -base;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -831,6 +886,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
     }
   const bool whole_unit = it - seg_it == cur.s.tiles;
   float* part = p.part + (static_cast<long long>(w) * 2 + (leads ? 0 : 1)) * ROWS * (D + kPartTail);
+  if (TREE && whole_unit) part = p.done + static_cast<long long>(cur.unit) * ROWS * (D + kPartTail);
 #pragma unroll
   for (int x = 0; x < NR; ++x) {
 #pragma unroll
@@ -842,7 +898,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
       const float from = Q8 ? __shfl_sync(0xffffffffu, mv_run[x / 2][x & 1], 8 * t + 4 * c) - kLift : mm;
       const int row = x * 8 + 2 * t + c;
       if (row >= rows) continue;
-      if (whole_unit) {
+      if (!TREE && whole_unit) {
         const int gr = rt * ROWS + row;
         const int in_group = p.n_q == 1 ? gr : gr / p.n_q, qi = gr - in_group * p.n_q;
         const int head = hk * p.G + in_group;
@@ -886,12 +942,99 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   }
 }
 
+// What a node sees of its tree: O relative to 2^m, its values in the lanes.
+template <int E>
+struct OwnPart {
+  float a[E], m, l;
+  bool node;
+};
+template <int D>
+__device__ __forceinline__ OwnPart<(D + 31) / 32> tree_part(const ScoredDecParams& p, int b, int hk,
+                                                            int in_group, int node, int lane) {
+  constexpr int E = (D + 31) / 32;
+  OwnPart<E> own;
+  const int* parents = p.parents + static_cast<long long>(b) * p.n_q;
+  const int up0 = lane < p.n_q ? __ldg(parents + lane) : -2,
+            up1 = lane + 32 < p.n_q ? __ldg(parents + lane + 32) : -2;
+  auto up = [&](int at) {
+    const int x = __shfl_sync(0xffffffffu, at < 32 ? up0 : up1, at & 31);
+    return x < -1 || x >= at ? -2 : x;
+  };
+  int root = node;
+  while (root >= 0) root = up(root);
+  own.node = root == -1;
+  own.m = -INFINITY;
+  own.l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) own.a[e] = 0.f;
+  if (!own.node) return own;
+  const int head = hk * p.G + in_group;
+  const __nv_bfloat16* q = p.q + b * p.sq.b + head * p.sq.h + node * p.sq.n;
+  const __nv_bfloat16* k = p.k_tree + b * p.skt.b + hk * p.skt.h;
+  const __nv_bfloat16* v = p.v_tree + b * p.svt.b + hk * p.svt.h;
+  const float slope = p.slopes != nullptr ? __ldg(p.slopes + head) : 0.f;
+  float x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = lane + 32 * e < D ? __bfloat162float(q[lane + 32 * e]) : 0.f;
+  // four ancestors at a time, the node itself first
+  int at = node, back = 0;
+  while (at >= 0 && (p.window < 0 || back <= p.window)) {
+    int who[4];
+    float key[4][E], val[4][E], s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      who[i] = at >= 0 && (p.window < 0 || back + i <= p.window) ? at : -1;
+      if (at >= 0) at = up(at);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const bool in = who[i] >= 0 && lane + 32 * e < D;
+        key[i][e] = in ? __bfloat162float(k[who[i] * p.skt.n + lane + 32 * e]) : 0.f;
+        val[i][e] = in ? __bfloat162float(v[who[i] * p.svt.n + lane + 32 * e]) : 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[i] = fmaf(x[e], key[i][e], s[i]);
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], w);
+    float top = own.m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] *= p.scale;
+      if (p.softcap > 0.f) s[i] = p.softcap * tanhf(s[i] / p.softcap);
+      s[i] = who[i] >= 0 ? (s[i] - slope * static_cast<float>(back + i)) * kLog2e : -INFINITY;
+      top = fmaxf(top, s[i]);
+    }
+    const float alpha = ex2(own.m - top);  // 0 at first
+    own.m = top;
+    own.l *= alpha;
+#pragma unroll
+    for (int e = 0; e < E; ++e) own.a[e] *= alpha;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w = ex2(s[i] - top);
+      own.l += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) own.a[e] = fmaf(w, val[i][e], own.a[e]);
+    }
+    back += 4;
+  }
+  return own;
+}
+
 // Joins the parts of a query row.  ONE_WARP: a warp per row, eight rows to a
 // CTA, for the few parts that a unit has when there are many units; else a CTA
 // of eight warps per row, each warp every eighth part.  Units that one warp of
 // the first kernel covered are complete; units without keys get O = 0 and LSE
 // = -inf here.
-template <int D, int ROWS, bool ONE_WARP>
+template <int D, int ROWS, bool ONE_WARP, bool TREE>
 __global__ void __launch_bounds__(256)
     attn_decode_scored_merge_kernel(const ScoredDecParams p, unsigned total_rows) {
   constexpr int E = (D + 31) / 32;
@@ -903,17 +1046,34 @@ __global__ void __launch_bounds__(256)
   const int gr = id - bk * R, b = bk / static_cast<unsigned>(p.HK), hk = bk - b * p.HK;
   const int rt = gr / ROWS, row = gr - rt * ROWS;
   const unsigned subs = p.HK * p.row_tiles, sub = hk * p.row_tiles + rt;
+  OwnPart<E> own_part;  // TREE: of the row's ancestors
+  if (TREE && id < total_rows && (ONE_WARP || warp == 0))
+    own_part = tree_part<D>(p, b, hk, gr / p.n_q, gr % p.n_q, lane);
   grid_dependency_wait();  // the parts are complete
   if (id >= total_rows) return;
-  const unsigned here = p.first[b], next = p.first[b + 1], share = share_of(p.first[p.B], p.warps);
-  const unsigned tiles = (next - here) / subs, u0 = here + tiles * sub;
-  const unsigned w0 = u0 / share;
-  const int n = tiles > 0 ? static_cast<int>((u0 + tiles - 1) / share - w0) + 1 : 0;
-  if (n == 1) return;
+  unsigned w0 = 0, u0 = 0, share = 1;
+  int n;
+  if (TREE && p.whole) {
+    int L = p.L_max;
+    if (p.cache_lens != nullptr) L = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
+    n = L > 0 && p.window != 0 ? 1 : 0;
+  } else {
+    const unsigned here = p.first[b], next = p.first[b + 1];
+    share = share_of(p.first[p.B], p.warps);
+    const unsigned tiles = (next - here) / subs;
+    u0 = here + tiles * sub;
+    w0 = u0 / share;
+    n = tiles > 0 ? static_cast<int>((u0 + tiles - 1) / share - w0) + 1 : 0;
+  }
+  if (!TREE && n == 1) return;
   // part i: the first warp's run may have begun before the unit
   const float* part = p.part + (static_cast<long long>(w0) * 2 * ROWS + row) * (D + kPartTail);
   constexpr int NEXT = 2 * ROWS * (D + kPartTail);
-  const int late = share * w0 < u0 ? ROWS * (D + kPartTail) : 0;
+  const int late = share * w0 < u0 && !(TREE && n == 1) ? ROWS * (D + kPartTail) : 0;
+  if (TREE && n == 1) {
+    const long long unit = static_cast<long long>(b) * subs + sub;
+    part = p.done + (unit * ROWS + row) * (D + kPartTail);
+  }
   auto part_at = [&](int i) { return part + static_cast<long long>(i) * NEXT + (i == 0 ? late : 0); };
   const int first = ONE_WARP ? 0 : warp;
   constexpr int STEP = ONE_WARP ? 1 : 8;
@@ -977,7 +1137,25 @@ __global__ void __launch_bounds__(256)
   }
   const int head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
   __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
-  const float fac = value_factor(from, mb), inv = (ll > 0.f ? 1.f / ll : 0.f) * fac;
+  const float fac = value_factor(from, mb);
+  if (TREE) {
+    // the ancestors' part joins the cache's; a place that is no node sees neither
+    const bool cached = ll > 0.f && own_part.node;
+    const float most = fmaxf(cached ? mm : -INFINITY, own_part.node ? own_part.m : -INFINITY);
+    const float w1 = cached ? ex2(mm - most) : 0.f, w2 = own_part.node ? ex2(own_part.m - most) : 0.f;
+    const float sum = fmaf(w1, ll, w2 * own_part.l), inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float y = own_part.node ? w2 * own_part.a[e] : 0.f;
+      if (cached) y = fmaf(w1, a[e] * fac * fac, y);
+      if (lane + 32 * e < D) out[lane + 32 * e] = __float2bfloat16_rn(y * inv);
+    }
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
+          sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
+    return;
+  }
+  const float inv = (ll > 0.f ? 1.f / ll : 0.f) * fac;
 #pragma unroll
   for (int e = 0; e < E; ++e)
     if (lane + 32 * e < D) out[lane + 32 * e] = __float2bfloat16_rn(a[e] * fac * inv);
@@ -986,45 +1164,45 @@ __global__ void __launch_bounds__(256)
         ll > 0.f ? (mm + __log2f(ll)) * kLn2 : -INFINITY;
 }
 
-template <int FMT, int D, int NR, bool BIG>
+template <int FMT, int D, int NR, bool BIG, bool TREE>
 cudaError_t launch_scored_decode_rows(const ScoredDecParams& p, const CUtensorMap* maps,
                                       const LaunchCtx& ctx) {
   const size_t smem = DW * DCfg<FMT, D, NR, BIG>::RING + 1024;
-  auto* kernel = attn_decode_scored_kernel<FMT, D, NR, BIG>;
+  auto* kernel = attn_decode_scored_kernel<FMT, D, NR, BIG, TREE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   kernel<<<(p.warps + DW - 1) / DW, DW * 32, smem, ctx.stream>>>(maps[0], maps[1], p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.whole) return cudaSuccess;
+  if (!TREE && p.whole) return cudaSuccess;
   const unsigned rows = static_cast<unsigned>(p.B) * p.HK * p.G * p.n_q;
   // parts of a unit, on average
-  if (p.warps / p.units < 8)
-    return launch_dependent(attn_decode_scored_merge_kernel<D, NR * 8, true>, dim3((rows + 7) / 8),
+  if (p.whole || p.warps / p.units < 8)
+    return launch_dependent(attn_decode_scored_merge_kernel<D, NR * 8, true, TREE>, dim3((rows + 7) / 8),
                             dim3(256), 0, ctx.stream, p, rows);
-  return launch_dependent(attn_decode_scored_merge_kernel<D, NR * 8, false>, dim3(rows), dim3(256),
+  return launch_dependent(attn_decode_scored_merge_kernel<D, NR * 8, false, TREE>, dim3(rows), dim3(256),
                           0, ctx.stream, p, rows);
 }
 
-template <int FMT, int D>
+template <int FMT, int D, bool TREE>
 cudaError_t launch_scored_decode_d(const ScoredDecParams& p, const CUtensorMap* maps, int row_tile,
                                    const LaunchCtx& ctx) {
   constexpr int rb = D * (FMT == kCacheBf16 ? 2 : 1);
   switch (row_tile) {
     case 8:
       if constexpr (scored_big_tiles(rb, 1, false)) {
-        if (!p.whole) return launch_scored_decode_rows<FMT, D, 1, true>(p, maps, ctx);
+        if (!p.whole) return launch_scored_decode_rows<FMT, D, 1, true, TREE>(p, maps, ctx);
       }
-      return launch_scored_decode_rows<FMT, D, 1, false>(p, maps, ctx);
-    case 16: return launch_scored_decode_rows<FMT, D, 2, false>(p, maps, ctx);
-    default: return launch_scored_decode_rows<FMT, D, 4, false>(p, maps, ctx);
+      return launch_scored_decode_rows<FMT, D, 1, false, TREE>(p, maps, ctx);
+    case 16: return launch_scored_decode_rows<FMT, D, 2, false, TREE>(p, maps, ctx);
+    default: return launch_scored_decode_rows<FMT, D, 4, false, TREE>(p, maps, ctx);
   }
 }
 
-template <int FMT>
+template <int FMT, bool TREE = false>
 cudaError_t launch_scored_decode_fmt(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
                                      const ScoredDecodePlan& plan, float* workspace,
-                                     const LaunchCtx& ctx) {
+                                     const LaunchCtx& ctx, const TreeOwn* tree = nullptr) {
   ScoredDecParams p;
   p.q = static_cast<const __nv_bfloat16*>(pb.q);
   p.k_scale = pb.k_scale;
@@ -1061,11 +1239,19 @@ cudaError_t launch_scored_decode_fmt(const ScoredDecodeProblem& pb, const CUtens
   p.status = ctx.status;
   p.units = pb.B * pb.HK * plan.row_tiles;
   p.whole = plan.whole;
+  if (TREE) {
+    p.parents = tree->parents;
+    p.k_tree = static_cast<const __nv_bfloat16*>(tree->k);
+    p.v_tree = static_cast<const __nv_bfloat16*>(tree->v);
+    p.skt = tree->sk;
+    p.svt = tree->sv;
+    p.done = workspace + plan.done_off;
+  }
   switch (pb.d) {
-    case 16: return launch_scored_decode_d<FMT, 16>(p, maps, plan.row_tile, ctx);
-    case 32: return launch_scored_decode_d<FMT, 32>(p, maps, plan.row_tile, ctx);
-    case 64: return launch_scored_decode_d<FMT, 64>(p, maps, plan.row_tile, ctx);
-    case 128: return launch_scored_decode_d<FMT, 128>(p, maps, plan.row_tile, ctx);
+    case 16: return launch_scored_decode_d<FMT, 16, TREE>(p, maps, plan.row_tile, ctx);
+    case 32: return launch_scored_decode_d<FMT, 32, TREE>(p, maps, plan.row_tile, ctx);
+    case 64: return launch_scored_decode_d<FMT, 64, TREE>(p, maps, plan.row_tile, ctx);
+    case 128: return launch_scored_decode_d<FMT, 128, TREE>(p, maps, plan.row_tile, ctx);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -356,7 +356,6 @@ struct TreeDecodeProblem {
 };
 struct TreePlan {
   int ctas;
-  bool few;        // the kernel for few query rows of a key head
   bool whole;      // a CTA takes whole units (sequence, key head, block of query rows)
   int blocks;      // of query rows of a key head
   int block_rows;  // rows of a part in the workspace
@@ -365,8 +364,7 @@ struct TreePlan {
   size_t workspace_bytes;
 };
 TreePlan tree_plan(int B, int HK, int rows, int n, int L_max, int d, int window, int num_sms);
-int tree_tile_keys(int d, bool few);
-int tree_few_rows();  // of a key head, for the kernel for few rows
+int tree_tile_keys(int d);
 int tree_min_tiles();
 // maps: the key and the value cache with a box of a tile's rows (bf16: swizzled as
 // the operand of a product; 8 bits: as bytes), then the tree's keys and values.
@@ -404,6 +402,7 @@ struct ScoredDecodePlan {
   int warps;   // that share the units, or the list of their tiles
   size_t part_off;  // floats before the partial results in the workspace
   size_t workspace_bytes;
+  size_t done_off = 0;  // of a tree's nodes: floats before the results of whole units
 };
 // The kernel's shapes, for cache rows of `row_bytes` and `row_tile` query rows:
 // whether it uses big tiles, keys of one tile, resident warps per SM, least
@@ -418,6 +417,26 @@ int scored_decode_min_tiles();
 // seen: the most keys one call can read per sequence.
 ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int d, int elem_bytes,
                                     int num_sms);
+// The same for few nodes of a tree of drafted tokens (n_q of them, 64 query rows of
+// a key head at most), with what they see of the tree.
+struct TreeOwn {
+  const int* parents;  // [B, n_q]
+  const void* k;       // bf16 [B, HK, n_q, d]
+  const void* v;
+  RowStrides sk, sv;
+};
+constexpr int kFewTreeRows = 64;
+ScoredDecodePlan tree_few_plan(int B, int H, int HK, int n, int seen, int d, int elem_bytes,
+                               int num_sms);
+cudaError_t launch_tree_few_bf16(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                 const ScoredDecodePlan& plan, float* workspace,
+                                 const LaunchCtx& ctx, const TreeOwn& tree);
+cudaError_t launch_tree_few_e4m3(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                 const ScoredDecodePlan& plan, float* workspace,
+                                 const LaunchCtx& ctx, const TreeOwn& tree);
+cudaError_t launch_tree_few_int8(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                 const ScoredDecodePlan& plan, float* workspace,
+                                 const LaunchCtx& ctx, const TreeOwn& tree);
 cudaError_t launch_decode_scored_bf16(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
                                       const ScoredDecodePlan& plan, float* workspace,
                                       const LaunchCtx& ctx);

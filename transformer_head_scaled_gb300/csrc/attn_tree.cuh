@@ -59,47 +59,39 @@ constexpr int KLOAD_WARP = 12;
 constexpr int VLOAD_WARP = 13;
 constexpr int MMA_WARP = 14;   // and 15
 constexpr int NUM_THREADS = 512;
+constexpr uint32_t TMEM_COLS = 512;
 constexpr int SN = 64;  // keys of one score product
 constexpr float kRescale = 8.0f;  // a running maximum is kept until a score exceeds it by 2^8
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMergeStride = 20;  // floats: 16 columns of a part's row, four apart in the banks
 
-// Shapes.  FEW: for key heads of at most kFewRows query rows (attn_tree_few.cuh).
-constexpr int kFewRows = 64;
-template <int FMT_, int D_, bool FEW_>
+template <int FMT_, int D_>
 struct TCfg {
   static constexpr int FMT = FMT_, D = D_;
-  static constexpr bool Q8 = FMT_ != kCacheBf16, FEW = FEW_;
-  static constexpr int BN = D_ == 128 && !FEW_ ? 64 : 128;  // keys per tile
+  static constexpr bool Q8 = FMT_ != kCacheBf16;
+  static constexpr int BN = D_ == 128 ? 64 : 128;  // keys per tile
   static constexpr uint32_t RB = (D_ < 64 ? D_ : 64) * 2;   // bytes of a row in one block
   static constexpr int NB = D_ > 64 ? D_ / 64 : 1;
   static constexpr uint32_t SWZ = RB == 128 ? 2u : (RB == 64 ? 4u : 6u);
   static constexpr int KPB = RB / 32;
   static constexpr int CPB = RB / 16;  // 16-byte chunks of a block row
-  static constexpr int QROWS = FEW_ ? kFewRows : BM, QTILES = FEW_ ? 1 : 2;
-  static constexpr int QSLOTS = D_ == 128 && (Q8 || !FEW_) ? 1 : 2;
-  static constexpr uint32_t Q_TILE = QROWS * D_ * 2, Q_BLOCK = QROWS * RB;
+  static constexpr int QSLOTS = D_ == 128 ? 1 : 2;
+  static constexpr uint32_t Q_TILE = BM * D_ * 2, Q_BLOCK = BM * RB;
   static constexpr uint32_t KV_TILE = BN * D_ * 2, KV_BLOCK = BN * RB;
   static constexpr uint32_t RAW_TILE = BN * D_;  // codes
   // ring stages: of bf16 tiles, and of tiles of codes
-  static constexpr int WIDE = KV_TILE >= 32768 ? 2 : (KV_TILE >= 16384 ? 4 : 6);
-  static constexpr int KSTAGES = Q8 ? (KV_TILE >= 32768 ? 1 : WIDE / 2) : WIDE;
-  static constexpr int VSTAGES = Q8 ? (KV_TILE >= 32768 ? 2 : (WIDE == 4 ? 3 : WIDE / 2)) : WIDE;
-  static constexpr int RAWS = Q8 ? (KV_TILE >= 32768 ? 2 : (WIDE == 4 ? 3 : WIDE)) : 1;
+  static constexpr int KSTAGES = D_ >= 64 ? (Q8 ? 2 : 4) : (Q8 ? 4 : 6);
+  static constexpr int VSTAGES = D_ >= 64 && Q8 ? 3 : KSTAGES;
+  static constexpr int RAWS = Q8 ? (D_ >= 64 ? 3 : 6) : 1;
   static constexpr uint32_t OW = D_ < 32 ? 32 : D_;
-  static constexpr int NSUB = FEW_ ? 1 : BN / SN;
-  __host__ __device__ static constexpr uint32_t col_s(int s, int b) {
-    return (FEW_ ? 32 : SN) * (2 * s + b);
-  }
-  __host__ __device__ static constexpr uint32_t col_o(int s) {
-    return FEW_ ? 128 + 32 * s : 4 * SN + OW * s;
-  }
-  static constexpr uint32_t TMEM_COLS = FEW_ ? 256 : 512;
+  static constexpr int NSUB = BN / SN;
+  __host__ __device__ static constexpr uint32_t col_s(int s, int b) { return SN * (2 * s + b); }
+  __host__ __device__ static constexpr uint32_t col_o(int s) { return 4 * SN + OW * s; }
   __host__ __device__ static constexpr uint32_t swz(uint32_t r) {
     return ((r * RB) >> 7) & (RB / 16 - 1);
   }
-  static_assert((FEW_ ? 192 : col_o(2)) <= TMEM_COLS, "tensor memory");
+  static_assert(col_o(2) <= TMEM_COLS, "tensor memory");
 };
 
 // A run of a unit's tiles.
@@ -107,7 +99,7 @@ struct TreeItem {
   int more;        // 0: the CTA's work has ended
   int b, hk;
   int row0, rows;  // of the key head's query rows
-  int split;       // copies of each row in a tile (1 or 2); 0: rows for both streams
+  int split;       // copies of each row in a tile (1 or 2); 0: two tiles of rows
   int L, key0;     // cached tokens, and the first one that any node sees
   int base0, ctx;  // key of the unit's first cache tile, and how many there are
   int t0, n;       // this run of its tiles
@@ -140,33 +132,15 @@ struct TreeParams {
   bool capped, wide;
 };
 
-// What a stream knows of its query rows (few rows).
-struct FewTables {
-  alignas(16) float neg[32];    // less the running maximum; +inf before the first
-  alignas(16) float alpha[32];  // what sums are rescaled by
-  alignas(16) float zero[32];
-  alignas(16) float slope[32];  // log2 units
-  alignas(16) float offset[4][32];  // per warp: the bias's share of a row in this tile, less its maximum
-  alignas(16) float part[4][32];    // per warp: largest scores, sums
-  float m[32], sum[32];
-  long long out[32];  // where a row's result goes
-  int depth[32], node[32], first_key[32];
-  int flag[4];
-  uint64_t meet;  // barrier of the stream's 128 softmax threads
-};
-
 template <class C>
 struct __align__(1024) TreeSmem {
-  uint8_t q[C::QSLOTS][C::QTILES][C::Q_TILE];
+  uint8_t q[C::QSLOTS][2][C::Q_TILE];
   uint8_t k[C::KSTAGES][C::KV_TILE];
   uint8_t v[C::VSTAGES][C::KV_TILE];
   uint8_t raw_k[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
   uint8_t raw_v[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
-  alignas(1024) uint8_t prob[2][C::FEW ? BM * 64 : 16];  // few rows: P of each stream, a key's 32 rows in 64 bytes
-  // many rows: the parts of rows but the first
-  alignas(16) float merge[C::FEW ? 1 : 3 * BM / 2][kMergeStride];
-  float2 stat[C::FEW ? 1 : 2 * BM];
-  FewTables few[C::FEW ? 2 : 1];
+  float merge[3 * BM / 2][kMergeStride];  // the parts of rows but the first
+  float2 stat[2 * BM];
   uint32_t line[2][kMostNodes][4];  // what a node sees of the tree
   int depth[2][kMostNodes];         // -1: no node
   int up[2][kMostNodes];            // scratch: parents, and 2^k-th ancestors
@@ -176,7 +150,7 @@ struct __align__(1024) TreeSmem {
   uint64_t raw_full[2][C::RAWS], raw_empty[2][C::RAWS];  // keys, values
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // stream, buffer
   uint64_t drain[2];
-  uint64_t aux_sync, join_sync;  // barriers of the auxiliary and of the softmax threads
+  uint64_t aux_sync, join_sync;  // barriers of the auxiliary and of the softmax warps
   unsigned warp_sum[NUM_THREADS / 32];
   unsigned total;
   int start_b;
@@ -217,7 +191,7 @@ __host__ __device__ __forceinline__ unsigned tree_share(unsigned total, int ctas
 }
 
 // A CTA's place in its work.
-template <int BN, bool FEW>
+template <int BN>
 struct TreeCursor {
   TreeSeq s;
   int b, sub, tile;
@@ -251,7 +225,7 @@ struct TreeCursor {
     it.hk = sub / p.blocks;
     it.row0 = rb * kBlockRows;
     it.rows = min(p.rows - it.row0, kBlockRows);
-    it.split = FEW ? (it.rows > 32 ? 0 : 1) : (it.rows > BM ? 0 : (it.rows > BM / 2 ? 1 : 2));
+    it.split = it.rows > BM ? 0 : (it.rows > BM / 2 ? 1 : 2);
     it.L = s.L;
     it.key0 = s.key0;
     it.base0 = s.base0;
@@ -285,6 +259,23 @@ struct TreeCursor {
     return true;
   }
 };
+
+// mbar_wait with all but the first test in one place of the code: with many waits it
+// would not fit the instruction cache otherwise.
+__device__ __noinline__ bool mbar_wait_on(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                          const volatile int* abort) {
+  return mbar_wait(bar, parity, limit_ns, abort);
+}
+__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, uint64_t limit_ns,
+                                                const volatile int* abort) {
+  return mbar_try_wait(bar, parity) || mbar_wait_on(bar, parity, limit_ns, abort);
+}
+
+// One arrival for a whole warp, behind what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(bar);
+}
 
 __device__ __forceinline__ uint64_t tree_sdesc(uint32_t smem_addr, uint32_t lbo_bytes,
                                                uint32_t sbo_bytes, uint32_t swz) {
@@ -350,34 +341,41 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-// A tile of codes to bf16 in the layout of a swizzled copy, by the 128 threads of
-// the auxiliary warps; rows outside [lo, hi) become zeros.
+// Half (0 or 1) of a tile of codes to bf16 in the layout of a swizzled copy, by a warp;
+// rows outside [lo, hi) become zeros.  Four chunks of codes are in flight at a time, in a loop:
+// all of them side by side would crowd the instruction cache.
 template <class C>
-__device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int tid, int lo,
-                                           int hi) {
+__device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int half, int lane,
+                                           int lo, int hi) {
   constexpr int CPR = C::D / 16;  // 16-code chunks of a row
-  constexpr int N = C::BN * CPR / 128;
-  uint4 w[N];
+  constexpr int N = C::BN / 2 * CPR / 32, M = N < 4 ? N : 4;
+  constexpr int STEP = 32 / CPR;  // rows from one of a lane's chunks to the next
+  const int c = lane % CPR;
+  uint8_t* to = out + (2 * c / C::CPB) * C::KV_BLOCK;
+  const int c0 = 2 * c % C::CPB;
+  // (the two halves of a 256-byte row would meet in the same banks)
+  const bool turn = C::D == 128 && (c & 4);
+  int row = half * (C::BN / 2) + lane / CPR;
+#pragma unroll 1
+  for (int e = 0; e < N; e += M) {
+    uint4 w[M];
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const int i = tid + e * 128, row = i / CPR, c = i % CPR;
-    const int at = C::D == 128 ? c ^ (row & 7) : c;
-    w[e] = *reinterpret_cast<const uint4*>(raw + row * C::D + at * 16);
-  }
+    for (int i = 0; i < M; ++i) {
+      const int r = row + i * STEP, at = C::D == 128 ? c ^ (r & 7) : c;
+      w[i] = *reinterpret_cast<const uint4*>(raw + r * C::D + at * 16);
+    }
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const int i = tid + e * 128, row = i / CPR, c = i % CPR;
-    uint4 a = make_uint4(widen2<C::FMT, 0>(w[e].x), widen2<C::FMT, 1>(w[e].x),
-                         widen2<C::FMT, 0>(w[e].y), widen2<C::FMT, 1>(w[e].y));
-    uint4 b = make_uint4(widen2<C::FMT, 0>(w[e].z), widen2<C::FMT, 1>(w[e].z),
-                         widen2<C::FMT, 0>(w[e].w), widen2<C::FMT, 1>(w[e].w));
-    if (row < lo || row >= hi) a = b = make_uint4(0u, 0u, 0u, 0u);
-    uint8_t* to = out + (2 * c / C::CPB) * C::KV_BLOCK + row * C::RB;
-    const int c0 = 2 * c % C::CPB, x = C::swz(row);
-    // (the two halves of a 256-byte row would meet in the same banks)
-    const bool turn = C::D == 128 && (c & 4);
-    *reinterpret_cast<uint4*>(to + (((turn ? c0 + 1 : c0) ^ x) << 4)) = turn ? b : a;
-    *reinterpret_cast<uint4*>(to + (((turn ? c0 : c0 + 1) ^ x) << 4)) = turn ? a : b;
+    for (int i = 0; i < M; ++i, row += STEP) {
+      if (row < lo || row >= hi) w[i] = make_uint4(0u, 0u, 0u, 0u);  // (a code of 0 is the number 0)
+      const uint4 a = make_uint4(widen2<C::FMT, 0>(w[i].x), widen2<C::FMT, 1>(w[i].x),
+                                 widen2<C::FMT, 0>(w[i].y), widen2<C::FMT, 1>(w[i].y));
+      const uint4 b = make_uint4(widen2<C::FMT, 0>(w[i].z), widen2<C::FMT, 1>(w[i].z),
+                                 widen2<C::FMT, 0>(w[i].w), widen2<C::FMT, 1>(w[i].w));
+      uint8_t* dst = to + row * C::RB;
+      const int x = C::swz(row);
+      *reinterpret_cast<uint4*>(dst + (((turn ? c0 + 1 : c0) ^ x) << 4)) = turn ? b : a;
+      *reinterpret_cast<uint4*>(dst + (((turn ? c0 : c0 + 1) ^ x) << 4)) = turn ? a : b;
+    }
   }
 }
 
@@ -421,7 +419,6 @@ __device__ __forceinline__ void clear_rows(const TreeParams& p, TreeSmem<C>& sm,
 }  // namespace
 }  // namespace attn
 
-#include "attn_tree_few.cuh"
 #include "attn_tree_many.cuh"
 
 namespace attn {
@@ -437,37 +434,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   constexpr int D = C::D, BN = C::BN, KSTAGES = C::KSTAGES, VSTAGES = C::VSTAGES, RAWS = C::RAWS;
   constexpr bool Q8 = C::Q8;
   extern __shared__ uint8_t smem_raw[];
-  S& sm = *reinterpret_cast<S*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                ~static_cast<uintptr_t>(1023));
+  // at a 1024-byte boundary (an offset, so that the compiler still knows the address
+  // space: generic accesses and their 64-bit addresses cost more than the arithmetic)
+  S& sm = *reinterpret_cast<S*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const volatile int* abort = &sm.abort;
   grid_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sm.item_full[i]), 128);
-      mbar_init(smem_u32(&sm.item_empty[i]), 2 * BM + 2);  // softmax threads, MMA warps
+      mbar_init(smem_u32(&sm.item_full[i]), 4);  // one arrival per warp, here and below
+      mbar_init(smem_u32(&sm.item_empty[i]), 8 + 2);  // softmax threads, MMA warps
       for (int e = 0; e < 2; ++e) {
         mbar_init(smem_u32(&sm.s_full[i][e]), 1);
-        mbar_init(smem_u32(&sm.p_full[i][e]), BM);
+        mbar_init(smem_u32(&sm.p_full[i][e]), 4);
         mbar_init(smem_u32(&sm.pv_done[i][e]), 1);
       }
       mbar_init(smem_u32(&sm.drain[i]), 1);
-      if constexpr (C::FEW) mbar_init(smem_u32(&sm.few[i].meet), BM);
       for (int r = 0; r < RAWS; ++r) {
         mbar_init(smem_u32(&sm.raw_full[i][r]), 1);
-        mbar_init(smem_u32(&sm.raw_empty[i][r]), 4);
+        mbar_init(smem_u32(&sm.raw_empty[i][r]), 2);
       }
     }
-    mbar_init(smem_u32(&sm.aux_sync), 128);
-    mbar_init(smem_u32(&sm.join_sync), 2 * BM);
+    mbar_init(smem_u32(&sm.aux_sync), 4);
+    mbar_init(smem_u32(&sm.join_sync), 8);
     for (int i = 0; i < C::QSLOTS; ++i) mbar_init(smem_u32(&sm.q_empty[i]), 2);
     for (int i = 0; i < KSTAGES; ++i) {
-      mbar_init(smem_u32(&sm.k_full[i]), Q8 ? 4 : 1);
+      mbar_init(smem_u32(&sm.k_full[i]), Q8 ? 2 : 1);
       mbar_init(smem_u32(&sm.k_empty[i]), 2);  // both streams
     }
     for (int i = 0; i < VSTAGES; ++i) {
-      mbar_init(smem_u32(&sm.v_full[i]), Q8 ? 4 : 1);
+      mbar_init(smem_u32(&sm.v_full[i]), Q8 ? 2 : 1);
       mbar_init(smem_u32(&sm.v_empty[i]), 2);
     }
     sm.abort = 0;
@@ -482,7 +479,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     prefetch_tmap(&tmvt);
   }
   if (warp == MMA_WARP) {
-    tmem_alloc(smem_u32(&sm.tmem_base), C::TMEM_COLS);
+    tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
     tmem_relinquish();
   }
 
@@ -553,16 +550,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (warp >= MMA_WARP) {
     const int s = warp - MMA_WARP;
-    if constexpr (C::FEW)
-      ok = mma_few<C>(p, sm, tmem, s, lane);
-    else
-      ok = mma_many<C>(p, sm, tmem, s, lane);
+    ok = mma_many<C>(p, sm, tmem, s, lane);
     if (!ok && lane == 0) fail();
     // every product issued by this warp completes before tensor memory is freed
     if (elect_one()) tc_commit(smem_u32(&sm.drain[s]));
     __syncwarp();
     const int never = 0;
-    mbar_wait(smem_u32(&sm.drain[s]), 0, p.limit_ns, &never);
+    mbar_wait_small(smem_u32(&sm.drain[s]), 0, p.limit_ns, &never);
   } else if (warp >= KLOAD_WARP) {
     // ---------------------------------------------------------------- copies
     if (lane == 0 && count > 0) {
@@ -575,7 +569,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const CUtensorMap* map = is_v ? &tmv : &tmk;
       const CUtensorMap* tree_map = is_v ? &tmvt : &tmkt;
       const bool runs = is_v ? p.run_v : p.run_k;
-      TreeCursor<BN, C::FEW> cur;
+      TreeCursor<BN> cur;
       cur.begin(p, start_b, start_off, count);
       TreeItem it;
       uint32_t cnt = 0;
@@ -583,7 +577,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int stop = Q8 ? min(it.t0 + it.n, it.ctx) : it.t0 + it.n;
         for (int t = it.t0; t < stop; ++t) {
           const uint32_t at = cnt % ST;
-          ok = mbar_wait(smem_u32(&empty[at]), ((cnt / ST) & 1) ^ 1, p.limit_ns, abort);
+          ok = mbar_wait_small(smem_u32(&empty[at]), ((cnt / ST) & 1) ^ 1, p.limit_ns, abort);
           if (!ok) break;
           const uint32_t bar = smem_u32(&full[at]);
           if constexpr (Q8) {
@@ -616,92 +610,53 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int never = 0;  // the copies under way land before shared memory goes away
         for (uint32_t i = 0; i < ST; ++i) {
           const uint32_t uses = cnt / ST + (i < cnt % ST ? 1u : 0u);
-          if (uses > 0) mbar_wait(smem_u32(&full[i]), (uses - 1) & 1, p.limit_ns, &never);
+          if (uses > 0) mbar_wait_small(smem_u32(&full[i]), (uses - 1) & 1, p.limit_ns, &never);
         }
       }
     }
   } else if (warp >= AUX_WARP) {
     // ---------------------------------------------------------------- rows, trees, codes
-    const int tid = threadIdx.x - AUX_WARP * 32;
-    TreeCursor<BN, C::FEW> cur;
+    const int aw = warp - AUX_WARP, tid = aw * 32 + lane;
+    TreeCursor<BN> cur;
     cur.begin(p, start_b, start_off, count);
     int has[2] = {-1, -1};  // whose tree a slot's tables hold
     uint32_t cnt = 0, raws = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = mbar_wait(smem_u32(bar), parity, p.limit_ns, abort);
+      if (ok)
+        ok = __all_sync(0xffffffffu, mbar_wait_small(smem_u32(bar), parity, p.limit_ns, abort));
       return ok;
     };
     uint32_t syncs = 0;
     auto sync = [&]() {
-      mbar_arrive(smem_u32(&sm.aux_sync));
+      warp_arrive(smem_u32(&sm.aux_sync));
       return wait(&sm.aux_sync, syncs++ & 1);
     };
-    uint32_t copied[2] = {}, filled[2] = {};  // ring slots last filled by a copy; tiles so far
+    uint32_t copied = 0, phase = 0;  // ring slots that this warp copied to last, and when
+    const bool small = p.n <= 32;  // every warp has all the nodes
     for (uint32_t items = 0;; ++items) {
       const int slot = items & 1;
+      const int me = small ? lane : tid;  // this thread's node
+      int up = -2;
+      if (cur.left > 0 && has[slot] != cur.b && me < p.n)
+        up = __ldg(p.parents + static_cast<long long>(cur.b) * p.n + me);
       if (!wait(&sm.item_empty[slot], ((items >> 1) & 1) ^ 1)) break;
       TreeItem it;
       const bool more = cur.next(p, it);
       if (more && !it.whole) it.slot = items == 0 ? 0 : 1;
       if (tid == 0) sm.item[slot] = it;
       if (!more) {
-        mbar_arrive(smem_u32(&sm.item_full[slot]));
+        warp_arrive(smem_u32(&sm.item_full[slot]));
         break;
-      }
-      if (has[slot] != it.b) {
-        has[slot] = it.b;
-        // ancestors by pointer doubling: after round k a node knows 2^k of them
-        int up = -2;
-        if (tid < p.n) {
-          up = __ldg(p.parents + static_cast<long long>(it.b) * p.n + tid);
-          if (up < -1 || up >= tid) up = -2;
-        }
-        const int parent = up;
-        uint32_t line[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) line[w] = tid >> 5 == w ? 1u << (tid & 31) : 0u;
-        for (int r = 0; r < p.rounds && ok; ++r) {
-          sm.up[0][tid] = up;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) sm.line[slot][tid][w] = line[w];
-          if (!sync()) break;
-          if (up >= 0) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) line[w] |= sm.line[slot][up][w];
-            up = sm.up[0][up];
-          }
-          sync();
-        }
-        const bool node = up == -1;
-        const int depth =
-            __popc(line[0]) + __popc(line[1]) + __popc(line[2]) + __popc(line[3]) - 1;
-        sm.up[1][tid] = parent;
-        if (!sync()) break;
-        if (node && p.window >= 0 && p.window < depth) {
-          // only the nearest ancestors
-#pragma unroll
-          for (int w = 0; w < 4; ++w) line[w] = 0u;
-          int a = tid;
-          for (int k = 0; k <= p.window; ++k) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              if (a >> 5 == w) line[w] |= 1u << (a & 31);
-            a = sm.up[1][a];
-          }
-        }
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sm.line[slot][tid][w] = node ? line[w] : 0u;
-        sm.depth[slot][tid] = node ? depth : -1;
       }
       // the query rows, each `split` times
       const int qslot = items % C::QSLOTS;
       if (!wait(&sm.q_empty[qslot], ((items / C::QSLOTS) & 1) ^ 1)) break;
       constexpr int CPR = D / 8;  // 16-byte chunks of a row
-      const int tiles = it.split == 0 ? C::QTILES : 1;
-      const int lanes = C::FEW || it.split == 0 ? C::QROWS : C::QROWS / it.split;
+      const int tiles = it.split == 0 ? 2 : 1;
+      const int lanes = it.split == 0 ? BM : BM / it.split;
       for (int s = 0; s < tiles; ++s) {
-#pragma unroll 8
-        for (int e = tid; e < C::QROWS * CPR; e += 128) {
+#pragma unroll 4
+        for (int e = tid; e < BM * CPR; e += 128) {
           const int at = e / CPR, c = e % CPR;
           const int r = s * BM + (at & (lanes - 1));
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -716,71 +671,139 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(smem_u32(&sm.item_full[slot]));
-      if constexpr (Q8) {
-        for (int t = it.t0; t < it.t0 + it.n && ok; ++t, ++cnt) {
-          const uint32_t from = raws % RAWS, rph = (raws / RAWS) & 1;
-          const int key = it.base0 + t * BN;
+      if (has[slot] != it.b) {
+        // ancestors by pointer doubling: after round k a node knows 2^k of them
+        has[slot] = it.b;
+        if (up < -1 || up >= me) up = -2;
+        const int parent = up;
+        if (small) {
+          uint32_t line = me < p.n ? 1u << lane : 0u;
+          for (int r = 0; r < p.rounds; ++r) {
+            const int from = max(up, 0);
+            const uint32_t above = __shfl_sync(0xffffffffu, line, from);
+            const int next = __shfl_sync(0xffffffffu, up, from);
+            if (up >= 0) {
+              line |= above;
+              up = next;
+            }
+          }
+          const bool node = up == -1;
+          const int depth = node ? __popc(line) - 1 : -1;
+          if (p.window >= 0 && p.window < 31) {
+            // only the nearest ancestors
+            uint32_t near = 0u;
+            for (int k = 0, at = lane; k <= p.window; ++k) {
+              if (at >= 0) near |= 1u << at;
+              const int next = __shfl_sync(0xffffffffu, parent, max(at, 0));
+              at = at >= 0 ? next : at;
+            }
+            line &= near;
+          }
+          if (!node) line = 0u;
+          if (aw == 0) {
+            sm.depth[slot][lane] = depth;
+            sm.line[slot][lane][0] = line;
+          } else {
+            sm.depth[slot][tid] = -1;
+            sm.line[slot][lane][aw] = 0u;
+          }
+        } else {
+          uint32_t line[4];
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t stages = kv ? VSTAGES : KSTAGES, at = cnt % stages;
-            const uint32_t ph = ((cnt / stages) & 1) ^ 1;
-            uint64_t* full = kv ? sm.v_full : sm.k_full;
-            uint8_t* to = kv ? sm.v[at] : sm.k[at];
-            if (!wait(kv ? &sm.v_empty[at] : &sm.k_empty[at], ph)) break;
-            copied[kv] &= ~(1u << at);
-            ++filled[kv];
-            if (t < it.ctx) {
-              if (!wait(&sm.raw_full[kv][from], rph)) break;
-              widen_tile<C>(kv ? sm.raw_v[from] : sm.raw_k[from], to, tid,
-                            kv ? it.key0 - key : 0, kv ? it.L - key : BN);
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(smem_u32(&sm.raw_empty[kv][from]));
-                mbar_arrive(smem_u32(&full[at]));
-              }
-            } else if (lane == 0) {
-              // the tree's own keys are bf16 already
-              if (tid == 0) {
-                const uint32_t bar = smem_u32(&full[at]);
+          for (int w = 0; w < 4; ++w) line[w] = aw == w ? 1u << lane : 0u;
+          for (int r = 0; r < p.rounds && ok; ++r) {
+            sm.up[0][tid] = up;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) sm.line[slot][tid][w] = line[w];
+            if (!sync()) break;
+            if (up >= 0) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) line[w] |= sm.line[slot][up][w];
+              up = sm.up[0][up];
+            }
+            sync();
+          }
+          const bool node = up == -1;
+          const int depth =
+              __popc(line[0]) + __popc(line[1]) + __popc(line[2]) + __popc(line[3]) - 1;
+          sm.up[1][tid] = parent;
+          if (!sync()) break;
+          if (node && p.window >= 0 && p.window < depth) {
+            // only the nearest ancestors
+#pragma unroll
+            for (int w = 0; w < 4; ++w) line[w] = 0u;
+            int a = tid;
+            for (int k = 0; k <= p.window; ++k) {
+#pragma unroll
+              for (int w = 0; w < 4; ++w)
+                if (a >> 5 == w) line[w] |= 1u << (a & 31);
+              a = sm.up[1][a];
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) sm.line[slot][tid][w] = node ? line[w] : 0u;
+          sm.depth[slot][tid] = node ? depth : -1;
+        }
+      }
+      warp_arrive(smem_u32(&sm.item_full[slot]));
+      if constexpr (Q8) {
+        // two warps take the keys, two the values, half a tile each
+        const int kv = aw & 1, half = aw >> 1;
+        const uint32_t stages = kv ? VSTAGES : KSTAGES;
+        uint64_t* full = kv ? sm.v_full : sm.k_full;
+        uint64_t* empty = kv ? sm.v_empty : sm.k_empty;
+        for (int t = it.t0; t < it.t0 + it.n; ++t, ++cnt) {
+          const uint32_t at = cnt % stages, ph = (cnt / stages) & 1;
+          uint8_t* to = kv ? sm.v[at] : sm.k[at];
+          if (!wait(&empty[at], ph ^ 1)) break;
+          if (t < it.ctx) {
+            const uint32_t from = raws % RAWS;
+            if (!wait(&sm.raw_full[kv][from], (raws / RAWS) & 1)) break;
+            ++raws;
+            const int key = it.base0 + t * BN;
+            widen_tile<C>(kv ? sm.raw_v[from] : sm.raw_k[from], to, half, lane,
+                          kv ? it.key0 - key : 0, kv ? it.L - key : BN);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&sm.raw_empty[kv][from]));
+              mbar_arrive(smem_u32(&full[at]));
+            }
+            copied &= ~(1u << at);
+          } else {
+            // the tree's own keys are bf16 already
+            if (lane == 0) {
+              const uint32_t bar = smem_u32(&full[at]);
+              if (half == 0) {
                 mbar_arrive_expect_tx(bar, C::KV_TILE);
 #pragma unroll
                 for (int nb = 0; nb < C::NB; ++nb)
                   tma_load_4d(smem_u32(to) + nb * C::KV_BLOCK, kv ? &tmvt : &tmkt, bar, 64 * nb,
                               (t - it.ctx) * BN, it.hk, it.b);
-                copied[kv] |= 1u << at;
               } else {
-                mbar_arrive(smem_u32(&full[at]));
+                mbar_arrive(bar);
               }
             }
-            __syncwarp();
+            if (half == 0) {
+              copied |= 1u << at;
+              phase = (phase & ~(1u << at)) | (ph << at);
+            }
           }
-          if (t < it.ctx) ++raws;
+          __syncwarp();
         }
         if (!ok) break;
       }
     }
     if (!ok && lane == 0) {
       fail();
-      if (Q8 && tid == 0) {
-        const int never = 0;  // the copies under way land before shared memory goes away
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint32_t stages = kv ? VSTAGES : KSTAGES;
-          for (uint32_t i = 0; i < stages; ++i) {
-            const uint32_t uses = filled[kv] / stages + (i < filled[kv] % stages ? 1u : 0u);
-            if ((copied[kv] >> i) & 1u)
-              mbar_wait(smem_u32(kv ? &sm.v_full[i] : &sm.k_full[i]), (uses - 1) & 1, p.limit_ns,
-                        &never);
-          }
-        }
-      }
+      const int never = 0;  // the copies under way land before shared memory goes away
+      for (uint32_t i = 0; copied >> i != 0; ++i)
+        if ((copied >> i) & 1u)
+          mbar_wait_small(smem_u32(aw & 1 ? &sm.v_full[i] : &sm.k_full[i]), (phase >> i) & 1u,
+                          p.limit_ns, &never);
     }
   } else {
-    if constexpr (C::FEW)
-      ok = softmax_few<C, CHANGED>(p, sm, tmem, warp >> 2, warp & 3, lane);
-    else
-      ok = softmax_many<C, CHANGED>(p, sm, tmem, warp >> 2, warp & 3, lane);
+    ok = softmax_many<C, CHANGED>(p, sm, tmem, warp >> 2, warp & 3, lane);
     if (!ok) fail();
   }
 
@@ -789,7 +812,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == MMA_WARP) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    tmem_dealloc(tmem, TMEM_COLS);
   }
 }
 
@@ -860,13 +883,9 @@ cudaError_t launch_tree_d(const TreeParams& p, const CUtensorMap* maps, const Tr
 template <int FMT, int D>
 cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
                              const LaunchCtx& ctx) {
-  using Few = TCfg<FMT, D, true>;
-  using Many = TCfg<FMT, D, false>;
-  if (p.capped || p.slopes)
-    return plan.few ? launch_tree_d<Few, true>(p, maps, plan, ctx)
-                    : launch_tree_d<Many, true>(p, maps, plan, ctx);
-  return plan.few ? launch_tree_d<Few, false>(p, maps, plan, ctx)
-                  : launch_tree_d<Many, false>(p, maps, plan, ctx);
+  using C = TCfg<FMT, D>;
+  return p.capped || p.slopes ? launch_tree_d<C, true>(p, maps, plan, ctx)
+                              : launch_tree_d<C, false>(p, maps, plan, ctx);
 }
 
 template <int FMT>

@@ -9,10 +9,7 @@ cudaError_t launch_decode_tree_bf16(const TreeDecodeProblem& pb, const CUtensorM
   return launch_tree_fmt<kCacheBf16>(pb, maps, plan, workspace, ctx);
 }
 
-int tree_tile_keys(int d, bool few) {
-  return few || d < 128 ? TCfg<kCacheBf16, 64, true>::BN : TCfg<kCacheBf16, 128, false>::BN;
-}
-int tree_few_rows() { return kFewRows; }
+int tree_tile_keys(int d) { return d == 128 ? TCfg<kCacheBf16, 128>::BN : TCfg<kCacheBf16, 64>::BN; }
 int tree_min_tiles() { return kMinTreeTiles; }
 
 }  // namespace attn

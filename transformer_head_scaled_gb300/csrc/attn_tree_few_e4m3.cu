@@ -1,0 +1,13 @@
+// attn_tree_few_e4m3.cu -- the decoding step (attn_decode_scored.cuh) for trees of
+// drafted tokens with few query rows to a key head, over a cache of e4m3 rows.
+#include "attn_decode_scored.cuh"
+
+namespace attn {
+
+cudaError_t launch_tree_few_e4m3(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
+                                 const ScoredDecodePlan& plan, float* workspace,
+                                 const LaunchCtx& ctx, const TreeOwn& tree) {
+  return launch_scored_decode_fmt<kCacheE4M3, true>(pb, maps, plan, workspace, ctx, &tree);
+}
+
+}  // namespace attn

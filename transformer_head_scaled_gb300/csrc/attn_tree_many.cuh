@@ -31,7 +31,7 @@ __device__ __forceinline__ bool mma_many(const TreeParams& p, TreeSmem<C>& sm, u
   const uint32_t t_o = tmem + C::col_o(s);
   const bool leader = elect_one();
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_small(smem_u32(bar), parity, p.limit_ns, abort));
     return ok;
   };
   auto v_wait = [&](uint32_t g) { return wait(&sm.v_full[g % VSTAGES], (g / VSTAGES) & 1); };
@@ -151,12 +151,12 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
   constexpr int OC = C::OW / 32;
   uint32_t u = 0;  // parts of SN keys of this stream
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, p.limit_ns, abort));
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_small(smem_u32(bar), parity, p.limit_ns, abort));
     return ok;
   };
   uint32_t joins = 0;
   auto join = [&]() {
-    mbar_arrive(smem_u32(&sm.join_sync));
+    warp_arrive(smem_u32(&sm.join_sync));
     return wait(&sm.join_sync, joins++ & 1);
   };
   for (uint32_t items = 0; ok; ++items) {
@@ -401,7 +401,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
         }
         first = false;
         tc_fence_before();
-        mbar_arrive(smem_u32(&sm.p_full[s][u & 1]));
+        warp_arrive(smem_u32(&sm.p_full[s][u & 1]));
         ++u;
       }
     }
@@ -500,7 +500,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
     }
     if (!ok) break;
     tc_fence_before();
-    mbar_arrive(smem_u32(&sm.item_empty[slot]));
+    warp_arrive(smem_u32(&sm.item_empty[slot]));
   }
   return ok;
 }
