@@ -127,7 +127,7 @@ struct TreeParams {
   int B, H, HK, G, n, L_max, T_log2, num_blocks, window;
   int rows, blocks, block_rows;  // query rows of a key head, their blocks, rows of a part
   int tree_tiles, rounds;
-  float scale_log2, cap_log2, cap_in;
+  float scale_log2, cap_log2, cap_in, inv_n;
   CapPoly cap;
   bool capped, wide;
 };
@@ -150,6 +150,7 @@ struct __align__(1024) TreeSmem {
   uint64_t raw_full[2][C::RAWS], raw_empty[2][C::RAWS];  // keys, values
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // stream, buffer
   uint64_t drain[2];
+  uint64_t q_there;  // the first item's query rows
   uint64_t aux_sync, join_sync;  // barriers of the auxiliary and of the softmax warps
   unsigned warp_sum[NUM_THREADS / 32];
   unsigned total;
@@ -456,6 +457,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         mbar_init(smem_u32(&sm.raw_empty[i][r]), 2);
       }
     }
+    mbar_init(smem_u32(&sm.q_there), 4);
     mbar_init(smem_u32(&sm.aux_sync), 4);
     mbar_init(smem_u32(&sm.join_sync), 8);
     for (int i = 0; i < C::QSLOTS; ++i) mbar_init(smem_u32(&sm.q_empty[i]), 2);
@@ -573,6 +575,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       cur.begin(p, start_b, start_off, count);
       TreeItem it;
       uint32_t cnt = 0;
+      // the first query rows come before the first tiles: behind those of all CTAs at
+      // once they would take 6 us and more
+      ok = mbar_wait_small(smem_u32(&sm.q_there), 0, p.limit_ns, abort);
       while (ok && cur.next(p, it)) {
         const int stop = Q8 ? min(it.t0 + it.n, it.ctx) : it.t0 + it.n;
         for (int t = it.t0; t < stop; ++t) {
@@ -651,26 +656,36 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // the query rows, each `split` times
       const int qslot = items % C::QSLOTS;
       if (!wait(&sm.q_empty[qslot], ((items / C::QSLOTS) & 1) ^ 1)) break;
+      // (rows by a product with 1 / n: exact for numbers this small.  Loads go together,
+      // of the first row where there is none: a branch around each would make them wait
+      // for one another)
       constexpr int CPR = D / 8;  // 16-byte chunks of a row
+      constexpr int BATCH = CPR < 8 ? CPR : 8;
       const int tiles = it.split == 0 ? 2 : 1;
       const int lanes = it.split == 0 ? BM : BM / it.split;
+      const __nv_bfloat16* q = p.q + it.b * p.sq.b + static_cast<long long>(it.hk) * p.G * p.sq.h;
       for (int s = 0; s < tiles; ++s) {
-#pragma unroll 4
-        for (int e = tid; e < BM * CPR; e += 128) {
-          const int at = e / CPR, c = e % CPR;
-          const int r = s * BM + (at & (lanes - 1));
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (r < it.rows) {
-            const int row = it.row0 + r, g = row / p.n, i = row - g * p.n;
-            x = __ldg(reinterpret_cast<const uint4*>(p.q + it.b * p.sq.b +
-                                                     (it.hk * p.G + g) * p.sq.h + i * p.sq.n) +
-                      c);
+#pragma unroll 1
+        for (int e0 = tid; e0 < BM * CPR; e0 += 128 * BATCH) {
+          uint4 x[BATCH];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int at = (e0 + 128 * i) / CPR, c = (e0 + 128 * i) % CPR;
+            const int r = s * BM + (at & (lanes - 1)), row = it.row0 + (r < it.rows ? r : 0);
+            const int g = static_cast<int>((row + 0.5f) * p.inv_n);
+            x[i] = __ldg(reinterpret_cast<const uint4*>(q + g * p.sq.h + (row - g * p.n) * p.sq.n) + c);
           }
-          *reinterpret_cast<uint4*>(sm.q[qslot][s] + (c / C::CPB) * C::Q_BLOCK + at * C::RB +
-                                    (((c % C::CPB) ^ C::swz(at)) << 4)) = x;
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int at = (e0 + 128 * i) / CPR, c = (e0 + 128 * i) % CPR;
+            if (s * BM + (at & (lanes - 1)) >= it.rows) x[i] = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(sm.q[qslot][s] + (c / C::CPB) * C::Q_BLOCK + at * C::RB +
+                                      (((c % C::CPB) ^ C::swz(at)) << 4)) = x[i];
+          }
         }
       }
       fence_proxy_async_smem();
+      if (items == 0) warp_arrive(smem_u32(&sm.q_there));
       if (has[slot] != it.b) {
         // ancestors by pointer doubling: after round k a node knows 2^k of them
         has[slot] = it.b;
@@ -918,6 +933,7 @@ cudaError_t launch_tree_fmt(const TreeDecodeProblem& pb, const CUtensorMap* maps
   p.HK = pb.HK;
   p.G = pb.H / pb.HK;
   p.n = pb.n;
+  p.inv_n = 1.f / pb.n;
   p.L_max = pb.L_max;
   while ((1 << p.T_log2) < pb.block_tokens) ++p.T_log2;
   p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
