@@ -122,6 +122,15 @@ CASES = [
     (1, 3, 1, 10, 9000, 32, 128, 0.0, False, None, "star", [8991]),
     (2, 2, 2, 32, 260, 16, 16, 0.0, True, 64, "chain", [260, 30]),
     (5, 2, 1, 3, 640, 16, 64, 0.0, False, None, "holes", [640, 1, 0, 333, 64]),
+    # query rows of a key head on both sides of where the kernel changes
+    (17, 4, 2, 8, 130, 128, 64, 0.0, False, None, "random", list(range(114, 131))),    # 16 rows
+    (17, 2, 2, 17, 130, 128, 64, 0.0, False, None, "random", list(range(114, 131))),   # 17 of 34
+    (16, 2, 2, 32, 130, 128, 64, 20.0, False, None, "random", list(range(115, 131))),  # 32 of 32
+    (2, 3, 3, 33, 130, 128, 64, 0.0, False, 40, "random", [130, 128]),
+    (2, 4, 2, 16, 200, 64, 32, 0.0, True, None, "holes", [200, 191]),
+    (2, 3, 1, 11, 200, 64, 32, 0.0, True, None, "holes", [200, 191]),
+    (2, 2, 1, 32, 200, 32, 32, 0.0, False, None, "chain", [200, 192]),
+    (2, 5, 1, 13, 200, 32, 32, 0.0, False, None, "chain", [200, 192]),
 ]
 
 

@@ -1250,7 +1250,7 @@ size_t attn_decode_tree_workspace_bytes(int B, int h, int h_kv, int n, int L_max
   if (tree_decode_sizes(B, h, h_kv, n, L_max, d_k, cache_format, window) != ATTN_OK) return 0;
   DeviceInfo* di = nullptr;
   if (device_info(&di) != ATTN_OK) return 0;
-  if (h / h_kv * n <= kFewTreeRows)
+  if (tree_few(B, h_kv, h / h_kv * n, d_k))
     return tree_few_plan(B, h, h_kv, n, scored_seen(n, L_max, window), d_k,
                          elem_bytes(cache_format), di->num_sms)
         .workspace_bytes;
@@ -1289,7 +1289,7 @@ int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, cons
   const int near = window < L_max + n ? window : -1;
   const LaunchCtx ctx = make_ctx(*di, stream);
   CUtensorMap maps[4];
-  if (h / h_kv * n <= kFewTreeRows) {
+  if (tree_few(B, h_kv, h / h_kv * n, d_k)) {
     const ScoredDecodePlan plan = tree_few_plan(B, h, h_kv, n, scored_seen(n, L_max, window), d_k,
                                                 e1, di->num_sms);
     if (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace))

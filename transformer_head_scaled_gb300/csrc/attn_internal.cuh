@@ -425,7 +425,15 @@ struct TreeOwn {
   const void* v;
   RowStrides sk, sv;
 };
-constexpr int kFewTreeRows = 64;
+// Whether it is taken.  Measured against the tensor-memory kernel below (us, this one
+// first): 16 x 8 heads x 4096-8192 tokens, d = 64, bf16, 8 rows of a key head 44 and 63, 16 rows
+// 51 and 64, 32 rows 72 and 66, e4m3 30 and 73, 44 and 74, 71 and 75; d = 128, e4m3, 16 rows
+// 66 and 105, 32 rows 124 and 106, 64 rows 166 and 112; d = 32, e4m3, 64 rows 66 and 79; and
+// with few units it starts sooner: 8 heads x 4096 tokens, d = 128, 32 rows 25 and 39.
+inline bool tree_few(int B, int HK, int rows, int d) {
+  return rows <= 16 || (rows <= 32 && (d < 128 || static_cast<long long>(B) * HK <= 32)) ||
+         (rows <= 64 && d <= 32);
+}
 ScoredDecodePlan tree_few_plan(int B, int H, int HK, int n, int seen, int d, int elem_bytes,
                                int num_sms);
 cudaError_t launch_tree_few_bf16(const ScoredDecodeProblem& pb, const CUtensorMap* maps,

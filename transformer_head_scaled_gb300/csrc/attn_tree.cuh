@@ -134,7 +134,7 @@ struct TreeParams {
 
 template <class C>
 struct __align__(1024) TreeSmem {
-  uint8_t q[C::QSLOTS][2][C::Q_TILE];
+  uint8_t q[2 * C::QSLOTS][C::Q_TILE];
   uint8_t k[C::KSTAGES][C::KV_TILE];
   uint8_t v[C::VSTAGES][C::KV_TILE];
   uint8_t raw_k[C::RAWS][C::Q8 ? C::RAW_TILE : 16];
@@ -145,7 +145,7 @@ struct __align__(1024) TreeSmem {
   int depth[2][kMostNodes];         // -1: no node
   int up[2][kMostNodes];            // scratch: parents, and 2^k-th ancestors
   TreeItem item[2];
-  uint64_t item_full[2], item_empty[2], q_empty[C::QSLOTS];
+  uint64_t item_full[2], item_empty[2], q_empty[2];
   uint64_t k_full[C::KSTAGES], k_empty[C::KSTAGES], v_full[C::VSTAGES], v_empty[C::VSTAGES];
   uint64_t raw_full[2][C::RAWS], raw_empty[2][C::RAWS];  // keys, values
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // stream, buffer
@@ -158,6 +158,11 @@ struct __align__(1024) TreeSmem {
   unsigned start_off;
   uint32_t tmem_base;
   int abort;
+  // tile s of an item's query rows; both: an item with two of them
+  __device__ __forceinline__ uint8_t* q_tile(uint32_t items, bool both, int s) {
+    if (C::QSLOTS == 2) return q[2 * (items & 1) + s];
+    return q[both ? s : items & 1];
+  }
 };
 
 // The tiles of a sequence's visible cache and of its tree.
@@ -460,7 +465,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(smem_u32(&sm.q_there), 4);
     mbar_init(smem_u32(&sm.aux_sync), 4);
     mbar_init(smem_u32(&sm.join_sync), 8);
-    for (int i = 0; i < C::QSLOTS; ++i) mbar_init(smem_u32(&sm.q_empty[i]), 2);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sm.q_empty[i]), 2);
     for (int i = 0; i < KSTAGES; ++i) {
       mbar_init(smem_u32(&sm.k_full[i]), Q8 ? 2 : 1);
       mbar_init(smem_u32(&sm.k_empty[i]), 2);  // both streams
@@ -637,6 +642,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       return wait(&sm.aux_sync, syncs++ & 1);
     };
     uint32_t copied = 0, phase = 0;  // ring slots that this warp copied to last, and when
+    bool was_wide = false;         // the item before
     const bool small = p.n <= 32;  // every warp has all the nodes
     for (uint32_t items = 0;; ++items) {
       const int slot = items & 1;
@@ -654,8 +660,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         break;
       }
       // the query rows, each `split` times
-      const int qslot = items % C::QSLOTS;
-      if (!wait(&sm.q_empty[qslot], ((items / C::QSLOTS) & 1) ^ 1)) break;
+      if (!wait(&sm.q_empty[slot], ((items >> 1) & 1) ^ 1)) break;
+      // (d = 128: two tiles in all, which one item takes with both streams' rows)
+      const bool wide = it.split == 0;
+      if (C::QSLOTS == 1 && items > 0 && (wide || was_wide) &&
+          !wait(&sm.q_empty[slot ^ 1], ((items - 1) >> 1) & 1))
+        break;
+      was_wide = wide;
       // (rows by a product with 1 / n: exact for numbers this small.  Loads go together,
       // of the first row where there is none: a branch around each would make them wait
       // for one another)
@@ -679,7 +690,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int i = 0; i < BATCH; ++i) {
             const int at = (e0 + 128 * i) / CPR, c = (e0 + 128 * i) % CPR;
             if (s * BM + (at & (lanes - 1)) >= it.rows) x[i] = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(sm.q[qslot][s] + (c / C::CPB) * C::Q_BLOCK + at * C::RB +
+            *reinterpret_cast<uint4*>(sm.q_tile(items, wide, s) + (c / C::CPB) * C::Q_BLOCK + at * C::RB +
                                       (((c % C::CPB) ^ C::swz(at)) << 4)) = x[i];
           }
         }

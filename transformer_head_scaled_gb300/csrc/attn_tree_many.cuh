@@ -73,8 +73,8 @@ __device__ __forceinline__ bool mma_many(const TreeParams& p, TreeSmem<C>& sm, u
     const TreeItem it = sm.item[slot];
     if (it.more == 0) break;
     const bool both = it.split == 0;
-    const uint64_t dq = tree_sdesc(smem_u32(sm.q[items % C::QSLOTS][both ? s : 0]), 16,
-                                   8 * C::RB, C::SWZ);
+    const uint64_t dq =
+        tree_sdesc(smem_u32(sm.q_tile(items, both, both ? s : 0)), 16, 8 * C::RB, C::SWZ);
     bool first = true;
     for (int j = 0; j < it.n && ok; ++j) {
       const uint32_t g = g0 + j;
@@ -123,7 +123,7 @@ __device__ __forceinline__ bool mma_many(const TreeParams& p, TreeSmem<C>& sm, u
       }
     }
     if (!ok) break;
-    if (leader) tc_commit(smem_u32(&sm.q_empty[items % C::QSLOTS]));
+    if (leader) tc_commit(smem_u32(&sm.q_empty[slot]));
     if (!first && pending) {
       plast = true;
     } else {
