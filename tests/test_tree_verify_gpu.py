@@ -90,6 +90,26 @@ def test_drafts_near_and_far_from_the_target(noise):
         assert (got[0][:, 1] == 1).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,V", [(5, 30001), (2, 131072), (1, 300007), (1, 500000), (1, 4500000)])
+def test_many_rejections_over_large_rows(B, V, dtype):
+    """Rows that shared memory holds, holds in part, and segments of several blocks."""
+    p, q, _, _, u = _case(B, 2, V, dtype, True, 5, noise=4.0)
+    n = 9
+    p, q = (x[:, [0, 1] + [1] * (n - 2)].contiguous() for x in (p, q))
+    g = torch.Generator(device="cuda").manual_seed(4)
+    cum = q[:, 0].double().cumsum(-1)  # (multinomial takes 2^24 values at most)
+    tokens = torch.searchsorted(cum, torch.rand((B, n), generator=g, device="cuda",
+                                                dtype=torch.float64) * cum[:, -1:])
+    tokens = tokens.clamp(max=V - 1).to(torch.int32)
+    u = torch.rand((B, n), generator=g, device="cuda") * 0.5 + 0.5
+    parents = np.tile(np.where(np.arange(n) == 0, -1, 0), (B, 1))
+    got = binding.attn_tree_verify(p, tokens, _int(parents), u, draft=q)
+    _check(got, p, q, tokens, parents, u)
+    got = binding.attn_tree_verify(p, tokens, _int(parents), u)
+    _check(got, p, None, tokens, parents, u)
+
+
 def _one(p, tokens, parents, u, q=None):
     """A single sequence of exactly held numbers."""
     p = torch.tensor([p], device="cuda", dtype=torch.float32)
