@@ -1157,7 +1157,7 @@ def attn_decode_tree(q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor
             if out.shape != q.shape:
                 raise ValueError("out must be shaped like q")
         if lse is None:
-            lse = q.new_empty((B, h, n), dtype=torch.float32)
+            lse = torch.empty((B, h, n), dtype=torch.float32, device=dev)
         else:
             _vector("lse", lse, torch.float32, B * h * n, dev)
         window = -1 if window is None else min(int(window), _INT_MAX)
@@ -1218,11 +1218,11 @@ def attn_tree_verify(target: torch.Tensor, tokens: torch.Tensor, parents: torch.
         strides = _strides_array(strides)
     with _call_on(dev, stream) as ptr:
         if path is None:
-            path = tokens.new_empty((B, n))
+            path = torch.empty_like(tokens)
         if path_lens is None:
-            path_lens = tokens.new_empty(B)
+            path_lens = torch.empty(B, dtype=torch.int32, device=dev)
         if next_tokens is None:
-            next_tokens = tokens.new_empty(B)
+            next_tokens = torch.empty(B, dtype=torch.int32, device=dev)
         rc = attn_tree_verify_raw(
             _ptr(target), _ptr(draft), _ptr(tokens), _ptr(parents), _ptr(uniforms), _ptr(path),
             _ptr(path_lens), _ptr(next_tokens), B, n, V, strides,
@@ -1241,6 +1241,15 @@ def attn_cache_append_tree_raw(kt_ptr, vt_ptr, path_ptr, path_lens_ptr, k_ptr, v
         L_max, d, _strides_array(strides), cache_format, block_tokens, lens_ptr, stream_ptr)
 
 
+@functools.lru_cache(maxsize=1024)
+def _layer_strides_of(layouts):
+    flat = []
+    for step, shape in layouts:
+        room = -(-max(*step, shape[3] * shape[4]) // 16) * 16
+        flat += [step[i] if shape[i] > 1 else room for i in range(4)]
+    return _strides_array(flat)
+
+
 def _layer_strides(*tensors):
     """The (layer, b, h, row) element strides of [layers, B, h, n, d] views; None
     when all are contiguous.  The stride of a dimension of one entry is never
@@ -1250,12 +1259,7 @@ def _layer_strides(*tensors):
             break
     else:
         return None
-    flat = []
-    for t in tensors:
-        step, shape = t.stride(), t.shape
-        room = -(-max(*step, shape[3] * shape[4]) // 16) * 16
-        flat += [step[i] if shape[i] > 1 else room for i in range(4)]
-    return _strides_array(flat)
+    return _layer_strides_of(tuple([(t.stride(), t.shape) for t in tensors]))
 
 
 def attn_cache_append_tree(k_tree: torch.Tensor, v_tree: torch.Tensor, path: torch.Tensor,

@@ -27,8 +27,9 @@
 // sequences, 8 heads: 3 us, the launch.
 //
 // The accepted path of a tree of drafted tokens (attn_cache_append_tree) goes
-// the same way: token i of it is row path[b][i] of the tree's keys and values,
-// and one launch does it for all layers.  Into a cache of bf16 rows it is a copy.
+// the same way, in kernels of its own: token i of it is row path[b][i] of the
+// tree's keys and values, and one launch does it for all layers.  Into a cache of
+// bf16 rows it is a copy.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -45,7 +46,7 @@ struct CacheParams {
   const int* new_lens;  // new tokens per sequence, or null (n_new each)
   RowStrides ss[2], sd[2];
   int H, n_new, L_max, T, num_blocks, touched;
-  // TREE: token i of sequence b is row path[b][i] of n; B sequences in each of
+  // for a tree: token i of sequence b is row path[b][i] of n; B sequences in each of
   // the layers, whose strides these are
   const int* path;
   int B, n;
@@ -100,8 +101,7 @@ __device__ __forceinline__ float decode1(uint32_t byte) {
 // THREADS threads work on one block of one (b, head) and of keys or values;
 // CHUNKS chunks of 8 elements each wait in a thread's registers.  WARP: one
 // warp per block, eight blocks to a CTA and no barrier; else one CTA per block.
-// TREE: the new tokens are a path through a tree's, in every layer.
-template <bool E4M3, bool WARP, int THREADS, int CHUNKS, bool TREE>
+template <bool E4M3, bool WARP, int THREADS, int CHUNKS>
 __global__ void __launch_bounds__(WARP ? 256 : THREADS)
     attn_cache_append_kernel(const CacheParams p, unsigned units, int cpr_log2) {
   __shared__ float red[WARP ? 1 : THREADS / 32];
@@ -112,12 +112,9 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   const int kv = unit & 1u;
   const unsigned rest = unit >> 1;
   const unsigned bh = rest / static_cast<unsigned>(p.touched);
-  const int bl = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(bl) * p.H;
-  const int layer = TREE ? bl / p.B : 0, b = TREE ? bl - layer * p.B : bl;
+  const int b = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(b) * p.H;
   const int len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
-  int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
-  const int* path = TREE ? p.path + static_cast<long long>(b) * p.n_new : nullptr;
-  if (TREE) more = path_length(path, more, p.n, threadIdx.x & 31);
+  const int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
   const int end = len + min(more, p.L_max - len);  // tokens that do not fit are dropped
   const int blk = len / p.T + static_cast<int>(rest - bh * p.touched);
   if (blk >= p.num_blocks) return;
@@ -126,29 +123,16 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   const int first = max(len, row0), last = min(end, row0 + p.T);  // new rows of this block
   if (first >= last) return;  // the same for every thread of the unit
 
-  const __nv_bfloat16* src = p.src[kv] + b * p.ss[kv].b + hh * p.ss[kv].h;
-  if (TREE)
-    src += layer * p.sl[kv];
-  else
-    src += static_cast<long long>(first - len) * p.ss[kv].n;
+  const __nv_bfloat16* src = p.src[kv] + b * p.ss[kv].b + hh * p.ss[kv].h +
+                             static_cast<long long>(first - len) * p.ss[kv].n;
   uint8_t* dst = p.dst[kv] + b * p.sd[kv].b + hh * p.sd[kv].h;
-  if (TREE) dst += layer * p.dl[kv];
   const int chunks = (last - first) << cpr_log2;  // 8-element chunks, a row's side by side
 
   // a thread's chunks stand in one column, `rows` rows apart
   const int rows = THREADS >> cpr_log2, row = tid >> cpr_log2;
   const int col = (tid - (row << cpr_log2)) * 8;
   uint4 w[CHUNKS];
-  if constexpr (TREE) {
-#pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (tid + i * THREADS < chunks) {
-        const int node = __ldg(path + (first - len) + row + i * rows);
-        w[i] = __ldg(reinterpret_cast<const uint4*>(src + node * p.ss[kv].n + col));
-      }
-    }
-  } else {
+  {
     const __nv_bfloat16* at = src + row * p.ss[kv].n + col;
     const long long step = rows * p.ss[kv].n;
 #pragma unroll
@@ -219,55 +203,182 @@ __global__ void __launch_bounds__(WARP ? 256 : THREADS)
   }
 }
 
-template <bool E4M3, bool TREE>
+template <bool E4M3>
 cudaError_t launch_append(const CacheParams& p, unsigned units, int cpr_log2, cudaStream_t stream) {
   // most 8-element chunks of new tokens that one block can get
   const int most = (p.n_new < p.T ? p.n_new : p.T) << cpr_log2;
   if (most <= 4 * 32) {
-    attn_cache_append_kernel<E4M3, true, 32, 4, TREE>
+    attn_cache_append_kernel<E4M3, true, 32, 4>
         <<<(units + 7) / 8, 256, 0, stream>>>(p, units, cpr_log2);
   } else if (most <= 8 * 32) {
-    attn_cache_append_kernel<E4M3, true, 32, 8, TREE>
+    attn_cache_append_kernel<E4M3, true, 32, 8>
         <<<(units + 7) / 8, 256, 0, stream>>>(p, units, cpr_log2);
   } else if (most <= 8 * 64) {
-    attn_cache_append_kernel<E4M3, false, 64, 8, TREE>
-        <<<units, 64, 0, stream>>>(p, units, cpr_log2);
+    attn_cache_append_kernel<E4M3, false, 64, 8><<<units, 64, 0, stream>>>(p, units, cpr_log2);
   } else if (most <= 8 * 128) {
-    attn_cache_append_kernel<E4M3, false, 128, 8, TREE>
-        <<<units, 128, 0, stream>>>(p, units, cpr_log2);
+    attn_cache_append_kernel<E4M3, false, 128, 8><<<units, 128, 0, stream>>>(p, units, cpr_log2);
   } else {
-    attn_cache_append_kernel<E4M3, false, 256, 8, TREE>
-        <<<units, 256, 0, stream>>>(p, units, cpr_log2);
+    attn_cache_append_kernel<E4M3, false, 256, 8><<<units, 256, 0, stream>>>(p, units, cpr_log2);
   }
   return cudaGetLastError();
 }
 
+// One sequence of one layer and what a warp does there.
+struct TreeUnit {
+  const __nv_bfloat16* src;
+  const int* path;
+  long long dst;  // offset of the head's rows in the cache
+  long long bh;   // (layer, sequence, head)
+  int kv, len, end;
+};
+
+__device__ __forceinline__ TreeUnit tree_unit(const CacheParams& p, unsigned unit, int lane) {
+  TreeUnit u;
+  u.kv = unit & 1u;
+  const unsigned bh = unit >> 1;
+  u.bh = bh;
+  const int bl = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(bl) * p.H;
+  const int layer = bl / p.B, b = bl - layer * p.B;
+  u.path = p.path + static_cast<long long>(b) * p.n_new;
+  // (lengths and path in one round of loads)
+  const int first = lane < p.n_new ? __ldg(u.path + lane) : 0;
+  const int more = min(max(__ldg(p.new_lens + b), 0), p.n_new);
+  u.len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
+  const unsigned bad =
+      __ballot_sync(0xffffffffu, lane < more && (first < 0 || first >= p.n));
+  int good = bad != 0 ? __ffs(bad) - 1 : min(more, 32);
+  if (good == 32) good += path_length(u.path + 32, more - 32, p.n, lane);
+  u.end = u.len + min(good, p.L_max - u.len);  // tokens that do not fit are dropped
+  u.src = p.src[u.kv] + layer * p.sl[u.kv] + b * p.ss[u.kv].b + hh * p.ss[u.kv].h;
+  u.dst = layer * p.dl[u.kv] + b * p.sd[u.kv].b + hh * p.sd[u.kv].h;
+  return u;
+}
+
+// A path into an 8-bit cache: a warp per (layer, sequence, head, keys or values),
+// which takes the path's blocks one after the other, or every `ways`-th of them
+// where there are too few such warps.  256 chunks of new rows (most paths are far
+// shorter than the tree) stay in registers between the maximum and the codes.
+// Bound by latency: lengths and path, rows and scale, codes.  24 layers, 32
+// sequences, 8 heads of 128, 32 nodes to e4m3: 16 us (with the kernel above, a block
+// of threads per unit and block: 23); 4 layers, 3 sequences, 5 heads of 32: 3.8 us.
+template <bool E4M3>
+__global__ void __launch_bounds__(256)
+    attn_cache_append_tree_kernel(const CacheParams p, unsigned units, int cpr_log2, int ways) {
+  constexpr int CHUNKS = 8;
+  const unsigned at_unit = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (at_unit >= units) return;
+  const int lane = threadIdx.x & 31;
+  const unsigned unit = at_unit / static_cast<unsigned>(ways);
+  const TreeUnit u = tree_unit(p, unit, lane);
+  if (u.end == u.len) return;
+  const long long sn = p.ss[u.kv].n, dn = p.sd[u.kv].n;
+  uint8_t* dst = p.dst[u.kv] + u.dst;
+  for (int blk = u.len / p.T + static_cast<int>(at_unit - unit * ways); blk * p.T < u.end;
+       blk += ways) {
+    const int row0 = blk * p.T;
+    const int first = max(u.len, row0), last = min(u.end, row0 + p.T);  // the block's new rows
+    const int chunks = (last - first) << cpr_log2;
+    float* scale_at = p.scale[u.kv] + u.bh * p.num_blocks + blk;
+    const float held = first > row0 ? *scale_at : 0.f;
+    uint4 w[CHUNKS];
+    auto load = [&](int c0) {
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const int c = c0 + i * 32 + lane, row = c >> cpr_log2;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < chunks)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(
+              u.src + __ldg(u.path + first - u.len + row) * sn + (c - (row << cpr_log2)) * 8));
+      }
+    };
+    // (the larger of two bf16 magnitudes, exactly; a NaN gives way to a number)
+    __nv_bfloat162 most = __halves2bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+    int c0 = -CHUNKS * 32;
+    do {
+      c0 += CHUNKS * 32;
+      load(c0);
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = __hmax2(most, __habs2(x[e]));
+      }
+    } while (c0 + CHUNKS * 32 < chunks);
+    float top = fmaxf(__low2float(most), __high2float(most));
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    __syncwarp();  // every lane has read the held scale before it is replaced
+    const float scale = fmaxf(fmaxf(held, __fdiv_rn(top, code_max<E4M3>())), kScaleMin);
+    const float inv = __frcp_rn(scale);
+    for (bool again = false; c0 >= 0; c0 -= CHUNKS * 32, again = true) {
+      if (again) load(c0);
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        const int c = c0 + i * 32 + lane, row = c >> cpr_log2;
+        if (c >= chunks) break;
+        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = __bfloat1622float2(x[e]);
+          f[2 * e] = y.x * inv;
+          f[2 * e + 1] = y.y * inv;
+        }
+        *reinterpret_cast<uint2*>(dst + (first + row) * dn + (c - (row << cpr_log2)) * 8) =
+            make_uint2(encode4<E4M3>(f[0], f[1], f[2], f[3]),
+                       encode4<E4M3>(f[4], f[5], f[6], f[7]));
+      }
+    }
+    if (scale != held) {
+      if (lane == 0) *scale_at = scale;
+      // the rows the block held are rescaled; rows behind the new ones stay
+      const float ratio = held * inv;
+      const int old = (first - row0) << cpr_log2;
+      auto at = [&](int c) {
+        const int r = c >> cpr_log2;
+        return reinterpret_cast<uint2*>(dst + static_cast<long long>(row0 + r) * dn) +
+               (c - (r << cpr_log2));
+      };
+      for (int c = lane; c < old; c += CHUNKS * 32) {
+        uint2 v[CHUNKS];
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+          if (c + i * 32 < old) v[i] = *at(c + i * 32);
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i) {
+          if (c + i * 32 >= old) break;
+          uint32_t* words = reinterpret_cast<uint32_t*>(&v[i]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            words[e] = encode4<E4M3>(decode1<E4M3>(words[e] & 0xffu) * ratio,
+                                     decode1<E4M3>((words[e] >> 8) & 0xffu) * ratio,
+                                     decode1<E4M3>((words[e] >> 16) & 0xffu) * ratio,
+                                     decode1<E4M3>(words[e] >> 24) * ratio);
+          *at(c + i * 32) = v[i];
+        }
+      }
+    }
+  }
+}
+
 // The path's rows of a bf16 cache: a warp per (layer, sequence, head, keys or
 // values), 16-byte chunks of its rows side by side.  Bound by the latency of
-// three loads in a row (lengths, path, rows).
+// two rounds of loads (lengths and path, rows).
 __global__ void __launch_bounds__(256)
     attn_cache_copy_tree_kernel(const CacheParams p, unsigned units, int cpr_log2) {
   const unsigned unit = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (unit >= units) return;
   const int lane = threadIdx.x & 31;
-  const int kv = unit & 1u;
-  const unsigned bh = unit >> 1;
-  const int bl = bh / static_cast<unsigned>(p.H), hh = bh - static_cast<unsigned>(bl) * p.H;
-  const int layer = bl / p.B, b = bl - layer * p.B;
-  const int len = p.lens ? min(max(__ldg(p.lens + b), 0), p.L_max) : 0;
-  int more = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
-  const int* path = p.path + static_cast<long long>(b) * p.n_new;
-  more = min(path_length(path, more, p.n, lane), p.L_max - len);
-  const __nv_bfloat16* src = p.src[kv] + layer * p.sl[kv] + b * p.ss[kv].b + hh * p.ss[kv].h;
-  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.dst[kv]) + layer * p.dl[kv] +
-                       b * p.sd[kv].b + hh * p.sd[kv].h + len * p.sd[kv].n;
-  const int chunks = more << cpr_log2;
+  const TreeUnit u = tree_unit(p, unit, lane);
+  const long long sn = p.ss[u.kv].n, dn = p.sd[u.kv].n;
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.dst[u.kv]) + u.dst + u.len * dn;
+  const int chunks = (u.end - u.len) << cpr_log2;
 #pragma unroll 4
   for (int c = lane; c < chunks; c += 32) {
     const int row = c >> cpr_log2, col = (c - (row << cpr_log2)) * 8;
-    const int node = __ldg(path + row);
-    *reinterpret_cast<uint4*>(dst + row * p.sd[kv].n + col) =
-        __ldg(reinterpret_cast<const uint4*>(src + node * p.ss[kv].n + col));
+    const int node = __ldg(u.path + row);
+    *reinterpret_cast<uint4*>(dst + row * dn + col) =
+        __ldg(reinterpret_cast<const uint4*>(u.src + node * sn + col));
   }
 }
 
@@ -296,8 +407,8 @@ cudaError_t launch_cache_append(const CacheAppendProblem& pb, const LaunchCtx& c
   const unsigned units = 2u * pb.B * pb.H * p.touched;  // the caller keeps it below 2^31
   int cpr_log2 = 1;  // 8-element chunks of a row
   while ((8 << cpr_log2) < pb.d) ++cpr_log2;
-  return pb.e4m3 ? launch_append<true, false>(p, units, cpr_log2, ctx.stream)
-                 : launch_append<false, false>(p, units, cpr_log2, ctx.stream);
+  return pb.e4m3 ? launch_append<true>(p, units, cpr_log2, ctx.stream)
+                 : launch_append<false>(p, units, cpr_log2, ctx.stream);
 }
 
 cudaError_t launch_cache_append_tree(const CacheTreeProblem& pb, const LaunchCtx& ctx) {
@@ -331,10 +442,17 @@ cudaError_t launch_cache_append_tree(const CacheTreeProblem& pb, const LaunchCtx
   }
   p.T = pb.block_tokens;
   p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
-  p.touched = cache_blocks_touched(pb.n, pb.L_max, pb.block_tokens);
-  const unsigned units = rows * p.touched;  // the caller keeps it below 2^31
-  return pb.e4m3 ? launch_append<true, true>(p, units, cpr_log2, ctx.stream)
-                 : launch_append<false, true>(p, units, cpr_log2, ctx.stream);
+  // a warp for each block where that gives no more than 16 warps per SM
+  int ways = cache_blocks_touched(pb.n, pb.L_max, pb.block_tokens);
+  if (static_cast<long long>(rows) * ways > 16LL * ctx.num_sms) ways = 1;
+  const unsigned units = rows * ways;  // the caller keeps it below 2^31
+  if (pb.e4m3)
+    attn_cache_append_tree_kernel<true>
+        <<<(units + 7) / 8, 256, 0, ctx.stream>>>(p, units, cpr_log2, ways);
+  else
+    attn_cache_append_tree_kernel<false>
+        <<<(units + 7) / 8, 256, 0, ctx.stream>>>(p, units, cpr_log2, ways);
+  return cudaGetLastError();
 }
 
 int cache_blocks_touched(int n_new, int L_max, int block_tokens) {
