@@ -73,6 +73,8 @@
 // 47 us against the kernel's 55.
 #pragma once
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -942,90 +944,128 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   }
 }
 
-// What a node sees of its tree: O relative to 2^m, its values in the lanes.
+// What a node sees of its tree: O relative to 2^m, a lane's values side by side.
 template <int E>
 struct OwnPart {
   float a[E], m, l;
   bool node;
 };
+
+// E values of a bf16 row, one load.
+template <int E>
+__device__ __forceinline__ void load_values(const __nv_bfloat16* at, float (&x)[E]) {
+  if constexpr (E == 1) {
+    x[0] = __bfloat162float(*at);
+  } else if constexpr (E == 2) {
+    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(at));
+    x[0] = y.x;
+    x[1] = y.y;
+  } else {
+    static_assert(E == 4, "head sizes up to 128");
+    const uint2 w = *reinterpret_cast<const uint2*>(at);
+    const float2 y = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w.x)),
+                 z = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w.y));
+    x[0] = y.x;
+    x[1] = y.y;
+    x[2] = z.x;
+    x[3] = z.y;
+  }
+}
+
+// By a warp: the node's lineage in the lanes first, then N ancestors at a time (the
+// node itself first): their products by N-fold sums across the warp, after which lane
+// l has the score of ancestor l / (32 / N), so that cap, bias and exponential are
+// computed once for each.
 template <int D>
 __device__ __forceinline__ OwnPart<(D + 31) / 32> tree_part(const ScoredDecParams& p, int b, int hk,
                                                             int in_group, int node, int lane) {
-  constexpr int E = (D + 31) / 32;
+  constexpr int E = (D + 31) / 32, N = E == 1 ? 8 : 4, W = 32 / N;
   OwnPart<E> own;
   const int* parents = p.parents + static_cast<long long>(b) * p.n_q;
   const int up0 = lane < p.n_q ? __ldg(parents + lane) : -2,
             up1 = lane + 32 < p.n_q ? __ldg(parents + lane + 32) : -2;
-  auto up = [&](int at) {
+  // ancestor i (0: the node) in lane i of line0, ancestor i + 32 in lane i of line1
+  int line0 = node, line1 = node, at = node, length = 0;
+  while (at >= 0) {
+    if (lane == length) line0 = at;
+    if (lane == length - 32) line1 = at;
+    ++length;
     const int x = __shfl_sync(0xffffffffu, at < 32 ? up0 : up1, at & 31);
-    return x < -1 || x >= at ? -2 : x;
-  };
-  int root = node;
-  while (root >= 0) root = up(root);
-  own.node = root == -1;
+    at = x < -1 || x >= at ? -2 : x;
+  }
+  own.node = at == -1;
   own.m = -INFINITY;
   own.l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) own.a[e] = 0.f;
   if (!own.node) return own;
+  if (p.window >= 0) length = min(length, p.window + 1);
   const int head = hk * p.G + in_group;
-  const __nv_bfloat16* q = p.q + b * p.sq.b + head * p.sq.h + node * p.sq.n;
-  const __nv_bfloat16* k = p.k_tree + b * p.skt.b + hk * p.skt.h;
-  const __nv_bfloat16* v = p.v_tree + b * p.svt.b + hk * p.svt.h;
-  const float slope = p.slopes != nullptr ? __ldg(p.slopes + head) : 0.f;
+  const int el = min(lane * E, D - E);  // (d = 16: the upper lanes have no part)
+  const __nv_bfloat16* q = p.q + b * p.sq.b + head * p.sq.h + node * p.sq.n + el;
+  const __nv_bfloat16* k = p.k_tree + b * p.skt.b + hk * p.skt.h + el;
+  const __nv_bfloat16* v = p.v_tree + b * p.svt.b + hk * p.svt.h + el;
+  const float slope = p.slopes != nullptr ? __ldg(p.slopes + head) * kLog2e : 0.f;
   float x[E];
+  load_values<E>(q, x);
+  float l = 0.f;  // of this lane's ancestors
+  for (int back = 0; back < length; back += N) {
+    float s[N], val[N][E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = lane + 32 * e < D ? __bfloat162float(q[lane + 32 * e]) : 0.f;
-  // four ancestors at a time, the node itself first
-  int at = node, back = 0;
-  while (at >= 0 && (p.window < 0 || back <= p.window)) {
-    int who[4];
-    float key[4][E], val[4][E], s[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      who[i] = at >= 0 && (p.window < 0 || back + i <= p.window) ? at : -1;
-      if (at >= 0) at = up(at);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const bool in = who[i] >= 0 && lane + 32 * e < D;
-        key[i][e] = in ? __bfloat162float(k[who[i] * p.skt.n + lane + 32 * e]) : 0.f;
-        val[i][e] = in ? __bfloat162float(v[who[i] * p.svt.n + lane + 32 * e]) : 0.f;
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; ++i) {
+      // (past the last: the node itself, at weight 0)
+      const int far = back + i;
+      int who = __shfl_sync(0xffffffffu, far < 32 ? line0 : line1, far & 31);
+      if (far >= length) who = node;
+      float key[E];
+      load_values<E>(k + who * p.skt.n, key);
+      load_values<E>(v + who * p.svt.n, val[i]);
       s[i] = 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[i] = fmaf(x[e], key[i][e], s[i]);
+      for (int e = 0; e < E; ++e) {
+        if (D >= 32 || lane < D) s[i] = fmaf(x[e], key[e], s[i]);
+        if (far >= length) val[i][e] = 0.f;
+      }
     }
+    // each step halves the ancestors that a lane sums, by exchange with lane ^ w
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1)
+    for (int w = 16, have = N; w > 0; w >>= 1) {
+      if (have > 1) {
+        have >>= 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], w);
-    float top = own.m;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[i] *= p.scale;
-      if (p.softcap > 0.f) s[i] = p.softcap * tanhf(s[i] / p.softcap);
-      s[i] = who[i] >= 0 ? (s[i] - slope * static_cast<float>(back + i)) * kLog2e : -INFINITY;
-      top = fmaxf(top, s[i]);
+        for (int i = 0; i < have; ++i) {
+          const bool upper = lane & w;
+          const float keep = upper ? s[i + have] : s[i], give = upper ? s[i] : s[i + have];
+          s[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
+      } else {
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], w);
+      }
     }
+    const int far = back + lane / W;
+    float y = s[0] * p.scale;
+    if (p.softcap > 0.f) y = p.softcap * tanhf(y / p.softcap);
+    y = far < length ? fmaf(-slope, static_cast<float>(far), y * kLog2e) : -INFINITY;
+    float top = y;
+#pragma unroll
+    for (int w = 16; w >= W; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+    top = fmaxf(top, own.m);
     const float alpha = ex2(own.m - top);  // 0 at first
     own.m = top;
-    own.l *= alpha;
+    const float share = ex2(y - top);
+    l = fmaf(l, alpha, share);
 #pragma unroll
     for (int e = 0; e < E; ++e) own.a[e] *= alpha;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float w = ex2(s[i] - top);
-      own.l += w;
+    for (int i = 0; i < N; ++i) {
+      const float w = __shfl_sync(0xffffffffu, share, i * W);
 #pragma unroll
       for (int e = 0; e < E; ++e) own.a[e] = fmaf(w, val[i][e], own.a[e]);
     }
-    back += 4;
   }
+#pragma unroll
+  for (int w = 16; w >= W; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
+  own.l = l;
   return own;
 }
 
@@ -1035,11 +1075,14 @@ __device__ __forceinline__ OwnPart<(D + 31) / 32> tree_part(const ScoredDecParam
 // the first kernel covered are complete; units without keys get O = 0 and LSE
 // = -inf here.
 template <int D, int ROWS, bool ONE_WARP, bool TREE>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, TREE ? 5 : 1)
     attn_decode_scored_merge_kernel(const ScoredDecParams p, unsigned total_rows) {
   constexpr int E = (D + 31) / 32;
   __shared__ float joined[ONE_WARP ? 1 : 8][D + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // a lane's values: side by side for a tree's, as its loads are
+  using Values = typename std::conditional<E == 4, float4, float2>::type;
+  auto elem = [lane](int e) { return TREE ? lane * E + e : lane + 32 * e; };
   const unsigned id = ONE_WARP ? blockIdx.x * 8 + warp : blockIdx.x;
   const unsigned R = p.G * p.n_q;  // rows of one key head
   const unsigned bk = id / R;
@@ -1049,14 +1092,17 @@ __global__ void __launch_bounds__(256)
   OwnPart<E> own_part;  // TREE: of the row's ancestors
   if (TREE && id < total_rows && (ONE_WARP || warp == 0))
     own_part = tree_part<D>(p, b, hk, gr / p.n_q, gr % p.n_q, lane);
+  int cached_len = 0;
+  if (TREE && p.whole && id < total_rows) {
+    cached_len = p.L_max;
+    if (p.cache_lens != nullptr) cached_len = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
+  }
   grid_dependency_wait();  // the parts are complete
   if (id >= total_rows) return;
   unsigned w0 = 0, u0 = 0, share = 1;
   int n;
   if (TREE && p.whole) {
-    int L = p.L_max;
-    if (p.cache_lens != nullptr) L = min(max(__ldg(p.cache_lens + b), 0), p.L_max);
-    n = L > 0 && p.window != 0 ? 1 : 0;
+    n = cached_len > 0 && p.window != 0 ? 1 : 0;
   } else {
     const unsigned here = p.first[b], next = p.first[b + 1];
     share = share_of(p.first[p.B], p.warps);
@@ -1080,59 +1126,78 @@ __global__ void __launch_bounds__(256)
   float mm = -INFINITY, from = -INFINITY, ll = 0.f, a[E] = {};
   // {maximum, sum, what the values are relative to}
   auto tail_of = [](const float* at) { return *reinterpret_cast<const float4*>(at + D); };
-  for (int i = lane; i < n; i += 32) {
-    const float4 x = tail_of(part_at(i));
-    mm = fmaxf(mm, x.x);
-    from = fmaxf(from, x.z);
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) {
-    mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
-    from = fmaxf(from, __shfl_xor_sync(0xffffffffu, from, x));
-  }
-  const float mb = mm == -INFINITY ? 0.f : mm, fb = from == -INFINITY ? 0.f : from;
-  // 32 of this warp's parts at a time: their weights in the lanes, then their values
-  for (int c = first; c < n; c += 32 * STEP) {
-    const int own = c + lane * STEP;
-    float f = 0.f;
-    if (own < n) {
-      const float4 x = tail_of(part_at(own));
-      f = ex2(x.z - fb);
-      ll += ex2(x.x - mb) * x.y;
-    }
-    const int here_n = min((n - c + STEP - 1) / STEP, 32);
-    for (int y0 = 0; y0 < here_n; y0 += 4) {  // four parts' loads in flight
-      float x[4][E];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        // (past the last part: the last one again, at weight 0)
-        const float* at = part_at(c + min(y0 + y, here_n - 1) * STEP);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[y][e] = lane + 32 * e < D ? at[lane + 32 * e] : 0.f;
-      }
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float fy = __shfl_sync(0xffffffffu, f, y0 + y);
-#pragma unroll
-        for (int e = 0; e < E; ++e) a[e] = fmaf(fy, x[y][e], a[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, x);
-  if (!ONE_WARP) {
+  float mb = 0.f;
+  if (TREE && ONE_WARP && n == 1) {  // one round of loads
+    const float4 x = tail_of(part);
+    mm = x.x;
+    from = x.z;
+    ll = mm == -INFINITY ? 0.f : x.y;
+    mb = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (lane + 32 * e < D) joined[warp][lane + 32 * e] = a[e];
-    if (lane == 0) joined[warp][D] = ll;
-    __syncthreads();
-    if (warp != 0) return;
+      if (elem(e) < D) a[e] = part[elem(e)];
+  } else {
+    for (int i = lane; i < n; i += 32) {
+      const float4 x = tail_of(part_at(i));
+      mm = fmaxf(mm, x.x);
+      from = fmaxf(from, x.z);
+    }
 #pragma unroll
-    for (int o = 1; o < 8; ++o) {
+    for (int x = 16; x > 0; x >>= 1) {
+      mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, x));
+      from = fmaxf(from, __shfl_xor_sync(0xffffffffu, from, x));
+    }
+    mb = mm == -INFINITY ? 0.f : mm;
+    const float fb = from == -INFINITY ? 0.f : from;
+    // 32 of this warp's parts at a time: their weights in the lanes, then their values
+    for (int c = first; c < n; c += 32 * STEP) {
+      const int own = c + lane * STEP;
+      float f = 0.f;
+      if (own < n) {
+        const float4 x = tail_of(part_at(own));
+        f = ex2(x.z - fb);
+        ll += ex2(x.x - mb) * x.y;
+      }
+      const int here_n = min((n - c + STEP - 1) / STEP, 32);
+      for (int y0 = 0; y0 < here_n; y0 += 4) {  // four parts' loads in flight
+        float x[4][E];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          // (past the last part: the last one again, at weight 0)
+          const float* at = part_at(c + min(y0 + y, here_n - 1) * STEP);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if (TREE && E > 1) {
+              *reinterpret_cast<Values*>(x[y]) = *reinterpret_cast<const Values*>(at + lane * E);
+              break;
+            }
+            x[y][e] = elem(e) < D ? at[elem(e)] : 0.f;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float fy = __shfl_sync(0xffffffffu, f, y0 + y);
+#pragma unroll
+          for (int e = 0; e < E; ++e) a[e] = fmaf(fy, x[y][e], a[e]);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, x);
+    if (!ONE_WARP) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (lane + 32 * e < D) a[e] += joined[o][lane + 32 * e];
-      ll += joined[o][D];
+        if (elem(e) < D) joined[warp][elem(e)] = a[e];
+      if (lane == 0) joined[warp][D] = ll;
+      __syncthreads();
+      if (warp != 0) return;
+#pragma unroll
+      for (int o = 1; o < 8; ++o) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (elem(e) < D) a[e] += joined[o][elem(e)];
+        ll += joined[o][D];
+      }
     }
   }
   const int head = hk * p.G + gr / p.n_q, qi = gr % p.n_q;
@@ -1144,12 +1209,17 @@ __global__ void __launch_bounds__(256)
     const float most = fmaxf(cached ? mm : -INFINITY, own_part.node ? own_part.m : -INFINITY);
     const float w1 = cached ? ex2(mm - most) : 0.f, w2 = own_part.node ? ex2(own_part.m - most) : 0.f;
     const float sum = fmaf(w1, ll, w2 * own_part.l), inv = sum > 0.f ? 1.f / sum : 0.f;
+    float y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      float y = own_part.node ? w2 * own_part.a[e] : 0.f;
-      if (cached) y = fmaf(w1, a[e] * fac * fac, y);
-      if (lane + 32 * e < D) out[lane + 32 * e] = __float2bfloat16_rn(y * inv);
+      y[e] = own_part.node ? w2 * own_part.a[e] : 0.f;
+      if (cached) y[e] = fmaf(w1, a[e] * fac * fac, y[e]);
+      if (E == 1 && lane < D) out[lane] = __float2bfloat16_rn(y[e] * inv);
     }
+#pragma unroll
+    for (int e = 0; e + 1 < E; e += 2)
+      reinterpret_cast<__nv_bfloat162*>(out + lane * E)[e / 2] =
+          __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
     if (lane == 0 && p.lse != nullptr)
       p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
           sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
@@ -1158,7 +1228,7 @@ __global__ void __launch_bounds__(256)
   const float inv = (ll > 0.f ? 1.f / ll : 0.f) * fac;
 #pragma unroll
   for (int e = 0; e < E; ++e)
-    if (lane + 32 * e < D) out[lane + 32 * e] = __float2bfloat16_rn(a[e] * fac * inv);
+    if (elem(e) < D) out[elem(e)] = __float2bfloat16_rn(a[e] * fac * inv);
   if (lane == 0 && p.lse != nullptr)
     p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
         ll > 0.f ? (mm + __log2f(ll)) * kLn2 : -INFINITY;

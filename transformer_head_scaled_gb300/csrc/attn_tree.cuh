@@ -846,11 +846,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int D>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p, int ctas) {
   grid_dependency_wait();
-  const long long at = blockIdx.x * 8LL + (threadIdx.x >> 5);
-  if (at >= static_cast<long long>(p.B) * p.HK * p.rows) return;
+  // (one CTA for eight rows of a key head: divisions of 32 bits, by what is the same
+  // for all of it)
+  const unsigned eights = (p.rows + 7u) / 8u, bk = blockIdx.x / eights;
+  const int b = bk / static_cast<unsigned>(p.HK), hk = bk - b * p.HK;
+  const int row = (blockIdx.x - bk * eights) * 8 + (threadIdx.x >> 5);
+  if (row >= p.rows) return;
   const int lane = threadIdx.x & 31;
-  const int row = at % p.rows;
-  const int hk = at / p.rows % p.HK, b = at / p.rows / p.HK;
   const int subs = p.HK * p.blocks;
   const unsigned f0 = p.first[b], f1 = p.first[b + 1];
   const unsigned tiles = (f1 - f0) / subs;
@@ -869,21 +871,28 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p,
   for (int w = 16; w > 0; w >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
   constexpr int E = D < 32 ? 1 : D / 32;
   float y[E] = {}, sum = 0.f;
+  using Values = typename std::conditional<E == 4, float4,
+                                           typename std::conditional<E == 2, float2, float>::type>::type;
 #pragma unroll 4
   for (unsigned c = c0; c <= c1; ++c) {
     const float* x = part(c);
-    const float w = x[D + 1] > 0.f ? ex2(x[D] - most) : 0.f;
-    sum = fmaf(w, x[D + 1], sum);
+    const float2 tail = *reinterpret_cast<const float2*>(x + D);
+    const float w = tail.y > 0.f ? ex2(tail.x - most) : 0.f;
+    sum = fmaf(w, tail.y, sum);
+    if (lane * E < D) {
+      const Values v = *reinterpret_cast<const Values*>(x + lane * E);
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (lane * E + e < D) y[e] = fmaf(w, x[lane * E + e], y[e]);
+      for (int e = 0; e < E; ++e) y[e] = fmaf(w, reinterpret_cast<const float*>(&v)[e], y[e]);
+    }
   }
   const int g = row / p.n, node = row - g * p.n;
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   __nv_bfloat16* out = p.o + b * p.so.b + (hk * p.G + g) * p.so.h + node * p.so.n;
+  if (E == 1 && lane < D) out[lane] = __float2bfloat16_rn(y[0] * inv);
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (lane * E + e < D) out[lane * E + e] = __float2bfloat16_rn(y[e] * inv);
+  for (int e = 0; e + 1 < E; e += 2)
+    reinterpret_cast<__nv_bfloat162*>(out + lane * E)[e / 2] =
+        __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
   if (lane == 0 && p.lse != nullptr)
     p.lse[(static_cast<size_t>(b) * p.H + hk * p.G + g) * p.n + node] =
         sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
@@ -901,9 +910,9 @@ cudaError_t launch_tree_d(const TreeParams& p, const CUtensorMap* maps, const Tr
   attn_tree_kernel<C, CHANGED>
       <<<plan.ctas, NUM_THREADS, smem, ctx.stream>>>(maps[0], maps[1], maps[2], maps[3], p);
   if ((err = cudaGetLastError()) != cudaSuccess || plan.whole) return err;
-  const long long rows = static_cast<long long>(p.B) * p.HK * p.rows;
-  return launch_dependent(attn_tree_join_kernel<C::D>, dim3(static_cast<unsigned>((rows + 7) / 8)),
-                          dim3(256), 0, ctx.stream, p, plan.ctas);
+  return launch_dependent(attn_tree_join_kernel<C::D>,
+                          dim3(static_cast<unsigned>(p.B) * p.HK * ((p.rows + 7) / 8)), dim3(256), 0,
+                          ctx.stream, p, plan.ctas);
 }
 
 template <int FMT, int D>
