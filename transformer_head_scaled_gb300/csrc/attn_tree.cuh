@@ -53,6 +53,7 @@ using namespace ptx;
 enum CacheFormat : int { kCacheBf16 = 0, kCacheE4M3 = 1, kCacheInt8 = 2 };
 
 constexpr int BM = 128;        // query rows per tile (= tensor-memory lanes)
+constexpr int kTreeCapped = 1, kTreeSlopes = 2;  // what a kernel does to the scores
 constexpr int kBlockRows = 2 * BM;
 constexpr int AUX_WARP = 8;
 constexpr int KLOAD_WARP = 12;
@@ -430,7 +431,7 @@ __device__ __forceinline__ void clear_rows(const TreeParams& p, TreeSmem<C>& sm,
 namespace attn {
 namespace {
 
-template <class C, bool CHANGED>
+template <class C, int MODE>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attn_tree_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                           p.limit_ns, &never);
     }
   } else {
-    ok = softmax_many<C, CHANGED>(p, sm, tmem, warp >> 2, warp & 3, lane);
+    ok = softmax_many<C, MODE>(p, sm, tmem, warp >> 2, warp & 3, lane);
     if (!ok) fail();
   }
 
@@ -898,16 +899,16 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p,
         sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <class C, bool CHANGED>
+template <class C, int MODE>
 cudaError_t launch_tree_d(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
                           const LaunchCtx& ctx) {
   static_assert(sizeof(TreeSmem<C>) + 1024 <= 232448, "dynamic shared memory per CTA");
   const size_t smem = sizeof(TreeSmem<C>) + 1024;
-  cudaError_t err = cudaFuncSetAttribute(attn_tree_kernel<C, CHANGED>,
+  cudaError_t err = cudaFuncSetAttribute(attn_tree_kernel<C, MODE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
   if (err != cudaSuccess) return err;
-  attn_tree_kernel<C, CHANGED>
+  attn_tree_kernel<C, MODE>
       <<<plan.ctas, NUM_THREADS, smem, ctx.stream>>>(maps[0], maps[1], maps[2], maps[3], p);
   if ((err = cudaGetLastError()) != cudaSuccess || plan.whole) return err;
   return launch_dependent(attn_tree_join_kernel<C::D>,
@@ -919,8 +920,12 @@ template <int FMT, int D>
 cudaError_t launch_tree_mode(const TreeParams& p, const CUtensorMap* maps, const TreePlan& plan,
                              const LaunchCtx& ctx) {
   using C = TCfg<FMT, D>;
-  return p.capped || p.slopes ? launch_tree_d<C, true>(p, maps, plan, ctx)
-                              : launch_tree_d<C, false>(p, maps, plan, ctx);
+  // (a kernel for each: code that is not there costs no instruction fetches)
+  if (p.capped)
+    return p.slopes ? launch_tree_d<C, kTreeCapped | kTreeSlopes>(p, maps, plan, ctx)
+                    : launch_tree_d<C, kTreeCapped>(p, maps, plan, ctx);
+  return p.slopes ? launch_tree_d<C, kTreeSlopes>(p, maps, plan, ctx)
+                  : launch_tree_d<C, 0>(p, maps, plan, ctx);
 }
 
 template <int FMT>

@@ -138,11 +138,11 @@ __device__ __forceinline__ bool mma_many(const TreeParams& p, TreeSmem<C>& sm, u
   return ok;
 }
 
-template <class C, bool CHANGED>
+template <class C, int MODE>
 __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& sm, uint32_t tmem,
                                              int s, int quarter, int lane) {
   constexpr int D = C::D, BN = C::BN;
-  constexpr bool Q8 = C::Q8;
+  constexpr bool Q8 = C::Q8, CAPPED = MODE & kTreeCapped, SLOPES = MODE & kTreeSlopes;
   const volatile int* abort = &sm.abort;
   bool ok = true;
   const int at = quarter * 32 + lane;  // tensor-memory lane
@@ -173,7 +173,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
     const int g = row / p.n, node = row - g * p.n, head = it.hk * p.G + g;
     const int depth = max(sm.depth[slot][node], 0);
     const bool alive = valid && sm.depth[slot][node] >= 0;
-    const float slope2 = CHANGED && p.slopes ? kLog2e * __ldg(p.slopes + head) : 0.f;
+    const float slope2 = SLOPES ? kLog2e * __ldg(p.slopes + head) : 0.f;
     // position of the row's first visible key, for the window
     const int first_key = p.window >= 0 ? it.L + depth - p.window : 0;
     float m = -INFINITY, l = 0.f;
@@ -197,9 +197,9 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
       float factor[NC / 16];
 #pragma unroll
       for (int c = 0; c < NC / 16; ++c)
-        factor[c] = (Q8 ? scale_at(16 * c, 0) : 1.f) * (CHANGED && p.capped ? 1.f : p.scale_log2);
+        factor[c] = (Q8 ? scale_at(16 * c, 0) : 1.f) * (CAPPED ? 1.f : p.scale_log2);
       // (a factor of zero would make NaN of masked scores)
-      if constexpr (Q8 && !CHANGED) {
+      if constexpr (Q8 && MODE == 0) {
 #pragma unroll
         for (int c = 0; c < NC / 16; ++c) factor[c] = fmaxf(factor[c], 0x1p-126f);
       }
@@ -209,9 +209,9 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
       tmem_ld_wait(x[0]);
 #pragma unroll
       for (int c = 1; c < NC / 32; ++c) reg_fence(x[c]);
-      if constexpr (CHANGED) {
+      if constexpr (MODE != 0) {
         // finished scores in log2 units, but for `off`
-        if (p.capped) {
+        if constexpr (CAPPED) {
           float big = 0.f;
 #pragma unroll
           for (int c = 0; c < NC / 32; ++c)
@@ -260,10 +260,15 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
 #pragma unroll
           for (int c = 0; c < NC / 32; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              x[c][i] = __float_as_uint(__uint_as_float(x[c][i]) * factor[2 * c + i / 16]);
+            for (int i = 0; i < 32; i += 2) {
+              float a, b;
+              fma2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]),
+                   factor[2 * c + i / 16], factor[2 * c + i / 16], 0.f, 0.f);
+              x[c][i] = __float_as_uint(a);
+              x[c][i + 1] = __float_as_uint(b);
+            }
         }
-        if (p.slopes) {
+        if constexpr (SLOPES) {
           if (tree) {
             off = -slope2 * depth;
 #pragma unroll
@@ -312,7 +317,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
           for (int e = 0; e < 2; ++e)
             m2[e] = max3(m2[e], __uint_as_float(x[c >> 1][(c & 1) * 16 + i + 2 * e]),
                          __uint_as_float(x[c >> 1][(c & 1) * 16 + i + 2 * e + 1]));
-        mt = fmaxf(mt, fmaxf(m2[0], m2[1]) * (CHANGED ? 1.f : factor[c]));
+        mt = fmaxf(mt, fmaxf(m2[0], m2[1]) * (MODE != 0 ? 1.f : factor[c]));
       }
       mt += off;
       float alpha = 1.f;
@@ -346,7 +351,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
 #pragma unroll
           for (int i = 16 * half; i < 16 * half + 16; i += 2) {
             float a, b;
-            if constexpr (CHANGED)
+            if constexpr (MODE != 0)
               add2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]), neg_m, neg_m);
             else
               fma2(a, b, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]), f, f, neg_m,
