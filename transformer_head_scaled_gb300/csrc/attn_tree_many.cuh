@@ -11,7 +11,7 @@ namespace {
 // has read P there, PV(u - 1) right after it, once its P is there.  A ring slot is
 // released by one arrival per stream: a commit by a stream that used the tile, a
 // plain arrival by one that did not.
-template <class C>
+template <class C, int MODE>
 __device__ __forceinline__ bool mma_many(const TreeParams& p, TreeSmem<C>& sm, uint32_t tmem,
                                          int s, int lane) {
   constexpr int D = C::D, BN = C::BN, KSTAGES = C::KSTAGES, VSTAGES = C::VSTAGES;
@@ -78,7 +78,7 @@ __device__ __forceinline__ bool mma_many(const TreeParams& p, TreeSmem<C>& sm, u
     bool first = true;
     for (int j = 0; j < it.n && ok; ++j) {
       const uint32_t g = g0 + j;
-      const int t = it.t0 + j, parts = parts_of<C>(it, t, p.n);
+      const int t = tile_of<MODE>(it, j), parts = parts_of<C>(it, t, p.n);
       int sub0 = 0, sub1 = parts;  // this stream's
       if (!both) {
         sub0 = C::NSUB == 1 ? 0 : s;
@@ -375,25 +375,31 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
       tmem_st_wait();
     };
 
+    // lane i: the scale of the i-th block of keys of the j-th tile, 8 + i: of values
+    auto scales_of = [&](int j) {
+      float sc = 1.f;
+      const int t = j < it.n ? tile_of<MODE>(it, j) : it.ctx;
+      if (t < it.ctx) {
+        const int base = it.base0 + t * BN, blk = (base >> p.T_log2) + (lane & 7);
+        sc = 0.f;
+        if (lane < 16 && (blk << p.T_log2) < min(it.L, base + BN) &&
+            ((blk + 1) << p.T_log2) > it.key0)
+          sc = __ldg((lane < 8 ? p.k_scale : p.v_scale) +
+                     (static_cast<long long>(it.b) * p.HK + it.hk) * p.num_blocks + blk);
+      }
+      return sc;
+    };
+    float next_sc = Q8 ? scales_of(0) : 1.f;
     for (int j = 0; j < it.n && ok; ++j) {
-      const int t = it.t0 + j, parts = parts_of<C>(it, t, p.n);
+      const int t = tile_of<MODE>(it, j), parts = parts_of<C>(it, t, p.n);
       int sub0 = 0, sub1 = parts;
       if (!both) {
         sub0 = C::NSUB == 1 ? 0 : s;
         sub1 = C::NSUB == 1 ? ((j & 1) == s ? 1 : 0) : min(s + 1, parts);
       }
+      const float sc = next_sc;
+      if constexpr (Q8) next_sc = scales_of(j + 1);  // (loaded a tile ahead)
       if (sub0 >= sub1) continue;
-      float sc = 1.f;  // lane i: the scale of the tile's i-th block of keys, 8 + i: of values
-      if constexpr (Q8) {
-        if (t < it.ctx) {
-          const int base = it.base0 + t * BN, blk = (base >> p.T_log2) + (lane & 7);
-          sc = 0.f;
-          if (lane < 16 && (blk << p.T_log2) < min(it.L, base + BN) &&
-              ((blk + 1) << p.T_log2) > it.key0)
-            sc = __ldg((lane < 8 ? p.k_scale : p.v_scale) +
-                       (static_cast<long long>(it.b) * p.HK + it.hk) * p.num_blocks + blk);
-        }
-      }
       for (int sub = sub0; sub < sub1; ++sub) {
         if (!wait(&sm.s_full[s][u & 1], (u >> 1) & 1)) break;
         tc_fence_after();
@@ -421,8 +427,10 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
       m = -INFINITY;
       l = 0.f;
     }
-    float* part = p.part + ((static_cast<size_t>(blockIdx.x) * 2 + it.slot) * p.block_rows + r) *
-                               (D + kPartTail);
+    // (values of neighbouring rows side by side, four of each: a warp's stores are whole lines)
+    float* part = p.part + (static_cast<size_t>(blockIdx.x) * 2 + it.slot) * p.block_rows *
+                               (D + kPartTail) + 4 * r;
+    const int column = 4 * p.block_rows;  // from four values to the next four
     const int split = twice ? 2 : 1;
     const int pidx = s * split + copy;  // which part of the row (not both)
     float weight = alive ? 1.f : 0.f, most = m, sum = l;
@@ -445,7 +453,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
     const bool writer = valid && (both || pidx == 0);
     if (writer) {
       if (!it.whole)
-        *reinterpret_cast<float2*>(part + D) = make_float2(most, sum);
+        *reinterpret_cast<float2*>(part + (D / 4) * column) = make_float2(most, sum);
       else if (p.lse != nullptr)
         p.lse[(static_cast<size_t>(it.b) * p.H + head) * p.n + node] =
             sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
@@ -494,10 +502,10 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
                                pack_bf16x2(__uint_as_float(y[6]), __uint_as_float(y[7])));
           }
         } else {
-          uint4* to = reinterpret_cast<uint4*>(part + c);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            to[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            *reinterpret_cast<uint4*>(part + (c / 4 + e) * column) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
       if (!both && !join()) break;
