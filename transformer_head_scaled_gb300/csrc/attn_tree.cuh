@@ -288,6 +288,16 @@ __device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, u
   return mbar_try_wait(bar, parity) || mbar_wait_on(bar, parity, limit_ns, abort);
 }
 
+// 16 bytes to shared memory, asynchronously; zeros where there are none.
+__device__ __forceinline__ void copy_chunk(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(there ? 16u : 0u)
+               : "memory");
+}
+__device__ __forceinline__ void copy_chunks_done() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // One arrival for a whole warp, behind what all its lanes did.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -679,34 +689,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           !wait(&sm.q_empty[slot ^ 1], ((items - 1) >> 1) & 1))
         break;
       was_wide = wide;
-      // (rows by a product with 1 / n: exact for numbers this small.  Loads go together,
-      // of the first row where there is none: a branch around each would make them wait
-      // for one another)
+      // (rows by a product with 1 / n: exact for numbers this small.  All copies are under
+      // way at once: in batches of 8 loads the first tile's scores came 3 us later)
       constexpr int CPR = D / 8;  // 16-byte chunks of a row
-      constexpr int BATCH = CPR < 8 ? CPR : 8;
       const int tiles = it.split == 0 ? 2 : 1;
       const int lanes = it.split == 0 ? BM : BM / it.split;
       const __nv_bfloat16* q = p.q + it.b * p.sq.b + static_cast<long long>(it.hk) * p.G * p.sq.h;
       for (int s = 0; s < tiles; ++s) {
-#pragma unroll 1
-        for (int e0 = tid; e0 < BM * CPR; e0 += 128 * BATCH) {
-          uint4 x[BATCH];
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const int at = (e0 + 128 * i) / CPR, c = (e0 + 128 * i) % CPR;
-            const int r = s * BM + (at & (lanes - 1)), row = it.row0 + (r < it.rows ? r : 0);
-            const int g = static_cast<int>((row + 0.5f) * p.inv_n);
-            x[i] = __ldg(reinterpret_cast<const uint4*>(q + g * p.sq.h + (row - g * p.n) * p.sq.n) + c);
-          }
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const int at = (e0 + 128 * i) / CPR, c = (e0 + 128 * i) % CPR;
-            if (s * BM + (at & (lanes - 1)) >= it.rows) x[i] = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(sm.q_tile(items, wide, s) + (c / C::CPB) * C::Q_BLOCK + at * C::RB +
-                                      (((c % C::CPB) ^ C::swz(at)) << 4)) = x[i];
-          }
+        const uint32_t to = smem_u32(sm.q_tile(items, wide, s));
+#pragma unroll 4
+        for (int e = tid; e < BM * CPR; e += 128) {
+          const int at = e / CPR, c = e % CPR;
+          const int r = s * BM + (at & (lanes - 1));
+          const bool there = r < it.rows;
+          const int row = it.row0 + (there ? r : 0), g = static_cast<int>((row + 0.5f) * p.inv_n);
+          copy_chunk(to + (c / C::CPB) * C::Q_BLOCK + at * C::RB + (((c % C::CPB) ^ C::swz(at)) << 4),
+                     q + g * p.sq.h + (row - g * p.n) * p.sq.n + c * 8, there);
         }
       }
+      copy_chunks_done();
       fence_proxy_async_smem();
       if (items == 0) warp_arrive(smem_u32(&sm.q_there));
       if (has[slot] != it.b) {
