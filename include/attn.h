@@ -470,11 +470,14 @@ size_t attn_decode_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int L
  *   workspace, workspace_bytes : at least attn_decode_tree_workspace_bytes(...)
  *              bytes, 16-byte aligned; may be NULL when that is 0.  Its contents
  *              on entry do not matter; calls that may overlap need one each.
- *   d_k      : 16, 32, 64 or 128, B*h*n <= 2^24, L_max <= 2^30 (else
+ *   d_k      : 16, 32, 64 or 128, B*h*n <= 2^24, L_max <= 2^30 and
+ *              B*h_kv*ceil(h/h_kv*n / 32)*(L_max/16 + 8) < 2^31 (else
  *              ATTN_ERR_UNSUPPORTED).
  * Scores, cap, bias and softmax are computed in fp32; 8-bit codes enter the
- * products exactly; P (times the value scale) is rounded to bf16 before the
- * second product.
+ * products exactly.  P is rounded before the second product: to bf16 (times the
+ * value scale of an 8-bit cache), or, where key heads have few query rows, against
+ * 8-bit caches to f16 as in attn_decode_scored (with q brought to f16 as there) and
+ * for the tree's own keys not at all.  One or two kernels on `stream`.
  */
 int attn_decode_tree(const void* q, const void* k_tree, const void* v_tree, const void* k_cache,
                      const void* v_cache, const float* k_scale, const float* v_scale,
@@ -523,7 +526,9 @@ typedef enum { ATTN_PROB_F32 = 0, ATTN_PROB_BF16 = 1 } attn_prob_type;
  *              read without one); NULL: contiguous.  V is contiguous.
  *   n <= 128, V <= 2^24, B <= 2^24 (else ATTN_ERR_UNSUPPORTED).
  * r is rounded to fp32 and summed exactly in multiples of 2^-60: the answer does
- * not depend on the order of the sums.  One kernel on `stream`.
+ * not depend on the order of the sums.  C, Z and the tests of single nodes are held
+ * as pairs of fp32 numbers (48 bits).  One kernel on `stream`, as clusters of up to
+ * 16 CTAs.
  */
 int attn_tree_verify(const void* target, const void* draft, const int* tokens,
                      const int* parents, const float* uniforms, int* path, int* path_lens,

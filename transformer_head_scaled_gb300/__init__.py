@@ -13,7 +13,8 @@ def __getattr__(name):
                 "decode_workspace_bytes",
                 "attn_mask_plan", "attn_fwd_scored", "attn_bwd_scored", "attn_cache_append",
                 "attn_decode_scored", "mask_plan_bytes", "bwd_scored_workspace_bytes",
-                "decode_scored_workspace_bytes",
+                "decode_scored_workspace_bytes", "attn_decode_tree", "attn_tree_verify",
+                "attn_cache_append_tree", "decode_tree_workspace_bytes",
                 "load", "AttnError", "status_string", "check"):
         from . import binding
         return getattr(binding, name)

@@ -426,13 +426,14 @@ struct TreeOwn {
   RowStrides sk, sv;
 };
 // Whether it is taken.  Measured against the tensor-memory kernel below (us, this one
-// first): 16 x 8 heads x 4096-8192 tokens, d = 64, bf16, 8 rows of a key head 44 and 63, 16 rows
-// 51 and 64, 32 rows 72 and 66, e4m3 30 and 73, 44 and 74, 71 and 75; d = 128, e4m3, 16 rows
-// 66 and 105, 32 rows 124 and 106, 64 rows 166 and 112; d = 32, e4m3, 64 rows 66 and 79; and
-// with few units it starts sooner: 8 heads x 4096 tokens, d = 128, 32 rows 25 and 39.
+// first).  16 sequences of 4096-8192 tokens, 8 key heads: d = 64, bf16, 8 rows of a key
+// head 45 and 62, 16 rows 51 and 62, 32 rows 70 and 65, e4m3 31 and 78, 44 and 78, 70 and
+// 79; d = 128, 16 rows 84 and 84, e4m3 58 and 109, 32 rows 114 and 86, 107 and 110.  With
+// few units it starts sooner: one of 4096 tokens, 8 key heads, d = 128, 32 rows 29 and 34
+// (64 rows 29 and 36, but 72 and 58 at 32768 tokens).  d = 32, 32 rows 41 and 54, 64 rows
+// 73 and 55, e4m3 68 and 72.
 inline bool tree_few(int B, int HK, int rows, int d) {
-  return rows <= 16 || (rows <= 32 && (d < 128 || static_cast<long long>(B) * HK <= 32)) ||
-         (rows <= 64 && d <= 32);
+  return rows <= 16 || (rows <= 32 && (d < 128 || static_cast<long long>(B) * HK <= 32));
 }
 ScoredDecodePlan tree_few_plan(int B, int H, int HK, int n, int seen, int d, int elem_bytes,
                                int num_sms);
