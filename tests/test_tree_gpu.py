@@ -122,6 +122,11 @@ CASES = [
     (1, 3, 1, 10, 9000, 32, 128, 0.0, False, None, "star", [8991]),
     (2, 2, 2, 32, 260, 16, 16, 0.0, True, 64, "chain", [260, 30]),
     (5, 2, 1, 3, 640, 16, 64, 0.0, False, None, "holes", [640, 1, 0, 333, 64]),
+    # many query rows, biased: the cached tiles from the newest on, in runs, with windows
+    (2, 8, 2, 33, 1500, 64, 32, 0.0, True, 700, "random", [1500, 901]),
+    (1, 16, 2, 70, 2100, 128, 128, 30.0, True, None, "random", [2100]),
+    (3, 8, 2, 20, 700, 32, 16, 20.0, True, 130, "holes", [700, 3, 0]),
+    (2, 6, 2, 13, 5000, 16, 64, 0.0, True, None, "random", [5000, 2049]),
     # query rows of a key head on both sides of where the kernel changes
     (17, 4, 2, 8, 130, 128, 64, 0.0, False, None, "random", list(range(114, 131))),    # 16 rows
     (17, 2, 2, 17, 130, 128, 64, 0.0, False, None, "random", list(range(114, 131))),   # 17 of 34
@@ -283,10 +288,11 @@ def test_rows_of_other_tensors_are_left_alone():
 
 
 @TYPES
-def test_captured_step_and_two_streams(dtype):
+@pytest.mark.parametrize("n", [30, 4], ids=["many", "few"])
+def test_captured_step_and_two_streams(dtype, n):
     """A captured call replayed on new inputs; calls of two streams at once, each
     with a workspace of its own."""
-    B, h, hk, n, L, d, block = 2, 8, 2, 30, 3000, 64, 64
+    B, h, hk, L, d, block = 2, 8, 2, 3000, 64, 64
     q = _random((B, h, n, d), 1).to(BF16)
     kt, vt = _random((B, hk, n, d), 8).to(BF16), _random((B, hk, n, d), 9).to(BF16)
     kc, ks, _ = _cache(B, hk, L, d, dtype, block, 2)

@@ -220,6 +220,20 @@ def test_verify_captured():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_verify_on_two_streams():
+    """Calls of two streams at once, of clusters of 16 CTAs and of one."""
+    cases = [_case(1, 9, 140000, torch.float32, True, 2), _case(300, 9, 900, BF16, False, 3)]
+    calls = [(p, tokens, _int(parents), u, q) for p, q, tokens, parents, u in cases]
+    want = [binding.attn_tree_verify(*c) for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [(i, binding.attn_tree_verify(*calls[i], stream=streams[i])) for _ in range(8)
+           for i in (0, 1)]
+    torch.cuda.synchronize()
+    for i, res in got:
+        assert all(torch.equal(a, b) for a, b in zip(res, want[i]))
+
+
 def test_verify_refusals():
     p = torch.full((2, 3, 8), 0.125, device="cuda")
     ids, u = torch.zeros((2, 3), dtype=torch.int32, device="cuda"), torch.zeros((2, 3), device="cuda")
