@@ -18,7 +18,7 @@
 // or the walk ends; else by the chain of a sequence's scans, one after the other,
 // since each C needs the sum before it (1.5 to 2 us a scan: the loads 0.7, the
 // exchange in the cluster 0.4, the walk 0.5).  128 sequences of 32 nodes over 131072
-// fp32 values take 69 us (read once: 20), 64 of 64 nodes over 131072 bf16 values
+// fp32 values take 63 us (read once: 20), 64 of 64 nodes over 131072 bf16 values
 // without a draft's row 19 us (2.5), one of 6 nodes over 32000 fp32 values 9 us.
 // What the walk needs of the other rows, p and q at each node's own
 // token, is gathered in one round of loads for all nodes before it begins.  A
@@ -455,12 +455,15 @@ cudaError_t launch_tree_verify(const TreeVerifyProblem& pb, const LaunchCtx& ctx
   par.pb = pb;
   const int es = pb.bf16 ? 2 : 4;
   // CTAs per sequence: as many as are all resident, four per SM, with at least a
-  // segment for each of two warps of each.  Measured (us, with 2, 4, 8, 16 of them):
+  // segment for each of two warps of each; and up to twice as many where a chain of scans
+  // is over runs of 16384 values and more.  Measured (us, with 2, 4, 8, 16 of them):
   // 1 sequence of 131072 fp32 values 21, 14, 11, 9; 32 sequences 53, 33, 24, 21; 64 of
-  // 32000 28, 21, 20, 29; 128 of 8000 17, 17, 26, 46; 128 of 131072 97, 69, 63, 74.
+  // 32000 28, 21, 20, 29; 128 of 8000 17, 17, 26, 46; 128 of 131072 97, 69, 63, 74; 100 of
+  // 150000 -, 70, 56, 60; without a draft's row 128 of 150000 bf16 values 31, 26, 31, 48.
   int cluster = 1;
-  while (cluster < kMostCluster && 2LL * cluster * pb.B <= 4LL * ctx.num_sms &&
-         2048LL * cluster <= pb.V)
+  while (cluster < kMostCluster && 2048LL * cluster <= pb.V &&
+         2LL * cluster * pb.B <=
+             (pb.draft && 32768LL * cluster <= pb.V ? 8LL : 4LL) * ctx.num_sms)
     cluster *= 2;
   par.cluster = cluster;
   const long long most = static_cast<long long>(cluster) * kMostSegments * kSegment;
