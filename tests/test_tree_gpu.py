@@ -134,8 +134,9 @@ CASES = [
     (2, 3, 3, 33, 130, 128, 64, 0.0, False, 40, "random", [130, 128]),
     (2, 4, 2, 16, 200, 64, 32, 0.0, True, None, "holes", [200, 191]),
     (2, 3, 1, 11, 200, 64, 32, 0.0, True, None, "holes", [200, 191]),
-    (2, 2, 1, 32, 200, 32, 32, 0.0, False, None, "chain", [200, 192]),
-    (2, 5, 1, 13, 200, 32, 32, 0.0, False, None, "chain", [200, 192]),
+    (2, 2, 1, 16, 200, 32, 32, 0.0, False, None, "chain", [200, 192]),
+    (2, 3, 1, 11, 200, 32, 32, 0.0, False, None, "chain", [200, 192]),
+    (1, 1, 1, 32, 200, 64, 32, 0.0, True, 20, "chain", [200]),
 ]
 
 

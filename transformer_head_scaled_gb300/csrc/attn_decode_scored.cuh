@@ -58,12 +58,12 @@
 // computes.
 //
 // TREE: the queries are the nodes of trees of drafted tokens (attn_decode_tree) with
-// few rows to a key head.  Node i stands at L + depth_i and sees the whole cache; what
+// at most 32 rows to a key head.  Node i stands at L + depth_i and sees the whole cache; what
 // it sees of its tree, its ancestors' own keys, is taken by the second kernel, which
 // needs nothing of the first for that and does it while the first still runs.  Every
 // unit's result therefore goes through the workspace.  Measured: 64 sequences of 64 to
-// 512 tokens, 8 heads of d = 64, int8, 16 nodes 22 us (floor 3.4); 32 of 2 to 4 thousand,
-// 16 heads, e4m3, caps, 25 nodes 113 us (31), the first kernel 95 of them (three
+// 512 tokens, 8 heads of d = 64, int8, 16 nodes 21 us (floor 3.4); 32 of 2 to 4 thousand,
+// 16 heads, e4m3, caps, 25 nodes 112 us (31), the first kernel 95 of them (three
 // special-function operations a score at two warps per scheduler); one of 512 tokens, 5
 // nodes 7.7 us, launches and latencies.
 //
@@ -332,37 +332,21 @@ __device__ __forceinline__ unsigned share_of(unsigned total, int warps) {
   return each < kMinTiles ? kMinTiles : each;
 }
 
-// The depths of a tree's nodes `lane` and `lane + 32` (0 where there is no node), by a
-// warp: after round k of pointer doubling a node knows how far its 2^k-th ancestor is.
-__device__ __forceinline__ int2 node_depths(const int* parents, int n, int lane) {
-  int up[2], depth[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = lane + 32 * e;
-    up[e] = i < n ? __ldg(parents + i) : -2;
-    if (up[e] < -1 || up[e] >= i) up[e] = -2;
-    depth[e] = up[e] >= 0 ? 1 : 0;
-  }
+// The depth of a tree's node `lane` (0 where there is no node), n <= 32, by a warp: after
+// round k of pointer doubling a node knows how far its 2^k-th ancestor is.
+__device__ __forceinline__ int node_depth(const int* parents, int n, int lane) {
+  int up = lane < n ? __ldg(parents + lane) : -2;
+  if (up < -1 || up >= lane) up = -2;
+  int depth = up >= 0 ? 1 : 0;
   for (int r = 1; r < n; r *= 2) {
-    int far[2], further[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int from = max(up[e], 0);
-      const int d0 = __shfl_sync(0xffffffffu, depth[0], from & 31),
-                d1 = __shfl_sync(0xffffffffu, depth[1], from & 31),
-                u0 = __shfl_sync(0xffffffffu, up[0], from & 31),
-                u1 = __shfl_sync(0xffffffffu, up[1], from & 31);
-      far[e] = from < 32 ? d0 : d1;
-      further[e] = from < 32 ? u0 : u1;
+    const int from = max(up, 0), far = __shfl_sync(0xffffffffu, depth, from),
+              further = __shfl_sync(0xffffffffu, up, from);
+    if (up >= 0) {
+      depth += far;
+      up = further;
     }
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      if (up[e] >= 0) {
-        depth[e] += far[e];
-        up[e] = further[e];
-      }
   }
-  return make_int2(up[0] == -1 ? depth[0] : 0, up[1] == -1 ? depth[1] : 0);
+  return up == -1 ? depth : 0;
 }
 
 template <int FMT, int D, int NR, bool BIG, bool TREE>
@@ -544,9 +528,9 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
   uint32_t qa[MQ][C::KS][4];
   float qscale[MQ][2], nslope[MQ][2];
   int pos[MQ][2];
-  int2 depths = make_int2(0, 0);
+  int depth = 0;  // TREE: of node `lane`
   if (TREE && (biased || p.window >= 0))
-    depths = node_depths(p.parents + static_cast<long long>(b) * p.n_q, p.n_q, lane);
+    depth = node_depth(p.parents + static_cast<long long>(b) * p.n_q, p.n_q, lane);
 #pragma unroll
   for (int m = 0; m < MQ; ++m) {
 #pragma unroll
@@ -589,9 +573,7 @@ __global__ void __launch_bounds__(DW * 32, DCfg<FMT, D, NR, BIG>::CTAS)
         }
       }
       if (TREE) {
-        const int d0 = __shfl_sync(0xffffffffu, depths.x, qi & 31),
-                  d1 = __shfl_sync(0xffffffffu, depths.y, qi & 31);
-        pos[m][r] = L + (qi < 32 ? d0 : d1);
+        pos[m][r] = L + __shfl_sync(0xffffffffu, depth, qi);
       } else {
         pos[m][r] = in ? L - p.n_q + qi : -1;
       }
@@ -986,16 +968,13 @@ __device__ __forceinline__ OwnPart<(D + 31) / 32> tree_part(const ScoredDecParam
   constexpr int E = (D + 31) / 32, N = E == 1 ? 8 : 4, W = 32 / N;
   OwnPart<E> own;
   const int* parents = p.parents + static_cast<long long>(b) * p.n_q;
-  const int up0 = lane < p.n_q ? __ldg(parents + lane) : -2,
-            up1 = lane + 32 < p.n_q ? __ldg(parents + lane + 32) : -2;
-  // ancestor i (0: the node) in lane i of line0, ancestor i + 32 in lane i of line1
-  int line0 = node, line1 = node, at = node, length = 0;
-  while (at >= 0) {
-    if (lane == length) line0 = at;
-    if (lane == length - 32) line1 = at;
-    ++length;
-    const int x = __shfl_sync(0xffffffffu, at < 32 ? up0 : up1, at & 31);
-    at = x < -1 || x >= at ? -2 : x;
+  int up = lane < p.n_q ? __ldg(parents + lane) : -2;
+  if (up < -1 || up >= lane) up = -2;
+  // ancestor i (0: the node) in lane i
+  int line = node, at = node, length = 0;
+  for (; at >= 0; ++length) {
+    if (lane == length) line = at;
+    at = __shfl_sync(0xffffffffu, up, at);
   }
   own.node = at == -1;
   own.m = -INFINITY;
@@ -1018,9 +997,7 @@ __device__ __forceinline__ OwnPart<(D + 31) / 32> tree_part(const ScoredDecParam
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       // (past the last: the node itself, at weight 0)
-      const int far = back + i;
-      int who = __shfl_sync(0xffffffffu, far < 32 ? line0 : line1, far & 31);
-      if (far >= length) who = node;
+      const int far = back + i, who = __shfl_sync(0xffffffffu, line, far & 31);
       float key[E];
       load_values<E>(k + who * p.skt.n, key);
       load_values<E>(v + who * p.svt.n, val[i]);
