@@ -1,0 +1,142 @@
+"""Attention over drafted trees (attn_decode_tree) where its arguments end, for few and
+for many query rows of a key head: scores in the thousands, value scales over many
+powers of two, caps from tiny to idle, hidden keys with anything in them, more units
+of work than SMs, the largest groups of query heads.
+
+Tolerances count roundings as in test_tree_gpu: O half a step of bf16 and each
+probability rounded once to bf16, 2^-8 each; scores (and LSE) to SCORE_TOL, with the
+general form of the tanh 3e-7 of the cap more, and sums of d products whose terms add
+up to `size` to (d + 8) 2^-24 size.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import tree
+from transformer_head_scaled_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+SCORE_TOL = 3e-4
+E4M3, INT8, BF16 = torch.float8_e4m3fn, torch.int8, torch.bfloat16
+TYPES = pytest.mark.parametrize("dtype", [BF16, E4M3, INT8], ids=["bf16", "e4m3", "int8"])
+# query heads of one key head, nodes: 6 and 24 query rows, 70, 200
+ROWS = pytest.mark.parametrize("h,n", [(1, 6), (2, 12), (1, 70), (2, 100)],
+                               ids=["6", "24", "70", "200"])
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.fail("CUDA device required for -m gpu tests")
+    from transformer_head_scaled_gb300.build import build
+    build()
+    return binding.load()
+
+
+def _random(shape, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda") * std
+
+
+def _cache(x, dtype, block, top=4.0):
+    """Rows x (about `top` at most) as a cache: rows or codes, scales, float64 values."""
+    if dtype == BF16:
+        c = x.to(BF16)
+        return c, None, c.double()
+    most = 127.0 if dtype == INT8 else 448.0
+    c = (x * (most / top)).clamp(-most, most)
+    c = c.round().to(INT8) if dtype == INT8 else c.to(E4M3)
+    s = torch.full((*x.shape[:2], -(-x.shape[2] // block)), top / most, device="cuda")
+    return c, s, c.float().double() * s.double().repeat_interleave(block, 2)[:, :, :x.shape[2], None]
+
+
+def _parents(B, n, seed=0, holes=False):
+    rng = np.random.default_rng(seed)
+    p = np.array([[-1] + [int(rng.integers(max(0, i - 5), i)) for i in range(1, n)]
+                  for _ in range(B)], dtype=np.int32).reshape(B, n)
+    if holes:
+        p[:, 2::7] = -2
+    return p
+
+
+def _reference(q, kt, vt, k, v, parents, lens, scale, softcap=0.0, slopes=None, window=None):
+    """O, LSE and sum p |v| in 64 bits, all sequences at once; NaN is not allowed."""
+    B, h, n, d = q.shape
+    hk, L = k.shape[1:3]
+    see = torch.zeros((B, n, L + n), dtype=torch.bool)
+    far = torch.zeros((B, n, L + n), dtype=torch.float64)
+    for b in range(B):
+        for i, line in enumerate(tree.lineages(parents[b])):
+            if line:
+                see[b, i, :lens[b]] = True
+                far[b, i, :L] = lens[b] + len(line) - 1 - torch.arange(L)
+                at = L + torch.tensor(line)
+                see[b, i, at] = True
+                far[b, i, at] = torch.arange(len(line) - 1, -1, -1, dtype=torch.float64)
+    see, far = see.cuda()[:, None, None], far.cuda()[:, None, None]
+    if window is not None:
+        see = see & (far <= window)
+    keys, values = (torch.cat([a, b], 2).double()[:, :, None] for a, b in ((k, kt), (v, vt)))
+    x = torch.matmul(q.double().view(B, hk, h // hk, n, d), keys.transpose(-1, -2)) * scale
+    if softcap > 0:
+        x = softcap * torch.tanh(x / softcap)
+    if slopes is not None:
+        x = x - slopes.double().view(1, hk, h // hk, 1, 1) * far
+    x = torch.where(see, x, -math.inf)
+    lse = torch.logsumexp(x, -1, keepdim=True)
+    p = torch.where(see, torch.exp(x - torch.where(lse == -math.inf, 0.0, lse)), 0.0)
+    return (torch.matmul(p, values).view(B, h, n, d), lse.view(B, h, n),
+            torch.matmul(p, values.abs()).view(B, h, n, d))
+
+
+def _check(got, want, tol=SCORE_TOL, extra=0.0):
+    (o, lse), (ro, rl, weight) = got, want
+    assert torch.isfinite(o).all()
+    off = (o.double() - ro).abs()
+    most = 2.0 ** -8 * ro.abs() + (2.0 ** -8 + 2 * tol) * weight + 1e-6 + extra
+    assert (off <= most).all(), (off / most).max()
+    none = rl == -math.inf
+    assert torch.equal(lse == -math.inf, none)
+    assert ((lse.double() - rl).abs()[~none] <= tol).all(), (lse.double() - rl).abs()[~none].max()
+
+
+def _run(q, kt, vt, parents, kc, vc, lens, **kw):
+    got = binding.attn_decode_tree(q, kt, vt, torch.tensor(parents, device="cuda"), kc, vc,
+                                   torch.tensor(lens, dtype=torch.int32, device="cuda"), **kw)
+    binding.check()
+    return got
+
+
+def _inputs(h, n, L, d, dtype, block, std=2.0, B=1, hk=1, seed=1):
+    q = _random((B, h, n, d), seed, std).to(BF16)
+    own = [_random((B, hk, n, d), seed + i).to(BF16) for i in (1, 2)]
+    kc, ks, k = _cache(_random((B, hk, L, d), seed + 3), dtype, block)
+    vc, vs, v = _cache(_random((B, hk, L, d), seed + 4), dtype, block)
+    return q, own, (kc, vc), (ks, vs), (k, v)
+
+
+def _slopes(h):
+    return torch.tensor([2.0 ** (-8.0 * (i + 1) / h) for i in range(h)], device="cuda")
+
+
+@pytest.mark.parametrize("h,n", [(69798, 63), (131072, 127), (131072, 128), (4200000, 3)])
+def test_the_largest_groups_of_query_heads(h, n):
+    """Millions of query rows of one key head, packed as projections are, so that a row of
+    another head or node is another address: against 256 heads at a time (whole blocks of
+    256 rows, so that rows have the same bits)."""
+    L, d = 20, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((1, n, h + 2, d), generator=g, device="cuda", dtype=BF16)
+    q, kt, vt = (t.transpose(1, 2) for t in x.split([h, 1, 1], 2))
+    kc, vc = (torch.randn((1, 1, L, d), generator=g, device="cuda", dtype=BF16) for _ in "kv")
+    parents = _parents(1, n, 4, holes=True)
+    o, lse = _run(q, kt, vt, parents, kc, vc, [L])
+    for at in (0, h // 2, 4 * h // 5, h - 256):
+        part = q[:, at:at + 256].contiguous()
+        want = _run(part, kt, vt, parents, kc, vc, [L])
+        assert torch.equal(o[:, at:at + 256], want[0]) and torch.equal(lse[:, at:at + 256], want[1])
+    last = slice(h - 3, h)
+    _check((o[:, last], lse[:, last]), _reference(q[:, last], kt, vt, kc, vc, parents, [L], 0.25))

@@ -134,7 +134,8 @@ struct TreeParams {
   int B, H, HK, G, n, L_max, T_log2, num_blocks, window;
   int rows, blocks, block_rows;  // query rows of a key head, their blocks, rows of a part
   int tree_tiles, rounds;
-  float scale_log2, cap_log2, cap_in, inv_n;
+  float scale_log2, cap_log2, cap_in;
+  unsigned div_n;  // floor(2^31 / n) + 1
   CapPoly cap;
   bool capped, wide;
 };
@@ -697,8 +698,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           !wait(&sm.q_empty[slot ^ 1], ((items - 1) >> 1) & 1))
         break;
       was_wide = wide;
-      // (rows by a product with 1 / n: exact for numbers this small.  All copies are under
-      // way at once: in batches of 8 loads the first tile's scores came 3 us later)
+      // (a row's head by a product with (2^31 + e) / n, 1 <= e <= n: row e < 2^31 for all 2^24
+      // rows and 128 nodes, so that the quotient's whole part is exact.  All copies are
+      // under way at once: in batches of 8 loads the first tile's scores came 3 us later)
       constexpr int CPR = D / 8;  // 16-byte chunks of a row
       const int tiles = it.split == 0 ? 2 : 1;
       const int lanes = it.split == 0 ? BM : BM / it.split;
@@ -710,7 +712,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           const int at = e / CPR, c = e % CPR;
           const int r = s * BM + (at & (lanes - 1));
           const bool there = r < it.rows;
-          const int row = it.row0 + (there ? r : 0), g = static_cast<int>((row + 0.5f) * p.inv_n);
+          const int row = it.row0 + (there ? r : 0), g = __umulhi(2u * row, p.div_n);
           copy_chunk(to + (c / C::CPB) * C::Q_BLOCK + at * C::RB + (((c % C::CPB) ^ C::swz(at)) << 4),
                      q + g * p.sq.h + (row - g * p.n) * p.sq.n + c * 8, there);
         }
@@ -1005,7 +1007,7 @@ cudaError_t launch_tree_fmt(const TreeDecodeProblem& pb, const CUtensorMap* maps
   p.HK = pb.HK;
   p.G = pb.H / pb.HK;
   p.n = pb.n;
-  p.inv_n = 1.f / pb.n;
+  p.div_n = (1u << 31) / static_cast<unsigned>(pb.n) + 1u;
   p.L_max = pb.L_max;
   while ((1 << p.T_log2) < pb.block_tokens) ++p.T_log2;
   p.num_blocks = (pb.L_max + pb.block_tokens - 1) / pb.block_tokens;
