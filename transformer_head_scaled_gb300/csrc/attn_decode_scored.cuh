@@ -1031,9 +1031,10 @@ __device__ __forceinline__ OwnPart<(D + 31) / 32> tree_part(const ScoredDecParam
 #pragma unroll
     for (int w = 16; w >= W; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
     top = fmaxf(top, own.m);
-    const float alpha = ex2(own.m - top);  // 0 at first
+    const float base = top == -INFINITY ? 0.f : top;  // (scores of -inf weigh nothing)
+    const float alpha = ex2(own.m - base);  // 0 at first
     own.m = top;
-    const float share = ex2(y - top);
+    const float share = ex2(y - base);
     l = fmaf(l, alpha, share);
 #pragma unroll
     for (int e = 0; e < E; ++e) own.a[e] *= alpha;
@@ -1112,7 +1113,7 @@ __global__ void __launch_bounds__(256, TREE ? 5 : 1)
     const float4 x = tail_of(part);
     mm = x.x;
     from = x.z;
-    ll = mm == -INFINITY ? 0.f : x.y;
+    ll = x.y;
     mb = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -1185,11 +1186,13 @@ __global__ void __launch_bounds__(256, TREE ? 5 : 1)
   __nv_bfloat16* out = p.o + b * p.so.b + head * p.so.h + qi * p.so.n;
   const float fac = value_factor(from, mb);
   if (TREE) {
-    // the ancestors' part joins the cache's; a place that is no node sees neither
-    const bool cached = ll > 0.f && own_part.node;
-    const float most = fmaxf(cached ? mm : -INFINITY, own_part.node ? own_part.m : -INFINITY);
+    // the ancestors' part joins the cache's; a place that is no node sees neither.  (Sums
+    // of NaN are not 0: they go on to O and LSE)
+    const bool cached = ll != 0.f && own_part.node;
+    float most = fmaxf(cached ? mm : -INFINITY, own_part.node ? own_part.m : -INFINITY);
+    most = most == -INFINITY ? 0.f : most;
     const float w1 = cached ? ex2(mm - most) : 0.f, w2 = own_part.node ? ex2(own_part.m - most) : 0.f;
-    const float sum = fmaf(w1, ll, w2 * own_part.l), inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float sum = fmaf(w1, ll, w2 * own_part.l), inv = sum != 0.f ? 1.f / sum : 0.f;
     float y[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -1203,7 +1206,7 @@ __global__ void __launch_bounds__(256, TREE ? 5 : 1)
           __floats2bfloat162_rn(y[e] * inv, y[e + 1] * inv);
     if (lane == 0 && p.lse != nullptr)
       p.lse[(static_cast<long long>(b) * p.HK * p.G + head) * p.n_q + qi] =
-          sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
+          sum != 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
     return;
   }
   const float inv = (ll > 0.f ? 1.f / ll : 0.f) * fac;
