@@ -21,11 +21,13 @@ pytestmark = pytest.mark.gpu
 SCORE_TOL = 3e-4
 BF16 = torch.bfloat16
 
-# B, h, h_kv, n, L_max, d.  Few query rows of a key head (up to 16, or 32); keys whole and
-# in parts.
+# B, h, h_kv, n, L_max, d.  Few query rows of a key head (up to 16, or 32), and many:
+# up to 64 (twice in a tile), up to 128, up to 256; keys whole and in parts.
 SHAPES = pytest.mark.parametrize("B,h,hk,n,L,d", [
     (2, 2, 1, 5, 60, 64), (1, 2, 1, 6, 9000, 64), (48, 8, 8, 4, 1000, 16), (1, 2, 1, 16, 3000, 64),
-    (160, 4, 4, 3, 200, 32)])
+    (160, 4, 4, 3, 200, 32), (2, 1, 1, 40, 200, 64), (1, 1, 1, 40, 5000, 64),
+    (2, 2, 1, 40, 200, 128), (1, 2, 1, 40, 5000, 32), (1, 2, 1, 100, 200, 128),
+    (1, 2, 1, 100, 5000, 64)])
 
 
 @pytest.fixture(scope="module", autouse=True)

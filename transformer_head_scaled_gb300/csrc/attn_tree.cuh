@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(64) attn_tree_join_kernel(const TreeParams p, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (c + i > c1) tail[i].y = 0.f;
-      if (tail[i].y > 0.f) most = fmaxf(most, tail[i].x);
+      if (tail[i].y != 0.f) most = fmaxf(most, tail[i].x);
     }
     const float old = was == -INFINITY ? 0.f : ex2(was - most);
     sum *= old;
@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(64) attn_tree_join_kernel(const TreeParams p, 
       for (int e = 0; e < 4; ++e) y[k][e] *= old;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float w = tail[i].y > 0.f ? ex2(tail[i].x - most) : 0.f;
+      const float w = tail[i].y != 0.f ? ex2(tail[i].x - most) : 0.f;
       sum = fmaf(w, tail[i].y, sum);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -935,7 +935,7 @@ __global__ void __launch_bounds__(64) attn_tree_join_kernel(const TreeParams p, 
     }
   }
   const int g = row / p.n, node = row - g * p.n;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;  // (a sum of NaN goes on)
   __nv_bfloat16* out = p.o + b * p.so.b + (hk * p.G + g) * p.so.h + node * p.so.n + warp * K * 4;
 #pragma unroll
   for (int k = 0; k < K; ++k)
@@ -943,7 +943,7 @@ __global__ void __launch_bounds__(64) attn_tree_join_kernel(const TreeParams p, 
         make_uint2(pack_bf16x2(y[k][0] * inv, y[k][1] * inv), pack_bf16x2(y[k][2] * inv, y[k][3] * inv));
   if (warp == 0 && p.lse != nullptr)
     p.lse[(static_cast<size_t>(b) * p.H + hk * p.G + g) * p.n + node] =
-        sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
+        sum != 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <class C, int MODE>

@@ -433,6 +433,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
     const int column = 4 * p.block_rows;  // from four values to the next four
     const int split = twice ? 2 : 1;
     const int pidx = s * split + copy;  // which part of the row (not both)
+    // (sums of NaN are not 0: they go on to O and LSE)
     float weight = alive ? 1.f : 0.f, most = m, sum = l;
     if (!both) {
       sm.stat[threadIdx.x] = make_float2(m, l);
@@ -445,18 +446,18 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
 #pragma unroll 1
       for (int e = at0; e < 2 * BM; e += step) {
         const float2 x = sm.stat[e];
-        if (x.y > 0.f) sum = fmaf(x.y, ex2(x.x - most), sum);
+        if (x.y != 0.f) sum = fmaf(x.y, ex2(x.x - most), sum);
       }
-      weight = l > 0.f ? ex2(m - most) : 0.f;
+      weight = l != 0.f ? ex2(m - most) : 0.f;
     }
-    if (it.whole) weight = sum > 0.f ? weight / sum : 0.f;
+    if (it.whole) weight = sum != 0.f ? weight / sum : 0.f;
     const bool writer = valid && (both || pidx == 0);
     if (writer) {
       if (!it.whole)
         *reinterpret_cast<float2*>(part + (D / 4) * column) = make_float2(most, sum);
       else if (p.lse != nullptr)
         p.lse[(static_cast<size_t>(it.b) * p.H + head) * p.n + node] =
-            sum > 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
+            sum != 0.f ? (most + __log2f(sum)) * kLn2 : -INFINITY;
     }
     __nv_bfloat16* out = p.o + it.b * p.so.b + head * p.so.h + node * p.so.n;
     const int lanes = twice ? 64 : BM;
@@ -466,7 +467,7 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
       if (!first) tmem_ld16(tO + c, o);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        o[i] = weight > 0.f && !first ? __float_as_uint(__uint_as_float(o[i]) * weight) : 0u;
+        o[i] = weight != 0.f && !first ? __float_as_uint(__uint_as_float(o[i]) * weight) : 0u;
       if (!both) {
         if (pidx > 0) {
           uint4* to = reinterpret_cast<uint4*>(sm.merge[(pidx - 1) * lanes + r]);
