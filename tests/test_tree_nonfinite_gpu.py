@@ -1,7 +1,7 @@
 """NaN and infinities that nodes of a drafted tree see (attn_decode_tree): a NaN
 among what a node sees is in its output and its LSE, whichever kernel takes the call
 and however the keys are split, and in nobody else's; a score of -inf weighs
-nothing.
+nothing.  Every 8-bit code enters both products exactly.
 
 Tolerances: O half a step of bf16 (2^-8 |O|), each probability rounded to bf16 once
 (2^-8 of that share of sum p |v|), scores to 3e-4 as in test_tree_gpu; where a test
@@ -19,7 +19,7 @@ from transformer_head_scaled_gb300 import binding
 pytestmark = pytest.mark.gpu
 
 SCORE_TOL = 3e-4
-BF16 = torch.bfloat16
+E4M3, INT8, BF16 = torch.float8_e4m3fn, torch.int8, torch.bfloat16
 
 # B, h, h_kv, n, L_max, d.  Few query rows of a key head (up to 16, or 32), and many:
 # up to 64 (twice in a tile), up to 128, up to 256; keys whole and in parts.
@@ -160,3 +160,47 @@ def test_infinite_scores(B, h, hk, n, L, d):
         got = _run(q, (kt, vt), (k, v), parents, lens)
         _against_reference(got, q, (kt, vt), (k, v), parents, [m] * B)
     assert (got[0][0, 0, 0] == 0).all() and got[1][0, 0, 0] == -math.inf
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8], ids=["e4m3", "int8"])
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("n", [16, 40, 128], ids=["few", "many", "most"])
+def test_every_code_enters_exactly(dtype, d, n):
+    """One cached token a sequence, with scale 1, and nodes' own keys that weigh nothing: O
+    is the token's value codes, exactly, and node i, whose query is the unit vector
+    i mod d, has its i-th key code for LSE: four fp32 roundings of it (2^-22), and what
+    the exponential of a number near 0 and the logarithm of one near 1 are off by, 2^-22
+    and 2^-21.4 in steps of log2 (2^-21 together)."""
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").view(dtype)
+    value = codes.float()
+    finite = torch.isfinite(value)
+    order = torch.cat([torch.nonzero(finite)[:, 0], torch.nonzero(~finite)[:, 0]])
+    rows = -(-int(finite.sum()) // d)
+    use = torch.zeros((rows + 1) * d, dtype=torch.long, device="cuda")  # (code 0: the number 0)
+    use[:int(finite.sum())] = order[:int(finite.sum())]
+    if int(finite.sum()) < 256:  # codes of NaN in a sequence of their own
+        use[rows * d:rows * d + 2] = order[int(finite.sum()):]
+    B = rows + 1
+    grid = codes.view(torch.uint8)[use].view(dtype).view(B, 1, 1, d)
+    cache = torch.zeros((B, 1, 100, d), dtype=torch.uint8, device="cuda").view(dtype)
+    cache.view(torch.uint8).fill_(0x7f)  # behind the token: NaN, or 127
+    cache[:, :, :1] = grid
+    ones = torch.ones((B, 1, 7), device="cuda")
+    q = torch.eye(d, device="cuda").repeat(-(-n // d), 1)[:n].expand(B, 1, n, d).to(BF16).contiguous()
+    kt = torch.full((B, 1, n, d), -4096.0, device="cuda", dtype=BF16)
+    vt = torch.ones((B, 1, n, d), device="cuda", dtype=BF16)
+    parents = np.full((B, n), -1, dtype=np.int32)
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    plain = torch.zeros_like(cache)
+    plain[:, :, :1] = torch.ones((), device="cuda").to(dtype)
+    kw = dict(k_scale=ones, v_scale=ones, block_tokens=16, scale=1.0)
+    o, _ = _run(q, (kt, vt), (plain, cache), parents, lens, **kw)
+    want = grid.float().expand(B, 1, n, d)
+    gone = torch.isnan(want)
+    assert torch.equal(torch.isnan(o), gone)
+    assert torch.equal(o.float()[~gone], want[~gone])
+    _, lse = _run(q, (kt, vt), (cache, plain), parents, lens, **kw)
+    want = grid.float().view(B, 1, d).repeat(1, 1, -(-n // d))[:, :, :n]
+    gone = torch.isnan(want).any(-1, keepdim=True).expand_as(want)  # (NaN times 0 too)
+    assert torch.equal(torch.isnan(lse), gone)
+    assert ((lse - want).abs()[~gone] <= 2.0 ** -22 * want.abs()[~gone] + 2.0 ** -21).all()

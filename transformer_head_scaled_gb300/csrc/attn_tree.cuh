@@ -355,7 +355,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "memory");
 }
 
-// Two of a word's four codes (bytes 2 * HI and 2 * HI + 1) as a bf16 pair, exactly.
+// Two of a word's four codes (bytes 2 * HI and 2 * HI + 1) as a bf16 pair, exactly (but
+// e4m3's codes of NaN, which become +-480: see no_number).
 template <int FMT, int HI>
 __device__ __forceinline__ uint32_t widen2(uint32_t w) {
   uint32_t t, y;
@@ -377,6 +378,21 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&x);
 }
 
+// NaN in the place of the +-480 among a lane's widened codes of half a tile (no code is
+// that number: 448 is the largest).  Out of the way of what widens them.
+template <class C>
+__device__ __noinline__ void no_number(uint8_t* out, int half, int lane) {
+  for (int e = lane; e < C::BN / 2 * C::CPB * C::NB; e += 32) {
+    const int nb = e / (C::BN / 2 * C::CPB);
+    uint4& w = *reinterpret_cast<uint4*>(out + nb * C::KV_BLOCK + half * (C::KV_BLOCK / 2) +
+                                         (e - nb * (C::BN / 2 * C::CPB)) * 16);
+    auto nan = [](uint32_t x) {
+      return x | (__vcmpeq2(x & 0x7fff7fffu, 0x43f043f0u) & 0x7fff7fffu);
+    };
+    w = make_uint4(nan(w.x), nan(w.y), nan(w.z), nan(w.w));
+  }
+}
+
 // Half (0 or 1) of a tile of codes to bf16 in the layout of a swizzled copy, by a warp;
 // rows outside [lo, hi) become zeros.  Four chunks of codes are in flight at a time, in a loop:
 // all of them side by side would crowd the instruction cache.
@@ -392,6 +408,9 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int
   // (the two halves of a 256-byte row would meet in the same banks)
   const bool turn = C::D == 128 && (c & 4);
   int row = half * (C::BN / 2) + lane / CPR;
+  // (bit 7 of a byte whose seven low bits are all set: e4m3's two codes of NaN)
+  uint32_t nans = 0;
+  auto seven = [](uint32_t x) { return (x & 0x7f7f7f7fu) + 0x01010101u; };
 #pragma unroll 1
   for (int e = 0; e < N; e += M) {
     uint4 w[M];
@@ -403,6 +422,8 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int
 #pragma unroll
     for (int i = 0; i < M; ++i, row += STEP) {
       if (row < lo || row >= hi) w[i] = make_uint4(0u, 0u, 0u, 0u);  // (a code of 0 is the number 0)
+      if (C::FMT == kCacheE4M3)
+        nans |= seven(w[i].x) | seven(w[i].y) | seven(w[i].z) | seven(w[i].w);
       const uint4 a = make_uint4(widen2<C::FMT, 0>(w[i].x), widen2<C::FMT, 1>(w[i].x),
                                  widen2<C::FMT, 0>(w[i].y), widen2<C::FMT, 1>(w[i].y));
       const uint4 b = make_uint4(widen2<C::FMT, 0>(w[i].z), widen2<C::FMT, 1>(w[i].z),
@@ -412,6 +433,10 @@ __device__ __forceinline__ void widen_tile(const uint8_t* raw, uint8_t* out, int
       *reinterpret_cast<uint4*>(dst + (((turn ? c0 + 1 : c0) ^ x) << 4)) = turn ? b : a;
       *reinterpret_cast<uint4*>(dst + (((turn ? c0 : c0 + 1) ^ x) << 4)) = turn ? a : b;
     }
+  }
+  if (C::FMT == kCacheE4M3 && __any_sync(0xffffffffu, nans & 0x80808080u)) {
+    __syncwarp();  // (its chunks are other lanes')
+    no_number<C>(out, half, lane);
   }
 }
 
