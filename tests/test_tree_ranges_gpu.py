@@ -122,6 +122,42 @@ def _slopes(h):
     return torch.tensor([2.0 ** (-8.0 * (i + 1) / h) for i in range(h)], device="cuda")
 
 
+@TYPES
+@ROWS
+@pytest.mark.parametrize("d", [16, 64, 128])
+@pytest.mark.parametrize("window", [None, 150])
+def test_what_nobody_sees_changes_no_bit_under_a_cap(dtype, h, n, d, window):
+    """Cache rows behind the last token and before every window, keys, values and queries
+    of places that are no node: zeros, or large."""
+    L, block, lens, cap = 700, 16, [500, 3], 100.0
+    q, own, caches, (ks, vs), _ = _inputs(h, n, L, d, dtype, block, B=2)
+    parents = _parents(2, n, 2, holes=True)
+    gone = torch.tensor([[not x for x in tree.lineages(parents[b])] for b in range(2)], device="cuda")
+    hidden = torch.zeros((2, L), dtype=torch.bool, device="cuda")
+    for b, m in enumerate(lens):
+        hidden[b, m:] = True
+        if window is not None:
+            hidden[b, :max(0, m - window)] = True
+    res = []
+    for large in (0.0, 1.0, 0.0):
+        kc, vc, kt, vt, qq = (t.clone() for t in (*caches, *own, q))
+        for b in range(2):
+            for t, fill in ((kc, 3e4), (vc, 3e4)):
+                if dtype == BF16:
+                    t[b, :, hidden[b]] = fill * large
+                else:  # 96 and 112, the same byte of a code as for e4m3 numbers
+                    t.view(torch.uint8)[b, :, hidden[b]] = 0x70 if large else 0
+            for t in (kt, vt, qq):
+                t[b, :, gone[b]] = 3e4 * large
+        if large:  # what an earlier call left in shared memory
+            _run(qq, kt, vt, parents, torch.full_like(kc, 100.0) if dtype != E4M3 else kc, vc,
+                 [L, L], k_scale=ks, v_scale=vs, block_tokens=block, softcap=cap)
+        res.append(_run(qq, kt, vt, parents, kc, vc, lens, k_scale=ks, v_scale=vs,
+                        block_tokens=block, softcap=cap, window=window))
+    for other in res[1:]:
+        assert torch.equal(res[0][0], other[0]) and torch.equal(res[0][1], other[1])
+
+
 @pytest.mark.parametrize("h,n", [(69798, 63), (131072, 127), (131072, 128), (4200000, 3)])
 def test_the_largest_groups_of_query_heads(h, n):
     """Millions of query rows of one key head, packed as projections are, so that a row of

@@ -226,7 +226,9 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
               }
               big = max3_abs(big, __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
             }
-          const bool small = __all_sync(0xffffffffu, big <= p.cap.small);
+          // (which form is taken follows from what nodes see alone, since the two round
+          // differently: the general one where a tile holds anything else)
+          const bool small = !edge && __all_sync(0xffffffffu, !alive || big <= p.cap.small);
           if (small) {
 #pragma unroll
             for (int c = 0; c < NC / 32; ++c)
