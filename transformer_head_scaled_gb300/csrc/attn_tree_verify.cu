@@ -118,7 +118,7 @@ __device__ __forceinline__ void cluster_wait() {
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// What is left of one probability; NaN counts as 0.
+// What is left of one probability; a NaN of p counts as 0, one of q has to be 0 already.
 __device__ __forceinline__ float left_of(float p, float q, Pair c) {
   return __saturatef(__fmaf_rn(-c.lo, q, __fmaf_rn(-c.hi, q, p)));
 }
@@ -136,7 +136,8 @@ __device__ __forceinline__ u64 fixed(float r) {
 
 template <class T>
 __device__ __forceinline__ float left_at(const Row<T>& row, int v) {
-  return left_of(widen(__ldg(row.p + v)), row.q ? widen(__ldg(row.q + v)) : 0.f, row.c);
+  return left_of(widen(__ldg(row.p + v)), row.q ? fmaxf(widen(__ldg(row.q + v)), 0.f) : 0.f,
+                 row.c);
 }
 
 // The warp's sum: of three parts that 32 bits hold 32 times.
@@ -167,6 +168,19 @@ __device__ __forceinline__ void load_part(const T* row, int at, int end, int lan
       v[i] = k < end ? __ldg(row + k) : T(0.f);
     }
   }
+}
+
+// 0 in the place of NaN in a lane's part of the draft's row.
+__device__ __forceinline__ void no_nan(uint4 (&x)[kPart<float>]) {
+  float* v = reinterpret_cast<float*>(x);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) v[i] = fmaxf(v[i], 0.f);
+}
+__device__ __forceinline__ void no_nan(uint4 (&x)[kPart<__nv_bfloat16>]) {
+  __nv_bfloat162* v = reinterpret_cast<__nv_bfloat162*>(x);
+  const __nv_bfloat162 zero = __halves2bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+#pragma unroll
+  for (int i = 0; i < kEach / 2; ++i) v[i] = __hmax2(v[i], zero);
 }
 
 template <class T>
@@ -244,7 +258,10 @@ __global__ void __launch_bounds__(kThreads, 4) attn_tree_verify_kernel(const Ver
 #pragma unroll
         for (int i = 0; i < kPart<T>; ++i) q[i] = make_uint4(0u, 0u, 0u, 0u);
         load_part<T, VEC>(row.p, v, to, lane, p);
-        if (row.q) load_part<T, VEC>(row.q, v, to, lane, q);
+        if (row.q) {
+          load_part<T, VEC>(row.q, v, to, lane, q);
+          no_nan(q);
+        }
         part += part_sum(p, q, row);
       }
       if (without >= 0) {
