@@ -525,6 +525,8 @@ typedef enum { ATTN_PROB_F32 = 0, ATTN_PROB_BF16 = 1 } attn_prob_type;
  *              batch entry and from row to row, then draft's (those two are not
  *              read without one); NULL: contiguous.  V is contiguous.
  *   n <= 128, V <= 2^24, B <= 2^24 (else ATTN_ERR_UNSUPPORTED).
+ * path, path_lens and next_tokens must not overlap the inputs, from their first
+ * entry to their last, or one another (else ATTN_ERR_INVALID_ARG).
  * r is rounded to fp32 and summed exactly in multiples of 2^-60: the answer does
  * not depend on the order of the sums.  C, Z and the tests of single nodes are held
  * as pairs of fp32 numbers (48 bits).  One kernel on `stream`, as clusters of up to

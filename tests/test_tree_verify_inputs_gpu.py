@@ -62,3 +62,27 @@ def test_a_token_of_the_drafts_nan_may_follow():
                                       u[0].cpu().numpy(), q[0].double().cpu().numpy())
         assert want_path == [0] and tree.next_tokens(r, u0, 1e-9) == {want}
         assert lens.tolist() == [1] and path.tolist() == [[0, -1]] and token.tolist() == [want]
+
+
+def test_buffers_side_by_side():
+    """Inputs and outputs as neighbours in one buffer are no overlap; in place is refused."""
+    B, n, V = 2, 3, 50
+    g = torch.Generator(device="cuda").manual_seed(1)
+    p = torch.softmax(torch.randn((B, n, V), generator=g, device="cuda"), -1)
+    parents = torch.tensor([[-1, 0, 1], [-1, 0, 0]], dtype=torch.int32, device="cuda")
+    tokens = torch.randint(0, V, (B, n), generator=g, device="cuda", dtype=torch.int32)
+    u = torch.rand((B, n), generator=g, device="cuda") * 0.02
+    want = binding.attn_tree_verify(p, tokens, parents, u)
+    flat = torch.zeros(3 * B * n + 2 * B, dtype=torch.int32, device="cuda")
+    parts = flat.split([B * n, B * n, B, B, B * n])
+    tok, path, lens, token, par = (parts[0].view(B, n), parts[1].view(B, n), parts[2], parts[3],
+                                   parts[4].view(B, n))
+    tok.copy_(tokens)
+    par.copy_(parents)
+    got = binding.attn_tree_verify(p, tok, par, u, path=path, path_lens=lens, next_tokens=token)
+    binding.check()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(par, parents)
+    for kw in (dict(path=tok), dict(path=par), dict(path=lens.new_empty(1), path_lens=lens),
+               dict(path_lens=token, next_tokens=token), dict(path_lens=tok.view(-1)[:B])):
+        with pytest.raises((binding.AttnError, ValueError)):
+            binding.attn_tree_verify(p, tok, par, u, **kw)

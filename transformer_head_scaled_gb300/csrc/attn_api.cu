@@ -1208,6 +1208,16 @@ int tree_decode_sizes(int B, int h, int h_kv, int n, int L_max, int d_k, int cac
     return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
+
+// Bytes that a call reads or writes, and whether two such have any in common.
+struct Extent {
+  const void* at;
+  long long bytes;
+};
+bool overlap(const Extent& a, const Extent& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return x < y ? y - x < static_cast<uintptr_t>(a.bytes) : x - y < static_cast<uintptr_t>(b.bytes);
+}
 }  // namespace
 
 ScoredDecodePlan tree_few_plan(int B, int H, int HK, int n, int seen, int d, int elem_bytes,
@@ -1356,6 +1366,23 @@ int attn_tree_verify(const void* target, const void* draft, const int* tokens,
   for (int i = 0; strides != nullptr && i < (draft ? 4 : 2); ++i) {
     if (strides[i] < 0 || strides[i] >= (1LL << 40)) return ATTN_ERR_INVALID_ARG;
     st[i] = strides[i];
+  }
+  // every CTA of a sequence's cluster walks for itself, over what it has read while another
+  // may write already: walks that differ would wait for each other's barriers
+  const long long ints = 4LL * B * n;
+  const int es = prob_type == ATTN_PROB_BF16 ? 2 : 4;
+  auto rows = [&](int i) {  // (strides may be larger than any memory)
+    const double x = ((B - 1.0) * st[i] + (n - 1.0) * st[i + 1] + V) * es;
+    return static_cast<long long>(x < 0x1p60 ? x : 0x1p60);
+  };
+  const Extent in[5] = {{target, rows(0)}, {draft, draft ? rows(2) : 0}, {tokens, ints},
+                        {parents, ints}, {uniforms, ints}};
+  const Extent out[3] = {{path, ints}, {path_lens, 4LL * B}, {next_tokens, 4LL * B}};
+  for (int i = 0; i < 3; ++i) {
+    for (const Extent& x : in)
+      if (overlap(out[i], x)) return ATTN_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return ATTN_ERR_INVALID_ARG;
   }
   DeviceInfo* di = nullptr;
   int rc;
