@@ -1065,8 +1065,9 @@ def attn_bwd_scored(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     return dq, dk, dv
 
 
-def _cache_scales(fmt, k_scale, v_scale, block_tokens, count, device):
-    """The scales of a cache, checked (bf16: none); count: tokens to entries."""
+def _cache_scales(fmt, k_scale, v_scale, block_tokens, heads, L_max, device):
+    """The scales of a cache of that many heads in all, checked (bf16: none, and
+    block_tokens may be anything)."""
     if fmt == CACHE_BF16:
         return None, None
     if block_tokens not in (16, 32, 64, 128):
@@ -1074,7 +1075,7 @@ def _cache_scales(fmt, k_scale, v_scale, block_tokens, count, device):
     if k_scale is None or v_scale is None:
         raise ValueError("an 8-bit cache needs k_scale and v_scale")
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _vector(name, t, torch.float32, count, device)
+        _vector(name, t, torch.float32, heads * -(-L_max // block_tokens), device)
     return k_scale, v_scale
 
 
@@ -1140,8 +1141,7 @@ def attn_decode_tree(q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor
     if L_max > _INT_MAX:
         raise ValueError("caches of 2^31 tokens and more are not supported")
     dev = q.device
-    k_scale, v_scale = _cache_scales(fmt, k_scale, v_scale, block_tokens,
-                                     B * h_kv * -(-L_max // block_tokens), dev)
+    k_scale, v_scale = _cache_scales(fmt, k_scale, v_scale, block_tokens, B * h_kv, L_max, dev)
     _nodes("parents", parents, torch.int32, B, n, dev)
     _vector("cache_lens", cache_lens, torch.int32, B, dev)
     _vector("slopes", slopes, torch.float32, h, dev)
@@ -1295,8 +1295,8 @@ def attn_cache_append_tree(k_tree: torch.Tensor, v_tree: torch.Tensor, path: tor
                          "[layers, B, h, L_max, d]")
     if L_max > _INT_MAX:
         raise ValueError("caches of 2^31 tokens and more are not supported")
-    k_scale, v_scale = _cache_scales(fmt, k_scale, v_scale, block_tokens,
-                                     layers * B * h * -(-L_max // block_tokens), dev)
+    k_scale, v_scale = _cache_scales(fmt, k_scale, v_scale, block_tokens, layers * B * h, L_max,
+                                     dev)
     _nodes("path", path, torch.int32, B, n, dev)
     if path_lens is None:
         raise ValueError("path_lens must be given")
