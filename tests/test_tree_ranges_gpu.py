@@ -124,6 +124,74 @@ def _slopes(h):
 
 @TYPES
 @ROWS
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("L", [200, 6000])
+def test_large_scores_and_scales_of_many_powers(dtype, h, n, d, L):
+    """Scores in the thousands (a softmax of one key, whose place changes from tile to
+    tile), value scales from 2^-30 to 2^30.  Probabilities times value scales in f16 (few
+    rows) are off by half a step of its subnormal numbers at least, 2^-25 where a row's
+    largest is 2^7 or more: `extra`."""
+    block = 16
+    q, own, caches, (ks, vs), (k, v) = _inputs(h, n, L, d, dtype, block, 400.0)
+    if ks is not None:
+        power = 5.0 * (torch.arange(vs.shape[2], device="cuda") % 13 - 6)
+        vs *= torch.exp2(power)
+        v *= torch.exp2(power).double().repeat_interleave(block)[:L, None]
+    parents, scale = _parents(1, n), 2.0 ** -6
+    got = _run(q, *own, parents, *caches, [L], k_scale=ks, v_scale=vs, block_tokens=block,
+               scale=scale)
+    keys = torch.cat([k, own[0].double()], 2)
+    size = scale * torch.matmul(q.double().abs(), keys.abs().transpose(-1, -2)).max().item()
+    tol = SCORE_TOL + (d + 8) * 2.0 ** -24 * size
+    want, extra = _reference(q, *own, k, v, parents, [L], scale), 0.0
+    if ks is not None:
+        s = torch.matmul(q.double(), k.transpose(-1, -2)) * scale
+        p = torch.exp(s - want[1][..., None].clamp(min=-1e300))
+        most = (p * vs.double().repeat_interleave(block, 2)[:, :, None, :L]).amax(-1, keepdim=True)
+        extra = 2.0 ** -32 * most * caches[1].float().double().abs().sum(2, keepdim=True)
+    _check(got, want, math.expm1(2 * tol) / 2, extra)
+
+
+@TYPES
+@ROWS
+@pytest.mark.parametrize("alibi", [False, True], ids=["plain", "alibi"])
+@pytest.mark.parametrize("cap", [1e-6, 0.01, 1.0, 300.0, 1e9, 2.0 ** 64])
+def test_caps_from_tiny_to_idle(dtype, h, n, cap, alibi):
+    d, L, block = 64, 330, 64
+    q, own, caches, (ks, vs), (k, v) = _inputs(h, n, L, d, dtype, block)
+    slopes, parents = _slopes(h) if alibi else None, _parents(1, n, 2, holes=True)
+    got = _run(q, *own, parents, *caches, [L - 9], k_scale=ks, v_scale=vs, block_tokens=block,
+               softcap=cap, slopes=slopes)
+    _check(got, _reference(q, *own, k, v, parents, [L - 9], 0.125, cap, slopes))
+
+
+@TYPES
+@ROWS
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("alibi", [False, True], ids=["plain", "alibi"])
+@pytest.mark.parametrize("sign", [1.0, -1.0], ids=["above", "below"])
+def test_scores_past_the_polynomials(dtype, h, n, d, alibi, sign):
+    """Under a wide cap one cached key, and one node's, of 0.6 caps among ordinary ones."""
+    L, block, cap = 330, 16, 300.0
+    q = (_random((1, h, n, d), 1) * 0.05 + 2.0).to(BF16)
+    kt, vt = (_random((1, 1, n, d), i).to(BF16) for i in (2, 3))
+    x = _random((1, 1, L, d), 4)
+    x[:, :, 130] = sign * 0.3 * cap / math.sqrt(d)
+    kt[:, :, n // 3] = sign * 0.3 * cap / math.sqrt(d)
+    kc, ks, k = _cache(x, dtype, block, 0.3 * cap / math.sqrt(d))
+    vc, vs, v = _cache(_random((1, 1, L, d), 5), dtype, block)
+    slopes, parents = _slopes(h) if alibi else None, _parents(1, n, 2)
+    scale = 1 / math.sqrt(d)
+    s = torch.matmul(q.double(), k.transpose(-1, -2)) * scale
+    assert (s[..., 130].abs() > 0.3 * cap).all() and (s[..., 131:].abs() < 0.3 * cap).all()
+    got = _run(q, kt, vt, parents, kc, vc, [L], k_scale=ks, v_scale=vs, block_tokens=block,
+               softcap=cap, slopes=slopes)
+    tol = SCORE_TOL + 3e-7 * cap + (d + 8) * 2.0 ** -24 * cap
+    _check(got, _reference(q, kt, vt, k, v, parents, [L], scale, cap, slopes), tol)
+
+
+@TYPES
+@ROWS
 @pytest.mark.parametrize("d", [16, 64, 128])
 @pytest.mark.parametrize("window", [None, 150])
 def test_what_nobody_sees_changes_no_bit_under_a_cap(dtype, h, n, d, window):
@@ -156,6 +224,48 @@ def test_what_nobody_sees_changes_no_bit_under_a_cap(dtype, h, n, d, window):
                         block_tokens=block, softcap=cap, window=window))
     for other in res[1:]:
         assert torch.equal(res[0][0], other[0]) and torch.equal(res[0][1], other[1])
+
+
+UNITS = [
+    # B, h, h_kv, n, L_max, d, window, lens.  Sequences x key heads (x blocks of 256 query
+    # rows) past 152 and 304.
+    (40, 8, 8, 40, 300, 64, None, (0, 300)),       # 320 units of 40 rows, whole
+    (40, 16, 8, 50, 300, 128, None, (0, 300)),     # of 100
+    (20, 32, 8, 50, 300, 64, None, (0, 300)),      # of 200
+    (40, 12, 4, 100, 260, 128, None, (0, 260)),    # 300 rows: blocks of 256 and of 44 in turn
+    (40, 12, 4, 100, 500, 32, None, (0, 500)),
+    (64, 8, 8, 40, 3000, 64, None, (0, 200)),      # runs of many short units
+    (64, 16, 8, 50, 3000, 128, None, (0, 500)),
+    (48, 12, 4, 100, 3000, 128, None, (0, 300)),
+    (24, 32, 4, 41, 3000, 128, None, (0, 3000)),   # 328 rows, short and long ones
+    (24, 32, 8, 40, 3000, 64, 300, (0, 3000)),
+    (24, 32, 8, 40, 3000, 16, None, (0, 3000)),
+    (100, 8, 8, 4, 3000, 64, None, (0, 600)),      # few rows
+    (100, 16, 8, 4, 400, 128, 100, (0, 400)),
+]
+
+
+@TYPES
+@pytest.mark.parametrize("B,h,hk,n,L,d,window,lens", UNITS)
+@pytest.mark.parametrize("changed", [False, True], ids=["plain", "cap+alibi"])
+def test_more_units_than_sms(dtype, B, h, hk, n, L, d, window, lens, changed):
+    block = 32
+    q, own, caches, (ks, vs), (k, v) = _inputs(h, n, L, d, dtype, block, B=B, hk=hk)
+    rng = np.random.default_rng(B + n)
+    lens = [int(x) for x in rng.integers(lens[0], lens[1] + 1, B)]
+    lens[3], lens[-1] = 0, 1
+    parents = _parents(B, n, 7, holes=True)
+    kw = dict(softcap=20.0, slopes=_slopes(h)) if changed else {}
+    got = _run(q, *own, parents, *caches, lens, k_scale=ks, v_scale=vs, block_tokens=block,
+               window=window, **kw)
+    for b0 in range(0, B, 10):  # (a few at a time: 64-bit scores are large)
+        at = slice(b0, b0 + 10)
+        want = _reference(q[at], own[0][at], own[1][at], k[at], v[at], parents[at], lens[at],
+                          1 / math.sqrt(d), window=window, **kw)
+        _check((got[0][at], got[1][at]), want)
+    again = _run(q, *own, parents, *caches, lens, k_scale=ks, v_scale=vs, block_tokens=block,
+                 window=window, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
 
 
 @pytest.mark.parametrize("h,n", [(69798, 63), (131072, 127), (131072, 128), (4200000, 3)])
