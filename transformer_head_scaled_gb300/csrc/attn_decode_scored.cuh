@@ -1260,6 +1260,8 @@ template <int FMT, bool TREE = false>
 cudaError_t launch_scored_decode_fmt(const ScoredDecodeProblem& pb, const CUtensorMap* maps,
                                      const ScoredDecodePlan& plan, float* workspace,
                                      const LaunchCtx& ctx, const TreeOwn* tree = nullptr) {
+  // (a node to a lane, a lineage's nodes to the lanes)
+  if (TREE && pb.n_q > 32) return cudaErrorInvalidValue;
   ScoredDecParams p;
   p.q = static_cast<const __nv_bfloat16*>(pb.q);
   p.k_scale = pb.k_scale;

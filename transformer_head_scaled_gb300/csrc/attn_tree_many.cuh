@@ -148,7 +148,6 @@ __device__ __forceinline__ bool softmax_many(const TreeParams& p, TreeSmem<C>& s
   const int at = quarter * 32 + lane;  // tensor-memory lane
   const uint32_t base_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const uint32_t tO = base_addr + C::col_o(s);
-  constexpr int OC = C::OW / 32;
   uint32_t u = 0;  // parts of SN keys of this stream
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait_small(smem_u32(bar), parity, p.limit_ns, abort));
