@@ -455,7 +455,10 @@ size_t attn_decode_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int L
  * with a window only those at positions p_i - window and later:
  *   s_j = scale * q_i.k_j;   capped: softcap * tanh(s_j / softcap);
  *   biased: minus slopes[head] * (p_i - p_j);   O = softmax(s) V,  LSE = ln sum e^s.
- * A place that is no node gets O = 0 and LSE = -inf and is not seen.
+ * A place that is no node gets O = 0 and LSE = -inf and is not seen.  A NaN in a key
+ * that a node sees (or a score of +inf without a cap) makes its O and LSE NaN and leaves
+ * the nodes that do not see it as they are; a value that is not finite may reach those of
+ * its key head too, as 0 times it.
  *   q, o     : bf16 [B, h, n, d_k], 1 <= n <= 128; lse float [B, h, n] or NULL.
  *   k_tree, v_tree : the nodes' own keys and values, bf16 [B, h_kv, n, d_k].  They
  *              are not in the cache; those of places that are no node are never
@@ -470,6 +473,7 @@ size_t attn_decode_scored_workspace_bytes(int B, int h, int h_kv, int n_q, int L
  *   workspace, workspace_bytes : at least attn_decode_tree_workspace_bytes(...)
  *              bytes, 16-byte aligned; may be NULL when that is 0.  Its contents
  *              on entry do not matter; calls that may overlap need one each.
+ *   o and lse must not overlap the inputs.
  *   d_k      : 16, 32, 64 or 128, B*h*n <= 2^24, L_max <= 2^30 and
  *              B*h_kv*ceil(h/h_kv*n / 32)*(L_max/16 + 8) < 2^31 (else
  *              ATTN_ERR_UNSUPPORTED).

@@ -63,9 +63,9 @@
 // needs nothing of the first for that and does it while the first still runs.  Every
 // unit's result therefore goes through the workspace.  Measured: 64 sequences of 64 to
 // 512 tokens, 8 heads of d = 64, int8, 16 nodes 21 us (floor 3.4); 32 of 2 to 4 thousand,
-// 16 heads, e4m3, caps, 25 nodes 112 us (31), the first kernel 95 of them (three
-// special-function operations a score at two warps per scheduler); one of 512 tokens, 5
-// nodes 7.7 us, launches and latencies.
+// 16 heads, e4m3, caps, 25 nodes 112 us (31), the first kernel 95 of them (four
+// special-function operations a score, two of the cap and one for each running maximum, at
+// two warps per scheduler); one of 512 tokens, 5 nodes 7.7 us, launches and latencies.
 //
 // Measured (the floor is the visible cache at the rate of a plain copy, 6.7 TB/s):
 // 4 sequences of 65 to 131 thousand tokens, 32 query heads on 8, d = 128, e4m3,

@@ -417,8 +417,8 @@ int scored_decode_min_tiles();
 // seen: the most keys one call can read per sequence.
 ScoredDecodePlan scored_decode_plan(int B, int H, int HK, int n_q, int seen, int d, int elem_bytes,
                                     int num_sms);
-// The same for few nodes of a tree of drafted tokens (n_q of them, 64 query rows of
-// a key head at most), with what they see of the tree.
+// The same for few nodes of a tree of drafted tokens (n_q of them, 32 query rows of
+// a key head at most: a node to a lane), with what they see of the tree.
 struct TreeOwn {
   const int* parents;  // [B, n_q]
   const void* k;       // bf16 [B, HK, n_q, d]
@@ -431,7 +431,9 @@ struct TreeOwn {
 // 79; d = 128, 16 rows 84 and 84, e4m3 58 and 109, 32 rows 114 and 86, 107 and 110.  With
 // few units it starts sooner: one of 4096 tokens, 8 key heads, d = 128, 32 rows 29 and 34
 // (64 rows 29 and 36, but 72 and 58 at 32768 tokens).  d = 32, 32 rows 41 and 54, 64 rows
-// 73 and 55, e4m3 68 and 72.
+// 73 and 55, e4m3 68 and 72.  Neither the format nor the length is an argument, so the
+// slower one is taken where these change the order: 17 to 32 rows of bf16 with d = 64, and
+// with d = 128 few key heads of long caches.
 inline bool tree_few(int B, int HK, int rows, int d) {
   return rows <= 16 || (rows <= 32 && (d < 128 || static_cast<long long>(B) * HK <= 32));
 }

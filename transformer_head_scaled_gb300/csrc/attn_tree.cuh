@@ -10,17 +10,18 @@
 //
 // The kernel for more than 32 query rows of a key head (16 where the heads are large
 // and many; fewer: attn_decode_scored.cuh).  Bound by HBM (the visible cache, read once
-// for each 256 query rows) while the rows are few, by the exponentials and the tensor
-// cores from about 200 rows on.  The G * n query rows of a key head (G query heads share
+// for each 256 query rows) while the rows are few, from about 200 rows on by a tile's chain
+// of scores, softmax and product.  The G * n query rows of a key head (G query heads share
 // it) are the rows of tcgen05 tiles of 128, so that a cache tile is multiplied
 // for all of them while it is in shared memory.
 //
 // Measured: 4 sequences of 65 to 131 thousand tokens, 32 heads on 8, d = 128, bf16, 64
-// nodes 329 us (floor 238: the cache at the rate of a plain copy, 6.8 TB/s; 1900 cycles
-// for 64 keys of 256 rows, of which the exponentials and the products take 1024 each).
+// nodes 331 us (floor 238: the cache at the rate of a plain copy, 6.8 TB/s; 1900 cycles
+// for 64 keys of 256 rows, where the products take 1024 and the exponentials 512).
 // 8 of 8 to 16 thousand, 32 heads on 4, d = 128, e4m3, 61 nodes, bias and a window of
-// 2047 keys 55 us (9): 6 us to the first scores, 15 tiles of 3400 cycles, 3 us to write
-// parts and 5 to join them.
+// 2047 keys 54 us (9): 6 us to the first scores, 15 tiles of 3400 cycles, 3 us to write
+// parts and 5 to join them.  Every instance stands at the 128 registers that 512 threads
+// leave, and spills 16 to 128 bytes.
 //
 // Work split: the visible cache of all sequences and key heads, and behind each
 // its tree's own keys, are one list of tiles of BN keys; a unit is a sequence,

@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(kThreads, 4) attn_tree_verify_kernel(const Ver
     return warp_sum(sum);
   };
 
-  // ---- the walk: by the first warp (fp64 is slow here), up to where a row has to
-  // be summed; all warps sum it
+  // ---- the walk: by the first warp, up to where a row has to be summed; all warps
+  // sum it
   const bool writes = rank == 0 && tid == 0;
   if (tid == 0) sm.walk = {{0.f, 0.f}, {1.f, 0.f}, 0, 1, 0, false, false};
   if (writes) pb.path[static_cast<long long>(b) * pb.n] = 0;
